@@ -3,7 +3,8 @@
  * attention: the sliding-window index rows, the fp8 round trip of new KV rows into the ring,
  * and sparse_attn itself (gathered-row latent attention with an attention sink); beside them the
  * RoPE rotation (fused into the ring write, or on its own for the output's inverse rotation) and
- * an fp8 row store that keeps KV rows as their e4m3 codes.
+ * an fp8 row store that keeps KV rows as their e4m3 codes; and a paged row store of 4-bit codes
+ * with the calls that fill it and attend over it for sequences at positions of their own.
  *
  * Conventions for every call:
  *   - All tensor pointers are DEVICE pointers, owned by the caller.  The library allocates no
@@ -341,6 +342,106 @@ int ds_indexer_select(const float *scores, int64_t ld, int b, int s, int64_t sta
 int ds_indexer_topk(const uint16_t *q, const uint16_t *k, const float *w, int b, int s, int H, int D, int64_t T,
                     int64_t start_pos, int ratio, int topk, int64_t offset, int32_t *idx, void *workspace,
                     size_t workspace_bytes, ds_stream_t stream);
+
+/*
+ * The paged 4-bit row store, and the two calls around it.  Sources: "DeepSeek V4.1",
+ * attention/query-latent (Attention.forward: q normalised per head and rotated; kv_norm, the
+ * rotation and the ring slot of the KV row; the compressed rows behind the window's; the inverse
+ * rotation of the output; RMSNorm) and "Module attn" (act_quant_inplace: a power-of-two scale per
+ * block of 32, amax floored at 1e-4).  The pages give every sequence of a batch one start
+ * position and one contiguous cache; 4-bit values, pages and a position for each sequence are
+ * this library's layout:
+ *     codes        uint8 [pages][page][d / 2]    e2m1 codes (sign, 2 exponent bits, 1 mantissa bit:
+ *                  0, 0.5, 1, 1.5, 2, 3, 4, 6), the even value of a pair in the low nibble
+ *     exps         int8  [pages][page][d / 32]   k with scale = 2^k for the block of 32
+ *     block_table  int32 [b][max_pages]          page of a sequence's logical rows
+ * Logical row r of sequence bi is slot r % page of page block_table[bi][r / page], for any page
+ * size >= 1.  The logical rows are those of a sequence's kv elsewhere in this library: the ring's
+ * window rows first, the compressed rows behind them, so that the rows of ds_window_topk_idxs and
+ * ds_indexer_topk (offset = window) are used as they are.  17/32 byte a value.
+ *
+ * In the three calls below first[bi] is the position (>= 0) of the sequence's first token of this
+ * call, and lens[bi], where given, how many of the s tokens it has (the others are padding:
+ * nothing of them is read, and what they would write is left as it was).  A position outside the
+ * table, or a row whose page is not in the block table or not one of the pages, raises
+ * DS_DEV_BAD_INDEX; what it would have written is left as it was.
+ */
+
+/*
+ * ds_norm_rotary -- RMS norm of rows and the rotation of their last rd values in one pass.
+ * For row (bi, t, hh) of d values, at position first[bi] + t:
+ *     z_i = x_i * w_i / sqrt(mean(x^2) + eps)        (w_i = 1 when weight is NULL)
+ * then the last rd values of z, adjacent pairs (a, b), become (a c - b s, a s + b c) with
+ * (c, s) = table[position][pair]; f32, rounded to bf16 once.
+ *
+ * x          device bf16, row (bi, t, hh) at x + bi * x_bstride + t * x_tstride + hh * d (strides in
+ *            elements, multiples of 8), 16-byte aligned: heads may lie in a wider projection
+ * y          device bf16 [b][s][h][d], 16-byte aligned; y may be x when x is laid out so
+ * weight     device f32 [d], one for all heads, or NULL
+ * eps        > 0
+ * rd         multiple of 8, 0 <= rd <= d (0: no rotation, table may be NULL)
+ * table      device f32 [table_rows][rd / 2][2] of (cos, sin), 8-byte aligned
+ * first      device int32 [b];  lens: device int32 [b], or NULL for s
+ * d          multiple of 8, <= 1024;  b * s * h < 2^31 (DS_EUNSUPPORTED otherwise)
+ * Errors: DS_EINVAL, DS_EUNSUPPORTED, DS_ECUDA.
+ */
+int ds_norm_rotary(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint16_t *y, int b, int s, int h, int d,
+                   const float *weight, float eps, int rd, const float *table, int64_t table_rows,
+                   const int32_t *first, const int32_t *lens, ds_stream_t stream);
+
+/*
+ * ds_kv_append_fp4_paged -- new KV rows, normalised and rotated, into the paged 4-bit row store.
+ * Token t of sequence bi is row i = first[bi] + t of what is appended: a token's position for the
+ * ring (pos_step 1), a compressed row's number for the compressed rows (pos_step = ratio).  Its
+ * rotation is that of position i * pos_step, and it is stored as logical row
+ *     base + i % window   (window > 0; the last `window` of the sequence's tokens are stored)
+ *     base + i            (window == 0; every token is stored)
+ * z is ds_norm_rotary's (no norm when eps = 0; no rotation when rd = 0), per block of 32
+ *     k = ceil(log2(max(amax, 1e-4) / 6)),  code = z / 2^k to the nearest e2m1, ties to even,
+ * decided on z itself and not on a rounded one: the codes are those of an evaluation in 64 bits.
+ * Logical rows of one call are distinct within a sequence; pages written for different sequences
+ * must be distinct too.  Rows must be finite.
+ *
+ * x          device bf16, row (bi, t) at x + bi * x_bstride + t * x_tstride (elements, multiples
+ *            of 8), 16-byte aligned, not modified
+ * y          device bf16 [b][s][d] or NULL: the values that the codes stand for (exact in bf16), of
+ *            every token, stored or not, as ds_kv_quant_ring_write leaves them in place; 16-byte
+ *            aligned; y may be x when x is laid out so
+ * codes      16-byte aligned.  d multiple of 32, <= 1024; b * s < 2^31, pages * page < 2^31
+ * weight, rd, table, first, lens as for ds_norm_rotary (weight is read only when eps > 0)
+ * Errors: DS_EINVAL, DS_EUNSUPPORTED, DS_ECUDA.
+ */
+int ds_kv_append_fp4_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint16_t *y, int b, int s, int d,
+                           const float *weight, float eps, int rd, const float *table, int64_t table_rows,
+                           const int32_t *first, const int32_t *lens, int pos_step, int base, int window,
+                           uint8_t *codes, int8_t *exps, int64_t pages, int page, const int32_t *block_table,
+                           int max_pages, ds_stream_t stream);
+
+/*
+ * ds_sparse_attn_fp4_paged -- ds_sparse_attn over the paged 4-bit row store, with the inverse RoPE
+ * of its output fused in when rd > 0.
+ * idx [b][m][topk] lists logical rows; entries < 0 are skipped, entries without a page are skipped
+ * and flagged.  Otherwise the operation is ds_sparse_attn's on the decoded rows: duplicates count as
+ * often as they are listed, a query without rows gives o = 0.  Scores, softmax and accumulation
+ * are f32, the probabilities enter the value product with at least bf16's precision, and the
+ * rotation of position first[bi] + t is applied before o's one rounding (a position outside the
+ * table leaves that token's o unrotated).
+ * Within a row, blocks whose exponent is more than 26 below the row's largest count as zeros (2^-26
+ * of the row's scale).  Exponents must lie in [-126, 126], and scores must be finite in f32.
+ *
+ * rd         multiple of 8, 0 <= rd <= d (0: no rotation; table and first may be NULL)
+ * workspace  at least ds_sparse_attn_fp4_paged_workspace_bytes(b, m, h, d, topk) bytes, 256-byte
+ *            aligned (may be NULL when that size is 0); its contents need no initialisation and
+ *            mean nothing afterwards.  Calls that may run at the same time need one each.
+ * Supported: d = 512, 1 <= h <= 128; pages * page < 2^31.  q, o, codes and exps 16-byte aligned.
+ * Other arguments and the errors are those of ds_sparse_attn.
+ */
+size_t ds_sparse_attn_fp4_paged_workspace_bytes(int b, int m, int h, int d, int topk);
+int ds_sparse_attn_fp4_paged(const uint16_t *q, const uint8_t *codes, const int8_t *exps, int64_t pages, int page,
+                             const int32_t *block_table, int max_pages, const float *sink, const int32_t *idx,
+                             int topk, float scale, uint16_t *o, int b, int m, int h, int d, void *workspace,
+                             size_t workspace_bytes, int rd, const float *table, int64_t table_rows,
+                             const int32_t *first, ds_stream_t stream);
 
 /*
  * ds_device_status -- synchronise `stream`, then read and clear the current device's status word

@@ -5,6 +5,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "sparse_attn_fp4.cuh"
 #include "sparse_attn_ot.cuh"
 
 namespace dsattn {
@@ -303,6 +304,96 @@ int ds_indexer_topk(const uint16_t *q, const uint16_t *k, const float *w, int b,
     st = launch_indexer_scores(a, scores, ld, strm);
     if (st != DS_OK) return st;
     return launch_indexer_select(scores, ld, a, idx, strm);
+}
+
+// ---- the paged 4-bit row store -------------------------------------------------------------------
+
+namespace {
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// rd, table and first of a call that rotates rows of d values (rd = 0: none of them is used)
+bool rotation_ok(int rd, int d, const float *table, int64_t table_rows) {
+    if (rd < 0 || rd % 8 != 0 || rd > d) return false;
+    return rd == 0 || (table && table_rows >= 0 && (reinterpret_cast<uintptr_t>(table) & 7u) == 0);
+}
+
+// rows (bi, t) of `row` elements at bi * bstride + t * tstride
+bool strides_ok(int64_t bstride, int64_t tstride, int b, int s, int64_t row) {
+    return bstride % 8 == 0 && tstride % 8 == 0 && (s <= 1 || tstride >= row) && (b <= 1 || bstride >= row);
+}
+
+bool pool_ok(int64_t pages, int page, int max_pages) { return pages >= 0 && page >= 1 && max_pages >= 0; }
+bool pool_fits(int64_t pages, int page) { return pages <= INT32_MAX / page; }
+}  // namespace
+
+int ds_norm_rotary(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint16_t *y, int b, int s, int h, int d,
+                   const float *weight, float eps, int rd, const float *table, int64_t table_rows,
+                   const int32_t *first, const int32_t *lens, ds_stream_t stream) {
+    const Range range("ds_norm_rotary");
+    if (b < 0 || s < 0 || h < 1 || d < 8 || d % 8 != 0 || !(eps > 0.0f)) return DS_EINVAL;
+    if (!rotation_ok(rd, d, table, table_rows)) return DS_EINVAL;
+    if (d > 1024) return DS_EUNSUPPORTED;
+    if ((int64_t)b * s == 0) return DS_OK;
+    if ((int64_t)b * s > INT32_MAX / h) return DS_EUNSUPPORTED;
+    if (!x || !y || !first || !aligned16(x) || !aligned16(y) || !aligned4(weight) || !aligned4(first) || !aligned4(lens))
+        return DS_EINVAL;
+    if (!strides_ok(x_bstride, x_tstride, b, s, (int64_t)h * d)) return DS_EINVAL;
+    unsigned int *status = status_word();
+    if (!status) return DS_ECUDA;
+    return launch_norm_rotary(x, x_bstride, x_tstride, y, b, s, h, d, weight, eps, rd, table, table_rows, first, lens,
+                              status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int ds_kv_append_fp4_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint16_t *y, int b, int s, int d,
+                           const float *weight, float eps, int rd, const float *table, int64_t table_rows,
+                           const int32_t *first, const int32_t *lens, int pos_step, int base, int window,
+                           uint8_t *codes, int8_t *exps, int64_t pages, int page, const int32_t *block_table,
+                           int max_pages, ds_stream_t stream) {
+    const Range range("ds_kv_append_fp4_paged");
+    if (b < 0 || s < 0 || d < 32 || d % 32 != 0 || !(eps >= 0.0f) || pos_step < 1 || base < 0 || window < 0)
+        return DS_EINVAL;
+    if (!rotation_ok(rd, d, table, table_rows) || !pool_ok(pages, page, max_pages)) return DS_EINVAL;
+    if (d > 1024 || !pool_fits(pages, page) || (int64_t)b * s > INT32_MAX) return DS_EUNSUPPORTED;
+    if ((int64_t)b * s == 0) return DS_OK;
+    if (!x || !first || !aligned16(x) || !aligned16(y) || !aligned4(weight) || !aligned4(first) || !aligned4(lens))
+        return DS_EINVAL;
+    if (!codes || !exps || !block_table || !aligned16(codes) || !aligned4(block_table)) return DS_EINVAL;
+    if (!strides_ok(x_bstride, x_tstride, b, s, d)) return DS_EINVAL;
+    unsigned int *status = status_word();
+    if (!status) return DS_ECUDA;
+    return launch_kv_append_fp4(x, x_bstride, x_tstride, y, b, s, d, weight, eps, rd, table, table_rows, first, lens,
+                                pos_step, base, window, codes, exps, pages, page, block_table, max_pages, status,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t ds_sparse_attn_fp4_paged_workspace_bytes(int b, int m, int h, int d, int topk) {
+    if (b < 0 || m < 0 || h < 1 || h > 128 || topk < 0 || d != 512) return 0;
+    return sparse_attn_fp4_workspace_bytes(b, m, h, topk);
+}
+
+int ds_sparse_attn_fp4_paged(const uint16_t *q, const uint8_t *codes, const int8_t *exps, int64_t pages, int page,
+                             const int32_t *block_table, int max_pages, const float *sink, const int32_t *idx,
+                             int topk, float scale, uint16_t *o, int b, int m, int h, int d, void *workspace,
+                             size_t workspace_bytes, int rd, const float *table, int64_t table_rows,
+                             const int32_t *first, ds_stream_t stream) {
+    const Range range("ds_sparse_attn_fp4_paged");
+    if (b < 0 || m < 0 || topk < 0 || h < 1 || !pool_ok(pages, page, max_pages)) return DS_EINVAL;
+    if (!rotation_ok(rd, d, table, table_rows)) return DS_EINVAL;
+    if (d != 512 || h > 128 || !pool_fits(pages, page)) return DS_EUNSUPPORTED;
+    if ((int64_t)b * m == 0) return DS_OK;
+    if (!q || !o || !sink || (rd > 0 && !first)) return DS_EINVAL;
+    if (topk > 0 && (!idx || !codes || !exps || !block_table)) return DS_EINVAL;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(codes) || !aligned16(exps)) return DS_EINVAL;
+    if (!aligned4(sink) || !aligned4(idx) || !aligned4(block_table) || !aligned4(first)) return DS_EINVAL;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (topk == 0)   // nothing to attend to: every output is 0
+        return cudaMemsetAsync(o, 0, (size_t)b * m * h * d * sizeof(uint16_t), st) == cudaSuccess ? DS_OK : DS_ECUDA;
+    if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return DS_EWORKSPACE;
+    const fp4::Args a{q, codes, exps, pages, page, block_table, max_pages, sink, idx, topk, scale, o, b, m, h,
+                      workspace, workspace_bytes, rd, reinterpret_cast<const float2 *>(table), table_rows, first,
+                      status_word()};
+    if (!a.status) return DS_ECUDA;
+    return launch_sparse_attn_fp4(a, st);
 }
 
 void ds_test_set_stall(int on) { set_test_stall(on != 0); }

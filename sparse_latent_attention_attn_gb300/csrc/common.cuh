@@ -50,6 +50,15 @@ int launch_apply_rotary(uint16_t *x, int64_t rows, int row_len, int rd, int64_t 
                         int64_t positions_per_seq, int64_t start_pos, const float *table, bool inverse,
                         cudaStream_t stream);
 
+int launch_norm_rotary(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint16_t *y, int b, int s, int h, int d,
+                       const float *weight, float eps, int rd, const float *table, int64_t table_rows,
+                       const int32_t *first, const int32_t *lens, unsigned int *status, cudaStream_t stream);
+int launch_kv_append_fp4(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint16_t *y, int b, int s, int d,
+                         const float *weight, float eps, int rd, const float *table, int64_t table_rows,
+                         const int32_t *first, const int32_t *lens, int pos_step, int base, int window, uint8_t *codes,
+                         int8_t *exps, int64_t pages, int page, const int32_t *block_table, int max_pages,
+                         unsigned int *status, cudaStream_t stream);
+
 struct AttnArgs {
     const uint16_t *q;
     const uint16_t *kv;

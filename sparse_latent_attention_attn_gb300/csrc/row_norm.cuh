@@ -1,0 +1,81 @@
+// row_norm.cuh -- what the kernels over rows of bf16 values at positions share: the lanes of a row,
+// its chunks of 8 values, the norm factor and the rotation in f32.
+//
+// A row of d values (d % 8 == 0, d <= 1024) is d / 8 chunks of 16 bytes.  L = 8, 16 or 32 lanes share a
+// row; lane l of them holds chunks l, l + L, ..., so that a warp's accesses are contiguous.
+#pragma once
+
+#include "common.cuh"
+
+namespace dsattn {
+namespace rows {
+
+constexpr int kMaxRow = 1024;
+constexpr int kThreads = 256;
+constexpr uint32_t kAll = 0xffffffffu;
+
+// Lanes of a row and chunks of a lane, for a row of d values.
+inline int lanes_of(int d) { return d <= 64 ? 8 : d <= 128 ? 16 : 32; }
+inline int chunks_of(int d) { return (d / 8 + lanes_of(d) - 1) / lanes_of(d); }
+
+// Calls f(integral constants L, N) for a row of d values.
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
+template <typename F>
+void for_row(int d, F f) {
+    if (d <= 64) f(Int<8>(), Int<1>());
+    else if (d <= 128) f(Int<16>(), Int<1>());
+    else if (d <= 256) f(Int<32>(), Int<1>());
+    else if (d <= 512) f(Int<32>(), Int<2>());
+    else f(Int<32>(), Int<4>());
+}
+
+__device__ __forceinline__ void unpack8(const uint4 v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(w[i]);
+        x[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x[2 * i])) |
+               ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x[2 * i + 1])) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Sum over the L lanes of a row; every lane gets it.
+template <int L, typename T>
+__device__ __forceinline__ T row_sum(T v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+// The chunk's values times the row's factor and the weights of its columns (w: f32 [8], 4-byte aligned
+// or null).
+__device__ __forceinline__ void scale8(float (&x)[8], float r, const float *__restrict__ w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = w ? __fmul_rn(__fmul_rn(x[i], r), __ldg(w + i)) : __fmul_rn(x[i], r);
+}
+
+// Four adjacent pairs (a, b) turned by cs[j] = (cos, sin): (a c - b s, a s + b c).  Stays in f32: the
+// result is rounded once, by whoever stores it.
+__device__ __forceinline__ void rotate8(float (&x)[8], const float2 *__restrict__ cs) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 t = __ldg(cs + j);
+        const float a = x[2 * j], b = x[2 * j + 1];
+        x[2 * j] = a * t.x - b * t.y;
+        x[2 * j + 1] = a * t.y + b * t.x;
+    }
+}
+
+}  // namespace rows
+}  // namespace dsattn

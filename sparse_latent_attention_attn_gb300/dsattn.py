@@ -12,6 +12,7 @@ sparse_attn, window_topk_idxs, the ring-cache and Precision paragraphs).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -73,6 +74,16 @@ _lib.ds_indexer_select.argtypes = [_P, _i64, _i32, _i32, _i64, _i32, _i32, _i64,
 _lib.ds_indexer_select.restype = _i32
 _lib.ds_indexer_topk.argtypes = [_P, _P, _P, _i32, _i32, _i32, _i32, _i64, _i64, _i32, _i32, _i64, _P, _P, _sz, _P]
 _lib.ds_indexer_topk.restype = _i32
+_lib.ds_norm_rotary.argtypes = [_P, _i64, _i64, _P, _i32, _i32, _i32, _i32, _P, _f32, _i32, _P, _i64, _P, _P, _P]
+_lib.ds_norm_rotary.restype = _i32
+_lib.ds_kv_append_fp4_paged.argtypes = [_P, _i64, _i64, _P, _i32, _i32, _i32, _P, _f32, _i32, _P, _i64, _P, _P, _i32,
+                                        _i32, _i32, _P, _P, _i64, _i32, _P, _i32, _P]
+_lib.ds_kv_append_fp4_paged.restype = _i32
+_lib.ds_sparse_attn_fp4_paged_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32]
+_lib.ds_sparse_attn_fp4_paged_workspace_bytes.restype = _sz
+_lib.ds_sparse_attn_fp4_paged.argtypes = [_P, _P, _P, _i64, _i32, _P, _i32, _P, _P, _i32, _f32, _P, _i32, _i32, _i32,
+                                          _i32, _P, _sz, _i32, _P, _i64, _P, _P]
+_lib.ds_sparse_attn_fp4_paged.restype = _i32
 _lib.ds_test_set_stall.argtypes = [_i32]
 _lib.ds_test_set_stall.restype = None
 _lib.ds_test_set_kernel.argtypes = [_i32]
@@ -370,6 +381,167 @@ def sparse_attn_fp8kv(q: torch.Tensor, kv_codes: torch.Tensor, kv_exps: torch.Te
            _lib.ds_sparse_attn_fp8kv(_ptr(q), _ptr(kv_codes), _ptr(kv_exps), n, _ptr(sink), _ptr(idx), topk,
                                      float(scale), _ptr(o), b, m, h, d, _ptr(workspace), ws_bytes,
                                      _stream(stream)))
+    return o
+
+
+def _on(stream):
+    """Tensors made inside belong to the stream of the call, not to the current one."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _check_rows(first: torch.Tensor, lens: torch.Tensor | None, b: int) -> None:
+    _need(first, torch.int32, "first")
+    if first.shape != (b,) or not first.is_contiguous():
+        raise ValueError("first must be a contiguous int32 [b]")
+    if lens is not None:
+        _need(lens, torch.int32, "lens")
+        if lens.shape != (b,) or not lens.is_contiguous():
+            raise ValueError("lens must be a contiguous int32 [b]")
+
+
+def _check_weight(weight: torch.Tensor | None, d: int) -> None:
+    if weight is not None:
+        _need(weight, torch.float32, "weight")
+        if weight.shape != (d,) or not weight.is_contiguous():
+            raise ValueError("weight must be a contiguous f32 [d]")
+
+
+def _check_rotation(rd: int, table: torch.Tensor | None) -> int:
+    """Rows of the table (0 without a rotation)."""
+    if rd == 0:
+        return 0
+    if table is None:
+        raise ValueError("rd > 0 needs a table")
+    _check_table(table, rd)
+    return table.shape[0]
+
+
+def _same_device(**tensors: torch.Tensor | None) -> None:
+    """Every tensor on the current device: the library launches there."""
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"{name}: must be on the current CUDA device")
+
+
+def _check_store(codes: torch.Tensor, exps: torch.Tensor, block_table: torch.Tensor, b: int, d: int) -> None:
+    _need(codes, torch.uint8, "codes")
+    _need(exps, torch.int8, "exps")
+    _need(block_table, torch.int32, "block_table")
+    if codes.dim() != 3 or codes.shape[2] * 2 != d or exps.shape != codes.shape[:2] + (d // 32,) \
+            or not codes.is_contiguous() or not exps.is_contiguous():
+        raise ValueError("codes must be a contiguous [pages][page][d/2] and exps a contiguous [pages][page][d/32]")
+    if block_table.dim() != 2 or block_table.shape[0] != b or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 [b][max_pages]")
+
+
+def norm_rotary(x: torch.Tensor, eps: float, rd: int, table: torch.Tensor | None, first: torch.Tensor,
+                weight: torch.Tensor | None = None, lens: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """RMS norm of every row of ``x [b][s][h][d]`` (bf16, the h * d values of a token contiguous; tokens may
+    lie in a wider tensor) and the rotation of its last ``rd`` values to position ``first[b] + t``, in
+    one pass.  ``y``: bf16 [b][s][h][d] contiguous (``x`` itself when laid out so); tokens at or behind
+    ``lens[b]`` leave it as it was (zeros in a new one)."""
+    _need(x, torch.bfloat16, "x")
+    if x.dim() != 4:
+        raise ValueError("x must be [b][s][h][d]")
+    b, s, h, d = x.shape
+    if x.numel() and (x.stride(3) != 1 or (h > 1 and x.stride(2) != d)):
+        raise ValueError("the heads of a token must be contiguous")
+    _check_rows(first, lens, b)
+    _check_weight(weight, d)
+    rows = _check_rotation(rd, table)
+    if y is None:
+        with _on(stream):
+            y = torch.empty((b, s, h, d), dtype=torch.bfloat16, device=x.device) if lens is None else \
+                torch.zeros((b, s, h, d), dtype=torch.bfloat16, device=x.device)
+    elif y.shape != x.shape or y.dtype != torch.bfloat16 or not y.is_contiguous() or not y.is_cuda:
+        raise ValueError("y must be a contiguous bf16 tensor shaped like x")
+    _same_device(x=x, y=y, first=first, lens=lens, weight=weight, table=table if rd else None)
+    _check("ds_norm_rotary",
+           _lib.ds_norm_rotary(_ptr(x), x.stride(0) if b > 1 else 0, x.stride(1) if s > 1 else 0, _ptr(y), b, s, h, d,
+                               _ptr(weight), float(eps), rd, _ptr(table) if rd else None, rows, _ptr(first),
+                               _ptr(lens), _stream(stream)))
+    return y
+
+
+def kv_append_fp4_paged(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor, block_table: torch.Tensor,
+                        first: torch.Tensor, rd: int = 0, table: torch.Tensor | None = None, eps: float = 0.0,
+                        weight: torch.Tensor | None = None, lens: torch.Tensor | None = None, pos_step: int = 1,
+                        base: int = 0, window: int = 0, y: torch.Tensor | None = None, stream=None) -> None:
+    """Rows ``x [b][s][d]`` (bf16), normalised (``eps`` > 0) and rotated (``rd`` > 0), into the paged 4-bit
+    row store ``codes [pages][page][d/2]``, ``exps [pages][page][d/32]``: row ``i = first[b] + t`` goes to
+    logical row ``base + i % window`` (``window`` > 0, the last ``window`` tokens) or ``base + i``, rotated
+    to position ``i * pos_step``.  ``y``: bf16 [b][s][d] contiguous, receives the stored values."""
+    _need(x, torch.bfloat16, "x")
+    if x.dim() != 3:
+        raise ValueError("x must be [b][s][d]")
+    b, s, d = x.shape
+    if x.numel() and x.stride(2) != 1:
+        raise ValueError("the values of a row must be contiguous")
+    _check_store(codes, exps, block_table, b, d)
+    _check_rows(first, lens, b)
+    _check_weight(weight, d)
+    rows = _check_rotation(rd, table)
+    if y is not None and (y.shape != x.shape or y.dtype != torch.bfloat16 or not y.is_contiguous() or not y.is_cuda):
+        raise ValueError("y must be a contiguous bf16 tensor shaped like x")
+    _same_device(x=x, codes=codes, exps=exps, block_table=block_table, first=first, lens=lens, weight=weight, y=y,
+                 table=table if rd else None)
+    _check("ds_kv_append_fp4_paged",
+           _lib.ds_kv_append_fp4_paged(_ptr(x), x.stride(0) if b > 1 else 0, x.stride(1) if s > 1 else 0, _ptr(y), b,
+                                       s, d, _ptr(weight), float(eps), rd, _ptr(table) if rd else None, rows,
+                                       _ptr(first), _ptr(lens), pos_step, base, window, _ptr(codes), _ptr(exps),
+                                       codes.shape[0], codes.shape[1], _ptr(block_table), block_table.shape[1],
+                                       _stream(stream)))
+
+
+def sparse_attn_fp4_paged_workspace_bytes(b: int, m: int, h: int, d: int, topk: int) -> int:
+    return int(_lib.ds_sparse_attn_fp4_paged_workspace_bytes(b, m, h, d, topk))
+
+
+def sparse_attn_fp4_paged(q: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor, block_table: torch.Tensor,
+                          sink: torch.Tensor, idx: torch.Tensor, scale: float, rd: int = 0,
+                          table: torch.Tensor | None = None, first: torch.Tensor | None = None,
+                          o: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """``sparse_attn`` over the paged 4-bit row store (``idx`` lists logical rows of each sequence); with
+    ``rd`` > 0 the last ``rd`` values of token t's output are rotated back by position ``first[b] + t``."""
+    _need(q, torch.bfloat16, "q")
+    _need(sink, torch.float32, "sink")
+    _need(idx, torch.int32, "idx")
+    if q.dim() != 4 or idx.dim() != 3:
+        raise ValueError("q must be [b][m][h][d] and idx [b][m][topk]")
+    b, m, h, d = q.shape
+    topk = idx.shape[2]
+    if idx.shape[:2] != (b, m) or sink.shape != (h,):
+        raise ValueError("shape mismatch")
+    for t, name in ((q, "q"), (idx, "idx"), (sink, "sink")):
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    _check_store(codes, exps, block_table, b, d)
+    rows = _check_rotation(rd, table)
+    if rd:
+        if first is None:
+            raise ValueError("rd > 0 needs first")
+        _check_rows(first, None, b)
+    if o is None:
+        with _on(stream):
+            o = torch.empty_like(q)
+    elif o.shape != q.shape or o.dtype != torch.bfloat16 or not o.is_contiguous() or not o.is_cuda:
+        raise ValueError("o must be a contiguous bf16 tensor shaped like q")
+    _same_device(q=q, codes=codes, exps=exps, block_table=block_table, sink=sink, idx=idx, o=o, workspace=workspace,
+                 first=first if rd else None, table=table if rd else None)
+    need = sparse_attn_fp4_paged_workspace_bytes(b, m, h, d, topk)
+    if need and workspace is None:
+        with _on(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("ds_sparse_attn_fp4_paged",
+           _lib.ds_sparse_attn_fp4_paged(_ptr(q), _ptr(codes), _ptr(exps), codes.shape[0], codes.shape[1],
+                                         _ptr(block_table), block_table.shape[1], _ptr(sink), _ptr(idx), topk,
+                                         float(scale), _ptr(o), b, m, h, d, _ptr(workspace), ws_bytes, rd,
+                                         _ptr(table) if rd else None, rows, _ptr(first) if rd else None,
+                                         _stream(stream)))
     return o
 
 

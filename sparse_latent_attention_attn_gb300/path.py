@@ -11,6 +11,10 @@ A prefill step at start_pos 0 rounds the whole chunk in place (it is also the wi
 for this step), keeps its last `window` rows in the ring, writes one causal window row per query
 and runs sparse_attn over kv = [chunk | compressed rows].
 
+A decode step over the paged 4-bit row store has every sequence at a position of its own: the new
+row is normalised, rotated and stored as codes in its ring slot, the queries are normalised and rotated,
+and sparse_attn runs over the listed rows of the store with its output rotated back.
+
 The caller lays kv out as [window rows | compressed rows] per sequence and idx as
 [window cols | compressed cols], so no concatenation copy is made.
 """
@@ -44,3 +48,21 @@ def prefill_step(q: torch.Tensor, kv: torch.Tensor, ring: torch.Tensor, sink: to
     if pairs:
         return dsattn.sparse_attn_prefill(q, kv, sink, idx, scale, o=o, workspace=workspace, stream=stream)
     return dsattn.sparse_attn(q, kv, sink, idx, scale, o=o, workspace=workspace, stream=stream)
+
+
+def decode_step_fp4_paged(q: torch.Tensor, new_kv: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor,
+                          block_table: torch.Tensor, first: torch.Tensor, sink: torch.Tensor, idx: torch.Tensor,
+                          window: int, scale: float, rd: int, table: torch.Tensor, eps: float,
+                          kv_weight: torch.Tensor | None = None, lens: torch.Tensor | None = None,
+                          o: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """q [b][s][h][d] and new_kv [b][s][d] as their projections leave them (neither is modified); the token
+    (bi, t) is at position first[bi] + t; codes, exps, block_table: the paged store, whose logical rows
+    are the ring's `window` slots, then the compressed rows; idx [b][s][topk] lists logical rows, complete.
+    s > 1 stores all s rows before any query reads them: a query whose ring is full then misses the rows
+    that later tokens of the step replaced."""
+    dsattn.kv_append_fp4_paged(new_kv, codes, exps, block_table, first, rd=rd, table=table, eps=eps, weight=kv_weight,
+                               lens=lens, window=window, stream=stream)
+    qn = dsattn.norm_rotary(q, eps, rd, table, first, lens=lens, stream=stream)
+    return dsattn.sparse_attn_fp4_paged(qn, codes, exps, block_table, sink, idx, scale, rd=rd, table=table,
+                                        first=first, o=o, workspace=workspace, stream=stream)

@@ -1,0 +1,658 @@
+"""The paged 4-bit row store: ds_norm_rotary, ds_kv_append_fp4_paged and ds_sparse_attn_fp4_paged against
+plain implementations in 64 bits, their refusals, and a run of them together.
+
+Tolerances.  A bf16 result is off by half a step, 2^-8 of its value; the f32 work before it by less than
+2^-20 of the magnitudes it adds up.  The attention's probabilities may be rounded by 2^-8 of themselves
+before the value product (as bf16 would), with a floor of 2^-20 of the largest, so with A = sum p |v| / l
+and F = sum |v| / l (l the denominator relative to the largest probability) an output is off by at most
+2^-8 |o| + (2^-8 + 2^-12) A + 2^-20 F; a rotation adds up both values of a pair.  An output below f32's
+least normal number, 2^-126, may come as 0 (a sink of 300 makes the exact ones about e^-300).
+Codes, exponents and the values they stand for are equal.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+gpu = pytest.mark.gpu
+MAG = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+# ---- plain implementations, 64 bits, on the CPU ---------------------------------------------------
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def table_of(positions, rd, scale=1.0):
+    ang = np.arange(positions)[:, None] * 10000.0 ** (-np.arange(0, rd, 2) / max(rd, 1))[None]
+    return torch.from_numpy(scale * np.stack((np.cos(ang), np.sin(ang)), -1)).float().contiguous()
+
+
+def rotate(z, cs, inverse=False):
+    rd = 2 * cs.shape[-2]
+    if rd == 0:
+        return z
+    out = z.copy()
+    a, b, c, s = z[..., -rd::2], z[..., -rd + 1::2], cs[..., 0], cs[..., 1] * (-1 if inverse else 1)
+    out[..., -rd::2] = a * c - b * s
+    out[..., -rd + 1::2] = a * s + b * c
+    return out
+
+
+def normed(x, weight, eps):
+    z = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    return z if weight is None else z * weight
+
+
+def quantise(z):
+    """codes (0..15) and block exponents, decided value by value against the whole grid."""
+    v = z.reshape(z.shape[:-1] + (-1, 32))
+    amax = np.maximum(np.abs(v).max(-1), 1e-4)
+    k = np.array([next(e for e in range(-20, 130) if a <= 6 * 2.0 ** e) for a in amax.ravel()]).reshape(amax.shape)
+    y = np.abs(v) / 2.0 ** k[..., None]
+    dist = np.abs(y[..., None] - MAG)
+    lower = dist.argmin(-1)                                    # the lower of two that are as near
+    upper = np.minimum(lower + 1, 7)
+    tie = np.take_along_axis(dist, lower[..., None], -1) == np.take_along_axis(dist, upper[..., None], -1)
+    near = np.where(tie[..., 0] & (lower < 7) & (lower % 2 == 1), upper, lower)
+    code = near + 8 * np.signbit(v)
+    return code.reshape(z.shape).astype(np.uint8), k.astype(np.int8)
+
+
+def values(code, k):
+    v = MAG[code & 7] * np.where(code & 8, -1.0, 1.0)
+    return (v.reshape(v.shape[:-1] + (-1, 32)) * 2.0 ** k[..., None].astype(float)).reshape(v.shape)
+
+
+def pack(code):
+    return code[..., 0::2] | (code[..., 1::2] << 4)
+
+
+def unpack(packed):
+    return np.stack((packed & 15, packed >> 4), -1).reshape(packed.shape[:-1] + (-1,))
+
+
+def attention(q, rows, live, sink, scale):
+    """q [h][d], rows [n][d], live [n] -> o, A, F of the header comment."""
+    rows = rows[live]
+    if not len(rows):
+        return np.zeros_like(q), np.zeros_like(q), np.zeros_like(q)
+    s = scale * q @ rows.T
+    top = s.max(-1, keepdims=True)
+    p = np.exp(s - top)
+    with np.errstate(over="ignore"):
+        den = p.sum(-1, keepdims=True) + np.exp(sink[:, None] - top)
+    return p @ rows / den, p @ np.abs(rows) / den, np.abs(rows).sum(0)[None] / den
+
+
+def pair_sum(a, rd):
+    out = a.copy()
+    if rd:
+        both = a[..., -rd::2] + a[..., -rd + 1::2]
+        out[..., -rd::2] = out[..., -rd + 1::2] = both
+    return out
+
+
+# ---- helpers on the GPU -----------------------------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def ds():
+    from sparse_latent_attention_attn_gb300 import dsattn
+    dsattn.device_status()
+    return dsattn
+
+
+def dev(*ts):
+    return [t if t is None else t.cuda() for t in ts]
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+def random_pool(g, b, rows, page, d, kmin=-3, kmax=3, spare=2):
+    """A pool with every sequence's pages in random order among `spare` unused ones."""
+    per = -(-rows // page)
+    pages = b * per + spare
+    bt = torch.randperm(pages, generator=g)[: b * per].view(b, per).to(torch.int32)
+    codes = torch.randint(0, 256, (pages, page, d // 2), generator=g, dtype=torch.uint8)
+    exps = torch.randint(kmin, kmax + 1, (pages, page, d // 32), generator=g, dtype=torch.int8)
+    return codes, exps, bt
+
+
+def logical_rows(codes, exps, bt, seq, r, page):
+    """64-bit rows of logical numbers r (clamped at 0) of one sequence."""
+    r = np.maximum(r, 0)
+    pg = bt.numpy()[seq][r // page]
+    return values(unpack(codes.numpy()[pg, r % page]), exps.numpy()[pg, r % page])
+
+
+# ---- norm and rotation --------------------------------------------------------------------------------
+
+NORMS = [  # b, s, h, d, rd, gap, weight, ragged
+    (1, 1, 1, 8, 8, 0, False, False),
+    (1, 1, 4, 64, 16, 0, False, False),
+    (3, 5, 3, 40, 8, 24, True, True),
+    (2, 3, 5, 128, 128, 8, True, False),
+    (2, 7, 9, 192, 40, 64, False, True),
+    (64, 1, 64, 512, 64, 0, False, False),
+    (2, 33, 17, 512, 0, 0, True, True),
+    (2, 3, 2, 1024, 1024, 0, True, False),
+    (1, 2, 3, 520, 520, 0, False, False),
+]
+
+
+@gpu
+@pytest.mark.parametrize("b,s,h,d,rd,gap,weight,ragged", NORMS)
+def test_norm_rotary(ds, b, s, h, d, rd, gap, weight, ragged):
+    g = torch.Generator().manual_seed(d + s)
+    wide = (torch.randn((b, s, h * d + gap), generator=g) * 3).to(torch.bfloat16)
+    w = torch.randn((d,), generator=g) if weight else None
+    first = torch.randint(0, 100, (b,), generator=g, dtype=torch.int32)
+    lens = torch.randint(0, s + 1, (b,), generator=g, dtype=torch.int32) if ragged else None
+    tab = table_of(100 + s, rd, 1.25) if rd else None
+    xg = wide.cuda()[..., : h * d].unflatten(-1, (h, d))
+    y = torch.full((b, s, h, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    fg, wg, lg, tg = dev(first, w, lens, tab)
+    out = ds.norm_rotary(xg, 1e-5, rd, tg, fg, weight=wg, lens=lg, y=y)
+    assert ds.device_status() == 0 and out.data_ptr() == y.data_ptr()
+    z = normed(f64(wide[..., : h * d].unflatten(-1, (h, d))), None if w is None else f64(w), 1e-5)
+    mag = np.abs(z)
+    if rd:
+        cs = f64(tab)[first.numpy()[:, None] + np.arange(s)][:, :, None]
+        mag = 1.25 * pair_sum(mag, rd)
+        z = rotate(z, cs)
+    live = np.ones((b, s), bool) if lens is None else np.arange(s) < lens.numpy()[:, None]
+    got = f64(y)
+    assert (got[~live] == 7).all()
+    assert (np.abs(got - z) <= 2.0 ** -8 * np.abs(z) + 2.0 ** -20 * mag)[live].all()
+    # a new output is zero where there is no token; in place gives the same as beside it
+    if ragged:
+        new = f64(ds.norm_rotary(xg, 1e-5, rd, tg, fg, weight=wg, lens=lg))
+        assert (new[~live] == 0).all() and (new[live] == got[live]).all()
+    if gap == 0:
+        x2 = xg.clone()
+        ds.norm_rotary(x2, 1e-5, rd, tg, fg, weight=wg, y=x2)
+        assert (f64(x2)[live] == got[live]).all()
+
+
+@gpu
+def test_norm_rotary_positions_outside_the_table(ds):
+    x = torch.ones((3, 2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    tab = table_of(10, 64).cuda()
+    y = torch.full_like(x, 5.0)
+    ds.norm_rotary(x, 1e-5, 64, tab, ints(0, 9, -1).cuda(), y=y)
+    assert ds.device_status() == ds.DS_DEV_BAD_INDEX
+    bad = (y == 5.0).all(-1).all(-1).cpu()
+    assert bad.tolist() == [[False, False], [False, True], [True, False]]
+    assert ds.norm_rotary(x[:0], 1e-5, 64, tab, ints().cuda()).shape == (0, 2, 2, 64)
+    assert ds.norm_rotary(x[:, :0], 1e-5, 64, tab, ints(0, 0, 0).cuda()).shape == (3, 0, 2, 64)
+
+
+@gpu
+def test_norm_rotary_zero_and_extreme_rows(ds):
+    x = torch.zeros((1, 1, 4, 64), dtype=torch.bfloat16)
+    x[0, 0, 1] = 1e-30
+    x[0, 0, 2] = 1e15
+    x[0, 0, 3, 5] = float("nan")
+    y = f64(ds.norm_rotary(x.cuda(), 1e-6, 0, None, ints(0).cuda()))[0, 0]
+    assert (y[0] == 0).all() and np.isfinite(y[:3]).all() and np.isnan(y[3]).all()
+    np.testing.assert_allclose(y[2], 1.0, rtol=2.0 ** -8)
+
+
+# ---- append ---------------------------------------------------------------------------------------------
+
+APPENDS = [  # b, s, d, rd, page, window, base, step, eps, weight, ragged
+    (1, 1, 32, 8, 1, 0, 0, 1, 1e-6, False, False),
+    (3, 1, 64, 16, 4, 8, 0, 1, 1e-6, True, False),
+    (2, 12, 64, 16, 3, 8, 2, 1, 1e-6, False, False),       # the chunk is longer than the ring
+    (4, 9, 128, 64, 5, 0, 11, 4, 1e-6, True, True),
+    (5, 7, 512, 64, 16, 128, 0, 1, 1e-6, True, True),
+    (2, 40, 512, 64, 64, 16, 3, 1, 0.0, False, True),      # no norm
+    (2, 6, 512, 0, 7, 0, 0, 1, 0.0, False, False),         # neither norm nor rotation: ties are real
+    (2, 5, 224, 24, 9, 6, 1, 2, 1e-6, True, False),
+    (1, 3, 1024, 1024, 2, 0, 0, 1, 1e-6, True, False),
+    (64, 64, 512, 64, 24, 0, 5, 1, 1e-6, True, False),     # enough rows that some are near a border
+]
+
+
+def append_reference(x, w, eps, rd, tab, first, lens, step, base, window, codes, exps, bt, y):
+    b, s, d = x.shape
+    page = codes.shape[1]
+    z = f64(x)
+    if eps:
+        z = normed(z, None if w is None else f64(w), np.float64(np.float32(eps)))
+    i = first.numpy()[:, None].astype(np.int64) + np.arange(s)
+    if rd:
+        z = rotate(z, f64(tab)[i * step])
+    code, k = quantise(z)
+    codes, exps, y = codes.numpy().copy(), exps.numpy().copy(), f64(y)
+    n = np.full(b, s) if lens is None else lens.numpy()
+    for bi in range(b):
+        for t in range(n[bi]):
+            y[bi, t] = values(code[bi, t], k[bi, t])
+            if window and t < n[bi] - window:
+                continue
+            r = base + (i[bi, t] % window if window else i[bi, t])
+            pg = bt.numpy()[bi, r // page]
+            codes[pg, r % page], exps[pg, r % page] = pack(code[bi, t]), k[bi, t]
+    return codes, exps, y
+
+
+@gpu
+@pytest.mark.parametrize("b,s,d,rd,page,window,base,step,eps,weight,ragged", APPENDS)
+def test_append(ds, b, s, d, rd, page, window, base, step, eps, weight, ragged):
+    g = torch.Generator().manual_seed(d + s)
+    wide = (torch.randn((b, s, d + 8), generator=g) * 2).to(torch.bfloat16)
+    wide[0, 0, :32] = 0                                        # a block of zeros: the floor's scale
+    x = wide[..., :d]
+    w = torch.randn((d,), generator=g) if weight else None
+    first = torch.randint(0, 50, (b,), generator=g, dtype=torch.int32)
+    lens = torch.randint(0, s + 1, (b,), generator=g, dtype=torch.int32) if ragged else None
+    tab = table_of((50 + s) * step, rd, 1.25) if rd else None
+    codes, exps, bt = random_pool(g, b, base + (window or 50 + s), page, d)
+    y = torch.full((b, s, d), 7.0, dtype=torch.bfloat16)
+    want = append_reference(x, w, eps, rd, tab, first, lens, step, base, window, codes, exps, bt, y)
+    cg, eg, btg, fg, wg, lg, tg, yg = dev(codes, exps, bt, first, w, lens, tab, y)
+    args = dict(rd=rd, table=tg, eps=eps, weight=wg, lens=lg, pos_step=step, base=base, window=window)
+    ds.kv_append_fp4_paged(wide.cuda()[..., :d], cg, eg, btg, fg, y=yg, **args)
+    assert ds.device_status() == 0
+    np.testing.assert_array_equal(eg.cpu().numpy(), want[1])
+    np.testing.assert_array_equal(cg.cpu().numpy(), want[0])
+    np.testing.assert_array_equal(f64(yg), want[2])
+    # without y, and with y in place of x
+    c2, e2 = dev(codes, exps)
+    ds.kv_append_fp4_paged(wide.cuda()[..., :d], c2, e2, btg, fg, **args)
+    assert torch.equal(c2, cg) and torch.equal(e2, eg)
+    c3, e3, x3 = dev(codes, exps, x.contiguous())
+    ds.kv_append_fp4_paged(x3, c3, e3, btg, fg, y=x3, **args)
+    assert torch.equal(c3, cg) and torch.equal(e3, eg)
+    live = np.ones((b, s), bool) if lens is None else np.arange(s) < lens.numpy()[:, None]
+    assert (f64(x3)[live] == want[2][live]).all() and (f64(x3)[~live] == f64(x)[~live]).all()
+
+
+@gpu
+def test_append_ties_and_scales(ds):
+    """Every border between two codes at every scale, exactly and one bf16 step to either side."""
+    borders = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    rows = []
+    for k in (-15, -8, 0, 5, 60, 120):
+        near = torch.from_numpy(borders * 2.0 ** k).to(torch.bfloat16).view(torch.int16)
+        v = torch.cat([(near + j).view(torch.bfloat16) for j in (-1, 0, 1)])
+        for top in (6.0, 4.0, 3.0):        # 3 * 2^k is the next smaller scale's largest value
+            for edge in (-1, 0, 1):
+                t = (torch.tensor([top * 2.0 ** k]).to(torch.bfloat16).view(torch.int16) + edge).view(torch.bfloat16)
+                rows.append(torch.cat([t, v, -v])[:32])
+    x = torch.stack([torch.nn.functional.pad(r, (0, 32 - len(r))) for r in rows])[None]
+    n = x.shape[1]
+    codes = torch.zeros((n, 1, 16), dtype=torch.uint8)
+    exps = torch.zeros((n, 1, 1), dtype=torch.int8)
+    bt = torch.arange(n, dtype=torch.int32)[None]
+    y = torch.zeros_like(x)
+    want = append_reference(x, None, 0.0, 0, None, ints(0), None, 1, 0, 0, codes, exps, bt, y)
+    cg, eg, btg, fg, yg = dev(codes, exps, bt, ints(0), y)
+    ds.kv_append_fp4_paged(x.cuda(), cg, eg, btg, fg, y=yg)
+    np.testing.assert_array_equal(eg.cpu().numpy(), want[1])
+    np.testing.assert_array_equal(cg.cpu().numpy(), want[0])
+    np.testing.assert_array_equal(f64(yg), want[2])
+
+
+@gpu
+def test_append_bad_pages_and_positions(ds):
+    x = torch.randn((6, 2, 64)).to(torch.bfloat16).cuda()
+    codes = torch.full((4, 2, 32), 9, dtype=torch.uint8, device="cuda")
+    exps = torch.full((4, 2, 2), 9, dtype=torch.int8, device="cuda")
+    bt = torch.tensor([[0], [4], [-1], [1], [2], [3]], dtype=torch.int32, device="cuda")
+    tab = table_of(100, 16).cuda()
+    y = torch.full_like(x, 5.0)
+    # sequence 3 starts past its only page, 4 at a negative row, 5 at the table's end
+    ds.kv_append_fp4_paged(x, codes, exps, bt, ints(0, 0, 0, 2, -2, 99).cuda(), rd=16, table=tab, eps=1e-6, y=y)
+    assert ds.device_status() == ds.DS_DEV_BAD_INDEX
+    touched = [[bool((exps[p, r] != 9).any()) for r in range(2)] for p in range(4)]
+    assert touched == [[True, True], [False, False], [False, False], [False, False]]
+    assert (codes[1:] == 9).all()
+    # the rows themselves are known wherever the position is: y is written, the page is what is missing
+    assert [(y[i] != 5.0).any(-1).tolist() for i in range(6)] == [[True, True]] * 4 + [[False, False], [True, False]]
+
+
+# ---- attention -------------------------------------------------------------------------------------------
+
+ATTNS = [  # b, m, h, rows, topk, neg, page, rd
+    (1, 1, 1, 1, 1, 0.0, 1, 0),
+    (1, 1, 4, 7, 3, 0.0, 4, 16),
+    (2, 1, 64, 128, 128, 0.0, 64, 64),
+    (3, 2, 33, 500, 129, 0.3, 24, 64),
+    (1, 1, 64, 300, 127, 0.0, 7, 0),
+    (2, 3, 65, 400, 200, 0.1, 16, 64),
+    (5, 1, 128, 700, 640, 0.05, 64, 64),
+    (1, 1, 16, 9000, 2300, 0.02, 64, 512),
+    (40, 4, 20, 300, 140, 0.5, 10, 8),
+    (1, 2, 100, 3000, 1500, 0.9, 48, 64),
+    (300, 1, 5, 40, 33, 0.2, 8, 64),
+    (2, 1, 70, 20, 400, 0.0, 6, 64),        # the same row many times
+]
+
+
+def check_attention(ds, q, codes, exps, bt, sink, idx, rd=0, first=None, tab=None, scale=None, sample=None, **more):
+    b, m, h, d = q.shape
+    page = codes.shape[1]
+    scale = d ** -0.5 if scale is None else scale
+    qg, cg, eg, btg, sg, ig, fg, tg = dev(q, codes, exps, bt, sink, idx, first, tab)
+    o = ds.sparse_attn_fp4_paged(qg, cg, eg, btg, sg, ig, scale, rd=rd, table=tg, first=fg, **more)
+    assert ds.device_status() == 0
+    got = f64(o)
+    assert np.isfinite(got).all()
+    toks = [(i, t) for i in range(b) for t in range(m)]
+    if sample and len(toks) > sample:
+        toks = [toks[j] for j in np.random.RandomState(3).choice(len(toks), sample, replace=False)]
+    for i, t in toks:
+        ix = idx[i, t].numpy()
+        rows = logical_rows(codes, exps, bt, i, ix, page)
+        ref, A, F = attention(f64(q[i, t]), rows, ix >= 0, f64(sink), scale)
+        if rd:
+            ref = rotate(ref, f64(tab)[int(first[i]) + t], inverse=True)
+            A, F = pair_sum(A, rd), pair_sum(F, rd)
+        tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * A + 2.0 ** -20 * F + 2.0 ** -126
+        bad = np.abs(got[i, t] - ref) > tol
+        assert not bad.any(), (i, t, int(bad.sum()), float(np.abs(got[i, t] - ref)[bad].max()))
+    return o
+
+
+def attention_inputs(seed, b, m, h, rows, topk, neg, page, rd, d=512, qscale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    codes, exps, bt = random_pool(g, b, rows, page, d)
+    q = (torch.randn((b, m, h, d), generator=g) * qscale).to(torch.bfloat16)
+    sink = torch.randn((h,), generator=g)
+    if topk <= rows:
+        idx = torch.stack([torch.randperm(rows, generator=g)[:topk] for _ in range(b * m)]).view(b, m, topk)
+    else:
+        idx = torch.randint(0, rows, (b, m, topk), generator=g)
+    idx = torch.where(torch.rand((b, m, topk), generator=g) < neg, -1, idx).to(torch.int32)
+    first = torch.randint(0, 64, (b,), generator=g, dtype=torch.int32) if rd else None
+    tab = table_of(64 + m, rd) if rd else None
+    return q, codes, exps, bt, sink, idx, rd, first, tab
+
+
+@gpu
+@pytest.mark.parametrize("b,m,h,rows,topk,neg,page,rd", ATTNS)
+def test_attention(ds, b, m, h, rows, topk, neg, page, rd):
+    x = attention_inputs(b + m + h, b, m, h, rows, topk, neg, page, rd)
+    o = check_attention(ds, *x, sample=60)
+    # the same call again, into given buffers, gives the same
+    need = ds.sparse_attn_fp4_paged_workspace_bytes(b, m, h, 512, topk)
+    ws = torch.randint(0, 256, (max(need, 16),), dtype=torch.uint8, device="cuda")
+    again = check_attention(ds, *x, sample=1, o=torch.full_like(o, float("nan")), workspace=ws)
+    assert torch.equal(again, o)
+
+
+@gpu
+def test_attention_rows_without_entries(ds):
+    q, codes, exps, bt, sink, idx, rd, first, tab = attention_inputs(5, 4, 3, 40, 200, 150, 0.1, 16, 64)
+    idx[0, 1] = -1
+    idx[2] = -1
+    idx[3, 2, 1:] = -7
+    o = check_attention(ds, q, codes, exps, bt, sink, idx, rd, first, tab)
+    assert (o[0, 1] == 0).all() and (o[2] == 0).all()
+    # nothing at all to attend to
+    idx[:] = -1
+    assert (check_attention(ds, q, codes, exps, bt, sink, idx, rd, first, tab) == 0).all()
+    none = ds.sparse_attn_fp4_paged(*dev(q, codes, exps, bt, sink, idx[..., :0].contiguous()), 0.1)
+    assert (none == 0).all()
+    assert ds.sparse_attn_fp4_paged(*dev(q[:0], codes, exps, bt[:0], sink, idx[:0]), 0.1).shape == (0, 3, 40, 512)
+
+
+@gpu
+@pytest.mark.parametrize("h", [3, 64, 128])
+def test_attention_peaked_growing_and_flat(ds, h):
+    """Scores whose maximum moves through the row, one row far above the rest, and equal scores."""
+    q, codes, exps, bt, sink, idx, *_ = attention_inputs(9, 2, 1, h, 1000, 900, 0.0, 32, 0)
+    idx = idx.sort(-1).values
+    for qs in (8.0, 40.0):
+        check_attention(ds, (q.float() * qs).to(torch.bfloat16), codes, exps, bt, sink, idx)
+    check_attention(ds, torch.zeros_like(q), codes, exps, bt, sink, idx)
+    up = exps.clone()                                     # rows whose scale grows with their number
+    for i in range(2):
+        for r in range(1000):
+            up[bt[i, r // 32], r % 32] = -6 + r // 100
+    check_attention(ds, q, codes, up, bt, sink, idx)
+    down = exps.clone()
+    for i in range(2):
+        for r in range(1000):
+            down[bt[i, r // 32], r % 32] = 4 - r // 100
+    check_attention(ds, q, codes, down, bt, sink, idx)
+    # heads of very different size, and values within a head too
+    check_attention(ds, (q * torch.logspace(-4, 1, h)[:, None]).to(torch.bfloat16), codes, exps, bt, sink, idx)
+    check_attention(ds, (q * torch.logspace(-6, 0, 512)).to(torch.bfloat16), codes, exps, bt, sink, idx)
+
+
+@gpu
+def test_attention_sinks(ds):
+    q, codes, exps, bt, sink, idx, *_ = attention_inputs(11, 2, 2, 30, 300, 200, 0.1, 16, 0)
+    check_attention(ds, q, codes, exps, bt, torch.full_like(sink, -math.inf), idx)
+    check_attention(ds, q, codes, exps, bt, torch.full_like(sink, 30.0), idx)
+    o = check_attention(ds, q, codes, exps, bt, torch.full_like(sink, 300.0), idx)
+    assert (o.abs() < 1e-30).all()
+
+
+@gpu
+def test_attention_scale_spread_within_a_row(ds):
+    """Blocks of one row 24 octaves apart, rows of zeros, and exponents far from 0."""
+    q, codes, exps, bt, sink, idx, *_ = attention_inputs(13, 2, 1, 24, 300, 200, 0.0, 16, 0)
+    wide = exps.clone()
+    wide[..., 1::2] = -24
+    wide[..., 0::2] = 0
+    check_attention(ds, q, codes, wide, bt, sink, idx)
+    zero = codes.clone()
+    zero[::2] = 0
+    check_attention(ds, q, zero, exps, bt, sink, idx)
+    zero[:] = 0x88                                         # minus zero
+    assert (check_attention(ds, q, zero, exps, bt, sink, idx) == 0).all()
+    for k in (-60, 40):
+        check_attention(ds, (q.float() * 2.0 ** -k).to(torch.bfloat16), codes, (exps + k), bt, sink, idx)
+
+
+@gpu
+def test_attention_bad_entries(ds):
+    q, codes, exps, bt, sink, idx, rd, first, tab = attention_inputs(15, 3, 1, 40, 200, 150, 0.1, 16, 64)
+    o = check_attention(ds, q, codes, exps, bt, sink, idx, rd, first, tab)
+    bad = torch.cat((idx, torch.full((3, 1, 3), 13 * 16, dtype=torch.int32)), -1)   # past the table's 13 pages
+    bad[..., -1] = 2 ** 31 - 1
+    args = dev(q, codes, exps, bt, sink)
+    got = ds.sparse_attn_fp4_paged(*args, bad.cuda(), 512 ** -0.5, rd=rd, table=tab.cuda(), first=first.cuda())
+    assert ds.device_status() == ds.DS_DEV_BAD_INDEX
+    assert (got.float() - o.float()).abs().max() <= 2.0 ** -7 * o.float().abs().max()
+    hole = bt.clone()
+    hole[1, :] = -1
+    hole[2, :] = codes.shape[0]
+    got = ds.sparse_attn_fp4_paged(args[0], args[1], args[2], hole.cuda(), sink.cuda(), idx.cuda(), 512 ** -0.5)
+    assert ds.device_status() == ds.DS_DEV_BAD_INDEX
+    assert (got[1:] == 0).all() and (got[0] != 0).any()
+    # a position outside the table: that token is not rotated
+    far = first.clone()
+    far[1] = 1000
+    got = ds.sparse_attn_fp4_paged(*args, idx.cuda(), 512 ** -0.5, rd=rd, table=tab.cuda(), first=far.cuda())
+    plain = ds.sparse_attn_fp4_paged(*args, idx.cuda(), 512 ** -0.5)
+    assert ds.device_status() == ds.DS_DEV_BAD_INDEX
+    assert torch.equal(got[1], plain[1]) and torch.equal(got[0], o[0]) and torch.equal(got[2], o[2])
+
+
+# ---- together ----------------------------------------------------------------------------------------------
+
+@gpu
+def test_step_together_and_in_a_graph(ds):
+    """A prompt and decode steps of two sequences at positions of their own, through path.decode_step_fp4_paged;
+    the last step captured, and replayed for the next position."""
+    from sparse_latent_attention_attn_gb300 import path
+    g = torch.Generator().manual_seed(3)
+    b, h, d, rd, W, page, ratio = 2, 24, 512, 64, 16, 5, 4
+    eps, scale = 1e-6, d ** -0.5
+    rows = W + 20
+    codes, exps, bt = random_pool(g, b, rows, page, d)
+    codes.zero_(), exps.zero_()
+    tab = table_of(128, rd)
+    w = 1 + 0.1 * torch.randn((d,), generator=g)
+    sink = torch.randn((h,), generator=g)
+    comp = torch.randn((b, 9, d), generator=g).to(torch.bfloat16)
+    cg, eg, btg, tg, wg, sg = dev(codes, exps, bt, tab, w, sink)
+    ds.kv_append_fp4_paged(comp.cuda(), cg, eg, btg, ints(0, 0).cuda(), rd=rd, table=tg, eps=eps, weight=wg,
+                           lens=ints(9, 4).cuda(), pos_step=ratio, base=W)
+    ref_c, ref_e, _ = append_reference(comp, w, eps, rd, tab, ints(0, 0), ints(9, 4), ratio, W, 0, codes, exps, bt,
+                                       torch.zeros_like(comp))
+    ncomp = [9, 4]
+    prompt = torch.randn((b, 20, d), generator=g).to(torch.bfloat16)
+    n0 = ints(20, 7)
+    ds.kv_append_fp4_paged(prompt.cuda(), cg, eg, btg, ints(0, 0).cuda(), rd=rd, table=tg, eps=eps, weight=wg,
+                           lens=n0.cuda(), window=W)
+    ref_c, ref_e, _ = append_reference(prompt, w, eps, rd, tab, ints(0, 0), n0, 1, 0, W, torch.from_numpy(ref_c),
+                                       torch.from_numpy(ref_e), bt, torch.zeros_like(prompt))
+    first = n0.clone()
+    static = {"q": torch.zeros((b, 1, h, d), dtype=torch.bfloat16, device="cuda"),
+              "kv": torch.zeros((b, 1, d), dtype=torch.bfloat16, device="cuda"),
+              "first": torch.zeros((b,), dtype=torch.int32, device="cuda"),
+              "idx": torch.full((b, 1, W + 10), -1, dtype=torch.int32, device="cuda")}
+
+    def step():
+        return path.decode_step_fp4_paged(static["q"], static["kv"], cg, eg, btg, static["first"], sg, static["idx"],
+                                          W, scale, rd, tg, eps, kv_weight=wg)
+
+    graph = out = None
+    side = torch.cuda.Stream()
+    for n in range(4):
+        q = torch.randn((b, 1, h, d), generator=g).to(torch.bfloat16)
+        kv = torch.randn((b, 1, d), generator=g).to(torch.bfloat16)
+        idx = torch.full((b, 1, W + 10), -1, dtype=torch.int32)
+        for i in range(b):
+            idx[i, 0, :W] = torch.where(torch.arange(W) <= first[i], torch.arange(W), -1)
+            idx[i, 0, W:W + ncomp[i]] = W + torch.arange(ncomp[i])
+        for k, v in (("q", q), ("kv", kv), ("first", first), ("idx", idx)):
+            static[k].copy_(v)
+        torch.cuda.synchronize()
+        if n < 2:
+            with torch.cuda.stream(side):
+                got = step()
+            side.synchronize()
+        else:
+            if graph is None:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    out = step()
+            graph.replay()
+            torch.cuda.synchronize()
+            got = out
+        ref_c, ref_e, _ = append_reference(kv, w, eps, rd, tab, first, None, 1, 0, W, torch.from_numpy(ref_c),
+                                           torch.from_numpy(ref_e), bt, torch.zeros_like(kv))
+        np.testing.assert_array_equal(cg.cpu().numpy(), ref_c)
+        np.testing.assert_array_equal(eg.cpu().numpy(), ref_e)
+        for i in range(b):
+            zq = rotate(normed(f64(q[i, 0]), None, eps), f64(tab)[int(first[i])][None])
+            zq = f64(torch.from_numpy(zq).to(torch.bfloat16))
+            ix = idx[i, 0].numpy()
+            rr = logical_rows(torch.from_numpy(ref_c), torch.from_numpy(ref_e), bt, i, ix, page)
+            ref, A, F = attention(zq, rr, ix >= 0, f64(sink), scale)
+            ref = rotate(ref, f64(tab)[int(first[i])][None], inverse=True)
+            A, F = pair_sum(A, rd), pair_sum(F, rd)
+            # beside the attention's own: q may be one bf16 step off where the norm's f32 falls on the other
+            # side of a border; its effect is far below a step of all 512 products together
+            tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -10) * A + 2.0 ** -20 * F
+            assert (np.abs(f64(got[i, 0]) - ref) <= tol).all()
+        first += 1
+    assert ds.device_status() == 0
+
+
+# ---- refusals, no GPU needed ---------------------------------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def lib():
+    from sparse_latent_attention_attn_gb300 import build
+    build.build()
+    from sparse_latent_attention_attn_gb300 import dsattn
+    return dsattn._lib
+
+
+FAKE = 4096   # never dereferenced: every call below fails its checks first
+
+
+def call(fn, base, /, **change):
+    args = {**base, **change}
+    return fn(*args.values())
+
+
+def test_norm_rotary_refusals(lib):
+    base = dict(x=FAKE, xb=512, xt=512, y=FAKE, b=2, s=1, h=8, d=64, w=None, eps=1e-6, rd=16, table=FAKE, rows=10,
+                first=FAKE, lens=None, stream=None)
+    f = lib.ds_norm_rotary
+    for bad in (dict(b=-1), dict(s=-1), dict(h=0), dict(d=0), dict(d=60), dict(eps=0.0), dict(eps=-1.0),
+                dict(eps=float("nan")), dict(rd=12), dict(rd=-8), dict(rd=72), dict(table=None), dict(table=FAKE + 4),
+                dict(rows=-1), dict(x=None), dict(x=FAKE + 8), dict(y=None), dict(y=FAKE + 2), dict(first=None),
+                dict(first=FAKE + 2), dict(lens=FAKE + 1), dict(w=FAKE + 2), dict(xb=511), dict(xb=504), dict(xb=-512),
+                dict(s=2, xt=504)):
+        assert call(f, base, **bad) == -1, bad
+    assert call(f, base, d=1032, xb=8 * 1032) == -2
+    assert call(f, base, b=1 << 20, s=1 << 10, h=2) == -2
+    assert call(f, base, b=0, x=None, y=None, first=None) == 0
+    assert call(f, base, s=0, x=None, y=None, first=None) == 0
+
+
+def test_append_refusals(lib):
+    base = dict(x=FAKE, xb=64, xt=64, y=None, b=2, s=1, d=64, w=None, eps=1e-6, rd=16, table=FAKE, rows=10, first=FAKE,
+                lens=None, step=1, base=0, window=8, codes=FAKE, exps=FAKE, pages=4, page=16, bt=FAKE, mp=1, stream=None)
+    f = lib.ds_kv_append_fp4_paged
+    for bad in (dict(b=-1), dict(s=-1), dict(d=0), dict(d=48), dict(eps=-1.0), dict(eps=float("nan")), dict(step=0),
+                dict(base=-1), dict(window=-1), dict(rd=12), dict(rd=72), dict(table=None), dict(table=FAKE + 4),
+                dict(pages=-1), dict(page=0), dict(mp=-1), dict(x=None), dict(x=FAKE + 8), dict(y=FAKE + 8),
+                dict(first=None), dict(lens=FAKE + 2), dict(w=FAKE + 2), dict(codes=None), dict(codes=FAKE + 4),
+                dict(exps=None), dict(bt=None), dict(bt=FAKE + 2), dict(xb=60), dict(xb=56), dict(s=2, xb=128, xt=56)):
+        assert call(f, base, **bad) == -1, bad
+    assert call(f, base, d=1056, xb=1056, xt=1056) == -2
+    assert call(f, base, pages=1 << 27) == -2
+    assert call(f, base, b=1 << 16, s=1 << 16) == -2
+    assert call(f, base, b=0, x=None, codes=None, exps=None, bt=None, first=None) == 0
+
+
+def test_attention_refusals(lib):
+    base = dict(q=FAKE, codes=FAKE, exps=FAKE, pages=4, page=16, bt=FAKE, mp=1, sink=FAKE, idx=FAKE, topk=4, scale=0.1,
+                o=FAKE, b=1, m=1, h=4, d=512, ws=None, wsb=0, rd=0, table=None, rows=0, first=None, stream=None)
+    f = lib.ds_sparse_attn_fp4_paged
+    for bad in (dict(b=-1), dict(m=-1), dict(h=0), dict(topk=-1), dict(pages=-1), dict(page=0), dict(mp=-1),
+                dict(q=None), dict(q=FAKE + 8), dict(o=None), dict(o=FAKE + 8), dict(sink=None), dict(sink=FAKE + 2),
+                dict(idx=None), dict(idx=FAKE + 2), dict(codes=None), dict(codes=FAKE + 8), dict(exps=None),
+                dict(exps=FAKE + 8), dict(bt=None), dict(bt=FAKE + 1), dict(rd=12, table=FAKE, rows=9, first=FAKE),
+                dict(rd=520, table=FAKE, rows=9, first=FAKE), dict(rd=16, rows=9, first=FAKE),
+                dict(rd=16, table=FAKE + 4, rows=9, first=FAKE), dict(rd=16, table=FAKE, rows=9),
+                dict(rd=16, table=FAKE, rows=9, first=FAKE + 2)):
+        assert call(f, base, **bad) == -1, bad
+    for bad in (dict(d=256), dict(h=129), dict(pages=1 << 27)):
+        assert call(f, base, **bad) == -2, bad
+    assert call(f, base, b=0, q=None, o=None, sink=None) == 0
+    w = lib.ds_sparse_attn_fp4_paged_workspace_bytes
+    assert w(1, 1, 4, 256, 8) == 0 and w(1, 1, 129, 512, 8) == 0 and w(-1, 1, 4, 512, 8) == 0
+
+
+def test_bindings_refuse_cpu_tensors_and_shapes(lib):
+    from sparse_latent_attention_attn_gb300 import dsattn
+    x = torch.zeros((1, 1, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        dsattn.norm_rotary(x, 1e-6, 0, None, ints(0))
+    with pytest.raises(TypeError):
+        dsattn.norm_rotary(x.float(), 1e-6, 0, None, ints(0))
+    with pytest.raises(ValueError, match="CUDA"):
+        dsattn.kv_append_fp4_paged(x[:, 0], torch.zeros((1, 1, 32), dtype=torch.uint8),
+                                   torch.zeros((1, 1, 2), dtype=torch.int8), ints(0).view(1, 1), ints(0))
+    with pytest.raises(ValueError, match="CUDA"):
+        dsattn.sparse_attn_fp4_paged(x, torch.zeros((1, 1, 32), dtype=torch.uint8),
+                                     torch.zeros((1, 1, 2), dtype=torch.int8), ints(0).view(1, 1), torch.zeros(2),
+                                     torch.zeros((1, 1, 1), dtype=torch.int32), 0.1)
+
+
+def test_the_plain_quantiser():
+    """The tests' own quantiser: ties to even, the smallest scale that holds the block."""
+    z = np.zeros((1, 32))
+    z[0, :8] = [6.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]
+    z[0, 8:] = -0.3
+    code, k = quantise(z)
+    assert k.tolist() == [[0]] and code[0, :8].tolist() == [7, 0, 2, 2, 4, 4, 6, 6] and (code[0, 8:] == 9).all()
+    assert quantise(np.full((1, 32), 6.01))[1].tolist() == [[1]] and quantise(np.full((1, 32), 3.0))[1].tolist() == [[-1]]
+    assert quantise(np.zeros((1, 32)))[1].tolist() == [[-15]]
