@@ -423,9 +423,10 @@ int ds_kv_append_fp4_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstri
  * idx [b][m][topk] lists logical rows; entries < 0 are skipped, entries without a page are skipped
  * and flagged.  Otherwise the operation is ds_sparse_attn's on the decoded rows: duplicates count as
  * often as they are listed, a query without rows gives o = 0.  Scores, softmax and accumulation
- * are f32, the probabilities enter the value product with at least bf16's precision, and the
- * rotation of position first[bi] + t is applied before o's one rounding (a position outside the
- * table leaves that token's o unrotated).
+ * are f32, and the rotation of position first[bi] + t is applied before o's one rounding (a
+ * position outside the table leaves that token's o unrotated).  A probability enters the value
+ * product rounded by at most 2^-8 of itself (as bf16) or, where that is more, by 2^-17 of the
+ * head's largest, times 2^(E - e) for a row whose largest exponent e is below the list's, E.
  * Within a row, blocks whose exponent is more than 26 below the row's largest count as zeros (2^-26
  * of the row's scale).  Exponents must lie in [-126, 126], and scores must be finite in f32.
  *

@@ -102,6 +102,7 @@ struct IndexerArgs {
 int launch_indexer_scores(const IndexerArgs &a, float *scores, int64_t ld, cudaStream_t stream);
 int launch_indexer_select(const float *scores, int64_t ld, const IndexerArgs &a, int32_t *idx, cudaStream_t stream);
 void set_test_stall(bool on);
+bool test_stall();
 size_t sparse_attn_tc_workspace_bytes(int b, int m, int h, int d, int topk, bool pair = false);
 int pair_union_cap(int topk);
 int launch_pair_union(const int32_t *idx, int b, int m, int topk, int64_t n, int32_t *uidx, unsigned int *status,

@@ -1,114 +1,962 @@
-// sparse_attn_fp4.cu -- sparse_attn over a paged cache of 4-bit rows.
+// sparse_attn_fp4.cu -- sparse_attn over a paged cache of 4-bit rows, on 8-bit tensor-core operands.
 //
 // "Module attn", sparse_attn and the Precision paragraph: softmax over the index-listed rows of the shared
 // latent tensor with a sink in the denominator, the rows reused as values, f32 arithmetic, bf16 output;
 // "DeepSeek V4.1", attention/query-latent, Attention.forward (the output's inverse rotation).  Rows are
 // e2m1 codes with a power-of-two scale per 32 values, reached through a table of pages.
 //
-// A plain kernel: one warp per head, eight heads of a token to a block; the block decodes 16 listed rows
-// to f32 in shared memory, and each warp scores and accumulates them with a running maximum and sum.
+// The mathematics.  A row is v_r = 2^(e_r - 13) c_r, e_r its largest block exponent and c_r its codes times
+// 2^(k - e_r + 13): e2m1 has one mantissa bit, so c_r is exact in e5m2 for blocks down to 26 octaves below
+// e_r (lower ones count as zeros).  One byte a value serves as key and as value, and the row's own power
+// of two moves to where the row is a single number: to its scores, and to its probability.
+//  * q = 2^g (hi + 2^-5 lo), hi and lo in e4m3: hi holds q's top four significant bits, lo the four below
+//    them, so a bf16 q (eight) is exact down to 2^-9 of its head's largest value and off by 2^-22 of that
+//    largest value below.  S^T = C [hi | lo]: M = 128 rows, N = 64 heads twice, and the score is
+//    (S_hi + 2^-5 S_lo) 2^(g + e_r - 13) scale.
+//  * P' = 2^(s - m + e_r - E + 4) for running m (per head, lazily raised, at most 4 octaves late) and E (the
+//    largest e_r so far), at most 256; P' = hi - lo with hi in e4m3 and lo in e5m2, each to nearest: off by
+//    2^-8 of itself, as bf16 would be, from 2^-6 on (hi has four bits, lo three of the rest), and by 2^-13
+//    below (hi is a multiple of 2^-9): 2^-17 of the largest probability of a head.  O^T += C^T (hi - lo), d = 512 as four blocks of 128 lanes, heads as
+//    columns; O 2^(E - 17) / l is the output.  l sums the unrounded f32 p.
+//
+// Why so.  A tile is 128 rows of 512 bytes, so two tiles, q (64 KB as hi and lo) and P fit the 227 KB of an
+// SM; as bf16 only tiles of 64 rows would, and a 64-row tcgen05.mma takes the time of a 128-row one.  With
+// N = 128 in S and K = 32 a step a tile takes 16 + 32 instructions where bf16 rows would take 64 + 64.  The
+// widening to e5m2 is a table of 8 bytes per block: byte permutes with the code words as selectors.
+//
+// Warps: 0-7 softmax and epilogue (warp w: TMEM lanes 32 (w % 4).., heads 32 (w / 4)..), 8-15 rows (codes
+// loaded a tile ahead into registers, widened into the swizzled stage; q at a unit's first tile), 16 MMA
+// issue, 17 index rows: it drops entries without a row, turns the others into row numbers and hands out
+// tiles of up to 128 through a ring of messages that every role reads in order.
+// A unit is one token and up to 64 heads; units are shared out as in the other attention kernels
+// (attn_split.cuh), and units cut by a range boundary leave f32 partials that a second kernel merges.
+// Every wait is bounded (2 s): then DS_DEV_TIMEOUT is flagged, issued MMAs are drained, TMEM is freed.
+#include <atomic>
+#include <mutex>
+
+#include "attn_split.cuh"
 #include "common.cuh"
+#include "ptx.cuh"
 #include "sparse_attn_fp4.cuh"
 
 namespace dsattn {
 namespace fp4 {
-namespace {
 
-constexpr int D = 512, HG = 8, RT = 16;
+using namespace ptx;
+using split::kMaxCut;
+using split::range_start;
+using split::unit_at;
+
+constexpr int D = 512;
+constexpr int HM = 64;                  // heads of a unit
+constexpr int BN = 128;                 // rows of a tile
+constexpr int NPAN = D / 128;           // panels of 128 columns
+constexpr int PANEL = BN * 128;         // bytes of a panel: 128 rows (of C or of [hi | lo]) of 128
+constexpr int STAGE = NPAN * PANEL;     // 64 KB
+constexpr int NR = 3;                   // index messages
+constexpr int SM_Q = 0;
+constexpr int SM_KV = SM_Q + STAGE;
+constexpr int SM_P = SM_KV + 2 * STAGE;
+constexpr int P_BYTES = BN * 128;       // row r: 64 bytes hi, 64 bytes lo
+constexpr int SM_CTL = SM_P + 2 * P_BYTES;
+// control block
+constexpr int C_ROWS = 0;                       // [NR][128] int32 row numbers
+constexpr int C_REXP = C_ROWS + NR * BN * 4;    // [2][128] int8 e_r
+constexpr int C_M = C_REXP + 2 * BN;            // [64] f32 running maximum
+constexpr int C_FAC = C_M + HM * 4;             // [64] f32 rescale factor; at the end 1 / denominator
+constexpr int C_QS = C_FAC + HM * 4;            // [2][64] f32 2^g scale log2(e), by unit parity
+constexpr int C_BAR = C_QS + 2 * HM * 4;
+enum : int {
+    B_MSG = 0,                  // [NR] index -> all: message written
+    B_MSGFREE = B_MSG + NR,     // [NR] all -> index
+    B_KV = B_MSGFREE + NR,      // [2] rows -> MMA, softmax: stage written (and q, at a unit's first tile)
+    B_PV = B_KV + 2,            // [2] MMA -> rows, softmax: P V of the tile done
+    B_S = B_PV + 2,             // [2] MMA -> softmax, rows: scores ready
+    B_SFREE = B_S + 2,          // [2] softmax -> MMA: scores read
+    B_P = B_SFREE + 2,          // [2] softmax -> MMA: P written
+    B_DRAIN = B_P + 2,
+    B_COUNT = B_DRAIN + 1
+};
+constexpr int C_MSG = C_BAR + 8 * B_COUNT;      // [NR] int32 message heads
+constexpr int C_TMEM = C_MSG + 4 * NR;
+constexpr int C_ABORT = C_TMEM + 4;
+constexpr int SMEM_BYTES = SM_CTL + C_ABORT + 4;
+static_assert(C_BAR % 8 == 0 && SMEM_BYTES <= 232448, "shared memory budget");
+
+constexpr int TM_O = 0, TM_S = NPAN * HM, TMEM_COLS = 512;
+static_assert(TM_S + 2 * 2 * HM <= TMEM_COLS, "TMEM budget");
+
+constexpr int W_ROWS = 8, W_MMA = 16, W_IDX = 17, NTHREADS = 576;   // 112 registers a thread
+constexpr int NSOFT = 256;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 4.0f;          // octaves that m may be late
 constexpr uint32_t kAll = 0xffffffffu;
 
-__device__ __forceinline__ float decode1(uint32_t code) {
-    const uint32_t m = code & 7u;
-    const float a = m < 4u ? 0.5f * (float)m : m == 7u ? 6.0f : (float)(m - 2u);
-    return code & 8u ? -a : a;
+// messages: kind | first tile of its unit << 8 | rows << 16
+constexpr int kTile = 1, kEnd = 2, kFin = 3;
+
+// a partial slot (f32): O [64][512], then running maxima [64] (log2 domain, -inf: no row) and sums [64]
+constexpr int SLOT_O = HM * D;
+constexpr size_t SLOT = (size_t)SLOT_O + 2 * HM;
+
+struct Params {
+    Args a;
+    int64_t ntok, nunit;
+    int groups;       // units of a token
+    int G;
+    int seg_cost;
+    bool interleave;
+    float scale_log2;
+    float *ws;
+    int stall_first_tile;
+};
+
+__host__ __device__ constexpr uint32_t idesc8(int M, int N, int afmt, int bfmt, bool mn, bool minus = false) {
+    // kind::f8f6f4: f32 accumulator; formats 0 = e4m3, 1 = e5m2; both operands K-major or MN-major; B negated
+    return (1u << 4) | ((uint32_t)afmt << 7) | ((uint32_t)bfmt << 10) | ((minus ? 1u : 0u) << 14) | ((mn ? 3u : 0u) << 15) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__global__ void __launch_bounds__(HG * 32) plain_kernel(const Args p) {
-    __shared__ float rows[RT][D];
-    __shared__ int64_t slot[RT];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int groups = (p.h + HG - 1) / HG;
-    const int64_t tok = blockIdx.x / groups;
-    const int hh = (int)(blockIdx.x % groups) * HG + warp;
-    const int64_t bi = tok / p.m;
-    const bool live = hh < p.h;
-    float q[16], o[16], mx = -INFINITY, l = 0.0f;
-    for (int i = 0; i < 16; ++i) {
-        o[i] = 0.0f;
-        q[i] = live ? __uint_as_float((uint32_t)p.q[(tok * p.h + hh) * D + lane * 16 + i] << 16) : 0.0f;
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ bool bar_or(bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(pred ? 1u : 0u), "n"(NSOFT)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    const bool ok = mbar_wait(bar, parity, abort, kWaitLimitNs);
+    return __all_sync(kAll, ok);
+}
+
+__device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
+
+// two f32 to e4m3, lo in the low byte; nearest, saturating
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t v) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
+    return r;
+}
+
+// Two probabilities as hi (e4m3) - lo (e5m2): lo from hi - p, which is exact in f32.
+__device__ __forceinline__ void split_p(float p0, float p1, uint32_t &hi, uint32_t &lo) {
+    asm("{\n\t.reg .b32 f;\n\t.reg .b16 h, l, f0, f1;\n\t.reg .f32 r0, r1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h, %3, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 f, h;\n\t"
+        "mov.b32 {f0, f1}, f;\n\t"
+        "sub.rn.f32.f16 r0, f0, %2;\n\t"
+        "sub.rn.f32.f16 r1, f1, %3;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f32 l, r1, r0;\n\t"
+        "cvt.u32.u16 %0, h;\n\t"
+        "cvt.u32.u16 %1, l;\n\t}"
+        : "=r"(hi), "=r"(lo)
+        : "f"(p0), "f"(p1));
+}
+
+// 16 columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Unit of a position in the unit order: groups of a token are neighbours, so that their gathers meet in L2.
+struct Unit {
+    int64_t tok;
+    int h0, nh;
+};
+__device__ __forceinline__ Unit unit_of(const Params &p, int64_t u) {
+    const int64_t t = p.groups == 1 ? u : u >> 1;
+    const int g = p.groups == 1 ? 0 : (int)(u & 1);
+    return {unit_at(t, p.ntok, p.interleave), g * HM, min(HM, p.a.h - g * HM)};
+}
+
+// sin and cos of the output's rotation back, or null
+__device__ __forceinline__ const float2 *rotation_row(const Args &a, int64_t tok, bool flag) {
+    const int64_t pos = (int64_t)__ldg(a.first + tok / a.m) + tok % a.m;
+    if (pos < 0 || pos >= a.table_rows) {
+        if (flag) flag_status(a.status, DS_DEV_BAD_INDEX);
+        return nullptr;
     }
-    for (int j0 = 0; j0 < p.topk; j0 += RT) {
-        __syncthreads();
-        if (threadIdx.x < RT) {
-            int64_t s = -1;
-            const int j = j0 + threadIdx.x;
-            if (j < p.topk) {
-                const int r = p.idx[tok * p.topk + j];
-                if (r >= 0) {
-                    const int pg = r / p.page;
-                    const int id = pg < p.max_pages ? p.block_table[bi * p.max_pages + pg] : -1;
-                    if (id >= 0 && id < p.pages) s = (int64_t)id * p.page + r % p.page;
-                    else flag_status(p.status, DS_DEV_BAD_INDEX);
+    return a.table + pos * (a.rd / 2);
+}
+
+template <bool ROPE>
+__global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    uint8_t *ctl = smem + SM_CTL;
+    auto BAR = [&](int i) -> uint32_t { return base + SM_CTL + C_BAR + 8u * (uint32_t)i; };
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(ctl + C_ABORT);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int T = p.a.topk;
+    const int64_t cid = blockIdx.x;
+    const int64_t e0 = range_start(cid, p.nunit, T, p.seg_cost, p.G);
+    const int64_t e1 = range_start(cid + 1, p.nunit, T, p.seg_cost, p.G);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NR; ++i) {
+            mbar_init(BAR(B_MSG + i), 1);
+            mbar_init(BAR(B_MSGFREE + i), 17);   // 8 softmax warps, 8 row warps, the MMA thread
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(BAR(B_KV + i), 8);
+            mbar_init(BAR(B_PV + i), 1);
+            mbar_init(BAR(B_S + i), 1);
+            mbar_init(BAR(B_SFREE + i), 8);
+            mbar_init(BAR(B_P + i), 8);
+        }
+        mbar_init(BAR(B_DRAIN), 1);
+        *abort_flag = (base & 1023u) != 0;       // the swizzled operands need this alignment
+        fence_mbar_init();
+        grid_launch_dependents();
+    }
+    if (warp == W_MMA) {
+        tmem_alloc(base + SM_CTL + C_TMEM, TMEM_COLS);
+        tmem_relinquish();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl + C_TMEM);
+    grid_dependency_wait();
+    volatile int *msgs = reinterpret_cast<volatile int *>(ctl + C_MSG);
+
+    // message number n, in order; released at once by all readers but the row warps, which still need its rows
+    auto read_msg = [&](uint32_t n, int &msg) -> bool {
+        if (!warp_wait(BAR(B_MSG + n % NR), (n / NR) & 1u, abort_flag)) return false;
+        msg = msgs[n % NR];
+        return true;
+    };
+    auto free_msg = [&](uint32_t n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_MSGFREE + n % NR));
+    };
+
+    if (warp == W_IDX) {
+        // ================================ index rows to tiles of row numbers ================================
+        uint32_t n = 0;
+        auto open = [&]() -> bool {               // the slot of message n is free
+            return n < NR || warp_wait(BAR(B_MSGFREE + n % NR), (n / NR - 1) & 1u, abort_flag);
+        };
+        auto publish = [&](int msg) {
+            if (lane == 0) msgs[n % NR] = msg;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(B_MSG + n % NR));
+            ++n;
+        };
+        bool ok = true, flagged = false;
+        for (int64_t u = T > 0 ? e0 / T : 0; ok && u * T < e1; ++u) {
+            const Unit un = unit_of(p, u);
+            const int64_t bi = un.tok / p.a.m;
+            const int32_t *idx = p.a.idx + un.tok * T;
+            const int32_t *bt = p.a.block_table + bi * p.a.max_pages;
+            const int a = (int)((e0 > u * T ? e0 : u * T) - u * T);
+            const int z = (int)((e1 < (u + 1) * T ? e1 : (u + 1) * T) - u * T);
+            int fill = 0, first = 1 << 8;
+            int nxt[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) nxt[k] = a + 32 * k + lane < z ? __ldg(idx + a + 32 * k + lane) : -1;
+            ok = open();
+            for (int j = a; ok && j < z; j += 128) {
+                int row[4], pg[4];
+                bool bad = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t r = (uint32_t)nxt[k];
+                    const uint32_t q = r / (uint32_t)p.a.page;
+                    row[k] = nxt[k] < 0 ? -1 : (int)(r - q * (uint32_t)p.a.page);
+                    pg[k] = nxt[k] < 0 ? 0 : q < (uint32_t)p.a.max_pages ? __ldg(bt + q) : -1;
+                    const int jj = j + 128 + 32 * k + lane;
+                    nxt[k] = jj < z ? __ldg(idx + jj) : -1;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (row[k] >= 0) {
+                        if (pg[k] < 0 || pg[k] >= p.a.pages) {
+                            bad = true;
+                            row[k] = -1;
+                        } else {
+                            row[k] += pg[k] * p.a.page;
+                        }
+                    }
+                    const uint32_t have = __ballot_sync(kAll, row[k] >= 0);
+                    const int at = fill + __popc(have & lanemask_lt()), total = fill + __popc(have);
+                    int32_t *slot = reinterpret_cast<int32_t *>(ctl + C_ROWS) + (n % NR) * BN;
+                    if (row[k] >= 0 && at < BN) slot[at] = row[k];
+                    fill = total;
+                    if (total >= BN) {
+                        publish(kTile | first | (BN << 16));
+                        first = 0;
+                        ok = ok && open();
+                        slot = reinterpret_cast<int32_t *>(ctl + C_ROWS) + (n % NR) * BN;
+                        if (ok && row[k] >= 0 && at >= BN) slot[at - BN] = row[k];
+                        fill = total - BN;
+                    }
+                }
+                if (bad && !flagged) {
+                    flag_status(p.a.status, DS_DEV_BAD_INDEX);
+                    flagged = true;
                 }
             }
-            slot[threadIdx.x] = s;
+            if (ok && fill > 0) {
+                publish(kTile | first | (fill << 16));
+                ok = open();
+            }
+            if (ok) publish(kEnd);
         }
-        __syncthreads();
-        for (int e = threadIdx.x; e < RT * D / 2; e += HG * 32) {
-            const int r = e / (D / 2), c = e % (D / 2);
-            if (slot[r] < 0) continue;
-            const uint32_t v = p.codes[slot[r] * (D / 2) + c];
-            const float sc = exp2f((float)p.exps[slot[r] * (D / 32) + c / 16]);
-            rows[r][2 * c] = decode1(v & 15u) * sc;
-            rows[r][2 * c + 1] = decode1(v >> 4) * sc;
+        if (ok && open()) publish(kFin);
+    } else if (warp >= W_ROWS && warp < W_ROWS + 8) {
+        // ======================== rows (and q) into the swizzled operands ========================
+        const int g = warp - W_ROWS, u = lane & 15, half = lane >> 4;
+        const int panel = u >> 2, c0 = (u & 3) * 2;
+        int64_t unit = T > 0 ? e0 / T : 0;
+        uint32_t J = 0, seg = 0;
+        for (uint32_t n = 0;; ++n) {
+            int msg = 0;
+            if (!read_msg(n, msg)) break;
+            const int kind = msg & 255, count = msg >> 16;
+            const bool first = (msg >> 8) & 1;
+            if (kind == kFin) break;
+            if (kind == kEnd) {
+                free_msg(n);
+                ++unit;
+                continue;
+            }
+            // the tile's codes, 16 bytes (one block) of two rows a step, in flight until the stage is free
+            const int32_t *rows = reinterpret_cast<const int32_t *>(ctl + C_ROWS) + (n % NR) * BN + 16 * g;
+            const int myrow = 16 * g + u < count ? rows[u] : -1;
+            uint4 raw[8];
+            uint32_t kx[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = __shfl_sync(kAll, myrow, 2 * i + half);
+                raw[i] = make_uint4(0, 0, 0, 0);
+                if (r >= 0) {
+                    raw[i] = __ldg(reinterpret_cast<const uint4 *>(p.a.codes + (int64_t)r * (D / 2)) + u);
+                    kx[i >> 2] |= (uint32_t)(uint8_t)__ldg(p.a.exps + (int64_t)r * (D / 32) + u) << (8 * (i & 3));
+                }
+            }
+            int emax = -128;                      // of row 16 g + u
+            if (myrow >= 0) {
+                const uint4 ev = __ldg(reinterpret_cast<const uint4 *>(p.a.exps + (int64_t)myrow * (D / 32)));
+                const uint32_t m4 = __vmaxs4(__vmaxs4(ev.x, ev.y), __vmaxs4(ev.z, ev.w));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) emax = max(emax, (int)(int8_t)(m4 >> (8 * i)));
+            }
+            free_msg(n);
+            const uint32_t st = J & 1u;
+            if (first) {
+                // q of the unit, once S of the tile before has read the last one's
+                if (J > 0 && !warp_wait(BAR(B_S + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag)) break;
+            }
+            float qs = 0.0f;
+            if (first) {
+                const Unit un = unit_of(p, unit);
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {
+                    const int hh = 8 * g + i;
+                    uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                    if (hh < un.nh) {
+                        const uint4 *src =
+                            reinterpret_cast<const uint4 *>(p.a.q + (un.tok * p.a.h + un.h0 + hh) * D) + 2 * lane;
+                        v[0] = __ldg(src);
+                        v[1] = __ldg(src + 1);
+                    }
+                    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+                    top = __reduce_max_sync(kAll, top);
+                    // 2^g such that the largest value lies in [128, 256) 2^g
+                    const int ge = max((int)(top >> 7) - 127 - 7, -126);
+                    const float down = __uint_as_float((uint32_t)(127 - ge) << 23);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float x0 = bf16_lo(w[k]) * down, x1 = bf16_hi(w[k]) * down;
+                        const uint32_t h2 = e4m3x2(x0, x1);
+                        const uint32_t f2 = f16x2_of_e4m3x2(h2);
+                        const float y0 = __half2float(__ushort_as_half((unsigned short)(f2 & 0xffffu)));
+                        const float y1 = __half2float(__ushort_as_half((unsigned short)(f2 >> 16)));
+                        const uint32_t l2 = e4m3x2((x0 - y0) * 32.0f, (x1 - y1) * 32.0f);
+                        if (k & 1) {
+                            hi[k >> 1] |= h2 << 16;
+                            lo[k >> 1] |= l2 << 16;
+                        } else {
+                            hi[k >> 1] = h2;
+                            lo[k >> 1] = l2;
+                        }
+                    }
+                    const uint32_t at = base + SM_Q + (uint32_t)(lane >> 3) * PANEL + (uint32_t)hh * 128 +
+                                        (uint32_t)(((lane & 7) ^ (hh & 7)) * 16);
+                    st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+                    st_shared_v4(at + HM * 128, lo[0], lo[1], lo[2], lo[3]);
+                    if (lane == i) qs = ldexpf(p.scale_log2, ge);
+                }
+            }
+            if (J >= 2 && !warp_wait(BAR(B_PV + st), ((J >> 1) - 1) & 1u, abort_flag)) break;
+            if (first) {
+                // P V of tile J - 2 is done, so the softmax is through with the scales of two units ago
+                if (lane < 8) reinterpret_cast<float *>(ctl + C_QS)[(seg & 1u) * HM + 8 * g + lane] = qs;
+                ++seg;
+            }
+            const uint32_t sbase = base + SM_KV + st * STAGE + (uint32_t)panel * PANEL;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = 16 * g + 2 * i + half;
+                const int er = __shfl_sync(kAll, emax, 2 * i + half);
+                const int x = (int)(int8_t)(kx[i >> 2] >> (8 * (i & 3))) - er + 13;
+                // e5m2 of the eight magnitudes at 2^x: 2 more in the exponent field's place for each octave
+                const uint32_t on = x >= -13 ? kAll : 0u;
+                const uint32_t t0 = (0x3E3C3800u + (uint32_t)x * 0x04040400u) & on;
+                const uint32_t t1 = (0x46444240u + (uint32_t)x * 0x04040404u) & on;
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                uint32_t o[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t m = w[k] & 0x77777777u, s = (w[k] >> 1) & 0x44444444u;
+                    o[2 * k] = prmt(t0, t1, m) | prmt(0u, 0x80808080u, s);
+                    o[2 * k + 1] = prmt(t0, t1, m >> 16) | prmt(0u, 0x80808080u, s >> 16);
+                }
+                // both 16-byte halves of the block; odd panels start with the other one, so that eight
+                // neighbouring lanes cover all banks
+                const int odd = panel & 1;
+                const uint32_t rb = sbase + (uint32_t)row * 128;
+                const uint32_t ca = rb + (uint32_t)((c0 ^ (row & 7)) * 16), cb = rb + (uint32_t)(((c0 + 1) ^ (row & 7)) * 16);
+                if (odd) {
+                    st_shared_v4(cb, o[4], o[5], o[6], o[7]);
+                    st_shared_v4(ca, o[0], o[1], o[2], o[3]);
+                } else {
+                    st_shared_v4(ca, o[0], o[1], o[2], o[3]);
+                    st_shared_v4(cb, o[4], o[5], o[6], o[7]);
+                }
+            }
+            if (lane < 16) reinterpret_cast<int8_t *>(ctl + C_REXP)[st * BN + 16 * g + lane] = (int8_t)emax;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && !(p.stall_first_tile && J == 0)) mbar_arrive(BAR(B_KV + st));
+            ++J;
         }
-        __syncthreads();
-        if (!live) continue;
-        for (int r = 0; r < RT; ++r) {
-            if (slot[r] < 0) continue;
-            float dot = 0.0f;
-            for (int i = 0; i < 16; ++i) dot = fmaf(q[i], rows[r][lane * 16 + i], dot);
-            for (int k = 16; k; k >>= 1) dot += __shfl_xor_sync(kAll, dot, k);
-            const float s = dot * p.scale, m2 = fmaxf(mx, s);
-            const float f = expf(mx - m2), w = expf(s - m2);
-            mx = m2;
-            l = l * f + w;
-            for (int i = 0; i < 16; ++i) o[i] = o[i] * f + w * rows[r][lane * 16 + i];
+    } else if (warp == W_MMA) {
+        // =============================== MMA issue (one thread) ===============================
+        if (lane == 0) {
+            constexpr uint32_t I_S = idesc8(BN, 2 * HM, 1, 0, false);
+            constexpr uint32_t I_HI = idesc8(128, HM, 1, 0, true), I_LO = idesc8(128, HM, 1, 1, true, true);
+            uint32_t n = 0, sJ = 0, vJ = 0;    // next message, next tile of S and of P V
+            int msg = 0;                       // the message in hand (0: none)
+            uint32_t firsts = 0;               // bit J & 1: tile J is its unit's first
+            uint32_t idle = 0;
+            uint64_t since = 0;
+            for (;;) {
+                bool did = false;
+                if (msg == 0 && mbar_test_wait(BAR(B_MSG + n % NR), (n / NR) & 1u)) {
+                    msg = msgs[n % NR];
+                    mbar_arrive(BAR(B_MSGFREE + n % NR));
+                    ++n;
+                    if ((msg & 255) == kEnd) msg = 0;
+                    did = true;
+                }
+                if ((msg & 255) == kTile && sJ - vJ < 2) {
+                    const uint32_t st = sJ & 1u;
+                    if (mbar_test_wait(BAR(B_KV + st), (sJ >> 1) & 1u) &&
+                        (sJ < 2 || mbar_test_wait(BAR(B_SFREE + st), ((sJ >> 1) - 1) & 1u))) {
+                        tc_fence_after();
+                        const uint64_t ad = smem_desc_sw128(base + SM_KV + st * STAGE, 16, 1024);
+                        const uint64_t bd = smem_desc_sw128(base + SM_Q, 16, 1024);
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            const uint64_t off = (uint64_t)(((k >> 2) * PANEL + (k & 3) * 32) >> 4);
+                            mma_f8(tmem + TM_S + st * 2 * HM, ad + off, bd + off, I_S, k ? 1u : 0u);
+                        }
+                        mma_commit(BAR(B_S + st));
+                        firsts = (firsts & ~(1u << st)) | (((uint32_t)(msg >> 8) & 1u) << st);
+                        msg = 0;
+                        ++sJ;
+                        did = true;
+                    }
+                }
+                if (vJ < sJ) {
+                    const uint32_t st = vJ & 1u;
+                    if (mbar_test_wait(BAR(B_P + st), (vJ >> 1) & 1u)) {
+                        tc_fence_after();
+                        // C^T: panel c's 128 columns as M (one 128-byte atom), 32 rows a step (four groups of
+                        // eight, 1024 bytes apart); P the same with its 64 heads as N
+                        const uint64_t ad = smem_desc_sw128(base + SM_KV + st * STAGE, PANEL, 1024);
+                        const uint64_t bd = smem_desc_sw128(base + SM_P + st * P_BYTES, P_BYTES, 1024);
+                        const uint32_t keep = (firsts >> st) & 1u ? 0u : 1u;
+#pragma unroll
+                        for (int c = 0; c < NPAN; ++c)
+#pragma unroll
+                            for (int k = 0; k < BN / 32; ++k) {
+                                const uint64_t ao = ad + (uint64_t)((c * PANEL + k * 4096) >> 4);
+                                const uint64_t bo = bd + (uint64_t)((k * 4096) >> 4);
+                                mma_f8(tmem + TM_O + c * HM, ao, bo, I_HI, k ? 1u : keep);
+                                mma_f8(tmem + TM_O + c * HM, ao, bo + (64 >> 4), I_LO, 1u);
+                            }
+                        mma_commit(BAR(B_PV + st));
+                        ++vJ;
+                        did = true;
+                    }
+                }
+                if ((msg & 255) == kFin && vJ == sJ) break;
+                if (did) {
+                    idle = 0;
+                    since = 0;
+                    continue;
+                }
+                __nanosleep(32);
+                if ((++idle & 63u) == 0u) {
+                    if (*abort_flag) break;
+                    const uint64_t now = globaltimer_ns();
+                    if (since == 0) since = now;
+                    else if (now - since > kWaitLimitNs) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                }
+            }
+            if (*abort_flag) {   // let issued MMAs finish before TMEM is freed
+                mma_commit(BAR(B_DRAIN));
+                mbar_wait_drain(BAR(B_DRAIN), 0, 100000000ull);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ============================ softmax and epilogue ============================
+        const int quarter = warp & 3, hb = (warp >> 2) * 32, row = quarter * 32 + lane;
+        const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16);
+        float *m_h = reinterpret_cast<float *>(ctl + C_M), *fac = reinterpret_cast<float *>(ctl + C_FAC);
+        const float *qs = reinterpret_cast<const float *>(ctl + C_QS);
+        float l[32];
+        int64_t unit = T > 0 ? e0 / T : 0;
+        const int64_t unit0 = unit;
+        uint32_t J = 0, seg = 0;
+        int E = 0;
+        bool any = false;      // the unit has a tile
+        bool bad = false;
+        for (uint32_t n = 0;; ++n) {
+            int msg = 0;
+            bad = bad || *abort_flag || !read_msg(n, msg);
+            const int kind = msg & 255;
+            if (!bad) {
+                free_msg(n);
+                if (kind == kFin) {
+                    bar_or(false);   // a warp that gave up meets the others here
+                    break;
+                }
+            }
+            if (!bad && kind == kEnd) {
+                // ---- the unit's output, or this range's part of it
+                const Unit un = unit_of(p, unit);
+                const bool whole = unit * T >= e0 && (unit + 1) * T <= e1;
+                float *scr = reinterpret_cast<float *>(smem + SM_P);     // [4][64] sums of the quarters
+                if (any) {
+                    bad = !warp_wait(BAR(B_PV + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag);
+                    tc_fence_after();
+                    // sums over the warp's rows: lane i ends up with head hb + i
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) {
+                        const bool up = (lane & o) != 0;
+#pragma unroll
+                        for (int i = 0; i < o; ++i) {
+                            const float give = up ? l[i] : l[i + o];
+                            l[i] = (up ? l[i + o] : l[i]) + __shfl_xor_sync(kAll, give, o);
+                        }
+                    }
+                    scr[quarter * HM + hb + lane] = l[0];
+                }
+                if (bar_or(bad)) break;
+                float *ws = p.ws + ((size_t)cid * 2 + (unit == unit0 ? 0 : 1)) * SLOT;
+                if (threadIdx.x < HM) {
+                    const int hh = threadIdx.x;
+                    const float m = any ? m_h[hh] : -INFINITY;
+                    const float sum = any ? scr[hh] + scr[HM + hh] + scr[2 * HM + hh] + scr[3 * HM + hh] : 0.0f;
+                    if (whole) {
+                        const float sink = hh < un.nh ? __ldg(p.a.sink + un.h0 + hh) * kLog2e : 0.0f;
+                        fac[hh] = any ? 1.0f / (sum + exp2f(sink - m)) : 0.0f;
+                    } else {
+                        ws[SLOT_O + hh] = m;
+                        ws[SLOT_O + HM + hh] = sum;
+                    }
+                }
+                if (bar_or(false)) break;
+                const float unfold = ldexpf(1.0f, E - 17);
+                const float2 *cs = nullptr;
+                if constexpr (ROPE)
+                    if (whole) cs = rotation_row(p.a, un.tok, threadIdx.x == 0);
+                uint16_t *out = p.a.o + (un.tok * p.a.h + un.h0) * D;
+                // warps 0-3 take panels 0 and 1, warps 4-7 panels 2 and 3: thread = column
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k) {
+                    const int c = (hb >> 4) + (k >> 2), h0 = (k & 3) * 16, d = c * 128 + row;
+                    if (h0 >= un.nh) continue;
+                    uint32_t r[16];
+                    if (any) {
+                        tmem_ld16(tm + TM_O + c * HM + h0, r);
+                        tmem_wait16(r);
+                    }
+                    if (whole) {
+                        uint16_t *col = out + (int64_t)h0 * D + d;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float x = any ? __uint_as_float(r[i]) * fac[h0 + i] * unfold : 0.0f;
+                            if constexpr (ROPE) {
+                                if (cs && c * 128 + quarter * 32 + 31 >= D - p.a.rd) {
+                                    const float y = __shfl_xor_sync(kAll, x, 1);
+                                    if (d >= D - p.a.rd) {
+                                        const float2 t = __ldg(cs + ((d - (D - p.a.rd)) >> 1));
+                                        x = (d & 1) ? x * t.x - y * t.y : x * t.x + y * t.y;
+                                    }
+                                }
+                            }
+                            if (h0 + i < un.nh) col[i * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+                        }
+                    } else if (any) {
+                        float *col = ws + h0 * D + d;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (h0 + i < un.nh) col[i * D] = __uint_as_float(r[i]) * unfold;
+                    }
+                }
+                tc_fence_before();
+                any = false;
+                ++unit;
+                continue;
+            }
+            // ---- a tile
+            const int count = msg >> 16;
+            const bool first = (msg >> 8) & 1;
+            const uint32_t st = J & 1u;
+            const bool live = row < count;
+            float *scr = reinterpret_cast<float *>(smem + SM_P + st * P_BYTES);   // [4][64] maxima, [4] exponents
+            float v[32];
+            int e = 0;
+            if (!bad) {
+                bad = !warp_wait(BAR(B_KV + st), (J >> 1) & 1u, abort_flag) ||
+                      !warp_wait(BAR(B_S + st), (J >> 1) & 1u, abort_flag) ||
+                      (J >= 2 && !warp_wait(BAR(B_PV + st), ((J >> 1) - 1) & 1u, abort_flag));
+            }
+            if (!bad) {
+                if (first) ++seg;
+                tc_fence_after();
+                e = (int)reinterpret_cast<const int8_t *>(ctl + C_REXP)[st * BN + row];
+                const float cr = ldexpf(1.0f, e - 13);
+                const float *q = qs + ((seg - 1) & 1u) * HM + hb;
+#pragma unroll
+                for (int j = 0; j < 32; j += 16) {
+                    uint32_t r0[16], r1[16];
+                    tmem_ld16(tm + TM_S + st * 2 * HM + hb + j, r0);
+                    tmem_ld16(tm + TM_S + st * 2 * HM + HM + hb + j, r1);
+                    tmem_wait16(r0);
+                    tmem_wait16(r1);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 q4 = lds4(q + j + i);
+                        const float qv[4] = {q4.x, q4.y, q4.z, q4.w};
+                        float mx[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float s = fmaf(__uint_as_float(r1[i + k]), 0.03125f, __uint_as_float(r0[i + k]));
+                            v[j + i + k] = live ? s * qv[k] * cr : -INFINITY;
+                            mx[k] = warp_max(v[j + i + k]);
+                        }
+                        if (lane == 0)
+                            *reinterpret_cast<float4 *>(scr + quarter * HM + hb + j + i) =
+                                make_float4(mx[0], mx[1], mx[2], mx[3]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(B_SFREE + st));
+                const int te = __reduce_max_sync(kAll, live ? e : -128);
+                if (lane == 0 && hb == 0) reinterpret_cast<int *>(scr + 4 * HM)[quarter] = te;
+            }
+            if (bar_or(bad)) break;
+            bool moved = false;
+            if (threadIdx.x < HM) {
+                const int hh = threadIdx.x;
+                const float t = fmaxf(fmaxf(scr[hh], scr[HM + hh]), fmaxf(scr[2 * HM + hh], scr[3 * HM + hh]));
+                const float m = m_h[hh];
+                const bool raise = !first && t > m + kSlack;
+                if (first || raise) m_h[hh] = t;
+                fac[hh] = raise ? exp2f(m - t) : 1.0f;
+                moved = raise;
+            }
+            const int4 te4 = *reinterpret_cast<const int4 *>(scr + 4 * HM);
+            const int tile_e = max(max(te4.x, te4.y), max(te4.z, te4.w));
+            const int E0 = E;
+            E = first ? tile_e : max(E, tile_e);
+            moved = moved || (!first && E > E0);
+            moved = bar_or(moved);
+            if (first) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) l[i] = 0.0f;
+            }
+            if (moved) {
+                const float down = ldexpf(1.0f, E0 - E);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 f = lds4(fac + hb + i);
+                    l[i] *= f.x;
+                    l[i + 1] *= f.y;
+                    l[i + 2] *= f.z;
+                    l[i + 3] *= f.w;
+                }
+                // O^T: every thread scales its column's heads (panels shared out as in the epilogue)
+                bad = !warp_wait(BAR(B_PV + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag);
+                tc_fence_after();
+#pragma unroll 1
+                for (int k = 0; k < 8 && !bad; ++k) {
+                    const int c = (hb >> 4) + (k >> 2), h0 = (k & 3) * 16;
+                    uint32_t r[16];
+                    tmem_ld16(tm + TM_O + c * HM + h0, r);
+                    tmem_wait16(r);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (fac[h0 + i] * down));
+                    tmem_st16(tm + TM_O + c * HM + h0, r);
+                }
+                tmem_st_wait();
+            }
+            any = true;
+            {
+                const float fr = live ? ldexpf(1.0f, e - E + 4) : 0.0f;
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 m4 = lds4(m_h + hb + i);
+                    const float mv[4] = {m4.x, m4.y, m4.z, m4.w};
+                    float pr[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        pr[k] = ex2(v[i + k] - mv[k]);
+                        l[i + k] += pr[k];
+                        pr[k] *= fr;
+                    }
+                    uint32_t h0, h1, l0, l1;
+                    split_p(pr[0], pr[1], h0, l0);
+                    split_p(pr[2], pr[3], h1, l1);
+                    hi[i >> 2] = prmt(h0, h1, 0x5410);
+                    lo[i >> 2] = prmt(l0, l1, 0x5410);
+                }
+                const uint32_t pb = base + SM_P + st * P_BYTES + (uint32_t)row * 128;
+                const int ch = hb >> 4, sw = row & 7;
+                st_shared_v4(pb + (uint32_t)(((ch + 0) ^ sw) * 16), hi[0], hi[1], hi[2], hi[3]);
+                st_shared_v4(pb + (uint32_t)(((ch + 1) ^ sw) * 16), hi[4], hi[5], hi[6], hi[7]);
+                st_shared_v4(pb + (uint32_t)(((ch + 4) ^ sw) * 16), lo[0], lo[1], lo[2], lo[3]);
+                st_shared_v4(pb + (uint32_t)(((ch + 5) ^ sw) * 16), lo[4], lo[5], lo[6], lo[7]);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(B_P + st));
+            ++J;
         }
     }
-    if (!live) return;
-    const float inv = l > 0.0f ? 1.0f / (l + expf(p.sink[hh] - mx)) : 0.0f;
-    int64_t pos = -1;
-    if (p.rd) {
-        pos = (int64_t)p.first[bi] + tok % p.m;
-        if (pos < 0 || pos >= p.table_rows) {
-            pos = -1;
-            if (lane == 0) flag_status(p.status, DS_DEV_BAD_INDEX);
-        }
-    }
-    for (int i = 0; i < 16; i += 2) {
-        const int c = lane * 16 + i;
-        float a = o[i] * inv, b = o[i + 1] * inv;
-        if (pos >= 0 && c >= D - p.rd) {
-            const float2 cs = p.table[pos * (p.rd / 2) + (c - (D - p.rd)) / 2];
-            const float re = a * cs.x + b * cs.y, im = b * cs.x - a * cs.y;
-            a = re;
-            b = im;
-        }
-        p.o[(tok * p.h + hh) * D + c] = __bfloat16_as_ushort(__float2bfloat16_rn(a));
-        p.o[(tok * p.h + hh) * D + c + 1] = __bfloat16_as_ushort(__float2bfloat16_rn(b));
+
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) flag_status(p.a.status, DS_DEV_TIMEOUT);
+    if (warp == W_MMA) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
     }
 }
 
-}  // namespace
+// Merge the partials of the units that a range boundary cuts: block (cut unit, head), thread = four columns.
+struct CombineParams {
+    Args a;
+    int64_t ntok;
+    int groups;
+    bool interleave;
+    const float *ws;
+    int ncut;
+    int4 cut[kMaxCut];            // {unit, first part, parts, slot bits}
+};
+
+template <bool ROPE>
+__global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
+    grid_dependency_wait();
+    const int4 c = p.cut[blockIdx.x];
+    const int64_t ord = p.groups == 1 ? c.x : c.x >> 1;
+    const int64_t tok = unit_at(ord, p.ntok, p.interleave);
+    const int h0 = p.groups == 1 ? 0 : (c.x & 1) * HM, hh = blockIdx.y;
+    if (h0 + hh >= p.a.h) return;
+    auto part = [&](int i) { return p.ws + ((size_t)(c.y + i) * 2 + (((uint32_t)c.w >> i) & 1u)) * SLOT; };
+    // lane i of each warp: part i (at most 32)
+    const int lane = threadIdx.x & 31;
+    float m = -INFINITY, l = 0.0f;
+    if (lane < c.z) {
+        m = part(lane)[SLOT_O + hh];
+        l = part(lane)[SLOT_O + HM + hh];
+    }
+    const float top = warp_max(m);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (top != -INFINITY) {
+        const float w = m == -INFINITY ? 0.0f : exp2f(m - top);
+        float den = w * l;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kAll, den, o);
+        den += exp2f(__ldg(p.a.sink + h0 + hh) * kLog2e - top);
+        const float inv = 1.0f / den;
+        for (int i = 0; i < c.z; ++i) {
+            const float wi = __shfl_sync(kAll, w, i);
+            if (wi == 0.0f) continue;              // a part without rows has no accumulator
+            const float4 x = reinterpret_cast<const float4 *>(part(i) + hh * D)[threadIdx.x];
+            acc.x += wi * x.x;
+            acc.y += wi * x.y;
+            acc.z += wi * x.z;
+            acc.w += wi * x.w;
+        }
+        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    }
+    const int d = threadIdx.x * 4;
+    if constexpr (ROPE) {
+        const float2 *cs = rotation_row(p.a, tok, threadIdx.x == 0 && hh == 0);
+        if (cs && d >= D - p.a.rd) {
+            const float2 t0 = __ldg(cs + ((d - (D - p.a.rd)) >> 1)), t1 = __ldg(cs + ((d - (D - p.a.rd)) >> 1) + 1);
+            acc = make_float4(acc.x * t0.x + acc.y * t0.y, acc.y * t0.x - acc.x * t0.y, acc.z * t1.x + acc.w * t1.y,
+                              acc.w * t1.x - acc.z * t1.y);
+        }
+    }
+    *reinterpret_cast<uint2 *>(p.a.o + (tok * p.a.h + h0 + hh) * D + d) =
+        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+}
+
+// ---- host side ---------------------------------------------------------------------------------------
+
+constexpr int kMaxDev = 64;
+int g_sms[kMaxDev];
+std::mutex g_mutex;
+
+// CTAs that run at once on the current device (one per SM), 0 when the kernel cannot be configured.
+int max_ctas() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (g_sms[dev]) return g_sms[dev];
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    for (const void *k : {(const void *)sparse_attn_fp4_kernel<false>, (const void *)sparse_attn_fp4_kernel<true>})
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess) return 0;
+    return g_sms[dev] = sms;
+}
+
+struct Plan {
+    int64_t ntok, nunit, G, K;
+    int groups;
+    bool split;
+};
+
+// Fixed cost of a unit on the cost line (q, the epilogue), in index entries.
+constexpr int kSegCost = BN;
+
+bool plan(int b, int m, int h, int topk, Plan &pl) {
+    const int gmax = max_ctas();
+    if (gmax <= 0) return false;
+    pl.ntok = (int64_t)b * m;
+    pl.groups = h > HM ? 2 : 1;
+    pl.nunit = pl.ntok * pl.groups;
+    pl.G = split::choose_ranges(pl.nunit, topk, gmax, BN);
+    pl.K = split::seg_cost(pl.nunit, pl.G, kSegCost);
+    pl.split = split::splits_units(pl.nunit, topk, pl.G, pl.K);
+    return true;
+}
+
+size_t workspace_bytes(const Plan &pl) { return pl.split ? (size_t)pl.G * 2 * SLOT * sizeof(float) : 0; }
+
 }  // namespace fp4
 
-size_t sparse_attn_fp4_workspace_bytes(int, int, int, int) { return 0; }
+size_t sparse_attn_fp4_workspace_bytes(int b, int m, int h, int topk) {
+    fp4::Plan pl;
+    if (topk == 0 || (int64_t)b * m == 0 || !fp4::plan(b, m, h, topk, pl)) return 0;
+    return fp4::workspace_bytes(pl);
+}
 
 int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream) {
-    const int64_t blocks = (int64_t)a.b * a.m * ((a.h + fp4::HG - 1) / fp4::HG);
-    fp4::plain_kernel<<<(unsigned)blocks, fp4::HG * 32, 0, stream>>>(a);
-    return launch_status();
+    fp4::Plan pl;
+    if (!fp4::plan(a.b, a.m, a.h, a.topk, pl)) return DS_ECUDA;
+    if (pl.nunit > INT32_MAX || pl.nunit > (INT64_MAX / (pl.G + 1)) / (a.topk + pl.K)) return DS_EUNSUPPORTED;
+    const size_t need = fp4::workspace_bytes(pl);
+    if (a.workspace_bytes < need || (need && !a.workspace)) return DS_EWORKSPACE;
+    const bool rope = a.rd > 0, interleave = a.m > 1;
+    fp4::Params p{a, pl.ntok, pl.nunit, pl.groups, (int)pl.G, (int)pl.K, interleave, a.scale * fp4::kLog2e,
+                  static_cast<float *>(a.workspace), test_stall() ? 1 : 0};
+    fp4::CombineParams c;
+    if (pl.split) {
+        c.a = a;
+        c.ntok = pl.ntok;
+        c.groups = pl.groups;
+        c.interleave = interleave;
+        c.ws = p.ws;
+        c.ncut = split::cut_units(pl.nunit, a.topk, pl.K, pl.G, c.cut);
+        if (c.ncut <= 0) return DS_EUNSUPPORTED;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)pl.G, 1, 1);
+    cfg.blockDim = dim3(fp4::NTHREADS, 1, 1);
+    cfg.dynamicSmemBytes = fp4::SMEM_BYTES;
+    cfg.stream = stream;
+    // programmatic dependent launch: the set-up overlaps the previous kernel on the stream
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, rope ? fp4::sparse_attn_fp4_kernel<true> : fp4::sparse_attn_fp4_kernel<false>, p) !=
+        cudaSuccess)
+        return DS_ECUDA;
+    if (pl.split) {
+        cfg.gridDim = dim3((unsigned)c.ncut, (unsigned)(a.h < fp4::HM ? a.h : fp4::HM), 1);
+        cfg.blockDim = dim3(128, 1, 1);
+        cfg.dynamicSmemBytes = 0;
+        if (cudaLaunchKernelEx(&cfg, rope ? fp4::combine_kernel<true> : fp4::combine_kernel<false>, c) != cudaSuccess)
+            return DS_ECUDA;
+    }
+    return DS_OK;
 }
 
 }  // namespace dsattn

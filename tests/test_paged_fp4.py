@@ -2,10 +2,13 @@
 plain implementations in 64 bits, their refusals, and a run of them together.
 
 Tolerances.  A bf16 result is off by half a step, 2^-8 of its value; the f32 work before it by less than
-2^-20 of the magnitudes it adds up.  The attention's probabilities may be rounded by 2^-8 of themselves
-before the value product (as bf16 would), with a floor of 2^-20 of the largest, so with A = sum p |v| / l
-and F = sum |v| / l (l the denominator relative to the largest probability) an output is off by at most
-2^-8 |o| + (2^-8 + 2^-12) A + 2^-20 F; a rotation adds up both values of a pair.  An output below f32's
+2^-20 of the magnitudes it adds up.  A probability, scaled to P = 16 p 2^(e - E) (e the row's largest block
+exponent, E the list's), enters the value product as hi - lo, hi in e4m3 and lo in e5m2.  From P >= 2^-6, hi
+has four bits, so hi - P is at most 2^-4 of the power of two below P, and three bits of that leave 2^-8 of
+P.  Below, hi is a multiple of 2^-9, so hi - P is at most 2^-10, and e5m2's half step of 2^-3 of it (down to
+2^-17) leaves 2^-13: 2^-17 of p = 1 at e = E.  With A = sum p |v| / l and F = sum |v| 2^(E - e) / l (l the
+denominator relative to the largest probability) an output is off by at most
+2^-8 |o| + (2^-8 + 2^-12) A + 2^-17 F; a rotation adds up both values of a pair.  An output below f32's
 least normal number, 2^-126, may come as 0 (a sink of 300 makes the exact ones about e^-300).
 Codes, exponents and the values they stand for are equal.
 """
@@ -75,9 +78,9 @@ def unpack(packed):
     return np.stack((packed & 15, packed >> 4), -1).reshape(packed.shape[:-1] + (-1,))
 
 
-def attention(q, rows, live, sink, scale):
-    """q [h][d], rows [n][d], live [n] -> o, A, F of the header comment."""
-    rows = rows[live]
+def attention(q, rows, live, sink, scale, tops):
+    """q [h][d], rows [n][d], live [n], tops [n] the rows' largest exponents -> o, A, F of the header comment."""
+    rows, tops = rows[live], tops[live].astype(float)
     if not len(rows):
         return np.zeros_like(q), np.zeros_like(q), np.zeros_like(q)
     s = scale * q @ rows.T
@@ -85,7 +88,8 @@ def attention(q, rows, live, sink, scale):
     p = np.exp(s - top)
     with np.errstate(over="ignore"):
         den = p.sum(-1, keepdims=True) + np.exp(sink[:, None] - top)
-    return p @ rows / den, p @ np.abs(rows) / den, np.abs(rows).sum(0)[None] / den
+    worth = np.abs(rows) * 2.0 ** (tops.max() - tops)[:, None]
+    return p @ rows / den, p @ np.abs(rows) / den, worth.sum(0)[None] / den
 
 
 def pair_sum(a, rd):
@@ -124,10 +128,11 @@ def random_pool(g, b, rows, page, d, kmin=-3, kmax=3, spare=2):
 
 
 def logical_rows(codes, exps, bt, seq, r, page):
-    """64-bit rows of logical numbers r (clamped at 0) of one sequence."""
+    """64-bit rows of logical numbers r (clamped at 0) of one sequence, and their largest exponents."""
     r = np.maximum(r, 0)
     pg = bt.numpy()[seq][r // page]
-    return values(unpack(codes.numpy()[pg, r % page]), exps.numpy()[pg, r % page])
+    k = exps.numpy()[pg, r % page]
+    return values(unpack(codes.numpy()[pg, r % page]), k), k.max(-1)
 
 
 # ---- norm and rotation --------------------------------------------------------------------------------
@@ -350,12 +355,12 @@ def check_attention(ds, q, codes, exps, bt, sink, idx, rd=0, first=None, tab=Non
         toks = [toks[j] for j in np.random.RandomState(3).choice(len(toks), sample, replace=False)]
     for i, t in toks:
         ix = idx[i, t].numpy()
-        rows = logical_rows(codes, exps, bt, i, ix, page)
-        ref, A, F = attention(f64(q[i, t]), rows, ix >= 0, f64(sink), scale)
+        rows, tops = logical_rows(codes, exps, bt, i, ix, page)
+        ref, A, F = attention(f64(q[i, t]), rows, ix >= 0, f64(sink), scale, tops)
         if rd:
             ref = rotate(ref, f64(tab)[int(first[i]) + t], inverse=True)
             A, F = pair_sum(A, rd), pair_sum(F, rd)
-        tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * A + 2.0 ** -20 * F + 2.0 ** -126
+        tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * A + 2.0 ** -17 * F + 2.0 ** -126
         bad = np.abs(got[i, t] - ref) > tol
         assert not bad.any(), (i, t, int(bad.sum()), float(np.abs(got[i, t] - ref)[bad].max()))
     return o
@@ -550,13 +555,13 @@ def test_step_together_and_in_a_graph(ds):
             zq = rotate(normed(f64(q[i, 0]), None, eps), f64(tab)[int(first[i])][None])
             zq = f64(torch.from_numpy(zq).to(torch.bfloat16))
             ix = idx[i, 0].numpy()
-            rr = logical_rows(torch.from_numpy(ref_c), torch.from_numpy(ref_e), bt, i, ix, page)
-            ref, A, F = attention(zq, rr, ix >= 0, f64(sink), scale)
+            rr, tops = logical_rows(torch.from_numpy(ref_c), torch.from_numpy(ref_e), bt, i, ix, page)
+            ref, A, F = attention(zq, rr, ix >= 0, f64(sink), scale, tops)
             ref = rotate(ref, f64(tab)[int(first[i])][None], inverse=True)
             A, F = pair_sum(A, rd), pair_sum(F, rd)
             # beside the attention's own: q may be one bf16 step off where the norm's f32 falls on the other
             # side of a border; its effect is far below a step of all 512 products together
-            tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -10) * A + 2.0 ** -20 * F
+            tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -10) * A + 2.0 ** -17 * F
             assert (np.abs(f64(got[i, 0]) - ref) <= tol).all()
         first += 1
     assert ds.device_status() == 0
