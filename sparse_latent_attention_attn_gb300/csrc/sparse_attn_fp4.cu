@@ -24,9 +24,9 @@
 // N = 128 in S and K = 32 a step a tile takes 16 + 32 instructions where bf16 rows would take 64 + 64.  The
 // widening to e5m2 is a table of 8 bytes per block: byte permutes with the code words as selectors.
 //
-// Warps: 0-7 softmax and epilogue (warp w: TMEM lanes 32 (w % 4).., heads 32 (w / 4)..), 8-15 rows (codes
-// loaded a tile ahead into registers, widened into the swizzled stage; q at a unit's first tile), 16 MMA
-// issue, 17 index rows: it drops entries without a row, turns the others into row numbers and hands out
+// Warps: 0-15 softmax and epilogue (warp w: TMEM lanes 32 (w % 4).., heads 16 (w / 4)..), 16-23 rows (codes
+// loaded a tile ahead into registers, widened into the swizzled stage; q at a unit's first tile), 24 MMA
+// issue, 25 index rows: it drops entries without a row, turns the others into row numbers and hands out
 // tiles of up to 128 through a ring of messages that every role reads in order.
 // A unit is one token and up to 64 heads; units are shared out as in the other attention kernels
 // (attn_split.cuh), and units cut by a range boundary leave f32 partials that a second kernel merges.
@@ -53,18 +53,20 @@ constexpr int BN = 128;                 // rows of a tile
 constexpr int NPAN = D / 128;           // panels of 128 columns
 constexpr int PANEL = BN * 128;         // bytes of a panel: 128 rows (of C or of [hi | lo]) of 128
 constexpr int STAGE = NPAN * PANEL;     // 64 KB
-constexpr int NR = 3;                   // index messages
+constexpr int NR = 4;                   // index messages
 constexpr int SM_Q = 0;
 constexpr int SM_KV = SM_Q + STAGE;
 constexpr int SM_P = SM_KV + 2 * STAGE;
 constexpr int P_BYTES = BN * 128;       // row r: 64 bytes hi, 64 bytes lo
-constexpr int SM_CTL = SM_P + 2 * P_BYTES;
+constexpr int SM_CTL = SM_P + P_BYTES;
 // control block
 constexpr int C_ROWS = 0;                       // [NR][128] int32 row numbers
 constexpr int C_REXP = C_ROWS + NR * BN * 4;    // [2][128] int8 e_r
-constexpr int C_M = C_REXP + 2 * BN;            // [64] f32 running maximum
-constexpr int C_FAC = C_M + HM * 4;             // [64] f32 rescale factor; at the end 1 / denominator
-constexpr int C_QS = C_FAC + HM * 4;            // [2][64] f32 2^g scale log2(e), by unit parity
+constexpr int C_MAX = C_REXP + 2 * BN;          // [2][4][64] f32 maxima of the quarters, by tile parity
+constexpr int C_EMAX = C_MAX + 2 * 4 * HM * 4;  // [2][4] int32 largest e_r of the quarters
+constexpr int C_SUM = C_EMAX + 32;              // [4][64] f32 sums of the quarters, at a unit's end
+constexpr int C_HEAD = C_SUM + 4 * HM * 4;      // [64] f32 running maximum; at a unit's end the output's factor
+constexpr int C_QS = C_HEAD + HM * 4;           // [2][64] f32 2^g scale log2(e), by unit parity
 constexpr int C_BAR = C_QS + 2 * HM * 4;
 enum : int {
     B_MSG = 0,                  // [NR] index -> all: message written
@@ -73,8 +75,8 @@ enum : int {
     B_PV = B_KV + 2,            // [2] MMA -> rows, softmax: P V of the tile done
     B_S = B_PV + 2,             // [2] MMA -> softmax, rows: scores ready
     B_SFREE = B_S + 2,          // [2] softmax -> MMA: scores read
-    B_P = B_SFREE + 2,          // [2] softmax -> MMA: P written
-    B_DRAIN = B_P + 2,
+    B_P = B_SFREE + 2,          // softmax -> MMA: P written
+    B_DRAIN = B_P + 1,
     B_COUNT = B_DRAIN + 1
 };
 constexpr int C_MSG = C_BAR + 8 * B_COUNT;      // [NR] int32 message heads
@@ -86,8 +88,9 @@ static_assert(C_BAR % 8 == 0 && SMEM_BYTES <= 232448, "shared memory budget");
 constexpr int TM_O = 0, TM_S = NPAN * HM, TMEM_COLS = 512;
 static_assert(TM_S + 2 * 2 * HM <= TMEM_COLS, "TMEM budget");
 
-constexpr int W_ROWS = 8, W_MMA = 16, W_IDX = 17, NTHREADS = 576;   // 112 registers a thread
-constexpr int NSOFT = 256;
+constexpr int NSOFTW = 16, NSOFT = 32 * NSOFTW, HPW = 16;   // softmax warps; heads of one
+constexpr int W_ROWS = NSOFTW, NROWW = 8, W_MMA = W_ROWS + NROWW, W_IDX = W_MMA + 1, NTHREADS = 32 * (W_IDX + 1);
+constexpr int RPL = BN / (2 * NROWW);                // steps of two rows that a row warp takes a tile
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 4.0f;          // octaves that m may be late
@@ -146,9 +149,31 @@ __device__ __forceinline__ bool bar_or(bool pred) {
     return r != 0;
 }
 
+// One try at a phase that lets the hardware suspend the thread for up to about 20 us.
+__device__ __forceinline__ bool try_long(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded wait of a whole warp; false when it gave up, or another role did.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    const bool ok = mbar_wait(bar, parity, abort, kWaitLimitNs);
-    return __all_sync(kAll, ok);
+    bool ok = try_long(bar, parity);
+    if (!__all_sync(kAll, ok)) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!ok && !*abort) {
+            ok = try_long(bar, parity);
+            if (!ok && globaltimer_ns() - t0 > kWaitLimitNs) *abort = 1;
+        }
+        ok = __all_sync(kAll, ok);
+    }
+    return ok;
 }
 
 __device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
@@ -167,6 +192,56 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t v) {
     return r;
 }
 
+// One head of q (16 values a lane) into [hi | lo]; returns g.
+__device__ __forceinline__ int put_q(uint32_t sq, int hh, const uint4 (&v)[2], int lane) {
+    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+    top = __reduce_max_sync(kAll, top);
+    const int g = max((int)(top >> 7) - 127 - 7, -126);      // the largest value lies in [128, 256) 2^g
+    const float down = __uint_as_float((uint32_t)(127 - g) << 23);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float x0 = bf16_lo(w[k]) * down, x1 = bf16_hi(w[k]) * down;
+        const uint32_t h2 = e4m3x2(x0, x1);
+        const uint32_t f2 = f16x2_of_e4m3x2(h2);
+        const float y0 = __half2float(__ushort_as_half((unsigned short)(f2 & 0xffffu)));
+        const float y1 = __half2float(__ushort_as_half((unsigned short)(f2 >> 16)));
+        const uint32_t l2 = e4m3x2((x0 - y0) * 32.0f, (x1 - y1) * 32.0f);
+        hi[k >> 1] = k & 1 ? hi[k >> 1] | (h2 << 16) : h2;
+        lo[k >> 1] = k & 1 ? lo[k >> 1] | (l2 << 16) : l2;
+    }
+    const uint32_t at = sq + (uint32_t)(lane >> 3) * PANEL + (uint32_t)hh * 128 + (uint32_t)(((lane & 7) ^ (hh & 7)) * 16);
+    st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+    st_shared_v4(at + HM * 128, lo[0], lo[1], lo[2], lo[3]);
+    return g;
+}
+
+// The 32 codes of a block at 2^x in e5m2: pairs widened to f16, times 2^x (exact), and the high bytes of the
+// f16 values, which are e5m2 (e2m1 has one mantissa bit, e5m2 two).
+__device__ __forceinline__ void widen(const uint4 raw, int x, uint32_t (&o)[8]) {
+    const uint32_t sc = x >= -13 ? (uint32_t)(x + 15) * 0x04000400u : 0u;
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t.reg .b32 f0, f1, f2, f3;\n\t"
+            "mov.b32 {c0, c1, c2, c3}, %2;\n\t"
+            "cvt.rn.f16x2.e2m1x2 f0, c0;\n\t"
+            "cvt.rn.f16x2.e2m1x2 f1, c1;\n\t"
+            "cvt.rn.f16x2.e2m1x2 f2, c2;\n\t"
+            "cvt.rn.f16x2.e2m1x2 f3, c3;\n\t"
+            "mul.rn.f16x2 f0, f0, %3;\n\t"
+            "mul.rn.f16x2 f1, f1, %3;\n\t"
+            "mul.rn.f16x2 f2, f2, %3;\n\t"
+            "mul.rn.f16x2 f3, f3, %3;\n\t"
+            "prmt.b32 %0, f0, f1, 0x7531;\n\t"
+            "prmt.b32 %1, f2, f3, 0x7531;\n\t}"
+            : "=r"(o[2 * k]), "=r"(o[2 * k + 1])
+            : "r"(w[k]), "r"(sc));
+}
+
 // Two probabilities as hi (e4m3) - lo (e5m2): lo from hi - p, which is exact in f32.
 __device__ __forceinline__ void split_p(float p0, float p1, uint32_t &hi, uint32_t &lo) {
     asm("{\n\t.reg .b32 f;\n\t.reg .b16 h, l, f0, f1;\n\t.reg .f32 r0, r1;\n\t"
@@ -180,6 +255,17 @@ __device__ __forceinline__ void split_p(float p0, float p1, uint32_t &hi, uint32
         "cvt.u32.u16 %1, l;\n\t}"
         : "=r"(hi), "=r"(lo)
         : "f"(p0), "f"(p1));
+}
+
+// One step of summing 16 values over a warp: lanes O apart share the first 2 O of them out.
+template <int O>
+__device__ __forceinline__ void fold(float (&l)[HPW], int lane) {
+    const bool up = (lane & O) != 0;
+#pragma unroll
+    for (int i = 0; i < O; ++i) {
+        const float give = up ? l[i] : l[i + O];
+        l[i] = (up ? l[i + O] : l[i]) + __shfl_xor_sync(kAll, give, O);
+    }
 }
 
 // 16 columns of this thread's TMEM lane
@@ -226,6 +312,33 @@ __device__ __forceinline__ const float2 *rotation_row(const Args &a, int64_t tok
     return a.table + pos * (a.rd / 2);
 }
 
+// S^T of a tile: rows of the stage by [hi | lo], 32 columns (bytes) a step.
+template <int ST, uint32_t IDESC>
+__device__ __forceinline__ void issue_s(uint32_t base, uint32_t tmem) {
+    const uint64_t a = smem_desc_sw128(base + SM_KV + ST * STAGE, 16, 1024), b = smem_desc_sw128(base + SM_Q, 16, 1024);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+        const uint64_t off = (uint64_t)(((k >> 2) * PANEL + (k & 3) * 32) >> 4);
+        mma_f8(tmem + TM_S + ST * 2 * HM, a + off, b + off, IDESC, k ? 1u : 0u);
+    }
+}
+
+// O^T += C^T P: panel c's 128 columns as M (one 128-byte atom), 32 rows a step (four groups of eight, 1024
+// bytes apart); P the same with its 64 heads as N, hi then lo.
+template <int ST, uint32_t I_HI, uint32_t I_LO>
+__device__ __forceinline__ void issue_pv(uint32_t base, uint32_t tmem, uint32_t keep) {
+    const uint64_t a = smem_desc_sw128(base + SM_KV + ST * STAGE, PANEL, 1024);
+    const uint64_t b = smem_desc_sw128(base + SM_P, P_BYTES, 1024);
+#pragma unroll
+    for (int c = 0; c < NPAN; ++c)
+#pragma unroll
+        for (int k = 0; k < BN / 32; ++k) {
+            const uint64_t ao = a + (uint64_t)((c * PANEL + k * 4096) >> 4), bo = b + (uint64_t)((k * 4096) >> 4);
+            mma_f8(tmem + TM_O + c * HM, ao, bo, I_HI, k ? 1u : keep);
+            mma_f8(tmem + TM_O + c * HM, ao, bo + (64 >> 4), I_LO, 1u);
+        }
+}
+
 template <bool ROPE>
 __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -242,15 +355,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
     if (threadIdx.x == 0) {
         for (int i = 0; i < NR; ++i) {
             mbar_init(BAR(B_MSG + i), 1);
-            mbar_init(BAR(B_MSGFREE + i), 17);   // 8 softmax warps, 8 row warps, the MMA thread
+            mbar_init(BAR(B_MSGFREE + i), NSOFTW + NROWW + 1);   // softmax warps, row warps, the MMA warp
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(BAR(B_KV + i), 8);
+            mbar_init(BAR(B_KV + i), NROWW);
             mbar_init(BAR(B_PV + i), 1);
             mbar_init(BAR(B_S + i), 1);
-            mbar_init(BAR(B_SFREE + i), 8);
-            mbar_init(BAR(B_P + i), 8);
+            mbar_init(BAR(B_SFREE + i), NSOFTW);
         }
+        mbar_init(BAR(B_P), NSOFTW);
         mbar_init(BAR(B_DRAIN), 1);
         *abort_flag = (base & 1023u) != 0;       // the swizzled operands need this alignment
         fence_mbar_init();
@@ -350,10 +463,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             if (ok) publish(kEnd);
         }
         if (ok && open()) publish(kFin);
-    } else if (warp >= W_ROWS && warp < W_ROWS + 8) {
+    } else if (warp >= W_ROWS && warp < W_MMA) {
         // ======================== rows (and q) into the swizzled operands ========================
-        const int g = warp - W_ROWS, u = lane & 15, half = lane >> 4;
+        // Warp w takes rows 16 w .. 16 w + 15, two a step: lanes 0-15 and 16-31 hold their 16 blocks.
+        const int w = warp - W_ROWS, u = lane & 15, half = lane >> 4;
         const int panel = u >> 2, c0 = (u & 3) * 2;
+        const int mytile = 16 * w + u;                       // the row whose number and largest exponent this lane holds
         int64_t unit = T > 0 ? e0 / T : 0;
         uint32_t J = 0, seg = 0;
         for (uint32_t n = 0;; ++n) {
@@ -367,108 +482,80 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 ++unit;
                 continue;
             }
-            // the tile's codes, 16 bytes (one block) of two rows a step, in flight until the stage is free
-            const int32_t *rows = reinterpret_cast<const int32_t *>(ctl + C_ROWS) + (n % NR) * BN + 16 * g;
-            const int myrow = 16 * g + u < count ? rows[u] : -1;
-            uint4 raw[8];
-            uint32_t kx[2] = {0, 0};
+            const int myrow =
+                mytile < count ? reinterpret_cast<const int32_t *>(ctl + C_ROWS)[(n % NR) * BN + mytile] : -1;
+            free_msg(n);
+            const uint32_t st = J & 1u;
+            float qs = 0.0f;                      // lane i < 8: the scale of head 8 w + i
+            if (first) {
+                // q of the unit, once S of the tile before has read the last one's
+                if (J > 0 && !warp_wait(BAR(B_S + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag)) break;
+                const Unit un = unit_of(p, unit);
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.a.q + (un.tok * p.a.h + un.h0) * D) + 2 * lane;
+#pragma unroll 1
+                for (int i0 = 0; i0 < 8; i0 += 4) {
+                    uint4 v[4][2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = __shfl_sync(kAll, myrow, 2 * i + half);
-                raw[i] = make_uint4(0, 0, 0, 0);
-                if (r >= 0) {
-                    raw[i] = __ldg(reinterpret_cast<const uint4 *>(p.a.codes + (int64_t)r * (D / 2)) + u);
-                    kx[i >> 2] |= (uint32_t)(uint8_t)__ldg(p.a.exps + (int64_t)r * (D / 32) + u) << (8 * (i & 3));
+                    for (int k = 0; k < 4; ++k) {
+                        const int hh = 8 * w + i0 + k;
+                        v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
+                        if (hh < un.nh) {
+                            v[k][0] = __ldg(src + hh * (D / 8));
+                            v[k][1] = __ldg(src + hh * (D / 8) + 1);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int g = put_q(base + SM_Q, 8 * w + i0 + k, v[k], lane);
+                        if (lane == i0 + k) qs = ldexpf(p.scale_log2, g);
+                    }
                 }
             }
-            int emax = -128;                      // of row 16 g + u
-            if (myrow >= 0) {
-                const uint4 ev = __ldg(reinterpret_cast<const uint4 *>(p.a.exps + (int64_t)myrow * (D / 32)));
+            // the tile's codes, 16 bytes (one block) a lane and row, in flight until the stage is free
+            uint4 raw[RPL];
+            int kx[RPL];
+#pragma unroll
+            for (int i = 0; i < RPL; ++i) {
+                const int r = __shfl_sync(kAll, myrow, 2 * i + half);
+                raw[i] = make_uint4(0, 0, 0, 0);
+                kx[i] = 0;
+                if (r >= 0) {
+                    raw[i] = __ldg(reinterpret_cast<const uint4 *>(p.a.codes + (int64_t)r * (D / 2)) + u);
+                    kx[i] = __ldg(p.a.exps + (int64_t)r * (D / 32) + u);
+                }
+            }
+            uint4 ev = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+            if (myrow >= 0) ev = __ldg(reinterpret_cast<const uint4 *>(p.a.exps + (int64_t)myrow * (D / 32)));
+            if (J >= 2 && !warp_wait(BAR(B_PV + st), ((J >> 1) - 1) & 1u, abort_flag)) break;
+            if (first) {
+                // P V of tile J - 2 is done, so the softmax is through with the scales of two units ago
+                if (lane < 8) reinterpret_cast<float *>(ctl + C_QS)[(seg & 1u) * HM + 8 * w + lane] = qs;
+                ++seg;
+            }
+            // what was loaded is first touched here, behind the wait
+            asm volatile("" : "+r"(ev.x), "+r"(ev.y), "+r"(ev.z), "+r"(ev.w));
+#pragma unroll
+            for (int i = 0; i < RPL; ++i)
+                asm volatile("" : "+r"(raw[i].x), "+r"(raw[i].y), "+r"(raw[i].z), "+r"(raw[i].w), "+r"(kx[i]));
+            int emax = -128;                      // of row mytile
+            {
                 const uint32_t m4 = __vmaxs4(__vmaxs4(ev.x, ev.y), __vmaxs4(ev.z, ev.w));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) emax = max(emax, (int)(int8_t)(m4 >> (8 * i)));
             }
-            free_msg(n);
-            const uint32_t st = J & 1u;
-            if (first) {
-                // q of the unit, once S of the tile before has read the last one's
-                if (J > 0 && !warp_wait(BAR(B_S + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag)) break;
-            }
-            float qs = 0.0f;
-            if (first) {
-                const Unit un = unit_of(p, unit);
-#pragma unroll 1
-                for (int i = 0; i < 8; ++i) {
-                    const int hh = 8 * g + i;
-                    uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                    if (hh < un.nh) {
-                        const uint4 *src =
-                            reinterpret_cast<const uint4 *>(p.a.q + (un.tok * p.a.h + un.h0 + hh) * D) + 2 * lane;
-                        v[0] = __ldg(src);
-                        v[1] = __ldg(src + 1);
-                    }
-                    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-                    top = __reduce_max_sync(kAll, top);
-                    // 2^g such that the largest value lies in [128, 256) 2^g
-                    const int ge = max((int)(top >> 7) - 127 - 7, -126);
-                    const float down = __uint_as_float((uint32_t)(127 - ge) << 23);
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float x0 = bf16_lo(w[k]) * down, x1 = bf16_hi(w[k]) * down;
-                        const uint32_t h2 = e4m3x2(x0, x1);
-                        const uint32_t f2 = f16x2_of_e4m3x2(h2);
-                        const float y0 = __half2float(__ushort_as_half((unsigned short)(f2 & 0xffffu)));
-                        const float y1 = __half2float(__ushort_as_half((unsigned short)(f2 >> 16)));
-                        const uint32_t l2 = e4m3x2((x0 - y0) * 32.0f, (x1 - y1) * 32.0f);
-                        if (k & 1) {
-                            hi[k >> 1] |= h2 << 16;
-                            lo[k >> 1] |= l2 << 16;
-                        } else {
-                            hi[k >> 1] = h2;
-                            lo[k >> 1] = l2;
-                        }
-                    }
-                    const uint32_t at = base + SM_Q + (uint32_t)(lane >> 3) * PANEL + (uint32_t)hh * 128 +
-                                        (uint32_t)(((lane & 7) ^ (hh & 7)) * 16);
-                    st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-                    st_shared_v4(at + HM * 128, lo[0], lo[1], lo[2], lo[3]);
-                    if (lane == i) qs = ldexpf(p.scale_log2, ge);
-                }
-            }
-            if (J >= 2 && !warp_wait(BAR(B_PV + st), ((J >> 1) - 1) & 1u, abort_flag)) break;
-            if (first) {
-                // P V of tile J - 2 is done, so the softmax is through with the scales of two units ago
-                if (lane < 8) reinterpret_cast<float *>(ctl + C_QS)[(seg & 1u) * HM + 8 * g + lane] = qs;
-                ++seg;
-            }
             const uint32_t sbase = base + SM_KV + st * STAGE + (uint32_t)panel * PANEL;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = 16 * g + 2 * i + half;
+            for (int i = 0; i < RPL; ++i) {
+                const int row = 16 * w + 2 * i + half;
                 const int er = __shfl_sync(kAll, emax, 2 * i + half);
-                const int x = (int)(int8_t)(kx[i >> 2] >> (8 * (i & 3))) - er + 13;
-                // e5m2 of the eight magnitudes at 2^x: 2 more in the exponent field's place for each octave
-                const uint32_t on = x >= -13 ? kAll : 0u;
-                const uint32_t t0 = (0x3E3C3800u + (uint32_t)x * 0x04040400u) & on;
-                const uint32_t t1 = (0x46444240u + (uint32_t)x * 0x04040404u) & on;
-                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                const int x = kx[i] - er + 13;
                 uint32_t o[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t m = w[k] & 0x77777777u, s = (w[k] >> 1) & 0x44444444u;
-                    o[2 * k] = prmt(t0, t1, m) | prmt(0u, 0x80808080u, s);
-                    o[2 * k + 1] = prmt(t0, t1, m >> 16) | prmt(0u, 0x80808080u, s >> 16);
-                }
+                widen(raw[i], x, o);
                 // both 16-byte halves of the block; odd panels start with the other one, so that eight
                 // neighbouring lanes cover all banks
-                const int odd = panel & 1;
                 const uint32_t rb = sbase + (uint32_t)row * 128;
                 const uint32_t ca = rb + (uint32_t)((c0 ^ (row & 7)) * 16), cb = rb + (uint32_t)(((c0 + 1) ^ (row & 7)) * 16);
-                if (odd) {
+                if (panel & 1) {
                     st_shared_v4(cb, o[4], o[5], o[6], o[7]);
                     st_shared_v4(ca, o[0], o[1], o[2], o[3]);
                 } else {
@@ -476,107 +563,99 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     st_shared_v4(cb, o[4], o[5], o[6], o[7]);
                 }
             }
-            if (lane < 16) reinterpret_cast<int8_t *>(ctl + C_REXP)[st * BN + 16 * g + lane] = (int8_t)emax;
+            if (lane < 16) reinterpret_cast<int8_t *>(ctl + C_REXP)[st * BN + mytile] = (int8_t)emax;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0 && !(p.stall_first_tile && J == 0)) mbar_arrive(BAR(B_KV + st));
             ++J;
         }
     } else if (warp == W_MMA) {
-        // =============================== MMA issue (one thread) ===============================
-        if (lane == 0) {
-            constexpr uint32_t I_S = idesc8(BN, 2 * HM, 1, 0, false);
-            constexpr uint32_t I_HI = idesc8(128, HM, 1, 0, true), I_LO = idesc8(128, HM, 1, 1, true, true);
-            uint32_t n = 0, sJ = 0, vJ = 0;    // next message, next tile of S and of P V
-            int msg = 0;                       // the message in hand (0: none)
-            uint32_t firsts = 0;               // bit J & 1: tile J is its unit's first
-            uint32_t idle = 0;
-            uint64_t since = 0;
-            for (;;) {
-                bool did = false;
-                if (msg == 0 && mbar_test_wait(BAR(B_MSG + n % NR), (n / NR) & 1u)) {
-                    msg = msgs[n % NR];
-                    mbar_arrive(BAR(B_MSGFREE + n % NR));
-                    ++n;
-                    if ((msg & 255) == kEnd) msg = 0;
+        // ================================== MMA issue ==================================
+        // The whole warp walks the loop, so that its addresses stay uniform; one lane issues.
+        constexpr uint32_t I_S = idesc8(BN, 2 * HM, 1, 0, false);
+        constexpr uint32_t I_HI = idesc8(128, HM, 1, 0, true), I_LO = idesc8(128, HM, 1, 1, true, true);
+        const bool lead = lane == 0;
+        auto done = [&](int bar, uint32_t phase) -> bool { return __all_sync(kAll, mbar_test_wait(BAR(bar), phase & 1u)); };
+        uint32_t n = 0, sJ = 0, vJ = 0;    // next message, next tile of S and of P V
+        int msg = 0;                       // the message in hand (0: none)
+        uint32_t firsts = 0;               // bit J & 1: tile J is its unit's first
+        uint32_t idle = 0;
+        uint64_t since = 0;
+        for (;;) {
+            bool did = false;
+            if (msg == 0 && done(B_MSG + n % NR, n / NR)) {
+                msg = __shfl_sync(kAll, msgs[n % NR], 0);
+                if (lead) mbar_arrive(BAR(B_MSGFREE + n % NR));
+                ++n;
+                if ((msg & 255) == kEnd) msg = 0;
+                did = true;
+            }
+            if ((msg & 255) == kTile && sJ - vJ < 2) {
+                const uint32_t st = sJ & 1u;
+                if (done(B_KV + st, sJ >> 1) && (sJ < 2 || done(B_SFREE + st, (sJ >> 1) - 1))) {
+                    tc_fence_after();
+                    if (lead) {
+                        if (st == 0) issue_s<0, I_S>(base, tmem);
+                        else issue_s<1, I_S>(base, tmem);
+                        mma_commit(BAR(B_S + st));
+                    }
+                    __syncwarp();
+                    firsts = (firsts & ~(1u << st)) | (((uint32_t)(msg >> 8) & 1u) << st);
+                    msg = 0;
+                    ++sJ;
                     did = true;
                 }
-                if ((msg & 255) == kTile && sJ - vJ < 2) {
-                    const uint32_t st = sJ & 1u;
-                    if (mbar_test_wait(BAR(B_KV + st), (sJ >> 1) & 1u) &&
-                        (sJ < 2 || mbar_test_wait(BAR(B_SFREE + st), ((sJ >> 1) - 1) & 1u))) {
-                        tc_fence_after();
-                        const uint64_t ad = smem_desc_sw128(base + SM_KV + st * STAGE, 16, 1024);
-                        const uint64_t bd = smem_desc_sw128(base + SM_Q, 16, 1024);
-#pragma unroll
-                        for (int k = 0; k < D / 32; ++k) {
-                            const uint64_t off = (uint64_t)(((k >> 2) * PANEL + (k & 3) * 32) >> 4);
-                            mma_f8(tmem + TM_S + st * 2 * HM, ad + off, bd + off, I_S, k ? 1u : 0u);
-                        }
-                        mma_commit(BAR(B_S + st));
-                        firsts = (firsts & ~(1u << st)) | (((uint32_t)(msg >> 8) & 1u) << st);
-                        msg = 0;
-                        ++sJ;
-                        did = true;
-                    }
-                }
-                if (vJ < sJ) {
-                    const uint32_t st = vJ & 1u;
-                    if (mbar_test_wait(BAR(B_P + st), (vJ >> 1) & 1u)) {
-                        tc_fence_after();
-                        // C^T: panel c's 128 columns as M (one 128-byte atom), 32 rows a step (four groups of
-                        // eight, 1024 bytes apart); P the same with its 64 heads as N
-                        const uint64_t ad = smem_desc_sw128(base + SM_KV + st * STAGE, PANEL, 1024);
-                        const uint64_t bd = smem_desc_sw128(base + SM_P + st * P_BYTES, P_BYTES, 1024);
-                        const uint32_t keep = (firsts >> st) & 1u ? 0u : 1u;
-#pragma unroll
-                        for (int c = 0; c < NPAN; ++c)
-#pragma unroll
-                            for (int k = 0; k < BN / 32; ++k) {
-                                const uint64_t ao = ad + (uint64_t)((c * PANEL + k * 4096) >> 4);
-                                const uint64_t bo = bd + (uint64_t)((k * 4096) >> 4);
-                                mma_f8(tmem + TM_O + c * HM, ao, bo, I_HI, k ? 1u : keep);
-                                mma_f8(tmem + TM_O + c * HM, ao, bo + (64 >> 4), I_LO, 1u);
-                            }
-                        mma_commit(BAR(B_PV + st));
-                        ++vJ;
-                        did = true;
-                    }
-                }
-                if ((msg & 255) == kFin && vJ == sJ) break;
-                if (did) {
-                    idle = 0;
-                    since = 0;
-                    continue;
-                }
-                __nanosleep(32);
-                if ((++idle & 63u) == 0u) {
-                    if (*abort_flag) break;
-                    const uint64_t now = globaltimer_ns();
-                    if (since == 0) since = now;
-                    else if (now - since > kWaitLimitNs) {
-                        *abort_flag = 1;
-                        break;
-                    }
-                }
             }
-            if (*abort_flag) {   // let issued MMAs finish before TMEM is freed
-                mma_commit(BAR(B_DRAIN));
-                mbar_wait_drain(BAR(B_DRAIN), 0, 100000000ull);
+            if (vJ < sJ && done(B_P, vJ)) {
+                const uint32_t st = vJ & 1u;
+                tc_fence_after();
+                if (lead) {
+                    const uint32_t keep = (firsts >> st) & 1u ? 0u : 1u;
+                    if (st == 0) issue_pv<0, I_HI, I_LO>(base, tmem, keep);
+                    else issue_pv<1, I_HI, I_LO>(base, tmem, keep);
+                    mma_commit(BAR(B_PV + st));
+                }
+                __syncwarp();
+                ++vJ;
+                did = true;
+            }
+            if ((msg & 255) == kFin && vJ == sJ) break;
+            if (did) {
+                idle = 0;
+                since = 0;
+                continue;
+            }
+            __nanosleep(32);
+            if ((++idle & 63u) == 0u) {
+                if (__any_sync(kAll, *abort_flag != 0)) break;
+                const uint64_t now = globaltimer_ns();
+                if (since == 0) since = now;
+                else if (__any_sync(kAll, now - since > kWaitLimitNs)) {
+                    *abort_flag = 1;
+                    break;
+                }
             }
         }
+        if (lead && *abort_flag) {   // let issued MMAs finish before TMEM is freed
+            mma_commit(BAR(B_DRAIN));
+            mbar_wait_drain(BAR(B_DRAIN), 0, 100000000ull);
+        }
         __syncwarp();
-    } else if (warp < 8) {
+    } else {
         // ============================ softmax and epilogue ============================
-        const int quarter = warp & 3, hb = (warp >> 2) * 32, row = quarter * 32 + lane;
+        // Warp (quarter, heads hb..): its 32 rows by its 16 heads of every tile, and in O^T its 32 lanes of every
+        // panel by the same heads.  The four warps of the same heads agree on m and E without talking
+        // about them: they read the same maxima.
+        const int quarter = warp & 3, hb = (warp >> 2) * HPW, row = quarter * 32 + lane, hl = hb + (lane & (HPW - 1));
         const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16);
-        float *m_h = reinterpret_cast<float *>(ctl + C_M), *fac = reinterpret_cast<float *>(ctl + C_FAC);
+        float *head = reinterpret_cast<float *>(ctl + C_HEAD), *sums = reinterpret_cast<float *>(ctl + C_SUM);
         const float *qs = reinterpret_cast<const float *>(ctl + C_QS);
-        float l[32];
+        float l[HPW];
+        float m = 0.0f;        // of head hl
+        int E = 0;
         int64_t unit = T > 0 ? e0 / T : 0;
         const int64_t unit0 = unit;
         uint32_t J = 0, seg = 0;
-        int E = 0;
         bool any = false;      // the unit has a tile
         bool bad = false;
         for (uint32_t n = 0;; ++n) {
@@ -594,73 +673,76 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 // ---- the unit's output, or this range's part of it
                 const Unit un = unit_of(p, unit);
                 const bool whole = unit * T >= e0 && (unit + 1) * T <= e1;
-                float *scr = reinterpret_cast<float *>(smem + SM_P);     // [4][64] sums of the quarters
                 if (any) {
+                    // sums over the warp's rows: lanes i and i + 16 end up with head hb + i
+                    fold<8>(l, lane);
+                    fold<4>(l, lane);
+                    fold<2>(l, lane);
+                    fold<1>(l, lane);
+                    l[0] += __shfl_xor_sync(kAll, l[0], 16);
+                    if (lane < HPW) sums[quarter * HM + hl] = l[0];
                     bad = !warp_wait(BAR(B_PV + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag);
                     tc_fence_after();
-                    // sums over the warp's rows: lane i ends up with head hb + i
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) {
-                        const bool up = (lane & o) != 0;
-#pragma unroll
-                        for (int i = 0; i < o; ++i) {
-                            const float give = up ? l[i] : l[i + o];
-                            l[i] = (up ? l[i + o] : l[i]) + __shfl_xor_sync(kAll, give, o);
-                        }
-                    }
-                    scr[quarter * HM + hb + lane] = l[0];
                 }
                 if (bar_or(bad)) break;
                 float *ws = p.ws + ((size_t)cid * 2 + (unit == unit0 ? 0 : 1)) * SLOT;
-                if (threadIdx.x < HM) {
-                    const int hh = threadIdx.x;
-                    const float m = any ? m_h[hh] : -INFINITY;
-                    const float sum = any ? scr[hh] + scr[HM + hh] + scr[2 * HM + hh] + scr[3 * HM + hh] : 0.0f;
-                    if (whole) {
-                        const float sink = hh < un.nh ? __ldg(p.a.sink + un.h0 + hh) * kLog2e : 0.0f;
-                        fac[hh] = any ? 1.0f / (sum + exp2f(sink - m)) : 0.0f;
-                    } else {
-                        ws[SLOT_O + hh] = m;
-                        ws[SLOT_O + HM + hh] = sum;
-                    }
-                }
-                if (bar_or(false)) break;
+                const float sum = any ? sums[hl] + sums[HM + hl] + sums[2 * HM + hl] + sums[3 * HM + hl] : 0.0f;
                 const float unfold = ldexpf(1.0f, E - 17);
+                float f = unfold;                          // of head hl
+                if (whole) {
+                    const float sink = hl < un.nh ? __ldg(p.a.sink + un.h0 + hl) * kLog2e : 0.0f;
+                    f = any ? unfold / (sum + exp2f(sink - m)) : 0.0f;
+                } else if (quarter == 0 && lane < HPW) {
+                    ws[SLOT_O + hl] = any ? m : -INFINITY;
+                    ws[SLOT_O + HM + hl] = sum;
+                }
+                __syncwarp();
+                if (lane < HPW) head[hl] = f;              // the same from every quarter
+                __syncwarp();
                 const float2 *cs = nullptr;
                 if constexpr (ROPE)
                     if (whole) cs = rotation_row(p.a, un.tok, threadIdx.x == 0);
-                uint16_t *out = p.a.o + (un.tok * p.a.h + un.h0) * D;
-                // warps 0-3 take panels 0 and 1, warps 4-7 panels 2 and 3: thread = column
+                if (hb < un.nh && (whole || any)) {
 #pragma unroll 1
-                for (int k = 0; k < 8; ++k) {
-                    const int c = (hb >> 4) + (k >> 2), h0 = (k & 3) * 16, d = c * 128 + row;
-                    if (h0 >= un.nh) continue;
-                    uint32_t r[16];
-                    if (any) {
-                        tmem_ld16(tm + TM_O + c * HM + h0, r);
+                    for (int c = 0; c < NPAN; ++c) {
+                        const int d = c * 128 + row;
+                        uint32_t r[HPW];
+                        float x[HPW];
+                        tmem_ld16(tm + TM_O + c * HM + hb, r);
                         tmem_wait16(r);
-                    }
-                    if (whole) {
-                        uint16_t *col = out + (int64_t)h0 * D + d;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float x = any ? __uint_as_float(r[i]) * fac[h0 + i] * unfold : 0.0f;
-                            if constexpr (ROPE) {
-                                if (cs && c * 128 + quarter * 32 + 31 >= D - p.a.rd) {
-                                    const float y = __shfl_xor_sync(kAll, x, 1);
-                                    if (d >= D - p.a.rd) {
-                                        const float2 t = __ldg(cs + ((d - (D - p.a.rd)) >> 1));
-                                        x = (d & 1) ? x * t.x - y * t.y : x * t.x + y * t.y;
-                                    }
+                        for (int i = 0; i < HPW; i += 4) {
+                            const float4 f4 = lds4(head + hb + i);
+                            const float fv[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) x[i + k] = any ? __uint_as_float(r[i + k]) * fv[k] : 0.0f;
+                        }
+                        if (whole) {
+                            if (ROPE && cs && c * 128 + quarter * 32 + 31 >= D - p.a.rd) {
+                                const bool turned = d >= D - p.a.rd;
+                                float2 t = turned ? __ldg(cs + ((d - (D - p.a.rd)) >> 1)) : make_float2(1.0f, 0.0f);
+                                if (d & 1) t.y = -t.y;
+#pragma unroll
+                                for (int i = 0; i < HPW; ++i) {
+                                    const float y = __shfl_xor_sync(kAll, x[i], 1);
+                                    x[i] = turned ? x[i] * t.x + y * t.y : x[i];
                                 }
                             }
-                            if (h0 + i < un.nh) col[i * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-                        }
-                    } else if (any) {
-                        float *col = ws + h0 * D + d;
+                            uint16_t *col = p.a.o + (un.tok * p.a.h + un.h0 + hb) * D + d;
+                            if (hb + HPW <= un.nh) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (h0 + i < un.nh) col[i * D] = __uint_as_float(r[i]) * unfold;
+                                for (int i = 0; i < HPW; ++i) col[i * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < HPW; ++i)
+                                    if (hb + i < un.nh) col[i * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
+                            }
+                        } else {
+                            float *col = ws + hb * D + d;
+#pragma unroll
+                            for (int i = 0; i < HPW; ++i)
+                                if (hb + i < un.nh) col[i * D] = x[i];
+                        }
                     }
                 }
                 tc_fence_before();
@@ -673,102 +755,88 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             const bool first = (msg >> 8) & 1;
             const uint32_t st = J & 1u;
             const bool live = row < count;
-            float *scr = reinterpret_cast<float *>(smem + SM_P + st * P_BYTES);   // [4][64] maxima, [4] exponents
-            float v[32];
+            float *maxima = reinterpret_cast<float *>(ctl + C_MAX) + st * 4 * HM;
+            int *emax = reinterpret_cast<int *>(ctl + C_EMAX) + st * 4;
+            float v[HPW];
             int e = 0;
-            if (!bad) {
+            if (!bad)
                 bad = !warp_wait(BAR(B_KV + st), (J >> 1) & 1u, abort_flag) ||
-                      !warp_wait(BAR(B_S + st), (J >> 1) & 1u, abort_flag) ||
-                      (J >= 2 && !warp_wait(BAR(B_PV + st), ((J >> 1) - 1) & 1u, abort_flag));
-            }
+                      !warp_wait(BAR(B_S + st), (J >> 1) & 1u, abort_flag);
             if (!bad) {
                 if (first) ++seg;
                 tc_fence_after();
+                uint32_t r0[HPW], r1[HPW];
+                tmem_ld16(tm + TM_S + st * 2 * HM + hb, r0);
+                tmem_ld16(tm + TM_S + st * 2 * HM + HM + hb, r1);
                 e = (int)reinterpret_cast<const int8_t *>(ctl + C_REXP)[st * BN + row];
-                const float cr = ldexpf(1.0f, e - 13);
+                // a row beyond the tile's count scores -inf
+                const float cr = live ? ldexpf(1.0f, e - 13) : 0.0f, off = live ? 0.0f : -INFINITY;
                 const float *q = qs + ((seg - 1) & 1u) * HM + hb;
-#pragma unroll
-                for (int j = 0; j < 32; j += 16) {
-                    uint32_t r0[16], r1[16];
-                    tmem_ld16(tm + TM_S + st * 2 * HM + hb + j, r0);
-                    tmem_ld16(tm + TM_S + st * 2 * HM + HM + hb + j, r1);
-                    tmem_wait16(r0);
-                    tmem_wait16(r1);
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 q4 = lds4(q + j + i);
-                        const float qv[4] = {q4.x, q4.y, q4.z, q4.w};
-                        float mx[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float s = fmaf(__uint_as_float(r1[i + k]), 0.03125f, __uint_as_float(r0[i + k]));
-                            v[j + i + k] = live ? s * qv[k] * cr : -INFINITY;
-                            mx[k] = warp_max(v[j + i + k]);
-                        }
-                        if (lane == 0)
-                            *reinterpret_cast<float4 *>(scr + quarter * HM + hb + j + i) =
-                                make_float4(mx[0], mx[1], mx[2], mx[3]);
-                    }
-                }
+                tmem_wait16(r0);
+                tmem_wait16(r1);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(B_SFREE + st));
+#pragma unroll
+                for (int i = 0; i < HPW; i += 4) {
+                    const float4 q4 = lds4(q + i);
+                    const float qv[4] = {q4.x, q4.y, q4.z, q4.w};
+                    float mx[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float s = fmaf(__uint_as_float(r1[i + k]), 0.03125f, __uint_as_float(r0[i + k]));
+                        v[i + k] = fmaf(s * qv[k], cr, off);
+                        mx[k] = warp_max(v[i + k]);
+                    }
+                    if (lane == 0)
+                        *reinterpret_cast<float4 *>(maxima + quarter * HM + hb + i) = make_float4(mx[0], mx[1], mx[2], mx[3]);
+                }
                 const int te = __reduce_max_sync(kAll, live ? e : -128);
-                if (lane == 0 && hb == 0) reinterpret_cast<int *>(scr + 4 * HM)[quarter] = te;
+                if (lane == 0 && hb == 0) emax[quarter] = te;
             }
             if (bar_or(bad)) break;
-            bool moved = false;
-            if (threadIdx.x < HM) {
-                const int hh = threadIdx.x;
-                const float t = fmaxf(fmaxf(scr[hh], scr[HM + hh]), fmaxf(scr[2 * HM + hh], scr[3 * HM + hh]));
-                const float m = m_h[hh];
+            {
+                const float t = fmaxf(fmaxf(maxima[hl], maxima[HM + hl]), fmaxf(maxima[2 * HM + hl], maxima[3 * HM + hl]));
+                const int4 e4 = *reinterpret_cast<const int4 *>(emax);
+                const int tile_e = max(max(e4.x, e4.y), max(e4.z, e4.w));
+                const float m0 = m;
+                const int E0 = E;
                 const bool raise = !first && t > m + kSlack;
-                if (first || raise) m_h[hh] = t;
-                fac[hh] = raise ? exp2f(m - t) : 1.0f;
-                moved = raise;
-            }
-            const int4 te4 = *reinterpret_cast<const int4 *>(scr + 4 * HM);
-            const int tile_e = max(max(te4.x, te4.y), max(te4.z, te4.w));
-            const int E0 = E;
-            E = first ? tile_e : max(E, tile_e);
-            moved = moved || (!first && E > E0);
-            moved = bar_or(moved);
-            if (first) {
+                if (first || raise) m = t;
+                E = first ? tile_e : max(E, tile_e);
+                __syncwarp();
+                if (lane < HPW) head[hl] = m;          // the same from every quarter
+                __syncwarp();
+                if (first) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) l[i] = 0.0f;
-            }
-            if (moved) {
-                const float down = ldexpf(1.0f, E0 - E);
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 f = lds4(fac + hb + i);
-                    l[i] *= f.x;
-                    l[i + 1] *= f.y;
-                    l[i + 2] *= f.z;
-                    l[i + 3] *= f.w;
-                }
-                // O^T: every thread scales its column's heads (panels shared out as in the epilogue)
-                bad = !warp_wait(BAR(B_PV + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag);
-                tc_fence_after();
+                    for (int i = 0; i < HPW; ++i) l[i] = 0.0f;
+                } else if (__any_sync(kAll, raise) || E > E0) {
+                    // this warp's part of O^T, and its sums, follow m and E
+                    const float f = raise ? exp2f(m0 - m) : 1.0f, down = ldexpf(1.0f, E0 - E);
+                    bad = !warp_wait(BAR(B_PV + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag);
+                    tc_fence_after();
 #pragma unroll 1
-                for (int k = 0; k < 8 && !bad; ++k) {
-                    const int c = (hb >> 4) + (k >> 2), h0 = (k & 3) * 16;
-                    uint32_t r[16];
-                    tmem_ld16(tm + TM_O + c * HM + h0, r);
-                    tmem_wait16(r);
+                    for (int c = 0; c < NPAN && !bad; ++c) {
+                        uint32_t r[HPW];
+                        tmem_ld16(tm + TM_O + c * HM + hb, r);
+                        tmem_wait16(r);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (fac[h0 + i] * down));
-                    tmem_st16(tm + TM_O + c * HM + h0, r);
+                        for (int i = 0; i < HPW; ++i)
+                            r[i] = __float_as_uint(__uint_as_float(r[i]) * (__shfl_sync(kAll, f, i) * down));
+                        tmem_st16(tm + TM_O + c * HM + hb, r);
+                    }
+                    tmem_st_wait();
+#pragma unroll
+                    for (int i = 0; i < HPW; ++i) l[i] *= __shfl_sync(kAll, f, i);
                 }
-                tmem_st_wait();
             }
             any = true;
+            uint32_t hi[4], lo[4];
             {
                 const float fr = live ? ldexpf(1.0f, e - E + 4) : 0.0f;
-                uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 m4 = lds4(m_h + hb + i);
+                for (int i = 0; i < HPW; i += 4) {
+                    const float4 m4 = lds4(head + hb + i);
                     const float mv[4] = {m4.x, m4.y, m4.z, m4.w};
                     float pr[4];
 #pragma unroll
@@ -783,17 +851,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     hi[i >> 2] = prmt(h0, h1, 0x5410);
                     lo[i >> 2] = prmt(l0, l1, 0x5410);
                 }
-                const uint32_t pb = base + SM_P + st * P_BYTES + (uint32_t)row * 128;
-                const int ch = hb >> 4, sw = row & 7;
-                st_shared_v4(pb + (uint32_t)(((ch + 0) ^ sw) * 16), hi[0], hi[1], hi[2], hi[3]);
-                st_shared_v4(pb + (uint32_t)(((ch + 1) ^ sw) * 16), hi[4], hi[5], hi[6], hi[7]);
-                st_shared_v4(pb + (uint32_t)(((ch + 4) ^ sw) * 16), lo[0], lo[1], lo[2], lo[3]);
-                st_shared_v4(pb + (uint32_t)(((ch + 5) ^ sw) * 16), lo[4], lo[5], lo[6], lo[7]);
             }
+            // P is free once the tile before has been multiplied
+            if (J > 0 && !bad) bad = !warp_wait(BAR(B_PV + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag);
+            const uint32_t pb = base + SM_P + (uint32_t)row * 128;
+            st_shared_v4(pb + (uint32_t)((((hb >> 4) + 0) ^ (row & 7)) * 16), hi[0], hi[1], hi[2], hi[3]);
+            st_shared_v4(pb + (uint32_t)((((hb >> 4) + 4) ^ (row & 7)) * 16), lo[0], lo[1], lo[2], lo[3]);
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(B_P + st));
+            if (lane == 0) mbar_arrive(BAR(B_P));
             ++J;
         }
     }
