@@ -61,7 +61,8 @@ constexpr int P_BYTES = BN * 128;       // row r: 64 bytes hi, 64 bytes lo
 constexpr int SM_CTL = SM_P + P_BYTES;
 // control block
 constexpr int C_ROWS = 0;                       // [NR][128] int32 row numbers
-constexpr int C_REXP = C_ROWS + NR * BN * 4;    // [2][128] int8 e_r
+constexpr int C_EXPS = C_ROWS + NR * BN * 4;    // [128][16] int8 exponents of the tile being widened
+constexpr int C_REXP = C_EXPS + BN * (D / 32);  // [2][128] int8 e_r
 constexpr int C_MAX = C_REXP + 2 * BN;          // [2][4][64] f32 maxima of the quarters, by tile parity
 constexpr int C_EMAX = C_MAX + 2 * 4 * HM * 4;  // [2][4] int32 largest e_r of the quarters
 constexpr int C_SUM = C_EMAX + 32;              // [4][64] f32 sums of the quarters, at a unit's end
@@ -149,32 +150,36 @@ __device__ __forceinline__ bool bar_or(bool pred) {
     return r != 0;
 }
 
-// One try at a phase that lets the hardware suspend the thread for up to about 20 us.
-__device__ __forceinline__ bool try_long(uint32_t bar, uint32_t parity) {
+// One try at a phase that lets the hardware suspend the thread for up to NS nanoseconds.
+template <int NS>
+__device__ __forceinline__ bool try_hint(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "n"(NS)
         : "memory");
     return ok != 0;
 }
 
 // Bounded wait of a whole warp; false when it gave up, or another role did.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    bool ok = try_long(bar, parity);
+    bool ok = try_hint<20000>(bar, parity);
     if (!__all_sync(kAll, ok)) {
         const uint64_t t0 = globaltimer_ns();
         while (!ok && !*abort) {
-            ok = try_long(bar, parity);
+            ok = try_hint<20000>(bar, parity);
             if (!ok && globaltimer_ns() - t0 > kWaitLimitNs) *abort = 1;
         }
         ok = __all_sync(kAll, ok);
     }
     return ok;
 }
+
+// 2^k, 0 below the normal numbers
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)max(k + 127, 0) << 23); }
 
 __device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
@@ -190,6 +195,16 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t v) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
     return r;
+}
+
+// 16 bytes of the cache that no L1 line is kept for: beside 220 KB of shared memory L1 has 28 KB, less than the
+// rows of a tile in flight.
+__device__ __forceinline__ uint4 ld_row(const void *ptr) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(ptr));
+    return v;
 }
 
 // One head of q (16 values a lane) into [hi | lo]; returns g.
@@ -465,10 +480,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
         if (ok && open()) publish(kFin);
     } else if (warp >= W_ROWS && warp < W_MMA) {
         // ======================== rows (and q) into the swizzled operands ========================
-        // Warp w takes rows 16 w .. 16 w + 15, two a step: lanes 0-15 and 16-31 hold their 16 blocks.
-        const int w = warp - W_ROWS, u = lane & 15, half = lane >> 4;
-        const int panel = u >> 2, c0 = (u & 3) * 2;
-        const int mytile = 16 * w + u;                       // the row whose number and largest exponent this lane holds
+        // Warp w takes rows 16 w .. 16 w + 15, two a step; lane: panel lane / 8, row (lane / 4) % 2 of the two, block
+        // lane % 4 of the panel.  Eight neighbouring lanes then store to all eight 16-byte columns of a
+        // 128-byte row: the even ones from the even row, the odd ones from the odd row.
+        const int w = warp - W_ROWS, panel = lane >> 3, half = (lane >> 2) & 1, u = panel * 4 + (lane & 3);
+        const int mytile = 16 * w + (lane & 15);             // the row whose number and largest exponent this lane holds
+        uint32_t at[4];                                      // of the block's first half in step i % 4
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            at[i] = base + SM_KV + (uint32_t)panel * PANEL + (uint32_t)(16 * w + half) * 128 +
+                    (uint32_t)(((lane & 3) * 2 ^ (2 * i + half)) * 16);
         int64_t unit = T > 0 ? e0 / T : 0;
         uint32_t J = 0, seg = 0;
         for (uint32_t n = 0;; ++n) {
@@ -513,19 +534,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             }
             // the tile's codes, 16 bytes (one block) a lane and row, in flight until the stage is free
             uint4 raw[RPL];
-            int kx[RPL];
+            const uint4 *codes = reinterpret_cast<const uint4 *>(p.a.codes) + u;
 #pragma unroll
             for (int i = 0; i < RPL; ++i) {
-                const int r = __shfl_sync(kAll, myrow, 2 * i + half);
-                raw[i] = make_uint4(0, 0, 0, 0);
-                kx[i] = 0;
-                if (r >= 0) {
-                    raw[i] = __ldg(reinterpret_cast<const uint4 *>(p.a.codes + (int64_t)r * (D / 2)) + u);
-                    kx[i] = __ldg(p.a.exps + (int64_t)r * (D / 32) + u);
-                }
+                // beyond the tile's count: the pool's first row, which counts as zeros below
+                const int r = max(__shfl_sync(kAll, myrow, 2 * i + half), 0);
+                raw[i] = ld_row(codes + (int64_t)r * (D / 32));
             }
-            uint4 ev = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-            if (myrow >= 0) ev = __ldg(reinterpret_cast<const uint4 *>(p.a.exps + (int64_t)myrow * (D / 32)));
+            uint4 ev = ld_row(p.a.exps + (int64_t)max(myrow, 0) * (D / 32));
             if (J >= 2 && !warp_wait(BAR(B_PV + st), ((J >> 1) - 1) & 1u, abort_flag)) break;
             if (first) {
                 // P V of tile J - 2 is done, so the softmax is through with the scales of two units ago
@@ -536,32 +552,22 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             asm volatile("" : "+r"(ev.x), "+r"(ev.y), "+r"(ev.z), "+r"(ev.w));
 #pragma unroll
             for (int i = 0; i < RPL; ++i)
-                asm volatile("" : "+r"(raw[i].x), "+r"(raw[i].y), "+r"(raw[i].z), "+r"(raw[i].w), "+r"(kx[i]));
-            int emax = -128;                      // of row mytile
-            {
-                const uint32_t m4 = __vmaxs4(__vmaxs4(ev.x, ev.y), __vmaxs4(ev.z, ev.w));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) emax = max(emax, (int)(int8_t)(m4 >> (8 * i)));
-            }
-            const uint32_t sbase = base + SM_KV + st * STAGE + (uint32_t)panel * PANEL;
+                asm volatile("" : "+r"(raw[i].x), "+r"(raw[i].y), "+r"(raw[i].z), "+r"(raw[i].w));
+            const uint32_t m4 = __vmaxs4(__vmaxs4(ev.x, ev.y), __vmaxs4(ev.z, ev.w));
+            const int emax = max(max((int)(int8_t)m4, (int)(int8_t)(m4 >> 8)), max((int)(int8_t)(m4 >> 16), (int)m4 >> 24));
+            const int emask = myrow >= 0 ? emax : 1 << 20;       // no block of a row that is not there is in reach
+            int8_t *mine = reinterpret_cast<int8_t *>(ctl + C_EXPS) + w * 16 * (D / 32);
+            __syncwarp();
+            if (lane < 16) reinterpret_cast<uint4 *>(mine)[lane] = ev;
+            __syncwarp();
 #pragma unroll
             for (int i = 0; i < RPL; ++i) {
-                const int row = 16 * w + 2 * i + half;
-                const int er = __shfl_sync(kAll, emax, 2 * i + half);
-                const int x = kx[i] - er + 13;
+                const int er = __shfl_sync(kAll, emask, 2 * i + half);
                 uint32_t o[8];
-                widen(raw[i], x, o);
-                // both 16-byte halves of the block; odd panels start with the other one, so that eight
-                // neighbouring lanes cover all banks
-                const uint32_t rb = sbase + (uint32_t)row * 128;
-                const uint32_t ca = rb + (uint32_t)((c0 ^ (row & 7)) * 16), cb = rb + (uint32_t)(((c0 + 1) ^ (row & 7)) * 16);
-                if (panel & 1) {
-                    st_shared_v4(cb, o[4], o[5], o[6], o[7]);
-                    st_shared_v4(ca, o[0], o[1], o[2], o[3]);
-                } else {
-                    st_shared_v4(ca, o[0], o[1], o[2], o[3]);
-                    st_shared_v4(cb, o[4], o[5], o[6], o[7]);
-                }
+                widen(raw[i], mine[(2 * i + half) * (D / 32) + u] - er + 13, o);
+                const uint32_t to = at[i & 3] + st * STAGE + (uint32_t)i * 256;
+                st_shared_v4(to, o[0], o[1], o[2], o[3]);
+                st_shared_v4(to ^ 16u, o[4], o[5], o[6], o[7]);
             }
             if (lane < 16) reinterpret_cast<int8_t *>(ctl + C_REXP)[st * BN + mytile] = (int8_t)emax;
             fence_proxy_async_smem();
@@ -625,7 +631,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 since = 0;
                 continue;
             }
-            __nanosleep(32);
+            // nothing to issue: sleep on the likelier of the two for up to 100 ns
+            if (vJ < sJ) try_hint<100>(BAR(B_P), vJ & 1u);
+            else if (msg) try_hint<100>(BAR(B_KV + (sJ & 1u)), (sJ >> 1) & 1u);
+            else try_hint<100>(BAR(B_MSG + n % NR), (n / NR) & 1u);
             if ((++idle & 63u) == 0u) {
                 if (__any_sync(kAll, *abort_flag != 0)) break;
                 const uint64_t now = globaltimer_ns();
@@ -687,7 +696,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 if (bar_or(bad)) break;
                 float *ws = p.ws + ((size_t)cid * 2 + (unit == unit0 ? 0 : 1)) * SLOT;
                 const float sum = any ? sums[hl] + sums[HM + hl] + sums[2 * HM + hl] + sums[3 * HM + hl] : 0.0f;
-                const float unfold = ldexpf(1.0f, E - 17);
+                const float unfold = pow2(E - 17);
                 float f = unfold;                          // of head hl
                 if (whole) {
                     const float sink = hl < un.nh ? __ldg(p.a.sink + un.h0 + hl) * kLog2e : 0.0f;
@@ -770,7 +779,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 tmem_ld16(tm + TM_S + st * 2 * HM + HM + hb, r1);
                 e = (int)reinterpret_cast<const int8_t *>(ctl + C_REXP)[st * BN + row];
                 // a row beyond the tile's count scores -inf
-                const float cr = live ? ldexpf(1.0f, e - 13) : 0.0f, off = live ? 0.0f : -INFINITY;
+                const float cr = live ? pow2(e - 13) : 0.0f, off = live ? 0.0f : -INFINITY;
                 const float *q = qs + ((seg - 1) & 1u) * HM + hb;
                 tmem_wait16(r0);
                 tmem_wait16(r1);
@@ -812,7 +821,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     for (int i = 0; i < HPW; ++i) l[i] = 0.0f;
                 } else if (__any_sync(kAll, raise) || E > E0) {
                     // this warp's part of O^T, and its sums, follow m and E
-                    const float f = raise ? exp2f(m0 - m) : 1.0f, down = ldexpf(1.0f, E0 - E);
+                    const float f = raise ? exp2f(m0 - m) : 1.0f, down = pow2(E0 - E);
                     bad = !warp_wait(BAR(B_PV + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag);
                     tc_fence_after();
 #pragma unroll 1
@@ -833,7 +842,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             any = true;
             uint32_t hi[4], lo[4];
             {
-                const float fr = live ? ldexpf(1.0f, e - E + 4) : 0.0f;
+                const float fr = live ? pow2(e - E + 4) : 0.0f;
 #pragma unroll
                 for (int i = 0; i < HPW; i += 4) {
                     const float4 m4 = lds4(head + hb + i);
