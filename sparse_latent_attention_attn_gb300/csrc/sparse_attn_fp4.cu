@@ -5,19 +5,20 @@
 // "DeepSeek V4.1", attention/query-latent, Attention.forward (the output's inverse rotation).  Rows are
 // e2m1 codes with a power-of-two scale per 32 values, reached through a table of pages.
 //
-// The mathematics.  A row is v_r = 2^(e_r - 13) c_r, e_r its largest block exponent and c_r its codes times
-// 2^(k - e_r + 13): e2m1 has one mantissa bit, so c_r is exact in e5m2 for blocks down to 26 octaves below
+// The mathematics.  A row is v_r = 2^(e_r - 12) c_r, e_r its largest block exponent and c_r its codes times
+// 2^(k - e_r + 12): e2m1 has one mantissa bit, so c_r is exact in e5m2 for blocks down to 26 octaves below
 // e_r (lower ones count as zeros).  One byte a value serves as key and as value, and the row's own power
 // of two moves to where the row is a single number: to its scores, and to its probability.
 //  * q = 2^g (hi + 2^-5 lo), hi and lo in e4m3: hi holds q's top four significant bits, lo the four below
 //    them, so a bf16 q (eight) is exact down to 2^-9 of its head's largest value and off by 2^-22 of that
 //    largest value below.  S^T = C [hi | lo]: M = 128 rows, N = 64 heads twice, and the score is
-//    (S_hi + 2^-5 S_lo) 2^(g + e_r - 13) scale.
+//    (S_hi + 2^-5 S_lo) 2^(g + e_r - 12) scale.
 //  * P' = 2^(s - m + e_r - E + 4) for running m (per head, lazily raised, at most 4 octaves late) and E (the
 //    largest e_r so far), at most 256; P' = hi - lo with hi in e4m3 and lo in e5m2, each to nearest: off by
 //    2^-8 of itself, as bf16 would be, from 2^-6 on (hi has four bits, lo three of the rest), and by 2^-13
-//    below (hi is a multiple of 2^-9): 2^-17 of the largest probability of a head.  O^T += C^T (hi - lo), d = 512 as four blocks of 128 lanes, heads as
-//    columns; O 2^(E - 17) / l is the output.  l sums the unrounded f32 p.
+//    below (hi is a multiple of 2^-9): 2^-17 of the largest probability of a head.  O^T +=
+//    C^T (hi - lo), d = 512 as four blocks of 128 lanes, heads as columns; O 2^(E - 16) / l is the
+//    output.  l sums the unrounded f32 p.
 //
 // Why so.  A tile is 128 rows of 512 bytes, so two tiles, q (64 KB as hi and lo) and P fit the 227 KB of an
 // SM; as bf16 only tiles of 64 rows would, and a 64-row tcgen05.mma takes the time of a 128-row one.  With
@@ -26,8 +27,9 @@
 //
 // Warps: 0-15 softmax and epilogue (warp w: TMEM lanes 32 (w % 4).., heads 16 (w / 4)..), 16-23 rows (codes
 // loaded a tile ahead into registers, widened into the swizzled stage; q at a unit's first tile), 24 MMA
-// issue, 25 index rows: it drops entries without a row, turns the others into row numbers and hands out
-// tiles of up to 128 through a ring of messages that every role reads in order.
+// issue, 25 index rows: it drops entries without a row, turns the others into row numbers and hands tiles of
+// up to 128 to the row warps (a unit without rows gives one tile of none).  What a tile is (its rows, whether
+// it is its unit's first or last) goes on with the stage.
 // A unit is one token and up to 64 heads; units are shared out as in the other attention kernels
 // (attn_split.cuh), and units cut by a range boundary leave f32 partials that a second kernel merges.
 // Every wait is bounded (2 s): then DS_DEV_TIMEOUT is flagged, issued MMAs are drained, TMEM is freed.
@@ -61,27 +63,28 @@ constexpr int P_BYTES = BN * 128;       // row r: 64 bytes hi, 64 bytes lo
 constexpr int SM_CTL = SM_P + P_BYTES;
 // control block
 constexpr int C_ROWS = 0;                       // [NR][128] int32 row numbers
-constexpr int C_EXPS = C_ROWS + NR * BN * 4;    // [128][16] int8 exponents of the tile being widened
+constexpr int C_EXPS = C_ROWS + NR * BN * 4;    // [128][16] k - e_r + 27 (0: out of reach) of the tile being widened
 constexpr int C_REXP = C_EXPS + BN * (D / 32);  // [2][128] int8 e_r
-constexpr int C_MAX = C_REXP + 2 * BN;          // [2][4][64] f32 maxima of the quarters, by tile parity
-constexpr int C_EMAX = C_MAX + 2 * 4 * HM * 4;  // [2][4] int32 largest e_r of the quarters
-constexpr int C_SUM = C_EMAX + 32;              // [4][64] f32 sums of the quarters, at a unit's end
+constexpr int C_MAX = C_REXP + 2 * BN;          // [4][64] f32 maxima of the quarters
+constexpr int C_EMAX = C_MAX + 4 * HM * 4;      // [4] int32 largest e_r of the quarters
+constexpr int C_SUM = C_EMAX + 16;              // [4][64] f32 sums of the quarters, at a unit's end
 constexpr int C_HEAD = C_SUM + 4 * HM * 4;      // [64] f32 running maximum; at a unit's end the output's factor
 constexpr int C_QS = C_HEAD + HM * 4;           // [2][64] f32 2^g scale log2(e), by unit parity
 constexpr int C_BAR = C_QS + 2 * HM * 4;
 enum : int {
-    B_MSG = 0,                  // [NR] index -> all: message written
-    B_MSGFREE = B_MSG + NR,     // [NR] all -> index
-    B_KV = B_MSGFREE + NR,      // [2] rows -> MMA, softmax: stage written (and q, at a unit's first tile)
-    B_PV = B_KV + 2,            // [2] MMA -> rows, softmax: P V of the tile done
-    B_S = B_PV + 2,             // [2] MMA -> softmax, rows: scores ready
+    B_MSG = 0,                  // [NR] index -> rows: message written
+    B_MSGFREE = B_MSG + NR,     // [NR] rows -> index
+    B_KV = B_MSGFREE + NR,      // [2] rows -> MMA, softmax: stage and its meta written (and q, at a unit's first tile)
+    B_PV = B_KV + 2,            // [2][4] MMA -> rows, softmax: P V of the tile's rows 32 k .. done
+    B_S = B_PV + 8,             // [2] MMA -> softmax, rows: scores ready
     B_SFREE = B_S + 2,          // [2] softmax -> MMA: scores read
     B_P = B_SFREE + 2,          // softmax -> MMA: P written
     B_DRAIN = B_P + 1,
     B_COUNT = B_DRAIN + 1
 };
 constexpr int C_MSG = C_BAR + 8 * B_COUNT;      // [NR] int32 message heads
-constexpr int C_TMEM = C_MSG + 4 * NR;
+constexpr int C_META = C_MSG + 4 * NR;          // [2] int32 the stages' messages
+constexpr int C_TMEM = C_META + 8;
 constexpr int C_ABORT = C_TMEM + 4;
 constexpr int SMEM_BYTES = SM_CTL + C_ABORT + 4;
 static_assert(C_BAR % 8 == 0 && SMEM_BYTES <= 232448, "shared memory budget");
@@ -97,8 +100,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 4.0f;          // octaves that m may be late
 constexpr uint32_t kAll = 0xffffffffu;
 
-// messages: kind | first tile of its unit << 8 | rows << 16
-constexpr int kTile = 1, kEnd = 2, kFin = 3;
+// messages: kind | first tile of its unit << 8 | last << 9 | the unit is whole << 10 | the range's first << 11 |
+// rows << 16
+constexpr int kTile = 1, kFin = 2, kFirst = 1 << 8, kLast = 1 << 9, kWhole = 1 << 10, kSlot0 = 1 << 11;
 
 // a partial slot (f32): O [64][512], then running maxima [64] (log2 domain, -inf: no row) and sums [64]
 constexpr int SLOT_O = HM * D;
@@ -207,15 +211,15 @@ __device__ __forceinline__ uint4 ld_row(const void *ptr) {
     return v;
 }
 
-// One head of q (16 values a lane) into [hi | lo]; returns g.
-__device__ __forceinline__ int put_q(uint32_t sq, int hh, const uint4 (&v)[2], int lane) {
+// One head of q (16 values a lane; sign: its sign bit is flipped) into [hi | lo]; returns g.
+__device__ __forceinline__ int put_q(uint32_t sq, int hh, const uint4 (&v)[2], int lane, uint32_t sign) {
     const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
     uint32_t top = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
     top = __reduce_max_sync(kAll, top);
     const int g = max((int)(top >> 7) - 127 - 7, -126);      // the largest value lies in [128, 256) 2^g
-    const float down = __uint_as_float((uint32_t)(127 - g) << 23);
+    const float down = __uint_as_float(((uint32_t)(127 - g) << 23) | sign);
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -234,10 +238,11 @@ __device__ __forceinline__ int put_q(uint32_t sq, int hh, const uint4 (&v)[2], i
     return g;
 }
 
-// The 32 codes of a block at 2^x in e5m2: pairs widened to f16, times 2^x (exact), and the high bytes of the
-// f16 values, which are e5m2 (e2m1 has one mantissa bit, e5m2 two).
-__device__ __forceinline__ void widen(const uint4 raw, int x, uint32_t (&o)[8]) {
-    const uint32_t sc = x >= -13 ? (uint32_t)(x + 15) * 0x04000400u : 0u;
+// The 32 codes of a block at 2^(y - 15) in e5m2: pairs widened to f16, times the f16 number whose exponent field
+// is y (exact; y = 0 is zero), and the high bytes of the f16 values, which are e5m2 (e2m1 has one
+// mantissa bit, e5m2 two).
+__device__ __forceinline__ void widen(const uint4 raw, uint32_t y, uint32_t (&o)[8]) {
+    const uint32_t sc = y * 0x04000400u;
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -255,6 +260,11 @@ __device__ __forceinline__ void widen(const uint4 raw, int x, uint32_t (&o)[8]) 
             "prmt.b32 %1, f2, f3, 0x7531;\n\t}"
             : "=r"(o[2 * k]), "=r"(o[2 * k + 1])
             : "r"(w[k]), "r"(sc));
+}
+
+// Four bytes of max(k, low) - low + lift (signed k and low, biased to unsigned so that no byte borrows).
+__device__ __forceinline__ uint32_t above(uint32_t k, uint32_t low, uint32_t lift) {
+    return (__vmaxs4(k, low) ^ 0x80808080u) - (low ^ 0x80808080u) + lift;
 }
 
 // Two probabilities as hi (e4m3) - lo (e5m2): lo from hi - p, which is exact in f32.
@@ -339,19 +349,22 @@ __device__ __forceinline__ void issue_s(uint32_t base, uint32_t tmem) {
 }
 
 // O^T += C^T P: panel c's 128 columns as M (one 128-byte atom), 32 rows a step (four groups of eight, 1024
-// bytes apart); P the same with its 64 heads as N, hi then lo.
+// bytes apart); P the same with its 64 heads as N, hi then lo.  Rows outermost: each step's rows are handed
+// back (bar) as soon as its four panels are multiplied.
 template <int ST, uint32_t I_HI, uint32_t I_LO>
-__device__ __forceinline__ void issue_pv(uint32_t base, uint32_t tmem, uint32_t keep) {
+__device__ __forceinline__ void issue_pv(uint32_t base, uint32_t tmem, uint32_t keep, uint32_t bar) {
     const uint64_t a = smem_desc_sw128(base + SM_KV + ST * STAGE, PANEL, 1024);
     const uint64_t b = smem_desc_sw128(base + SM_P, P_BYTES, 1024);
 #pragma unroll
-    for (int c = 0; c < NPAN; ++c)
+    for (int k = 0; k < BN / 32; ++k) {
 #pragma unroll
-        for (int k = 0; k < BN / 32; ++k) {
+        for (int c = 0; c < NPAN; ++c) {
             const uint64_t ao = a + (uint64_t)((c * PANEL + k * 4096) >> 4), bo = b + (uint64_t)((k * 4096) >> 4);
             mma_f8(tmem + TM_O + c * HM, ao, bo, I_HI, k ? 1u : keep);
             mma_f8(tmem + TM_O + c * HM, ao, bo + (64 >> 4), I_LO, 1u);
         }
+        mma_commit(bar + 8 * k);
+    }
 }
 
 template <bool ROPE>
@@ -370,11 +383,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
     if (threadIdx.x == 0) {
         for (int i = 0; i < NR; ++i) {
             mbar_init(BAR(B_MSG + i), 1);
-            mbar_init(BAR(B_MSGFREE + i), NSOFTW + NROWW + 1);   // softmax warps, row warps, the MMA warp
+            mbar_init(BAR(B_MSGFREE + i), NROWW);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(BAR(B_KV + i), NROWW);
-            mbar_init(BAR(B_PV + i), 1);
+            for (int k = 0; k < 4; ++k) mbar_init(BAR(B_PV + 4 * i + k), 1);
             mbar_init(BAR(B_S + i), 1);
             mbar_init(BAR(B_SFREE + i), NSOFTW);
         }
@@ -394,16 +407,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
     grid_dependency_wait();
     volatile int *msgs = reinterpret_cast<volatile int *>(ctl + C_MSG);
 
-    // message number n, in order; released at once by all readers but the row warps, which still need its rows
-    auto read_msg = [&](uint32_t n, int &msg) -> bool {
-        if (!warp_wait(BAR(B_MSG + n % NR), (n / NR) & 1u, abort_flag)) return false;
-        msg = msgs[n % NR];
-        return true;
-    };
-    auto free_msg = [&](uint32_t n) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_MSGFREE + n % NR));
-    };
+    volatile int *meta = reinterpret_cast<volatile int *>(ctl + C_META);
 
     if (warp == W_IDX) {
         // ================================ index rows to tiles of row numbers ================================
@@ -418,18 +422,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             ++n;
         };
         bool ok = true, flagged = false;
-        for (int64_t u = T > 0 ? e0 / T : 0; ok && u * T < e1; ++u) {
+        const int64_t u0 = e0 / T;
+        for (int64_t u = u0; ok && u * T < e1; ++u) {
             const Unit un = unit_of(p, u);
             const int64_t bi = un.tok / p.a.m;
             const int32_t *idx = p.a.idx + un.tok * T;
             const int32_t *bt = p.a.block_table + bi * p.a.max_pages;
             const int a = (int)((e0 > u * T ? e0 : u * T) - u * T);
             const int z = (int)((e1 < (u + 1) * T ? e1 : (u + 1) * T) - u * T);
-            int fill = 0, first = 1 << 8;
+            const int tile = kTile | (a == 0 && z == T ? kWhole : 0) | (u == u0 ? kSlot0 : 0);
+            int fill = 0, first = kFirst;
             int nxt[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) nxt[k] = a + 32 * k + lane < z ? __ldg(idx + a + 32 * k + lane) : -1;
             ok = open();
+            int32_t *slot = reinterpret_cast<int32_t *>(ctl + C_ROWS) + (n % NR) * BN;
             for (int j = a; ok && j < z; j += 128) {
                 int row[4], pg[4];
                 bool bad = false;
@@ -453,17 +460,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                         }
                     }
                     const uint32_t have = __ballot_sync(kAll, row[k] >= 0);
-                    const int at = fill + __popc(have & lanemask_lt()), total = fill + __popc(have);
-                    int32_t *slot = reinterpret_cast<int32_t *>(ctl + C_ROWS) + (n % NR) * BN;
+                    const int at = fill + __popc(have & lanemask_lt());
                     if (row[k] >= 0 && at < BN) slot[at] = row[k];
-                    fill = total;
-                    if (total >= BN) {
-                        publish(kTile | first | (BN << 16));
+                    fill += __popc(have);
+                    if (fill > BN) {     // a full tile goes out once it is known not to be the last
+                        publish(tile | first | (BN << 16));
                         first = 0;
                         ok = ok && open();
                         slot = reinterpret_cast<int32_t *>(ctl + C_ROWS) + (n % NR) * BN;
                         if (ok && row[k] >= 0 && at >= BN) slot[at - BN] = row[k];
-                        fill = total - BN;
+                        fill -= BN;
                     }
                 }
                 if (bad && !flagged) {
@@ -471,42 +477,41 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     flagged = true;
                 }
             }
-            if (ok && fill > 0) {
-                publish(kTile | first | (fill << 16));
-                ok = open();
-            }
-            if (ok) publish(kEnd);
+            if (ok) publish(tile | first | kLast | (fill << 16));
         }
         if (ok && open()) publish(kFin);
     } else if (warp >= W_ROWS && warp < W_MMA) {
         // ======================== rows (and q) into the swizzled operands ========================
-        // Warp w takes rows 16 w .. 16 w + 15, two a step; lane: panel lane / 8, row (lane / 4) % 2 of the two, block
-        // lane % 4 of the panel.  Eight neighbouring lanes then store to all eight 16-byte columns of a
-        // 128-byte row: the even ones from the even row, the odd ones from the odd row.
+        // Warp w takes rows 4 w .. 4 w + 3 of each 32 (of each step of P V), two a step: step i rows
+        // 32 (i / 2) + 4 w + 2 (i % 2) + 0, 1.  Lane: panel lane / 8, row (lane / 4) % 2 of the two, block lane % 4
+        // of the panel.  Eight neighbouring lanes then store to all eight 16-byte columns of a 128-byte row:
+        // the even ones from the even row, the odd ones from the odd row.
         const int w = warp - W_ROWS, panel = lane >> 3, half = (lane >> 2) & 1, u = panel * 4 + (lane & 3);
-        const int mytile = 16 * w + (lane & 15);             // the row whose number and largest exponent this lane holds
-        uint32_t at[4];                                      // of the block's first half in step i % 4
+        const int mytile = 32 * ((lane >> 2) & 3) + 4 * w + (lane & 3);   // the row (of step i: lane 2 i + half) it holds
+        uint32_t at[2];                                      // of the block's first half in step i % 2
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            at[i] = base + SM_KV + (uint32_t)panel * PANEL + (uint32_t)(16 * w + half) * 128 +
-                    (uint32_t)(((lane & 3) * 2 ^ (2 * i + half)) * 16);
-        int64_t unit = T > 0 ? e0 / T : 0;
-        uint32_t J = 0, seg = 0;
-        for (uint32_t n = 0;; ++n) {
-            int msg = 0;
-            if (!read_msg(n, msg)) break;
-            const int kind = msg & 255, count = msg >> 16;
-            const bool first = (msg >> 8) & 1;
-            if (kind == kFin) break;
-            if (kind == kEnd) {
-                free_msg(n);
-                ++unit;
-                continue;
+        for (int i = 0; i < 2; ++i)
+            at[i] = base + SM_KV + (uint32_t)panel * PANEL + (uint32_t)(4 * w + 2 * i + half) * 128 +
+                    (uint32_t)(((lane & 3) * 2 ^ (4 * (w & 1) + 2 * i + half)) * 16);
+        const uint32_t sign = p.scale_log2 < 0.0f ? 0x80000000u : 0u;
+        int unit = (int)(e0 / T);
+        uint32_t seg = 0;
+        for (uint32_t J = 0;; ++J) {
+            if (!warp_wait(BAR(B_MSG + J % NR), (J / NR) & 1u, abort_flag)) break;
+            const int msg = msgs[J % NR], count = msg >> 16;
+            const bool first = msg & kFirst;
+            const uint32_t st = J & 1u;
+            if ((msg & 255) == kFin) {
+                if (J >= 2 && !warp_wait(BAR(B_PV + 4 * st + 3), ((J >> 1) - 1) & 1u, abort_flag)) break;
+                if (warp == W_ROWS && lane == 0) meta[st] = msg;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(B_KV + st));
+                break;
             }
             const int myrow =
-                mytile < count ? reinterpret_cast<const int32_t *>(ctl + C_ROWS)[(n % NR) * BN + mytile] : -1;
-            free_msg(n);
-            const uint32_t st = J & 1u;
+                mytile < count ? reinterpret_cast<const int32_t *>(ctl + C_ROWS)[(J % NR) * BN + mytile] : -1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(B_MSGFREE + J % NR));
             float qs = 0.0f;                      // lane i < 8: the scale of head 8 w + i
             if (first) {
                 // q of the unit, once S of the tile before has read the last one's
@@ -527,105 +532,106 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int g = put_q(base + SM_Q, 8 * w + i0 + k, v[k], lane);
-                        if (lane == i0 + k) qs = ldexpf(p.scale_log2, g);
+                        const int g = put_q(base + SM_Q, 8 * w + i0 + k, v[k], lane, sign);
+                        if (lane == i0 + k) qs = fmaxf(fabsf(p.scale_log2) * pow2(g), 1.17549435e-38f);   // never 0: see the scores
                     }
                 }
             }
             // the tile's codes, 16 bytes (one block) a lane and row, in flight until the stage is free
-            uint4 raw[RPL];
-            const uint4 *codes = reinterpret_cast<const uint4 *>(p.a.codes) + u;
+            // beyond the tile's count: the pool's first row (q, if there may be none), which counts as zeros below
+            uint4 raw[RPL], ev;
+            const uint8_t *pool = count > 0 ? p.a.codes : reinterpret_cast<const uint8_t *>(p.a.q);
+#pragma unroll
+            for (int i = 0; i < RPL; ++i)
+                raw[i] = ld_row(pool + (int64_t)max(__shfl_sync(kAll, myrow, 2 * i + half), 0) * (D / 2) + u * 16);
+            ev = ld_row(count > 0 ? (const void *)(p.a.exps + (int64_t)max(myrow, 0) * (D / 32)) : (const void *)p.a.q);
+            // the row's largest exponent, and k - e_r + 27 of its 16 blocks, 0 where that is less (or there is no row)
+            const uint32_t m4 = __vmaxs4(__vmaxs4(ev.x, ev.y), __vmaxs4(ev.z, ev.w));
+            const int emax = max(max((int)(int8_t)m4, (int)(int8_t)(m4 >> 8)), max((int)(int8_t)(m4 >> 16), (int)m4 >> 24));
+            const uint32_t low = (uint32_t)(uint8_t)max(emax - 27, -128) * 0x01010101u;
+            const uint32_t lift = (uint32_t)(uint8_t)(max(emax - 27, -128) - (emax - 27)) * 0x01010101u;
+            const uint32_t on = myrow >= 0 ? kAll : 0u;
+            uint8_t *mine = ctl + C_EXPS + w * 16 * (D / 32);
+            __syncwarp();
+            if (lane < 16)
+                reinterpret_cast<uint4 *>(mine)[lane] =
+                    make_uint4(above(ev.x, low, lift) & on, above(ev.y, low, lift) & on, above(ev.z, low, lift) & on,
+                               above(ev.w, low, lift) & on);
+            __syncwarp();
+            uint32_t y[RPL];
+#pragma unroll
+            for (int i = 0; i < RPL; ++i) y[i] = mine[(2 * i + half) * (D / 32) + u];
+            bool ok = true;
 #pragma unroll
             for (int i = 0; i < RPL; ++i) {
-                // beyond the tile's count: the pool's first row, which counts as zeros below
-                const int r = max(__shfl_sync(kAll, myrow, 2 * i + half), 0);
-                raw[i] = ld_row(codes + (int64_t)r * (D / 32));
+                if (J >= 2 && (i & 1) == 0) ok = ok && warp_wait(BAR(B_PV + 4 * st + (i >> 1)), ((J >> 1) - 1) & 1u, abort_flag);
+                // the codes are first touched here, behind the wait
+                asm volatile("" : "+r"(raw[i].x), "+r"(raw[i].y), "+r"(raw[i].z), "+r"(raw[i].w));
+                uint32_t o[8];
+                widen(raw[i], y[i], o);
+                const uint32_t to = at[i & 1] + st * STAGE + (uint32_t)(i >> 1) * 4096;
+                st_shared_v4(to, o[0], o[1], o[2], o[3]);
+                st_shared_v4(to ^ 16u, o[4], o[5], o[6], o[7]);
             }
-            uint4 ev = ld_row(p.a.exps + (int64_t)max(myrow, 0) * (D / 32));
-            if (J >= 2 && !warp_wait(BAR(B_PV + st), ((J >> 1) - 1) & 1u, abort_flag)) break;
+            if (!ok) break;
+            if (warp == W_ROWS && lane == 0) meta[st] = msg;
+            if (msg & kLast) ++unit;
             if (first) {
                 // P V of tile J - 2 is done, so the softmax is through with the scales of two units ago
                 if (lane < 8) reinterpret_cast<float *>(ctl + C_QS)[(seg & 1u) * HM + 8 * w + lane] = qs;
                 ++seg;
             }
-            // what was loaded is first touched here, behind the wait
-            asm volatile("" : "+r"(ev.x), "+r"(ev.y), "+r"(ev.z), "+r"(ev.w));
-#pragma unroll
-            for (int i = 0; i < RPL; ++i)
-                asm volatile("" : "+r"(raw[i].x), "+r"(raw[i].y), "+r"(raw[i].z), "+r"(raw[i].w));
-            const uint32_t m4 = __vmaxs4(__vmaxs4(ev.x, ev.y), __vmaxs4(ev.z, ev.w));
-            const int emax = max(max((int)(int8_t)m4, (int)(int8_t)(m4 >> 8)), max((int)(int8_t)(m4 >> 16), (int)m4 >> 24));
-            const int emask = myrow >= 0 ? emax : 1 << 20;       // no block of a row that is not there is in reach
-            int8_t *mine = reinterpret_cast<int8_t *>(ctl + C_EXPS) + w * 16 * (D / 32);
-            __syncwarp();
-            if (lane < 16) reinterpret_cast<uint4 *>(mine)[lane] = ev;
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < RPL; ++i) {
-                const int er = __shfl_sync(kAll, emask, 2 * i + half);
-                uint32_t o[8];
-                widen(raw[i], mine[(2 * i + half) * (D / 32) + u] - er + 13, o);
-                const uint32_t to = at[i & 3] + st * STAGE + (uint32_t)i * 256;
-                st_shared_v4(to, o[0], o[1], o[2], o[3]);
-                st_shared_v4(to ^ 16u, o[4], o[5], o[6], o[7]);
-            }
             if (lane < 16) reinterpret_cast<int8_t *>(ctl + C_REXP)[st * BN + mytile] = (int8_t)emax;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0 && !(p.stall_first_tile && J == 0)) mbar_arrive(BAR(B_KV + st));
-            ++J;
         }
     } else if (warp == W_MMA) {
         // ================================== MMA issue ==================================
-        // The whole warp walks the loop, so that its addresses stay uniform; one lane issues.
+        // The whole warp walks the loop, one lane issues.
         constexpr uint32_t I_S = idesc8(BN, 2 * HM, 1, 0, false);
         constexpr uint32_t I_HI = idesc8(128, HM, 1, 0, true), I_LO = idesc8(128, HM, 1, 1, true, true);
         const bool lead = lane == 0;
         auto done = [&](int bar, uint32_t phase) -> bool { return __all_sync(kAll, mbar_test_wait(BAR(bar), phase & 1u)); };
-        uint32_t n = 0, sJ = 0, vJ = 0;    // next message, next tile of S and of P V
-        int msg = 0;                       // the message in hand (0: none)
+        uint32_t sJ = 0, vJ = 0;           // next tile of S and of P V
+        bool fin = false;                  // no more tiles
         uint32_t firsts = 0;               // bit J & 1: tile J is its unit's first
         uint32_t idle = 0;
         uint64_t since = 0;
-        for (;;) {
+        while (!fin || vJ < sJ) {
             bool did = false;
-            if (msg == 0 && done(B_MSG + n % NR, n / NR)) {
-                msg = __shfl_sync(kAll, msgs[n % NR], 0);
-                if (lead) mbar_arrive(BAR(B_MSGFREE + n % NR));
-                ++n;
-                if ((msg & 255) == kEnd) msg = 0;
-                did = true;
-            }
-            if ((msg & 255) == kTile && sJ - vJ < 2) {
+            if (!fin && sJ - vJ < 2) {
                 const uint32_t st = sJ & 1u;
                 if (done(B_KV + st, sJ >> 1) && (sJ < 2 || done(B_SFREE + st, (sJ >> 1) - 1))) {
-                    tc_fence_after();
-                    if (lead) {
-                        if (st == 0) issue_s<0, I_S>(base, tmem);
-                        else issue_s<1, I_S>(base, tmem);
-                        mma_commit(BAR(B_S + st));
-                    }
-                    __syncwarp();
-                    firsts = (firsts & ~(1u << st)) | (((uint32_t)(msg >> 8) & 1u) << st);
-                    msg = 0;
-                    ++sJ;
+                    const int msg = __shfl_sync(kAll, meta[st], 0);
                     did = true;
+                    if ((msg & 255) == kFin) {
+                        fin = true;
+                    } else {
+                        tc_fence_after();
+                        if (lead) {
+                            if (st == 0) issue_s<0, I_S>(base, tmem);
+                            else issue_s<1, I_S>(base, tmem);
+                            mma_commit(BAR(B_S + st));
+                        }
+                        __syncwarp();
+                        firsts = (firsts & ~(1u << st)) | ((msg & kFirst ? 1u : 0u) << st);
+                        ++sJ;
+                    }
                 }
             }
             if (vJ < sJ && done(B_P, vJ)) {
                 const uint32_t st = vJ & 1u;
                 tc_fence_after();
+                const uint32_t keep = (firsts >> st) & 1u ? 0u : 1u;
                 if (lead) {
-                    const uint32_t keep = (firsts >> st) & 1u ? 0u : 1u;
-                    if (st == 0) issue_pv<0, I_HI, I_LO>(base, tmem, keep);
-                    else issue_pv<1, I_HI, I_LO>(base, tmem, keep);
-                    mma_commit(BAR(B_PV + st));
+                    if (st == 0) issue_pv<0, I_HI, I_LO>(base, tmem, keep, BAR(B_PV));
+                    else issue_pv<1, I_HI, I_LO>(base, tmem, keep, BAR(B_PV + 4));
                 }
                 __syncwarp();
                 ++vJ;
                 did = true;
             }
-            if ((msg & 255) == kFin && vJ == sJ) break;
             if (did) {
                 idle = 0;
                 since = 0;
@@ -633,8 +639,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             }
             // nothing to issue: sleep on the likelier of the two for up to 100 ns
             if (vJ < sJ) try_hint<100>(BAR(B_P), vJ & 1u);
-            else if (msg) try_hint<100>(BAR(B_KV + (sJ & 1u)), (sJ >> 1) & 1u);
-            else try_hint<100>(BAR(B_MSG + n % NR), (n / NR) & 1u);
+            else try_hint<100>(BAR(B_KV + (sJ & 1u)), (sJ >> 1) & 1u);
             if ((++idle & 63u) == 0u) {
                 if (__any_sync(kAll, *abort_flag != 0)) break;
                 const uint64_t now = globaltimer_ns();
@@ -662,41 +667,155 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
         float l[HPW];
         float m = 0.0f;        // of head hl
         int E = 0;
-        int64_t unit = T > 0 ? e0 / T : 0;
-        const int64_t unit0 = unit;
-        uint32_t J = 0, seg = 0;
-        bool any = false;      // the unit has a tile
+        int unit = (int)(e0 / T);
+        uint32_t seg = 0;
         bool bad = false;
-        for (uint32_t n = 0;; ++n) {
-            int msg = 0;
-            bad = bad || *abort_flag || !read_msg(n, msg);
-            const int kind = msg & 255;
+        for (uint32_t J = 0;; ++J) {
+            const uint32_t st = J & 1u;
+            bad = bad || *abort_flag || !warp_wait(BAR(B_KV + st), (J >> 1) & 1u, abort_flag);
+            const int msg = bad ? 0 : meta[st];
+            if ((msg & 255) == kFin) {
+                if (bar_or(false)) bar_or(true);   // a warp that gave up meets the others here
+                break;
+            }
+            // ---- a tile
+            const int count = msg >> 16;
+            const bool first = msg & kFirst;
+            const bool live = row < count;
+            float *maxima = reinterpret_cast<float *>(ctl + C_MAX);
+            int *emax = reinterpret_cast<int *>(ctl + C_EMAX);
+            float v[HPW];          // scores in octaves, less m
+            int e = 0;
+            bool late = true;      // m or E has to move
+            if (!bad) bad = !warp_wait(BAR(B_S + st), (J >> 1) & 1u, abort_flag);
             if (!bad) {
-                free_msg(n);
-                if (kind == kFin) {
-                    bar_or(false);   // a warp that gave up meets the others here
-                    break;
+                if (first) {
+                    ++seg;
+                    m = 0.0f;
+                }
+                tc_fence_after();
+                uint32_t r0[HPW], r1[HPW];
+                tmem_ld16(tm + TM_S + st * 2 * HM + hb, r0);
+                tmem_ld16(tm + TM_S + st * 2 * HM + HM + hb, r1);
+                e = (int)reinterpret_cast<const int8_t *>(ctl + C_REXP)[st * BN + row];
+                const float cr = pow2(e - 12);
+                const float *q = qs + ((seg - 1) & 1u) * HM + hb;
+                tmem_wait16(r0);
+                tmem_wait16(r1);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(B_SFREE + st));
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < HPW; i += 4) {
+                    const float4 q4 = lds4(q + i), m4 = lds4(head + hb + i);
+                    const float qv[4] = {q4.x, q4.y, q4.z, q4.w}, mv[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float s = fmaf(__uint_as_float(r1[i + k]), 0.03125f, __uint_as_float(r0[i + k])) * cr;
+                        v[i + k] = first ? s * qv[k] : fmaf(s, qv[k], -mv[k]);
+                    }
+                }
+                if (!live) {       // a row beyond the tile's count
+#pragma unroll
+                    for (int i = 0; i < HPW; ++i) v[i] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < HPW; ++i) top = fmaxf(top, v[i]);
+                late = first || top > kSlack || (live && e > E);
+            }
+            if (bar_or(late)) {
+                // the tile's maxima, and the heads' m and E behind them: always at a unit's first tile, seldom later
+#pragma unroll
+                for (int i = 0; i < HPW; ++i) {
+                    const float mx = warp_max(v[i]);
+                    if (lane == 0) maxima[quarter * HM + hb + i] = mx;
+                }
+                const int te = __reduce_max_sync(kAll, live ? e : -128);
+                if (lane == 0 && hb == 0) emax[quarter] = te;
+                if (bar_or(bad)) break;
+                const float t = fmaxf(fmaxf(maxima[hl], maxima[HM + hl]), fmaxf(maxima[2 * HM + hl], maxima[3 * HM + hl]));
+                const int4 e4 = *reinterpret_cast<const int4 *>(emax);
+                const int tile_e = max(max(e4.x, e4.y), max(e4.z, e4.w));
+                const int E0 = E;
+                E = first ? tile_e : max(E, tile_e);
+                // up to the tile's maximum; no change when that is lower, or there is no row (-inf)
+                const float up = first ? (t == -INFINITY ? 0.0f : t) : fmaxf(t, 0.0f);
+                m += up;
+                __syncwarp();
+                if (lane < HPW) head[hl] = m;          // the same from every quarter
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < HPW; ++i) v[i] -= __shfl_sync(kAll, up, i);
+                if (first) {
+#pragma unroll
+                    for (int i = 0; i < HPW; ++i) l[i] = 0.0f;
+                } else {
+                    // this warp's part of O^T, and its sums, follow m and E
+                    const float f = ex2(-up), down = pow2(E0 - E);
+                    bad = !warp_wait(BAR(B_PV + 4 * (st ^ 1u) + 3), ((J - 1) >> 1) & 1u, abort_flag);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < NPAN && !bad; ++c) {
+                        uint32_t r[HPW];
+                        tmem_ld16(tm + TM_O + c * HM + hb, r);
+                        tmem_wait16(r);
+#pragma unroll
+                        for (int i = 0; i < HPW; ++i)
+                            r[i] = __float_as_uint(__uint_as_float(r[i]) * (__shfl_sync(kAll, f, i) * down));
+                        tmem_st16(tm + TM_O + c * HM + hb, r);
+                    }
+                    tmem_st_wait();
+#pragma unroll
+                    for (int i = 0; i < HPW; ++i) l[i] *= __shfl_sync(kAll, f, i);
                 }
             }
-            if (!bad && kind == kEnd) {
+            uint32_t hi[4], lo[4];
+            {
+                const float fr = live ? pow2(e - E + 4) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < HPW; i += 4) {
+                    float pr[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        pr[k] = ex2(v[i + k]);
+                        l[i + k] += pr[k];
+                        pr[k] *= fr;
+                    }
+                    uint32_t h0, h1, l0, l1;
+                    split_p(pr[0], pr[1], h0, l0);
+                    split_p(pr[2], pr[3], h1, l1);
+                    hi[i >> 2] = prmt(h0, h1, 0x5410);
+                    lo[i >> 2] = prmt(l0, l1, 0x5410);
+                }
+            }
+            // P is free once the tile before has been multiplied
+            if (J > 0 && !bad) bad = !warp_wait(BAR(B_PV + 4 * (st ^ 1u) + 3), ((J - 1) >> 1) & 1u, abort_flag);
+            const uint32_t pb = base + SM_P + (uint32_t)row * 128;
+            st_shared_v4(pb + (uint32_t)((((hb >> 4) + 0) ^ (row & 7)) * 16), hi[0], hi[1], hi[2], hi[3]);
+            st_shared_v4(pb + (uint32_t)((((hb >> 4) + 4) ^ (row & 7)) * 16), lo[0], lo[1], lo[2], lo[3]);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(B_P));
+            if (msg & kLast) {
                 // ---- the unit's output, or this range's part of it
                 const Unit un = unit_of(p, unit);
-                const bool whole = unit * T >= e0 && (unit + 1) * T <= e1;
-                if (any) {
-                    // sums over the warp's rows: lanes i and i + 16 end up with head hb + i
-                    fold<8>(l, lane);
-                    fold<4>(l, lane);
-                    fold<2>(l, lane);
-                    fold<1>(l, lane);
-                    l[0] += __shfl_xor_sync(kAll, l[0], 16);
-                    if (lane < HPW) sums[quarter * HM + hl] = l[0];
-                    bad = !warp_wait(BAR(B_PV + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag);
-                    tc_fence_after();
-                }
+                const bool whole = msg & kWhole;
+                // sums over the warp's rows: lanes i and i + 16 end up with head hb + i
+                fold<8>(l, lane);
+                fold<4>(l, lane);
+                fold<2>(l, lane);
+                fold<1>(l, lane);
+                l[0] += __shfl_xor_sync(kAll, l[0], 16);
+                if (lane < HPW) sums[quarter * HM + hl] = l[0];
+                bad = bad || !warp_wait(BAR(B_PV + 4 * st + 3), (J >> 1) & 1u, abort_flag);
+                tc_fence_after();
                 if (bar_or(bad)) break;
-                float *ws = p.ws + ((size_t)cid * 2 + (unit == unit0 ? 0 : 1)) * SLOT;
-                const float sum = any ? sums[hl] + sums[HM + hl] + sums[2 * HM + hl] + sums[3 * HM + hl] : 0.0f;
-                const float unfold = pow2(E - 17);
+                float *ws = p.ws + ((size_t)cid * 2 + (msg & kSlot0 ? 0 : 1)) * SLOT;
+                const float sum = sums[hl] + sums[HM + hl] + sums[2 * HM + hl] + sums[3 * HM + hl];
+                const bool any = sum != 0.0f;              // false: no rows (NaN counts)
+                const float unfold = pow2(E - 16);
                 float f = unfold;                          // of head hl
                 if (whole) {
                     const float sink = hl < un.nh ? __ldg(p.a.sink + un.h0 + hl) * kLog2e : 0.0f;
@@ -711,7 +830,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 const float2 *cs = nullptr;
                 if constexpr (ROPE)
                     if (whole) cs = rotation_row(p.a, un.tok, threadIdx.x == 0);
-                if (hb < un.nh && (whole || any)) {
+                if (hb < un.nh) {
 #pragma unroll 1
                     for (int c = 0; c < NPAN; ++c) {
                         const int d = c * 128 + row;
@@ -724,7 +843,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                             const float4 f4 = lds4(head + hb + i);
                             const float fv[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) x[i + k] = any ? __uint_as_float(r[i + k]) * fv[k] : 0.0f;
+                            for (int k = 0; k < 4; ++k) x[i + k] = __uint_as_float(r[i + k]) * fv[k];
                         }
                         if (whole) {
                             if (ROPE && cs && c * 128 + quarter * 32 + 31 >= D - p.a.rd) {
@@ -755,122 +874,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     }
                 }
                 tc_fence_before();
-                any = false;
                 ++unit;
-                continue;
             }
-            // ---- a tile
-            const int count = msg >> 16;
-            const bool first = (msg >> 8) & 1;
-            const uint32_t st = J & 1u;
-            const bool live = row < count;
-            float *maxima = reinterpret_cast<float *>(ctl + C_MAX) + st * 4 * HM;
-            int *emax = reinterpret_cast<int *>(ctl + C_EMAX) + st * 4;
-            float v[HPW];
-            int e = 0;
-            if (!bad)
-                bad = !warp_wait(BAR(B_KV + st), (J >> 1) & 1u, abort_flag) ||
-                      !warp_wait(BAR(B_S + st), (J >> 1) & 1u, abort_flag);
-            if (!bad) {
-                if (first) ++seg;
-                tc_fence_after();
-                uint32_t r0[HPW], r1[HPW];
-                tmem_ld16(tm + TM_S + st * 2 * HM + hb, r0);
-                tmem_ld16(tm + TM_S + st * 2 * HM + HM + hb, r1);
-                e = (int)reinterpret_cast<const int8_t *>(ctl + C_REXP)[st * BN + row];
-                // a row beyond the tile's count scores -inf
-                const float cr = live ? pow2(e - 13) : 0.0f, off = live ? 0.0f : -INFINITY;
-                const float *q = qs + ((seg - 1) & 1u) * HM + hb;
-                tmem_wait16(r0);
-                tmem_wait16(r1);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(B_SFREE + st));
-#pragma unroll
-                for (int i = 0; i < HPW; i += 4) {
-                    const float4 q4 = lds4(q + i);
-                    const float qv[4] = {q4.x, q4.y, q4.z, q4.w};
-                    float mx[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float s = fmaf(__uint_as_float(r1[i + k]), 0.03125f, __uint_as_float(r0[i + k]));
-                        v[i + k] = fmaf(s * qv[k], cr, off);
-                        mx[k] = warp_max(v[i + k]);
-                    }
-                    if (lane == 0)
-                        *reinterpret_cast<float4 *>(maxima + quarter * HM + hb + i) = make_float4(mx[0], mx[1], mx[2], mx[3]);
-                }
-                const int te = __reduce_max_sync(kAll, live ? e : -128);
-                if (lane == 0 && hb == 0) emax[quarter] = te;
-            }
-            if (bar_or(bad)) break;
-            {
-                const float t = fmaxf(fmaxf(maxima[hl], maxima[HM + hl]), fmaxf(maxima[2 * HM + hl], maxima[3 * HM + hl]));
-                const int4 e4 = *reinterpret_cast<const int4 *>(emax);
-                const int tile_e = max(max(e4.x, e4.y), max(e4.z, e4.w));
-                const float m0 = m;
-                const int E0 = E;
-                const bool raise = !first && t > m + kSlack;
-                if (first || raise) m = t;
-                E = first ? tile_e : max(E, tile_e);
-                __syncwarp();
-                if (lane < HPW) head[hl] = m;          // the same from every quarter
-                __syncwarp();
-                if (first) {
-#pragma unroll
-                    for (int i = 0; i < HPW; ++i) l[i] = 0.0f;
-                } else if (__any_sync(kAll, raise) || E > E0) {
-                    // this warp's part of O^T, and its sums, follow m and E
-                    const float f = raise ? exp2f(m0 - m) : 1.0f, down = pow2(E0 - E);
-                    bad = !warp_wait(BAR(B_PV + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag);
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < NPAN && !bad; ++c) {
-                        uint32_t r[HPW];
-                        tmem_ld16(tm + TM_O + c * HM + hb, r);
-                        tmem_wait16(r);
-#pragma unroll
-                        for (int i = 0; i < HPW; ++i)
-                            r[i] = __float_as_uint(__uint_as_float(r[i]) * (__shfl_sync(kAll, f, i) * down));
-                        tmem_st16(tm + TM_O + c * HM + hb, r);
-                    }
-                    tmem_st_wait();
-#pragma unroll
-                    for (int i = 0; i < HPW; ++i) l[i] *= __shfl_sync(kAll, f, i);
-                }
-            }
-            any = true;
-            uint32_t hi[4], lo[4];
-            {
-                const float fr = live ? pow2(e - E + 4) : 0.0f;
-#pragma unroll
-                for (int i = 0; i < HPW; i += 4) {
-                    const float4 m4 = lds4(head + hb + i);
-                    const float mv[4] = {m4.x, m4.y, m4.z, m4.w};
-                    float pr[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        pr[k] = ex2(v[i + k] - mv[k]);
-                        l[i + k] += pr[k];
-                        pr[k] *= fr;
-                    }
-                    uint32_t h0, h1, l0, l1;
-                    split_p(pr[0], pr[1], h0, l0);
-                    split_p(pr[2], pr[3], h1, l1);
-                    hi[i >> 2] = prmt(h0, h1, 0x5410);
-                    lo[i >> 2] = prmt(l0, l1, 0x5410);
-                }
-            }
-            // P is free once the tile before has been multiplied
-            if (J > 0 && !bad) bad = !warp_wait(BAR(B_PV + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag);
-            const uint32_t pb = base + SM_P + (uint32_t)row * 128;
-            st_shared_v4(pb + (uint32_t)((((hb >> 4) + 0) ^ (row & 7)) * 16), hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(pb + (uint32_t)((((hb >> 4) + 4) ^ (row & 7)) * 16), lo[0], lo[1], lo[2], lo[3]);
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(B_P));
-            ++J;
         }
     }
 
