@@ -25,9 +25,9 @@
 // N = 128 in S and K = 32 a step a tile takes 16 + 32 instructions where bf16 rows would take 64 + 64.  The
 // widening to e5m2 is a table of 8 bytes per block: byte permutes with the code words as selectors.
 //
-// Warps: 0-15 softmax and epilogue (warp w: TMEM lanes 32 (w % 4).., heads 16 (w / 4)..), 16-23 rows (codes
-// loaded a tile ahead into registers, widened into the swizzled stage; q at a unit's first tile), 24 MMA
-// issue, 25 index rows: it drops entries without a row, turns the others into row numbers and hands tiles of
+// Warps: 0-7 softmax and epilogue (warp w: TMEM lanes 32 (w % 4).., heads 32 (w / 4)..), 8-15 rows (codes
+// loaded a tile ahead into registers, widened into the swizzled stage; q at a unit's first tile), 16 MMA
+// issue, 17 index rows: it drops entries without a row, turns the others into row numbers and hands tiles of
 // up to 128 to the row warps (a unit without rows gives one tile of none).  What a tile is (its rows, whether
 // it is its unit's first or last) goes on with the stage.
 // A unit is one token and up to 64 heads; units are shared out as in the other attention kernels
@@ -47,7 +47,6 @@ namespace fp4 {
 using namespace ptx;
 using split::kMaxCut;
 using split::range_start;
-using split::unit_at;
 
 constexpr int D = 512;
 constexpr int HM = 64;                  // heads of a unit
@@ -56,6 +55,12 @@ constexpr int NPAN = D / 128;           // panels of 128 columns
 constexpr int PANEL = BN * 128;         // bytes of a panel: 128 rows (of C or of [hi | lo]) of 128
 constexpr int STAGE = NPAN * PANEL;     // 64 KB
 constexpr int NR = 4;                   // index messages
+constexpr int NSOFTW = 8, NSOFT = 32 * NSOFTW, HPW = 32;    // softmax warps; heads of one
+constexpr int W_ROWS = NSOFTW, NROWW = 8, W_MMA = W_ROWS + NROWW, W_IDX = W_MMA + 1, NTHREADS = 640;   // 18, 19: none
+constexpr int RPL = BN / (2 * NROWW);                // steps of two rows that a row warp takes a tile
+// of the 96 registers a thread of the launch the softmax warps take more
+constexpr uint32_t REG_SOFT = 112, REG_OTHER = 80;
+static_assert(NSOFT * REG_SOFT + (NTHREADS - NSOFT) * REG_OTHER <= NTHREADS * 96, "register split");
 constexpr int SM_Q = 0;
 constexpr int SM_KV = SM_Q + STAGE;
 constexpr int SM_P = SM_KV + 2 * STAGE;
@@ -68,8 +73,9 @@ constexpr int C_REXP = C_EXPS + BN * (D / 32);  // [2][128] int8 e_r
 constexpr int C_MAX = C_REXP + 2 * BN;          // [4][64] f32 maxima of the quarters
 constexpr int C_EMAX = C_MAX + 4 * HM * 4;      // [4] int32 largest e_r of the quarters
 constexpr int C_SUM = C_EMAX + 16;              // [4][64] f32 sums of the quarters, at a unit's end
-constexpr int C_HEAD = C_SUM + 4 * HM * 4;      // [64] f32 running maximum; at a unit's end the output's factor
-constexpr int C_QS = C_HEAD + HM * 4;           // [2][64] f32 2^g scale log2(e), by unit parity
+constexpr int C_HEAD = C_SUM + 4 * HM * 4;      // [64] f32 running maximum m, 0 at a unit's start
+constexpr int C_FAC = C_HEAD + HM * 4;          // [64] f32 factor of O^T: at m's rise, and at a unit's end
+constexpr int C_QS = C_FAC + HM * 4;           // [2][64] f32 2^g scale log2(e), by unit parity
 constexpr int C_BAR = C_QS + 2 * HM * 4;
 enum : int {
     B_MSG = 0,                  // [NR] index -> rows: message written
@@ -92,9 +98,6 @@ static_assert(C_BAR % 8 == 0 && SMEM_BYTES <= 232448, "shared memory budget");
 constexpr int TM_O = 0, TM_S = NPAN * HM, TMEM_COLS = 512;
 static_assert(TM_S + 2 * 2 * HM <= TMEM_COLS, "TMEM budget");
 
-constexpr int NSOFTW = 16, NSOFT = 32 * NSOFTW, HPW = 16;   // softmax warps; heads of one
-constexpr int W_ROWS = NSOFTW, NROWW = 8, W_MMA = W_ROWS + NROWW, W_IDX = W_MMA + 1, NTHREADS = 32 * (W_IDX + 1);
-constexpr int RPL = BN / (2 * NROWW);                // steps of two rows that a row warp takes a tile
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 4.0f;          // octaves that m may be late
@@ -110,7 +113,7 @@ constexpr size_t SLOT = (size_t)SLOT_O + 2 * HM;
 
 struct Params {
     Args a;
-    int64_t ntok, nunit;
+    int ntok, nunit;
     int groups;       // units of a token
     int G;
     int seg_cost;
@@ -133,6 +136,14 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// One lane of a converged warp.  Behind it (and not behind lane == 0) the compiler keeps what is the same for the
+// warp in uniform registers, where the MMA's operands have to be: 5 instructions an MMA instead of 15.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+    return r != 0;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -170,16 +181,14 @@ __device__ __forceinline__ bool try_hint(uint32_t bar, uint32_t parity) {
 
 // Bounded wait of a whole warp; false when it gave up, or another role did.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    bool ok = try_hint<20000>(bar, parity);
-    if (!__all_sync(kAll, ok)) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!ok && !*abort) {
-            ok = try_hint<20000>(bar, parity);
-            if (!ok && globaltimer_ns() - t0 > kWaitLimitNs) *abort = 1;
-        }
-        ok = __all_sync(kAll, ok);
+    uint64_t t0 = 0;
+    while (!__all_sync(kAll, try_hint<20000>(bar, parity))) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) *abort = 1;
+        if (__any_sync(kAll, *abort != 0)) return false;
     }
-    return ok;
+    return true;
 }
 
 // 2^k, 0 below the normal numbers
@@ -282,7 +291,7 @@ __device__ __forceinline__ void split_p(float p0, float p1, uint32_t &hi, uint32
         : "f"(p0), "f"(p1));
 }
 
-// One step of summing 16 values over a warp: lanes O apart share the first 2 O of them out.
+// One step of summing 32 values over a warp: lanes O apart share the first 2 O of them out.
 template <int O>
 __device__ __forceinline__ void fold(float (&l)[HPW], int lane) {
     const bool up = (lane & O) != 0;
@@ -316,20 +325,24 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
     for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// Token of a position in the token order (split::unit_at; the launch keeps the numbers below 2^31).
+__device__ __forceinline__ int token_at(uint32_t i, int ntok, bool interleave) {
+    return interleave ? (i & 1u ? ntok - 1 - (int)(i >> 1) : (int)(i >> 1)) : (int)i;
+}
+
 // Unit of a position in the unit order: groups of a token are neighbours, so that their gathers meet in L2.
 struct Unit {
-    int64_t tok;
-    int h0, nh;
+    int tok, h0, nh;
 };
-__device__ __forceinline__ Unit unit_of(const Params &p, int64_t u) {
-    const int64_t t = p.groups == 1 ? u : u >> 1;
-    const int g = p.groups == 1 ? 0 : (int)(u & 1);
-    return {unit_at(t, p.ntok, p.interleave), g * HM, min(HM, p.a.h - g * HM)};
+__device__ __forceinline__ Unit unit_of(const Params &p, uint32_t u) {
+    const int g = p.groups == 1 ? 0 : (int)(u & 1u);
+    return {token_at(p.groups == 1 ? u : u >> 1, p.ntok, p.interleave), g * HM, min(HM, p.a.h - g * HM)};
 }
 
 // sin and cos of the output's rotation back, or null
-__device__ __forceinline__ const float2 *rotation_row(const Args &a, int64_t tok, bool flag) {
-    const int64_t pos = (int64_t)__ldg(a.first + tok / a.m) + tok % a.m;
+__device__ __forceinline__ const float2 *rotation_row(const Args &a, int tok, bool flag) {
+    const uint32_t bi = (uint32_t)tok / (uint32_t)a.m;
+    const int64_t pos = (int64_t)__ldg(a.first + bi) + (tok - (int)bi * a.m);
     if (pos < 0 || pos >= a.table_rows) {
         if (flag) flag_status(a.status, DS_DEV_BAD_INDEX);
         return nullptr;
@@ -338,30 +351,29 @@ __device__ __forceinline__ const float2 *rotation_row(const Args &a, int64_t tok
 }
 
 // S^T of a tile: rows of the stage by [hi | lo], 32 columns (bytes) a step.
-template <int ST, uint32_t IDESC>
-__device__ __forceinline__ void issue_s(uint32_t base, uint32_t tmem) {
-    const uint64_t a = smem_desc_sw128(base + SM_KV + ST * STAGE, 16, 1024), b = smem_desc_sw128(base + SM_Q, 16, 1024);
+template <uint32_t IDESC>
+__device__ __forceinline__ void issue_s(uint32_t rows, uint32_t q, uint32_t d) {
+    const uint64_t a = smem_desc_sw128(rows, 16, 1024), b = smem_desc_sw128(q, 16, 1024);
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) {
         const uint64_t off = (uint64_t)(((k >> 2) * PANEL + (k & 3) * 32) >> 4);
-        mma_f8(tmem + TM_S + ST * 2 * HM, a + off, b + off, IDESC, k ? 1u : 0u);
+        mma_f8(d, a + off, b + off, IDESC, k ? 1u : 0u);
     }
 }
 
 // O^T += C^T P: panel c's 128 columns as M (one 128-byte atom), 32 rows a step (four groups of eight, 1024
 // bytes apart); P the same with its 64 heads as N, hi then lo.  Rows outermost: each step's rows are handed
 // back (bar) as soon as its four panels are multiplied.
-template <int ST, uint32_t I_HI, uint32_t I_LO>
-__device__ __forceinline__ void issue_pv(uint32_t base, uint32_t tmem, uint32_t keep, uint32_t bar) {
-    const uint64_t a = smem_desc_sw128(base + SM_KV + ST * STAGE, PANEL, 1024);
-    const uint64_t b = smem_desc_sw128(base + SM_P, P_BYTES, 1024);
+template <uint32_t I_HI, uint32_t I_LO>
+__device__ __forceinline__ void issue_pv(uint32_t rows, uint32_t pr, uint32_t d, uint32_t keep, uint32_t bar) {
+    const uint64_t a = smem_desc_sw128(rows, PANEL, 1024), b = smem_desc_sw128(pr, P_BYTES, 1024);
 #pragma unroll
     for (int k = 0; k < BN / 32; ++k) {
 #pragma unroll
         for (int c = 0; c < NPAN; ++c) {
             const uint64_t ao = a + (uint64_t)((c * PANEL + k * 4096) >> 4), bo = b + (uint64_t)((k * 4096) >> 4);
-            mma_f8(tmem + TM_O + c * HM, ao, bo, I_HI, k ? 1u : keep);
-            mma_f8(tmem + TM_O + c * HM, ao, bo + (64 >> 4), I_LO, 1u);
+            mma_f8(d + c * HM, ao, bo, I_HI, k ? 1u : keep);
+            mma_f8(d + c * HM, ao, bo + (64 >> 4), I_LO, 1u);
         }
         mma_commit(bar + 8 * k);
     }
@@ -374,11 +386,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
     uint8_t *ctl = smem + SM_CTL;
     auto BAR = [&](int i) -> uint32_t { return base + SM_CTL + C_BAR + 8u * (uint32_t)i; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(ctl + C_ABORT);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int T = p.a.topk;
     const int64_t cid = blockIdx.x;
     const int64_t e0 = range_start(cid, p.nunit, T, p.seg_cost, p.G);
     const int64_t e1 = range_start(cid + 1, p.nunit, T, p.seg_cost, p.G);
+    const uint32_t u0 = (uint32_t)(e0 / T);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NR; ++i) {
@@ -403,11 +416,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
     }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl + C_TMEM);
+    const uint32_t tmem = __shfl_sync(kAll, *reinterpret_cast<volatile uint32_t *>(ctl + C_TMEM), 0);
     grid_dependency_wait();
     volatile int *msgs = reinterpret_cast<volatile int *>(ctl + C_MSG);
 
     volatile int *meta = reinterpret_cast<volatile int *>(ctl + C_META);
+    if (warp >= W_ROWS) setmaxnreg_dec<REG_OTHER>();
 
     if (warp == W_IDX) {
         // ================================ index rows to tiles of row numbers ================================
@@ -422,14 +436,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             ++n;
         };
         bool ok = true, flagged = false;
-        const int64_t u0 = e0 / T;
-        for (int64_t u = u0; ok && u * T < e1; ++u) {
+        for (uint32_t u = u0; ok && (int64_t)u * T < e1; ++u) {
             const Unit un = unit_of(p, u);
-            const int64_t bi = un.tok / p.a.m;
-            const int32_t *idx = p.a.idx + un.tok * T;
-            const int32_t *bt = p.a.block_table + bi * p.a.max_pages;
-            const int a = (int)((e0 > u * T ? e0 : u * T) - u * T);
-            const int z = (int)((e1 < (u + 1) * T ? e1 : (u + 1) * T) - u * T);
+            const int32_t *idx = p.a.idx + (int64_t)un.tok * T;
+            const int32_t *bt = p.a.block_table + (int64_t)((uint32_t)un.tok / (uint32_t)p.a.m) * p.a.max_pages;
+            const int a = u == u0 ? (int)(e0 - (int64_t)u * T) : 0;
+            const int z = (int)min((int64_t)T, e1 - (int64_t)u * T);
             const int tile = kTile | (a == 0 && z == T ? kWhole : 0) | (u == u0 ? kSlot0 : 0);
             int fill = 0, first = kFirst;
             int nxt[4];
@@ -494,89 +506,98 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             at[i] = base + SM_KV + (uint32_t)panel * PANEL + (uint32_t)(4 * w + 2 * i + half) * 128 +
                     (uint32_t)(((lane & 3) * 2 ^ (4 * (w & 1) + 2 * i + half)) * 16);
         const uint32_t sign = p.scale_log2 < 0.0f ? 0x80000000u : 0u;
-        int unit = (int)(e0 / T);
+        uint8_t *mine = ctl + C_EXPS + w * 16 * (D / 32);
+        uint32_t unit = u0;
+        int msg = 0, row = -1;                               // row: number of row mytile of the tile in hand, or -1
         uint32_t seg = 0;
-        for (uint32_t J = 0;; ++J) {
-            if (!warp_wait(BAR(B_MSG + J % NR), (J / NR) & 1u, abort_flag)) break;
-            const int msg = msgs[J % NR], count = msg >> 16;
-            const bool first = msg & kFirst;
+        uint4 raw[RPL], ev;                                  // its codes and exponents, 16 bytes a lane and step
+        // message n: what it says, and this lane's row
+        auto next_msg = [&](uint32_t n) -> bool {
+            if (!warp_wait(BAR(B_MSG + n % NR), (n / NR) & 1u, abort_flag)) return false;
+            msg = msgs[n % NR];
+            row = (msg & 255) == kTile && mytile < msg >> 16
+                      ? reinterpret_cast<const int32_t *>(ctl + C_ROWS)[(n % NR) * BN + mytile]
+                      : -1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(B_MSGFREE + n % NR));
+            return true;
+        };
+        // where there is no row: q, which is there, and counts as zeros below
+        auto load = [&](int i) {
+            const int r = __shfl_sync(kAll, row, 2 * i + half);
+            raw[i] = ld_row(r >= 0 ? p.a.codes + (int64_t)r * (D / 2) + u * 16 : reinterpret_cast<const uint8_t *>(p.a.q));
+        };
+        auto load_exps = [&]() {
+            ev = ld_row(row >= 0 ? (const void *)(p.a.exps + (int64_t)row * (D / 32)) : (const void *)p.a.q);
+        };
+        bool ok = next_msg(0);
+        if (ok) {
+            load_exps();
+#pragma unroll
+            for (int i = 0; i < RPL; ++i) load(i);
+        }
+        for (uint32_t J = 0; ok; ++J) {
+            const int tile = msg;
             const uint32_t st = J & 1u;
-            if ((msg & 255) == kFin) {
+            if ((tile & 255) == kFin) {
                 if (J >= 2 && !warp_wait(BAR(B_PV + 4 * st + 3), ((J >> 1) - 1) & 1u, abort_flag)) break;
-                if (warp == W_ROWS && lane == 0) meta[st] = msg;
+                if (warp == W_ROWS && lane == 0) meta[st] = tile;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(B_KV + st));
                 break;
             }
-            const int myrow =
-                mytile < count ? reinterpret_cast<const int32_t *>(ctl + C_ROWS)[(J % NR) * BN + mytile] : -1;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(B_MSGFREE + J % NR));
             float qs = 0.0f;                      // lane i < 8: the scale of head 8 w + i
-            if (first) {
+            if (tile & kFirst) {
                 // q of the unit, once S of the tile before has read the last one's
-                if (J > 0 && !warp_wait(BAR(B_S + ((J - 1) & 1u)), ((J - 1) >> 1) & 1u, abort_flag)) break;
+                if (J > 0 && !warp_wait(BAR(B_S + (st ^ 1u)), ((J - 1) >> 1) & 1u, abort_flag)) break;
                 const Unit un = unit_of(p, unit);
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.a.q + (un.tok * p.a.h + un.h0) * D) + 2 * lane;
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.a.q + ((int64_t)un.tok * p.a.h + un.h0) * D) + 2 * lane;
+                uint4 v[2], nx[2];
+                auto load_q = [&](int i) {
+                    nx[0] = nx[1] = make_uint4(0, 0, 0, 0);
+                    if (i < 8 && 8 * w + i < un.nh) {
+                        nx[0] = __ldg(src + (8 * w + i) * (D / 8));
+                        nx[1] = __ldg(src + (8 * w + i) * (D / 8) + 1);
+                    }
+                };
+                load_q(0);
 #pragma unroll 1
-                for (int i0 = 0; i0 < 8; i0 += 4) {
-                    uint4 v[4][2];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int hh = 8 * w + i0 + k;
-                        v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
-                        if (hh < un.nh) {
-                            v[k][0] = __ldg(src + hh * (D / 8));
-                            v[k][1] = __ldg(src + hh * (D / 8) + 1);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int g = put_q(base + SM_Q, 8 * w + i0 + k, v[k], lane, sign);
-                        if (lane == i0 + k) qs = fmaxf(fabsf(p.scale_log2) * pow2(g), 1.17549435e-38f);   // never 0: see the scores
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    v[0] = nx[0];
+                    v[1] = nx[1];
+                    load_q(i + 1);
+                    const int g = put_q(base + SM_Q, 8 * w + i, v, lane, sign);
+                    if (lane == i) qs = fmaxf(fabsf(p.scale_log2) * pow2(g), 1.17549435e-38f);   // never 0: see the scores
                 }
             }
-            // the tile's codes, 16 bytes (one block) a lane and row, in flight until the stage is free
-            // beyond the tile's count: the pool's first row (q, if there may be none), which counts as zeros below
-            uint4 raw[RPL], ev;
-            const uint8_t *pool = count > 0 ? p.a.codes : reinterpret_cast<const uint8_t *>(p.a.q);
-#pragma unroll
-            for (int i = 0; i < RPL; ++i)
-                raw[i] = ld_row(pool + (int64_t)max(__shfl_sync(kAll, myrow, 2 * i + half), 0) * (D / 2) + u * 16);
-            ev = ld_row(count > 0 ? (const void *)(p.a.exps + (int64_t)max(myrow, 0) * (D / 32)) : (const void *)p.a.q);
             // the row's largest exponent, and k - e_r + 27 of its 16 blocks, 0 where that is less (or there is no row)
             const uint32_t m4 = __vmaxs4(__vmaxs4(ev.x, ev.y), __vmaxs4(ev.z, ev.w));
             const int emax = max(max((int)(int8_t)m4, (int)(int8_t)(m4 >> 8)), max((int)(int8_t)(m4 >> 16), (int)m4 >> 24));
             const uint32_t low = (uint32_t)(uint8_t)max(emax - 27, -128) * 0x01010101u;
             const uint32_t lift = (uint32_t)(uint8_t)(max(emax - 27, -128) - (emax - 27)) * 0x01010101u;
-            const uint32_t on = myrow >= 0 ? kAll : 0u;
-            uint8_t *mine = ctl + C_EXPS + w * 16 * (D / 32);
+            const uint32_t on = row >= 0 ? kAll : 0u;
             __syncwarp();
             if (lane < 16)
                 reinterpret_cast<uint4 *>(mine)[lane] =
                     make_uint4(above(ev.x, low, lift) & on, above(ev.y, low, lift) & on, above(ev.z, low, lift) & on,
                                above(ev.w, low, lift) & on);
             __syncwarp();
-            uint32_t y[RPL];
-#pragma unroll
-            for (int i = 0; i < RPL; ++i) y[i] = mine[(2 * i + half) * (D / 32) + u];
-            bool ok = true;
+            if (!next_msg(J + 1)) break;
+            load_exps();
 #pragma unroll
             for (int i = 0; i < RPL; ++i) {
                 if (J >= 2 && (i & 1) == 0) ok = ok && warp_wait(BAR(B_PV + 4 * st + (i >> 1)), ((J >> 1) - 1) & 1u, abort_flag);
-                // the codes are first touched here, behind the wait
-                asm volatile("" : "+r"(raw[i].x), "+r"(raw[i].y), "+r"(raw[i].z), "+r"(raw[i].w));
                 uint32_t o[8];
-                widen(raw[i], y[i], o);
+                widen(raw[i], mine[(2 * i + half) * (D / 32) + u], o);
+                load(i);                          // of the next tile: in flight until its turn
                 const uint32_t to = at[i & 1] + st * STAGE + (uint32_t)(i >> 1) * 4096;
                 st_shared_v4(to, o[0], o[1], o[2], o[3]);
                 st_shared_v4(to ^ 16u, o[4], o[5], o[6], o[7]);
             }
             if (!ok) break;
-            if (warp == W_ROWS && lane == 0) meta[st] = msg;
-            if (msg & kLast) ++unit;
-            if (first) {
+            if (warp == W_ROWS && lane == 0) meta[st] = tile;
+            if (tile & kLast) ++unit;
+            if (tile & kFirst) {
                 // P V of tile J - 2 is done, so the softmax is through with the scales of two units ago
                 if (lane < 8) reinterpret_cast<float *>(ctl + C_QS)[(seg & 1u) * HM + 8 * w + lane] = qs;
                 ++seg;
@@ -588,88 +609,78 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
         }
     } else if (warp == W_MMA) {
         // ================================== MMA issue ==================================
-        // The whole warp walks the loop, one lane issues.
+        // The whole warp walks the loop (its conditions are votes), an elected lane issues.
         constexpr uint32_t I_S = idesc8(BN, 2 * HM, 1, 0, false);
         constexpr uint32_t I_HI = idesc8(128, HM, 1, 0, true), I_LO = idesc8(128, HM, 1, 1, true, true);
-        const bool lead = lane == 0;
         auto done = [&](int bar, uint32_t phase) -> bool { return __all_sync(kAll, mbar_test_wait(BAR(bar), phase & 1u)); };
         uint32_t sJ = 0, vJ = 0;           // next tile of S and of P V
         bool fin = false;                  // no more tiles
-        uint32_t firsts = 0;               // bit J & 1: tile J is its unit's first
+        uint32_t keep = 0;                 // bit J & 1: tile J adds to O^T (is not its unit's first)
         uint32_t idle = 0;
         uint64_t since = 0;
         while (!fin || vJ < sJ) {
-            bool did = false;
-            if (!fin && sJ - vJ < 2) {
-                const uint32_t st = sJ & 1u;
-                if (done(B_KV + st, sJ >> 1) && (sJ < 2 || done(B_SFREE + st, (sJ >> 1) - 1))) {
-                    const int msg = __shfl_sync(kAll, meta[st], 0);
-                    did = true;
-                    if ((msg & 255) == kFin) {
-                        fin = true;
-                    } else {
-                        tc_fence_after();
-                        if (lead) {
-                            if (st == 0) issue_s<0, I_S>(base, tmem);
-                            else issue_s<1, I_S>(base, tmem);
-                            mma_commit(BAR(B_S + st));
-                        }
-                        __syncwarp();
-                        firsts = (firsts & ~(1u << st)) | ((msg & kFirst ? 1u : 0u) << st);
-                        ++sJ;
-                    }
-                }
-            }
             if (vJ < sJ && done(B_P, vJ)) {
                 const uint32_t st = vJ & 1u;
                 tc_fence_after();
-                const uint32_t keep = (firsts >> st) & 1u ? 0u : 1u;
-                if (lead) {
-                    if (st == 0) issue_pv<0, I_HI, I_LO>(base, tmem, keep, BAR(B_PV));
-                    else issue_pv<1, I_HI, I_LO>(base, tmem, keep, BAR(B_PV + 4));
-                }
+                if (elect_one())
+                    issue_pv<I_HI, I_LO>(base + SM_KV + st * STAGE, base + SM_P, tmem + TM_O, (keep >> st) & 1u,
+                                         BAR(B_PV + 4 * st));
                 __syncwarp();
                 ++vJ;
-                did = true;
-            }
-            if (did) {
                 idle = 0;
-                since = 0;
-                continue;
-            }
-            // nothing to issue: sleep on the likelier of the two for up to 100 ns
-            if (vJ < sJ) try_hint<100>(BAR(B_P), vJ & 1u);
-            else try_hint<100>(BAR(B_KV + (sJ & 1u)), (sJ >> 1) & 1u);
-            if ((++idle & 63u) == 0u) {
-                if (__any_sync(kAll, *abort_flag != 0)) break;
-                const uint64_t now = globaltimer_ns();
-                if (since == 0) since = now;
-                else if (__any_sync(kAll, now - since > kWaitLimitNs)) {
-                    *abort_flag = 1;
-                    break;
+            } else if (!fin && sJ - vJ < 2 && done(B_KV + (sJ & 1u), sJ >> 1) &&
+                       (sJ < 2 || done(B_SFREE + (sJ & 1u), (sJ >> 1) - 1))) {
+                const uint32_t st = sJ & 1u;
+                const int msg = __shfl_sync(kAll, meta[st], 0);
+                idle = 0;
+                if ((msg & 255) == kFin) {
+                    fin = true;
+                    continue;
+                }
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_s<I_S>(base + SM_KV + st * STAGE, base + SM_Q, tmem + TM_S + st * 2 * HM);
+                    mma_commit(BAR(B_S + st));
+                }
+                __syncwarp();
+                keep = (keep & ~(1u << st)) | ((msg & kFirst ? 0u : 1u) << st);
+                ++sJ;
+            } else {
+                // nothing to issue: sleep on the likelier of the two for up to 100 ns
+                if (vJ < sJ) try_hint<100>(BAR(B_P), vJ & 1u);
+                else try_hint<100>(BAR(B_KV + (sJ & 1u)), (sJ >> 1) & 1u);
+                if ((++idle & 63u) == 0u) {
+                    const uint64_t now = globaltimer_ns();
+                    if (idle == 64u) since = now;
+                    else if (now - since > kWaitLimitNs) *abort_flag = 1;
+                    if (__any_sync(kAll, *abort_flag != 0)) break;
                 }
             }
         }
-        if (lead && *abort_flag) {   // let issued MMAs finish before TMEM is freed
-            mma_commit(BAR(B_DRAIN));
-            mbar_wait_drain(BAR(B_DRAIN), 0, 100000000ull);
+        if (__any_sync(kAll, *abort_flag != 0)) {   // let issued MMAs finish before TMEM is freed
+            if (elect_one()) {
+                mma_commit(BAR(B_DRAIN));
+                mbar_wait_drain(BAR(B_DRAIN), 0, 100000000ull);
+            }
         }
         __syncwarp();
-    } else {
+    } else if (warp < NSOFTW) {
         // ============================ softmax and epilogue ============================
+        setmaxnreg_inc<REG_SOFT>();
         // Warp (quarter, heads hb..): its 32 rows by its 16 heads of every tile, and in O^T its 32 lanes of every
         // panel by the same heads.  The four warps of the same heads agree on m and E without talking
         // about them: they read the same maxima.
-        const int quarter = warp & 3, hb = (warp >> 2) * HPW, row = quarter * 32 + lane, hl = hb + (lane & (HPW - 1));
+        const int quarter = warp & 3, hb = (warp >> 2) * HPW, row = quarter * 32 + lane, hl = hb + lane;
         const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16);
-        float *head = reinterpret_cast<float *>(ctl + C_HEAD), *sums = reinterpret_cast<float *>(ctl + C_SUM);
+        float *head = reinterpret_cast<float *>(ctl + C_HEAD), *fac = reinterpret_cast<float *>(ctl + C_FAC), *sums = reinterpret_cast<float *>(ctl + C_SUM);
         const float *qs = reinterpret_cast<const float *>(ctl + C_QS);
         float l[HPW];
         float m = 0.0f;        // of head hl
         int E = 0;
-        int unit = (int)(e0 / T);
-        uint32_t seg = 0;
+        uint32_t unit = u0, seg = 0;
         bool bad = false;
+        head[hl] = 0.0f;
+        __syncwarp();
         for (uint32_t J = 0;; ++J) {
             const uint32_t st = J & 1u;
             bad = bad || *abort_flag || !warp_wait(BAR(B_KV + st), (J >> 1) & 1u, abort_flag);
@@ -694,28 +705,31 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     m = 0.0f;
                 }
                 tc_fence_after();
-                uint32_t r0[HPW], r1[HPW];
-                tmem_ld16(tm + TM_S + st * 2 * HM + hb, r0);
-                tmem_ld16(tm + TM_S + st * 2 * HM + HM + hb, r1);
                 e = (int)reinterpret_cast<const int8_t *>(ctl + C_REXP)[st * BN + row];
                 const float cr = pow2(e - 12);
                 const float *q = qs + ((seg - 1) & 1u) * HM + hb;
-                tmem_wait16(r0);
-                tmem_wait16(r1);
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < HPW; j += 16) {
+                    uint32_t r0[16], r1[16];
+                    tmem_ld16(tm + TM_S + st * 2 * HM + hb + j, r0);
+                    tmem_ld16(tm + TM_S + st * 2 * HM + HM + hb + j, r1);
+                    tmem_wait16(r0);
+                    tmem_wait16(r1);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 q4 = lds4(q + j + i), m4 = lds4(head + hb + j + i);
+                        const float qv[4] = {q4.x, q4.y, q4.z, q4.w}, mv[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float s = fmaf(__uint_as_float(r1[i + k]), 0.03125f, __uint_as_float(r0[i + k])) * cr;
+                            v[j + i + k] = fmaf(s, qv[k], -mv[k]);
+                        }
+                    }
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(B_SFREE + st));
-                float top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < HPW; i += 4) {
-                    const float4 q4 = lds4(q + i), m4 = lds4(head + hb + i);
-                    const float qv[4] = {q4.x, q4.y, q4.z, q4.w}, mv[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float s = fmaf(__uint_as_float(r1[i + k]), 0.03125f, __uint_as_float(r0[i + k])) * cr;
-                        v[i + k] = first ? s * qv[k] : fmaf(s, qv[k], -mv[k]);
-                    }
-                }
                 if (!live) {       // a row beyond the tile's count
 #pragma unroll
                     for (int i = 0; i < HPW; ++i) v[i] = -INFINITY;
@@ -742,8 +756,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 // up to the tile's maximum; no change when that is lower, or there is no row (-inf)
                 const float up = first ? (t == -INFINITY ? 0.0f : t) : fmaxf(t, 0.0f);
                 m += up;
+                const float down = pow2(E0 - E);
                 __syncwarp();
-                if (lane < HPW) head[hl] = m;          // the same from every quarter
+                head[hl] = m;                          // the same from every quarter
+                fac[hl] = ex2(-up);
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < HPW; ++i) v[i] -= __shfl_sync(kAll, up, i);
@@ -752,25 +768,25 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     for (int i = 0; i < HPW; ++i) l[i] = 0.0f;
                 } else {
                     // this warp's part of O^T, and its sums, follow m and E
-                    const float f = ex2(-up), down = pow2(E0 - E);
                     bad = !warp_wait(BAR(B_PV + 4 * (st ^ 1u) + 3), ((J - 1) >> 1) & 1u, abort_flag);
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < NPAN && !bad; ++c) {
-                        uint32_t r[HPW];
-                        tmem_ld16(tm + TM_O + c * HM + hb, r);
+                    for (int c = 0; c < 2 * NPAN && !bad; ++c) {
+                        const uint32_t at = tm + TM_O + (c >> 1) * HM + hb + (c & 1) * 16;
+                        const float *f = fac + hb + (c & 1) * 16;
+                        uint32_t r[16];
+                        tmem_ld16(at, r);
                         tmem_wait16(r);
 #pragma unroll
-                        for (int i = 0; i < HPW; ++i)
-                            r[i] = __float_as_uint(__uint_as_float(r[i]) * (__shfl_sync(kAll, f, i) * down));
-                        tmem_st16(tm + TM_O + c * HM + hb, r);
+                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (f[i] * down));
+                        tmem_st16(at, r);
                     }
                     tmem_st_wait();
 #pragma unroll
-                    for (int i = 0; i < HPW; ++i) l[i] *= __shfl_sync(kAll, f, i);
+                    for (int i = 0; i < HPW; ++i) l[i] *= fac[hb + i];
                 }
             }
-            uint32_t hi[4], lo[4];
+            uint32_t hi[HPW / 4], lo[HPW / 4];
             {
                 const float fr = live ? pow2(e - E + 4) : 0.0f;
 #pragma unroll
@@ -792,8 +808,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             // P is free once the tile before has been multiplied
             if (J > 0 && !bad) bad = !warp_wait(BAR(B_PV + 4 * (st ^ 1u) + 3), ((J - 1) >> 1) & 1u, abort_flag);
             const uint32_t pb = base + SM_P + (uint32_t)row * 128;
-            st_shared_v4(pb + (uint32_t)((((hb >> 4) + 0) ^ (row & 7)) * 16), hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(pb + (uint32_t)((((hb >> 4) + 4) ^ (row & 7)) * 16), lo[0], lo[1], lo[2], lo[3]);
+            const uint32_t c0 = (uint32_t)((hb >> 4) ^ (row & 7)) * 16;     // its 16-byte column; hb / 16 is even
+            st_shared_v4(pb + c0, hi[0], hi[1], hi[2], hi[3]);
+            st_shared_v4(pb + (c0 ^ 16), hi[4], hi[5], hi[6], hi[7]);
+            st_shared_v4(pb + (c0 ^ 64), lo[0], lo[1], lo[2], lo[3]);
+            st_shared_v4(pb + (c0 ^ 80), lo[4], lo[5], lo[6], lo[7]);
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
@@ -802,13 +821,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 // ---- the unit's output, or this range's part of it
                 const Unit un = unit_of(p, unit);
                 const bool whole = msg & kWhole;
-                // sums over the warp's rows: lanes i and i + 16 end up with head hb + i
+                // sums over the warp's rows: lane i ends up with head hb + i
+                fold<16>(l, lane);
                 fold<8>(l, lane);
                 fold<4>(l, lane);
                 fold<2>(l, lane);
                 fold<1>(l, lane);
-                l[0] += __shfl_xor_sync(kAll, l[0], 16);
-                if (lane < HPW) sums[quarter * HM + hl] = l[0];
+                sums[quarter * HM + hl] = l[0];
                 bad = bad || !warp_wait(BAR(B_PV + 4 * st + 3), (J >> 1) & 1u, abort_flag);
                 tc_fence_after();
                 if (bar_or(bad)) break;
@@ -820,57 +839,53 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 if (whole) {
                     const float sink = hl < un.nh ? __ldg(p.a.sink + un.h0 + hl) * kLog2e : 0.0f;
                     f = any ? unfold / (sum + exp2f(sink - m)) : 0.0f;
-                } else if (quarter == 0 && lane < HPW) {
+                } else if (quarter == 0) {
                     ws[SLOT_O + hl] = any ? m : -INFINITY;
                     ws[SLOT_O + HM + hl] = sum;
                 }
                 __syncwarp();
-                if (lane < HPW) head[hl] = f;              // the same from every quarter
+                fac[hl] = f;                               // the same from every quarter
+                head[hl] = 0.0f;
                 __syncwarp();
                 const float2 *cs = nullptr;
                 if constexpr (ROPE)
                     if (whole) cs = rotation_row(p.a, un.tok, threadIdx.x == 0);
-                if (hb < un.nh) {
 #pragma unroll 1
-                    for (int c = 0; c < NPAN; ++c) {
-                        const int d = c * 128 + row;
-                        uint32_t r[HPW];
-                        float x[HPW];
-                        tmem_ld16(tm + TM_O + c * HM + hb, r);
-                        tmem_wait16(r);
+                for (int k = 0; k < 2 * NPAN; ++k) {
+                    const int c = k >> 1, h0 = hb + (k & 1) * 16, d = c * 128 + row;
+                    if (h0 >= un.nh) continue;
+                    uint32_t r[16];
+                    float x[16];
+                    tmem_ld16(tm + TM_O + c * HM + h0, r);
+                    tmem_wait16(r);
 #pragma unroll
-                        for (int i = 0; i < HPW; i += 4) {
-                            const float4 f4 = lds4(head + hb + i);
-                            const float fv[4] = {f4.x, f4.y, f4.z, f4.w};
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 f4 = lds4(fac + h0 + i);
+                        x[i] = __uint_as_float(r[i]) * f4.x;
+                        x[i + 1] = __uint_as_float(r[i + 1]) * f4.y;
+                        x[i + 2] = __uint_as_float(r[i + 2]) * f4.z;
+                        x[i + 3] = __uint_as_float(r[i + 3]) * f4.w;
+                    }
+                    if (whole) {
+                        if (ROPE && cs && c * 128 + quarter * 32 + 31 >= D - p.a.rd) {
+                            const bool turned = d >= D - p.a.rd;
+                            float2 t = turned ? __ldg(cs + ((d - (D - p.a.rd)) >> 1)) : make_float2(1.0f, 0.0f);
+                            if (d & 1) t.y = -t.y;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) x[i + k] = __uint_as_float(r[i + k]) * fv[k];
-                        }
-                        if (whole) {
-                            if (ROPE && cs && c * 128 + quarter * 32 + 31 >= D - p.a.rd) {
-                                const bool turned = d >= D - p.a.rd;
-                                float2 t = turned ? __ldg(cs + ((d - (D - p.a.rd)) >> 1)) : make_float2(1.0f, 0.0f);
-                                if (d & 1) t.y = -t.y;
-#pragma unroll
-                                for (int i = 0; i < HPW; ++i) {
-                                    const float y = __shfl_xor_sync(kAll, x[i], 1);
-                                    x[i] = turned ? x[i] * t.x + y * t.y : x[i];
-                                }
+                            for (int i = 0; i < 16; ++i) {
+                                const float y = __shfl_xor_sync(kAll, x[i], 1);
+                                x[i] = turned ? x[i] * t.x + y * t.y : x[i];
                             }
-                            uint16_t *col = p.a.o + (un.tok * p.a.h + un.h0 + hb) * D + d;
-                            if (hb + HPW <= un.nh) {
-#pragma unroll
-                                for (int i = 0; i < HPW; ++i) col[i * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < HPW; ++i)
-                                    if (hb + i < un.nh) col[i * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
-                            }
-                        } else {
-                            float *col = ws + hb * D + d;
-#pragma unroll
-                            for (int i = 0; i < HPW; ++i)
-                                if (hb + i < un.nh) col[i * D] = x[i];
                         }
+                        uint16_t *col = p.a.o + ((int64_t)un.tok * p.a.h + un.h0 + h0) * D + d;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (h0 + i < un.nh) col[i * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
+                    } else {
+                        float *col = ws + h0 * D + d;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (h0 + i < un.nh) col[i * D] = x[i];
                     }
                 }
                 tc_fence_before();
@@ -890,7 +905,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
 // Merge the partials of the units that a range boundary cuts: block (cut unit, head), thread = four columns.
 struct CombineParams {
     Args a;
-    int64_t ntok;
+    int ntok;
     int groups;
     bool interleave;
     const float *ws;
@@ -902,8 +917,7 @@ template <bool ROPE>
 __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
     grid_dependency_wait();
     const int4 c = p.cut[blockIdx.x];
-    const int64_t ord = p.groups == 1 ? c.x : c.x >> 1;
-    const int64_t tok = unit_at(ord, p.ntok, p.interleave);
+    const int tok = token_at((uint32_t)(p.groups == 1 ? c.x : c.x >> 1), p.ntok, p.interleave);
     const int h0 = p.groups == 1 ? 0 : (c.x & 1) * HM, hh = blockIdx.y;
     if (h0 + hh >= p.a.h) return;
     auto part = [&](int i) { return p.ws + ((size_t)(c.y + i) * 2 + (((uint32_t)c.w >> i) & 1u)) * SLOT; };
@@ -943,7 +957,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
                               acc.w * t1.x - acc.z * t1.y);
         }
     }
-    *reinterpret_cast<uint2 *>(p.a.o + (tok * p.a.h + h0 + hh) * D + d) =
+    *reinterpret_cast<uint2 *>(p.a.o + ((int64_t)tok * p.a.h + h0 + hh) * D + d) =
         make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
 }
 
@@ -1004,12 +1018,12 @@ int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream) {
     const size_t need = fp4::workspace_bytes(pl);
     if (a.workspace_bytes < need || (need && !a.workspace)) return DS_EWORKSPACE;
     const bool rope = a.rd > 0, interleave = a.m > 1;
-    fp4::Params p{a, pl.ntok, pl.nunit, pl.groups, (int)pl.G, (int)pl.K, interleave, a.scale * fp4::kLog2e,
+    fp4::Params p{a, (int)pl.ntok, (int)pl.nunit, pl.groups, (int)pl.G, (int)pl.K, interleave, a.scale * fp4::kLog2e,
                   static_cast<float *>(a.workspace), test_stall() ? 1 : 0};
     fp4::CombineParams c;
     if (pl.split) {
         c.a = a;
-        c.ntok = pl.ntok;
+        c.ntok = (int)pl.ntok;
         c.groups = pl.groups;
         c.interleave = interleave;
         c.ws = p.ws;
