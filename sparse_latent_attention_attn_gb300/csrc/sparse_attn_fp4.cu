@@ -27,9 +27,10 @@
 //
 // Warps: 0-7 softmax and epilogue (warp w: TMEM lanes 32 (w % 4).., heads 32 (w / 4)..), 8-15 rows (codes
 // loaded a tile ahead into registers, widened into the swizzled stage; q at a unit's first tile), 16 MMA
-// issue, 17 index rows: it drops entries without a row, turns the others into row numbers and hands tiles of
-// up to 128 to the row warps (a unit without rows gives one tile of none).  What a tile is (its rows, whether
-// it is its unit's first or last) goes on with the stage.
+// issue, 17 index rows: it drops entries without a row, turns the others into row numbers and hands out tiles of
+// up to 128 (a unit without rows gives one tile of none), 18-19 the exponents of a tile's rows, between
+// the index warp and the row warps.  What a tile is (its rows, whether it is its unit's first or last) goes on
+// with the stage.
 // A unit is one token and up to 64 heads; units are shared out as in the other attention kernels
 // (attn_split.cuh), and units cut by a range boundary leave f32 partials that a second kernel merges.
 // Every wait is bounded (2 s): then DS_DEV_TIMEOUT is flagged, issued MMAs are drained, TMEM is freed.
@@ -56,7 +57,7 @@ constexpr int PANEL = BN * 128;         // bytes of a panel: 128 rows (of C or o
 constexpr int STAGE = NPAN * PANEL;     // 64 KB
 constexpr int NR = 4;                   // index messages
 constexpr int NSOFTW = 8, NSOFT = 32 * NSOFTW, HPW = 32;    // softmax warps; heads of one
-constexpr int W_ROWS = NSOFTW, NROWW = 8, W_MMA = W_ROWS + NROWW, W_IDX = W_MMA + 1, NTHREADS = 640;   // 18, 19: none
+constexpr int W_ROWS = NSOFTW, NROWW = 8, W_MMA = W_ROWS + NROWW, W_IDX = W_MMA + 1, W_EXP = W_IDX + 1, NTHREADS = 640;
 constexpr int RPL = BN / (2 * NROWW);                // steps of two rows that a row warp takes a tile
 // of the 96 registers a thread of the launch the softmax warps take more
 constexpr uint32_t REG_SOFT = 112, REG_OTHER = 80;
@@ -68,8 +69,9 @@ constexpr int P_BYTES = BN * 128;       // row r: 64 bytes hi, 64 bytes lo
 constexpr int SM_CTL = SM_P + P_BYTES;
 // control block
 constexpr int C_ROWS = 0;                       // [NR][128] int32 row numbers
-constexpr int C_EXPS = C_ROWS + NR * BN * 4;    // [128][16] k - e_r + 27 (0: out of reach) of the tile being widened
-constexpr int C_REXP = C_EXPS + BN * (D / 32);  // [2][128] int8 e_r
+constexpr int C_EXPS = C_ROWS + NR * BN * 4;    // [NR][128][16] k - e_r + 27 of the rows' blocks (0: out of reach)
+constexpr int C_TOPS = C_EXPS + NR * BN * (D / 32);   // [NR][128] int8 e_r
+constexpr int C_REXP = C_TOPS + NR * BN;        // [2][128] int8 e_r of the stages' rows
 constexpr int C_MAX = C_REXP + 2 * BN;          // [4][64] f32 maxima of the quarters
 constexpr int C_EMAX = C_MAX + 4 * HM * 4;      // [4] int32 largest e_r of the quarters
 constexpr int C_SUM = C_EMAX + 16;              // [4][64] f32 sums of the quarters, at a unit's end
@@ -78,8 +80,9 @@ constexpr int C_FAC = C_HEAD + HM * 4;          // [64] f32 factor of O^T: at m'
 constexpr int C_QS = C_FAC + HM * 4;           // [2][64] f32 2^g scale log2(e), by unit parity
 constexpr int C_BAR = C_QS + 2 * HM * 4;
 enum : int {
-    B_MSG = 0,                  // [NR] index -> rows: message written
-    B_MSGFREE = B_MSG + NR,     // [NR] rows -> index
+    B_MSG = 0,                  // [NR] index -> exponents: message written
+    B_EXP = B_MSG + NR,         // [NR] exponents -> rows: message and exponents written
+    B_MSGFREE = B_EXP + NR,     // [NR] rows -> index
     B_KV = B_MSGFREE + NR,      // [2] rows -> MMA, softmax: stage and its meta written (and q, at a unit's first tile)
     B_PV = B_KV + 2,            // [2][4] MMA -> rows, softmax: P V of the tile's rows 32 k .. done
     B_S = B_PV + 8,             // [2] MMA -> softmax, rows: scores ready
@@ -396,6 +399,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
     if (threadIdx.x == 0) {
         for (int i = 0; i < NR; ++i) {
             mbar_init(BAR(B_MSG + i), 1);
+            mbar_init(BAR(B_EXP + i), 2);
             mbar_init(BAR(B_MSGFREE + i), NROWW);
         }
         for (int i = 0; i < 2; ++i) {
@@ -499,42 +503,35 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
         // of the panel.  Eight neighbouring lanes then store to all eight 16-byte columns of a 128-byte row:
         // the even ones from the even row, the odd ones from the odd row.
         const int w = warp - W_ROWS, panel = lane >> 3, half = (lane >> 2) & 1, u = panel * 4 + (lane & 3);
-        const int mytile = 32 * ((lane >> 2) & 3) + 4 * w + (lane & 3);   // the row (of step i: lane 2 i + half) it holds
         uint32_t at[2];                                      // of the block's first half in step i % 2
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             at[i] = base + SM_KV + (uint32_t)panel * PANEL + (uint32_t)(4 * w + 2 * i + half) * 128 +
                     (uint32_t)(((lane & 3) * 2 ^ (4 * (w & 1) + 2 * i + half)) * 16);
         const uint32_t sign = p.scale_log2 < 0.0f ? 0x80000000u : 0u;
-        uint8_t *mine = ctl + C_EXPS + w * 16 * (D / 32);
         uint32_t unit = u0;
-        int msg = 0, row = -1;                               // row: number of row mytile of the tile in hand, or -1
+        int msg = 0;
         uint32_t seg = 0;
-        uint4 raw[RPL], ev;                                  // its codes and exponents, 16 bytes a lane and step
-        // message n: what it says, and this lane's row
+        uint4 raw[RPL];                                      // codes of the tile in hand, 16 bytes a lane and step
+        const uint8_t *codes = p.a.codes + u * 16;
+        const int first_row = 4 * w + half;                  // of step 0
         auto next_msg = [&](uint32_t n) -> bool {
-            if (!warp_wait(BAR(B_MSG + n % NR), (n / NR) & 1u, abort_flag)) return false;
+            if (!warp_wait(BAR(B_EXP + n % NR), (n / NR) & 1u, abort_flag)) return false;
             msg = msgs[n % NR];
-            row = (msg & 255) == kTile && mytile < msg >> 16
-                      ? reinterpret_cast<const int32_t *>(ctl + C_ROWS)[(n % NR) * BN + mytile]
-                      : -1;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(B_MSGFREE + n % NR));
             return true;
         };
-        // where there is no row: q, which is there, and counts as zeros below
-        auto load = [&](int i) {
-            const int r = __shfl_sync(kAll, row, 2 * i + half);
-            raw[i] = ld_row(r >= 0 ? p.a.codes + (int64_t)r * (D / 2) + u * 16 : reinterpret_cast<const uint8_t *>(p.a.q));
-        };
-        auto load_exps = [&]() {
-            ev = ld_row(row >= 0 ? (const void *)(p.a.exps + (int64_t)row * (D / 32)) : (const void *)p.a.q);
+        // step i of message n; a tile without rows loads nothing, its exponents are all 0
+        auto load = [&](uint32_t n, int i) {
+            const int r = reinterpret_cast<const int32_t *>(ctl + C_ROWS)[(n % NR) * BN + first_row + 32 * (i >> 1) + 2 * (i & 1)];
+            if (msg >> 16) raw[i] = ld_row(codes + (int64_t)r * (D / 2));
         };
         bool ok = next_msg(0);
         if (ok) {
-            load_exps();
 #pragma unroll
-            for (int i = 0; i < RPL; ++i) load(i);
+            for (int i = 0; i < RPL; ++i) {
+                raw[i] = make_uint4(0, 0, 0, 0);
+                load(0, i);
+            }
         }
         for (uint32_t J = 0; ok; ++J) {
             const int tile = msg;
@@ -570,31 +567,23 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     if (lane == i) qs = fmaxf(fabsf(p.scale_log2) * pow2(g), 1.17549435e-38f);   // never 0: see the scores
                 }
             }
-            // the row's largest exponent, and k - e_r + 27 of its 16 blocks, 0 where that is less (or there is no row)
-            const uint32_t m4 = __vmaxs4(__vmaxs4(ev.x, ev.y), __vmaxs4(ev.z, ev.w));
-            const int emax = max(max((int)(int8_t)m4, (int)(int8_t)(m4 >> 8)), max((int)(int8_t)(m4 >> 16), (int)m4 >> 24));
-            const uint32_t low = (uint32_t)(uint8_t)max(emax - 27, -128) * 0x01010101u;
-            const uint32_t lift = (uint32_t)(uint8_t)(max(emax - 27, -128) - (emax - 27)) * 0x01010101u;
-            const uint32_t on = row >= 0 ? kAll : 0u;
-            __syncwarp();
-            if (lane < 16)
-                reinterpret_cast<uint4 *>(mine)[lane] =
-                    make_uint4(above(ev.x, low, lift) & on, above(ev.y, low, lift) & on, above(ev.z, low, lift) & on,
-                               above(ev.w, low, lift) & on);
-            __syncwarp();
             if (!next_msg(J + 1)) break;
-            load_exps();
+            const uint8_t *exps = ctl + C_EXPS + ((J % NR) * BN + first_row) * (D / 32) + u;
 #pragma unroll
             for (int i = 0; i < RPL; ++i) {
-                if (J >= 2 && (i & 1) == 0) ok = ok && warp_wait(BAR(B_PV + 4 * st + (i >> 1)), ((J >> 1) - 1) & 1u, abort_flag);
+                // handed back by halves: each wait costs about as much as a step
+                if (J >= 2 && (i & 3) == 0) ok = ok && warp_wait(BAR(B_PV + 4 * st + (i >> 1) + 1), ((J >> 1) - 1) & 1u, abort_flag);
                 uint32_t o[8];
-                widen(raw[i], mine[(2 * i + half) * (D / 32) + u], o);
-                load(i);                          // of the next tile: in flight until its turn
+                widen(raw[i], exps[(32 * (i >> 1) + 2 * (i & 1)) * (D / 32)], o);
+                load(J + 1, i);                   // in flight until its turn
                 const uint32_t to = at[i & 1] + st * STAGE + (uint32_t)(i >> 1) * 4096;
                 st_shared_v4(to, o[0], o[1], o[2], o[3]);
                 st_shared_v4(to ^ 16u, o[4], o[5], o[6], o[7]);
             }
             if (!ok) break;
+            if (lane < 16)
+                reinterpret_cast<int8_t *>(ctl + C_REXP)[st * BN + 16 * w + lane] =
+                    reinterpret_cast<const int8_t *>(ctl + C_TOPS)[(J % NR) * BN + 16 * w + lane];
             if (warp == W_ROWS && lane == 0) meta[st] = tile;
             if (tile & kLast) ++unit;
             if (tile & kFirst) {
@@ -602,10 +591,44 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 if (lane < 8) reinterpret_cast<float *>(ctl + C_QS)[(seg & 1u) * HM + 8 * w + lane] = qs;
                 ++seg;
             }
-            if (lane < 16) reinterpret_cast<int8_t *>(ctl + C_REXP)[st * BN + mytile] = (int8_t)emax;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && !(p.stall_first_tile && J == 0)) mbar_arrive(BAR(B_KV + st));
+            if (lane == 0) {
+                mbar_arrive(BAR(B_MSGFREE + J % NR));
+                if (!(p.stall_first_tile && J == 0)) mbar_arrive(BAR(B_KV + st));
+            }
+        }
+    } else if (warp >= W_EXP) {
+        // ========================= exponents of the rows: lane = two rows =========================
+        for (uint32_t n = 0;; ++n) {
+            if (!warp_wait(BAR(B_MSG + n % NR), (n / NR) & 1u, abort_flag)) break;
+            const int msg = msgs[n % NR], count = (msg & 255) == kTile ? msg >> 16 : 0;
+            int32_t *rows = reinterpret_cast<int32_t *>(ctl + C_ROWS) + (n % NR) * BN;
+            const int r0 = count > 0 ? rows[0] : 0;
+            uint4 ev[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int i = 64 * (warp - W_EXP) + 32 * k + lane;
+                ev[k] = make_uint4(0, 0, 0, 0);
+                if (i < count) ev[k] = ld_row(p.a.exps + (int64_t)rows[i] * (D / 32));
+                else rows[i] = r0;                // beyond the count: the tile's first row, with exponents 0
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int i = 64 * (warp - W_EXP) + 32 * k + lane;
+                const uint32_t m4 = __vmaxs4(__vmaxs4(ev[k].x, ev[k].y), __vmaxs4(ev[k].z, ev[k].w));
+                const int top = max(max((int)(int8_t)m4, (int)(int8_t)(m4 >> 8)), max((int)(int8_t)(m4 >> 16), (int)m4 >> 24));
+                const uint32_t low = (uint32_t)(uint8_t)max(top - 27, -128) * 0x01010101u;
+                const uint32_t lift = (uint32_t)(uint8_t)(max(top - 27, -128) - (top - 27)) * 0x01010101u;
+                const uint32_t on = i < count ? kAll : 0u;
+                reinterpret_cast<uint4 *>(ctl + C_EXPS)[(n % NR) * BN + i] =
+                    make_uint4(above(ev[k].x, low, lift) & on, above(ev[k].y, low, lift) & on, above(ev[k].z, low, lift) & on,
+                               above(ev[k].w, low, lift) & on);
+                reinterpret_cast<int8_t *>(ctl + C_TOPS)[(n % NR) * BN + i] = (int8_t)top;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(B_EXP + n % NR));
+            if ((msg & 255) == kFin) break;
         }
     } else if (warp == W_MMA) {
         // ================================== MMA issue ==================================
