@@ -60,7 +60,7 @@ constexpr int NSOFTW = 8, NSOFT = 32 * NSOFTW, HPW = 32;    // softmax warps; he
 constexpr int W_ROWS = NSOFTW, NROWW = 8, W_MMA = W_ROWS + NROWW, W_IDX = W_MMA + 1, W_EXP = W_IDX + 1, NTHREADS = 640;
 constexpr int RPL = BN / (2 * NROWW);                // steps of two rows that a row warp takes a tile
 // of the 96 registers a thread of the launch the softmax warps take more
-constexpr uint32_t REG_SOFT = 112, REG_OTHER = 80;
+constexpr uint32_t REG_SOFT = 120, REG_OTHER = 80;
 static_assert(NSOFT * REG_SOFT + (NTHREADS - NSOFT) * REG_OTHER <= NTHREADS * 96, "register split");
 constexpr int SM_Q = 0;
 constexpr int SM_KV = SM_Q + STAGE;
@@ -75,7 +75,7 @@ constexpr int C_REXP = C_TOPS + NR * BN;        // [2][128] int8 e_r of the stag
 constexpr int C_MAX = C_REXP + 2 * BN;          // [4][64] f32 maxima of the quarters
 constexpr int C_EMAX = C_MAX + 4 * HM * 4;      // [4] int32 largest e_r of the quarters
 constexpr int C_SUM = C_EMAX + 16;              // [4][64] f32 sums of the quarters, at a unit's end
-constexpr int C_HEAD = C_SUM + 4 * HM * 4;      // [64] f32 running maximum m, 0 at a unit's start
+constexpr int C_HEAD = C_SUM + 4 * HM * 4;      // [64] f32 minus the running maximum m, 0 at a unit's start
 constexpr int C_FAC = C_HEAD + HM * 4;          // [64] f32 factor of O^T: at m's rise, and at a unit's end
 constexpr int C_QS = C_FAC + HM * 4;           // [2][64] f32 2^g scale log2(e), by unit parity
 constexpr int C_BAR = C_QS + 2 * HM * 4;
@@ -207,10 +207,17 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t v) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
-    return r;
+// 32 times what e4m3 values h leave of x0 and x1 (exact in f32), in e4m3
+__device__ __forceinline__ uint32_t e4m3x2_rest(uint32_t h, float x0, float x1) {
+    float r0, r1;
+    asm("{\n\t.reg .b32 f;\n\t.reg .b16 f0, f1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 f, %2;\n\t"
+        "mov.b32 {f0, f1}, f;\n\t"
+        "sub.rn.f32.f16 %0, f0, %3;\n\t"
+        "sub.rn.f32.f16 %1, f1, %4;\n\t}"
+        : "=f"(r0), "=f"(r1)
+        : "h"((uint16_t)h), "f"(x0), "f"(x1));
+    return e4m3x2(r0 * -32.0f, r1 * -32.0f);
 }
 
 // 16 bytes of the cache that no L1 line is kept for: beside 220 KB of shared memory L1 has 28 KB, less than the
@@ -237,10 +244,7 @@ __device__ __forceinline__ int put_q(uint32_t sq, int hh, const uint4 (&v)[2], i
     for (int k = 0; k < 8; ++k) {
         const float x0 = bf16_lo(w[k]) * down, x1 = bf16_hi(w[k]) * down;
         const uint32_t h2 = e4m3x2(x0, x1);
-        const uint32_t f2 = f16x2_of_e4m3x2(h2);
-        const float y0 = __half2float(__ushort_as_half((unsigned short)(f2 & 0xffffu)));
-        const float y1 = __half2float(__ushort_as_half((unsigned short)(f2 >> 16)));
-        const uint32_t l2 = e4m3x2((x0 - y0) * 32.0f, (x1 - y1) * 32.0f);
+        const uint32_t l2 = e4m3x2_rest(h2, x0, x1);
         hi[k >> 1] = k & 1 ? hi[k >> 1] | (h2 << 16) : h2;
         lo[k >> 1] = k & 1 ? lo[k >> 1] | (l2 << 16) : l2;
     }
@@ -279,19 +283,55 @@ __device__ __forceinline__ uint32_t above(uint32_t k, uint32_t low, uint32_t lif
     return (__vmaxs4(k, low) ^ 0x80808080u) - (low ^ 0x80808080u) + lift;
 }
 
-// Two probabilities as hi (e4m3) - lo (e5m2): lo from hi - p, which is exact in f32.
-__device__ __forceinline__ void split_p(float p0, float p1, uint32_t &hi, uint32_t &lo) {
-    asm("{\n\t.reg .b32 f;\n\t.reg .b16 h, l, f0, f1;\n\t.reg .f32 r0, r1;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 h, %3, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 f, h;\n\t"
+// Two f32 in a register pair, and the packed operations on them: half the instructions.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Four probabilities as hi (e4m3) - lo (e5m2): lo from hi - p, which is exact in f32.
+__device__ __forceinline__ void split_p(uint64_t p01, uint64_t p23, uint32_t &hi, uint32_t &lo) {
+    asm("{\n\t.reg .b32 f, g;\n\t.reg .b16 h0, h1, l0, l1, f0, f1, g0, g1;\n\t.reg .f32 p0, p1, p2, p3;\n\t"
+        "mov.b64 {p0, p1}, %2;\n\t"
+        "mov.b64 {p2, p3}, %3;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h0, p1, p0;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h1, p3, p2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 f, h0;\n\t"
+        "cvt.rn.f16x2.e4m3x2 g, h1;\n\t"
         "mov.b32 {f0, f1}, f;\n\t"
-        "sub.rn.f32.f16 r0, f0, %2;\n\t"
-        "sub.rn.f32.f16 r1, f1, %3;\n\t"
-        "cvt.rn.satfinite.e5m2x2.f32 l, r1, r0;\n\t"
-        "cvt.u32.u16 %0, h;\n\t"
-        "cvt.u32.u16 %1, l;\n\t}"
+        "mov.b32 {g0, g1}, g;\n\t"
+        "sub.rn.f32.f16 p0, f0, p0;\n\t"
+        "sub.rn.f32.f16 p1, f1, p1;\n\t"
+        "sub.rn.f32.f16 p2, g0, p2;\n\t"
+        "sub.rn.f32.f16 p3, g1, p3;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f32 l0, p1, p0;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f32 l1, p3, p2;\n\t"
+        "mov.b32 %0, {h0, h1};\n\t"
+        "mov.b32 %1, {l0, l1};\n\t}"
         : "=r"(hi), "=r"(lo)
-        : "f"(p0), "f"(p1));
+        : "l"(p01), "l"(p23));
 }
 
 // One step of summing 32 values over a warp: lanes O apart share the first 2 O of them out.
@@ -697,7 +737,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
         const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16);
         float *head = reinterpret_cast<float *>(ctl + C_HEAD), *fac = reinterpret_cast<float *>(ctl + C_FAC), *sums = reinterpret_cast<float *>(ctl + C_SUM);
         const float *qs = reinterpret_cast<const float *>(ctl + C_QS);
-        float l[HPW];
+        uint64_t l[HPW / 2];   // sums of p over this thread's rows, in pairs of heads
         float m = 0.0f;        // of head hl
         int E = 0;
         uint32_t unit = u0, seg = 0;
@@ -718,7 +758,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             const bool live = row < count;
             float *maxima = reinterpret_cast<float *>(ctl + C_MAX);
             int *emax = reinterpret_cast<int *>(ctl + C_EMAX);
-            float v[HPW];          // scores in octaves, less m
+            uint64_t v[HPW / 2];   // scores in octaves, less m, in pairs of heads
             int e = 0;
             bool late = true;      // m or E has to move
             if (!bad) bad = !warp_wait(BAR(B_S + st), (J >> 1) & 1u, abort_flag);
@@ -729,9 +769,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 }
                 tc_fence_after();
                 e = (int)reinterpret_cast<const int8_t *>(ctl + C_REXP)[st * BN + row];
-                const float cr = pow2(e - 12);
+                const float c = pow2(e - 12);
+                const uint64_t cr = pair(c, c), low = pair(0.03125f, 0.03125f);
                 const float *q = qs + ((seg - 1) & 1u) * HM + hb;
-                float top = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < HPW; j += 16) {
                     uint32_t r0[16], r1[16];
@@ -742,11 +782,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
                         const float4 q4 = lds4(q + j + i), m4 = lds4(head + hb + j + i);
-                        const float qv[4] = {q4.x, q4.y, q4.z, q4.w}, mv[4] = {m4.x, m4.y, m4.z, m4.w};
+                        const uint64_t qv[2] = {pair(q4.x, q4.y), pair(q4.z, q4.w)}, mv[2] = {pair(m4.x, m4.y), pair(m4.z, m4.w)};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float s = fmaf(__uint_as_float(r1[i + k]), 0.03125f, __uint_as_float(r0[i + k])) * cr;
-                            v[j + i + k] = fmaf(s, qv[k], -mv[k]);
+                        for (int k = 0; k < 2; ++k) {
+                            const uint64_t s = fma2(pair(__uint_as_float(r1[i + 2 * k]), __uint_as_float(r1[i + 2 * k + 1])), low,
+                                                    pair(__uint_as_float(r0[i + 2 * k]), __uint_as_float(r0[i + 2 * k + 1])));
+                            v[(j + i) / 2 + k] = fma2(mul2(s, cr), qv[k], mv[k]);
                         }
                     }
                 }
@@ -755,18 +796,26 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 if (lane == 0) mbar_arrive(BAR(B_SFREE + st));
                 if (!live) {       // a row beyond the tile's count
 #pragma unroll
-                    for (int i = 0; i < HPW; ++i) v[i] = -INFINITY;
+                    for (int i = 0; i < HPW / 2; ++i) v[i] = pair(-INFINITY, -INFINITY);
                 }
+                float top = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < HPW; ++i) top = fmaxf(top, v[i]);
+                for (int i = 0; i < HPW / 2; ++i) {
+                    float a, b;
+                    unpair(v[i], a, b);
+                    top = max3(top, a, b);
+                }
                 late = first || top > kSlack || (live && e > E);
             }
             if (bar_or(late)) {
                 // the tile's maxima, and the heads' m and E behind them: always at a unit's first tile, seldom later
 #pragma unroll
-                for (int i = 0; i < HPW; ++i) {
-                    const float mx = warp_max(v[i]);
-                    if (lane == 0) maxima[quarter * HM + hb + i] = mx;
+                for (int i = 0; i < HPW / 2; ++i) {
+                    float a, b;
+                    unpair(v[i], a, b);
+                    a = warp_max(a);
+                    b = warp_max(b);
+                    if (lane == 0) *reinterpret_cast<float2 *>(maxima + quarter * HM + hb + 2 * i) = make_float2(a, b);
                 }
                 const int te = __reduce_max_sync(kAll, live ? e : -128);
                 if (lane == 0 && hb == 0) emax[quarter] = te;
@@ -781,14 +830,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 m += up;
                 const float down = pow2(E0 - E);
                 __syncwarp();
-                head[hl] = m;                          // the same from every quarter
+                head[hl] = -m;                         // the same from every quarter
                 fac[hl] = ex2(-up);
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < HPW; ++i) v[i] -= __shfl_sync(kAll, up, i);
+                for (int i = 0; i < HPW / 2; ++i)
+                    v[i] = add2(v[i], pair(-__shfl_sync(kAll, up, 2 * i), -__shfl_sync(kAll, up, 2 * i + 1)));
                 if (first) {
 #pragma unroll
-                    for (int i = 0; i < HPW; ++i) l[i] = 0.0f;
+                    for (int i = 0; i < HPW / 2; ++i) l[i] = 0;
                 } else {
                     // this warp's part of O^T, and its sums, follow m and E
                     bad = !warp_wait(BAR(B_PV + 4 * (st ^ 1u) + 3), ((J - 1) >> 1) & 1u, abort_flag);
@@ -806,26 +856,25 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     }
                     tmem_st_wait();
 #pragma unroll
-                    for (int i = 0; i < HPW; ++i) l[i] *= fac[hb + i];
+                    for (int i = 0; i < HPW; i += 2) l[i / 2] = mul2(l[i / 2], pair(fac[hb + i], fac[hb + i + 1]));
                 }
             }
             uint32_t hi[HPW / 4], lo[HPW / 4];
             {
-                const float fr = live ? pow2(e - E + 4) : 0.0f;
+                const float f = live ? pow2(e - E + 4) : 0.0f;
+                const uint64_t fr = pair(f, f);
 #pragma unroll
-                for (int i = 0; i < HPW; i += 4) {
-                    float pr[4];
+                for (int i = 0; i < HPW / 2; i += 2) {
+                    uint64_t pr[2];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        pr[k] = ex2(v[i + k]);
-                        l[i + k] += pr[k];
-                        pr[k] *= fr;
+                    for (int k = 0; k < 2; ++k) {
+                        float a, b;
+                        unpair(v[i + k], a, b);
+                        pr[k] = pair(ex2(a), ex2(b));
+                        l[i + k] = add2(l[i + k], pr[k]);
+                        pr[k] = mul2(pr[k], fr);
                     }
-                    uint32_t h0, h1, l0, l1;
-                    split_p(pr[0], pr[1], h0, l0);
-                    split_p(pr[2], pr[3], h1, l1);
-                    hi[i >> 2] = prmt(h0, h1, 0x5410);
-                    lo[i >> 2] = prmt(l0, l1, 0x5410);
+                    split_p(pr[0], pr[1], hi[i / 2], lo[i / 2]);
                 }
             }
             // P is free once the tile before has been multiplied
@@ -845,12 +894,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 const Unit un = unit_of(p, unit);
                 const bool whole = msg & kWhole;
                 // sums over the warp's rows: lane i ends up with head hb + i
-                fold<16>(l, lane);
-                fold<8>(l, lane);
-                fold<4>(l, lane);
-                fold<2>(l, lane);
-                fold<1>(l, lane);
-                sums[quarter * HM + hl] = l[0];
+                float s[HPW];
+#pragma unroll
+                for (int i = 0; i < HPW; i += 2) unpair(l[i / 2], s[i], s[i + 1]);
+                fold<16>(s, lane);
+                fold<8>(s, lane);
+                fold<4>(s, lane);
+                fold<2>(s, lane);
+                fold<1>(s, lane);
+                sums[quarter * HM + hl] = s[0];
                 bad = bad || !warp_wait(BAR(B_PV + 4 * st + 3), (J >> 1) & 1u, abort_flag);
                 tc_fence_after();
                 if (bar_or(bad)) break;
@@ -901,9 +953,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                             }
                         }
                         uint16_t *col = p.a.o + ((int64_t)un.tok * p.a.h + un.h0 + h0) * D + d;
+                        if (h0 + 16 <= un.nh) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (h0 + i < un.nh) col[i * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
+                            for (int i = 0; i < 16; ++i) col[i * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (h0 + i < un.nh) col[i * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
+                        }
                     } else {
                         float *col = ws + h0 * D + d;
 #pragma unroll
