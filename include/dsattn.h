@@ -377,7 +377,7 @@ int ds_indexer_topk(const uint16_t *q, const uint16_t *k, const float *w, int b,
  * x          device bf16, row (bi, t, hh) at x + bi * x_bstride + t * x_tstride + hh * d (strides in
  *            elements, multiples of 8), 16-byte aligned: heads may lie in a wider projection
  * y          device bf16 [b][s][h][d], 16-byte aligned; y may be x when x is laid out so
- * weight     device f32 [d], one for all heads, or NULL
+ * weight     device f32 [d], one for all heads, 16-byte aligned, or NULL
  * eps        > 0
  * rd         multiple of 8, 0 <= rd <= d (0: no rotation, table may be NULL)
  * table      device f32 [table_rows][rd / 2][2] of (cos, sin), 8-byte aligned

@@ -335,7 +335,7 @@ int ds_norm_rotary(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint
     if (d > 1024) return DS_EUNSUPPORTED;
     if ((int64_t)b * s == 0) return DS_OK;
     if ((int64_t)b * s > INT32_MAX / h) return DS_EUNSUPPORTED;
-    if (!x || !y || !first || !aligned16(x) || !aligned16(y) || !aligned4(weight) || !aligned4(first) || !aligned4(lens))
+    if (!x || !y || !first || !aligned16(x) || !aligned16(y) || !aligned16(weight) || !aligned4(first) || !aligned4(lens))
         return DS_EINVAL;
     if (!strides_ok(x_bstride, x_tstride, b, s, (int64_t)h * d)) return DS_EINVAL;
     unsigned int *status = status_word();
@@ -355,7 +355,7 @@ int ds_kv_append_fp4_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstri
     if (!rotation_ok(rd, d, table, table_rows) || !pool_ok(pages, page, max_pages)) return DS_EINVAL;
     if (d > 1024 || !pool_fits(pages, page) || (int64_t)b * s > INT32_MAX) return DS_EUNSUPPORTED;
     if ((int64_t)b * s == 0) return DS_OK;
-    if (!x || !first || !aligned16(x) || !aligned16(y) || !aligned4(weight) || !aligned4(first) || !aligned4(lens))
+    if (!x || !first || !aligned16(x) || !aligned16(y) || !aligned16(weight) || !aligned4(first) || !aligned4(lens))
         return DS_EINVAL;
     if (!codes || !exps || !block_table || !aligned16(codes) || !aligned4(block_table)) return DS_EINVAL;
     if (!strides_ok(x_bstride, x_tstride, b, s, d)) return DS_EINVAL;

@@ -6,11 +6,12 @@
 // pages are this library's: with z the row after norm and rotation, per block of 32
 //     k = ceil(log2(max(amax, 1e-4) / 6)),  code_i = e2m1(z_i / 2^k), nearest, ties to the even code.
 //
-// A code is a decision, so it is made on the exact z: the f32 value is within 2^-21 of the magnitudes it
-// was made of (each product and sum below rounds by 2^-24; the norm factor comes from a sum carried in
-// two floats and one Newton step).  A value that near to a border between two codes (or a maximum that
-// near to a power of two times 6) sends its warp through the same formula in 64 bits: about one row of
-// 512 in a thousand.  Rows that are neither normalised nor rotated are exact in f32.
+// A code is a decision, so it is made on the exact z.  The f32 value is off by less than d = 2^-20 of the
+// magnitudes it was made of: half the 15 roundings of the longest chain into the sum of squares, three of the
+// factor 1 / sqrt(ss / d + eps), two products, a product and a sum of the rotation, each 2^-24.  So the codes of
+// z + d and z - d are formed; where they are the same (and the block's exponent is for its maximum + d and - d)
+// they are z's, and where a border lies between them the warp goes through the formula with two floats a
+// number (to about 2^-44): two rows of 512 in a thousand.  Rows that are neither normalised nor rotated are exact in f32 (d = 0).
 //
 // Bound by HBM (2 bytes read, 17/32 written a value, 2 more with y) and at decode sizes by latency: one
 // row a warp (half or a quarter for short rows), 16 bytes a lane and step; a block's maximum is two
@@ -43,22 +44,6 @@ struct AppendArgs {
     unsigned int *status;
 };
 
-// s + e == a + b exactly.
-__device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
-    s = __fadd_rn(a, b);
-    const float bb = __fsub_rn(s, a);
-    e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
-}
-
-// 1 / sqrt(hi + lo) within 2^-24 of itself: the library's value and one Newton step whose residual is
-// formed with fused products.
-__device__ __forceinline__ float rsqrt_near(float hi, float lo) {
-    const float r = 1.0f / sqrtf(hi);
-    const float t = __fmul_rn(r, r), te = fmaf(r, r, -t);
-    const float e = -fmaf(lo, t, fmaf(hi, te, fmaf(hi, t, -1.0f)));   // 1 - (hi + lo) r^2
-    return fmaf(r, 0.5f * e, r);
-}
-
 // Exponent k of a block: the smallest with amax <= 6 * 2^k, from amax's IEEE fields (6 = 1.5 * 4).
 __device__ __forceinline__ int block_exp(float amax) {
     const uint32_t u = __float_as_uint(amax);
@@ -67,49 +52,83 @@ __device__ __forceinline__ int block_exp(float amax) {
 
 __device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 
-// Two codes in a byte, lo in the low nibble; nearest, ties to even, saturating at 6.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+// Eight codes of z * s, the first in the lowest nibble; nearest, ties to even, saturating at 6.
+__device__ __forceinline__ uint32_t codes8(const float (&z)[8], float s) {
     uint32_t r;
-    asm("{\n\t.reg .b8 t;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
-        "cvt.u32.u8 %0, t;\n\t}"
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
         : "=r"(r)
-        : "f"(hi), "f"(lo));
+        : "f"(z[0] * s), "f"(z[1] * s), "f"(z[2] * s), "f"(z[3] * s), "f"(z[4] * s), "f"(z[5] * s), "f"(z[6] * s),
+          "f"(z[7] * s));
     return r;
 }
 
-// Whether |v| is within tol of a border between two codes.
-__device__ __forceinline__ bool near_border(float v, float tol) {
-    const float a = fabsf(v);
-    // borders 0.25, 0.75, 1.25, 1.75 | 2.5, 3.5 | 5: the nearest border of each part
-    const float b = a < 2.125f ? fminf(floorf(2.0f * a) * 0.5f + 0.25f, 1.75f) : a < 4.25f ? (a < 3.0f ? 2.5f : 3.5f) : 5.0f;
-    return fabsf(a - b) <= tol;
+// The values that eight codes stand for at scale sc.
+__device__ __forceinline__ void values8(uint32_t c, float sc, float (&x)[8]) {
+    uint32_t f[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+        : "r"(c));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __half2float(__ushort_as_half((unsigned short)(f[j] & 0xffffu))) * sc;
+        x[2 * j + 1] = __half2float(__ushort_as_half((unsigned short)(f[j] >> 16))) * sc;
+    }
 }
 
-// The value a code of block exponent k stands for.
-__device__ __forceinline__ float code_value(uint32_t code, float sc) {
-    const uint32_t m = code & 7u;
-    const float a = m < 4u ? 0.5f * (float)m : m == 7u ? 6.0f : (float)(m - 2u);
-    return (code & 8u ? -a : a) * sc;
+// ---- the same in two floats (hi + lo, good to about 2^-44), for values next to a border ----
+
+// s + e == a + b exactly.
+__device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
+    s = __fadd_rn(a, b);
+    const float bb = __fsub_rn(s, a);
+    e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
 }
 
-__device__ __forceinline__ uint32_t code_of(double v) {
-    const double a = fabs(v);
-    const uint32_t m = (a > 0.25) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0);
-    return m | (signbit(v) ? 8u : 0u);
+struct F2 {
+    float hi, lo;
+};
+__device__ __forceinline__ F2 times(F2 a, float b) {
+    const float h = __fmul_rn(a.hi, b);
+    return {h, fmaf(a.lo, b, fmaf(a.hi, b, -h))};
+}
+__device__ __forceinline__ F2 plus(F2 a, F2 b) {
+    F2 r;
+    float e;
+    two_sum(a.hi, b.hi, r.hi, e);
+    r.lo = __fadd_rn(e, __fadd_rn(a.lo, b.lo));
+    return r;
 }
 
-// One chunk of the row in 64 bits: norm (factor r), weight, rotation.
-__device__ __noinline__ void chunk64(const uint4 v, double r, const float *w, const float2 *cs, double (&z)[8]) {
-    float x[8];
-    unpack8(v, x);
-    for (int i = 0; i < 8; ++i) z[i] = (double)x[i] * r * (w ? (double)w[i] : 1.0);
-    if (cs)
-        for (int j = 0; j < 4; ++j) {
-            const double a = z[2 * j], b = z[2 * j + 1], c = cs[j].x, s = cs[j].y;
-            z[2 * j] = a * c - b * s;
-            z[2 * j + 1] = a * s + b * c;
-        }
+// One float that rounds like hi + lo: hi, but one unit in its last place towards lo where hi may lie on a border
+// itself.  Borders (and 6 times a power of two) have at most two mantissa bits, and a unit in the last
+// place moves no other such value across one.
+__device__ __forceinline__ float one_float(F2 a) {
+    if (a.lo == 0.0f) return a.hi;               // (a zero keeps its sign)
+    float h, l;
+    two_sum(a.hi, a.lo, h, l);
+    const uint32_t u = __float_as_uint(h);
+    if ((u & 0x1fffffu) != 0 || l == 0.0f) return h;
+    return __uint_as_float((l > 0.0f) == (h > 0.0f) ? u + 1 : u - 1);
+}
+
+// 1 / sqrt((hi + lo) / d + eps): the quotient's remainder goes to the low part; then one Newton step.
+__device__ __forceinline__ F2 norm_factor(float hi, float lo, float d, float eps) {
+    const float q = __fdiv_rn(hi, d), ql = __fdiv_rn(__fadd_rn(fmaf(-q, d, hi), lo), d);
+    float s, e;
+    two_sum(q, eps, s, e);
+    e = __fadd_rn(e, ql);
+    const float r = 1.0f / sqrtf(s), t = __fmul_rn(r, r), te = fmaf(r, r, -t);
+    return {r, __fmul_rn(r, -0.5f * fmaf(e, t, fmaf(s, te, fmaf(s, t, -1.0f))))};
 }
 
 template <int L, int N>
@@ -118,7 +137,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
     const uint32_t tok = blockIdx.x * (kThreads / L) + threadIdx.x / L;
     const int lane = threadIdx.x % L;
     const uint32_t bi = tok / (uint32_t)p.s, t = tok - bi * (uint32_t)p.s;
+    const int nch = p.d / 8, nblk = p.d / 32;
     bool live = tok < p.ntok;
+    // the row, before it is known whether it counts: it is there either way
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.x + (int64_t)bi * p.x_bstride + (int64_t)t * p.x_tstride);
+    uint4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = live && lane + L * i < nch ? src[lane + L * i] : make_uint4(0, 0, 0, 0);
     bool stored = false;
     int64_t pos = 0, slot = 0;
     if (live) {
@@ -147,43 +172,18 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
         if (bad && lane == 0) flag_status(p.status, DS_DEV_BAD_INDEX);
     }
     live = live && (stored || p.y);
-    const int nch = p.d / 8, nblk = p.d / 32;
-    const uint4 *src = reinterpret_cast<const uint4 *>(p.x + (int64_t)bi * p.x_bstride + (int64_t)t * p.x_tstride);
-    uint4 v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = live && lane + L * i < nch ? src[lane + L * i] : make_uint4(0, 0, 0, 0);
     const bool norm = p.eps > 0.0f;
     float r = 1.0f;
     if (norm) {
-        // squares of bf16 values are exact in f32; their sum is carried in two floats
-        float hi = 0.0f, lo = 0.0f;
+        float ss[4] = {0.0f, 0.0f, 0.0f, 0.0f};          // squares of bf16 values are exact in f32
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float x[8];
             unpack8(v[i], x);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float s, e;
-                two_sum(hi, __fmul_rn(x[k], x[k]), s, e);
-                hi = s;
-                lo = __fadd_rn(lo, e);
-            }
+            for (int k = 0; k < 8; ++k) ss[k & 3] = fmaf(x[k], x[k], ss[k & 3]);
         }
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) {
-            const float h2 = __shfl_xor_sync(kAll, hi, o), l2 = __shfl_xor_sync(kAll, lo, o);
-            float s, e;
-            two_sum(hi, h2, s, e);
-            hi = s;
-            lo = __fadd_rn(__fadd_rn(lo, l2), e);
-        }
-        // (hi + lo) / d + eps: the quotient's remainder goes to the low part
-        const float dd = (float)p.d;
-        const float q = __fdiv_rn(hi, dd);
-        const float ql = __fdiv_rn(__fadd_rn(fmaf(-q, dd, hi), lo), dd);
-        float s, e;
-        two_sum(q, p.eps, s, e);
-        r = rsqrt_near(s, __fadd_rn(ql, e));
+        r = 1.0f / sqrtf(row_sum<L>((ss[0] + ss[1]) + (ss[2] + ss[3])) / (float)p.d + p.eps);
     }
     const int rot = (p.d - p.rd) / 8;
     const float2 *cs = p.table + pos * (p.rd / 2);
@@ -193,11 +193,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int c = lane + L * i;
-        const bool in = live && c < nch;
-        float x[8], mag[8];   // a value, and the magnitudes it was made of
+        const bool in = live && c < nch, turned = in && c >= rot;
+        float x[8];
         unpack8(v[i], x);
         if (in && norm) scale8(x, r, p.weight ? p.weight + c * 8 : nullptr);
-        const bool turned = in && c >= rot;
+        float off[8];                                    // how far x may be off
+        const float tol = norm || turned ? 9.53674316e-7f : 0.0f;   // 2^-20
         if (turned) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -205,70 +206,88 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
                 const float a = x[2 * j], b = x[2 * j + 1];
                 x[2 * j] = a * cj.x - b * cj.y;
                 x[2 * j + 1] = a * cj.y + b * cj.x;
-                mag[2 * j] = mag[2 * j + 1] = (fabsf(a) + fabsf(b)) * fmaxf(fabsf(cj.x), fabsf(cj.y));
+                off[2 * j] = off[2 * j + 1] = tol * ((fabsf(a) + fabsf(b)) * fmaxf(fabsf(cj.x), fabsf(cj.y)));
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) mag[j] = fabsf(x[j]);
+            for (int j = 0; j < 8; ++j) off[j] = tol * x[j];      // of x's sign: minus zero stays what it is
         }
-        float amax = 0.0f, most = 0.0f;
+        float amax = 0.0f, far = 0.0f;
+        float up[8], down[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             amax = fmaxf(amax, fabsf(x[j]));
-            most = fmaxf(most, mag[j]);
+            far = fmaxf(far, fabsf(off[j]));
+            up[j] = x[j] + off[j];
+            down[j] = x[j] - off[j];
         }
 #pragma unroll
         for (int o = 1; o <= 2; o <<= 1) {
             amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
-            most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
+            far = fmaxf(far, __shfl_xor_sync(kAll, far, o));
         }
-        amax = fmaxf(amax, 1e-4f);
-        const int k = block_exp(amax);
+        const int k = block_exp(fmaxf(amax + far, 1e-4f));
         const float inv = pow2(-k);
         kexp[i] = k;
-        uint32_t cw = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) cw |= e2m1x2(x[2 * j] * inv, x[2 * j + 1] * inv) << (8 * j);
-        code[i] = cw;
-        if (in && (norm || turned)) {
-            const float tol = 4.76837158e-7f * inv;   // 2^-21, in units of the block's scale
-            const float top = amax * inv;             // in (3, 6]
-            near |= top >= 6.0f - tol * most || top <= 3.0f + tol * most;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) near |= near_border(x[j] * inv, tol * mag[j]);
-        }
+        code[i] = codes8(up, inv);
+        near |= in && tol > 0.0f && (code[i] != codes8(down, inv) || k != block_exp(fmaxf(amax - far, 1e-4f)));
     }
     if (__any_sync(kAll, near)) {
-        double r64 = 1.0;
+        F2 rr = {1.0f, 0.0f};
         if (norm) {
-            double ss = 0.0;
+            float hi = 0.0f, lo = 0.0f, s, e;
+#pragma unroll
             for (int i = 0; i < N; ++i) {
                 float x[8];
                 unpack8(v[i], x);
-                for (int k = 0; k < 8; ++k) ss += (double)x[k] * (double)x[k];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    two_sum(hi, __fmul_rn(x[k], x[k]), s, e);
+                    hi = s;
+                    lo = __fadd_rn(lo, e);
+                }
             }
-            ss = row_sum<L>(ss);
-            r64 = 1.0 / sqrt(ss / (double)p.d + (double)p.eps);
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) {
+                const float h2 = __shfl_xor_sync(kAll, hi, o), l2 = __shfl_xor_sync(kAll, lo, o);
+                two_sum(hi, h2, s, e);
+                hi = s;
+                lo = __fadd_rn(__fadd_rn(lo, l2), e);
+            }
+            rr = norm_factor(hi, lo, (float)p.d, p.eps);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = lane + L * i;
             const bool in = live && c < nch;
-            double z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (in)
-                chunk64(v[i], r64, norm && p.weight ? p.weight + c * 8 : nullptr,
-                        c >= rot ? cs + (c - rot) * 4 : nullptr, z);
-            double amax = 0.0;
-            for (int j = 0; j < 8; ++j) amax = fmax(amax, fabs(z[j]));
-            amax = fmax(amax, __shfl_xor_sync(kAll, amax, 1));
-            amax = fmax(amax, __shfl_xor_sync(kAll, amax, 2));
-            amax = fmax(amax, 1e-4);
-            int k = ilogb(amax) - 2;                 // amax in [4, 8) * 2^k
-            if (amax > 6.0 * scalbn(1.0, k)) ++k;
-            uint32_t cw = 0;
-            for (int j = 0; j < 8; ++j) cw |= code_of(z[j] * scalbn(1.0, -k)) << (4 * j);
-            kexp[i] = k;
-            code[i] = cw;
+            float x[8];
+            unpack8(v[i], x);
+            if (in && (norm || c >= rot)) {
+                const float *w = norm && p.weight ? p.weight + c * 8 : nullptr;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    F2 a = times(rr, x[2 * j]), b = times(rr, x[2 * j + 1]);
+                    if (w) {
+                        a = times(a, __ldg(w + 2 * j));
+                        b = times(b, __ldg(w + 2 * j + 1));
+                    }
+                    if (c >= rot) {
+                        const float2 cj = __ldg(cs + (c - rot) * 4 + j);
+                        const F2 re = plus(times(a, cj.x), times(b, -cj.y)), im = plus(times(a, cj.y), times(b, cj.x));
+                        a = re;
+                        b = im;
+                    }
+                    x[2 * j] = one_float(a);
+                    x[2 * j + 1] = one_float(b);
+                }
+            }
+            float amax = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
+            amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 2));
+            kexp[i] = block_exp(fmaxf(amax, 1e-4f));
+            code[i] = codes8(x, pow2(-kexp[i]));
         }
     }
     if (!live) return;
@@ -281,10 +300,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
             if ((c & 3) == 0) p.exps[slot * nblk + (c >> 2)] = (int8_t)kexp[i];
         }
         if (p.y) {
-            const float sc = pow2(kexp[i]);
             float x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = code_value((code[i] >> (4 * j)) & 15u, sc);
+            values8(code[i], pow2(kexp[i]), x);
             reinterpret_cast<uint4 *>(p.y + (int64_t)tok * p.d)[c] = pack8(x);
         }
     }

@@ -41,6 +41,13 @@ __global__ void __launch_bounds__(kThreads) norm_rotary_kernel(const NormArgs p)
     const uint32_t tok = row / (uint32_t)p.h, hh = row - tok * (uint32_t)p.h;
     const uint32_t bi = tok / (uint32_t)p.s, t = tok - bi * (uint32_t)p.s;
     bool live = row < p.nrows;
+    const int nch = p.d / 8;
+    // the row, before it is known whether it counts: it is there either way
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.x + (int64_t)bi * p.x_bstride + (int64_t)t * p.x_tstride +
+                                                       (int64_t)hh * p.d);
+    uint4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = live && lane + L * i < nch ? src[lane + L * i] : make_uint4(0, 0, 0, 0);
     int64_t pos = 0;
     if (live && p.lens) live = (int)t < __ldg(p.lens + bi);
     if (live && p.rd) {
@@ -50,12 +57,6 @@ __global__ void __launch_bounds__(kThreads) norm_rotary_kernel(const NormArgs p)
             live = false;
         }
     }
-    const int nch = p.d / 8;
-    const uint4 *src = reinterpret_cast<const uint4 *>(p.x + (int64_t)bi * p.x_bstride + (int64_t)t * p.x_tstride +
-                                                       (int64_t)hh * p.d);
-    uint4 v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = live && lane + L * i < nch ? src[lane + L * i] : make_uint4(0, 0, 0, 0);
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {

@@ -58,11 +58,17 @@ __device__ __forceinline__ T row_sum(T v) {
     return v;
 }
 
-// The chunk's values times the row's factor and the weights of its columns (w: f32 [8], 4-byte aligned
-// or null).
+// The chunk's values times the row's factor and the weights of its columns (w: f32 [8], 16-byte aligned, or
+// null).
 __device__ __forceinline__ void scale8(float (&x)[8], float r, const float *__restrict__ w) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = w ? __fmul_rn(__fmul_rn(x[i], r), __ldg(w + i)) : __fmul_rn(x[i], r);
+    for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], r);
+    if (w) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(w)), b = __ldg(reinterpret_cast<const float4 *>(w) + 1);
+        const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], f[i]);
+    }
 }
 
 // Four adjacent pairs (a, b) turned by cs[j] = (cos, sin): (a c - b s, a s + b c).  Stays in f32: the
