@@ -7,7 +7,7 @@
 //     k = ceil(log2(max(amax, 1e-4) / 6)),  code_i = e2m1(z_i / 2^k), nearest, ties to the even code.
 //
 // A code is a decision, so it is made on the exact z.  The f32 value is off by less than d = 2^-20 of the
-// magnitudes it was made of: half the 15 roundings of the longest chain into the sum of squares, three of the
+// magnitudes it was made of: half the 15 roundings of the longest chain into the sum of squares, four of the
 // factor 1 / sqrt(ss / d + eps), two products, a product and a sum of the rotation, each 2^-24.  So the codes of
 // z + d and z - d are formed; where they are the same (and the block's exponent is for its maximum + d and - d)
 // they are z's, and where a border lies between them the warp goes through the formula with two floats a
@@ -28,17 +28,19 @@ struct AppendArgs {
     int64_t x_bstride, x_tstride;
     uint16_t *y;
     uint32_t ntok;
-    int s, d, rd;
+    Divisor s;
+    int d, rd;
     const float *weight;
-    float eps;                 // 0: no norm
+    float inv_d, eps;          // eps 0: no norm
     const float2 *table;
     int64_t table_rows;
     const int32_t *first, *lens;
-    int pos_step, base, window;
+    int pos_step, base;
+    Divisor window;            // d 0: none
     uint8_t *codes;
     int8_t *exps;
     int64_t pages;
-    int page;
+    Divisor page;
     const int32_t *block_table;
     int max_pages;
     unsigned int *status;
@@ -52,8 +54,8 @@ __device__ __forceinline__ int block_exp(float amax) {
 
 __device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 
-// Eight codes of z * s, the first in the lowest nibble; nearest, ties to even, saturating at 6.
-__device__ __forceinline__ uint32_t codes8(const float (&z)[8], float s) {
+// Eight codes of z, the first in the lowest nibble; nearest, ties to even, saturating at 6.
+__device__ __forceinline__ uint32_t codes8(const float (&z)[8]) {
     uint32_t r;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -62,8 +64,7 @@ __device__ __forceinline__ uint32_t codes8(const float (&z)[8], float s) {
         "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
         "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
         : "=r"(r)
-        : "f"(z[0] * s), "f"(z[1] * s), "f"(z[2] * s), "f"(z[3] * s), "f"(z[4] * s), "f"(z[5] * s), "f"(z[6] * s),
-          "f"(z[7] * s));
+        : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
     return r;
 }
 
@@ -122,7 +123,7 @@ __device__ __forceinline__ float one_float(F2 a) {
 }
 
 // 1 / sqrt((hi + lo) / d + eps): the quotient's remainder goes to the low part; then one Newton step.
-__device__ __forceinline__ F2 norm_factor(float hi, float lo, float d, float eps) {
+__device__ __forceinline__ F2 norm_factor2(float hi, float lo, float d, float eps) {
     const float q = __fdiv_rn(hi, d), ql = __fdiv_rn(__fadd_rn(fmaf(-q, d, hi), lo), d);
     float s, e;
     two_sum(q, eps, s, e);
@@ -136,7 +137,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tok = blockIdx.x * (kThreads / L) + threadIdx.x / L;
     const int lane = threadIdx.x % L;
-    const uint32_t bi = tok / (uint32_t)p.s, t = tok - bi * (uint32_t)p.s;
+    uint32_t t;
+    const uint32_t bi = p.s.div(tok, t);
     const int nch = p.d / 8, nblk = p.d / 32;
     bool live = tok < p.ntok;
     // the row, before it is known whether it counts: it is there either way
@@ -147,10 +149,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
     bool stored = false;
     int64_t pos = 0, slot = 0;
     if (live) {
-        const int len = p.lens ? min(__ldg(p.lens + bi), p.s) : p.s;
+        const int len = p.lens ? min(__ldg(p.lens + bi), (int)p.s.d) : (int)p.s.d;
         const int64_t i = (int64_t)__ldg(p.first + bi) + t;
         live = (int)t < len;
-        stored = live && (p.window == 0 || (int)t >= len - p.window);
+        stored = live && (p.window.d == 0 || (int)t >= len - (int)p.window.d);
         bool bad = false;
         if (live) {
             pos = i * p.pos_step;
@@ -160,10 +162,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
             }
         }
         if (stored) {
-            const uint32_t r = (uint32_t)p.base + (p.window ? (uint32_t)i % (uint32_t)p.window : (uint32_t)i);
-            const uint32_t pg = r / (uint32_t)p.page;
+            uint32_t r = (uint32_t)i, off;
+            if (p.window.d) p.window.div((uint32_t)i, r);
+            const uint32_t pg = p.page.div((uint32_t)p.base + r, off);
             const int id = pg < (uint32_t)p.max_pages ? __ldg(p.block_table + (int64_t)bi * p.max_pages + pg) : -1;
-            slot = (int64_t)id * p.page + (r - pg * (uint32_t)p.page);
+            slot = (int64_t)id * p.page.d + off;
             if (id < 0 || id >= p.pages) {
                 bad = true;
                 stored = false;
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
 #pragma unroll
             for (int k = 0; k < 8; ++k) ss[k & 3] = fmaf(x[k], x[k], ss[k & 3]);
         }
-        r = 1.0f / sqrtf(row_sum<L>((ss[0] + ss[1]) + (ss[2] + ss[3])) / (float)p.d + p.eps);
+        r = norm_factor(row_sum<L>((ss[0] + ss[1]) + (ss[2] + ss[3])), p.inv_d, p.eps);
     }
     const int rot = (p.d - p.rd) / 8;
     const float2 *cs = p.table + pos * (p.rd / 2);
@@ -197,8 +200,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
         float x[8];
         unpack8(v[i], x);
         if (in && norm) scale8(x, r, p.weight ? p.weight + c * 8 : nullptr);
-        float off[8];                                    // how far x may be off
         const float tol = norm || turned ? 9.53674316e-7f : 0.0f;   // 2^-20
+        float mag[4];                                    // of the pairs, where turned
         if (turned) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -206,31 +209,32 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
                 const float a = x[2 * j], b = x[2 * j + 1];
                 x[2 * j] = a * cj.x - b * cj.y;
                 x[2 * j + 1] = a * cj.y + b * cj.x;
-                off[2 * j] = off[2 * j + 1] = tol * ((fabsf(a) + fabsf(b)) * fmaxf(fabsf(cj.x), fabsf(cj.y)));
+                mag[j] = (fabsf(a) + fabsf(b)) * fmaxf(fabsf(cj.x), fabsf(cj.y));
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) off[j] = tol * x[j];      // of x's sign: minus zero stays what it is
         }
-        float amax = 0.0f, far = 0.0f;
-        float up[8], down[8];
+        float amax = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            amax = fmaxf(amax, fabsf(x[j]));
-            far = fmaxf(far, fabsf(off[j]));
-            up[j] = x[j] + off[j];
-            down[j] = x[j] - off[j];
-        }
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
+        float far = turned ? fmaxf(fmaxf(mag[0], mag[1]), fmaxf(mag[2], mag[3])) : amax;
 #pragma unroll
         for (int o = 1; o <= 2; o <<= 1) {
             amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
             far = fmaxf(far, __shfl_xor_sync(kAll, far, o));
         }
+        far *= norm || rot < nch ? 9.53674316e-7f : 0.0f;   // a quad may hold turned chunks beside others
         const int k = block_exp(fmaxf(amax + far, 1e-4f));
         const float inv = pow2(-k);
         kexp[i] = k;
-        code[i] = codes8(up, inv);
-        near |= in && tol > 0.0f && (code[i] != codes8(down, inv) || k != block_exp(fmaxf(amax - far, 1e-4f)));
+        float up[8], down[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float z = x[j] * inv;
+            const float off = turned ? tol * inv * mag[j >> 1] : tol * z;   // of z's sign: minus zero stays what it is
+            up[j] = z + off;
+            down[j] = z - off;
+        }
+        code[i] = codes8(up);
+        near |= in && (tol > 0.0f && code[i] != codes8(down) || k != block_exp(fmaxf(amax - far, 1e-4f)));
     }
     if (__any_sync(kAll, near)) {
         F2 rr = {1.0f, 0.0f};
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
                 hi = s;
                 lo = __fadd_rn(__fadd_rn(lo, l2), e);
             }
-            rr = norm_factor(hi, lo, (float)p.d, p.eps);
+            rr = norm_factor2(hi, lo, (float)p.d, p.eps);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -287,7 +291,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
             amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 2));
             kexp[i] = block_exp(fmaxf(amax, 1e-4f));
-            code[i] = codes8(x, pow2(-kexp[i]));
+            const float inv = pow2(-kexp[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= inv;
+            code[i] = codes8(x);
         }
     }
     if (!live) return;
@@ -314,9 +321,11 @@ int launch_kv_append_fp4(const uint16_t *x, int64_t x_bstride, int64_t x_tstride
                          const int32_t *first, const int32_t *lens, int pos_step, int base, int window, uint8_t *codes,
                          int8_t *exps, int64_t pages, int page, const int32_t *block_table, int max_pages,
                          unsigned int *status, cudaStream_t stream) {
-    const AppendArgs p{x, x_bstride, x_tstride, y, (uint32_t)((int64_t)b * s), s, d, rd, weight, eps,
-                       reinterpret_cast<const float2 *>(table), table_rows, first, lens, pos_step, base, window,
-                       codes, exps, pages, page, block_table, max_pages, status};
+    Divisor ring(window > 0 ? (uint32_t)window : 1u);
+    if (window == 0) ring.d = 0;
+    const AppendArgs p{x, x_bstride, x_tstride, y, (uint32_t)((int64_t)b * s), Divisor((uint32_t)s), d, rd, weight,
+                       1.0f / (float)d, eps, reinterpret_cast<const float2 *>(table), table_rows, first, lens, pos_step,
+                       base, ring, codes, exps, pages, Divisor((uint32_t)page), block_table, max_pages, status};
     for_row(d, [&](auto l, auto n) {
         constexpr int L = decltype(l)::value;
         const uint32_t per = kThreads / L;

@@ -10,7 +10,8 @@
 // Bound by HBM: 2 bytes read and 2 written a value, and the row is held in registers between the sum
 // and the product, so it is read once.  A row is 16 bytes a lane and step (coalesced), one warp for
 // d > 128 and half or a quarter of one below; table and weight rows are shared by the heads of a token
-// and come from cache.
+// and come from cache.  R rows a warp in turn, all loaded first: with many rows four (fewer instructions for
+// indexes and more bytes in flight), else one.
 #include "row_norm.cuh"
 
 namespace dsattn {
@@ -23,64 +24,80 @@ struct NormArgs {
     int64_t x_bstride, x_tstride;
     uint16_t *y;
     uint32_t nrows;
-    int s, h, d, rd;
+    Divisor s, h;
+    int d, rd;
     const float *weight;
-    float eps;
+    float inv_d, eps;
     const float2 *table;
     int64_t table_rows;
     const int32_t *first, *lens;
     unsigned int *status;
 };
 
-template <int L, int N>
+template <int L, int N, int R>
 __global__ void __launch_bounds__(kThreads) norm_rotary_kernel(const NormArgs p) {
     // a dependent launch (the attention) may be set up while this grid runs; it waits before it reads
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const uint32_t row = blockIdx.x * (kThreads / L) + threadIdx.x / L;
+    const uint32_t row0 = (blockIdx.x * (kThreads / L) + threadIdx.x / L) * R;
     const int lane = threadIdx.x % L;
-    const uint32_t tok = row / (uint32_t)p.h, hh = row - tok * (uint32_t)p.h;
-    const uint32_t bi = tok / (uint32_t)p.s, t = tok - bi * (uint32_t)p.s;
-    bool live = row < p.nrows;
+    uint32_t hh, t;
+    uint32_t bi = p.s.div(p.h.div(row0, hh), t);
     const int nch = p.d / 8;
-    // the row, before it is known whether it counts: it is there either way
-    const uint4 *src = reinterpret_cast<const uint4 *>(p.x + (int64_t)bi * p.x_bstride + (int64_t)t * p.x_tstride +
-                                                       (int64_t)hh * p.d);
-    uint4 v[N];
+    uint4 v[R][N];
+    const float2 *cs[R];       // the row's table entries; null: nothing is written
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = live && lane + L * i < nch ? src[lane + L * i] : make_uint4(0, 0, 0, 0);
-    int64_t pos = 0;
-    if (live && p.lens) live = (int)t < __ldg(p.lens + bi);
-    if (live && p.rd) {
-        pos = (int64_t)__ldg(p.first + bi) + t;
-        if (pos < 0 || pos >= p.table_rows) {
-            if (lane == 0 && hh == 0) flag_status(p.status, DS_DEV_BAD_INDEX);
-            live = false;
+    for (int q = 0; q < R; ++q) {
+        const bool there = row0 + q < p.nrows;
+        // the row, before it is known whether it counts: it is there either way
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.x + (int64_t)bi * p.x_bstride + (int64_t)t * p.x_tstride +
+                                                           (int64_t)hh * p.d);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[q][i] = there && lane + L * i < nch ? src[lane + L * i] : make_uint4(0, 0, 0, 0);
+        cs[q] = nullptr;
+        if (there && (!p.lens || (int)t < __ldg(p.lens + bi))) {
+            const int64_t pos = p.rd ? (int64_t)__ldg(p.first + bi) + t : 0;
+            if (pos >= 0 && (p.rd == 0 || pos < p.table_rows)) cs[q] = p.rd ? p.table + pos * (p.rd / 2) : reinterpret_cast<const float2 *>(p.x);
+            else if (lane == 0 && hh == 0) flag_status(p.status, DS_DEV_BAD_INDEX);
+        }
+        if (++hh == p.h.d) {
+            hh = 0;
+            if (++t == p.s.d) {
+                t = 0;
+                ++bi;
+            }
         }
     }
-    float ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float x[8];
-        unpack8(v[i], x);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) ss = fmaf(x[k], x[k], ss);
-    }
-    ss = row_sum<L>(ss);
-    if (!live) return;
-    const float r = 1.0f / sqrtf(ss / (float)p.d + p.eps);
-    uint4 *dst = reinterpret_cast<uint4 *>(p.y + (int64_t)row * p.d);
     const int rot = (p.d - p.rd) / 8;      // first rotated chunk
-    const float2 *cs = p.table + pos * (p.rd / 2);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = lane + L * i;
-        if (c >= nch) continue;
-        float x[8];
-        unpack8(v[i], x);
-        scale8(x, r, p.weight ? p.weight + c * 8 : nullptr);
-        if (c >= rot) rotate8(x, cs + (c - rot) * 4);
-        dst[c] = pack8(x);
+    for (int q = 0; q < R; ++q) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float x[8];
+            unpack8(v[q][i], x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) ss = fmaf(x[k], x[k], ss);
+        }
+        const float r = norm_factor(row_sum<L>(ss), p.inv_d, p.eps);
+        if (!cs[q]) continue;
+        uint4 *dst = reinterpret_cast<uint4 *>(p.y + (int64_t)(row0 + q) * p.d);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = lane + L * i;
+            if (c >= nch) continue;
+            float x[8];
+            unpack8(v[q][i], x);
+            scale8(x, r, p.weight ? p.weight + c * 8 : nullptr);
+            if (c >= rot) rotate8(x, cs[q] + (c - rot) * 4);
+            dst[c] = pack8(x);
+        }
     }
+}
+
+template <int L, int N, int R>
+void launch(const NormArgs &p, cudaStream_t stream) {
+    const uint32_t per = kThreads / L * R;
+    norm_rotary_kernel<L, N, R><<<(p.nrows + per - 1) / per, kThreads, 0, stream>>>(p);
 }
 
 }  // namespace
@@ -88,13 +105,13 @@ __global__ void __launch_bounds__(kThreads) norm_rotary_kernel(const NormArgs p)
 int launch_norm_rotary(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint16_t *y, int b, int s, int h, int d,
                        const float *weight, float eps, int rd, const float *table, int64_t table_rows,
                        const int32_t *first, const int32_t *lens, unsigned int *status, cudaStream_t stream) {
-    const NormArgs p{x,      x_bstride, x_tstride, y,
-                     (uint32_t)((int64_t)b * s * h), s, h, d, rd, weight, eps,
-                     reinterpret_cast<const float2 *>(table), table_rows, first, lens, status};
+    const NormArgs p{x, x_bstride, x_tstride, y, (uint32_t)((int64_t)b * s * h), Divisor((uint32_t)s), Divisor((uint32_t)h),
+                     d, rd, weight, 1.0f / (float)d, eps, reinterpret_cast<const float2 *>(table), table_rows, first, lens, status};
     for_row(d, [&](auto l, auto n) {
-        constexpr int L = decltype(l)::value;
-        const uint32_t per = kThreads / L;
-        norm_rotary_kernel<L, decltype(n)::value><<<(p.nrows + per - 1) / per, kThreads, 0, stream>>>(p);
+        constexpr int L = decltype(l)::value, N = decltype(n)::value;
+        // four rows a warp once they still fill every SM (152 x 64 warps)
+        if (N <= 2 && (int64_t)p.nrows * L / 32 >= 4 * 152 * 64) launch<L, N, N <= 2 ? 4 : 1>(p, stream);
+        else launch<L, N, 1>(p, stream);
     });
     return launch_status();
 }

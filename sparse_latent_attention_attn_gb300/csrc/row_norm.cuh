@@ -44,11 +44,28 @@ __device__ __forceinline__ void unpack8(const uint4 v, float (&x)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x[2 * i])) |
-               ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x[2 * i + 1])) << 16);
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+// n / d and n % d for n < 2^32 with m = floor((2^32 - 1) / d) from the host: the product's high word is the
+// quotient or one less.
+struct Divisor {
+    uint32_t d, m;
+    explicit Divisor(uint32_t v = 1) : d(v), m(0xffffffffu / v) {}
+    __device__ __forceinline__ uint32_t div(uint32_t n, uint32_t &rest) const {
+        uint32_t q = __umulhi(n, m);
+        rest = n - q * d;
+        if (rest >= d) {
+            rest -= d;
+            ++q;
+        }
+        return q;
+    }
+};
+
+// 1 / sqrt(ss / d + eps) from inv_d = 1 / d rounded, within 4 * 2^-24 of it.
+__device__ __forceinline__ float norm_factor(float ss, float inv_d, float eps) { return rsqrtf(fmaf(ss, inv_d, eps)); }
 
 // Sum over the L lanes of a row; every lane gets it.
 template <int L, typename T>
