@@ -989,7 +989,6 @@ struct CombineParams {
     int groups;
     bool interleave;
     const float *ws;
-    int ncut;
     int4 cut[kMaxCut];            // {unit, first part, parts, slot bits}
 };
 
@@ -1047,10 +1046,9 @@ constexpr int kMaxDev = 64;
 int g_sms[kMaxDev];
 std::mutex g_mutex;
 
-// CTAs that run at once on the current device (one per SM), 0 when the kernel cannot be configured.
-int max_ctas() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
+// CTAs that run at once on a device, the current one (one per SM), 0 when the kernel cannot be configured.
+int max_ctas(int dev) {
+    if (dev < 0 || dev >= kMaxDev) return 0;
     std::lock_guard<std::mutex> lock(g_mutex);
     if (g_sms[dev]) return g_sms[dev];
     int sms = 0;
@@ -1064,21 +1062,36 @@ struct Plan {
     int64_t ntok, nunit, G, K;
     int groups;
     bool split;
+    int ncut;
+    int4 cut[kMaxCut];
 };
 
 // Fixed cost of a unit on the cost line (q, the epilogue), in index entries.
 constexpr int kSegCost = BN;
 
-bool plan(int b, int m, int h, int topk, Plan &pl) {
-    const int gmax = max_ctas();
-    if (gmax <= 0) return false;
+// The plan of a shape on the current device; each host thread keeps its last one (a decode loop asks for the
+// same one for every layer and step).  Null when there is none.
+const Plan *plan(int b, int m, int h, int topk) {
+    thread_local Plan last;
+    thread_local int key[5] = {-1, 0, 0, 0, 0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+    if (key[0] == dev && key[1] == b && key[2] == m && key[3] == h && key[4] == topk) return &last;
+    const int gmax = max_ctas(dev);
+    if (gmax <= 0) return nullptr;
+    key[0] = -1;
+    Plan &pl = last;
     pl.ntok = (int64_t)b * m;
     pl.groups = h > HM ? 2 : 1;
     pl.nunit = pl.ntok * pl.groups;
     pl.G = split::choose_ranges(pl.nunit, topk, gmax, BN);
     pl.K = split::seg_cost(pl.nunit, pl.G, kSegCost);
+    if (pl.nunit > INT32_MAX || pl.nunit > (INT64_MAX / (pl.G + 1)) / (topk + pl.K)) return nullptr;
     pl.split = split::splits_units(pl.nunit, topk, pl.G, pl.K);
-    return true;
+    pl.ncut = pl.split ? split::cut_units(pl.nunit, topk, pl.K, pl.G, pl.cut) : 0;
+    const int k[5] = {dev, b, m, h, topk};
+    for (int i = 0; i < 5; ++i) key[i] = k[i];
+    return &last;
 }
 
 size_t workspace_bytes(const Plan &pl) { return pl.split ? (size_t)pl.G * 2 * SLOT * sizeof(float) : 0; }
@@ -1086,30 +1099,22 @@ size_t workspace_bytes(const Plan &pl) { return pl.split ? (size_t)pl.G * 2 * SL
 }  // namespace fp4
 
 size_t sparse_attn_fp4_workspace_bytes(int b, int m, int h, int topk) {
-    fp4::Plan pl;
-    if (topk == 0 || (int64_t)b * m == 0 || !fp4::plan(b, m, h, topk, pl)) return 0;
-    return fp4::workspace_bytes(pl);
+    if (topk == 0 || (int64_t)b * m == 0) return 0;
+    const fp4::Plan *pl = fp4::plan(b, m, h, topk);
+    return pl ? fp4::workspace_bytes(*pl) : 0;
 }
 
 int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream) {
-    fp4::Plan pl;
-    if (!fp4::plan(a.b, a.m, a.h, a.topk, pl)) return DS_ECUDA;
-    if (pl.nunit > INT32_MAX || pl.nunit > (INT64_MAX / (pl.G + 1)) / (a.topk + pl.K)) return DS_EUNSUPPORTED;
+    if ((int64_t)a.b * a.m > INT32_MAX / 2) return DS_EUNSUPPORTED;
+    const fp4::Plan *plan = fp4::plan(a.b, a.m, a.h, a.topk);
+    if (!plan) return DS_ECUDA;
+    const fp4::Plan &pl = *plan;
     const size_t need = fp4::workspace_bytes(pl);
     if (a.workspace_bytes < need || (need && !a.workspace)) return DS_EWORKSPACE;
+    if (pl.split && pl.ncut <= 0) return DS_EUNSUPPORTED;
     const bool rope = a.rd > 0, interleave = a.m > 1;
     fp4::Params p{a, (int)pl.ntok, (int)pl.nunit, pl.groups, (int)pl.G, (int)pl.K, interleave, a.scale * fp4::kLog2e,
                   static_cast<float *>(a.workspace), test_stall() ? 1 : 0};
-    fp4::CombineParams c;
-    if (pl.split) {
-        c.a = a;
-        c.ntok = (int)pl.ntok;
-        c.groups = pl.groups;
-        c.interleave = interleave;
-        c.ws = p.ws;
-        c.ncut = split::cut_units(pl.nunit, a.topk, pl.K, pl.G, c.cut);
-        if (c.ncut <= 0) return DS_EUNSUPPORTED;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)pl.G, 1, 1);
     cfg.blockDim = dim3(fp4::NTHREADS, 1, 1);
@@ -1125,7 +1130,14 @@ int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream) {
         cudaSuccess)
         return DS_ECUDA;
     if (pl.split) {
-        cfg.gridDim = dim3((unsigned)c.ncut, (unsigned)(a.h < fp4::HM ? a.h : fp4::HM), 1);
+        fp4::CombineParams c;
+        c.a = a;
+        c.ntok = (int)pl.ntok;
+        c.groups = pl.groups;
+        c.interleave = interleave;
+        c.ws = p.ws;
+        for (int i = 0; i < pl.ncut; ++i) c.cut[i] = pl.cut[i];
+        cfg.gridDim = dim3((unsigned)pl.ncut, (unsigned)(a.h < fp4::HM ? a.h : fp4::HM), 1);
         cfg.blockDim = dim3(128, 1, 1);
         cfg.dynamicSmemBytes = 0;
         if (cudaLaunchKernelEx(&cfg, rope ? fp4::combine_kernel<true> : fp4::combine_kernel<false>, c) != cudaSuccess)

@@ -107,8 +107,8 @@ def _check(fn: str, status: int) -> None:
 
 
 def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    # the raw handle: torch.cuda.current_stream() builds an object around it (3 us against 0.2)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -384,55 +384,39 @@ def sparse_attn_fp8kv(q: torch.Tensor, kv_codes: torch.Tensor, kv_exps: torch.Te
     return o
 
 
+# ---- the paged 4-bit row store: calls of a few microseconds, so their checks are single comparisons on the
+# ---- way in, and only a refused call goes back over them to say what is wrong
+
+_BF16, _F32, _I32, _U8, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.int8
+
+
 def _on(stream):
     """Tensors made inside belong to the stream of the call, not to the current one."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _check_rows(first: torch.Tensor, lens: torch.Tensor | None, b: int) -> None:
-    _need(first, torch.int32, "first")
-    if first.shape != (b,) or not first.is_contiguous():
-        raise ValueError("first must be a contiguous int32 [b]")
-    if lens is not None:
-        _need(lens, torch.int32, "lens")
-        if lens.shape != (b,) or not lens.is_contiguous():
-            raise ValueError("lens must be a contiguous int32 [b]")
+def _fits(t: torch.Tensor, dtype, shape: tuple, dev: int) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
 
 
-def _check_weight(weight: torch.Tensor | None, d: int) -> None:
-    if weight is not None:
-        _need(weight, torch.float32, "weight")
-        if weight.shape != (d,) or not weight.is_contiguous():
-            raise ValueError("weight must be a contiguous f32 [d]")
-
-
-def _check_rotation(rd: int, table: torch.Tensor | None) -> int:
-    """Rows of the table (0 without a rotation)."""
-    if rd == 0:
-        return 0
-    if table is None:
-        raise ValueError("rd > 0 needs a table")
-    _check_table(table, rd)
-    return table.shape[0]
-
-
-def _same_device(**tensors: torch.Tensor | None) -> None:
-    """Every tensor on the current device: the library launches there."""
-    cur = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != cur:
+def _refuse(**tensors) -> None:
+    """Raise for the first tensor (name=(tensor, dtype, shape or None)) that is not as it has to be."""
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is missing")
+        _need(t, dtype, name)
+        if t.get_device() != cur:
             raise ValueError(f"{name}: must be on the current CUDA device")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if shape is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    raise ValueError("the tensors do not fit together")
 
 
-def _check_store(codes: torch.Tensor, exps: torch.Tensor, block_table: torch.Tensor, b: int, d: int) -> None:
-    _need(codes, torch.uint8, "codes")
-    _need(exps, torch.int8, "exps")
-    _need(block_table, torch.int32, "block_table")
-    if codes.dim() != 3 or codes.shape[2] * 2 != d or exps.shape != codes.shape[:2] + (d // 32,) \
-            or not codes.is_contiguous() or not exps.is_contiguous():
-        raise ValueError("codes must be a contiguous [pages][page][d/2] and exps a contiguous [pages][page][d/32]")
-    if block_table.dim() != 2 or block_table.shape[0] != b or not block_table.is_contiguous():
-        raise ValueError("block_table must be a contiguous int32 [b][max_pages]")
+def _table_shape(rd: int, table: torch.Tensor | None) -> tuple:
+    return (table.shape[0] if table is not None and table.dim() == 3 else 0, rd // 2, 2)
 
 
 def norm_rotary(x: torch.Tensor, eps: float, rd: int, table: torch.Tensor | None, first: torch.Tensor,
@@ -442,26 +426,28 @@ def norm_rotary(x: torch.Tensor, eps: float, rd: int, table: torch.Tensor | None
     lie in a wider tensor) and the rotation of its last ``rd`` values to position ``first[b] + t``, in
     one pass.  ``y``: bf16 [b][s][h][d] contiguous (``x`` itself when laid out so); tokens at or behind
     ``lens[b]`` leave it as it was (zeros in a new one)."""
-    _need(x, torch.bfloat16, "x")
     if x.dim() != 4:
         raise ValueError("x must be [b][s][h][d]")
     b, s, h, d = x.shape
-    if x.numel() and (x.stride(3) != 1 or (h > 1 and x.stride(2) != d)):
+    xb, xt, xh, xd = x.stride()
+    dev = x.get_device()
+    tab = _table_shape(rd, table) if rd else None
+    if not (x.dtype is _BF16 and dev >= 0 and dev == torch.cuda.current_device() and _fits(first, _I32, (b,), dev)
+            and (lens is None or _fits(lens, _I32, (b,), dev)) and (weight is None or _fits(weight, _F32, (d,), dev))
+            and (rd == 0 or (table is not None and _fits(table, _F32, tab, dev)))
+            and (y is None or _fits(y, _BF16, (b, s, h, d), dev))):
+        given = {"lens": (lens, _I32, (b,)), "weight": (weight, _F32, (d,)), "y": (y, _BF16, x.shape)}
+        _refuse(x=(x, _BF16, None), first=(first, _I32, (b,)), **{k: v for k, v in given.items() if v[0] is not None},
+                **({"table": (table, _F32, tab)} if rd else {}))
+    if x.numel() and (xd != 1 or (h > 1 and xh != d)):
         raise ValueError("the heads of a token must be contiguous")
-    _check_rows(first, lens, b)
-    _check_weight(weight, d)
-    rows = _check_rotation(rd, table)
     if y is None:
         with _on(stream):
-            y = torch.empty((b, s, h, d), dtype=torch.bfloat16, device=x.device) if lens is None else \
-                torch.zeros((b, s, h, d), dtype=torch.bfloat16, device=x.device)
-    elif y.shape != x.shape or y.dtype != torch.bfloat16 or not y.is_contiguous() or not y.is_cuda:
-        raise ValueError("y must be a contiguous bf16 tensor shaped like x")
-    _same_device(x=x, y=y, first=first, lens=lens, weight=weight, table=table if rd else None)
+            y = (torch.empty if lens is None else torch.zeros)((b, s, h, d), dtype=_BF16, device=x.device)
     _check("ds_norm_rotary",
-           _lib.ds_norm_rotary(_ptr(x), x.stride(0) if b > 1 else 0, x.stride(1) if s > 1 else 0, _ptr(y), b, s, h, d,
-                               _ptr(weight), float(eps), rd, _ptr(table) if rd else None, rows, _ptr(first),
-                               _ptr(lens), _stream(stream)))
+           _lib.ds_norm_rotary(x.data_ptr(), xb if b > 1 else 0, xt if s > 1 else 0, y.data_ptr(), b, s, h, d,
+                               _ptr(weight), eps, rd, table.data_ptr() if rd else None, tab[0] if rd else 0,
+                               first.data_ptr(), _ptr(lens), _stream(stream)))
     return y
 
 
@@ -473,25 +459,31 @@ def kv_append_fp4_paged(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor
     row store ``codes [pages][page][d/2]``, ``exps [pages][page][d/32]``: row ``i = first[b] + t`` goes to
     logical row ``base + i % window`` (``window`` > 0, the last ``window`` tokens) or ``base + i``, rotated
     to position ``i * pos_step``.  ``y``: bf16 [b][s][d] contiguous, receives the stored values."""
-    _need(x, torch.bfloat16, "x")
-    if x.dim() != 3:
-        raise ValueError("x must be [b][s][d]")
+    if x.dim() != 3 or codes.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("x must be [b][s][d], codes [pages][page][d/2] and block_table [b][max_pages]")
     b, s, d = x.shape
-    if x.numel() and x.stride(2) != 1:
+    xb, xt, xd = x.stride()
+    pages, page, _ = codes.shape
+    max_pages = block_table.shape[1]
+    dev = x.get_device()
+    tab = _table_shape(rd, table) if rd else None
+    if not (x.dtype is _BF16 and dev >= 0 and dev == torch.cuda.current_device()
+            and _fits(codes, _U8, (pages, page, d // 2), dev) and _fits(exps, _I8, (pages, page, d // 32), dev)
+            and _fits(block_table, _I32, (b, max_pages), dev) and _fits(first, _I32, (b,), dev)
+            and (lens is None or _fits(lens, _I32, (b,), dev)) and (weight is None or _fits(weight, _F32, (d,), dev))
+            and (rd == 0 or (table is not None and _fits(table, _F32, tab, dev)))
+            and (y is None or _fits(y, _BF16, (b, s, d), dev))):
+        given = {"lens": (lens, _I32, (b,)), "weight": (weight, _F32, (d,)), "y": (y, _BF16, x.shape)}
+        _refuse(x=(x, _BF16, None), codes=(codes, _U8, (pages, page, d // 2)), exps=(exps, _I8, (pages, page, d // 32)),
+                block_table=(block_table, _I32, (b, max_pages)), first=(first, _I32, (b,)),
+                **{k: v for k, v in given.items() if v[0] is not None}, **({"table": (table, _F32, tab)} if rd else {}))
+    if x.numel() and xd != 1:
         raise ValueError("the values of a row must be contiguous")
-    _check_store(codes, exps, block_table, b, d)
-    _check_rows(first, lens, b)
-    _check_weight(weight, d)
-    rows = _check_rotation(rd, table)
-    if y is not None and (y.shape != x.shape or y.dtype != torch.bfloat16 or not y.is_contiguous() or not y.is_cuda):
-        raise ValueError("y must be a contiguous bf16 tensor shaped like x")
-    _same_device(x=x, codes=codes, exps=exps, block_table=block_table, first=first, lens=lens, weight=weight, y=y,
-                 table=table if rd else None)
     _check("ds_kv_append_fp4_paged",
-           _lib.ds_kv_append_fp4_paged(_ptr(x), x.stride(0) if b > 1 else 0, x.stride(1) if s > 1 else 0, _ptr(y), b,
-                                       s, d, _ptr(weight), float(eps), rd, _ptr(table) if rd else None, rows,
-                                       _ptr(first), _ptr(lens), pos_step, base, window, _ptr(codes), _ptr(exps),
-                                       codes.shape[0], codes.shape[1], _ptr(block_table), block_table.shape[1],
+           _lib.ds_kv_append_fp4_paged(x.data_ptr(), xb if b > 1 else 0, xt if s > 1 else 0, _ptr(y), b, s, d,
+                                       _ptr(weight), eps, rd, table.data_ptr() if rd else None, tab[0] if rd else 0,
+                                       first.data_ptr(), _ptr(lens), pos_step, base, window, codes.data_ptr(),
+                                       exps.data_ptr(), pages, page, block_table.data_ptr(), max_pages,
                                        _stream(stream)))
 
 
@@ -506,42 +498,42 @@ def sparse_attn_fp4_paged(q: torch.Tensor, codes: torch.Tensor, exps: torch.Tens
                           stream=None) -> torch.Tensor:
     """``sparse_attn`` over the paged 4-bit row store (``idx`` lists logical rows of each sequence); with
     ``rd`` > 0 the last ``rd`` values of token t's output are rotated back by position ``first[b] + t``."""
-    _need(q, torch.bfloat16, "q")
-    _need(sink, torch.float32, "sink")
-    _need(idx, torch.int32, "idx")
-    if q.dim() != 4 or idx.dim() != 3:
-        raise ValueError("q must be [b][m][h][d] and idx [b][m][topk]")
+    if q.dim() != 4 or idx.dim() != 3 or codes.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [b][m][h][d], idx [b][m][topk], codes [pages][page][d/2] and block_table [b][max_pages]")
     b, m, h, d = q.shape
-    topk = idx.shape[2]
-    if idx.shape[:2] != (b, m) or sink.shape != (h,):
-        raise ValueError("shape mismatch")
-    for t, name in ((q, "q"), (idx, "idx"), (sink, "sink")):
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    _check_store(codes, exps, block_table, b, d)
-    rows = _check_rotation(rd, table)
-    if rd:
-        if first is None:
-            raise ValueError("rd > 0 needs first")
-        _check_rows(first, None, b)
+    pages, page, _ = codes.shape
+    topk, max_pages = idx.shape[2], block_table.shape[1]
+    dev = q.get_device()
+    tab = _table_shape(rd, table) if rd else None
+    if not (q.dtype is _BF16 and q.is_contiguous() and dev >= 0 and dev == torch.cuda.current_device()
+            and _fits(codes, _U8, (pages, page, d // 2), dev) and _fits(exps, _I8, (pages, page, d // 32), dev)
+            and _fits(block_table, _I32, (b, max_pages), dev) and _fits(sink, _F32, (h,), dev)
+            and _fits(idx, _I32, (b, m, topk), dev) and (o is None or _fits(o, _BF16, (b, m, h, d), dev))
+            and (rd == 0 or (table is not None and _fits(table, _F32, tab, dev) and first is not None
+                             and _fits(first, _I32, (b,), dev)))
+            and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))):
+        _refuse(q=(q, _BF16, q.shape), codes=(codes, _U8, (pages, page, d // 2)), exps=(exps, _I8, (pages, page, d // 32)),
+                block_table=(block_table, _I32, (b, max_pages)), sink=(sink, _F32, (h,)), idx=(idx, _I32, (b, m, topk)),
+                **({"o": (o, _BF16, q.shape)} if o is not None else {}),
+                **({"table": (table, _F32, tab), "first": (first, _I32, (b,))} if rd else {}),
+                **({"workspace": (workspace, workspace.dtype, workspace.shape)} if workspace is not None else {}))
     if o is None:
         with _on(stream):
             o = torch.empty_like(q)
-    elif o.shape != q.shape or o.dtype != torch.bfloat16 or not o.is_contiguous() or not o.is_cuda:
-        raise ValueError("o must be a contiguous bf16 tensor shaped like q")
-    _same_device(q=q, codes=codes, exps=exps, block_table=block_table, sink=sink, idx=idx, o=o, workspace=workspace,
-                 first=first if rd else None, table=table if rd else None)
-    need = sparse_attn_fp4_paged_workspace_bytes(b, m, h, d, topk)
-    if need and workspace is None:
-        with _on(stream):
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        need = _lib.ds_sparse_attn_fp4_paged_workspace_bytes(b, m, h, d, topk)
+        if need:
+            with _on(stream):
+                workspace = torch.empty(need, dtype=_U8, device=q.device)
+            ws, ws_bytes = workspace.data_ptr(), need
     _check("ds_sparse_attn_fp4_paged",
-           _lib.ds_sparse_attn_fp4_paged(_ptr(q), _ptr(codes), _ptr(exps), codes.shape[0], codes.shape[1],
-                                         _ptr(block_table), block_table.shape[1], _ptr(sink), _ptr(idx), topk,
-                                         float(scale), _ptr(o), b, m, h, d, _ptr(workspace), ws_bytes, rd,
-                                         _ptr(table) if rd else None, rows, _ptr(first) if rd else None,
-                                         _stream(stream)))
+           _lib.ds_sparse_attn_fp4_paged(q.data_ptr(), codes.data_ptr(), exps.data_ptr(), pages, page,
+                                         block_table.data_ptr(), max_pages, sink.data_ptr(), idx.data_ptr(), topk, scale,
+                                         o.data_ptr(), b, m, h, d, ws, ws_bytes, rd, table.data_ptr() if rd else None,
+                                         tab[0] if rd else 0, first.data_ptr() if rd else None, _stream(stream)))
     return o
 
 
