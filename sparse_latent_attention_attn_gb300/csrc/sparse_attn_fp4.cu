@@ -58,6 +58,7 @@ constexpr int STAGE = NPAN * PANEL;     // 64 KB
 constexpr int NR = 4;                   // index messages
 constexpr int NSOFTW = 8, NSOFT = 32 * NSOFTW, HPW = 32;    // softmax warps; heads of one
 constexpr int W_ROWS = NSOFTW, NROWW = 8, W_MMA = W_ROWS + NROWW, W_IDX = W_MMA + 1, W_EXP = W_IDX + 1, NTHREADS = 640;
+constexpr int QROWS = 2;                             // heads of 8 that a row warp takes of the first q; a softmax warp the others
 constexpr int RPL = BN / (2 * NROWW);                // steps of two rows that a row warp takes a tile
 // of the 96 registers a thread of the launch the softmax warps take more
 constexpr uint32_t REG_SOFT = 120, REG_OTHER = 80;
@@ -88,7 +89,8 @@ enum : int {
     B_S = B_PV + 8,             // [2] MMA -> softmax, rows: scores ready
     B_SFREE = B_S + 2,          // [2] softmax -> MMA: scores read
     B_P = B_SFREE + 2,          // softmax -> MMA: P written
-    B_DRAIN = B_P + 1,
+    B_Q = B_P + 1,              // softmax -> MMA: their share of the first q written
+    B_DRAIN = B_Q + 1,
     B_COUNT = B_DRAIN + 1
 };
 constexpr int C_MSG = C_BAR + 8 * B_COUNT;      // [NR] int32 message heads
@@ -254,6 +256,50 @@ __device__ __forceinline__ int put_q(uint32_t sq, int hh, const uint4 (&v)[2], i
     return g;
 }
 
+// Token of a position in the token order (split::unit_at; the launch keeps the numbers below 2^31).
+__device__ __forceinline__ int token_at(uint32_t i, int ntok, bool interleave) {
+    return interleave ? (i & 1u ? ntok - 1 - (int)(i >> 1) : (int)(i >> 1)) : (int)i;
+}
+
+// Unit of a position in the unit order: groups of a token are neighbours, so that their gathers meet in L2.
+struct Unit {
+    int tok, h0, nh;
+};
+__device__ __forceinline__ Unit unit_of(const Params &p, uint32_t u) {
+    const int g = p.groups == 1 ? 0 : (int)(u & 1u);
+    return {token_at(p.groups == 1 ? u : u >> 1, p.ntok, p.interleave), g * HM, min(HM, p.a.h - g * HM)};
+}
+
+// Heads hh .. hh + n - 1 of a unit's q into [hi | lo], the next head in flight; lane i < n gets the scale of head
+// hh + i, 2^g |scale| log2(e), never 0 (see the scores).
+__device__ __forceinline__ float put_heads(const Params &p, uint32_t sq, uint32_t unit, int hh, int n, int lane) {
+    const Unit un = unit_of(p, unit);
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.a.q + ((int64_t)un.tok * p.a.h + un.h0 + hh) * D) + 2 * lane;
+    const uint32_t sign = p.scale_log2 < 0.0f ? 0x80000000u : 0u;
+    const int there = min(un.nh - hh, n);
+    uint4 v[2], next[2];
+    next[0] = next[1] = make_uint4(0, 0, 0, 0);
+    if (there > 0) {
+        next[0] = __ldg(src);
+        next[1] = __ldg(src + 1);
+    }
+    float qs = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        v[0] = next[0];
+        v[1] = next[1];
+        next[0] = next[1] = make_uint4(0, 0, 0, 0);
+        src += D / 8;
+        if (i + 1 < there) {
+            next[0] = __ldg(src);
+            next[1] = __ldg(src + 1);
+        }
+        const int g = put_q(sq, hh + i, v, lane, sign);
+        if (lane == i) qs = fmaxf(fabsf(p.scale_log2) * pow2(g), 1.17549435e-38f);
+    }
+    return qs;
+}
+
 // The 32 codes of a block at 2^(y - 15) in e5m2: pairs widened to f16, times the f16 number whose exponent field
 // is y (exact; y = 0 is zero), and the high bytes of the f16 values, which are e5m2 (e2m1 has one
 // mantissa bit, e5m2 two).
@@ -368,20 +414,6 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
     for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// Token of a position in the token order (split::unit_at; the launch keeps the numbers below 2^31).
-__device__ __forceinline__ int token_at(uint32_t i, int ntok, bool interleave) {
-    return interleave ? (i & 1u ? ntok - 1 - (int)(i >> 1) : (int)(i >> 1)) : (int)i;
-}
-
-// Unit of a position in the unit order: groups of a token are neighbours, so that their gathers meet in L2.
-struct Unit {
-    int tok, h0, nh;
-};
-__device__ __forceinline__ Unit unit_of(const Params &p, uint32_t u) {
-    const int g = p.groups == 1 ? 0 : (int)(u & 1u);
-    return {token_at(p.groups == 1 ? u : u >> 1, p.ntok, p.interleave), g * HM, min(HM, p.a.h - g * HM)};
-}
-
 // sin and cos of the output's rotation back, or null
 __device__ __forceinline__ const float2 *rotation_row(const Args &a, int tok, bool flag) {
     const uint32_t bi = (uint32_t)tok / (uint32_t)a.m;
@@ -449,6 +481,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             mbar_init(BAR(B_SFREE + i), NSOFTW);
         }
         mbar_init(BAR(B_P), NSOFTW);
+        mbar_init(BAR(B_Q), NSOFTW);
         mbar_init(BAR(B_DRAIN), 1);
         *abort_flag = (base & 1023u) != 0;       // the swizzled operands need this alignment
         fence_mbar_init();
@@ -548,7 +581,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
         for (int i = 0; i < 2; ++i)
             at[i] = base + SM_KV + (uint32_t)panel * PANEL + (uint32_t)(4 * w + 2 * i + half) * 128 +
                     (uint32_t)(((lane & 3) * 2 ^ (4 * (w & 1) + 2 * i + half)) * 16);
-        const uint32_t sign = p.scale_log2 < 0.0f ? 0x80000000u : 0u;
         uint32_t unit = u0;
         int msg = 0;
         uint32_t seg = 0;
@@ -583,29 +615,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 if (lane == 0) mbar_arrive(BAR(B_KV + st));
                 break;
             }
-            float qs = 0.0f;                      // lane i < 8: the scale of head 8 w + i
+            float qs = 0.0f;
             if (tile & kFirst) {
-                // q of the unit, once S of the tile before has read the last one's
+                // the unit's q, once S of the tile before has read the last one's; of the first, the softmax warps,
+                // which have nothing else to do then, take a share
                 if (J > 0 && !warp_wait(BAR(B_S + (st ^ 1u)), ((J - 1) >> 1) & 1u, abort_flag)) break;
-                const Unit un = unit_of(p, unit);
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.a.q + ((int64_t)un.tok * p.a.h + un.h0) * D) + 2 * lane;
-                uint4 v[2], nx[2];
-                auto load_q = [&](int i) {
-                    nx[0] = nx[1] = make_uint4(0, 0, 0, 0);
-                    if (i < 8 && 8 * w + i < un.nh) {
-                        nx[0] = __ldg(src + (8 * w + i) * (D / 8));
-                        nx[1] = __ldg(src + (8 * w + i) * (D / 8) + 1);
-                    }
-                };
-                load_q(0);
-#pragma unroll 1
-                for (int i = 0; i < 8; ++i) {
-                    v[0] = nx[0];
-                    v[1] = nx[1];
-                    load_q(i + 1);
-                    const int g = put_q(base + SM_Q, 8 * w + i, v, lane, sign);
-                    if (lane == i) qs = fmaxf(fabsf(p.scale_log2) * pow2(g), 1.17549435e-38f);   // never 0: see the scores
-                }
+                qs = put_heads(p, base + SM_Q, unit, 8 * w, seg == 0 ? QROWS : 8, lane);
             }
             if (!next_msg(J + 1)) break;
             const uint8_t *exps = ctl + C_EXPS + ((J % NR) * BN + first_row) * (D / 32) + u;
@@ -628,7 +643,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             if (tile & kLast) ++unit;
             if (tile & kFirst) {
                 // P V of tile J - 2 is done, so the softmax is through with the scales of two units ago
-                if (lane < 8) reinterpret_cast<float *>(ctl + C_QS)[(seg & 1u) * HM + 8 * w + lane] = qs;
+                if (lane < (seg == 0 ? QROWS : 8)) reinterpret_cast<float *>(ctl + C_QS)[(seg & 1u) * HM + 8 * w + lane] = qs;
                 ++seg;
             }
             fence_proxy_async_smem();
@@ -640,6 +655,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
         }
     } else if (warp >= W_EXP) {
         // ========================= exponents of the rows: lane = two rows =========================
+        uint32_t unit = u0;
         for (uint32_t n = 0;; ++n) {
             if (!warp_wait(BAR(B_MSG + n % NR), (n / NR) & 1u, abort_flag)) break;
             const int msg = msgs[n % NR], count = (msg & 255) == kTile ? msg >> 16 : 0;
@@ -669,6 +685,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(B_EXP + n % NR));
             if ((msg & 255) == kFin) break;
+            // the q of the next unit on its way to L2: its loads wait for nothing else when their time comes
+            if ((msg & kFirst) && (int64_t)++unit * T < e1) {
+                const Unit un = unit_of(p, unit);
+                const uint16_t *q = p.a.q + ((int64_t)un.tok * p.a.h + un.h0) * D;
+                for (int i = 32 * (warp - W_EXP) + lane; i < un.nh * (D / 64); i += 64) prefetch_l2(q + i * 64);
+            }
         }
     } else if (warp == W_MMA) {
         // ================================== MMA issue ==================================
@@ -692,7 +714,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 ++vJ;
                 idle = 0;
             } else if (!fin && sJ - vJ < 2 && done(B_KV + (sJ & 1u), sJ >> 1) &&
-                       (sJ < 2 || done(B_SFREE + (sJ & 1u), (sJ >> 1) - 1))) {
+                       (sJ < 2 || done(B_SFREE + (sJ & 1u), (sJ >> 1) - 1)) &&
+                       (sJ > 0 || done(B_Q, 0))) {
                 const uint32_t st = sJ & 1u;
                 const int msg = __shfl_sync(kAll, meta[st], 0);
                 idle = 0;
@@ -743,7 +766,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
         uint32_t unit = u0, seg = 0;
         bool bad = false;
         head[hl] = 0.0f;
+        if (e0 < e1) {
+            const float s = put_heads(p, base + SM_Q, unit, 8 * warp + QROWS, 8 - QROWS, lane);
+            if (lane < 8 - QROWS) const_cast<float *>(qs)[8 * warp + QROWS + lane] = s;
+        }
+        fence_proxy_async_smem();
         __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_Q));
+        bar_or(false);
         for (uint32_t J = 0;; ++J) {
             const uint32_t st = J & 1u;
             bad = bad || *abort_flag || !warp_wait(BAR(B_KV + st), (J >> 1) & 1u, abort_flag);
@@ -891,7 +921,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             if (lane == 0) mbar_arrive(BAR(B_P));
             if (msg & kLast) {
                 // ---- the unit's output, or this range's part of it
-                const Unit un = unit_of(p, unit);
                 const bool whole = msg & kWhole;
                 // sums over the warp's rows: lane i ends up with head hb + i
                 float s[HPW];
@@ -903,6 +932,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 fold<2>(s, lane);
                 fold<1>(s, lane);
                 sums[quarter * HM + hl] = s[0];
+                const Unit un = unit_of(p, unit);
+                ++unit;
                 bad = bad || !warp_wait(BAR(B_PV + 4 * st + 3), (J >> 1) & 1u, abort_flag);
                 tc_fence_after();
                 if (bar_or(bad)) break;
@@ -942,24 +973,36 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                         x[i + 3] = __uint_as_float(r[i + 3]) * f4.w;
                     }
                     if (whole) {
+                        // neighbouring lanes trade, so that each stores a pair of columns: the even one of head i, the
+                        // odd one of head i + 1
+                        const bool odd = lane & 1;
+                        uint32_t *col = reinterpret_cast<uint32_t *>(
+                            p.a.o + ((int64_t)un.tok * p.a.h + un.h0 + h0) * D + d + (odd ? D - 1 : 0));
+                        uint32_t w[8];
                         if (ROPE && cs && c * 128 + quarter * 32 + 31 >= D - p.a.rd) {
-                            const bool turned = d >= D - p.a.rd;
-                            float2 t = turned ? __ldg(cs + ((d - (D - p.a.rd)) >> 1)) : make_float2(1.0f, 0.0f);
-                            if (d & 1) t.y = -t.y;
+                            float2 t = make_float2(1.0f, 0.0f);
+                            if (d >= D - p.a.rd) t = __ldg(cs + ((d - (D - p.a.rd)) >> 1));
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float y = __shfl_xor_sync(kAll, x[i], 1);
-                                x[i] = turned ? x[i] * t.x + y * t.y : x[i];
+                            for (int i = 0; i < 8; ++i) {
+                                const float y = __shfl_xor_sync(kAll, odd ? x[2 * i] : x[2 * i + 1], 1);
+                                const float lo = odd ? y : x[2 * i], hi = odd ? x[2 * i + 1] : y;
+                                w[i] = pack_bf16x2(lo * t.x + hi * t.y, hi * t.x - lo * t.y);
                             }
-                        }
-                        uint16_t *col = p.a.o + ((int64_t)un.tok * p.a.h + un.h0 + h0) * D + d;
-                        if (h0 + 16 <= un.nh) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) col[i * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (h0 + i < un.nh) col[i * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[i]));
+                            for (int i = 0; i < 8; ++i) {
+                                const float y = __shfl_xor_sync(kAll, odd ? x[2 * i] : x[2 * i + 1], 1);
+                                w[i] = odd ? pack_bf16x2(y, x[2 * i + 1]) : pack_bf16x2(x[2 * i], y);
+                            }
+                        }
+                        const int heads = un.nh - h0 - (odd ? 1 : 0);
+                        if (heads >= 16) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) col[i * D] = w[i];
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (2 * i < heads) col[i * D] = w[i];
                         }
                     } else {
                         float *col = ws + h0 * D + d;
@@ -969,7 +1012,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     }
                 }
                 tc_fence_before();
-                ++unit;
             }
         }
     }
