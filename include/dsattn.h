@@ -47,7 +47,7 @@ typedef struct CUstream_st *ds_stream_t;
 
 /* Bits of the device status word (ds_device_status). */
 #define DS_DEV_TIMEOUT 1u     /* a bounded wait inside a kernel gave up; that launch's output is invalid */
-/* Every wait inside ds_sparse_attn's kernel gives up after 2 s, sets DS_DEV_TIMEOUT, drains the
+/* Every wait inside the attention kernels gives up after 2 s, sets DS_DEV_TIMEOUT, drains the
  * launch's own copies and MMAs and returns, so the context stays usable (ds_test_set_stall
  * exercises that path). */
 #define DS_DEV_BAD_INDEX 2u   /* an index >= n was seen; the entry was skipped                       */
@@ -361,10 +361,11 @@ int ds_indexer_topk(const uint16_t *q, const uint16_t *k, const float *w, int b,
  * ds_indexer_topk (offset = window) are used as they are.  17/32 byte a value.
  *
  * In the three calls below first[bi] is the position (>= 0) of the sequence's first token of this
- * call, and lens[bi], where given, how many of the s tokens it has (the others are padding:
- * nothing of them is read, and what they would write is left as it was).  A position outside the
+ * call, and lens[bi], where given, how many of the s tokens it has (the others are padding: their
+ * values do not matter, and what they would write is left as it was).  A position outside the
  * table, or a row whose page is not in the block table or not one of the pages, raises
- * DS_DEV_BAD_INDEX; what it would have written is left as it was.
+ * DS_DEV_BAD_INDEX; what it would have written is left as it was.  codes and exps may be NULL when
+ * there are no pages, and block_table when max_pages is 0.
  */
 
 /*
@@ -372,7 +373,8 @@ int ds_indexer_topk(const uint16_t *q, const uint16_t *k, const float *w, int b,
  * For row (bi, t, hh) of d values, at position first[bi] + t:
  *     z_i = x_i * w_i / sqrt(mean(x^2) + eps)        (w_i = 1 when weight is NULL)
  * then the last rd values of z, adjacent pairs (a, b), become (a c - b s, a s + b c) with
- * (c, s) = table[position][pair]; f32, rounded to bf16 once.
+ * (c, s) = table[position][pair]; f32, rounded to bf16 once.  The sum of a row's squares must be
+ * finite in f32.
  *
  * x          device bf16, row (bi, t, hh) at x + bi * x_bstride + t * x_tstride + hh * d (strides in
  *            elements, multiples of 8), 16-byte aligned: heads may lie in a wider projection
@@ -400,7 +402,8 @@ int ds_norm_rotary(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint
  *     k = ceil(log2(max(amax, 1e-4) / 6)),  code = z / 2^k to the nearest e2m1, ties to even,
  * decided on z itself and not on a rounded one: the codes are those of an evaluation in 64 bits.
  * Logical rows of one call are distinct within a sequence; pages written for different sequences
- * must be distinct too.  Rows must be finite.
+ * must be distinct too.  Rows, and with a norm the sums of their squares in f32, must be finite,
+ * and eps 0 or at least 2^-100.
  *
  * x          device bf16, row (bi, t) at x + bi * x_bstride + t * x_tstride (elements, multiples
  *            of 8), 16-byte aligned, not modified
@@ -434,7 +437,8 @@ int ds_kv_append_fp4_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstri
  * workspace  at least ds_sparse_attn_fp4_paged_workspace_bytes(b, m, h, d, topk) bytes, 256-byte
  *            aligned (may be NULL when that size is 0); its contents need no initialisation and
  *            mean nothing afterwards.  Calls that may run at the same time need one each.
- * Supported: d = 512, 1 <= h <= 128; pages * page < 2^31.  q, o, codes and exps 16-byte aligned.
+ * Supported: d = 512, 1 <= h <= 128; pages * page < 2^31, b * m < 2^30.  q, o, codes and exps
+ * 16-byte aligned.
  * Other arguments and the errors are those of ds_sparse_attn.
  */
 size_t ds_sparse_attn_fp4_paged_workspace_bytes(int b, int m, int h, int d, int topk);
@@ -454,10 +458,10 @@ int ds_device_status(ds_stream_t stream, unsigned int *bits_out);
 
 /*
  * ds_test_set_stall -- test hook for the bounded waits (no counterpart on the pages).  While `on`
- * is nonzero (process-wide, every device), each ds_sparse_attn / ds_sparse_attn_fp8kv launch has
- * its gather warps withhold the first tile's arrivals: the launch's waits run out after about
- * 2 s, it drains its own copies and MMAs, raises DS_DEV_TIMEOUT and returns with its output
- * invalid; no GPU fault is involved.  Default off; nothing in the library turns it on.
+ * is nonzero (process-wide, every device), each ds_sparse_attn / ds_sparse_attn_fp8kv /
+ * ds_sparse_attn_fp4_paged launch has its gather warps withhold the first tile's arrivals: the
+ * launch's waits run out after about 2 s, it drains its own copies and MMAs, raises DS_DEV_TIMEOUT
+ * and returns with its output invalid; no GPU fault is involved.  Default off; nothing in the library turns it on.
  */
 void ds_test_set_stall(int on);
 

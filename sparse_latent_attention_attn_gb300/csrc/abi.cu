@@ -323,6 +323,10 @@ bool strides_ok(int64_t bstride, int64_t tstride, int b, int s, int64_t row) {
 }
 
 bool pool_ok(int64_t pages, int page, int max_pages) { return pages >= 0 && page >= 1 && max_pages >= 0; }
+// a store without pages, or a table without columns, needs no memory
+bool store_there(const uint8_t *codes, const int8_t *exps, int64_t pages, const int32_t *block_table, int max_pages) {
+    return (pages == 0 || (codes && exps)) && (max_pages == 0 || block_table);
+}
 bool pool_fits(int64_t pages, int page) { return pages <= INT32_MAX / page; }
 }  // namespace
 
@@ -357,7 +361,8 @@ int ds_kv_append_fp4_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstri
     if ((int64_t)b * s == 0) return DS_OK;
     if (!x || !first || !aligned16(x) || !aligned16(y) || !aligned16(weight) || !aligned4(first) || !aligned4(lens))
         return DS_EINVAL;
-    if (!codes || !exps || !block_table || !aligned16(codes) || !aligned4(block_table)) return DS_EINVAL;
+    if (!store_there(codes, exps, pages, block_table, max_pages) || !aligned16(codes) || !aligned4(block_table))
+        return DS_EINVAL;
     if (!strides_ok(x_bstride, x_tstride, b, s, d)) return DS_EINVAL;
     unsigned int *status = status_word();
     if (!status) return DS_ECUDA;
@@ -379,10 +384,10 @@ int ds_sparse_attn_fp4_paged(const uint16_t *q, const uint8_t *codes, const int8
     const Range range("ds_sparse_attn_fp4_paged");
     if (b < 0 || m < 0 || topk < 0 || h < 1 || !pool_ok(pages, page, max_pages)) return DS_EINVAL;
     if (!rotation_ok(rd, d, table, table_rows)) return DS_EINVAL;
-    if (d != 512 || h > 128 || !pool_fits(pages, page)) return DS_EUNSUPPORTED;
+    if (d != 512 || h > 128 || !pool_fits(pages, page) || !sparse_attn_fp4_fits(b, m, topk)) return DS_EUNSUPPORTED;
     if ((int64_t)b * m == 0) return DS_OK;
     if (!q || !o || !sink || (rd > 0 && !first)) return DS_EINVAL;
-    if (topk > 0 && (!idx || !codes || !exps || !block_table)) return DS_EINVAL;
+    if (topk > 0 && (!idx || !store_there(codes, exps, pages, block_table, max_pages))) return DS_EINVAL;
     if (!aligned16(q) || !aligned16(o) || !aligned16(codes) || !aligned16(exps)) return DS_EINVAL;
     if (!aligned4(sink) || !aligned4(idx) || !aligned4(block_table) || !aligned4(first)) return DS_EINVAL;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -1111,6 +1111,13 @@ struct Plan {
 // Fixed cost of a unit on the cost line (q, the epilogue), in index entries.
 constexpr int kSegCost = BN;
 
+// The units (two a token at most) in 32 bits, and every place on the cost line in 64: at most 1023 ranges' worth of
+// all the units' entries.
+bool fits(int b, int m, int topk) {
+    const int64_t ntok = (int64_t)b * m;
+    return ntok <= INT32_MAX / 2 && ntok <= (INT64_MAX >> 11) / ((int64_t)topk + kSegCost);
+}
+
 // The plan of a shape on the current device; each host thread keeps its last one (a decode loop asks for the
 // same one for every layer and step).  Null when there is none.
 const Plan *plan(int b, int m, int h, int topk) {
@@ -1120,7 +1127,7 @@ const Plan *plan(int b, int m, int h, int topk) {
     if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
     if (key[0] == dev && key[1] == b && key[2] == m && key[3] == h && key[4] == topk) return &last;
     const int gmax = max_ctas(dev);
-    if (gmax <= 0) return nullptr;
+    if (gmax <= 0 || !fits(b, m, topk)) return nullptr;
     key[0] = -1;
     Plan &pl = last;
     pl.ntok = (int64_t)b * m;
@@ -1128,7 +1135,6 @@ const Plan *plan(int b, int m, int h, int topk) {
     pl.nunit = pl.ntok * pl.groups;
     pl.G = split::choose_ranges(pl.nunit, topk, gmax, BN);
     pl.K = split::seg_cost(pl.nunit, pl.G, kSegCost);
-    if (pl.nunit > INT32_MAX || pl.nunit > (INT64_MAX / (pl.G + 1)) / (topk + pl.K)) return nullptr;
     pl.split = split::splits_units(pl.nunit, topk, pl.G, pl.K);
     pl.ncut = pl.split ? split::cut_units(pl.nunit, topk, pl.K, pl.G, pl.cut) : 0;
     const int k[5] = {dev, b, m, h, topk};
@@ -1140,6 +1146,8 @@ size_t workspace_bytes(const Plan &pl) { return pl.split ? (size_t)pl.G * 2 * SL
 
 }  // namespace fp4
 
+bool sparse_attn_fp4_fits(int b, int m, int topk) { return fp4::fits(b, m, topk); }
+
 size_t sparse_attn_fp4_workspace_bytes(int b, int m, int h, int topk) {
     if (topk == 0 || (int64_t)b * m == 0) return 0;
     const fp4::Plan *pl = fp4::plan(b, m, h, topk);
@@ -1147,7 +1155,6 @@ size_t sparse_attn_fp4_workspace_bytes(int b, int m, int h, int topk) {
 }
 
 int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream) {
-    if ((int64_t)a.b * a.m > INT32_MAX / 2) return DS_EUNSUPPORTED;
     const fp4::Plan *plan = fp4::plan(a.b, a.m, a.h, a.topk);
     if (!plan) return DS_ECUDA;
     const fp4::Plan &pl = *plan;

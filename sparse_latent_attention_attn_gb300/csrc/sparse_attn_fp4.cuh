@@ -32,6 +32,8 @@ struct Args {
 
 }  // namespace fp4
 
+// whether the shape's work can be numbered
+bool sparse_attn_fp4_fits(int b, int m, int topk);
 size_t sparse_attn_fp4_workspace_bytes(int b, int m, int h, int topk);
 int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream);
 

@@ -567,6 +567,220 @@ def test_step_together_and_in_a_graph(ds):
     assert ds.device_status() == 0
 
 
+# ---- the edges of what the documentation allows ---------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("b,s,h,d,rd", [(19, 33, 64, 512, 64), (31, 57, 89, 40, 16), (23, 45, 76, 128, 128),
+                                        (3, 21000, 1, 512, 512)])
+def test_norm_rotary_many_rows(ds, b, s, h, d, rd):
+    """Batches long enough for several rows a warp (rows of one warp then belong to different tokens and
+    sequences): against the formula, and the same as one sequence at a time."""
+    g = torch.Generator().manual_seed(d)
+    wide = torch.randn((b, s, h * d + 8), generator=g).to(torch.bfloat16)
+    w = torch.randn((d,), generator=g)
+    first = torch.randint(0, 100, (b,), generator=g, dtype=torch.int32)
+    lens = torch.randint(0, s + 1, (b,), generator=g, dtype=torch.int32)
+    lens[0], lens[-1] = s + 5, -3                          # more than there are: all of them; fewer than none: none
+    tab = table_of(100 + s, rd)
+    xg, fg, wg, lg, tg = dev(wide, first, w, lens, tab)
+    xg = xg[..., : h * d].unflatten(-1, (h, d))
+    y = torch.full((b, s, h, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    ds.norm_rotary(xg, 1e-5, rd, tg, fg, weight=wg, lens=lg, y=y)
+    one = torch.full_like(y, 7.0)
+    step = max(1, 20000 // h)                              # short enough for one row a warp
+    for i in range(b):
+        for t in range(0, s, step):
+            n = min(step, s - t)
+            o = one[i, t:t + n][None].clone()
+            ds.norm_rotary(xg[i:i + 1, t:t + n], 1e-5, rd, tg, fg[i:i + 1] + t, weight=wg, lens=lg[i:i + 1] - t, y=o)
+            one[i, t:t + n] = o[0]
+    assert ds.device_status() == 0
+    assert torch.equal(y, one)
+    assert (y[-1] == 7).all() and (y[0] != 7).any(-1).all()
+    for i in np.random.RandomState(1).choice(b - 1, min(b - 1, 3), replace=False):
+        n = min(max(int(lens[i]), 0), s, 2000)
+        z = normed(f64(wide[i, :n, : h * d].unflatten(-1, (h, d))), f64(w), 1e-5)
+        mag = pair_sum(np.abs(z), rd)
+        z = rotate(z, f64(tab)[int(first[i]) + np.arange(n)][:, None])
+        assert (np.abs(f64(y[i, :n]) - z) <= 2.0 ** -8 * np.abs(z) + 2.0 ** -20 * mag).all()
+
+
+@gpu
+def test_append_signs_of_zero(ds):
+    """Minus zero stays minus zero in its code, with and without norm and rotation by nothing."""
+    x = torch.randn((1, 6, 64), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    x[0, :, ::3] = -0.0
+    x[0, :, 1::3] = 0.0
+    x[0, 5] = -0.0
+    codes = torch.zeros((6, 1, 32), dtype=torch.uint8)
+    exps = torch.zeros((6, 1, 2), dtype=torch.int8)
+    bt = torch.arange(6, dtype=torch.int32)[None]
+    for eps in (0.0, 1e-6):
+        want = append_reference(x, None, eps, 0, None, ints(0), None, 1, 0, 0, codes, exps, bt, torch.zeros_like(x))
+        cg, eg, btg, fg = dev(codes, exps, bt, ints(0))
+        ds.kv_append_fp4_paged(x.cuda(), cg, eg, btg, fg, eps=eps)
+        np.testing.assert_array_equal(eg.cpu().numpy(), want[1])
+        np.testing.assert_array_equal(cg.cpu().numpy(), want[0])
+
+
+@gpu
+def test_append_lengths_and_last_positions(ds):
+    """Lengths below none and above all, rows at the largest number, and the position after it."""
+    x = torch.randn((4, 3, 32), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    codes = torch.full((4, 8, 16), 9, dtype=torch.uint8, device="cuda")
+    exps = torch.full((4, 8, 1), 99, dtype=torch.int8, device="cuda")
+    bt = torch.arange(4, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    last = 2 ** 31 - 1
+    y = torch.full_like(x, 5.0).cuda()
+    ds.kv_append_fp4_paged(x.cuda(), codes, exps, bt, ints(0, 0, last, last - 1).cuda(), window=8, y=y,
+                           lens=ints(-1, 7, 1, 3).cuda())
+    assert ds.device_status() == ds.DS_DEV_BAD_INDEX       # sequence 3 has a third token
+    want = [[], [0, 1, 2], [7], [6, 7]]
+    for i in range(4):
+        assert [r for r in range(8) if bool((exps[i, r] != 99).all())] == want[i]
+    assert (y != 5.0).any(-1).cpu().tolist() == [[False] * 3, [True] * 3, [True, False, False], [True, True, False]]
+
+
+@gpu
+def test_store_without_pages(ds):
+    """No pages at all, and a table without columns: every row is without a page."""
+    q, codes, exps, bt, sink, idx, *_ = attention_inputs(17, 2, 2, 70, 50, 30, 0.5, 16, 0)
+    x = torch.randn((2, 3, 512)).to(torch.bfloat16).cuda()
+    qg, cg, eg, btg, sg, ig = dev(q, codes, exps, bt, sink, idx)
+    for c, e, t in ((cg[:0], eg[:0], btg), (cg, eg, btg[:, :0].contiguous()), (cg[:0], eg[:0], btg[:, :0].contiguous())):
+        o = ds.sparse_attn_fp4_paged(qg, c, e, t, sg, ig, 0.1)
+        assert ds.device_status() == ds.DS_DEV_BAD_INDEX and (o == 0).all()
+        assert (ds.sparse_attn_fp4_paged(qg, c, e, t, sg, torch.full_like(ig, -1), 0.1) == 0).all()
+        assert ds.device_status() == 0
+        y = torch.zeros_like(x)
+        ds.kv_append_fp4_paged(x, c, e, t, ints(0, 0).cuda(), y=y)
+        assert ds.device_status() == ds.DS_DEV_BAD_INDEX and (y != 0).any(-1).all()
+    assert torch.equal(cg.cpu(), codes) and torch.equal(eg.cpu(), exps)
+
+
+@gpu
+@pytest.mark.parametrize("scale", [0.0, -0.05, 3e-5])
+def test_attention_scales(ds, scale):
+    q, codes, exps, bt, sink, idx, rd, first, tab = attention_inputs(19, 2, 2, 70, 300, 200, 0.1, 16, 64)
+    check_attention(ds, q, codes, exps, bt, sink, idx, rd, first, tab, scale=scale)
+
+
+@gpu
+@pytest.mark.parametrize("topk", [1, 32, 127, 128, 129, 255, 256, 257, 512])
+def test_attention_lengths_around_a_tile(ds, topk):
+    """Rows that leave every count of a last tile, in units of a range of their own and in shared ones."""
+    for b, m, h in ((1, 1, 64), (160, 1, 3), (2, 3, 128)):
+        x = attention_inputs(topk + b, b, m, h, 600, topk, 0.0, 16, 64)
+        check_attention(ds, *x, sample=12)
+
+
+@gpu
+def test_attention_and_append_in_a_large_pool(ds):
+    """Pages whose codes lie more than 2^31 and 2^32 bytes into the pool."""
+    page, d = 64, 512
+    pages = 2 ** 32 // (page * d // 2) + 40                   # 4.3 GB of codes
+    q, codes, exps, bt, sink, idx, rd, first, tab = attention_inputs(21, 2, 1, 64, 8 * page, 300, 0.1, page, 64)
+    n = codes.shape[0]
+    where = torch.tensor([0, 3, pages // 2 - 5, pages // 2 + 7] + list(range(pages - n + 4, pages)))
+    big = torch.zeros((pages, page, d // 2), dtype=torch.uint8, device="cuda")
+    bige = torch.zeros((pages, page, d // 32), dtype=torch.int8, device="cuda")
+    for i, j in enumerate(where.tolist()):
+        big[j], bige[j] = codes[i].cuda(), exps[i].cuda()
+    far = where[bt.long()].to(torch.int32)
+    o = check_attention(ds, q, codes, exps, bt, sink, idx, rd, first, tab)
+    got = ds.sparse_attn_fp4_paged(*dev(q), big, bige, *dev(far, sink, idx), d ** -0.5, rd=rd, table=tab.cuda(),
+                                   first=first.cuda())
+    assert torch.equal(got, o)
+    x = torch.randn((2, 70, d)).to(torch.bfloat16).cuda()
+    small, smalle = dev(codes, exps)
+    for c, e, t in ((small, smalle, bt), (big, bige, far)):
+        ds.kv_append_fp4_paged(x, c, e, t.cuda(), ints(5, 400).cuda(), rd=0, eps=1e-6)
+    assert ds.device_status() == 0
+    for i, j in enumerate(where.tolist()):
+        assert torch.equal(big[j], small[i]) and torch.equal(bige[j], smalle[i])
+
+
+@gpu
+def test_attention_calls_at_once_and_captured(ds):
+    """Two calls at once on streams of their own, then two graphs replayed at once and over again, each with
+    its workspace: the same as one after the other."""
+    shapes = ((4, 1, 128, 700), (1, 1, 16, 2300))             # both cut units, and need a workspace
+    x = [attention_inputs(23 + b, b, m, h, 3000, topk, 0.1, 64, 64) for b, m, h, topk in shapes]
+    want = [check_attention(ds, *v, sample=2) for v in x]
+    args = [dev(*v[:6]) + [512 ** -0.5] for v in x]
+    more = [dict(rd=v[6], first=v[7].cuda(), table=v[8].cuda()) for v in x]
+    for k, (b, m, h, topk) in enumerate(shapes):
+        need = ds.sparse_attn_fp4_paged_workspace_bytes(b, m, h, 512, topk)
+        assert need > 0
+        more[k]["workspace"] = torch.empty(need, dtype=torch.uint8, device="cuda")
+        more[k]["o"] = torch.empty_like(want[k])
+    streams = [torch.cuda.Stream() for _ in x]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for k, st in enumerate(streams):
+            more[k]["o"].zero_()
+        torch.cuda.synchronize()
+        for k, st in enumerate(streams):
+            ds.sparse_attn_fp4_paged(*args[k], **more[k], stream=st)
+        torch.cuda.synchronize()
+        assert all(torch.equal(more[k]["o"], want[k]) for k in range(2))
+    # without a workspace given, and on a stream given by a context
+    for k, st in enumerate(streams):
+        own = {n: v for n, v in more[k].items() if n not in ("o", "workspace")}
+        with torch.cuda.stream(st):
+            a = ds.sparse_attn_fp4_paged(*args[k], **own)
+        b = ds.sparse_attn_fp4_paged(*args[k], **own, stream=st)
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[k]) and torch.equal(b, want[k])
+    graphs, outs = [], []
+    for k in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        own = {n: v for n, v in more[k].items() if n != ("o" if k else "workspace")}
+        with torch.cuda.graph(graphs[k]):
+            outs.append(ds.sparse_attn_fp4_paged(*args[k], **own))
+    for _ in range(5):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                graphs[k].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(outs[k], want[k]) for k in range(2))
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+    assert ds.device_status() == 0
+
+
+@gpu
+def test_attention_workspace_refused(ds):
+    b, m, h, topk = 4, 1, 64, 700
+    q, codes, exps, bt, sink, idx, *_ = attention_inputs(29, b, m, h, 1000, topk, 0.0, 64, 0)
+    args = dev(q, codes, exps, bt, sink, idx)
+    need = ds.sparse_attn_fp4_paged_workspace_bytes(b, m, h, 512, topk)
+    ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+    o = torch.full_like(args[0], 3.0)
+    for bad in (ws[:need - 1], ws[16:16 + need], ws[:0]):
+        with pytest.raises(ds.DsError):
+            ds.sparse_attn_fp4_paged(*args, 0.1, o=o, workspace=bad)
+    assert ds.device_status() == 0 and (o == 3).all()
+
+
+@gpu
+@pytest.mark.parametrize("b,h,topk", [(4, 64, 700), (4, 128, 700), (1, 5, 1), (200, 64, 300)])
+def test_attention_wait_that_runs_out(ds, b, h, topk):
+    """With the hook on, the row warps withhold the first tile: the call ends, says so, and the next is clean."""
+    x = attention_inputs(31 + b, b, 1, h, 2000, topk, 0.0, 64, 64)
+    args, more = dev(*x[:6]) + [512 ** -0.5], dict(rd=x[6], first=x[7].cuda(), table=x[8].cuda())
+    assert ds.device_status() == 0
+    ds.test_set_stall(True)
+    try:
+        ds.sparse_attn_fp4_paged(*args, **more)
+        bits = ds.device_status()
+    finally:
+        ds.test_set_stall(False)
+    assert bits == ds.DS_DEV_TIMEOUT
+    check_attention(ds, *x, sample=4)
+
+
 # ---- refusals, no GPU needed ---------------------------------------------------------------------------------
 
 @pytest.fixture(scope="module")
@@ -634,6 +848,16 @@ def test_attention_refusals(lib):
     assert call(f, base, b=0, q=None, o=None, sink=None) == 0
     w = lib.ds_sparse_attn_fp4_paged_workspace_bytes
     assert w(1, 1, 4, 256, 8) == 0 and w(1, 1, 129, 512, 8) == 0 and w(-1, 1, 4, 512, 8) == 0
+
+
+def test_refusals_of_work_that_cannot_be_numbered_and_of_missing_stores(lib):
+    base = dict(q=FAKE, codes=FAKE, exps=FAKE, pages=4, page=16, bt=FAKE, mp=1, sink=FAKE, idx=FAKE, topk=4, scale=0.1,
+                o=FAKE, b=1, m=1, h=4, d=512, ws=None, wsb=0, rd=0, table=None, rows=0, first=None, stream=None)
+    f = lib.ds_sparse_attn_fp4_paged
+    assert call(f, base, b=1 << 15, m=1 << 15) == -2
+    assert call(f, base, b=1 << 14, m=1 << 15, topk=(1 << 31) - 1) == -2
+    assert call(f, base, pages=0, bt=None) == -1 and call(f, base, mp=0, codes=None) == -1
+    assert lib.ds_sparse_attn_fp4_paged_workspace_bytes(1 << 15, 1 << 15, 4, 512, 8) == 0
 
 
 def test_bindings_refuse_cpu_tensors_and_shapes(lib):
