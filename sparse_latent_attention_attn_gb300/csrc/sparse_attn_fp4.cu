@@ -85,8 +85,8 @@ enum : int {
     B_EXP = B_MSG + NR,         // [NR] exponents -> rows: message and exponents written
     B_MSGFREE = B_EXP + NR,     // [NR] rows -> index
     B_KV = B_MSGFREE + NR,      // [2] rows -> MMA, softmax: stage and its meta written (and q, at a unit's first tile)
-    B_PV = B_KV + 2,            // [2][4] MMA -> rows, softmax: P V of the tile's rows 32 k .. done
-    B_S = B_PV + 8,             // [2] MMA -> softmax, rows: scores ready
+    B_PV = B_KV + 2,            // [2][2] MMA -> rows, softmax: P V of the tile's rows 64 k .. done
+    B_S = B_PV + 4,             // [2] MMA -> softmax, rows: scores ready
     B_SFREE = B_S + 2,          // [2] softmax -> MMA: scores read
     B_P = B_SFREE + 2,          // softmax -> MMA: P written
     B_Q = B_P + 1,              // softmax -> MMA: their share of the first q written
@@ -436,21 +436,19 @@ __device__ __forceinline__ void issue_s(uint32_t rows, uint32_t q, uint32_t d) {
     }
 }
 
-// O^T += C^T P: panel c's 128 columns as M (one 128-byte atom), 32 rows a step (four groups of eight, 1024
-// bytes apart); P the same with its 64 heads as N, hi then lo.  Rows outermost: each step's rows are handed
-// back (bar) as soon as its four panels are multiplied.
+// Half of O^T += C^T P, two steps of 32 rows: panel c's 128 columns as M (one 128-byte atom), a step's rows as K (four
+// groups of eight, 1024 bytes apart); P the same with its 64 heads as N, hi then lo.
 template <uint32_t I_HI, uint32_t I_LO>
-__device__ __forceinline__ void issue_pv(uint32_t rows, uint32_t pr, uint32_t d, uint32_t keep, uint32_t bar) {
+__device__ __forceinline__ void issue_pv(uint32_t rows, uint32_t pr, uint32_t d, uint32_t keep) {
     const uint64_t a = smem_desc_sw128(rows, PANEL, 1024), b = smem_desc_sw128(pr, P_BYTES, 1024);
 #pragma unroll
-    for (int k = 0; k < BN / 32; ++k) {
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int c = 0; c < NPAN; ++c) {
             const uint64_t ao = a + (uint64_t)((c * PANEL + k * 4096) >> 4), bo = b + (uint64_t)((k * 4096) >> 4);
             mma_f8(d + c * HM, ao, bo, I_HI, k ? 1u : keep);
             mma_f8(d + c * HM, ao, bo + (64 >> 4), I_LO, 1u);
         }
-        mma_commit(bar + 8 * k);
     }
 }
 
@@ -476,7 +474,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(BAR(B_KV + i), NROWW);
-            for (int k = 0; k < 4; ++k) mbar_init(BAR(B_PV + 4 * i + k), 1);
+            for (int k = 0; k < 2; ++k) mbar_init(BAR(B_PV + 2 * i + k), 1);
             mbar_init(BAR(B_S + i), 1);
             mbar_init(BAR(B_SFREE + i), NSOFTW);
         }
@@ -609,7 +607,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             const int tile = msg;
             const uint32_t st = J & 1u;
             if ((tile & 255) == kFin) {
-                if (J >= 2 && !warp_wait(BAR(B_PV + 4 * st + 3), ((J >> 1) - 1) & 1u, abort_flag)) break;
+                if (J >= 2 && !warp_wait(BAR(B_PV + 2 * st + 1), ((J >> 1) - 1) & 1u, abort_flag)) break;
                 if (warp == W_ROWS && lane == 0) meta[st] = tile;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(B_KV + st));
@@ -627,7 +625,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
 #pragma unroll
             for (int i = 0; i < RPL; ++i) {
                 // handed back by halves: each wait costs about as much as a step
-                if (J >= 2 && (i & 3) == 0) ok = ok && warp_wait(BAR(B_PV + 4 * st + (i >> 1) + 1), ((J >> 1) - 1) & 1u, abort_flag);
+                if (J >= 2 && (i & 3) == 0) ok = ok && warp_wait(BAR(B_PV + 2 * st + (i >> 2)), ((J >> 1) - 1) & 1u, abort_flag);
                 uint32_t o[8];
                 widen(raw[i], exps[(32 * (i >> 1) + 2 * (i & 1)) * (D / 32)], o);
                 load(J + 1, i);                   // in flight until its turn
@@ -698,24 +696,14 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
         constexpr uint32_t I_S = idesc8(BN, 2 * HM, 1, 0, false);
         constexpr uint32_t I_HI = idesc8(128, HM, 1, 0, true), I_LO = idesc8(128, HM, 1, 1, true, true);
         auto done = [&](int bar, uint32_t phase) -> bool { return __all_sync(kAll, mbar_test_wait(BAR(bar), phase & 1u)); };
-        uint32_t sJ = 0, vJ = 0;           // next tile of S and of P V
+        uint32_t sJ = 0, vJ = 0, vk = 0;   // next tile of S and of P V, and its next half
         bool fin = false;                  // no more tiles
         uint32_t keep = 0;                 // bit J & 1: tile J adds to O^T (is not its unit's first)
         uint32_t idle = 0;
         uint64_t since = 0;
         while (!fin || vJ < sJ) {
-            if (vJ < sJ && done(B_P, vJ)) {
-                const uint32_t st = vJ & 1u;
-                tc_fence_after();
-                if (elect_one())
-                    issue_pv<I_HI, I_LO>(base + SM_KV + st * STAGE, base + SM_P, tmem + TM_O, (keep >> st) & 1u,
-                                         BAR(B_PV + 4 * st));
-                __syncwarp();
-                ++vJ;
-                idle = 0;
-            } else if (!fin && sJ - vJ < 2 && done(B_KV + (sJ & 1u), sJ >> 1) &&
-                       (sJ < 2 || done(B_SFREE + (sJ & 1u), (sJ >> 1) - 1)) &&
-                       (sJ > 0 || done(B_Q, 0))) {
+            if (!fin && sJ - vJ < 2 && done(B_KV + (sJ & 1u), sJ >> 1) &&
+                (sJ < 2 || done(B_SFREE + (sJ & 1u), (sJ >> 1) - 1)) && (sJ > 0 || done(B_Q, 0))) {
                 const uint32_t st = sJ & 1u;
                 const int msg = __shfl_sync(kAll, meta[st], 0);
                 idle = 0;
@@ -731,6 +719,20 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 __syncwarp();
                 keep = (keep & ~(1u << st)) | ((msg & kFirst ? 0u : 1u) << st);
                 ++sJ;
+            } else if (vJ < sJ && (vk > 0 || done(B_P, vJ))) {
+                // by halves, the rows of each handed back behind it: S of the next tile, for which the softmax waits,
+                // goes in between when it can
+                const uint32_t st = vJ & 1u;
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_pv<I_HI, I_LO>(base + SM_KV + st * STAGE + vk * 8192, base + SM_P + vk * 8192, tmem + TM_O,
+                                         vk ? 1u : (keep >> st) & 1u);
+                    mma_commit(BAR(B_PV + 2 * st + vk));
+                }
+                __syncwarp();
+                vJ += vk;
+                vk ^= 1u;
+                idle = 0;
             } else {
                 // nothing to issue: sleep on the likelier of the two for up to 100 ns
                 if (vJ < sJ) try_hint<100>(BAR(B_P), vJ & 1u);
@@ -871,7 +873,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     for (int i = 0; i < HPW / 2; ++i) l[i] = 0;
                 } else {
                     // this warp's part of O^T, and its sums, follow m and E
-                    bad = !warp_wait(BAR(B_PV + 4 * (st ^ 1u) + 3), ((J - 1) >> 1) & 1u, abort_flag);
+                    bad = !warp_wait(BAR(B_PV + 2 * (st ^ 1u) + 1), ((J - 1) >> 1) & 1u, abort_flag);
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 2 * NPAN && !bad; ++c) {
@@ -908,7 +910,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 }
             }
             // P is free once the tile before has been multiplied
-            if (J > 0 && !bad) bad = !warp_wait(BAR(B_PV + 4 * (st ^ 1u) + 3), ((J - 1) >> 1) & 1u, abort_flag);
+            if (J > 0 && !bad) bad = !warp_wait(BAR(B_PV + 2 * (st ^ 1u) + 1), ((J - 1) >> 1) & 1u, abort_flag);
             const uint32_t pb = base + SM_P + (uint32_t)row * 128;
             const uint32_t c0 = (uint32_t)((hb >> 4) ^ (row & 7)) * 16;     // its 16-byte column; hb / 16 is even
             st_shared_v4(pb + c0, hi[0], hi[1], hi[2], hi[3]);
@@ -934,7 +936,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 sums[quarter * HM + hl] = s[0];
                 const Unit un = unit_of(p, unit);
                 ++unit;
-                bad = bad || !warp_wait(BAR(B_PV + 4 * st + 3), (J >> 1) & 1u, abort_flag);
+                bad = bad || !warp_wait(BAR(B_PV + 2 * st + 1), (J >> 1) & 1u, abort_flag);
                 tc_fence_after();
                 if (bar_or(bad)) break;
                 float *ws = p.ws + ((size_t)cid * 2 + (msg & kSlot0 ? 0 : 1)) * SLOT;
