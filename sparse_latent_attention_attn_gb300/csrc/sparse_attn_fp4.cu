@@ -1026,7 +1026,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
     }
 }
 
-// Merge the partials of the units that a range boundary cuts: block (cut unit, head), thread = four columns.
+// Merge the partials of the units that a range boundary cuts: block (cut unit, four heads), warp = head.  A lane
+// has the first four parts' accumulators in flight before their weights are known.
+constexpr int kCombineHeads = 4;
 struct CombineParams {
     Args a;
     int ntok;
@@ -1037,22 +1039,35 @@ struct CombineParams {
 };
 
 template <bool ROPE>
-__global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(32 * kCombineHeads) combine_kernel(const CombineParams p) {
     grid_dependency_wait();
     const int4 c = p.cut[blockIdx.x];
     const int tok = token_at((uint32_t)(p.groups == 1 ? c.x : c.x >> 1), p.ntok, p.interleave);
-    const int h0 = p.groups == 1 ? 0 : (c.x & 1) * HM, hh = blockIdx.y;
-    if (h0 + hh >= p.a.h) return;
+    const int h0 = p.groups == 1 ? 0 : (c.x & 1) * HM, hh = blockIdx.y * kCombineHeads + (threadIdx.x >> 5);
+    if (hh >= HM || h0 + hh >= p.a.h) return;
     auto part = [&](int i) { return p.ws + ((size_t)(c.y + i) * 2 + (((uint32_t)c.w >> i) & 1u)) * SLOT; };
-    // lane i of each warp: part i (at most 32)
+    // lane i: statistics of part i (at most 32), and columns 128 j + 4 i .. of every part
     const int lane = threadIdx.x & 31;
     float m = -INFINITY, l = 0.0f;
     if (lane < c.z) {
         m = part(lane)[SLOT_O + hh];
         l = part(lane)[SLOT_O + HM + hh];
     }
+    float4 x[4][4];
+    auto load = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (i + k >= c.z) break;
+            const float4 *src = reinterpret_cast<const float4 *>(part(i + k) + hh * D) + lane;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[k][j] = src[32 * j];
+        }
+    };
+    load(0);
     const float top = warp_max(m);
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float4 acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (top != -INFINITY) {
         const float w = m == -INFINITY ? 0.0f : exp2f(m - top);
         float den = w * l;
@@ -1060,28 +1075,40 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
         for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kAll, den, o);
         den += exp2f(__ldg(p.a.sink + h0 + hh) * kLog2e - top);
         const float inv = 1.0f / den;
-        for (int i = 0; i < c.z; ++i) {
-            const float wi = __shfl_sync(kAll, w, i);
-            if (wi == 0.0f) continue;              // a part without rows has no accumulator
-            const float4 x = reinterpret_cast<const float4 *>(part(i) + hh * D)[threadIdx.x];
-            acc.x += wi * x.x;
-            acc.y += wi * x.y;
-            acc.z += wi * x.z;
-            acc.w += wi * x.w;
+        for (int i = 0;;) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (i + k >= c.z) break;
+                const float wi = __shfl_sync(kAll, w, i + k);
+                if (wi == 0.0f) continue;          // a part without rows has no accumulator
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    acc[j].x += wi * x[k][j].x;
+                    acc[j].y += wi * x[k][j].y;
+                    acc[j].z += wi * x[k][j].z;
+                    acc[j].w += wi * x[k][j].w;
+                }
+            }
+            i += 4;
+            if (i >= c.z) break;
+            load(i);
         }
-        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
     }
-    const int d = threadIdx.x * 4;
-    if constexpr (ROPE) {
-        const float2 *cs = rotation_row(p.a, tok, threadIdx.x == 0 && hh == 0);
+    const float2 *cs = nullptr;
+    if constexpr (ROPE) cs = rotation_row(p.a, tok, lane == 0 && hh == 0);
+    uint16_t *o = p.a.o + ((int64_t)tok * p.a.h + h0 + hh) * D;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int d = 128 * j + 4 * lane;
         if (cs && d >= D - p.a.rd) {
             const float2 t0 = __ldg(cs + ((d - (D - p.a.rd)) >> 1)), t1 = __ldg(cs + ((d - (D - p.a.rd)) >> 1) + 1);
-            acc = make_float4(acc.x * t0.x + acc.y * t0.y, acc.y * t0.x - acc.x * t0.y, acc.z * t1.x + acc.w * t1.y,
-                              acc.w * t1.x - acc.z * t1.y);
+            acc[j] = make_float4(acc[j].x * t0.x + acc[j].y * t0.y, acc[j].y * t0.x - acc[j].x * t0.y,
+                                 acc[j].z * t1.x + acc[j].w * t1.y, acc[j].w * t1.x - acc[j].z * t1.y);
         }
+        *reinterpret_cast<uint2 *>(o + d) = make_uint2(pack_bf16x2(acc[j].x, acc[j].y), pack_bf16x2(acc[j].z, acc[j].w));
     }
-    *reinterpret_cast<uint2 *>(p.a.o + ((int64_t)tok * p.a.h + h0 + hh) * D + d) =
-        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
 }
 
 // ---- host side ---------------------------------------------------------------------------------------
@@ -1188,8 +1215,9 @@ int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream) {
         c.interleave = interleave;
         c.ws = p.ws;
         for (int i = 0; i < pl.ncut; ++i) c.cut[i] = pl.cut[i];
-        cfg.gridDim = dim3((unsigned)pl.ncut, (unsigned)(a.h < fp4::HM ? a.h : fp4::HM), 1);
-        cfg.blockDim = dim3(128, 1, 1);
+        const int heads = a.h < fp4::HM ? a.h : fp4::HM;
+        cfg.gridDim = dim3((unsigned)pl.ncut, (unsigned)((heads + fp4::kCombineHeads - 1) / fp4::kCombineHeads), 1);
+        cfg.blockDim = dim3(32 * fp4::kCombineHeads, 1, 1);
         cfg.dynamicSmemBytes = 0;
         if (cudaLaunchKernelEx(&cfg, rope ? fp4::combine_kernel<true> : fp4::combine_kernel<false>, c) != cudaSuccess)
             return DS_ECUDA;
