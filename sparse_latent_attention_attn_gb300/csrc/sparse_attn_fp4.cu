@@ -209,17 +209,24 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// 32 times what e4m3 values h leave of x0 and x1 (exact in f32), in e4m3
-__device__ __forceinline__ uint32_t e4m3x2_rest(uint32_t h, float x0, float x1) {
-    float r0, r1;
-    asm("{\n\t.reg .b32 f;\n\t.reg .b16 f0, f1;\n\t"
-        "cvt.rn.f16x2.e4m3x2 f, %2;\n\t"
-        "mov.b32 {f0, f1}, f;\n\t"
-        "sub.rn.f32.f16 %0, f0, %3;\n\t"
-        "sub.rn.f32.f16 %1, f1, %4;\n\t}"
-        : "=f"(r0), "=f"(r1)
-        : "h"((uint16_t)h), "f"(x0), "f"(x1));
-    return e4m3x2(r0 * -32.0f, r1 * -32.0f);
+// A pair of bf16 values times f (a power of two, as a bf16 pair; their products are below 256) as hi + 2^-5 lo, both
+// e4m3 to nearest.  As f16 the products are exact, but for multiples of 2^-24 below 2^-17.
+__device__ __forceinline__ void split_q(uint32_t w, uint32_t f, uint32_t &hi, uint32_t &lo) {
+    uint16_t h, l;
+    asm("{\n\t.reg .b32 y, a, b, x, r;\n\t"
+        "mul.rn.bf16x2 y, %2, %3;\n\t"
+        "shl.b32 a, y, 16;\n\t"
+        "and.b32 b, y, 0xffff0000;\n\t"
+        "cvt.rn.f16x2.f32 x, b, a;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 %0, x;\n\t"
+        "cvt.rn.f16x2.e4m3x2 r, %0;\n\t"
+        "sub.rn.f16x2 r, x, r;\n\t"
+        "mul.rn.f16x2 r, r, %4;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 %1, r;\n\t}"
+        : "=&h"(h), "=&h"(l)
+        : "r"(w), "r"(f), "r"(0x50005000u));     // 32, twice
+    hi = h;
+    lo = l;
 }
 
 // 16 bytes of the cache that no L1 line is kept for: beside 220 KB of shared memory L1 has 28 KB, less than the
@@ -235,18 +242,17 @@ __device__ __forceinline__ uint4 ld_row(const void *ptr) {
 // One head of q (16 values a lane; sign: its sign bit is flipped) into [hi | lo]; returns g.
 __device__ __forceinline__ int put_q(uint32_t sq, int hh, const uint4 (&v)[2], int lane, uint32_t sign) {
     const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-    uint32_t top = 0;
+    uint32_t top2 = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-    top = __reduce_max_sync(kAll, top);
+    for (int k = 0; k < 8; ++k) top2 = __vmaxu2(top2, w[k] & 0x7fff7fffu);
+    const uint32_t top = __reduce_max_sync(kAll, max(top2 & 0xffffu, top2 >> 16));
     const int g = max((int)(top >> 7) - 127 - 7, -126);      // the largest value lies in [128, 256) 2^g
-    const float down = __uint_as_float(((uint32_t)(127 - g) << 23) | sign);
+    const uint32_t down = (((uint32_t)(127 - g) << 7) | sign) * 0x10001u;
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const float x0 = bf16_lo(w[k]) * down, x1 = bf16_hi(w[k]) * down;
-        const uint32_t h2 = e4m3x2(x0, x1);
-        const uint32_t l2 = e4m3x2_rest(h2, x0, x1);
+        uint32_t h2, l2;
+        split_q(w[k], down, h2, l2);
         hi[k >> 1] = k & 1 ? hi[k >> 1] | (h2 << 16) : h2;
         lo[k >> 1] = k & 1 ? lo[k >> 1] | (l2 << 16) : l2;
     }
@@ -270,32 +276,37 @@ __device__ __forceinline__ Unit unit_of(const Params &p, uint32_t u) {
     return {token_at(p.groups == 1 ? u : u >> 1, p.ntok, p.interleave), g * HM, min(HM, p.a.h - g * HM)};
 }
 
-// Heads hh .. hh + n - 1 of a unit's q into [hi | lo], the next head in flight; lane i < n gets the scale of head
-// hh + i, 2^g |scale| log2(e), never 0 (see the scores).
-__device__ __forceinline__ float put_heads(const Params &p, uint32_t sq, uint32_t unit, int hh, int n, int lane) {
+// Heads hh .. hh + n - 1 of a unit's q into [hi | lo], the next two heads in flight; lane i < n gets the scale of head
+// hh + i, 2^g |scale| log2(e), never 0 (see the scores).  ready(), between the first loads and the first store, says
+// whether to go on.
+template <typename F>
+__device__ __forceinline__ float put_heads(const Params &p, uint32_t sq, uint32_t unit, int hh, int n, int lane, F ready) {
     const Unit un = unit_of(p, unit);
     const uint4 *src = reinterpret_cast<const uint4 *>(p.a.q + ((int64_t)un.tok * p.a.h + un.h0 + hh) * D) + 2 * lane;
-    const uint32_t sign = p.scale_log2 < 0.0f ? 0x80000000u : 0u;
+    const uint32_t sign = p.scale_log2 < 0.0f ? 0x8000u : 0u;
     const int there = min(un.nh - hh, n);
-    uint4 v[2], next[2];
-    next[0] = next[1] = make_uint4(0, 0, 0, 0);
-    if (there > 0) {
-        next[0] = __ldg(src);
-        next[1] = __ldg(src + 1);
-    }
+    uint4 v[3][2];
+    auto load = [&](uint4 (&to)[2], int i) {
+        to[0] = to[1] = make_uint4(0, 0, 0, 0);
+        if (i < there) {
+            to[0] = __ldg(src + i * (D / 8));
+            to[1] = __ldg(src + i * (D / 8) + 1);
+        }
+    };
+    load(v[0], 0);
+    load(v[1], 1);
     float qs = 0.0f;
+    if (!ready()) return qs;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-        v[0] = next[0];
-        v[1] = next[1];
-        next[0] = next[1] = make_uint4(0, 0, 0, 0);
-        src += D / 8;
-        if (i + 1 < there) {
-            next[0] = __ldg(src);
-            next[1] = __ldg(src + 1);
-        }
-        const int g = put_q(sq, hh + i, v, lane, sign);
+        load(v[2], i + 2);
+        const int g = put_q(sq, hh + i, v[0], lane, sign);
         if (lane == i) qs = fmaxf(fabsf(p.scale_log2) * pow2(g), 1.17549435e-38f);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            v[0][k] = v[1][k];
+            v[1][k] = v[2][k];
+        }
     }
     return qs;
 }
@@ -617,8 +628,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             if (tile & kFirst) {
                 // the unit's q, once S of the tile before has read the last one's; of the first, the softmax warps,
                 // which have nothing else to do then, take a share
-                if (J > 0 && !warp_wait(BAR(B_S + (st ^ 1u)), ((J - 1) >> 1) & 1u, abort_flag)) break;
-                qs = put_heads(p, base + SM_Q, unit, 8 * w, seg == 0 ? QROWS : 8, lane);
+                qs = put_heads(p, base + SM_Q, unit, 8 * w, seg == 0 ? QROWS : 8, lane, [&]() -> bool {
+                    return ok = J == 0 || warp_wait(BAR(B_S + (st ^ 1u)), ((J - 1) >> 1) & 1u, abort_flag);
+                });
+                if (!ok) break;
             }
             if (!next_msg(J + 1)) break;
             const uint8_t *exps = ctl + C_EXPS + ((J % NR) * BN + first_row) * (D / 32) + u;
@@ -769,7 +782,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
         bool bad = false;
         head[hl] = 0.0f;
         if (e0 < e1) {
-            const float s = put_heads(p, base + SM_Q, unit, 8 * warp + QROWS, 8 - QROWS, lane);
+            const float s = put_heads(p, base + SM_Q, unit, 8 * warp + QROWS, 8 - QROWS, lane, [] { return true; });
             if (lane < 8 - QROWS) const_cast<float *>(qs)[8 * warp + QROWS + lane] = s;
         }
         fence_proxy_async_smem();
