@@ -949,6 +949,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 sums[quarter * HM + hl] = s[0];
                 const Unit un = unit_of(p, unit);
                 ++unit;
+                // what the output needs from memory, fetched while P V of the last tile runs
+                float sink = 0.0f;
+                const float2 *cs = nullptr;
+                if (whole) {
+                    if (hl < un.nh) sink = __ldg(p.a.sink + un.h0 + hl) * kLog2e;
+                    if constexpr (ROPE) cs = rotation_row(p.a, un.tok, threadIdx.x == 0);
+                }
                 bad = bad || !warp_wait(BAR(B_PV + 2 * st + 1), (J >> 1) & 1u, abort_flag);
                 tc_fence_after();
                 if (bar_or(bad)) break;
@@ -958,7 +965,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 const float unfold = pow2(E - 16);
                 float f = unfold;                          // of head hl
                 if (whole) {
-                    const float sink = hl < un.nh ? __ldg(p.a.sink + un.h0 + hl) * kLog2e : 0.0f;
                     f = any ? unfold / (sum + exp2f(sink - m)) : 0.0f;
                 } else if (quarter == 0) {
                     ws[SLOT_O + hl] = any ? m : -INFINITY;
@@ -968,9 +974,6 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 fac[hl] = f;                               // the same from every quarter
                 head[hl] = 0.0f;
                 __syncwarp();
-                const float2 *cs = nullptr;
-                if constexpr (ROPE)
-                    if (whole) cs = rotation_row(p.a, un.tok, threadIdx.x == 0);
 #pragma unroll 1
                 for (int k = 0; k < 2 * NPAN; ++k) {
                     const int c = k >> 1, h0 = hb + (k & 1) * 16, d = c * 128 + row;
@@ -982,10 +985,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
                         const float4 f4 = lds4(fac + h0 + i);
-                        x[i] = __uint_as_float(r[i]) * f4.x;
-                        x[i + 1] = __uint_as_float(r[i + 1]) * f4.y;
-                        x[i + 2] = __uint_as_float(r[i + 2]) * f4.z;
-                        x[i + 3] = __uint_as_float(r[i + 3]) * f4.w;
+                        unpair(mul2(pair(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), pair(f4.x, f4.y)), x[i], x[i + 1]);
+                        unpair(mul2(pair(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), pair(f4.z, f4.w)), x[i + 2],
+                               x[i + 3]);
                     }
                     if (whole) {
                         // neighbouring lanes trade, so that each stores a pair of columns: the even one of head i, the
@@ -1006,8 +1008,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                         } else {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float y = __shfl_xor_sync(kAll, odd ? x[2 * i] : x[2 * i + 1], 1);
-                                w[i] = odd ? pack_bf16x2(y, x[2 * i + 1]) : pack_bf16x2(x[2 * i], y);
+                                const uint32_t two = pack_bf16x2(x[2 * i], x[2 * i + 1]);     // the two heads
+                                w[i] = prmt(two, __shfl_xor_sync(kAll, two, 1), odd ? 0x3276u : 0x5410u);
                             }
                         }
                         const int heads = un.nh - h0 - (odd ? 1 : 0);
