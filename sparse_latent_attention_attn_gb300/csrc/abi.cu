@@ -5,6 +5,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "paged_rows.cuh"
 #include "sparse_attn_fp4.cuh"
 #include "sparse_attn_ot.cuh"
 
@@ -401,7 +402,10 @@ int ds_sparse_attn_fp4_paged(const uint16_t *q, const uint8_t *codes, const int8
     return launch_sparse_attn_fp4(a, st);
 }
 
-void ds_test_set_stall(int on) { set_test_stall(on != 0); }
+void ds_test_set_stall(int on) {
+    set_test_stall(on != 0);
+    set_test_stall_fp4(on != 0);
+}
 
 int ds_sparse_attn_launches(int b, int m, int h, int d, int topk, int *kernel, size_t *workspace_bytes) {
     if (b < 0 || m < 0 || h < 1 || h > 128 || topk < 0 || !supported_head_dim(d)) return DS_EINVAL;

@@ -50,15 +50,6 @@ int launch_apply_rotary(uint16_t *x, int64_t rows, int row_len, int rd, int64_t 
                         int64_t positions_per_seq, int64_t start_pos, const float *table, bool inverse,
                         cudaStream_t stream);
 
-int launch_norm_rotary(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint16_t *y, int b, int s, int h, int d,
-                       const float *weight, float eps, int rd, const float *table, int64_t table_rows,
-                       const int32_t *first, const int32_t *lens, unsigned int *status, cudaStream_t stream);
-int launch_kv_append_fp4(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint16_t *y, int b, int s, int d,
-                         const float *weight, float eps, int rd, const float *table, int64_t table_rows,
-                         const int32_t *first, const int32_t *lens, int pos_step, int base, int window, uint8_t *codes,
-                         int8_t *exps, int64_t pages, int page, const int32_t *block_table, int max_pages,
-                         unsigned int *status, cudaStream_t stream);
-
 struct AttnArgs {
     const uint16_t *q;
     const uint16_t *kv;
@@ -102,7 +93,6 @@ struct IndexerArgs {
 int launch_indexer_scores(const IndexerArgs &a, float *scores, int64_t ld, cudaStream_t stream);
 int launch_indexer_select(const float *scores, int64_t ld, const IndexerArgs &a, int32_t *idx, cudaStream_t stream);
 void set_test_stall(bool on);
-bool test_stall();
 size_t sparse_attn_tc_workspace_bytes(int b, int m, int h, int d, int topk, bool pair = false);
 int pair_union_cap(int topk);
 int launch_pair_union(const int32_t *idx, int b, int m, int topk, int64_t n, int32_t *uidx, unsigned int *status,

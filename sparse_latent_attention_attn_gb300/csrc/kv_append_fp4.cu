@@ -16,6 +16,8 @@
 // Bound by HBM (2 bytes read, 17/32 written a value, 2 more with y) and at decode sizes by latency: one
 // row a warp (half or a quarter for short rows), 16 bytes a lane and step; a block's maximum is two
 // shuffles over its four lanes, and a warp stores 128 contiguous bytes of codes.
+#include "f32x2.cuh"
+#include "paged_rows.cuh"
 #include "row_norm.cuh"
 
 namespace dsattn {
@@ -54,8 +56,18 @@ __device__ __forceinline__ int block_exp(float amax) {
 
 __device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 
+// The eight values of a chunk in four pairs.
+__device__ __forceinline__ void unpack_pairs(const uint4 v, uint64_t (&x)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = pair(bf16_lo(w[j]), bf16_hi(w[j]));
+}
+
 // Eight codes of z, the first in the lowest nibble; nearest, ties to even, saturating at 6.
-__device__ __forceinline__ uint32_t codes8(const float (&z)[8]) {
+__device__ __forceinline__ uint32_t codes8(const uint64_t (&zz)[4]) {
+    float z[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unpair(zz[j], z[2 * j], z[2 * j + 1]);
     uint32_t r;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -132,8 +144,10 @@ __device__ __forceinline__ F2 norm_factor2(float hi, float lo, float d, float ep
     return {r, __fmul_rn(r, -0.5f * fmaf(e, t, fmaf(s, te, fmaf(s, t, -1.0f))))};
 }
 
+// 64 registers, so that four blocks run on an SM (8 x 4096 rows of 512: 28.7 us; with three of 72, 33.3; with
+// five of 48, 30.8); rows above 512 take 86 registers
 template <int L, int N>
-__global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArgs p) {
+__global__ void __launch_bounds__(kThreads, N <= 2 ? 4 : 2) kv_append_fp4_kernel(const AppendArgs p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tok = blockIdx.x * (kThreads / L) + threadIdx.x / L;
     const int lane = threadIdx.x % L;
@@ -178,18 +192,21 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
     const bool norm = p.eps > 0.0f;
     float r = 1.0f;
     if (norm) {
-        float ss[4] = {0.0f, 0.0f, 0.0f, 0.0f};          // squares of bf16 values are exact in f32
+        uint64_t ss[2] = {0, 0};                         // squares of bf16 values are exact in f32
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float x[8];
-            unpack8(v[i], x);
+            uint64_t x[4];
+            unpack_pairs(v[i], x);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) ss[k & 3] = fmaf(x[k], x[k], ss[k & 3]);
+            for (int j = 0; j < 4; ++j) ss[j & 1] = fma2(x[j], x[j], ss[j & 1]);
         }
-        r = norm_factor(row_sum<L>((ss[0] + ss[1]) + (ss[2] + ss[3])), p.inv_d, p.eps);
+        float a, b;
+        unpair(add2(ss[0], ss[1]), a, b);
+        r = norm_factor(row_sum<L>(a + b), p.inv_d, p.eps);
     }
     const int rot = (p.d - p.rd) / 8;
     const float2 *cs = p.table + pos * (p.rd / 2);
+    constexpr float kTol = 9.53674316e-7f;               // 2^-20
     uint32_t code[N];
     int kexp[N];
     bool near = false;
@@ -197,44 +214,71 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
     for (int i = 0; i < N; ++i) {
         const int c = lane + L * i;
         const bool in = live && c < nch, turned = in && c >= rot;
-        float x[8];
-        unpack8(v[i], x);
-        if (in && norm) scale8(x, r, p.weight ? p.weight + c * 8 : nullptr);
-        const float tol = norm || turned ? 9.53674316e-7f : 0.0f;   // 2^-20
-        float mag[4];                                    // of the pairs, where turned
-        if (turned) {
+        uint64_t x[4];
+        unpack_pairs(v[i], x);
+        if (norm) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = mul2(x[j], pair(r, r));
+            if (p.weight && in) {
+                const float4 a = __ldg(reinterpret_cast<const float4 *>(p.weight + c * 8));
+                const float4 b = __ldg(reinterpret_cast<const float4 *>(p.weight + c * 8) + 1);
+                x[0] = mul2(x[0], pair(a.x, a.y));
+                x[1] = mul2(x[1], pair(a.z, a.w));
+                x[2] = mul2(x[2], pair(b.x, b.y));
+                x[3] = mul2(x[3], pair(b.z, b.w));
+            }
+        }
+        const bool any_turned = __any_sync(kAll, turned);
+        float mag[4] = {0.0f, 0.0f, 0.0f, 0.0f};         // of the pairs, where turned
+        if (any_turned && turned) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 cj = __ldg(cs + (c - rot) * 4 + j);
-                const float a = x[2 * j], b = x[2 * j + 1];
-                x[2 * j] = a * cj.x - b * cj.y;
-                x[2 * j + 1] = a * cj.y + b * cj.x;
+                float a, b;
+                unpair(x[j], a, b);
+                x[j] = pair(a * cj.x - b * cj.y, a * cj.y + b * cj.x);
                 mag[j] = (fabsf(a) + fabsf(b)) * fmaxf(fabsf(cj.x), fabsf(cj.y));
             }
         }
         float amax = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            unpair(x[j], a, b);
+            amax = max3(amax, fabsf(a), fabsf(b));
+        }
         float far = turned ? fmaxf(fmaxf(mag[0], mag[1]), fmaxf(mag[2], mag[3])) : amax;
 #pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) {
-            amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
-            far = fmaxf(far, __shfl_xor_sync(kAll, far, o));
+        for (int o = 1; o <= 2; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
+        if (any_turned) {                                // a quad may hold turned chunks beside others
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1) far = fmaxf(far, __shfl_xor_sync(kAll, far, o));
+        } else {
+            far = amax;
         }
-        far *= norm || rot < nch ? 9.53674316e-7f : 0.0f;   // a quad may hold turned chunks beside others
+        far *= norm || any_turned ? kTol : 0.0f;
         const int k = block_exp(fmaxf(amax + far, 1e-4f));
         const float inv = pow2(-k);
         kexp[i] = k;
-        float up[8], down[8];
+        // z (1 +- 2^-20): of z's sign, so that minus zero stays what it is
+        const float more = inv * (1.0f + kTol), less = inv * (1.0f - kTol);
+        uint64_t up[4], down[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float z = x[j] * inv;
-            const float off = turned ? tol * inv * mag[j >> 1] : tol * z;   // of z's sign: minus zero stays what it is
-            up[j] = z + off;
-            down[j] = z - off;
+        for (int j = 0; j < 4; ++j) {
+            up[j] = mul2(x[j], norm ? pair(more, more) : pair(inv, inv));
+            down[j] = mul2(x[j], pair(less, less));
+        }
+        if (any_turned && turned) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float off = kTol * inv * mag[j];
+                up[j] = fma2(x[j], pair(inv, inv), pair(off, off));
+                down[j] = fma2(x[j], pair(inv, inv), pair(-off, -off));
+            }
         }
         code[i] = codes8(up);
-        near |= in && (tol > 0.0f && code[i] != codes8(down) || k != block_exp(fmaxf(amax - far, 1e-4f)));
+        if (norm || any_turned)
+            near |= in && ((norm || turned) && code[i] != codes8(down) || k != block_exp(fmaxf(amax - far, 1e-4f)));
     }
     if (__any_sync(kAll, near)) {
         F2 rr = {1.0f, 0.0f};
@@ -292,9 +336,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const AppendArg
             amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 2));
             kexp[i] = block_exp(fmaxf(amax, 1e-4f));
             const float inv = pow2(-kexp[i]);
+            uint64_t z[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] *= inv;
-            code[i] = codes8(x);
+            for (int j = 0; j < 4; ++j) z[j] = pair(x[2 * j] * inv, x[2 * j + 1] * inv);
+            code[i] = codes8(z);
         }
     }
     if (!live) return;

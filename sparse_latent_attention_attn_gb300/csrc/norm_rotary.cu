@@ -12,6 +12,7 @@
 // d > 128 and half or a quarter of one below; table and weight rows are shared by the heads of a token
 // and come from cache.  R rows a warp in turn, all loaded first: with many rows four (fewer instructions for
 // indexes and more bytes in flight), else one.
+#include "paged_rows.cuh"
 #include "row_norm.cuh"
 
 namespace dsattn {

@@ -39,6 +39,7 @@
 
 #include "attn_split.cuh"
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "ptx.cuh"
 #include "sparse_attn_fp4.cuh"
 
@@ -338,34 +339,6 @@ __device__ __forceinline__ void widen(const uint4 raw, uint32_t y, uint32_t (&o)
 // Four bytes of max(k, low) - low + lift (signed k and low, biased to unsigned so that no byte borrows).
 __device__ __forceinline__ uint32_t above(uint32_t k, uint32_t low, uint32_t lift) {
     return (__vmaxs4(k, low) ^ 0x80808080u) - (low ^ 0x80808080u) + lift;
-}
-
-// Two f32 in a register pair, and the packed operations on them: half the instructions.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
 }
 
 // Four probabilities as hi (e4m3) - lo (e5m2): lo from hi - p, which is exact in f32.
@@ -1130,6 +1103,7 @@ __global__ void __launch_bounds__(32 * kCombineHeads) combine_kernel(const Combi
 
 constexpr int kMaxDev = 64;
 int g_sms[kMaxDev];
+std::atomic<int> g_test_stall{0};
 std::mutex g_mutex;
 
 // CTAs that run at once on a device, the current one (one per SM), 0 when the kernel cannot be configured.
@@ -1152,8 +1126,9 @@ struct Plan {
     int4 cut[kMaxCut];
 };
 
-// Fixed cost of a unit on the cost line (q, the epilogue), in index entries.
-constexpr int kSegCost = BN;
+// Fixed cost of a unit on the cost line (q, the epilogue), in index entries: two tiles' worth (256 tokens of 128 heads and
+// 2176 entries: 216 us; with one tile's worth 219, with one and a half 219; 4096 tokens of 640 entries: 519 either way).
+constexpr int kSegCost = 2 * BN;
 
 // The units (two a token at most) in 32 bits, and every place on the cost line in 64: at most 1023 ranges' worth of
 // all the units' entries.
@@ -1190,6 +1165,8 @@ size_t workspace_bytes(const Plan &pl) { return pl.split ? (size_t)pl.G * 2 * SL
 
 }  // namespace fp4
 
+void set_test_stall_fp4(bool on) { fp4::g_test_stall.store(on ? 1 : 0, std::memory_order_relaxed); }
+
 bool sparse_attn_fp4_fits(int b, int m, int topk) { return fp4::fits(b, m, topk); }
 
 size_t sparse_attn_fp4_workspace_bytes(int b, int m, int h, int topk) {
@@ -1207,7 +1184,7 @@ int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream) {
     if (pl.split && pl.ncut <= 0) return DS_EUNSUPPORTED;
     const bool rope = a.rd > 0, interleave = a.m > 1;
     fp4::Params p{a, (int)pl.ntok, (int)pl.nunit, pl.groups, (int)pl.G, (int)pl.K, interleave, a.scale * fp4::kLog2e,
-                  static_cast<float *>(a.workspace), test_stall() ? 1 : 0};
+                  static_cast<float *>(a.workspace), fp4::g_test_stall.load(std::memory_order_relaxed)};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)pl.G, 1, 1);
     cfg.blockDim = dim3(fp4::NTHREADS, 1, 1);

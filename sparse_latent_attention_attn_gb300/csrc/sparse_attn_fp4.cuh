@@ -35,6 +35,7 @@ struct Args {
 // whether the shape's work can be numbered
 bool sparse_attn_fp4_fits(int b, int m, int topk);
 size_t sparse_attn_fp4_workspace_bytes(int b, int m, int h, int topk);
+void set_test_stall_fp4(bool on);
 int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream);
 
 }  // namespace dsattn

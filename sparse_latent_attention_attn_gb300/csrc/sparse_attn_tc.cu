@@ -1553,7 +1553,6 @@ size_t sparse_attn_tc_workspace_bytes(int b, int m, int h, int d, int topk, bool
     return need;
 }
 
-bool test_stall() { return tc::g_test_stall.load(std::memory_order_relaxed) != 0; }
 void set_test_stall(bool on) { tc::g_test_stall.store(on ? 1 : 0, std::memory_order_relaxed); }
 
 namespace {
