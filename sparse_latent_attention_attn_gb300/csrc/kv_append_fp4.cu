@@ -13,9 +13,13 @@
 // they are z's, and where a border lies between them the warp goes through the formula with two floats a
 // number (to about 2^-44): two rows of 512 in a thousand.  Rows that are neither normalised nor rotated are exact in f32 (d = 0).
 //
-// Bound by HBM (2 bytes read, 17/32 written a value, 2 more with y) and at decode sizes by latency: one
-// row a warp (half or a quarter for short rows), 16 bytes a lane and step; a block's maximum is two
-// shuffles over its four lanes, and a warp stores 128 contiguous bytes of codes.
+// HBM has 2 bytes read and 17/32 written a value, 2 more with y; what bounds long batches is the integer pipe
+// (0.69 of its rate: conversions, byte permutes, maxima, exponents), decode sizes latency.  One row a warp (half
+// or a quarter for short rows), 16 bytes a lane and step; a block's maximum is two shuffles over its four lanes,
+// and a warp stores 128 contiguous bytes of codes.  Several rows a warp with the next one's loads ahead took as
+// long or longer (four 31.5 us, two 38.2), for their registers.
+// Measured: 8 x 4096 rows of 512 with y, 28.7 us (650 instructions a row; its bytes alone 12.4 us); 256 rows into
+// rings 4.3 us on the device.
 #include "f32x2.cuh"
 #include "paged_rows.cuh"
 #include "row_norm.cuh"

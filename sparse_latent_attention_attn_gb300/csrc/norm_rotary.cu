@@ -12,6 +12,8 @@
 // d > 128 and half or a quarter of one below; table and weight rows are shared by the heads of a token
 // and come from cache.  R rows a warp in turn, all loaded first: with many rows four (fewer instructions for
 // indexes and more bytes in flight), else one.
+// Measured: 4096 tokens of 64 heads of 512, 91 us, 5.9 TB/s (0.87 of a copy's rate; 95.6 us with one row a warp);
+// 64 tokens of 64 heads 2.9 us on the device, where four rows a warp would leave half of the SMs idle.
 #include "paged_rows.cuh"
 #include "row_norm.cuh"
 

@@ -23,17 +23,25 @@
 // Why so.  A tile is 128 rows of 512 bytes, so two tiles, q (64 KB as hi and lo) and P fit the 227 KB of an
 // SM; as bf16 only tiles of 64 rows would, and a 64-row tcgen05.mma takes the time of a 128-row one.  With
 // N = 128 in S and K = 32 a step a tile takes 16 + 32 instructions where bf16 rows would take 64 + 64.  The
-// widening to e5m2 is a table of 8 bytes per block: byte permutes with the code words as selectors.
+// widening to e5m2 goes through f16: a conversion and a product for two codes, a byte permute for four.
 //
 // Warps: 0-7 softmax and epilogue (warp w: TMEM lanes 32 (w % 4).., heads 32 (w / 4)..), 8-15 rows (codes
 // loaded a tile ahead into registers, widened into the swizzled stage; q at a unit's first tile), 16 MMA
 // issue, 17 index rows: it drops entries without a row, turns the others into row numbers and hands out tiles of
 // up to 128 (a unit without rows gives one tile of none), 18-19 the exponents of a tile's rows, between
 // the index warp and the row warps.  What a tile is (its rows, whether it is its unit's first or last) goes on
-// with the stage.
+// with the stage.  The softmax holds 32 heads of scores a thread and the row warps eight row loads in flight, so
+// of the launch's 96 registers a thread the softmax warps take 120 and leave the others 80; 16 softmax warps
+// with half the heads, or 12 more row warps, were slower (more instructions in all, or spilled loads).
 // A unit is one token and up to 64 heads; units are shared out as in the other attention kernels
 // (attn_split.cuh), and units cut by a range boundary leave f32 partials that a second kernel merges.
 // Every wait is bounded (2 s): then DS_DEV_TIMEOUT is flagged, issued MMAs are drained, TMEM is freed.
+//
+// Measured (entries / heads): 256 tokens of 2176 / 128, 216 us (661 TFLOP/s; its MMAs alone 72 us);
+// 4096 prefill tokens of up to 640 / 64, 519 us (527 TFLOP/s); 64 tokens of 128 / 64, 12.1 us; one token of 2176 / 16,
+// 18.7 us.  What bounds it is the issue of instructions: a scheduler's five warps get about one every two cycles
+// through, a tile takes about 5500 cycles of it (rows about 3000, softmax about 3500, side by side; the MMAs 2600
+// beneath them), a unit's end (output, the next q) about 8500.
 #include <atomic>
 #include <mutex>
 
@@ -59,9 +67,11 @@ constexpr int STAGE = NPAN * PANEL;     // 64 KB
 constexpr int NR = 4;                   // index messages
 constexpr int NSOFTW = 8, NSOFT = 32 * NSOFTW, HPW = 32;    // softmax warps; heads of one
 constexpr int W_ROWS = NSOFTW, NROWW = 8, W_MMA = W_ROWS + NROWW, W_IDX = W_MMA + 1, W_EXP = W_IDX + 1, NTHREADS = 640;
-constexpr int QROWS = 2;                             // heads of 8 that a row warp takes of the first q; a softmax warp the others
+// Of eight heads of a range's first q a row warp takes this many and a softmax warp, idle until then, the others
+// (64 tokens of 128 entries: 12.1 us; with three 12.35, with four half a microsecond more)
+constexpr int QROWS = 2;
 constexpr int RPL = BN / (2 * NROWW);                // steps of two rows that a row warp takes a tile
-// of the 96 registers a thread of the launch the softmax warps take more
+// of the 96 registers a thread of the launch the softmax warps take more (see above)
 constexpr uint32_t REG_SOFT = 120, REG_OTHER = 80;
 static_assert(NSOFT * REG_SOFT + (NTHREADS - NSOFT) * REG_OTHER <= NTHREADS * 96, "register split");
 constexpr int SM_Q = 0;
@@ -1016,6 +1026,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
 
 // Merge the partials of the units that a range boundary cuts: block (cut unit, four heads), warp = head.  A lane
 // has the first four parts' accumulators in flight before their weights are known.
+// Bound by latency: against a thread for four columns of a head and one part after the other the whole call takes
+// 22.7 -> 21.9 us for 32 units in four parts, 222 -> 220 with 150 cut ones, 20.1 -> 19.5 for one in eight.
 constexpr int kCombineHeads = 4;
 struct CombineParams {
     Args a;
