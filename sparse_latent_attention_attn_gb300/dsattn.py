@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -395,8 +396,15 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _fits(t: torch.Tensor, dtype, shape: tuple, dev: int) -> bool:
     return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+
+
+def _row_fits(t: torch.Tensor, dtype, n: int, dev: int) -> bool:
+    return t.dtype is dtype and t.dim() == 1 and t.numel() == n and t.is_contiguous() and t.get_device() == dev
 
 
 def _refuse(**tensors) -> None:
@@ -432,8 +440,8 @@ def norm_rotary(x: torch.Tensor, eps: float, rd: int, table: torch.Tensor | None
     xb, xt, xh, xd = x.stride()
     dev = x.get_device()
     tab = _table_shape(rd, table) if rd else None
-    if not (x.dtype is _BF16 and dev >= 0 and dev == torch.cuda.current_device() and _fits(first, _I32, (b,), dev)
-            and (lens is None or _fits(lens, _I32, (b,), dev)) and (weight is None or _fits(weight, _F32, (d,), dev))
+    if not (x.dtype is _BF16 and dev >= 0 and dev == _device() and _row_fits(first, _I32, b, dev)
+            and (lens is None or _row_fits(lens, _I32, b, dev)) and (weight is None or _row_fits(weight, _F32, d, dev))
             and (rd == 0 or (table is not None and _fits(table, _F32, tab, dev)))
             and (y is None or _fits(y, _BF16, (b, s, h, d), dev))):
         given = {"lens": (lens, _I32, (b,)), "weight": (weight, _F32, (d,)), "y": (y, _BF16, x.shape)}
@@ -444,10 +452,12 @@ def norm_rotary(x: torch.Tensor, eps: float, rd: int, table: torch.Tensor | None
     if y is None:
         with _on(stream):
             y = (torch.empty if lens is None else torch.zeros)((b, s, h, d), dtype=_BF16, device=x.device)
-    _check("ds_norm_rotary",
-           _lib.ds_norm_rotary(x.data_ptr(), xb if b > 1 else 0, xt if s > 1 else 0, y.data_ptr(), b, s, h, d,
-                               _ptr(weight), eps, rd, table.data_ptr() if rd else None, tab[0] if rd else 0,
-                               first.data_ptr(), _ptr(lens), _stream(stream)))
+    st = _lib.ds_norm_rotary(x.data_ptr(), xb if b > 1 else 0, xt if s > 1 else 0, y.data_ptr(), b, s, h, d,
+                             None if weight is None else weight.data_ptr(), eps, rd, table.data_ptr() if rd else None,
+                             tab[0] if rd else 0, first.data_ptr(), None if lens is None else lens.data_ptr(),
+                             _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check("ds_norm_rotary", st)
     return y
 
 
@@ -463,14 +473,15 @@ def kv_append_fp4_paged(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor
         raise ValueError("x must be [b][s][d], codes [pages][page][d/2] and block_table [b][max_pages]")
     b, s, d = x.shape
     xb, xt, xd = x.stride()
-    pages, page, _ = codes.shape
-    max_pages = block_table.shape[1]
+    pages, page, half = codes.shape
+    tables, max_pages = block_table.shape
     dev = x.get_device()
     tab = _table_shape(rd, table) if rd else None
-    if not (x.dtype is _BF16 and dev >= 0 and dev == torch.cuda.current_device()
-            and _fits(codes, _U8, (pages, page, d // 2), dev) and _fits(exps, _I8, (pages, page, d // 32), dev)
-            and _fits(block_table, _I32, (b, max_pages), dev) and _fits(first, _I32, (b,), dev)
-            and (lens is None or _fits(lens, _I32, (b,), dev)) and (weight is None or _fits(weight, _F32, (d,), dev))
+    if not (x.dtype is _BF16 and dev >= 0 and dev == _device()
+            and codes.dtype is _U8 and half == d // 2 and codes.is_contiguous() and codes.get_device() == dev
+            and _fits(exps, _I8, (pages, page, d // 32), dev) and block_table.dtype is _I32 and tables == b
+            and block_table.is_contiguous() and block_table.get_device() == dev and _row_fits(first, _I32, b, dev)
+            and (lens is None or _row_fits(lens, _I32, b, dev)) and (weight is None or _row_fits(weight, _F32, d, dev))
             and (rd == 0 or (table is not None and _fits(table, _F32, tab, dev)))
             and (y is None or _fits(y, _BF16, (b, s, d), dev))):
         given = {"lens": (lens, _I32, (b,)), "weight": (weight, _F32, (d,)), "y": (y, _BF16, x.shape)}
@@ -479,16 +490,24 @@ def kv_append_fp4_paged(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor
                 **{k: v for k, v in given.items() if v[0] is not None}, **({"table": (table, _F32, tab)} if rd else {}))
     if x.numel() and xd != 1:
         raise ValueError("the values of a row must be contiguous")
-    _check("ds_kv_append_fp4_paged",
-           _lib.ds_kv_append_fp4_paged(x.data_ptr(), xb if b > 1 else 0, xt if s > 1 else 0, _ptr(y), b, s, d,
-                                       _ptr(weight), eps, rd, table.data_ptr() if rd else None, tab[0] if rd else 0,
-                                       first.data_ptr(), _ptr(lens), pos_step, base, window, codes.data_ptr(),
-                                       exps.data_ptr(), pages, page, block_table.data_ptr(), max_pages,
-                                       _stream(stream)))
+    st = _lib.ds_kv_append_fp4_paged(x.data_ptr(), xb if b > 1 else 0, xt if s > 1 else 0,
+                                     None if y is None else y.data_ptr(), b, s, d,
+                                     None if weight is None else weight.data_ptr(), eps, rd,
+                                     table.data_ptr() if rd else None, tab[0] if rd else 0, first.data_ptr(),
+                                     None if lens is None else lens.data_ptr(), pos_step, base, window,
+                                     codes.data_ptr(), exps.data_ptr(), pages, page, block_table.data_ptr(), max_pages,
+                                     _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check("ds_kv_append_fp4_paged", st)
 
 
 def sparse_attn_fp4_paged_workspace_bytes(b: int, m: int, h: int, d: int, topk: int) -> int:
     return int(_lib.ds_sparse_attn_fp4_paged_workspace_bytes(b, m, h, d, topk))
+
+
+@functools.lru_cache(maxsize=64)
+def _fp4_workspace_bytes(dev: int, b: int, m: int, h: int, d: int, topk: int) -> int:
+    return sparse_attn_fp4_paged_workspace_bytes(b, m, h, d, topk)
 
 
 def sparse_attn_fp4_paged(q: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor, block_table: torch.Tensor,
@@ -501,16 +520,19 @@ def sparse_attn_fp4_paged(q: torch.Tensor, codes: torch.Tensor, exps: torch.Tens
     if q.dim() != 4 or idx.dim() != 3 or codes.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be [b][m][h][d], idx [b][m][topk], codes [pages][page][d/2] and block_table [b][max_pages]")
     b, m, h, d = q.shape
-    pages, page, _ = codes.shape
-    topk, max_pages = idx.shape[2], block_table.shape[1]
+    pages, page, half = codes.shape
+    tables, max_pages = block_table.shape
+    ib, im, topk = idx.shape
     dev = q.get_device()
     tab = _table_shape(rd, table) if rd else None
-    if not (q.dtype is _BF16 and q.is_contiguous() and dev >= 0 and dev == torch.cuda.current_device()
-            and _fits(codes, _U8, (pages, page, d // 2), dev) and _fits(exps, _I8, (pages, page, d // 32), dev)
-            and _fits(block_table, _I32, (b, max_pages), dev) and _fits(sink, _F32, (h,), dev)
-            and _fits(idx, _I32, (b, m, topk), dev) and (o is None or _fits(o, _BF16, (b, m, h, d), dev))
+    if not (q.dtype is _BF16 and q.is_contiguous() and dev >= 0 and dev == _device()
+            and codes.dtype is _U8 and half == d // 2 and codes.is_contiguous() and codes.get_device() == dev
+            and _fits(exps, _I8, (pages, page, d // 32), dev) and block_table.dtype is _I32 and tables == b
+            and block_table.is_contiguous() and block_table.get_device() == dev and _row_fits(sink, _F32, h, dev)
+            and idx.dtype is _I32 and ib == b and im == m and idx.is_contiguous() and idx.get_device() == dev
+            and (o is None or _fits(o, _BF16, (b, m, h, d), dev))
             and (rd == 0 or (table is not None and _fits(table, _F32, tab, dev) and first is not None
-                             and _fits(first, _I32, (b,), dev)))
+                             and _row_fits(first, _I32, b, dev)))
             and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))):
         _refuse(q=(q, _BF16, q.shape), codes=(codes, _U8, (pages, page, d // 2)), exps=(exps, _I8, (pages, page, d // 32)),
                 block_table=(block_table, _I32, (b, max_pages)), sink=(sink, _F32, (h,)), idx=(idx, _I32, (b, m, topk)),
@@ -518,22 +540,30 @@ def sparse_attn_fp4_paged(q: torch.Tensor, codes: torch.Tensor, exps: torch.Tens
                 **({"table": (table, _F32, tab), "first": (first, _I32, (b,))} if rd else {}),
                 **({"workspace": (workspace, workspace.dtype, workspace.shape)} if workspace is not None else {}))
     if o is None:
-        with _on(stream):
+        if stream is None:
             o = torch.empty_like(q)
+        else:
+            with _on(stream):
+                o = torch.empty_like(q)
     ws, ws_bytes = None, 0
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     else:
-        need = _lib.ds_sparse_attn_fp4_paged_workspace_bytes(b, m, h, d, topk)
+        need = _fp4_workspace_bytes(dev, b, m, h, d, topk)
         if need:
-            with _on(stream):
+            if stream is None:
                 workspace = torch.empty(need, dtype=_U8, device=q.device)
+            else:
+                with _on(stream):
+                    workspace = torch.empty(need, dtype=_U8, device=q.device)
             ws, ws_bytes = workspace.data_ptr(), need
-    _check("ds_sparse_attn_fp4_paged",
-           _lib.ds_sparse_attn_fp4_paged(q.data_ptr(), codes.data_ptr(), exps.data_ptr(), pages, page,
-                                         block_table.data_ptr(), max_pages, sink.data_ptr(), idx.data_ptr(), topk, scale,
-                                         o.data_ptr(), b, m, h, d, ws, ws_bytes, rd, table.data_ptr() if rd else None,
-                                         tab[0] if rd else 0, first.data_ptr() if rd else None, _stream(stream)))
+    st = _lib.ds_sparse_attn_fp4_paged(q.data_ptr(), codes.data_ptr(), exps.data_ptr(), pages, page,
+                                       block_table.data_ptr(), max_pages, sink.data_ptr(), idx.data_ptr(), topk, scale,
+                                       o.data_ptr(), b, m, h, d, ws, ws_bytes, rd, table.data_ptr() if rd else None,
+                                       tab[0] if rd else 0, first.data_ptr() if rd else None,
+                                       _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check("ds_sparse_attn_fp4_paged", st)
     return o
 
 

@@ -781,6 +781,39 @@ def test_attention_wait_that_runs_out(ds, b, h, topk):
     check_attention(ds, *x, sample=4)
 
 
+@gpu
+def test_bindings_refuse_what_does_not_fit(ds):
+    """Each argument in turn with another type, shape, layout or place: refused before anything runs."""
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device="cuda")
+    i32, f32, u8, i8 = torch.int32, torch.float32, torch.uint8, torch.int8
+    norm = dict(x=z(2, 3, 4, 64), eps=1e-6, rd=16, table=z(9, 8, 2, dt=f32), first=z(2, dt=i32), weight=z(64, dt=f32),
+                lens=z(2, dt=i32), y=z(2, 3, 4, 64))
+    app = dict(x=z(2, 3, 64), codes=z(5, 4, 32, dt=u8), exps=z(5, 4, 2, dt=i8), block_table=z(2, 3, dt=i32),
+               first=z(2, dt=i32), rd=16, table=z(9, 8, 2, dt=f32), eps=1e-6, weight=z(64, dt=f32), lens=z(2, dt=i32),
+               y=z(2, 3, 64))
+    attn = dict(q=z(2, 1, 4, 512), codes=z(5, 4, 256, dt=u8), exps=z(5, 4, 16, dt=i8), block_table=z(2, 3, dt=i32),
+                sink=z(4, dt=f32), idx=z(2, 1, 7, dt=i32), scale=0.1, rd=16, table=z(9, 8, 2, dt=f32), first=z(2, dt=i32),
+                o=z(2, 1, 4, 512))
+    for f, args in ((ds.norm_rotary, norm), (ds.kv_append_fp4_paged, app), (ds.sparse_attn_fp4_paged, attn)):
+        f(**args)
+        for name, t in args.items():
+            if not isinstance(t, torch.Tensor):
+                continue
+            wide = torch.zeros(t.shape + (2,), dtype=t.dtype, device="cuda")[..., 0]
+            bad = [t.to(torch.int64), t.cpu(), wide, t.unsqueeze(0)]
+            if (f, name) not in ((ds.norm_rotary, "table"), (ds.kv_append_fp4_paged, "table"), (ds.sparse_attn_fp4_paged, "table"),
+                                 (ds.kv_append_fp4_paged, "exps")):
+                bad.append(torch.zeros(t.shape[:-1] + (t.shape[-1] + 1,), dtype=t.dtype, device="cuda"))
+            for v in bad:
+                if (name, f) in (("idx", ds.sparse_attn_fp4_paged), ("block_table", ds.kv_append_fp4_paged),
+                                 ("block_table", ds.sparse_attn_fp4_paged)) and v.shape[:-1] == t.shape[:-1] \
+                        and v.dtype == t.dtype and v.is_cuda and v.is_contiguous():
+                    continue                               # another number of columns is another valid call
+                with pytest.raises((TypeError, ValueError, RuntimeError)):
+                    f(**{**args, name: v})
+    assert ds.device_status() == 0
+
+
 # ---- refusals, no GPU needed ---------------------------------------------------------------------------------
 
 @pytest.fixture(scope="module")
