@@ -42,7 +42,9 @@
 // 18.7 us.  What bounds it is the issue of instructions: a scheduler's five warps get about one every two cycles
 // through, a tile takes about 5500 cycles of it (rows about 3000, softmax about 3500, side by side; the MMAs 2600
 // beneath them), a unit's end (output, the next q) about 8500.
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "attn_split.cuh"
@@ -1149,6 +1151,29 @@ bool fits(int b, int m, int topk) {
     return ntok <= INT32_MAX / 2 && ntok <= (INT64_MAX >> 11) / ((int64_t)topk + kSegCost);
 }
 
+// Ranges for a problem.  With at least as many units as CTAs: one a CTA, cut where they fall.  With fewer, every unit
+// gets k of them, the k of the least estimated time in tiles of 2.8 us: a unit's tiles one after the other (the second
+// overlaps the first), and from two parts on the merge: its launch, the partials through L2, the parts in turn.
+// Measured, whole against parts of about one tile (64 heads): 1 token of 256 entries 13.8 us (14.4 in two), 384: 17.0
+// (14.5 in three), 1024: 16.4 in four, 15.3 in eight; 16 tokens of 1024: 17.3 in four, 18.2 in eight; 40 tokens
+// of 256: 14.0 (15.8 in two); 70 of 384: 17.5 (20.2 in two).
+int64_t ranges(int64_t nunit, int topk, int gmax) {
+    if (nunit >= gmax) return gmax;
+    const int64_t most = std::min<int64_t>({gmax / nunit, ((int64_t)topk + BN - 1) / BN, 32});
+    int64_t best = 1;
+    float least = INFINITY;
+    for (int64_t k = 1; k <= most; ++k) {
+        const int64_t part = (topk + k - 1) / k, tiles = (part + BN - 1) / BN;
+        float cost = tiles <= 2 ? 0.6f * (float)(tiles - 1) : (float)tiles - 1.25f;
+        if (k > 1) cost += 0.85f + (float)(nunit * k) / 120.0f + (float)k / 30.0f;
+        if (cost < least) {
+            least = cost;
+            best = k;
+        }
+    }
+    return nunit * best;
+}
+
 // The plan of a shape on the current device; each host thread keeps its last one (a decode loop asks for the
 // same one for every layer and step).  Null when there is none.
 const Plan *plan(int b, int m, int h, int topk) {
@@ -1164,7 +1189,7 @@ const Plan *plan(int b, int m, int h, int topk) {
     pl.ntok = (int64_t)b * m;
     pl.groups = h > HM ? 2 : 1;
     pl.nunit = pl.ntok * pl.groups;
-    pl.G = split::choose_ranges(pl.nunit, topk, gmax, BN);
+    pl.G = ranges(pl.nunit, topk, gmax);
     pl.K = split::seg_cost(pl.nunit, pl.G, kSegCost);
     pl.split = split::splits_units(pl.nunit, topk, pl.G, pl.K);
     pl.ncut = pl.split ? split::cut_units(pl.nunit, topk, pl.K, pl.G, pl.cut) : 0;
