@@ -39,7 +39,7 @@
 //
 // Measured (entries / heads): 256 tokens of 2176 / 128, 216 us (661 TFLOP/s; its MMAs alone 72 us);
 // 4096 prefill tokens of up to 640 / 64, 519 us (527 TFLOP/s); 64 tokens of 128 / 64, 12.1 us; one token of 2176 / 16,
-// 18.7 us.  What bounds it is the issue of instructions: a scheduler's five warps get about one every two cycles
+// 15.4 us.  What bounds it is the issue of instructions: a scheduler's five warps get about one every two cycles
 // through, a tile takes about 5500 cycles of it (rows about 3000, softmax about 3500, side by side; the MMAs 2600
 // beneath them), a unit's end (output, the next q) about 8500.
 #include <algorithm>
@@ -1028,8 +1028,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
 
 // Merge the partials of the units that a range boundary cuts: block (cut unit, four heads), warp = head.  A lane
 // has the first four parts' accumulators in flight before their weights are known.
-// Bound by latency: against a thread for four columns of a head and one part after the other the whole call takes
-// 22.7 -> 21.9 us for 32 units in four parts, 222 -> 220 with 150 cut ones, 20.1 -> 19.5 for one in eight.
+// Bound by latency: against a thread for four columns of a head and one part after the other the whole call took
+// 22.7 -> 21.9 us for 32 units in two parts, 222 -> 220 with 150 cut ones, 20.1 -> 19.5 for one in eight.
 constexpr int kCombineHeads = 4;
 struct CombineParams {
     Args a;
@@ -1037,13 +1037,21 @@ struct CombineParams {
     int groups;
     bool interleave;
     const float *ws;
+    int parts;                    // of every unit, each in its range's first slot
+};
+struct CutParams : CombineParams {
     int4 cut[kMaxCut];            // {unit, first part, parts, slot bits}
 };
 
-template <bool ROPE>
-__global__ void __launch_bounds__(32 * kCombineHeads) combine_kernel(const CombineParams p) {
+// Which unit and parts a block merges: from the table, or block u's unit u in p.parts parts (a launch costs the host
+// less without the table's 2.5 KB).
+__device__ __forceinline__ int4 cut_of(const CombineParams &p, int i) { return make_int4(i, i * p.parts, p.parts, 0); }
+__device__ __forceinline__ int4 cut_of(const CutParams &p, int i) { return p.cut[i]; }
+
+template <bool ROPE, typename P>
+__global__ void __launch_bounds__(32 * kCombineHeads) combine_kernel(const P p) {
     grid_dependency_wait();
-    const int4 c = p.cut[blockIdx.x];
+    const int4 c = cut_of(p, blockIdx.x);
     const int tok = token_at((uint32_t)(p.groups == 1 ? c.x : c.x >> 1), p.ntok, p.interleave);
     const int h0 = p.groups == 1 ? 0 : (c.x & 1) * HM, hh = blockIdx.y * kCombineHeads + (threadIdx.x >> 5);
     if (hh >= HM || h0 + hh >= p.a.h) return;
@@ -1140,8 +1148,9 @@ struct Plan {
     int4 cut[kMaxCut];
 };
 
-// Fixed cost of a unit on the cost line (q, the epilogue), in index entries: two tiles' worth (256 tokens of 128 heads and
-// 2176 entries: 216 us; with one tile's worth 219, with one and a half 219; 4096 tokens of 640 entries: 519 either way).
+// Fixed cost of a unit on the cost line (q, the epilogue), in index entries: two tiles' worth (256 tokens of 128
+// heads and 2176 entries: 216 us; with one tile's worth 219, with one and a half 219; 4096 tokens of 640 entries:
+// 519 either way).
 constexpr int kSegCost = 2 * BN;
 
 // The units (two a token at most) in 32 bits, and every place on the cost line in 64: at most 1023 ranges' worth of
@@ -1153,10 +1162,12 @@ bool fits(int b, int m, int topk) {
 
 // Ranges for a problem.  With at least as many units as CTAs: one a CTA, cut where they fall.  With fewer, every unit
 // gets k of them, the k of the least estimated time in tiles of 2.8 us: a unit's tiles one after the other (the second
-// overlaps the first), and from two parts on the merge: its launch, the partials through L2, the parts in turn.
-// Measured, whole against parts of about one tile (64 heads): 1 token of 256 entries 13.8 us (14.4 in two), 384: 17.0
-// (14.5 in three), 1024: 16.4 in four, 15.3 in eight; 16 tokens of 1024: 17.3 in four, 18.2 in eight; 40 tokens
-// of 256: 14.0 (15.8 in two); 70 of 384: 17.5 (20.2 in two).
+// overlaps the first), and from two parts on the merge: its launch (2.4 us on the device, and with the workspace 6 us
+// of the host's time, hence 1.3 tiles), the partials through L2, the parts in turn.
+// Measured on the device, whole against parts of about one tile (64 heads): 1 token of 256 entries 13.8 us (14.4 in two),
+// 384: 17.0 (14.5 in three), 1024: 16.4 in four, 15.3 in eight; 16 tokens of 1024: 17.3 in four, 18.2 in eight; 40
+// tokens of 256: 14.0 (15.8 in two); 70 of 384: 17.5 (20.2 in two).  15 tokens of 356, 40 heads: 17.0 whole, 14.4 in
+// three, but then 17 to 20 a call for the host.
 int64_t ranges(int64_t nunit, int topk, int gmax) {
     if (nunit >= gmax) return gmax;
     const int64_t most = std::min<int64_t>({gmax / nunit, ((int64_t)topk + BN - 1) / BN, 32});
@@ -1165,7 +1176,7 @@ int64_t ranges(int64_t nunit, int topk, int gmax) {
     for (int64_t k = 1; k <= most; ++k) {
         const int64_t part = (topk + k - 1) / k, tiles = (part + BN - 1) / BN;
         float cost = tiles <= 2 ? 0.6f * (float)(tiles - 1) : (float)tiles - 1.25f;
-        if (k > 1) cost += 0.85f + (float)(nunit * k) / 120.0f + (float)k / 30.0f;
+        if (k > 1) cost += 1.3f + (float)(nunit * k) / 120.0f + (float)k / 30.0f;
         if (cost < least) {
             least = cost;
             best = k;
@@ -1237,19 +1248,21 @@ int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream) {
         cudaSuccess)
         return DS_ECUDA;
     if (pl.split) {
-        fp4::CombineParams c;
-        c.a = a;
-        c.ntok = (int)pl.ntok;
-        c.groups = pl.groups;
-        c.interleave = interleave;
-        c.ws = p.ws;
-        for (int i = 0; i < pl.ncut; ++i) c.cut[i] = pl.cut[i];
+        const fp4::CombineParams head{a, (int)pl.ntok, pl.groups, interleave, p.ws, (int)(pl.G / pl.nunit)};
         const int heads = a.h < fp4::HM ? a.h : fp4::HM;
         cfg.gridDim = dim3((unsigned)pl.ncut, (unsigned)((heads + fp4::kCombineHeads - 1) / fp4::kCombineHeads), 1);
         cfg.blockDim = dim3(32 * fp4::kCombineHeads, 1, 1);
         cfg.dynamicSmemBytes = 0;
-        if (cudaLaunchKernelEx(&cfg, rope ? fp4::combine_kernel<true> : fp4::combine_kernel<false>, c) != cudaSuccess)
-            return DS_ECUDA;
+        cudaError_t e;
+        if (pl.G > pl.nunit) {
+            e = cudaLaunchKernelEx(&cfg, rope ? fp4::combine_kernel<true, fp4::CombineParams> : fp4::combine_kernel<false, fp4::CombineParams>, head);
+        } else {
+            fp4::CutParams c;
+            static_cast<fp4::CombineParams &>(c) = head;
+            for (int i = 0; i < pl.ncut; ++i) c.cut[i] = pl.cut[i];
+            e = cudaLaunchKernelEx(&cfg, rope ? fp4::combine_kernel<true, fp4::CutParams> : fp4::combine_kernel<false, fp4::CutParams>, c);
+        }
+        if (e != cudaSuccess) return DS_ECUDA;
     }
     return DS_OK;
 }
