@@ -427,9 +427,10 @@ int ds_kv_append_fp4_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstri
  * and flagged.  Otherwise the operation is ds_sparse_attn's on the decoded rows: duplicates count as
  * often as they are listed, a query without rows gives o = 0.  Scores, softmax and accumulation
  * are f32, and the rotation of position first[bi] + t is applied before o's one rounding (a
- * position outside the table leaves that token's o unrotated).  A probability enters the value
- * product rounded by at most 2^-8 of itself (as bf16) or, where that is more, by 2^-17 of the
- * head's largest, times 2^(E - e) for a row whose largest exponent e is below the list's, E.
+ * position outside the table leaves that token's o unrotated).  A probability p of a row whose
+ * largest exponent is e enters the value product rounded by at most 2^-8 of itself (as bf16) or,
+ * where that is more, p 2^e by 2^-17 of the head's largest such product: rows of little
+ * probability take nothing from the others, however large their values are.
  * Within a row, blocks whose exponent is more than 26 below the row's largest count as zeros (2^-26
  * of the row's scale).  Exponents must lie in [-126, 126], and scores must be finite in f32.
  *

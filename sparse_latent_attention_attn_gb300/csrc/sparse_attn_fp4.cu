@@ -13,12 +13,13 @@
 //    them, so a bf16 q (eight) is exact down to 2^-9 of its head's largest value and off by 2^-22 of that
 //    largest value below.  S^T = C [hi | lo]: M = 128 rows, N = 64 heads twice, and the score is
 //    (S_hi + 2^-5 S_lo) 2^(g + e_r - 12) scale.
-//  * P' = 2^(s - m + e_r - E + 4) for running m (per head, lazily raised, at most 4 octaves late) and E (the
-//    largest e_r so far), at most 256; P' = hi - lo with hi in e4m3 and lo in e5m2, each to nearest: off by
+//  * P' = 2^(s + e_r - m + 4), m the head's running maximum of s + e_r (lazily raised, at most 4 octaves late),
+//    at most 256: a row's weight is its probability times its scale, so a row of large values and no probability
+//    takes nothing from the others.  P' = hi - lo with hi in e4m3 and lo in e5m2, each to nearest: off by
 //    2^-8 of itself, as bf16 would be, from 2^-6 on (hi has four bits, lo three of the rest), and by 2^-13
-//    below (hi is a multiple of 2^-9): 2^-17 of the largest probability of a head.  O^T +=
-//    C^T (hi - lo), d = 512 as four blocks of 128 lanes, heads as columns; O 2^(E - 16) / l is the
-//    output.  l sums the unrounded f32 p.
+//    below (hi is a multiple of 2^-9): 2^-17 of the head's largest p 2^e.  O^T += C^T (hi - lo), d = 512
+//    as four blocks of 128 lanes, heads as columns; l = sum of P' 2^-e_r of the unrounded f32 P', which is
+//    2^(4 - m) times the denominator, so O 2^-12 / (l + 2^(sink + 4 - m)) is the output.
 //
 // Why so.  A tile is 128 rows of 512 bytes, so two tiles, q (64 KB as hi and lo) and P fit the 227 KB of an
 // SM; as bf16 only tiles of 64 rows would, and a 64-row tcgen05.mma takes the time of a 128-row one.  With
@@ -87,8 +88,7 @@ constexpr int C_EXPS = C_ROWS + NR * BN * 4;    // [NR][128][16] k - e_r + 27 of
 constexpr int C_TOPS = C_EXPS + NR * BN * (D / 32);   // [NR][128] int8 e_r
 constexpr int C_REXP = C_TOPS + NR * BN;        // [2][128] int8 e_r of the stages' rows
 constexpr int C_MAX = C_REXP + 2 * BN;          // [4][64] f32 maxima of the quarters
-constexpr int C_EMAX = C_MAX + 4 * HM * 4;      // [4] int32 largest e_r of the quarters
-constexpr int C_SUM = C_EMAX + 16;              // [4][64] f32 sums of the quarters, at a unit's end
+constexpr int C_SUM = C_MAX + 4 * HM * 4;       // [4][64] f32 sums of the quarters, at a unit's end
 constexpr int C_HEAD = C_SUM + 4 * HM * 4;      // [64] f32 minus the running maximum m, 0 at a unit's start
 constexpr int C_FAC = C_HEAD + HM * 4;          // [64] f32 factor of O^T: at m's rise, and at a unit's end
 constexpr int C_QS = C_FAC + HM * 4;           // [2][64] f32 2^g scale log2(e), by unit parity
@@ -118,6 +118,7 @@ static_assert(TM_S + 2 * 2 * HM <= TMEM_COLS, "TMEM budget");
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTop = 4;                 // octaves of P' at m
 constexpr float kSlack = 4.0f;          // octaves that m may be late
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -125,7 +126,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 // rows << 16
 constexpr int kTile = 1, kFin = 2, kFirst = 1 << 8, kLast = 1 << 9, kWhole = 1 << 10, kSlot0 = 1 << 11;
 
-// a partial slot (f32): O [64][512], then running maxima [64] (log2 domain, -inf: no row) and sums [64]
+// a partial slot (f32): O [64][512], then running maxima m [64] (octaves, -inf: no row) and sums l [64]
 constexpr int SLOT_O = HM * D;
 constexpr size_t SLOT = (size_t)SLOT_O + 2 * HM;
 
@@ -753,16 +754,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
     } else if (warp < NSOFTW) {
         // ============================ softmax and epilogue ============================
         setmaxnreg_inc<REG_SOFT>();
-        // Warp (quarter, heads hb..): its 32 rows by its 16 heads of every tile, and in O^T its 32 lanes of every
-        // panel by the same heads.  The four warps of the same heads agree on m and E without talking
-        // about them: they read the same maxima.
+        // Warp (quarter, heads hb..): its 32 rows by its 32 heads of every tile, and in O^T its 32 lanes of every
+        // panel by the same heads.  The four warps of the same heads agree on m without talking about it:
+        // they read the same maxima.
         const int quarter = warp & 3, hb = (warp >> 2) * HPW, row = quarter * 32 + lane, hl = hb + lane;
         const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16);
         float *head = reinterpret_cast<float *>(ctl + C_HEAD), *fac = reinterpret_cast<float *>(ctl + C_FAC), *sums = reinterpret_cast<float *>(ctl + C_SUM);
         const float *qs = reinterpret_cast<const float *>(ctl + C_QS);
-        uint64_t l[HPW / 2];   // sums of p over this thread's rows, in pairs of heads
+        uint64_t l[HPW / 2];   // sums of P' 2^-e over this thread's rows, in pairs of heads
         float m = 0.0f;        // of head hl
-        int E = 0;
         uint32_t unit = u0, seg = 0;
         bool bad = false;
         head[hl] = 0.0f;
@@ -787,10 +787,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             const bool first = msg & kFirst;
             const bool live = row < count;
             float *maxima = reinterpret_cast<float *>(ctl + C_MAX);
-            int *emax = reinterpret_cast<int *>(ctl + C_EMAX);
-            uint64_t v[HPW / 2];   // scores in octaves, less m, in pairs of heads
+            uint64_t v[HPW / 2];   // s + e - m + 4 in octaves, in pairs of heads
             int e = 0;
-            bool late = true;      // m or E has to move
+            bool late = true;      // m has to move
             if (!bad) bad = !warp_wait(BAR(B_S + st), (J >> 1) & 1u, abort_flag);
             if (!bad) {
                 if (first) {
@@ -800,7 +799,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 tc_fence_after();
                 e = (int)reinterpret_cast<const int8_t *>(ctl + C_REXP)[st * BN + row];
                 const float c = pow2(e - 12);
-                const uint64_t cr = pair(c, c), low = pair(0.03125f, 0.03125f);
+                const float e4 = (float)(e + kTop);
+                const uint64_t cr = pair(c, c), low = pair(0.03125f, 0.03125f), er = pair(e4, e4);
                 const float *q = qs + ((seg - 1) & 1u) * HM + hb;
 #pragma unroll
                 for (int j = 0; j < HPW; j += 16) {
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                         for (int k = 0; k < 2; ++k) {
                             const uint64_t s = fma2(pair(__uint_as_float(r1[i + 2 * k]), __uint_as_float(r1[i + 2 * k + 1])), low,
                                                     pair(__uint_as_float(r0[i + 2 * k]), __uint_as_float(r0[i + 2 * k + 1])));
-                            v[(j + i) / 2 + k] = fma2(mul2(s, cr), qv[k], mv[k]);
+                            v[(j + i) / 2 + k] = add2(fma2(mul2(s, cr), qv[k], mv[k]), er);
                         }
                     }
                 }
@@ -835,10 +835,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     unpair(v[i], a, b);
                     top = max3(top, a, b);
                 }
-                late = first || top > kSlack || (live && e > E);
+                late = first || top > (float)kTop + kSlack;
             }
             if (bar_or(late)) {
-                // the tile's maxima, and the heads' m and E behind them: always at a unit's first tile, seldom later
+                // the tile's maxima, and the heads' m behind them: always at a unit's first tile, seldom later
 #pragma unroll
                 for (int i = 0; i < HPW / 2; ++i) {
                     float a, b;
@@ -847,18 +847,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                     b = warp_max(b);
                     if (lane == 0) *reinterpret_cast<float2 *>(maxima + quarter * HM + hb + 2 * i) = make_float2(a, b);
                 }
-                const int te = __reduce_max_sync(kAll, live ? e : -128);
-                if (lane == 0 && hb == 0) emax[quarter] = te;
                 if (bar_or(bad)) break;
                 const float t = fmaxf(fmaxf(maxima[hl], maxima[HM + hl]), fmaxf(maxima[2 * HM + hl], maxima[3 * HM + hl]));
-                const int4 e4 = *reinterpret_cast<const int4 *>(emax);
-                const int tile_e = max(max(e4.x, e4.y), max(e4.z, e4.w));
-                const int E0 = E;
-                E = first ? tile_e : max(E, tile_e);
                 // up to the tile's maximum; no change when that is lower, or there is no row (-inf)
-                const float up = first ? (t == -INFINITY ? 0.0f : t) : fmaxf(t, 0.0f);
+                const float up = first ? (t == -INFINITY ? 0.0f : t - kTop) : fmaxf(t - kTop, 0.0f);
                 m += up;
-                const float down = pow2(E0 - E);
                 __syncwarp();
                 head[hl] = -m;                         // the same from every quarter
                 fac[hl] = ex2(-up);
@@ -870,7 +863,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
 #pragma unroll
                     for (int i = 0; i < HPW / 2; ++i) l[i] = 0;
                 } else {
-                    // this warp's part of O^T, and its sums, follow m and E
+                    // this warp's part of O^T, and its sums, follow m
                     bad = !warp_wait(BAR(B_PV + 2 * (st ^ 1u) + 1), ((J - 1) >> 1) & 1u, abort_flag);
                     tc_fence_after();
 #pragma unroll 1
@@ -881,7 +874,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                         tmem_ld16(at, r);
                         tmem_wait16(r);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (f[i] * down));
+                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f[i]);
                         tmem_st16(at, r);
                     }
                     tmem_st_wait();
@@ -891,7 +884,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             }
             uint32_t hi[HPW / 4], lo[HPW / 4];
             {
-                const float f = live ? pow2(e - E + 4) : 0.0f;
+                const float f = pow2(-e);
                 const uint64_t fr = pair(f, f);
 #pragma unroll
                 for (int i = 0; i < HPW / 2; i += 2) {
@@ -901,8 +894,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                         float a, b;
                         unpair(v[i + k], a, b);
                         pr[k] = pair(ex2(a), ex2(b));
-                        l[i + k] = add2(l[i + k], pr[k]);
-                        pr[k] = mul2(pr[k], fr);
+                        l[i + k] = fma2(pr[k], fr, l[i + k]);
                     }
                     split_p(pr[0], pr[1], hi[i / 2], lo[i / 2]);
                 }
@@ -947,10 +939,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 float *ws = p.ws + ((size_t)cid * 2 + (msg & kSlot0 ? 0 : 1)) * SLOT;
                 const float sum = sums[hl] + sums[HM + hl] + sums[2 * HM + hl] + sums[3 * HM + hl];
                 const bool any = sum != 0.0f;              // false: no rows (NaN counts)
-                const float unfold = pow2(E - 16);
-                float f = unfold;                          // of head hl
+                float f = 0x1p-12f;                        // of head hl
                 if (whole) {
-                    f = any ? unfold / (sum + exp2f(sink - m)) : 0.0f;
+                    f = any ? 0x1p-12f / (sum + exp2f(sink - m + kTop)) : 0.0f;
                 } else if (quarter == 0) {
                     ws[SLOT_O + hl] = any ? m : -INFINITY;
                     ws[SLOT_O + HM + hl] = sum;
@@ -1083,7 +1074,7 @@ __global__ void __launch_bounds__(32 * kCombineHeads) combine_kernel(const P p) 
         float den = w * l;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kAll, den, o);
-        den += exp2f(__ldg(p.a.sink + h0 + hh) * kLog2e - top);
+        den += exp2f(__ldg(p.a.sink + h0 + hh) * kLog2e - top + kTop);
         const float inv = 1.0f / den;
         for (int i = 0;;) {
 #pragma unroll

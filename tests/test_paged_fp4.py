@@ -918,3 +918,60 @@ def test_the_plain_quantiser():
     assert k.tolist() == [[0]] and code[0, :8].tolist() == [7, 0, 2, 2, 4, 4, 6, 6] and (code[0, 8:] == 9).all()
     assert quantise(np.full((1, 32), 6.01))[1].tolist() == [[1]] and quantise(np.full((1, 32), 3.0))[1].tolist() == [[-1]]
     assert quantise(np.zeros((1, 32)))[1].tolist() == [[-15]]
+
+
+# ---- rows of very different scale: a row's weight is its probability times its scale -------------------------
+
+def attention_by_weight(q, rows, live, sink, scale, tops):
+    """As attention(), F relative to each head's largest p 2^e (e the row's largest exponent, -48 at least): a
+    probability is held to 2^-8 of itself or to 2^-17 of that, whatever exponents other rows have."""
+    rows, e = rows[live], np.maximum(tops[live], -48).astype(float)
+    s = scale * q @ rows.T
+    top = s.max(-1, keepdims=True)
+    p = np.exp(s - top)
+    with np.errstate(over="ignore"):
+        den = p.sum(-1, keepdims=True) + np.exp(sink[:, None] - top)
+    worth = (np.exp((s - top) + e * math.log(2))).max(-1, keepdims=True) * (np.abs(rows) * 2.0 ** -e[:, None]).sum(0)[None]
+    return p @ rows / den, p @ np.abs(rows) / den, worth / den
+
+
+def check_by_weight(ds, q, codes, exps, bt, sink, idx, scale=512 ** -0.5, status=0, read=None):
+    """Every element against 64 bits; `read`: the exponents as the documentation says they are read."""
+    b, m = q.shape[:2]
+    o = ds.sparse_attn_fp4_paged(*dev(q, codes, exps, bt, sink, idx), scale)
+    assert ds.device_status() == status
+    got = f64(o)
+    for i in range(b):
+        for t in range(m):
+            ix = idx[i, t].numpy()
+            rows, tops = logical_rows(codes, exps if read is None else read, bt, i, ix, codes.shape[1])
+            ref, A, F = attention_by_weight(f64(q[i, t]), rows, ix >= 0, f64(sink), scale, tops)
+            tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * A + 2.0 ** -17 * F + 2.0 ** -126
+            assert (np.abs(got[i, t] - ref) <= tol).all(), (i, t, float((np.abs(got[i, t] - ref) / tol).max()))
+    return o
+
+
+@gpu
+@pytest.mark.parametrize("octaves", [8, 12, 16, 20, 30, 40])
+@pytest.mark.parametrize("b,h,topk", [(2, 24, 200), (1, 16, 1500), (1, 70, 90)])
+def test_attention_large_row_without_weight(ds, b, h, topk, octaves):
+    """One row `octaves` above the others: without probability in the even heads, whose output is the other
+    rows' as if it were not listed, and with all of it in the odd ones."""
+    q, codes, exps, bt, sink, idx, *_ = attention_inputs(41 + octaves, b, 1, h, 2000, topk, 0.0, 16, 0)
+    sign = torch.where(torch.rand(512, generator=torch.Generator().manual_seed(octaves)) < 0.5, -1.0, 1.0)
+    code = torch.where(sign < 0, 10, 2).to(torch.uint8)            # -1 and 1
+    exps.clamp_(max=0)
+    for i in range(b):
+        for at in (0, topk // 2, topk - 1):
+            r = int(idx[i, 0, at])
+            codes[bt[i, r // 16], r % 16] = code[0::2] | code[1::2] << 4
+            exps[bt[i, r // 16], r % 16] = octaves
+    half = torch.where(torch.arange(h) % 2 == 0, -1.0, 1.0)[:, None]
+    q = (q.float() + 0.5 * half * sign).to(torch.bfloat16)
+    o = check_by_weight(ds, q, codes, exps, bt, sink, idx)
+    # without the large rows at all: the even heads' sums are the same but for their order
+    rest = torch.ones(topk, dtype=torch.bool)
+    rest[[0, topk // 2, topk - 1]] = False
+    few = check_by_weight(ds, q, codes, exps, bt, sink, idx[..., rest].contiguous())
+    worst = (o - few).float().abs()[:, :, 0::2].amax() / few.float().abs()[:, :, 0::2].amax()
+    assert worst <= 2.0 ** -6
