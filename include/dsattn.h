@@ -51,6 +51,7 @@ typedef struct CUstream_st *ds_stream_t;
  * launch's own copies and MMAs and returns, so the context stays usable (ds_test_set_stall
  * exercises that path). */
 #define DS_DEV_BAD_INDEX 2u   /* an index >= n was seen; the entry was skipped                       */
+#define DS_DEV_BAD_VALUE 4u   /* a stored exponent above its range was seen; it was read as the range's largest */
 
 /*
  * ds_window_topk_idxs -- sliding-window ring-slot index rows.
@@ -431,8 +432,9 @@ int ds_kv_append_fp4_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstri
  * largest exponent is e enters the value product rounded by at most 2^-8 of itself (as bf16) or,
  * where that is more, p 2^e by 2^-17 of the head's largest such product: rows of little
  * probability take nothing from the others, however large their values are.
- * Within a row, blocks whose exponent is more than 26 below the row's largest count as zeros (2^-26
- * of the row's scale).  Exponents must lie in [-126, 126], and scores must be finite in f32.
+ * Block exponents above 48 are read as 48 and raise DS_DEV_BAD_VALUE (ds_kv_append_fp4_paged stores
+ * them for values above 6 * 2^48 only); blocks whose exponent is more than 26 below the row's
+ * largest, or below -74, count as zeros.  scale * q and the scores must be finite in f32.
  *
  * rd         multiple of 8, 0 <= rd <= d (0: no rotation; table and first may be NULL)
  * workspace  at least ds_sparse_attn_fp4_paged_workspace_bytes(b, m, h, d, topk) bytes, 256-byte

@@ -5,9 +5,10 @@
 // "DeepSeek V4.1", attention/query-latent, Attention.forward (the output's inverse rotation).  Rows are
 // e2m1 codes with a power-of-two scale per 32 values, reached through a table of pages.
 //
-// The mathematics.  A row is v_r = 2^(e_r - 12) c_r, e_r its largest block exponent and c_r its codes times
-// 2^(k - e_r + 12): e2m1 has one mantissa bit, so c_r is exact in e5m2 for blocks down to 26 octaves below
-// e_r (lower ones count as zeros).  One byte a value serves as key and as value, and the row's own power
+// The mathematics.  A row is v_r = 2^(e_r - 12) c_r, e_r its largest block exponent, -48 at least, and c_r its codes
+// times 2^(k - e_r + 12): e2m1 has one mantissa bit, so c_r is exact in e5m2 for blocks down to 26 octaves below
+// e_r (lower ones count as zeros).  Exponents above 48 are read as 48 and flagged: with e_r in [-48, 48] the scores'
+// products, P' 2^-e_r and their sums stay normal f32 numbers, and what falls below them is under 2^-34 of a sum.  One byte a value serves as key and as value, and the row's own power
 // of two moves to where the row is a single number: to its scores, and to its probability.
 //  * q = 2^g (hi + 2^-5 lo), hi and lo in e4m3: hi holds q's top four significant bits, lo the four below
 //    them, so a bf16 q (eight) is exact down to 2^-9 of its head's largest value and off by 2^-22 of that
@@ -119,6 +120,7 @@ static_assert(TM_S + 2 * 2 * HM <= TMEM_COLS, "TMEM budget");
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTop = 4;                 // octaves of P' at m
+constexpr int kMaxExp = 48;             // e_r lies in [-kMaxExp, kMaxExp]
 constexpr float kSlack = 4.0f;          // octaves that m may be late
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -291,7 +293,7 @@ __device__ __forceinline__ Unit unit_of(const Params &p, uint32_t u) {
 }
 
 // Heads hh .. hh + n - 1 of a unit's q into [hi | lo], the next two heads in flight; lane i < n gets the scale of head
-// hh + i, 2^g |scale| log2(e), never 0 (see the scores).  ready(), between the first loads and the first store, says
+// hh + i, 2^g |scale| log2(e).  ready(), between the first loads and the first store, says
 // whether to go on.
 template <typename F>
 __device__ __forceinline__ float put_heads(const Params &p, uint32_t sq, uint32_t unit, int hh, int n, int lane, F ready) {
@@ -315,7 +317,7 @@ __device__ __forceinline__ float put_heads(const Params &p, uint32_t sq, uint32_
     for (int i = 0; i < n; ++i) {
         load(v[2], i + 2);
         const int g = put_q(sq, hh + i, v[0], lane, sign);
-        if (lane == i) qs = fmaxf(fabsf(p.scale_log2) * pow2(g), 1.17549435e-38f);
+        if (lane == i) qs = fabsf(p.scale_log2) * pow2(g);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             v[0][k] = v[1][k];
@@ -349,9 +351,9 @@ __device__ __forceinline__ void widen(const uint4 raw, uint32_t y, uint32_t (&o)
             : "r"(w[k]), "r"(sc));
 }
 
-// Four bytes of max(k, low) - low + lift (signed k and low, biased to unsigned so that no byte borrows).
-__device__ __forceinline__ uint32_t above(uint32_t k, uint32_t low, uint32_t lift) {
-    return (__vmaxs4(k, low) ^ 0x80808080u) - (low ^ 0x80808080u) + lift;
+// Four bytes of max(k, low) - low (signed k and low, biased to unsigned so that no byte borrows).
+__device__ __forceinline__ uint32_t above(uint32_t k, uint32_t low) {
+    return (__vmaxs4(k, low) ^ 0x80808080u) - (low ^ 0x80808080u);
 }
 
 // Four probabilities as hi (e4m3) - lo (e5m2): lo from hi - p, which is exact in f32.
@@ -670,13 +672,20 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             for (int k = 0; k < 2; ++k) {
                 const int i = 64 * (warp - W_EXP) + 32 * k + lane;
                 const uint32_t m4 = __vmaxs4(__vmaxs4(ev[k].x, ev[k].y), __vmaxs4(ev[k].z, ev[k].w));
-                const int top = max(max((int)(int8_t)m4, (int)(int8_t)(m4 >> 8)), max((int)(int8_t)(m4 >> 16), (int)m4 >> 24));
-                const uint32_t low = (uint32_t)(uint8_t)max(top - 27, -128) * 0x01010101u;
-                const uint32_t lift = (uint32_t)(uint8_t)(max(top - 27, -128) - (top - 27)) * 0x01010101u;
+                int top = max(max((int)(int8_t)m4, (int)(int8_t)(m4 >> 8)), max((int)(int8_t)(m4 >> 16), (int)m4 >> 24));
+                top = max(top, -kMaxExp);
+                if (top > kMaxExp) {
+                    constexpr uint32_t most = (uint32_t)kMaxExp * 0x01010101u;
+                    ev[k] = make_uint4(__vmins4(ev[k].x, most), __vmins4(ev[k].y, most), __vmins4(ev[k].z, most),
+                                       __vmins4(ev[k].w, most));
+                    top = kMaxExp;
+                    flag_status(p.a.status, DS_DEV_BAD_VALUE);
+                }
+                const uint32_t low = (uint32_t)(uint8_t)(top - 27) * 0x01010101u;
                 const uint32_t on = i < count ? kAll : 0u;
                 reinterpret_cast<uint4 *>(ctl + C_EXPS)[(n % NR) * BN + i] =
-                    make_uint4(above(ev[k].x, low, lift) & on, above(ev[k].y, low, lift) & on, above(ev[k].z, low, lift) & on,
-                               above(ev[k].w, low, lift) & on);
+                    make_uint4(above(ev[k].x, low) & on, above(ev[k].y, low) & on, above(ev[k].z, low) & on,
+                               above(ev[k].w, low) & on);
                 reinterpret_cast<int8_t *>(ctl + C_TOPS)[(n % NR) * BN + i] = (int8_t)top;
             }
             __syncwarp();

@@ -36,6 +36,7 @@ DS_ECUDA = -4
 DS_EDEVICE = -5
 DS_DEV_TIMEOUT = 1
 DS_DEV_BAD_INDEX = 2
+DS_DEV_BAD_VALUE = 4
 
 _P = ctypes.c_void_p
 _i32, _i64, _f32, _sz = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t

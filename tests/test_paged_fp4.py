@@ -975,3 +975,69 @@ def test_attention_large_row_without_weight(ds, b, h, topk, octaves):
     few = check_by_weight(ds, q, codes, exps, bt, sink, idx[..., rest].contiguous())
     worst = (o - few).float().abs()[:, :, 0::2].amax() / few.float().abs()[:, :, 0::2].amax()
     assert worst <= 2.0 ** -6
+
+
+@gpu
+@pytest.mark.parametrize("b,h,topk", [(2, 24, 200), (1, 70, 900)])
+@pytest.mark.parametrize("k", [45, 20, -20, -45, -60, -71])
+def test_attention_exponent_range(ds, b, h, topk, k):
+    """All rows near one end of the exponents that are read as they are."""
+    q, codes, exps, bt, sink, idx, *_ = attention_inputs(43, b, 1, h, 1000, topk, 0.1, 16, 0)
+    q = (q.float() * 2.0 ** -k).to(torch.bfloat16)
+    check_by_weight(ds, q, codes, exps + k, bt, sink, idx)
+    # exponents of a block apart too: 26 below the row's largest still count
+    wide = exps + k
+    wide[..., 1::2] = max(k, -48) - 23
+    check_by_weight(ds, q, codes, wide, bt, sink, idx)
+
+
+@gpu
+@pytest.mark.parametrize("b,h,topk", [(2, 24, 200), (1, 70, 900)])
+def test_attention_both_ends_of_the_exponents(ds, b, h, topk):
+    """Rows at 2^48 beside rows at 2^-48: with the scores of order one, and with the large rows far below."""
+    q, codes, exps, bt, sink, idx, *_ = attention_inputs(45, b, 1, h, 1000, topk, 0.0, 16, 0)
+    odd = torch.zeros((b, 1000), dtype=torch.bool)
+    for i in range(b):
+        odd[i, idx[i, 0, 1::2].long()] = True
+    sign = torch.where(torch.rand(512, generator=torch.Generator().manual_seed(1)) < 0.5, -1.0, 1.0)
+    code = torch.where(sign < 0, 10, 2).to(torch.uint8)
+    for i in range(b):
+        for r in range(1000):
+            exps[bt[i, r // 16], r % 16] = 48 if odd[i, r] else -48
+    check_by_weight(ds, q, codes, exps, bt, sink, idx, scale=2.0 ** -48 * 512 ** -0.5)
+    for i in range(b):
+        for r in torch.nonzero(odd[i])[:, 0].tolist():
+            codes[bt[i, r // 16], r % 16] = code[0::2] | code[1::2] << 4
+    low = (q.float() - 20 * sign).to(torch.bfloat16)               # their scores: about -512
+    o = check_by_weight(ds, low, codes, exps, bt, torch.full_like(sink, -math.inf), idx, scale=2.0 ** -48 * 0.05)
+    assert (o.abs() < 2.0 ** -44).all() and (o != 0).any(-1).all()
+
+
+@gpu
+@pytest.mark.parametrize("b,h,topk", [(2, 24, 200), (1, 70, 900)])
+def test_attention_exponents_outside_the_range(ds, b, h, topk):
+    """Above 48: read as 48, and said so; below -74: zeros."""
+    q, codes, exps, bt, sink, idx, *_ = attention_inputs(47, b, 1, h, 1000, topk, 0.1, 16, 0)
+    q = (q.float() * 2.0 ** -48).to(torch.bfloat16)
+    for lo, hi in ((49, 127), (40, 60), (110, 121)):
+        high = torch.randint(lo, hi + 1, exps.shape, generator=torch.Generator().manual_seed(lo), dtype=torch.int8)
+        check_by_weight(ds, q, codes, high, bt, sink, idx, status=ds.DS_DEV_BAD_VALUE, read=high.clamp(max=48))
+    # one block of one listed row is enough; of a row that is not listed, none counts
+    one = torch.zeros_like(exps)
+    r = int(idx[0, 0][idx[0, 0] >= 0][5])
+    unlisted = next(x for x in range(1000) if x not in idx[0, 0].tolist())
+    one[bt[0, unlisted // 16], unlisted % 16] = 100
+    check_by_weight(ds, q, codes, one, bt, sink, idx)
+    one[bt[0, r // 16], r % 16, 7] = 49
+    check_by_weight(ds, q, codes, one, bt, sink, idx, status=ds.DS_DEV_BAD_VALUE, read=one.clamp(max=48))
+    for lo, hi in ((-128, -75), (-128, -128), (-101, -100)):
+        tiny = torch.randint(lo, hi + 1, exps.shape, generator=torch.Generator().manual_seed(hi + 200), dtype=torch.int8)
+        assert (check_by_weight(ds, q, codes, tiny, bt, sink, idx, read=torch.zeros_like(tiny) - 128) == 0).all()
+
+
+@gpu
+def test_attention_tiny_scales_of_queries(ds):
+    """Queries and scales whose product lies below the normal f32 numbers: scores of 0, not of a clamped scale."""
+    q, codes, exps, bt, sink, idx, *_ = attention_inputs(49, 2, 1, 24, 300, 200, 0.0, 16, 0)
+    for qs, scale in ((2.0 ** -126, 1e-3), (2.0 ** -130, 1.0), (1.0, 0.0), (0.0, 1.0), (2.0 ** -120, -1e-5)):
+        check_by_weight(ds, (q.float() * qs).to(torch.bfloat16), codes, exps + 44, bt, sink, idx, scale=scale)
