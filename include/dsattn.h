@@ -361,9 +361,10 @@ int ds_indexer_topk(const uint16_t *q, const uint16_t *k, const float *w, int b,
  * window rows first, the compressed rows behind them, so that the rows of ds_window_topk_idxs and
  * ds_indexer_topk (offset = window) are used as they are.  17/32 byte a value.
  *
- * In the three calls below first[bi] is the position (>= 0) of the sequence's first token of this
- * call, and lens[bi], where given, how many of the s tokens it has (the others are padding: their
- * values do not matter, and what they would write is left as it was).  A position outside the
+ * In the calls below first[bi] is the position (>= 0) of the sequence's first token of this call,
+ * and lens[bi], in the calls that take it, how many of the tokens it has (the others are padding:
+ * their values, positions and index rows do not matter, and what they would write is left as it
+ * was).  A position outside the
  * table, or a row whose page is not in the block table or not one of the pages, raises
  * DS_DEV_BAD_INDEX; what it would have written is left as it was.  codes and exps may be NULL when
  * there are no pages, and block_table when max_pages is 0.
@@ -450,6 +451,16 @@ int ds_sparse_attn_fp4_paged(const uint16_t *q, const uint8_t *codes, const int8
                              int topk, float scale, uint16_t *o, int b, int m, int h, int d, void *workspace,
                              size_t workspace_bytes, int rd, const float *table, int64_t table_rows,
                              const int32_t *first, ds_stream_t stream);
+
+/*
+ * ds_sparse_attn_fp4_paged_ragged -- ds_sparse_attn_fp4_paged of a padded batch: lens (device int32
+ * [b], or NULL for m) says how many of a sequence's m tokens there are.  The same workspace.
+ */
+int ds_sparse_attn_fp4_paged_ragged(const uint16_t *q, const uint8_t *codes, const int8_t *exps, int64_t pages, int page,
+                                    const int32_t *block_table, int max_pages, const float *sink, const int32_t *idx,
+                                    int topk, float scale, uint16_t *o, int b, int m, int h, int d, void *workspace,
+                                    size_t workspace_bytes, int rd, const float *table, int64_t table_rows,
+                                    const int32_t *first, const int32_t *lens, ds_stream_t stream);
 
 /*
  * ds_device_status -- synchronise `stream`, then read and clear the current device's status word

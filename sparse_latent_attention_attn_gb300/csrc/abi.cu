@@ -329,6 +329,30 @@ bool store_there(const uint8_t *codes, const int8_t *exps, int64_t pages, const 
     return (pages == 0 || (codes && exps)) && (max_pages == 0 || block_table);
 }
 bool pool_fits(int64_t pages, int page) { return pages <= INT32_MAX / page; }
+
+// ds_sparse_attn_fp4_paged and ds_sparse_attn_fp4_paged_ragged (lens null: m tokens of every sequence)
+int sparse_attn_fp4(const uint16_t *q, const uint8_t *codes, const int8_t *exps, int64_t pages, int page,
+                    const int32_t *block_table, int max_pages, const float *sink, const int32_t *idx, int topk, float scale,
+                    uint16_t *o, int b, int m, int h, int d, void *workspace, size_t workspace_bytes, int rd,
+                    const float *table, int64_t table_rows, const int32_t *first, const int32_t *lens, ds_stream_t stream) {
+    if (b < 0 || m < 0 || topk < 0 || h < 1 || !pool_ok(pages, page, max_pages)) return DS_EINVAL;
+    if (!rotation_ok(rd, d, table, table_rows)) return DS_EINVAL;
+    if (d != 512 || h > 128 || !pool_fits(pages, page) || !sparse_attn_fp4_fits(b, m, topk)) return DS_EUNSUPPORTED;
+    if ((int64_t)b * m == 0) return DS_OK;
+    if (!q || !o || !sink || (rd > 0 && !first)) return DS_EINVAL;
+    if (topk > 0 && (!idx || !store_there(codes, exps, pages, block_table, max_pages))) return DS_EINVAL;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(codes) || !aligned16(exps)) return DS_EINVAL;
+    if (!aligned4(sink) || !aligned4(idx) || !aligned4(block_table) || !aligned4(first) || !aligned4(lens)) return DS_EINVAL;
+    if (topk > 0 && workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return DS_EWORKSPACE;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (topk == 0 && !lens)   // nothing to attend to: every output is 0
+        return cudaMemsetAsync(o, 0, (size_t)b * m * h * d * sizeof(uint16_t), st) == cudaSuccess ? DS_OK : DS_ECUDA;
+    const fp4::Args a{q, codes, exps, pages, page, block_table, max_pages, sink, idx, topk, scale, o, b, m, h,
+                      workspace, workspace_bytes, rd, reinterpret_cast<const float2 *>(table), table_rows, first, lens,
+                      status_word()};
+    if (!a.status) return DS_ECUDA;
+    return topk == 0 ? launch_sparse_attn_fp4_none(a, st) : launch_sparse_attn_fp4(a, st);
+}
 }  // namespace
 
 int ds_norm_rotary(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint16_t *y, int b, int s, int h, int d,
@@ -383,23 +407,18 @@ int ds_sparse_attn_fp4_paged(const uint16_t *q, const uint8_t *codes, const int8
                              size_t workspace_bytes, int rd, const float *table, int64_t table_rows,
                              const int32_t *first, ds_stream_t stream) {
     const Range range("ds_sparse_attn_fp4_paged");
-    if (b < 0 || m < 0 || topk < 0 || h < 1 || !pool_ok(pages, page, max_pages)) return DS_EINVAL;
-    if (!rotation_ok(rd, d, table, table_rows)) return DS_EINVAL;
-    if (d != 512 || h > 128 || !pool_fits(pages, page) || !sparse_attn_fp4_fits(b, m, topk)) return DS_EUNSUPPORTED;
-    if ((int64_t)b * m == 0) return DS_OK;
-    if (!q || !o || !sink || (rd > 0 && !first)) return DS_EINVAL;
-    if (topk > 0 && (!idx || !store_there(codes, exps, pages, block_table, max_pages))) return DS_EINVAL;
-    if (!aligned16(q) || !aligned16(o) || !aligned16(codes) || !aligned16(exps)) return DS_EINVAL;
-    if (!aligned4(sink) || !aligned4(idx) || !aligned4(block_table) || !aligned4(first)) return DS_EINVAL;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (topk == 0)   // nothing to attend to: every output is 0
-        return cudaMemsetAsync(o, 0, (size_t)b * m * h * d * sizeof(uint16_t), st) == cudaSuccess ? DS_OK : DS_ECUDA;
-    if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return DS_EWORKSPACE;
-    const fp4::Args a{q, codes, exps, pages, page, block_table, max_pages, sink, idx, topk, scale, o, b, m, h,
-                      workspace, workspace_bytes, rd, reinterpret_cast<const float2 *>(table), table_rows, first,
-                      status_word()};
-    if (!a.status) return DS_ECUDA;
-    return launch_sparse_attn_fp4(a, st);
+    return sparse_attn_fp4(q, codes, exps, pages, page, block_table, max_pages, sink, idx, topk, scale, o, b, m, h, d,
+                           workspace, workspace_bytes, rd, table, table_rows, first, nullptr, stream);
+}
+
+int ds_sparse_attn_fp4_paged_ragged(const uint16_t *q, const uint8_t *codes, const int8_t *exps, int64_t pages, int page,
+                                    const int32_t *block_table, int max_pages, const float *sink, const int32_t *idx,
+                                    int topk, float scale, uint16_t *o, int b, int m, int h, int d, void *workspace,
+                                    size_t workspace_bytes, int rd, const float *table, int64_t table_rows,
+                                    const int32_t *first, const int32_t *lens, ds_stream_t stream) {
+    const Range range("ds_sparse_attn_fp4_paged_ragged");
+    return sparse_attn_fp4(q, codes, exps, pages, page, block_table, max_pages, sink, idx, topk, scale, o, b, m, h, d,
+                           workspace, workspace_bytes, rd, table, table_rows, first, lens, stream);
 }
 
 void ds_test_set_stall(int on) {

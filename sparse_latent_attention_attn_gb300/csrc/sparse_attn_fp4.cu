@@ -125,8 +125,8 @@ constexpr float kSlack = 4.0f;          // octaves that m may be late
 constexpr uint32_t kAll = 0xffffffffu;
 
 // messages: kind | first tile of its unit << 8 | last << 9 | the unit is whole << 10 | the range's first << 11 |
-// rows << 16
-constexpr int kTile = 1, kFin = 2, kFirst = 1 << 8, kLast = 1 << 9, kWhole = 1 << 10, kSlot0 = 1 << 11;
+// the unit is padding << 12 | rows << 16
+constexpr int kTile = 1, kFin = 2, kFirst = 1 << 8, kLast = 1 << 9, kWhole = 1 << 10, kSlot0 = 1 << 11, kPad = 1 << 12;
 
 // a partial slot (f32): O [64][512], then running maxima m [64] (octaves, -inf: no row) and sums l [64]
 constexpr int SLOT_O = HM * D;
@@ -413,6 +413,13 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
     for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// whether a token lies behind its sequence's last one: nothing is read for it (but its q) or written
+__device__ __forceinline__ bool is_padding(const Args &a, int tok) {
+    if (!a.lens) return false;
+    const uint32_t bi = (uint32_t)tok / (uint32_t)a.m;
+    return tok - (int)bi * a.m >= __ldg(a.lens + bi);
+}
+
 // sin and cos of the output's rotation back, or null
 __device__ __forceinline__ const float2 *rotation_row(const Args &a, int tok, bool flag) {
     const uint32_t bi = (uint32_t)tok / (uint32_t)a.m;
@@ -515,8 +522,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             const int32_t *idx = p.a.idx + (int64_t)un.tok * T;
             const int32_t *bt = p.a.block_table + (int64_t)((uint32_t)un.tok / (uint32_t)p.a.m) * p.a.max_pages;
             const int a = u == u0 ? (int)(e0 - (int64_t)u * T) : 0;
-            const int z = (int)min((int64_t)T, e1 - (int64_t)u * T);
-            const int tile = kTile | (a == 0 && z == T ? kWhole : 0) | (u == u0 ? kSlot0 : 0);
+            int z = (int)min((int64_t)T, e1 - (int64_t)u * T);
+            int tile = kTile | (a == 0 && z == T ? kWhole : 0) | (u == u0 ? kSlot0 : 0);
+            if (is_padding(p.a, un.tok)) {      // one tile of no rows, whose output is not written
+                z = a;
+                tile |= kPad;
+            }
             int fill = 0, first = kFirst;
             int nxt[4];
 #pragma unroll
@@ -642,7 +653,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             if (tile & kLast) ++unit;
             if (tile & kFirst) {
                 // P V of tile J - 2 is done, so the softmax is through with the scales of two units ago
-                if (lane < (seg == 0 ? QROWS : 8)) reinterpret_cast<float *>(ctl + C_QS)[(seg & 1u) * HM + 8 * w + lane] = qs;
+                if (lane < (seg == 0 ? QROWS : 8)) reinterpret_cast<float *>(ctl + C_QS)[((u0 + seg) & 1u) * HM + 8 * w + lane] = qs;
                 ++seg;
             }
             fence_proxy_async_smem();
@@ -772,12 +783,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
         const float *qs = reinterpret_cast<const float *>(ctl + C_QS);
         uint64_t l[HPW / 2];   // sums of P' 2^-e over this thread's rows, in pairs of heads
         float m = 0.0f;        // of head hl
-        uint32_t unit = u0, seg = 0;
+        uint32_t unit = u0;
         bool bad = false;
         head[hl] = 0.0f;
         if (e0 < e1) {
             const float s = put_heads(p, base + SM_Q, unit, 8 * warp + QROWS, 8 - QROWS, lane, [] { return true; });
-            if (lane < 8 - QROWS) const_cast<float *>(qs)[8 * warp + QROWS + lane] = s;
+            if (lane < 8 - QROWS) const_cast<float *>(qs)[(u0 & 1u) * HM + 8 * warp + QROWS + lane] = s;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -801,16 +812,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
             bool late = true;      // m has to move
             if (!bad) bad = !warp_wait(BAR(B_S + st), (J >> 1) & 1u, abort_flag);
             if (!bad) {
-                if (first) {
-                    ++seg;
-                    m = 0.0f;
-                }
+                if (first) m = 0.0f;
                 tc_fence_after();
                 e = (int)reinterpret_cast<const int8_t *>(ctl + C_REXP)[st * BN + row];
                 const float c = pow2(e - 12);
                 const float e4 = (float)(e + kTop);
                 const uint64_t cr = pair(c, c), low = pair(0.03125f, 0.03125f), er = pair(e4, e4);
-                const float *q = qs + ((seg - 1) & 1u) * HM + hb;
+                const float *q = qs + (unit & 1u) * HM + hb;
 #pragma unroll
                 for (int j = 0; j < HPW; j += 16) {
                     uint32_t r0[16], r1[16];
@@ -938,7 +946,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 // what the output needs from memory, fetched while P V of the last tile runs
                 float sink = 0.0f;
                 const float2 *cs = nullptr;
-                if (whole) {
+                if (whole && !(msg & kPad)) {
                     if (hl < un.nh) sink = __ldg(p.a.sink + un.h0 + hl) * kLog2e;
                     if constexpr (ROPE) cs = rotation_row(p.a, un.tok, threadIdx.x == 0);
                 }
@@ -960,7 +968,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 head[hl] = 0.0f;
                 __syncwarp();
 #pragma unroll 1
-                for (int k = 0; k < 2 * NPAN; ++k) {
+                for (int k = msg & kPad ? 2 * NPAN : 0; k < 2 * NPAN; ++k) {
                     const int c = k >> 1, h0 = hb + (k & 1) * 16, d = c * 128 + row;
                     if (h0 >= un.nh) continue;
                     uint32_t r[16];
@@ -1054,7 +1062,7 @@ __global__ void __launch_bounds__(32 * kCombineHeads) combine_kernel(const P p) 
     const int4 c = cut_of(p, blockIdx.x);
     const int tok = token_at((uint32_t)(p.groups == 1 ? c.x : c.x >> 1), p.ntok, p.interleave);
     const int h0 = p.groups == 1 ? 0 : (c.x & 1) * HM, hh = blockIdx.y * kCombineHeads + (threadIdx.x >> 5);
-    if (hh >= HM || h0 + hh >= p.a.h) return;
+    if (hh >= HM || h0 + hh >= p.a.h || is_padding(p.a, tok)) return;
     auto part = [&](int i) { return p.ws + ((size_t)(c.y + i) * 2 + (((uint32_t)c.w >> i) & 1u)) * SLOT; };
     // lane i: statistics of part i (at most 32), and columns 128 j + 4 i .. of every part
     const int lane = threadIdx.x & 31;
@@ -1119,6 +1127,13 @@ __global__ void __launch_bounds__(32 * kCombineHeads) combine_kernel(const P p) 
         }
         *reinterpret_cast<uint2 *>(o + d) = make_uint2(pack_bf16x2(acc[j].x, acc[j].y), pack_bf16x2(acc[j].z, acc[j].w));
     }
+}
+
+__global__ void __launch_bounds__(256) none_kernel(const Args a) {
+    const int tok = blockIdx.x;
+    if (is_padding(a, tok)) return;
+    uint4 *o = reinterpret_cast<uint4 *>(a.o + (int64_t)tok * a.h * D);
+    for (int i = threadIdx.x; i < a.h * (D / 8); i += 256) o[i] = make_uint4(0, 0, 0, 0);
 }
 
 // ---- host side ---------------------------------------------------------------------------------------
@@ -1221,6 +1236,11 @@ size_t sparse_attn_fp4_workspace_bytes(int b, int m, int h, int topk) {
     if (topk == 0 || (int64_t)b * m == 0) return 0;
     const fp4::Plan *pl = fp4::plan(b, m, h, topk);
     return pl ? fp4::workspace_bytes(*pl) : 0;
+}
+
+int launch_sparse_attn_fp4_none(const fp4::Args &a, cudaStream_t stream) {
+    fp4::none_kernel<<<(unsigned)(a.b * a.m), 256, 0, stream>>>(a);
+    return launch_status();
 }
 
 int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream) {

@@ -27,6 +27,7 @@ struct Args {
     const float2 *table;
     int64_t table_rows;
     const int32_t *first;       // [b] position of each sequence's first query
+    const int32_t *lens;        // [b] tokens of each sequence, or null: m of each
     unsigned int *status;
 };
 
@@ -37,5 +38,7 @@ bool sparse_attn_fp4_fits(int b, int m, int topk);
 size_t sparse_attn_fp4_workspace_bytes(int b, int m, int h, int topk);
 void set_test_stall_fp4(bool on);
 int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream);
+// o = 0 for the tokens that there are (a list of no entries)
+int launch_sparse_attn_fp4_none(const fp4::Args &a, cudaStream_t stream);
 
 }  // namespace dsattn

@@ -86,6 +86,8 @@ _lib.ds_sparse_attn_fp4_paged_workspace_bytes.restype = _sz
 _lib.ds_sparse_attn_fp4_paged.argtypes = [_P, _P, _P, _i64, _i32, _P, _i32, _P, _P, _i32, _f32, _P, _i32, _i32, _i32,
                                           _i32, _P, _sz, _i32, _P, _i64, _P, _P]
 _lib.ds_sparse_attn_fp4_paged.restype = _i32
+_lib.ds_sparse_attn_fp4_paged_ragged.argtypes = [*_lib.ds_sparse_attn_fp4_paged.argtypes[:-1], _P, _P]
+_lib.ds_sparse_attn_fp4_paged_ragged.restype = _i32
 _lib.ds_test_set_stall.argtypes = [_i32]
 _lib.ds_test_set_stall.restype = None
 _lib.ds_test_set_kernel.argtypes = [_i32]
@@ -515,9 +517,10 @@ def sparse_attn_fp4_paged(q: torch.Tensor, codes: torch.Tensor, exps: torch.Tens
                           sink: torch.Tensor, idx: torch.Tensor, scale: float, rd: int = 0,
                           table: torch.Tensor | None = None, first: torch.Tensor | None = None,
                           o: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                          stream=None) -> torch.Tensor:
+                          stream=None, lens: torch.Tensor | None = None) -> torch.Tensor:
     """``sparse_attn`` over the paged 4-bit row store (``idx`` lists logical rows of each sequence); with
-    ``rd`` > 0 the last ``rd`` values of token t's output are rotated back by position ``first[b] + t``."""
+    ``rd`` > 0 the last ``rd`` values of token t's output are rotated back by position ``first[b] + t``.
+    Tokens at or behind ``lens[b]`` leave ``o`` as it was (zeros in a new one)."""
     if q.dim() != 4 or idx.dim() != 3 or codes.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be [b][m][h][d], idx [b][m][topk], codes [pages][page][d/2] and block_table [b][max_pages]")
     b, m, h, d = q.shape
@@ -531,21 +534,21 @@ def sparse_attn_fp4_paged(q: torch.Tensor, codes: torch.Tensor, exps: torch.Tens
             and _fits(exps, _I8, (pages, page, d // 32), dev) and block_table.dtype is _I32 and tables == b
             and block_table.is_contiguous() and block_table.get_device() == dev and _row_fits(sink, _F32, h, dev)
             and idx.dtype is _I32 and ib == b and im == m and idx.is_contiguous() and idx.get_device() == dev
-            and (o is None or _fits(o, _BF16, (b, m, h, d), dev))
+            and (o is None or _fits(o, _BF16, (b, m, h, d), dev)) and (lens is None or _row_fits(lens, _I32, b, dev))
             and (rd == 0 or (table is not None and _fits(table, _F32, tab, dev) and first is not None
                              and _row_fits(first, _I32, b, dev)))
             and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))):
         _refuse(q=(q, _BF16, q.shape), codes=(codes, _U8, (pages, page, d // 2)), exps=(exps, _I8, (pages, page, d // 32)),
                 block_table=(block_table, _I32, (b, max_pages)), sink=(sink, _F32, (h,)), idx=(idx, _I32, (b, m, topk)),
-                **({"o": (o, _BF16, q.shape)} if o is not None else {}),
+                **({"o": (o, _BF16, q.shape)} if o is not None else {}), **({"lens": (lens, _I32, (b,))} if lens is not None else {}),
                 **({"table": (table, _F32, tab), "first": (first, _I32, (b,))} if rd else {}),
                 **({"workspace": (workspace, workspace.dtype, workspace.shape)} if workspace is not None else {}))
     if o is None:
-        if stream is None:
+        if stream is None and lens is None:
             o = torch.empty_like(q)
         else:
             with _on(stream):
-                o = torch.empty_like(q)
+                o = torch.empty_like(q) if lens is None else torch.zeros_like(q)
     ws, ws_bytes = None, 0
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -558,11 +561,14 @@ def sparse_attn_fp4_paged(q: torch.Tensor, codes: torch.Tensor, exps: torch.Tens
                 with _on(stream):
                     workspace = torch.empty(need, dtype=_U8, device=q.device)
             ws, ws_bytes = workspace.data_ptr(), need
-    st = _lib.ds_sparse_attn_fp4_paged(q.data_ptr(), codes.data_ptr(), exps.data_ptr(), pages, page,
-                                       block_table.data_ptr(), max_pages, sink.data_ptr(), idx.data_ptr(), topk, scale,
-                                       o.data_ptr(), b, m, h, d, ws, ws_bytes, rd, table.data_ptr() if rd else None,
-                                       tab[0] if rd else 0, first.data_ptr() if rd else None,
-                                       _raw_stream(dev) if stream is None else stream.cuda_stream)
+    args = (q.data_ptr(), codes.data_ptr(), exps.data_ptr(), pages, page, block_table.data_ptr(), max_pages,
+            sink.data_ptr(), idx.data_ptr(), topk, scale, o.data_ptr(), b, m, h, d, ws, ws_bytes, rd,
+            table.data_ptr() if rd else None, tab[0] if rd else 0, first.data_ptr() if rd else None)
+    on = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if lens is None:
+        st = _lib.ds_sparse_attn_fp4_paged(*args, on)
+    else:
+        st = _lib.ds_sparse_attn_fp4_paged_ragged(*args, lens.data_ptr(), on)
     if st:
         _check("ds_sparse_attn_fp4_paged", st)
     return o

@@ -59,10 +59,15 @@ def decode_step_fp4_paged(q: torch.Tensor, new_kv: torch.Tensor, codes: torch.Te
     """q [b][s][h][d] and new_kv [b][s][d] as their projections leave them (neither is modified); the token
     (bi, t) is at position first[bi] + t; codes, exps, block_table: the paged store, whose logical rows
     are the ring's `window` slots, then the compressed rows; idx [b][s][topk] lists logical rows, complete.
-    s > 1 stores all s rows before any query reads them: a query whose ring is full then misses the rows
-    that later tokens of the step replaced."""
+    Tokens at or behind lens[bi] are padding: nothing of theirs is stored, and o is left as it was (zeros in a
+    new one).  s > 1 stores all s rows before any query reads them: a query whose ring is full then misses the
+    rows that later tokens of the step replaced."""
     dsattn.kv_append_fp4_paged(new_kv, codes, exps, block_table, first, rd=rd, table=table, eps=eps, weight=kv_weight,
                                lens=lens, window=window, stream=stream)
-    qn = dsattn.norm_rotary(q, eps, rd, table, first, lens=lens, stream=stream)
+    qn = None
+    if lens is not None:                   # the padding of q is not read: no zeros for it
+        with dsattn._on(stream):
+            qn = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    qn = dsattn.norm_rotary(q, eps, rd, table, first, lens=lens, y=qn, stream=stream)
     return dsattn.sparse_attn_fp4_paged(qn, codes, exps, block_table, sink, idx, scale, rd=rd, table=table,
-                                        first=first, o=o, workspace=workspace, stream=stream)
+                                        first=first, o=o, workspace=workspace, stream=stream, lens=lens)

@@ -1041,3 +1041,107 @@ def test_attention_tiny_scales_of_queries(ds):
     q, codes, exps, bt, sink, idx, *_ = attention_inputs(49, 2, 1, 24, 300, 200, 0.0, 16, 0)
     for qs, scale in ((2.0 ** -126, 1e-3), (2.0 ** -130, 1.0), (1.0, 0.0), (0.0, 1.0), (2.0 ** -120, -1e-5)):
         check_by_weight(ds, (q.float() * qs).to(torch.bfloat16), codes, exps + 44, bt, sink, idx, scale=scale)
+
+
+# ---- padded batches -----------------------------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("b,m,h,topk", [(4, 5, 40, 150), (3, 2, 128, 700), (60, 4, 5, 33), (5, 1, 70, 0)])
+def test_attention_of_a_padded_batch(ds, b, m, h, topk):
+    """Tokens behind their sequence's last one: their q, positions and index rows do not matter, and o is left as
+    it was; the others are those of the call without lengths."""
+    g = torch.Generator().manual_seed(51)
+    q, codes, exps, bt, sink, idx, *_ = attention_inputs(51, b, m, h, 900, topk, 0.1, 16, 64)
+    lens = torch.randint(0, m + 1, (b,), generator=g, dtype=torch.int32)
+    lens[0], lens[1], lens[2] = 0, m + 3, -1
+    live = torch.arange(m) < lens[:, None]
+    tab = table_of(64 + m, 64)
+    first = torch.where(lens > 0, 64 + m - lens.clamp(0, m), -9).to(torch.int32)     # padding: behind the table
+    args = dev(q, codes, exps, bt, sink, idx)
+    want = ds.sparse_attn_fp4_paged(*args, 512 ** -0.5)
+    assert ds.device_status() == 0
+    bad_q, bad_idx = q.clone(), idx.clone()
+    bad_q[~live] = float("nan")
+    bad_idx[~live] = 2 ** 31 - 1
+    o = torch.full_like(args[0], 7.0)
+    ds.sparse_attn_fp4_paged(bad_q.cuda(), *args[1:5], bad_idx.cuda(), 512 ** -0.5, lens=lens.cuda(), o=o)
+    assert ds.device_status() == 0
+    assert torch.equal(o.cpu()[live], want.cpu()[live]) and (o.cpu()[~live] == 7).all()
+    more = dict(rd=64, table=tab.cuda(), first=first.cuda())
+    turned = ds.sparse_attn_fp4_paged(bad_q.cuda(), *args[1:5], bad_idx.cuda(), 512 ** -0.5, lens=lens.cuda(), **more)
+    assert ds.device_status() == 0 and (turned.cpu()[~live] == 0).all()
+    for i in range(b):
+        n = min(max(int(lens[i]), 0), m)
+        for t in range(n):
+            ix = idx[i, t].numpy()
+            if topk == 0:
+                assert (turned[i, t] == 0).all()
+                continue
+            rows, tops = logical_rows(codes, exps, bt, i, ix, 16)
+            ref, A, F = attention_by_weight(f64(q[i, t]), rows, ix >= 0, f64(sink), 512 ** -0.5, tops)
+            ref, A, F = rotate(ref, f64(tab)[int(first[i]) + t], inverse=True), pair_sum(A, 64), pair_sum(F, 64)
+            tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * A + 2.0 ** -17 * F
+            assert (np.abs(f64(turned[i, t]) - ref) <= tol).all()
+    with pytest.raises((TypeError, ValueError)):
+        ds.sparse_attn_fp4_paged(*args, 0.1, lens=lens.cuda().long())
+    with pytest.raises((TypeError, ValueError)):
+        ds.sparse_attn_fp4_paged(*args, 0.1, lens=lens[:-1].cuda())
+
+
+@gpu
+def test_step_of_several_tokens_in_a_padded_batch(ds):
+    """Three tokens a step, some sequences with fewer or none (their pages and position then do not matter, and the
+    padding lies behind the table), a ring that is full and holds the step's tokens beside the window: every
+    token against 64 bits."""
+    from sparse_latent_attention_attn_gb300 import path
+    g = torch.Generator().manual_seed(8)
+    b, s, h, d, rd, window, page, eps = 5, 3, 20, 512, 64, 12, 5, 1e-6
+    ring = window + s - 1                                  # slots: the window of the first token and the later ones
+    codes, exps, bt = random_pool(g, b, ring, page, d)
+    tab = table_of(60, rd)
+    w = 1 + 0.1 * torch.randn((d,), generator=g)
+    sink = torch.randn((h,), generator=g)
+    q = torch.randn((b, s, h, d), generator=g).to(torch.bfloat16)
+    kv = torch.randn((b, s, d), generator=g).to(torch.bfloat16)
+    first, lens = ints(40, 57, 3, 59, -5), ints(3, 3, 2, 1, 0)
+    bt[4] = -1
+    live = torch.arange(s) < lens[:, None]
+    idx = torch.full((b, s, window), 2 ** 31 - 1, dtype=torch.int32)
+    for i in range(b):
+        for t in range(int(lens[i])):
+            pos = torch.arange(int(first[i]) + t - window + 1, int(first[i]) + t + 1)
+            idx[i, t] = torch.where(pos >= 0, pos % ring, -1)
+    q[~live], kv[~live] = float("nan"), float("nan")
+    qg, kg, cg, eg, btg, fg, sg, ig, tg, wg, lg = dev(q, kv, codes, exps, bt, first, sink, idx, tab, w, lens)
+    o = torch.full_like(qg, 7.0)
+    for given in (o, None):
+        got = path.decode_step_fp4_paged(qg, kg, cg, eg, btg, fg, sg, ig, ring, d ** -0.5, rd, tg, eps, kv_weight=wg,
+                                         lens=lg, o=given)
+        assert ds.device_status() == 0
+        assert (got.cpu()[~live] == (0 if given is None else 7)).all()
+    assert torch.equal(got.cpu()[live], o.cpu()[live])
+    zero = torch.where(live[..., None], kv, 0)
+    ref_c, ref_e, _ = append_reference(zero, w, eps, rd, table_of(70, rd), first.clamp(min=0), lens, 1, 0, ring, codes, exps,
+                                       bt, torch.zeros_like(kv))
+    np.testing.assert_array_equal(cg.cpu().numpy(), ref_c)
+    np.testing.assert_array_equal(eg.cpu().numpy(), ref_e)
+    for i in range(b):
+        for t in range(int(lens[i])):
+            cs = f64(tab)[int(first[i]) + t][None]
+            zq = f64(torch.from_numpy(rotate(normed(f64(q[i, t]), None, eps), cs)).to(torch.bfloat16))
+            rr, tops = logical_rows(torch.from_numpy(ref_c), torch.from_numpy(ref_e), bt, i, idx[i, t].numpy(), page)
+            ref, A, F = attention_by_weight(zq, rr, idx[i, t].numpy() >= 0, f64(sink), d ** -0.5, tops)
+            ref = rotate(ref, cs, inverse=True)
+            A, F = pair_sum(A, rd), pair_sum(F, rd)
+            # q may be one bf16 step off where the norm's f32 falls on the other side of a border
+            tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -10) * A + 2.0 ** -17 * F
+            assert (np.abs(f64(got[i, t]) - ref) <= tol).all()
+
+
+def test_attention_of_a_padded_batch_refusals(lib):
+    base = dict(q=FAKE, codes=FAKE, exps=FAKE, pages=4, page=16, bt=FAKE, mp=1, sink=FAKE, idx=FAKE, topk=4, scale=0.1,
+                o=FAKE, b=1, m=1, h=4, d=512, ws=None, wsb=0, rd=0, table=None, rows=0, first=None, lens=FAKE, stream=None)
+    f = lib.ds_sparse_attn_fp4_paged_ragged
+    for bad in (dict(lens=FAKE + 2), dict(lens=FAKE + 1, topk=0), dict(q=None), dict(o=FAKE + 8), dict(h=0), dict(rd=16, rows=9)):
+        assert call(f, base, **bad) == -1, bad
+    assert call(f, base, h=129) == -2 and call(f, base, b=0, q=None, o=None, sink=None) == 0
