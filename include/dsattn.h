@@ -441,7 +441,7 @@ int ds_kv_append_fp4_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstri
  * workspace  at least ds_sparse_attn_fp4_paged_workspace_bytes(b, m, h, d, topk) bytes, 256-byte
  *            aligned (may be NULL when that size is 0); its contents need no initialisation and
  *            mean nothing afterwards.  Calls that may run at the same time need one each.
- * Supported: d = 512, 1 <= h <= 128; pages * page < 2^31, b * m < 2^30.  q, o, codes and exps
+ * Supported: d = 512, 1 <= h <= 128; pages * page < 2^31, b * m < 2^30, topk < 2^31 - 256.  q, o, codes and exps
  * 16-byte aligned.
  * Other arguments and the errors are those of ds_sparse_attn.
  */

@@ -1168,11 +1168,11 @@ struct Plan {
 // 519 either way).
 constexpr int kSegCost = 2 * BN;
 
-// The units (two a token at most) in 32 bits, and every place on the cost line in 64: at most 1023 ranges' worth of
-// all the units' entries.
+// The units (two a token at most) in 32 bits, an entry's place in its list with the two tiles that the index warp
+// looks ahead in 31, and every place on the cost line in 64: at most 1023 ranges' worth of all the units' entries.
 bool fits(int b, int m, int topk) {
     const int64_t ntok = (int64_t)b * m;
-    return ntok <= INT32_MAX / 2 && ntok <= (INT64_MAX >> 11) / ((int64_t)topk + kSegCost);
+    return topk <= INT32_MAX - 2 * BN && ntok <= INT32_MAX / 2 && ntok <= (INT64_MAX >> 11) / ((int64_t)topk + kSegCost);
 }
 
 // Ranges for a problem.  With at least as many units as CTAs: one a CTA, cut where they fall.  With fewer, every unit

@@ -1145,3 +1145,11 @@ def test_attention_of_a_padded_batch_refusals(lib):
     for bad in (dict(lens=FAKE + 2), dict(lens=FAKE + 1, topk=0), dict(q=None), dict(o=FAKE + 8), dict(h=0), dict(rd=16, rows=9)):
         assert call(f, base, **bad) == -1, bad
     assert call(f, base, h=129) == -2 and call(f, base, b=0, q=None, o=None, sink=None) == 0
+
+
+def test_refusal_of_lists_too_long_to_count(lib):
+    base = dict(q=FAKE, codes=FAKE, exps=FAKE, pages=4, page=16, bt=FAKE, mp=1, sink=FAKE, idx=FAKE, topk=4, scale=0.1,
+                o=FAKE, b=1, m=1, h=4, d=512, ws=None, wsb=0, rd=0, table=None, rows=0, first=None, stream=None)
+    for topk in (2 ** 31 - 1, 2 ** 31 - 256):
+        assert call(lib.ds_sparse_attn_fp4_paged, base, topk=topk) == -2
+        assert lib.ds_sparse_attn_fp4_paged_workspace_bytes(1, 1, 4, 512, topk) == 0
