@@ -404,8 +404,7 @@ int ds_norm_rotary(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint
  *     k = ceil(log2(max(amax, 1e-4) / 6)),  code = z / 2^k to the nearest e2m1, ties to even,
  * decided on z itself and not on a rounded one: the codes are those of an evaluation in 64 bits.
  * Logical rows of one call are distinct within a sequence; pages written for different sequences
- * must be distinct too.  Rows, and with a norm the sums of their squares in f32, must be finite,
- * and eps 0 or at least 2^-100.
+ * must be distinct too.  Rows, and with a norm the sums of their squares in f32, must be finite.
  *
  * x          device bf16, row (bi, t) at x + bi * x_bstride + t * x_tstride (elements, multiples
  *            of 8), 16-byte aligned, not modified
@@ -413,6 +412,7 @@ int ds_norm_rotary(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint
  *            every token, stored or not, as ds_kv_quant_ring_write leaves them in place; 16-byte
  *            aligned; y may be x when x is laid out so
  * codes      16-byte aligned.  d multiple of 32, <= 1024; b * s < 2^31, pages * page < 2^31
+ * eps        0, or at least 2^-100
  * weight, rd, table, first, lens as for ds_norm_rotary (weight is read only when eps > 0)
  * Errors: DS_EINVAL, DS_EUNSUPPORTED, DS_ECUDA.
  */

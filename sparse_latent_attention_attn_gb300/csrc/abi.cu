@@ -379,8 +379,8 @@ int ds_kv_append_fp4_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstri
                            uint8_t *codes, int8_t *exps, int64_t pages, int page, const int32_t *block_table,
                            int max_pages, ds_stream_t stream) {
     const Range range("ds_kv_append_fp4_paged");
-    if (b < 0 || s < 0 || d < 32 || d % 32 != 0 || !(eps >= 0.0f) || pos_step < 1 || base < 0 || window < 0)
-        return DS_EINVAL;
+    if (b < 0 || s < 0 || d < 32 || d % 32 != 0 || pos_step < 1 || base < 0 || window < 0) return DS_EINVAL;
+    if (eps != 0.0f && !(eps >= 0x1p-100f)) return DS_EINVAL;
     if (!rotation_ok(rd, d, table, table_rows) || !pool_ok(pages, page, max_pages)) return DS_EINVAL;
     if (d > 1024 || !pool_fits(pages, page) || (int64_t)b * s > INT32_MAX) return DS_EUNSUPPORTED;
     if ((int64_t)b * s == 0) return DS_OK;

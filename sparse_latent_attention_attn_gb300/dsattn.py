@@ -493,6 +493,8 @@ def kv_append_fp4_paged(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor
                 **{k: v for k, v in given.items() if v[0] is not None}, **({"table": (table, _F32, tab)} if rd else {}))
     if x.numel() and xd != 1:
         raise ValueError("the values of a row must be contiguous")
+    if 0.0 < eps < 2.0 ** -100:            # as a float it could be 0, which is no norm
+        raise DsError("ds_kv_append_fp4_paged", DS_EINVAL)
     st = _lib.ds_kv_append_fp4_paged(x.data_ptr(), xb if b > 1 else 0, xt if s > 1 else 0,
                                      None if y is None else y.data_ptr(), b, s, d,
                                      None if weight is None else weight.data_ptr(), eps, rd,

@@ -1153,3 +1153,23 @@ def test_refusal_of_lists_too_long_to_count(lib):
     for topk in (2 ** 31 - 1, 2 ** 31 - 256):
         assert call(lib.ds_sparse_attn_fp4_paged, base, topk=topk) == -2
         assert lib.ds_sparse_attn_fp4_paged_workspace_bytes(1, 1, 4, 512, topk) == 0
+
+
+def test_append_refuses_an_eps_that_is_next_to_nothing(lib):
+    base = dict(x=FAKE, xb=64, xt=64, y=None, b=2, s=1, d=64, w=None, eps=1e-6, rd=0, table=None, rows=0, first=FAKE,
+                lens=None, step=1, base=0, window=8, codes=FAKE, exps=FAKE, pages=4, page=16, bt=FAKE, mp=1, stream=None)
+    for eps in (1e-40, 7.8e-31, -1e-40, float("nan")):
+        assert call(lib.ds_kv_append_fp4_paged, base, eps=eps) == -1
+    assert call(lib.ds_kv_append_fp4_paged, base, eps=2.0 ** -100, b=0) == 0
+
+
+@gpu
+def test_append_binding_refuses_an_eps_that_rounds_to_none(ds):
+    x = torch.ones((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    codes = torch.full((1, 4, 32), 9, dtype=torch.uint8, device="cuda")
+    exps = torch.full((1, 4, 2), 9, dtype=torch.int8, device="cuda")
+    for eps in (1e-50, 1e-40):
+        with pytest.raises(ds.DsError):
+            ds.kv_append_fp4_paged(x, codes, exps, ints(0).view(1, 1).cuda(), ints(0).cuda(), eps=eps)
+    torch.cuda.synchronize()
+    assert (codes == 9).all() and (exps == 9).all()
