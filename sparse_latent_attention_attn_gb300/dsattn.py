@@ -426,6 +426,12 @@ def _refuse(**tensors) -> None:
     raise ValueError("the tensors do not fit together")
 
 
+def _refuse_wide(fn: str, *sizes: int) -> None:
+    """Raise for a number that the C call's int would not hold (ctypes would take its low 32 bits)."""
+    if any(not -1 << 31 <= v < 1 << 31 for v in sizes):
+        raise DsError(fn, DS_EUNSUPPORTED)
+
+
 def _table_shape(rd: int, table: torch.Tensor | None) -> tuple:
     return (table.shape[0] if table is not None and table.dim() == 3 else 0, rd // 2, 2)
 
@@ -452,6 +458,8 @@ def norm_rotary(x: torch.Tensor, eps: float, rd: int, table: torch.Tensor | None
                 **({"table": (table, _F32, tab)} if rd else {}))
     if x.numel() and (xd != 1 or (h > 1 and xh != d)):
         raise ValueError("the heads of a token must be contiguous")
+    if (b * s * h | rd) >> 31:
+        _refuse_wide("ds_norm_rotary", b * s * h, rd)
     if y is None:
         with _on(stream):
             y = (torch.empty if lens is None else torch.zeros)((b, s, h, d), dtype=_BF16, device=x.device)
@@ -493,6 +501,8 @@ def kv_append_fp4_paged(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor
                 **{k: v for k, v in given.items() if v[0] is not None}, **({"table": (table, _F32, tab)} if rd else {}))
     if x.numel() and xd != 1:
         raise ValueError("the values of a row must be contiguous")
+    if (b * s | page | max_pages | pos_step | base | window | rd) >> 31:
+        _refuse_wide("ds_kv_append_fp4_paged", b * s, page, max_pages, pos_step, base, window, rd)
     if 0.0 < eps < 2.0 ** -100:            # as a float it could be 0, which is no norm
         raise DsError("ds_kv_append_fp4_paged", DS_EINVAL)
     st = _lib.ds_kv_append_fp4_paged(x.data_ptr(), xb if b > 1 else 0, xt if s > 1 else 0,
@@ -545,6 +555,8 @@ def sparse_attn_fp4_paged(q: torch.Tensor, codes: torch.Tensor, exps: torch.Tens
                 **({"o": (o, _BF16, q.shape)} if o is not None else {}), **({"lens": (lens, _I32, (b,))} if lens is not None else {}),
                 **({"table": (table, _F32, tab), "first": (first, _I32, (b,))} if rd else {}),
                 **({"workspace": (workspace, workspace.dtype, workspace.shape)} if workspace is not None else {}))
+    if (b * m | topk | page | max_pages | rd) >> 31:
+        _refuse_wide("ds_sparse_attn_fp4_paged", b * m, topk, page, max_pages, rd)
     if o is None:
         if stream is None and lens is None:
             o = torch.empty_like(q)

@@ -1173,3 +1173,27 @@ def test_append_binding_refuses_an_eps_that_rounds_to_none(ds):
             ds.kv_append_fp4_paged(x, codes, exps, ints(0).view(1, 1).cuda(), ints(0).cuda(), eps=eps)
     torch.cuda.synchronize()
     assert (codes == 9).all() and (exps == 9).all()
+
+
+@gpu
+def test_bindings_refuse_numbers_beyond_an_int(ds):
+    """Numbers whose low 32 bits would be another valid call."""
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device="cuda")
+    wide = 1 << 32
+    app = dict(x=z(1, 1, 64), codes=z(1, 8, 32, dt=torch.uint8), exps=z(1, 8, 2, dt=torch.int8),
+               block_table=z(1, 1, dt=torch.int32), first=z(1, dt=torch.int32))
+    pool = dict(codes=z(0, wide + 8, 32, dt=torch.uint8), exps=z(0, wide + 8, 2, dt=torch.int8))
+    app["codes"].fill_(9)
+    for bad in (dict(base=wide), dict(window=wide + 8), dict(pos_step=wide + 1), dict(base=-wide), dict(base=2 ** 31), pool):
+        with pytest.raises(ds.DsError):
+            ds.kv_append_fp4_paged(**{**app, **bad})
+    assert ds.device_status() == 0 and (app["codes"] == 9).all()
+    with pytest.raises(ds.DsError):                        # in an int, and refused for what it is
+        ds.kv_append_fp4_paged(**app, base=-1)
+    attn = dict(q=z(1, 1, 4, 512), codes=z(0, wide + 16, 256, dt=torch.uint8), exps=z(0, wide + 16, 16, dt=torch.int8),
+                block_table=z(1, 1, dt=torch.int32), sink=z(4, dt=torch.float32), idx=z(1, 1, 3, dt=torch.int32), scale=0.1)
+    with pytest.raises(ds.DsError):
+        ds.sparse_attn_fp4_paged(**attn)
+    with pytest.raises((ds.DsError, ValueError)):
+        ds.norm_rotary(z(1, 1, 4, 64), 1e-6, wide, z(4, 0, 2, dt=torch.float32), z(1, dt=torch.int32))
+    assert ds.device_status() == 0
