@@ -584,6 +584,8 @@ def sparse_attn_fp4_paged(q: torch.Tensor, codes: torch.Tensor, exps: torch.Tens
     else:
         st = _lib.ds_sparse_attn_fp4_paged_ragged(*args, lens.data_ptr(), on)
     if st:
+        # the size kept for this shape may be the 0 of a query that failed: the next call asks anew
+        _fp4_workspace_bytes.cache_clear()
         _check("ds_sparse_attn_fp4_paged", st)
     return o
 

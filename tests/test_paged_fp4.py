@@ -1197,3 +1197,17 @@ def test_bindings_refuse_numbers_beyond_an_int(ds):
     with pytest.raises((ds.DsError, ValueError)):
         ds.norm_rotary(z(1, 1, 4, 64), 1e-6, wide, z(4, 0, 2, dt=torch.float32), z(1, dt=torch.int32))
     assert ds.device_status() == 0
+
+
+@gpu
+def test_attention_asks_anew_for_a_workspace_after_a_failure(ds, monkeypatch):
+    """The size of a shape's workspace is kept, but not that of a query that failed (0)."""
+    x = attention_inputs(53, 1, 1, 16, 3000, 2300, 0.1, 64, 0)
+    args = dev(*x[:6]) + [512 ** -0.5]
+    assert ds.sparse_attn_fp4_paged_workspace_bytes(1, 1, 16, 512, 2300) > 0
+    ds._fp4_workspace_bytes.cache_clear()
+    with monkeypatch.context() as mp:
+        mp.setattr(ds, "sparse_attn_fp4_paged_workspace_bytes", lambda *a: 0)
+        with pytest.raises(ds.DsError):
+            ds.sparse_attn_fp4_paged(*args)
+    check_attention(ds, *x)
