@@ -110,9 +110,14 @@ def _check(fn: str, status: int) -> None:
         raise DsError(fn, status)
 
 
+# The current device, and its current stream's raw handle: torch.cuda.current_stream() builds an object around that
+# (3 us against 0.2).  A torch without these two (one built without CUDA, say) has the public functions.
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _stream(stream) -> int:
-    # the raw handle: torch.cuda.current_stream() builds an object around it (3 us against 0.2)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+    return _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -397,9 +402,6 @@ _BF16, _F32, _I32, _U8, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.
 def _on(stream):
     """Tensors made inside belong to the stream of the call, not to the current one."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _fits(t: torch.Tensor, dtype, shape: tuple, dev: int) -> bool:

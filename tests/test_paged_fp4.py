@@ -1211,3 +1211,22 @@ def test_attention_asks_anew_for_a_workspace_after_a_failure(ds, monkeypatch):
         with pytest.raises(ds.DsError):
             ds.sparse_attn_fp4_paged(*args)
     check_attention(ds, *x)
+
+
+IMPORT_WITHOUT = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from sparse_latent_attention_attn_gb300 import dsattn
+assert dsattn._device is torch.cuda.current_device
+"""
+
+
+def test_import_without_the_private_functions_of_torch(lib):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", IMPORT_WITHOUT], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
