@@ -435,7 +435,8 @@ int ds_kv_append_fp4_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstri
  * probability take nothing from the others, however large their values are.
  * Block exponents above 48 are read as 48 and raise DS_DEV_BAD_VALUE (ds_kv_append_fp4_paged stores
  * them for values above 6 * 2^48 only); blocks whose exponent is more than 26 below the row's
- * largest, or below -74, count as zeros.  scale * q and the scores must be finite in f32.
+ * largest, or below -74, count as zeros.  A head of q that holds an infinity or a NaN gives NaN
+ * where it has rows; otherwise scale * q and the scores must be finite in f32.
  *
  * rd         multiple of 8, 0 <= rd <= d (0: no rotation; table and first may be NULL)
  * workspace  at least ds_sparse_attn_fp4_paged_workspace_bytes(b, m, h, d, topk) bytes, 256-byte

@@ -173,6 +173,13 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
+// NaN where any value is one (warp_max leaves them out)
+__device__ __forceinline__ float warp_max_nan(float v) {
+    float r;
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 __device__ __forceinline__ bool bar_or(bool pred) {
     uint32_t r;
     asm volatile(
@@ -255,7 +262,8 @@ __device__ __forceinline__ uint4 ld_row(const void *ptr) {
     return v;
 }
 
-// One head of q (16 values a lane; sign: its sign bit is flipped) into [hi | lo]; returns g.
+// One head of q (16 values a lane; sign: its sign bit is flipped) into [hi | lo]; returns g.  Where a value is not
+// finite, all of the head's hi are NaN (e4m3 has no infinity to hand one on).
 __device__ __forceinline__ int put_q(uint32_t sq, int hh, const uint4 (&v)[2], int lane, uint32_t sign) {
     const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
     uint32_t top2 = 0;
@@ -264,11 +272,13 @@ __device__ __forceinline__ int put_q(uint32_t sq, int hh, const uint4 (&v)[2], i
     const uint32_t top = __reduce_max_sync(kAll, max(top2 & 0xffffu, top2 >> 16));
     const int g = max((int)(top >> 7) - 127 - 7, -126);      // the largest value lies in [128, 256) 2^g
     const uint32_t down = (((uint32_t)(127 - g) << 7) | sign) * 0x10001u;
+    const uint32_t nan = top >= 0x7f80u ? 0x7f7fu : 0u;
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         uint32_t h2, l2;
         split_q(w[k], down, h2, l2);
+        h2 |= nan;
         hi[k >> 1] = k & 1 ? hi[k >> 1] | (h2 << 16) : h2;
         lo[k >> 1] = k & 1 ? lo[k >> 1] | (l2 << 16) : l2;
     }
@@ -1082,7 +1092,7 @@ __global__ void __launch_bounds__(32 * kCombineHeads) combine_kernel(const P p) 
         }
     };
     load(0);
-    const float top = warp_max(m);
+    const float top = warp_max_nan(m);
     float4 acc[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);

@@ -1230,3 +1230,24 @@ def test_import_without_the_private_functions_of_torch(lib):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", IMPORT_WITHOUT], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@gpu
+@pytest.mark.parametrize("b,m,h,topk", [(2, 1, 40, 150), (1, 1, 70, 2300), (200, 1, 100, 130), (1, 1, 3, 1)])
+@pytest.mark.parametrize("what", [math.inf, -math.inf, math.nan])
+def test_attention_of_queries_that_are_not_finite(ds, b, m, h, topk, what):
+    """One such value makes its head's output NaN, in units whole and cut; the other heads are as without it."""
+    q, codes, exps, bt, sink, idx, *_ = attention_inputs(55, b, m, h, 3000, topk, 0.1, 16, 0)
+    idx[0, 0, 0] = 7
+    args = dev(q, codes, exps, bt, sink, idx)
+    want = ds.sparse_attn_fp4_paged(*args, 512 ** -0.5)
+    hit = torch.zeros((b, m, h), dtype=torch.bool)
+    hit[0, 0, h // 2] = hit[-1, -1, 0] = True
+    bad = q.clone()
+    bad[0, 0, h // 2, 77] = what
+    bad[-1, -1, 0, 0] = what
+    got = ds.sparse_attn_fp4_paged(bad.cuda(), *args[1:], 512 ** -0.5)
+    assert ds.device_status() == 0
+    none = (idx < 0).all(-1)[..., None] & hit              # without rows: 0, whatever q is
+    assert got.cpu()[hit & ~none].isnan().all() and (got.cpu()[none] == 0).all()
+    assert torch.equal(got.cpu()[~hit], want.cpu()[~hit])
