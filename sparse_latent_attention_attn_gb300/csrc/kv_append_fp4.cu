@@ -6,12 +6,14 @@
 // pages are this library's: with z the row after norm and rotation, per block of 32
 //     k = ceil(log2(max(amax, 1e-4) / 6)),  code_i = e2m1(z_i / 2^k), nearest, ties to the even code.
 //
-// A code is a decision, so it is made on the exact z.  The f32 value is off by less than d = 2^-20 of the
-// magnitudes it was made of: half the 15 roundings of the longest chain into the sum of squares, four of the
-// factor 1 / sqrt(ss / d + eps), two products, a product and a sum of the rotation, each 2^-24.  So the codes of
-// z + d and z - d are formed; where they are the same (and the block's exponent is for its maximum + d and - d)
-// they are z's, and where a border lies between them the warp goes through the formula with two floats a
-// number (to about 2^-44): two rows of 512 in a thousand.  Rows that are neither normalised nor rotated are exact in f32 (d = 0).
+// A code is a decision, so it is made on the exact z.  The f32 value is off by less than t of the magnitudes it was
+// made of.  Its roundings, in units of 2^-24: half of those in the longest chain into the sum of squares, of N
+// chunks a lane (2 N - 1 products and sums, the first square exact, 2 + 5 sums of a lane's and the lanes' parts): 5 for
+// N <= 2, 7 for N = 4; 5 for the factor 1 / sqrt(ss / d + eps); two products; two for the rotation; and one for z + t
+// itself: 15 for rows of up to 512, t = 16, and 17 above, t = 32.  So the codes of z + t and z - t are formed;
+// where they are the same (and the block's exponent is for its maximum + t and - t) they are z's, and where a
+// border lies between them the warp goes through the formula with two floats a number (to about 2^-44): two rows
+// of 512 in a thousand.  Rows that are neither normalised nor rotated are exact in f32 (t = 0).
 //
 // HBM has 2 bytes read and 17/32 written a value, 2 more with y; what bounds long batches is the integer pipe
 // (0.69 of its rate: conversions, byte permutes, maxima, exponents), decode sizes latency.  One row a warp (half
@@ -104,7 +106,7 @@ __device__ __forceinline__ void values8(uint32_t c, float sc, float (&x)[8]) {
 
 // ---- the same in two floats (hi + lo, good to about 2^-44), for values next to a border ----
 
-// s + e == a + b exactly.
+// s + e == a + b exactly (Knuth's two-sum).
 __device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
     s = __fadd_rn(a, b);
     const float bb = __fsub_rn(s, a);
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, N <= 2 ? 4 : 2) kv_append_fp4_kernel
     }
     const int rot = (p.d - p.rd) / 8;
     const float2 *cs = p.table + pos * (p.rd / 2);
-    constexpr float kTol = 9.53674316e-7f;               // 2^-20
+    constexpr float kTol = N <= 2 ? 0x1p-20f : 0x1p-19f;  // t
     uint32_t code[N];
     int kexp[N];
     bool near = false;
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, N <= 2 ? 4 : 2) kv_append_fp4_kernel
         const int k = block_exp(fmaxf(amax + far, 1e-4f));
         const float inv = pow2(-k);
         kexp[i] = k;
-        // z (1 +- 2^-20): of z's sign, so that minus zero stays what it is
+        // z (1 +- t): of z's sign, so that minus zero stays what it is
         const float more = inv * (1.0f + kTol), less = inv * (1.0f - kTol);
         uint64_t up[4], down[4];
 #pragma unroll

@@ -64,7 +64,8 @@ struct Divisor {
     }
 };
 
-// 1 / sqrt(ss / d + eps) from inv_d = 1 / d rounded, within 4 * 2^-24 of it.
+// 1 / sqrt(ss / d + eps) from inv_d = 1 / d rounded, within 5 * 2^-24 of it: half of two roundings, and the two units
+// in the last place that rsqrtf's documentation allows.
 __device__ __forceinline__ float norm_factor(float ss, float inv_d, float eps) { return rsqrtf(fmaf(ss, inv_d, eps)); }
 
 // Sum over the L lanes of a row; every lane gets it.

@@ -1251,3 +1251,23 @@ def test_attention_of_queries_that_are_not_finite(ds, b, m, h, topk, what):
     none = (idx < 0).all(-1)[..., None] & hit              # without rows: 0, whatever q is
     assert got.cpu()[hit & ~none].isnan().all() and (got.cpu()[none] == 0).all()
     assert torch.equal(got.cpu()[~hit], want.cpu()[~hit])
+
+
+@gpu
+@pytest.mark.parametrize("d,rd", [(1024, 1024), (544, 64), (992, 480)])
+def test_append_many_wide_rows(ds, d, rd):
+    """Rows above 512 values, enough of them that many values lie next to a border between two codes."""
+    g = torch.Generator().manual_seed(d)
+    b, s = 3, 700
+    x = (torch.randn((b, s, d), generator=g) * 2).to(torch.bfloat16)
+    w = torch.randn((d,), generator=g)
+    first, tab = ints(0, 300, 77), table_of(1000, rd, 1.25)
+    codes, exps, bt = random_pool(g, b, 1000, 48, d)
+    y = torch.zeros((b, s, d), dtype=torch.bfloat16)
+    want = append_reference(x, w, 1e-6, rd, tab, first, None, 1, 0, 0, codes, exps, bt, y)
+    xg, cg, eg, btg, fg, wg, tg, yg = dev(x, codes, exps, bt, first, w, tab, y)
+    ds.kv_append_fp4_paged(xg, cg, eg, btg, fg, rd=rd, table=tg, eps=1e-6, weight=wg, y=yg)
+    assert ds.device_status() == 0
+    np.testing.assert_array_equal(eg.cpu().numpy(), want[1])
+    np.testing.assert_array_equal(cg.cpu().numpy(), want[0])
+    np.testing.assert_array_equal(f64(yg), want[2])
