@@ -408,9 +408,10 @@ int ds_norm_rotary(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint
  *
  * x          device bf16, row (bi, t) at x + bi * x_bstride + t * x_tstride (elements, multiples
  *            of 8), 16-byte aligned, not modified
- * y          device bf16 [b][s][d] or NULL: the values that the codes stand for (exact in bf16), of
- *            every token, stored or not, as ds_kv_quant_ring_write leaves them in place; 16-byte
- *            aligned; y may be x when x is laid out so
+ * y          device bf16 [b][s][d] or NULL: the values that the codes stand for, of every token, stored
+ *            or not, as ds_kv_quant_ring_write leaves them in place; exact in bf16, except that 2^128
+ *            (what values of z from 3.5 * 2^126 on are stored as) is infinity there; 16-byte aligned;
+ *            y may be x when x is laid out so
  * codes      16-byte aligned.  d multiple of 32, <= 1024; b * s < 2^31, pages * page < 2^31
  * eps        0, or at least 2^-100
  * weight, rd, table, first, lens as for ds_norm_rotary (weight is read only when eps > 0)

@@ -1271,3 +1271,28 @@ def test_append_many_wide_rows(ds, d, rd):
     np.testing.assert_array_equal(eg.cpu().numpy(), want[1])
     np.testing.assert_array_equal(cg.cpu().numpy(), want[0])
     np.testing.assert_array_equal(f64(yg), want[2])
+
+
+@gpu
+@pytest.mark.parametrize("rd", [0, 8])
+def test_append_of_the_largest_values(ds, rd):
+    """Values up to bf16's largest: below 3.5 * 2^126 y is finite, from there on the code stands for 2^128."""
+    top = torch.tensor([3.5 * 2.0 ** 126, float(torch.finfo(torch.bfloat16).max)]).to(torch.bfloat16)
+    x = torch.randn((1, 4, 64), generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    x[0, 0, 3] = (top[:1].view(torch.int16) - 1).view(torch.bfloat16)[0]
+    x[0, 1, 40], x[0, 1, 5] = top[0], -top[1]
+    x[0, 2, 20] = -3 * 2.0 ** 125
+    x[0, 3] = x[0, 3].float() * 2.0 ** 124
+    codes = torch.zeros((4, 1, 32), dtype=torch.uint8)
+    exps = torch.zeros((4, 1, 2), dtype=torch.int8)
+    bt = torch.arange(4, dtype=torch.int32)[None]
+    tab = table_of(4, rd) if rd else None
+    y = torch.zeros_like(x)
+    want = append_reference(x, None, 0.0, rd, tab, ints(0), None, 1, 0, 0, codes, exps, bt, y)
+    cg, eg, btg, fg, yg, tg = dev(codes, exps, bt, ints(0), y, tab)
+    ds.kv_append_fp4_paged(x.cuda(), cg, eg, btg, fg, rd=rd, table=tg, y=yg)
+    np.testing.assert_array_equal(eg.cpu().numpy(), want[1])
+    np.testing.assert_array_equal(cg.cpu().numpy(), want[0])
+    stored = np.where(np.abs(want[2]) == 2.0 ** 128, np.copysign(math.inf, want[2]), want[2])
+    np.testing.assert_array_equal(f64(yg), stored)
+    assert int(exps.new_tensor(want[1]).max()) == 126 and np.isinf(stored).sum() == 2 and np.isfinite(stored[0, 0]).all()
