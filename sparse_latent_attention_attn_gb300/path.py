@@ -60,8 +60,12 @@ def decode_step_fp4_paged(q: torch.Tensor, new_kv: torch.Tensor, codes: torch.Te
     (bi, t) is at position first[bi] + t; codes, exps, block_table: the paged store, whose logical rows
     are the ring's `window` slots, then the compressed rows; idx [b][s][topk] lists logical rows, complete.
     Tokens at or behind lens[bi] are padding: nothing of theirs is stored, and o is left as it was (zeros in a
-    new one).  s > 1 stores all s rows before any query reads them: a query whose ring is full then misses the
-    rows that later tokens of the step replaced."""
+    new one).  s > 1 stores all s rows before any query reads them, so the ring has to hold what every query of the step
+    lists: `window` = (the rows a query attends over) + s - 1 slots.  Fewer slots than tokens, which would not
+    keep the step's own rows, are refused (with lens, which must not exceed them either, they cannot be told);
+    window = 0 is a cache without a ring (row = position)."""
+    if lens is None and 0 < window < q.shape[1]:
+        raise ValueError(f"a ring of {window} slots does not hold the step's {q.shape[1]} tokens")
     dsattn.kv_append_fp4_paged(new_kv, codes, exps, block_table, first, rd=rd, table=table, eps=eps, weight=kv_weight,
                                lens=lens, window=window, stream=stream)
     qn = None

@@ -1296,3 +1296,39 @@ def test_append_of_the_largest_values(ds, rd):
     stored = np.where(np.abs(want[2]) == 2.0 ** 128, np.copysign(math.inf, want[2]), want[2])
     np.testing.assert_array_equal(f64(yg), stored)
     assert int(exps.new_tensor(want[1]).max()) == 126 and np.isinf(stored).sum() == 2 and np.isfinite(stored[0, 0]).all()
+
+
+def test_step_refuses_more_tokens_than_the_ring_holds(lib):
+    from sparse_latent_attention_attn_gb300 import path
+    q = torch.zeros((1, 5, 2, 512), dtype=torch.bfloat16)
+    store = (torch.zeros((1, 16, 256), dtype=torch.uint8), torch.zeros((1, 16, 16), dtype=torch.int8), ints(0).view(1, 1))
+    with pytest.raises(ValueError, match="ring"):
+        path.decode_step_fp4_paged(q, q[:, :, 0], *store, ints(0), torch.zeros(2), torch.zeros((1, 5, 4), dtype=torch.int32), 4,
+                                   0.1, 0, None, 1e-6)
+    with pytest.raises(ValueError, match="CUDA"):          # five slots are enough: refused for the CPU tensors only
+        path.decode_step_fp4_paged(q, q[:, :, 0], *store, ints(0), torch.zeros(2), torch.zeros((1, 5, 4), dtype=torch.int32), 5,
+                                   0.1, 0, None, 1e-6)
+
+
+@gpu
+def test_step_of_several_tokens_without_a_ring(ds):
+    """window = 0: rows are positions; three tokens a step, the same as three steps of one."""
+    from sparse_latent_attention_attn_gb300 import path
+    g = torch.Generator().manual_seed(12)
+    b, s, h, d, rd, page, eps = 2, 3, 9, 512, 64, 7, 1e-6
+    codes, exps, bt = random_pool(g, b, 40, page, d)
+    tab, sink = table_of(60, rd), torch.randn((h,), generator=g)
+    q = torch.randn((b, s, h, d), generator=g).to(torch.bfloat16)
+    kv = torch.randn((b, s, d), generator=g).to(torch.bfloat16)
+    first = ints(30, 5)
+    idx = torch.arange(40, dtype=torch.int32).expand(b, s, 40).clone()
+    idx[idx > (first[:, None] + torch.arange(s))[..., None]] = -1
+    qg, kg, btg, fg, sg, ig, tg = dev(q, kv, bt, first, sink, idx, tab)
+    c1, e1 = dev(codes, exps)
+    whole = path.decode_step_fp4_paged(qg, kg, c1, e1, btg, fg, sg, ig, 0, d ** -0.5, rd, tg, eps)
+    c2, e2 = dev(codes, exps)
+    for t in range(s):
+        one = path.decode_step_fp4_paged(qg[:, t:t + 1].contiguous(), kg[:, t:t + 1].contiguous(), c2, e2, btg, fg + t, sg,
+                                         ig[:, t:t + 1].contiguous(), 0, d ** -0.5, rd, tg, eps)
+        assert torch.equal(one, whole[:, t:t + 1])
+    assert torch.equal(c1, c2) and torch.equal(e1, e2) and ds.device_status() == 0
