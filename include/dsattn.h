@@ -359,7 +359,14 @@ int ds_indexer_topk(const uint16_t *q, const uint16_t *k, const float *w, int b,
  * Logical row r of sequence bi is slot r % page of page block_table[bi][r / page], for any page
  * size >= 1.  The logical rows are those of a sequence's kv elsewhere in this library: the ring's
  * window rows first, the compressed rows behind them, so that the rows of ds_window_topk_idxs and
- * ds_indexer_topk (offset = window) are used as they are.  17/32 byte a value.
+ * ds_indexer_topk (offset = window) list them.  Those two calls take one start position: a batch
+ * whose sequences stand at different ones makes them for each sequence (b = 1).  17/32 byte a value.
+ *
+ * A prompt of n rows, whose queries list window rows by position (ds_window_topk_idxs at start 0),
+ * has a block table of its own beside the one that decode steps use: n / page pages of the chunk's
+ * rows (window = 0, base = 0; free again once the prompt has been attended over), then the same
+ * pages of compressed rows as behind the ring.  The ring's size and n must be multiples of the page
+ * size for that.  The chunk's rows are also appended into the ring, which keeps the last ones.
  *
  * In the calls below first[bi] is the position (>= 0) of the sequence's first token of this call,
  * and lens[bi], in the calls that take it, how many of the tokens it has (the others are padding:

@@ -1332,3 +1332,95 @@ def test_step_of_several_tokens_without_a_ring(ds):
                                          ig[:, t:t + 1].contiguous(), 0, d ** -0.5, rd, tg, eps)
         assert torch.equal(one, whole[:, t:t + 1])
     assert torch.equal(c1, c2) and torch.equal(e1, e2) and ds.device_status() == 0
+
+
+# ---- with the library's other calls --------------------------------------------------------------------------
+
+def against_64_bits(got, q, codes, exps, bt, seq, ix, page, sink, scale, tab, pos, rd):
+    rows, tops = logical_rows(codes, exps, bt, seq, ix, page)
+    ref, A, F = attention_by_weight(f64(q), rows, ix >= 0, f64(sink), scale, tops)
+    ref, A, F = rotate(ref, f64(tab)[pos][None], inverse=True), pair_sum(A, rd), pair_sum(F, rd)
+    assert (np.abs(f64(got) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * A + 2.0 ** -17 * F).all()
+
+
+@gpu
+def test_index_rows_of_the_library_for_sequences_at_their_own_positions(ds):
+    """Window rows by ds_window_topk_idxs and compressed ones by ds_indexer_topk, a call for each sequence."""
+    g = torch.Generator().manual_seed(61)
+    b, h, d, rd, W, page, ratio, topk = 3, 12, 512, 64, 32, 8, 4, 40
+    start = [300, 17, 131]
+    codes, exps, bt = random_pool(g, b, W + 80, page, d)
+    q, sink, tab = torch.randn((b, 1, h, d), generator=g).to(torch.bfloat16), torch.randn((h,), generator=g), table_of(400, rd)
+    iq, ik = torch.randn((b, 1, 64, 128), generator=g).to(torch.bfloat16), torch.randn((b, 80, 128), generator=g).to(torch.bfloat16)
+    iw = torch.rand((b, 1, 64), generator=g)
+    idx = torch.full((b, 1, W + topk), -1, dtype=torch.int32, device="cuda")
+    for i in range(b):
+        assert ds.window_topk_idxs(idx[i], 1, 1, start[i], W) == W
+        comp = ds.indexer_topk(*dev(iq[i:i + 1], ik[i:i + 1], iw[i:i + 1]), start[i], ratio, topk, offset=W)
+        idx[i, 0, W:W + comp.shape[-1]] = comp[0, 0]
+    ix = idx.cpu()
+    for i in range(b):
+        ring = sorted(v for v in ix[i, 0, :W].tolist() if v >= 0)
+        assert ring == sorted({p % W for p in range(max(0, start[i] - W + 1), start[i] + 1)})
+        comp = [v for v in ix[i, 0, W:].tolist() if v >= 0]
+        assert len(comp) == min(topk, (start[i] + 1) // ratio) and all(W <= v < W + (start[i] + 1) // ratio for v in comp)
+    o = ds.sparse_attn_fp4_paged(*dev(q, codes, exps, bt, sink), idx, d ** -0.5, rd=rd, table=tab.cuda(), first=ints(*start).cuda())
+    assert ds.device_status() == 0
+    for i in range(b):
+        against_64_bits(o[i, 0], q[i, 0], codes, exps, bt, i, ix[i, 0].numpy(), page, sink, d ** -0.5, tab, start[i], rd)
+
+
+@gpu
+def test_prompt_and_decode_share_one_store(ds):
+    """A prompt through a block table of its own, the compressed rows' pages shared with the decode table; then a
+    decode step over ring and compressed rows."""
+    from sparse_latent_attention_attn_gb300 import path
+    g = torch.Generator().manual_seed(63)
+    n, W, page, ratio, h, d, rd, eps = 40, 16, 8, 4, 10, 512, 64, 1e-6
+    ncomp, scale = n // ratio, d ** -0.5
+    order = torch.randperm(20, generator=g).to(torch.int32)
+    chunk, comp, ring = order[:n // page], order[5:8], order[8:8 + W // page]
+    prompt_bt, decode_bt = torch.cat((chunk, comp))[None].contiguous(), torch.cat((ring, comp))[None].contiguous()
+    codes = torch.zeros((20, page, d // 2), dtype=torch.uint8, device="cuda")
+    exps = torch.zeros((20, page, d // 32), dtype=torch.int8, device="cuda")
+    tab, sink, w = table_of(64, rd), torch.randn((h,), generator=g), 1 + 0.1 * torch.randn((d,), generator=g)
+    kv = torch.randn((1, n, d), generator=g).to(torch.bfloat16)
+    ckv = torch.randn((1, ncomp, d), generator=g).to(torch.bfloat16)
+    q = torch.randn((1, n, h, d), generator=g).to(torch.bfloat16)
+    kvg, cg, qg, tg, sg, wg, pt, dt = dev(kv, ckv, q, tab, sink, w, prompt_bt, decode_bt)
+    zero = ints(0).cuda()
+    more = dict(rd=rd, table=tg, eps=eps, weight=wg)
+    ds.kv_append_fp4_paged(kvg, codes, exps, pt, zero, **more)
+    ds.kv_append_fp4_paged(kvg, codes, exps, dt, zero, window=W, **more)
+    ds.kv_append_fp4_paged(cg, codes, exps, dt, zero, pos_step=ratio, base=W, **more)
+    idx = torch.full((1, n, W + ncomp), -1, dtype=torch.int32, device="cuda")
+    assert ds.window_topk_idxs(idx, 1, n, 0, W) == W
+    seen = torch.arange(n, device="cuda")[:, None] + 1
+    j = torch.arange(ncomp, device="cuda")
+    idx[0, :, W:] = torch.where((j + 1) * ratio <= seen, n + j, -1).to(torch.int32)
+    qn = ds.norm_rotary(qg, eps, rd, tg, zero)
+    o = ds.sparse_attn_fp4_paged(qn, codes, exps, pt, sg, idx, scale, rd=rd, table=tg, first=zero)
+    assert ds.device_status() == 0
+    hc, he, ix = codes.cpu(), exps.cpu(), idx.cpu()
+    ref = append_reference(kv, w, eps, rd, tab, ints(0), None, 1, 0, 0, torch.zeros_like(hc), torch.zeros_like(he), prompt_bt,
+                           torch.zeros_like(kv))
+    assert (hc.numpy()[chunk.numpy()] == ref[0][chunk.numpy()]).all()
+    for t in range(n):
+        against_64_bits(o[0, t], qn[0, t].cpu(), hc, he, prompt_bt, 0, ix[0, t].numpy(), page, sink, scale, tab, t, rd)
+    # the chunk's own pages are free now: other rows may take them
+    codes[chunk.long().cuda()] = 255
+    exps[chunk.long().cuda()] = 40
+    nq, nkv = torch.randn((1, 1, h, d), generator=g).to(torch.bfloat16), torch.randn((1, 1, d), generator=g).to(torch.bfloat16)
+    step = torch.full((1, 1, W + ncomp), -1, dtype=torch.int32, device="cuda")
+    ds.window_topk_idxs(step, 1, 1, n, W)
+    step[0, 0, W:] = W + j
+    at = ints(n).cuda()
+    o = path.decode_step_fp4_paged(nq.cuda(), nkv.cuda(), codes, exps, dt, at, sg, step, W, scale, rd, tg, eps, kv_weight=wg)
+    assert ds.device_status() == 0
+    qd = ds.norm_rotary(nq.cuda(), eps, rd, tg, at).cpu()
+    hc, he = codes.cpu(), exps.cpu()
+    rows = logical_rows(hc, he, decode_bt, 0, np.arange(W), page)[0]
+    for p in range(n - W + 1, n):                          # the ring holds the prompt's last rows
+        one = append_reference(kv[:, p:p + 1], w, eps, rd, tab, ints(p), None, 1, 0, W, hc, he, decode_bt, torch.zeros_like(nkv))
+        np.testing.assert_array_equal(rows[p % W], one[2][0, 0])
+    against_64_bits(o[0, 0], qd[0, 0], hc, he, decode_bt, 0, step.cpu()[0, 0].numpy(), page, sink, scale, tab, n, rd)
