@@ -14,6 +14,8 @@
 // indexes and more bytes in flight), else one.
 // Measured: 4096 tokens of 64 heads of 512, 91 us, 5.9 TB/s (0.87 of a copy's rate; 95.6 us with one row a warp);
 // 64 tokens of 64 heads 2.9 us on the device, where four rows a warp would leave half of the SMs idle.
+#include <atomic>
+
 #include "paged_rows.cuh"
 #include "row_norm.cuh"
 
@@ -97,6 +99,17 @@ __global__ void __launch_bounds__(kThreads) norm_rotary_kernel(const NormArgs p)
     }
 }
 
+// SMs of the current device; where that cannot be asked, of the GPU that this is written for
+int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+    if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 template <int L, int N, int R>
 void launch(const NormArgs &p, cudaStream_t stream) {
     const uint32_t per = kThreads / L * R;
@@ -112,8 +125,8 @@ int launch_norm_rotary(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, 
                      d, rd, weight, 1.0f / (float)d, eps, reinterpret_cast<const float2 *>(table), table_rows, first, lens, status};
     for_row(d, [&](auto l, auto n) {
         constexpr int L = decltype(l)::value, N = decltype(n)::value;
-        // four rows a warp once they still fill every SM (152 x 64 warps)
-        if (N <= 2 && (int64_t)p.nrows * L / 32 >= 4 * 152 * 64) launch<L, N, N <= 2 ? 4 : 1>(p, stream);
+        // four rows a warp once they still fill every SM (64 warps each)
+        if (N <= 2 && (int64_t)p.nrows * L / 32 >= 4 * 64 * (int64_t)sm_count()) launch<L, N, N <= 2 ? 4 : 1>(p, stream);
         else launch<L, N, 1>(p, stream);
     });
     return launch_status();
