@@ -10,15 +10,10 @@
 namespace dsattn {
 namespace rows {
 
-constexpr int kMaxRow = 1024;
 constexpr int kThreads = 256;
 constexpr uint32_t kAll = 0xffffffffu;
 
-// Lanes of a row and chunks of a lane, for a row of d values.
-inline int lanes_of(int d) { return d <= 64 ? 8 : d <= 128 ? 16 : 32; }
-inline int chunks_of(int d) { return (d / 8 + lanes_of(d) - 1) / lanes_of(d); }
-
-// Calls f(integral constants L, N) for a row of d values.
+// Calls f(integral constants L, N) for a row of d values: its lanes and the chunks of a lane.
 template <int V>
 struct Int {
     static constexpr int value = V;
