@@ -1424,3 +1424,93 @@ def test_prompt_and_decode_share_one_store(ds):
         one = append_reference(kv[:, p:p + 1], w, eps, rd, tab, ints(p), None, 1, 0, W, hc, he, decode_bt, torch.zeros_like(nkv))
         np.testing.assert_array_equal(rows[p % W], one[2][0, 0])
     against_64_bits(o[0, 0], qd[0, 0], hc, he, decode_bt, 0, step.cpu()[0, 0].numpy(), page, sink, scale, tab, n, rd)
+
+
+# ---- long ranges of units, and the workloads' own shapes -----------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("b,m,h,rows,topk,page", [
+    (1, 4096, 5, 700, 30, 16),            # 27 units a CTA, one short tile each
+    (16, 200, 70, 300, 150, 12),          # 42 units a CTA, two tiles each, two groups of heads
+    (3, 1001, 16, 900, 260, 7),           # three tiles, cut wherever the ranges end
+])
+def test_attention_long_ranges_of_units(ds, b, m, h, rows, topk, page):
+    """Many units a CTA: messages, phases, both scale buffers and the order from both ends wrap many times.  Some
+    tokens list nothing, some are padding; a sample against 64 bits, all against calls of a few tokens."""
+    g = torch.Generator().manual_seed(m)
+    q, codes, exps, bt, sink, idx, rd, _, tab = attention_inputs(65, b, m, h, rows, topk, 0.2, page, 64)
+    first, tab = torch.randint(0, 50, (b,), generator=g, dtype=torch.int32), table_of(50 + m, 64)
+    empty = torch.rand((b, m), generator=g) < 0.05
+    idx[empty] = -1
+    lens = torch.randint(m // 2, m + 1, (b,), generator=g, dtype=torch.int32)
+    live = torch.arange(m) < lens[:, None]
+    qg, cg, eg, btg, sg, ig, fg, tg, lg = dev(q, codes, exps, bt, sink, idx, first, tab, lens)
+    o = ds.sparse_attn_fp4_paged(qg, cg, eg, btg, sg, ig, 512 ** -0.5, rd=rd, table=tg, first=fg, lens=lg,
+                                 o=torch.full_like(qg, 7.0))
+    assert ds.device_status() == 0
+    got = o.cpu()
+    assert (got[~live] == 7).all() and (got[live & empty] == 0).all() and got.isfinite().all()
+    assert (got[live & ~empty] != 0).any(-1).all()
+    for j in np.random.RandomState(2).choice(int(live.sum()), 40, replace=False):
+        i, t = (int(v) for v in torch.nonzero(live)[j])
+        if not empty[i, t]:
+            against_64_bits(got[i, t], q[i, t], codes, exps, bt, i, idx[i, t].numpy(), page, sink, 512 ** -0.5, tab,
+                            int(first[i]) + t, rd)
+    # every token again in calls of a few (other ranges, other CTAs): a token's result may differ by how its list is cut
+    # into parts, which is within twice the bound of a sum |v| <= 6 * 2^3 of probabilities
+    for i in range(b):
+        for t in range(0, m, 37):
+            few = ds.sparse_attn_fp4_paged(qg[i:i + 1, t:t + 37], cg, eg, btg[i:i + 1], sg, ig[i:i + 1, t:t + 37], 512 ** -0.5,
+                                           rd=rd, table=tg, first=fg[i:i + 1] + t)
+            there = live[i, t:t + 37]
+            far = (few[0].cpu().float() - got[i, t:t + 37].float()).abs()[there]
+            assert (far <= 2 * (2.0 ** -7 + 2.0 ** -11) * 48).all()
+    assert ds.device_status() == 0
+
+
+@gpu
+def test_attention_of_a_causal_prompt(ds):
+    """A prompt of 4096 tokens at 64 heads: causal windows of 128 and up to 512 of 1024 compressed rows, of which
+    the early tokens see few; a sample of tokens against 64 bits."""
+    g = torch.Generator().manual_seed(67)
+    n, h, win, comp, topk, page, rd = 4096, 64, 128, 1024, 512, 64, 64
+    codes, exps, bt = random_pool(g, 1, n + comp, page, 512)
+    q = torch.randn((1, n, h, 512), generator=g).to(torch.bfloat16)
+    sink, tab, first = torch.randn((h,), generator=g), table_of(n, rd), ints(0)
+    at = torch.arange(n)[:, None]
+    w = (at - win + 1).clamp(min=0) + torch.arange(win)
+    w = torch.where(w <= at, w, -1)
+    keys = torch.rand((n, comp), generator=g)
+    keys[torch.arange(comp) >= (at + 1) // 4] = -1
+    val, c = keys.topk(topk, dim=-1)
+    c = torch.where(val >= 0, c + n, -1)
+    idx = torch.cat((w, c), -1).to(torch.int32)[None].contiguous()
+    o = ds.sparse_attn_fp4_paged(*dev(q, codes, exps, bt, sink, idx), 512 ** -0.5, rd=rd, table=tab.cuda(), first=first.cuda())
+    assert ds.device_status() == 0
+    assert o.isfinite().all() and (o != 0).any(-1).all()
+    for t in [0, 1, 2, 3, 126, 127, 128, 129, 4095] + np.random.RandomState(4).choice(n, 25, replace=False).tolist():
+        against_64_bits(o[0, t], q[0, t], codes, exps, bt, 0, idx[0, t].numpy(), page, sink, 512 ** -0.5, tab, t, rd)
+
+
+@gpu
+def test_attention_of_a_full_decode_batch(ds):
+    """256 sequences at 128 heads over 128 ring rows and 2048 of 32768 compressed ones, some entries unseen; a sample."""
+    g = torch.Generator(device="cuda").manual_seed(69)
+    b, h, win, comp, topk, page, rd = 256, 128, 128, 32768, 2048, 64, 64
+    per = (win + comp) // page
+    bt = torch.randperm(b * per, generator=g, device="cuda").view(b, per).to(torch.int32)
+    codes = torch.randint(0, 256, (b * per, page, 256), generator=g, device="cuda", dtype=torch.uint8)
+    exps = torch.randint(-2, 2, (b * per, page, 16), generator=g, device="cuda", dtype=torch.int8)
+    q = torch.randn((b, 1, h, 512), generator=g, device="cuda").to(torch.bfloat16)
+    sink = torch.randn((h,), generator=g, device="cuda")
+    c = torch.rand((b, comp), generator=g, device="cuda").topk(topk, dim=-1).indices + win
+    c = torch.where(torch.rand((b, topk), generator=g, device="cuda") < 0.02, -1, c)
+    idx = torch.cat((torch.arange(win, device="cuda").expand(b, -1), c), -1).to(torch.int32)[:, None].contiguous()
+    first, tab = torch.randint(0, 90, (b,), generator=g, device="cuda", dtype=torch.int32), table_of(100, rd)
+    o = ds.sparse_attn_fp4_paged(q, codes, exps, bt, sink, idx, 512 ** -0.5, rd=rd, table=tab.cuda(), first=first)
+    assert ds.device_status() == 0 and o.isfinite().all() and (o != 0).any(-1).all()
+    for i in np.random.RandomState(6).choice(b, 6, replace=False).tolist():
+        pages = bt[i].long()
+        mine = torch.arange(per, dtype=torch.int32)[None]                # this sequence's pages alone
+        against_64_bits(o[i, 0], q[i, 0], codes[pages].cpu(), exps[pages].cpu(), mine, 0, idx[i, 0].cpu().numpy(), page,
+                        sink.cpu(), 512 ** -0.5, tab, int(first[i]), rd)
