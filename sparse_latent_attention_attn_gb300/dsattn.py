@@ -444,7 +444,8 @@ def norm_rotary(x: torch.Tensor, eps: float, rd: int, table: torch.Tensor | None
     """RMS norm of every row of ``x [b][s][h][d]`` (bf16, the h * d values of a token contiguous; tokens may
     lie in a wider tensor) and the rotation of its last ``rd`` values to position ``first[b] + t``, in
     one pass.  ``y``: bf16 [b][s][h][d] contiguous (``x`` itself when laid out so); tokens at or behind
-    ``lens[b]`` leave it as it was (zeros in a new one)."""
+    ``lens[b]`` leave it as it was (zeros in a new one).  So do tokens outside the table, which the device status
+    names; in a new ``y`` without ``lens`` they hold nothing defined."""
     if x.dim() != 4:
         raise ValueError("x must be [b][s][h][d]")
     b, s, h, d = x.shape

@@ -1514,3 +1514,30 @@ def test_attention_of_a_full_decode_batch(ds):
         mine = torch.arange(per, dtype=torch.int32)[None]                # this sequence's pages alone
         against_64_bits(o[i, 0], q[i, 0], codes[pages].cpu(), exps[pages].cpu(), mine, 0, idx[i, 0].cpu().numpy(), page,
                         sink.cpu(), 512 ** -0.5, tab, int(first[i]), rd)
+
+
+@gpu
+def test_attention_without_its_bad_entries(ds):
+    """Entries past the table, without a page or with one that is not there: every element as without them."""
+    q, codes, exps, bt, sink, idx, *_ = attention_inputs(71, 3, 2, 40, 200, 150, 0.1, 16, 0)
+    g = torch.Generator().manual_seed(71)
+    hole = bt.clone()
+    hole[0, 3], hole[1, 5], hole[2, 0] = -1, codes.shape[0], -2 ** 31
+    wild = torch.where(torch.rand(idx.shape, generator=g) < 0.1,
+                       torch.tensor([13 * 16, 13 * 16 + 5, 2 ** 31 - 1, 10 ** 6])[torch.randint(0, 4, idx.shape, generator=g)], idx)
+    wild = wild.to(torch.int32)
+    # entries of missing pages count as not listed
+    page = (wild.clamp(min=0) // 16).long()
+    inside = (wild >= 0) & (page < 13)
+    there = inside & (torch.gather(hole.long(), 1, page.clamp(max=12).flatten(1)).view(page.shape) >= 0)
+    there &= torch.gather(hole.long(), 1, page.clamp(max=12).flatten(1)).view(page.shape) < codes.shape[0]
+    kept = torch.where(there, wild, -1)
+    assert (there != (wild >= 0)).any(-1).all()
+    o = ds.sparse_attn_fp4_paged(*dev(q, codes, exps, hole, sink, wild), 512 ** -0.5)
+    assert ds.device_status() == ds.DS_DEV_BAD_INDEX
+    for i in range(3):
+        for t in range(2):
+            ix = kept[i, t].numpy()
+            rows, tops = logical_rows(codes, exps, bt, i, ix, 16)
+            ref, A, F = attention_by_weight(f64(q[i, t]), rows, ix >= 0, f64(sink), 512 ** -0.5, tops)
+            assert (np.abs(f64(o[i, t]) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * A + 2.0 ** -17 * F).all()
