@@ -62,7 +62,7 @@ int sparse_attn_bf16(const uint16_t *q, const uint16_t *kv, int64_t n, const flo
     if (!a.status) return DS_ECUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (topk == 0) {   // nothing to attend to: every output is 0 (then rotated, as a separate pass would)
-        if (cudaMemsetAsync(o, 0, (size_t)b * m * h * d * sizeof(uint16_t), st) != cudaSuccess) return DS_ECUDA;
+        if (cudaMemsetAsync(o, 0, (size_t)b * m * h * d * sizeof(uint16_t), st) != cudaSuccess) return launch_failed();
         if (!rope) return DS_OK;
         (void)table_rows;
         return launch_apply_rotary(o, (int64_t)b * m * h, d, rd, h, m, rope_pos0, rope, true, st);
@@ -152,7 +152,7 @@ int ds_sparse_attn_prefill(const uint16_t *q, const uint16_t *kv, int64_t n, con
     if (!aligned16(q) || !aligned16(o) || (kv && !aligned16(kv))) return DS_EINVAL;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (topk == 0)
-        return cudaMemsetAsync(o, 0, (size_t)b * m * h * d * sizeof(uint16_t), st) == cudaSuccess ? DS_OK : DS_ECUDA;
+        return cudaMemsetAsync(o, 0, (size_t)b * m * h * d * sizeof(uint16_t), st) == cudaSuccess ? DS_OK : launch_failed();
     const size_t need = ds_sparse_attn_prefill_workspace_bytes(b, m, h, d, topk);
     if (workspace_bytes < need || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return DS_EWORKSPACE;
@@ -231,7 +231,7 @@ int ds_sparse_attn_fp8kv(const uint16_t *q, const uint8_t *kv_codes, const int8_
     if (!a.status) return DS_ECUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (topk == 0) {   // nothing to attend to: every output is 0
-        return cudaMemsetAsync(o, 0, (size_t)b * m * h * d * sizeof(uint16_t), st) == cudaSuccess ? DS_OK : DS_ECUDA;
+        return cudaMemsetAsync(o, 0, (size_t)b * m * h * d * sizeof(uint16_t), st) == cudaSuccess ? DS_OK : launch_failed();
     }
     return launch_sparse_attn_tc(a, st);
 }
@@ -346,7 +346,7 @@ int sparse_attn_fp4(const uint16_t *q, const uint8_t *codes, const int8_t *exps,
     if (topk > 0 && workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return DS_EWORKSPACE;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (topk == 0 && !lens)   // nothing to attend to: every output is 0
-        return cudaMemsetAsync(o, 0, (size_t)b * m * h * d * sizeof(uint16_t), st) == cudaSuccess ? DS_OK : DS_ECUDA;
+        return cudaMemsetAsync(o, 0, (size_t)b * m * h * d * sizeof(uint16_t), st) == cudaSuccess ? DS_OK : launch_failed();
     const fp4::Args a{q, codes, exps, pages, page, block_table, max_pages, sink, idx, topk, scale, o, b, m, h,
                       workspace, workspace_bytes, rd, reinterpret_cast<const float2 *>(table), table_rows, first, lens,
                       status_word()};

@@ -11,6 +11,12 @@ namespace dsattn {
 
 // Launch helpers return DS_OK / DS_ECUDA.
 inline int launch_status() { return cudaGetLastError() == cudaSuccess ? DS_OK : DS_ECUDA; }
+// After a runtime call that returned its error: taken off the thread's record too, so that the next call's
+// launch_status() does not report it again.
+inline int launch_failed() {
+    (void)cudaGetLastError();
+    return DS_ECUDA;
+}
 
 __device__ __forceinline__ void flag_status(unsigned int *status, unsigned int bits) {
     if (status) atomicOr(status, bits);

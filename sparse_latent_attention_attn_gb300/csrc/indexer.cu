@@ -541,7 +541,7 @@ int launch_scores(const IndexerArgs &a, float *scores, int64_t ld, cudaStream_t 
     const bool wide = QB >= 2;
     auto kernel = wide ? indexer_scores_kernel<D, 8> : indexer_scores_kernel<D, 4>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return DS_ECUDA;
+        return launch_failed();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3(wide ? Roles<8>::NTHREADS : Roles<4>::NTHREADS, 1, 1);
@@ -552,7 +552,7 @@ int launch_scores(const IndexerArgs &a, float *scores, int64_t ld, cudaStream_t 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, kmap, qmap, p) != cudaSuccess) return DS_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, kmap, qmap, p) != cudaSuccess) return launch_failed();
     return DS_OK;
 }
 
@@ -562,7 +562,7 @@ int launch_select_variant(const SelectParams &p, int64_t rows, cudaStream_t stre
     if (SMEM && smem > 48 * 1024 &&
         cudaFuncSetAttribute(indexer_select_kernel<NT, SMEM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(kKeysInSmemMax * sizeof(uint32_t))) != cudaSuccess)
-        return DS_ECUDA;
+        return launch_failed();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)rows, 1, 1);
     cfg.blockDim = dim3(NT, 1, 1);
@@ -573,7 +573,7 @@ int launch_select_variant(const SelectParams &p, int64_t rows, cudaStream_t stre
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, indexer_select_kernel<NT, SMEM>, p) == cudaSuccess ? DS_OK : DS_ECUDA;
+    return cudaLaunchKernelEx(&cfg, indexer_select_kernel<NT, SMEM>, p) == cudaSuccess ? DS_OK : launch_failed();
 }
 
 int launch_select(const float *scores, int64_t ld, const IndexerArgs &a, int32_t *idx, cudaStream_t stream) {

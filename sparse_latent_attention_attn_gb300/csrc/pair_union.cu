@@ -197,7 +197,7 @@ int launch_pair_union(const int32_t *idx, int b, int m, int topk, int64_t n, int
     const size_t smem = (size_t)(3 * cap + 1) * sizeof(int32_t);
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(pair_union_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return DS_ECUDA;
+        return launch_failed();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)npairs, 1, 1);
     cfg.blockDim = dim3(UT, 1, 1);
@@ -210,7 +210,7 @@ int launch_pair_union(const int32_t *idx, int b, int m, int topk, int64_t n, int
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, pair_union_kernel, idx, m, topk, n, pps, uidx, cap, status) == cudaSuccess
                ? DS_OK
-               : DS_ECUDA;
+               : launch_failed();
 }
 
 }  // namespace dsattn

@@ -1255,7 +1255,7 @@ int launch_sparse_attn_fp4_none(const fp4::Args &a, cudaStream_t stream) {
 
 int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream) {
     const fp4::Plan *plan = fp4::plan(a.b, a.m, a.h, a.topk);
-    if (!plan) return DS_ECUDA;
+    if (!plan) return launch_failed();
     const fp4::Plan &pl = *plan;
     const size_t need = fp4::workspace_bytes(pl);
     if (a.workspace_bytes < need || (need && !a.workspace)) return DS_EWORKSPACE;
@@ -1276,7 +1276,7 @@ int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream) {
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, rope ? fp4::sparse_attn_fp4_kernel<true> : fp4::sparse_attn_fp4_kernel<false>, p) !=
         cudaSuccess)
-        return DS_ECUDA;
+        return launch_failed();
     if (pl.split) {
         const fp4::CombineParams head{a, (int)pl.ntok, pl.groups, interleave, p.ws, (int)(pl.G / pl.nunit)};
         const int heads = a.h < fp4::HM ? a.h : fp4::HM;
@@ -1292,7 +1292,7 @@ int launch_sparse_attn_fp4(const fp4::Args &a, cudaStream_t stream) {
             for (int i = 0; i < pl.ncut; ++i) c.cut[i] = pl.cut[i];
             e = cudaLaunchKernelEx(&cfg, rope ? fp4::combine_kernel<true, fp4::CutParams> : fp4::combine_kernel<false, fp4::CutParams>, c);
         }
-        if (e != cudaSuccess) return DS_ECUDA;
+        if (e != cudaSuccess) return launch_failed();
     }
     return DS_OK;
 }

@@ -1127,7 +1127,7 @@ int launch_sparse_attn_ot(const AttnArgs &a, cudaStream_t stream, bool stall_fir
                   : pl.kc == 3 ? (rope ? ot::sparse_attn_ot_kernel<3, true> : ot::sparse_attn_ot_kernel<3, false>)
                   : pl.kc == 4 ? (rope ? ot::sparse_attn_ot_kernel<4, true> : ot::sparse_attn_ot_kernel<4, false>)
                                : (rope ? ot::sparse_attn_ot_kernel<1, true> : ot::sparse_attn_ot_kernel<1, false>);
-    if (cudaLaunchKernelEx(&cfg, kernel, qmap, p) != cudaSuccess) return DS_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, qmap, p) != cudaSuccess) return launch_failed();
     if (combine) {
         cudaLaunchConfig_t ccfg = {};
         ccfg.gridDim = dim3((unsigned)cpar.ncut, (unsigned)(ot::D / ot::kCombineCols), 1);
@@ -1136,7 +1136,7 @@ int launch_sparse_attn_ot(const AttnArgs &a, cudaStream_t stream, bool stall_fir
         ccfg.attrs = attr;
         ccfg.numAttrs = 1;
         auto comb = rope ? ot::sparse_attn_ot_combine_kernel<true> : ot::sparse_attn_ot_combine_kernel<false>;
-        if (cudaLaunchKernelEx(&ccfg, comb, cpar) != cudaSuccess) return DS_ECUDA;
+        if (cudaLaunchKernelEx(&ccfg, comb, cpar) != cudaSuccess) return launch_failed();
     }
     return DS_OK;
 }

@@ -1518,7 +1518,7 @@ int launch(const AttnArgs &a, cudaStream_t stream) {
             return DS_EUNSUPPORTED;
         }
     }
-    if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return DS_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return launch_failed();
     if (split) {
         cudaLaunchConfig_t ccfg = {};
         ccfg.gridDim = dim3((unsigned)cpar.ncut, (unsigned)((D + kCombineCols - 1) / kCombineCols), 1);
@@ -1526,7 +1526,7 @@ int launch(const AttnArgs &a, cudaStream_t stream) {
         ccfg.stream = stream;
         ccfg.attrs = attr;   // programmatic serialization only
         ccfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&ccfg, combine, cpar) != cudaSuccess) return DS_ECUDA;
+        if (cudaLaunchKernelEx(&ccfg, combine, cpar) != cudaSuccess) return launch_failed();
     }
     return DS_OK;
 }

@@ -1541,3 +1541,35 @@ def test_attention_without_its_bad_entries(ds):
             rows, tops = logical_rows(codes, exps, bt, i, ix, 16)
             ref, A, F = attention_by_weight(f64(q[i, t]), rows, ix >= 0, f64(sink), 512 ** -0.5, tops)
             assert (np.abs(f64(o[i, t]) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * A + 2.0 ** -17 * F).all()
+
+
+@gpu
+def test_a_refused_launch_does_not_fail_the_next_call(ds):
+    """A launch that CUDA refuses (on the legacy stream while a blocking stream is captured) returns its error, and
+    only that call does."""
+    rt = ctypes.CDLL("libcudart.so.13")
+    x = attention_inputs(73, 1, 1, 4, 40, 20, 0.0, 8, 0)
+    qg, cg, eg, btg, sg, ig = dev(*x[:6])
+    o = torch.empty_like(qg)
+    row = torch.ones((1, 1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    y, zero = torch.zeros_like(row), ints(0).cuda()
+    attend = lambda: ds._lib.ds_sparse_attn_fp4_paged(qg.data_ptr(), cg.data_ptr(), eg.data_ptr(), cg.shape[0], 8, btg.data_ptr(),
+                                                      btg.shape[1], sg.data_ptr(), ig.data_ptr(), 20, 0.1, o.data_ptr(), 1, 1, 4,
+                                                      512, None, 0, 0, None, 0, None, None)
+    norm = lambda: ds._lib.ds_norm_rotary(row.data_ptr(), 64, 64, y.data_ptr(), 1, 1, 1, 64, None, 1e-6, 0, None, 0,
+                                          zero.data_ptr(), None, None)
+    assert attend() == 0 and norm() == 0
+    torch.cuda.synchronize()
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert rt.cudaStreamCreate(ctypes.byref(stream)) == 0
+    for refused in (attend, norm):
+        assert rt.cudaStreamBeginCapture(stream, 0) == 0           # 0: global
+        first = refused()
+        assert rt.cudaStreamEndCapture(stream, ctypes.byref(graph)) != 0
+        rt.cudaGetLastError()
+        assert first == -4
+        y.zero_()
+        assert norm() == 0 and attend() == 0
+        torch.cuda.synchronize()
+        assert (y != 0).all() and ds.device_status() == 0
+    assert rt.cudaStreamDestroy(stream) == 0
