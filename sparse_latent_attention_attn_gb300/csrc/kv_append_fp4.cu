@@ -15,13 +15,14 @@
 // border lies between them the warp goes through the formula with two floats a number (to about 2^-44): two rows
 // of 512 in a thousand.  Rows that are neither normalised nor rotated are exact in f32 (t = 0).
 //
-// HBM has 2 bytes read and 17/32 written a value, 2 more with y; what bounds long batches is the integer pipe
-// (0.69 of its rate: conversions, byte permutes, maxima, exponents), decode sizes latency.  One row a warp (half
+// HBM has 2 bytes read and 17/32 written a value, 2 more with y; no pipe is full in long batches (the
+// integer pipe 0.69 of its rate, issue 0.67 a cycle and scheduler, 43 % of the warps: 650 instructions a row, in chains
+// of conversions, byte permutes, maxima and exponents), decode sizes are bound by latency.  One row a warp (half
 // or a quarter for short rows), 16 bytes a lane and step; a block's maximum is two shuffles over its four lanes,
 // and a warp stores 128 contiguous bytes of codes.  Several rows a warp with the next one's loads ahead took as
 // long or longer (four 31.5 us, two 38.2), for their registers.
 // Measured: 8 x 4096 rows of 512 with y, 28.7 us (650 instructions a row; its bytes alone 12.4 us); 256 rows into
-// rings 4.3 us on the device.
+// rings 5.1 us a call in a graph.
 #include "f32x2.cuh"
 #include "paged_rows.cuh"
 #include "row_norm.cuh"
@@ -151,7 +152,7 @@ __device__ __forceinline__ F2 norm_factor2(float hi, float lo, float d, float ep
 }
 
 // 64 registers, so that four blocks run on an SM (8 x 4096 rows of 512: 28.7 us; with three of 72, 33.3; with
-// five of 48, 30.8); rows above 512 take 86 registers
+// five of 48, 30.8); rows above 512 take 96 registers
 template <int L, int N>
 __global__ void __launch_bounds__(kThreads, N <= 2 ? 4 : 2) kv_append_fp4_kernel(const AppendArgs p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -8,8 +8,9 @@
 // The mathematics.  A row is v_r = 2^(e_r - 12) c_r, e_r its largest block exponent, -48 at least, and c_r its codes
 // times 2^(k - e_r + 12): e2m1 has one mantissa bit, so c_r is exact in e5m2 for blocks down to 26 octaves below
 // e_r (lower ones count as zeros).  Exponents above 48 are read as 48 and flagged: with e_r in [-48, 48] the scores'
-// products, P' 2^-e_r and their sums stay normal f32 numbers, and what falls below them is under 2^-34 of a sum.  One byte a value serves as key and as value, and the row's own power
-// of two moves to where the row is a single number: to its scores, and to its probability.
+// products, P' 2^-e_r and their sums stay normal f32 numbers, and what falls below them is under 2^-34 of a sum.
+// One byte a value serves as key and as value, and the row's own power of two moves to where the row is a
+// single number: to its scores, and to its probability.
 //  * q = 2^g (hi + 2^-5 lo), hi and lo in e4m3: hi holds q's top four significant bits, lo the four below
 //    them, so a bf16 q (eight) is exact down to 2^-9 of its head's largest value and off by 2^-22 of that
 //    largest value below.  S^T = C [hi | lo]: M = 128 rows, N = 64 heads twice, and the score is
@@ -24,7 +25,10 @@
 //
 // Why so.  A tile is 128 rows of 512 bytes, so two tiles, q (64 KB as hi and lo) and P fit the 227 KB of an
 // SM; as bf16 only tiles of 64 rows would, and a 64-row tcgen05.mma takes the time of a 128-row one.  With
-// N = 128 in S and K = 32 a step a tile takes 16 + 32 instructions where bf16 rows would take 64 + 64.  The
+// N = 128 in S and K = 32 a step a tile takes 16 + 32 instructions where bf16 rows would take 64 + 64.  The price is
+// q and P in two 8-bit pieces each, which is a choice: with one piece each would keep four bits; a third for P
+// would add half to P V's instructions, and to the conversions, for bits that the output, bf16, mostly drops
+// (errors against 64 bits: 0.0018-0.0020 of the output, 0.0017 with everything in f32 before its rounding).  The
 // widening to e5m2 goes through f16: a conversion and a product for two codes, a byte permute for four.
 //
 // Warps: 0-7 softmax and epilogue (warp w: TMEM lanes 32 (w % 4).., heads 32 (w / 4)..), 8-15 rows (codes
@@ -34,16 +38,18 @@
 // the index warp and the row warps.  What a tile is (its rows, whether it is its unit's first or last) goes on
 // with the stage.  The softmax holds 32 heads of scores a thread and the row warps eight row loads in flight, so
 // of the launch's 96 registers a thread the softmax warps take 120 and leave the others 80; 16 softmax warps
-// with half the heads, or 12 more row warps, were slower (more instructions in all, or spilled loads).
+// with half the heads, or 12 more row warps, were slower (more instructions in all, or spilled loads).  ptxas spills
+// 36 bytes a thread.
 // A unit is one token and up to 64 heads; units are shared out as in the other attention kernels
 // (attn_split.cuh), and units cut by a range boundary leave f32 partials that a second kernel merges.
 // Every wait is bounded (2 s): then DS_DEV_TIMEOUT is flagged, issued MMAs are drained, TMEM is freed.
 //
-// Measured (entries / heads): 256 tokens of 2176 / 128, 216 us (661 TFLOP/s; its MMAs alone 72 us);
-// 4096 prefill tokens of up to 640 / 64, 519 us (527 TFLOP/s); 64 tokens of 128 / 64, 12.1 us; one token of 2176 / 16,
-// 15.4 us.  What bounds it is the issue of instructions: a scheduler's five warps get about one every two cycles
-// through, a tile takes about 5500 cycles of it (rows about 3000, softmax about 3500, side by side; the MMAs 2600
-// beneath them), a unit's end (output, the next q) about 8500.
+// Measured (entries / heads): 256 tokens of 2176 / 128, 217 us (658 TFLOP/s; its MMAs alone 72 us);
+// 4096 prefill tokens of up to 640 / 64, 523 us (523 TFLOP/s); 64 tokens of 128 / 64, 12.2 us; one token of 2176 / 16,
+// 15.6 us.  No pipe is full (a scheduler issues 0.43 to 0.46 a cycle, tensor 18 to 31 %, ALU 33 to 38 %, DRAM 11 to 13 %):
+// a stage is held from its widening (about 3000 cycles) through S (750, and 560 to its readers) and the softmax
+// (3500) to the end of P V (1400 to 1900), and with two stages that chain of 9000 to 9700 sets most of the 5500
+// cycles that a tile takes.  A unit's end (output, the next q) takes about 8500 more.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -303,8 +309,7 @@ __device__ __forceinline__ Unit unit_of(const Params &p, uint32_t u) {
 }
 
 // Heads hh .. hh + n - 1 of a unit's q into [hi | lo], the next two heads in flight; lane i < n gets the scale of head
-// hh + i, 2^g |scale| log2(e).  ready(), between the first loads and the first store, says
-// whether to go on.
+// hh + i, 2^g |scale| log2(e).  ready(), between the first loads and the first store, says whether to go on.
 template <typename F>
 __device__ __forceinline__ float put_heads(const Params &p, uint32_t sq, uint32_t unit, int hh, int n, int lane, F ready) {
     const Unit un = unit_of(p, unit);
