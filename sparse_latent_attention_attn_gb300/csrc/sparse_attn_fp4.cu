@@ -5,10 +5,10 @@
 // "DeepSeek V4.1", attention/query-latent, Attention.forward (the output's inverse rotation).  Rows are
 // e2m1 codes with a power-of-two scale per 32 values, reached through a table of pages.
 //
-// The mathematics.  A row is v_r = 2^(e_r - 12) c_r, e_r its largest block exponent, -48 at least, and c_r its codes
+// The mathematics.  A row is v_r = 2^(e_r - 12) c_r, e_r its largest block exponent, -96 at least, and c_r its codes
 // times 2^(k - e_r + 12): e2m1 has one mantissa bit, so c_r is exact in e5m2 for blocks down to 26 octaves below
-// e_r (lower ones count as zeros).  Exponents above 48 are read as 48 and flagged: with e_r in [-48, 48] the scores'
-// products, P' 2^-e_r and their sums stay normal f32 numbers, and what falls below them is under 2^-34 of a sum.
+// e_r (lower ones count as zeros).  Exponents above 100 are read as 100 and flagged: with e_r in [-96, 100] the scores'
+// products (2^32 2^(e_r - 12)) and the sums of P' 2^-e_r (of 2^20 rows) stay below f32's largest.
 // One byte a value serves as key and as value, and the row's own power of two moves to where the row is a
 // single number: to its scores, and to its probability.
 //  * q = 2^g (hi + 2^-5 lo), hi and lo in e4m3: hi holds q's top four significant bits, lo the four below
@@ -21,7 +21,8 @@
 //    2^-8 of itself, as bf16 would be, from 2^-6 on (hi has four bits, lo three of the rest), and by 2^-13
 //    below (hi is a multiple of 2^-9): 2^-17 of the head's largest p 2^e.  O^T += C^T (hi - lo), d = 512
 //    as four blocks of 128 lanes, heads as columns; l = sum of P' 2^-e_r of the unrounded f32 P', which is
-//    2^(4 - m) times the denominator, so O 2^-12 / (l + 2^(sink + 4 - m)) is the output.
+//    2^(4 - m) times the denominator, so O 2^-12 / (l + 2^(sink + 4 - m)) is the output.  P' below 2^-126 is 0: a
+//    row D octaves below the one that sets m loses its part in l from 2^(D - 130) of that one's probability on.
 //
 // Why so.  A tile is 128 rows of 512 bytes, so two tiles, q (64 KB as hi and lo) and P fit the 227 KB of an
 // SM; as bf16 only tiles of 64 rows would, and a 64-row tcgen05.mma takes the time of a 128-row one.  With
@@ -126,7 +127,7 @@ static_assert(TM_S + 2 * 2 * HM <= TMEM_COLS, "TMEM budget");
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTop = 4;                 // octaves of P' at m
-constexpr int kMaxExp = 48;             // e_r lies in [-kMaxExp, kMaxExp]
+constexpr int kMinExp = -96, kMaxExp = 100;     // of e_r
 constexpr float kSlack = 4.0f;          // octaves that m may be late
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -699,7 +700,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) sparse_attn_fp4_kernel(const Para
                 const int i = 64 * (warp - W_EXP) + 32 * k + lane;
                 const uint32_t m4 = __vmaxs4(__vmaxs4(ev[k].x, ev[k].y), __vmaxs4(ev[k].z, ev[k].w));
                 int top = max(max((int)(int8_t)m4, (int)(int8_t)(m4 >> 8)), max((int)(int8_t)(m4 >> 16), (int)m4 >> 24));
-                top = max(top, -kMaxExp);
+                top = max(top, kMinExp);
                 if (top > kMaxExp) {
                     constexpr uint32_t most = (uint32_t)kMaxExp * 0x01010101u;
                     ev[k] = make_uint4(__vmins4(ev[k].x, most), __vmins4(ev[k].y, most), __vmins4(ev[k].z, most),

@@ -923,9 +923,9 @@ def test_the_plain_quantiser():
 # ---- rows of very different scale: a row's weight is its probability times its scale -------------------------
 
 def attention_by_weight(q, rows, live, sink, scale, tops):
-    """As attention(), F relative to each head's largest p 2^e (e the row's largest exponent, -48 at least): a
+    """As attention(), F relative to each head's largest p 2^e (e the row's largest exponent, -96 at least): a
     probability is held to 2^-8 of itself or to 2^-17 of that, whatever exponents other rows have."""
-    rows, e = rows[live], np.maximum(tops[live], -48).astype(float)
+    rows, e = rows[live], np.maximum(tops[live], -96).astype(float)
     s = scale * q @ rows.T
     top = s.max(-1, keepdims=True)
     p = np.exp(s - top)
@@ -979,7 +979,7 @@ def test_attention_large_row_without_weight(ds, b, h, topk, octaves):
 
 @gpu
 @pytest.mark.parametrize("b,h,topk", [(2, 24, 200), (1, 70, 900)])
-@pytest.mark.parametrize("k", [45, 20, -20, -45, -60, -71])
+@pytest.mark.parametrize("k", [97, 60, 20, -20, -60, -93, -119])
 def test_attention_exponent_range(ds, b, h, topk, k):
     """All rows near one end of the exponents that are read as they are."""
     q, codes, exps, bt, sink, idx, *_ = attention_inputs(43, b, 1, h, 1000, topk, 0.1, 16, 0)
@@ -987,14 +987,15 @@ def test_attention_exponent_range(ds, b, h, topk, k):
     check_by_weight(ds, q, codes, exps + k, bt, sink, idx)
     # exponents of a block apart too: 26 below the row's largest still count
     wide = exps + k
-    wide[..., 1::2] = max(k, -48) - 23
+    wide[..., 1::2] = max(k, -96) - 23
     check_by_weight(ds, q, codes, wide, bt, sink, idx)
 
 
 @gpu
 @pytest.mark.parametrize("b,h,topk", [(2, 24, 200), (1, 70, 900)])
-def test_attention_both_ends_of_the_exponents(ds, b, h, topk):
-    """Rows at 2^48 beside rows at 2^-48: with the scores of order one, and with the large rows far below."""
+@pytest.mark.parametrize("hi,lo", [(100, 4), (48, -48), (81, -15), (0, -96)])
+def test_attention_both_ends_of_the_exponents(ds, b, h, topk, hi, lo):
+    """Rows 96 octaves above others: with the scores of order one, and with the large rows far below."""
     q, codes, exps, bt, sink, idx, *_ = attention_inputs(45, b, 1, h, 1000, topk, 0.0, 16, 0)
     odd = torch.zeros((b, 1000), dtype=torch.bool)
     for i in range(b):
@@ -1003,34 +1004,34 @@ def test_attention_both_ends_of_the_exponents(ds, b, h, topk):
     code = torch.where(sign < 0, 10, 2).to(torch.uint8)
     for i in range(b):
         for r in range(1000):
-            exps[bt[i, r // 16], r % 16] = 48 if odd[i, r] else -48
-    check_by_weight(ds, q, codes, exps, bt, sink, idx, scale=2.0 ** -48 * 512 ** -0.5)
+            exps[bt[i, r // 16], r % 16] = hi if odd[i, r] else lo
+    check_by_weight(ds, q, codes, exps, bt, sink, idx, scale=2.0 ** -hi * 512 ** -0.5)
     for i in range(b):
         for r in torch.nonzero(odd[i])[:, 0].tolist():
             codes[bt[i, r // 16], r % 16] = code[0::2] | code[1::2] << 4
     low = (q.float() - 20 * sign).to(torch.bfloat16)               # their scores: about -512
-    o = check_by_weight(ds, low, codes, exps, bt, torch.full_like(sink, -math.inf), idx, scale=2.0 ** -48 * 0.05)
-    assert (o.abs() < 2.0 ** -44).all() and (o != 0).any(-1).all()
+    o = check_by_weight(ds, low, codes, exps, bt, torch.full_like(sink, -math.inf), idx, scale=2.0 ** -hi * 0.05)
+    assert (o.abs() < 2.0 ** (lo + 4)).all() and (o != 0).any(-1).all()
 
 
 @gpu
 @pytest.mark.parametrize("b,h,topk", [(2, 24, 200), (1, 70, 900)])
 def test_attention_exponents_outside_the_range(ds, b, h, topk):
-    """Above 48: read as 48, and said so; below -74: zeros."""
+    """Above 100: read as 100, and said so; below -122: zeros."""
     q, codes, exps, bt, sink, idx, *_ = attention_inputs(47, b, 1, h, 1000, topk, 0.1, 16, 0)
-    q = (q.float() * 2.0 ** -48).to(torch.bfloat16)
-    for lo, hi in ((49, 127), (40, 60), (110, 121)):
+    q = (q.float() * 2.0 ** -100).to(torch.bfloat16)
+    for lo, hi in ((101, 127), (90, 110), (110, 121)):
         high = torch.randint(lo, hi + 1, exps.shape, generator=torch.Generator().manual_seed(lo), dtype=torch.int8)
-        check_by_weight(ds, q, codes, high, bt, sink, idx, status=ds.DS_DEV_BAD_VALUE, read=high.clamp(max=48))
+        check_by_weight(ds, q, codes, high, bt, sink, idx, status=ds.DS_DEV_BAD_VALUE, read=high.clamp(max=100))
     # one block of one listed row is enough; of a row that is not listed, none counts
     one = torch.zeros_like(exps)
     r = int(idx[0, 0][idx[0, 0] >= 0][5])
     unlisted = next(x for x in range(1000) if x not in idx[0, 0].tolist())
-    one[bt[0, unlisted // 16], unlisted % 16] = 100
+    one[bt[0, unlisted // 16], unlisted % 16] = 120
     check_by_weight(ds, q, codes, one, bt, sink, idx)
-    one[bt[0, r // 16], r % 16, 7] = 49
-    check_by_weight(ds, q, codes, one, bt, sink, idx, status=ds.DS_DEV_BAD_VALUE, read=one.clamp(max=48))
-    for lo, hi in ((-128, -75), (-128, -128), (-101, -100)):
+    one[bt[0, r // 16], r % 16, 7] = 101
+    check_by_weight(ds, q, codes, one, bt, sink, idx, status=ds.DS_DEV_BAD_VALUE, read=one.clamp(max=100))
+    for lo, hi in ((-128, -123), (-128, -128), (-125, -124)):
         tiny = torch.randint(lo, hi + 1, exps.shape, generator=torch.Generator().manual_seed(hi + 200), dtype=torch.int8)
         assert (check_by_weight(ds, q, codes, tiny, bt, sink, idx, read=torch.zeros_like(tiny) - 128) == 0).all()
 
