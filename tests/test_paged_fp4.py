@@ -1574,3 +1574,53 @@ def test_a_refused_launch_does_not_fail_the_next_call(ds):
         torch.cuda.synchronize()
         assert (y != 0).all() and ds.device_status() == 0
     assert rt.cudaStreamDestroy(stream) == 0
+
+
+@gpu
+@pytest.mark.parametrize("h,W", [(20, 40), (100, 300)])
+def test_padded_step_captured_and_replayed(ds, h, W):
+    """A step of two tokens captured with lens: each replay takes the lengths, positions and rows of its time; and
+    the same on a stream given by hand."""
+    from sparse_latent_attention_attn_gb300 import path
+    g = torch.Generator().manual_seed(81)
+    b, s, d, rd, page, eps = 3, 2, 512, 64, 16, 1e-6
+    codes, exps, bt = random_pool(g, b, W, page, d)
+    tab, sink = table_of(W + 60, rd).cuda(), torch.randn((h,), generator=g).cuda()
+    btg = bt.cuda()
+    static = {"q": torch.zeros((b, s, h, d), dtype=torch.bfloat16, device="cuda"),
+              "kv": torch.zeros((b, s, d), dtype=torch.bfloat16, device="cuda"),
+              "first": torch.zeros((b,), dtype=torch.int32, device="cuda"),
+              "lens": torch.full((b,), s, dtype=torch.int32, device="cuda"),
+              "idx": torch.zeros((b, s, W), dtype=torch.int32, device="cuda")}
+    o = torch.zeros((b, s, h, d), dtype=torch.bfloat16, device="cuda")
+
+    def step(c, e, out, stream=None):
+        return path.decode_step_fp4_paged(static["q"], static["kv"], c, e, btg, static["first"], sink, static["idx"], W,
+                                          d ** -0.5, rd, tab, eps, lens=static["lens"], o=out, stream=stream)
+
+    one, two = dev(codes, exps), dev(codes, exps)
+    step(*dev(codes, exps), torch.zeros_like(o))
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        step(*one, o)
+    for n, lens in enumerate((ints(2, 1, 0), ints(0, 2, 2), ints(0, 0, 0), ints(1, 2, 9))):
+        first = torch.randint(W, W + 50, (b,), generator=g, dtype=torch.int32)
+        idx = torch.stack([torch.randperm(W, generator=g) for _ in range(b * s)]).view(b, s, W).to(torch.int32)
+        for k, v in (("q", torch.randn((b, s, h, d), generator=g)), ("kv", torch.randn((b, s, d), generator=g)),
+                     ("first", first), ("lens", lens), ("idx", idx)):
+            static[k].copy_(v)
+        live = torch.arange(s) < lens[:, None]
+        o.fill_(5.0)
+        other = torch.full_like(o, 5.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        step(*two, other, stream=side)
+        torch.cuda.synchronize()
+        assert ds.device_status() == 0
+        assert torch.equal(o, other) and torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+        assert (o.cpu()[~live] == 5).all() and (o.cpu()[live] != 5).any(-1).all()
+        for i, t in torch.nonzero(live).tolist():
+            zq = ds.norm_rotary(static["q"], eps, rd, tab, static["first"])[i, t].cpu()
+            against_64_bits(o[i, t], zq, one[0].cpu(), one[1].cpu(), bt, i, idx[i, t].numpy(), page, sink.cpu(), d ** -0.5,
+                            tab.cpu(), int(first[i]) + t, rd)
