@@ -444,8 +444,9 @@ int ds_kv_append_fp4_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstri
  * Block exponents above 100 are read as 100 and raise DS_DEV_BAD_VALUE (ds_kv_append_fp4_paged
  * stores them for values above 6 * 2^100 only); blocks whose exponent is more than 26 below the
  * row's largest, or below -122, count as zeros.  In a list whose rows' largest exponents lie D > 96
- * apart, probabilities below 2^(D - 130) of the largest may count as 0.  A head of q that holds an infinity or a NaN gives NaN
- * where it has rows; otherwise scale * q and the scores must be finite in f32.
+ * apart, probabilities below 2^(D - 130) of the largest may count as 0.  A head of q that holds an
+ * infinity or a NaN gives NaN where it has rows; otherwise scale * q and the scores must be finite
+ * in f32.
  *
  * rd         multiple of 8, 0 <= rd <= d (0: no rotation; table and first may be NULL)
  * workspace  at least ds_sparse_attn_fp4_paged_workspace_bytes(b, m, h, d, topk) bytes, 256-byte
