@@ -3,8 +3,9 @@
  * attention: the sliding-window index rows, the fp8 round trip of new KV rows into the ring,
  * and sparse_attn itself (gathered-row latent attention with an attention sink); beside them the
  * RoPE rotation (fused into the ring write, or on its own for the output's inverse rotation) and
- * an fp8 row store that keeps KV rows as their e4m3 codes; and a paged row store of 4-bit codes
- * with the calls that fill it and attend over it for sequences at positions of their own.
+ * an fp8 row store that keeps KV rows as their e4m3 codes; and paged row stores of 4-bit and of
+ * 8-bit codes with the calls that fill them, read them back and attend over them for sequences at
+ * positions of their own.
  *
  * Conventions for every call:
  *   - All tensor pointers are DEVICE pointers, owned by the caller.  The library allocates no
@@ -472,6 +473,96 @@ int ds_sparse_attn_fp4_paged_ragged(const uint16_t *q, const uint8_t *codes, con
                                     int topk, float scale, uint16_t *o, int b, int m, int h, int d, void *workspace,
                                     size_t workspace_bytes, int rd, const float *table, int64_t table_rows,
                                     const int32_t *first, const int32_t *lens, ds_stream_t stream);
+
+/*
+ * The paged 8-bit row store: the fp8 row store's codes and exponents (above) in the pages of the 4-bit one,
+ *     codes        uint8 [pages][page][d]        e4m3fn codes
+ *     exps         int8  [pages][page][d / 32]   k with scale = 2^k for the block of 32
+ *     block_table  int32 [b][max_pages]          page of a sequence's logical rows
+ * so a row decodes to the bf16 row that the model itself computes with ("Module attn", act_quant_inplace),
+ * at 33/32 byte a value.  Logical rows, first, lens and the flags are those of the 4-bit store.  The pool is an
+ * fp8 row store of pages * page rows too: ds_sparse_attn_fp8kv reads it with b = 1, n = pages * page and the
+ * slots (page * page size + offset) as entries.
+ */
+
+/*
+ * ds_kv_append_fp8_paged -- ds_kv_append_fp4_paged into the paged 8-bit row store: per block of 32
+ *     k = ceil(log2(max(amax, 1e-4) / 448)),  code = z / 2^k to the nearest e4m3, ties to even,
+ * decided on z itself.  y: the values that the codes stand for, exact in bf16, except that 2^128 (what values of z
+ * from 31 * 2^123 on are stored as) is infinity there.  Other arguments and the errors are those of
+ * ds_kv_append_fp4_paged.
+ */
+int ds_kv_append_fp8_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint16_t *y, int b, int s, int d,
+                           const float *weight, float eps, int rd, const float *table, int64_t table_rows,
+                           const int32_t *first, const int32_t *lens, int pos_step, int base, int window,
+                           uint8_t *codes, int8_t *exps, int64_t pages, int page, const int32_t *block_table,
+                           int max_pages, ds_stream_t stream);
+
+/*
+ * ds_kv_read_fp8_paged, ds_kv_read_fp4_paged -- rows of a paged row store as the bf16 values that they stand for.
+ * y[bi][i] is logical row idx[bi][i] of sequence bi, or row first[bi] + i where idx is NULL.  Entries < 0 of
+ * idx give rows of zeros; so does a row without a page, or a negative one from first, which raises
+ * DS_DEV_BAD_INDEX.  Rows i at or behind lens[bi] are padding: y is left as it was there.  The values are exact
+ * wherever bf16 holds them (any exponent of [-128, 119], and above that what stays below 2^128), else
+ * rounded once.
+ *
+ * y          device bf16 [b][n][d], 16-byte aligned
+ * idx        device int32 [b][n], or NULL
+ * first      device int32 [b], or NULL for 0; not read when idx is there
+ * lens       device int32 [b], or NULL for n
+ * d          multiple of 32, <= 1024;  b * n < 2^31, pages * page < 2^31 (DS_EUNSUPPORTED otherwise)
+ * codes      16-byte aligned
+ * Errors: DS_EINVAL, DS_EUNSUPPORTED, DS_ECUDA.
+ */
+int ds_kv_read_fp8_paged(const uint8_t *codes, const int8_t *exps, int64_t pages, int page, const int32_t *block_table,
+                         int max_pages, const int32_t *idx, const int32_t *first, const int32_t *lens, uint16_t *y,
+                         int b, int n, int d, ds_stream_t stream);
+int ds_kv_read_fp4_paged(const uint8_t *codes, const int8_t *exps, int64_t pages, int page, const int32_t *block_table,
+                         int max_pages, const int32_t *idx, const int32_t *first, const int32_t *lens, uint16_t *y,
+                         int b, int n, int d, ds_stream_t stream);
+
+/*
+ * ds_chunk_attn_fp8_paged -- attention of a chunk of new tokens (one or many a sequence) over the paged 8-bit row
+ * store, where a query sees rows by its position and no index rows are listed: the window's rows, and all
+ * compressed rows that are complete.  Sources: "DeepSeek V4.1", attention/attend (get_window_topk_idxs: the
+ * causal window) and attention/query-latent (Attention.forward; the Indexer's compress_lens: position p sees
+ * (p + 1) / ratio compressed rows, all of which it keeps while they are at most index_topk).
+ *
+ * The query (bi, t, hh) is at position p = first[bi] + t.  It sees
+ *     the rows of positions max(0, p - window + 1) .. p (window 0: 0 .. p); position i is logical row
+ *         i % ring (ring > 0) or i (ring = 0);
+ *     compressed rows 0 .. (p + 1) / ratio - 1 (ratio 0: none); number j is logical row base + j.
+ * The chunk's own rows are in the store already (ds_kv_append_fp8_paged with the ring as its window, then the
+ * compressed rows with pos_step = ratio and this base).  Over the rows that it sees the operation is ds_sparse_attn's,
+ * with the inverse RoPE of position p before o's one rounding when rd > 0 (a position outside the table leaves
+ * that token's o unrotated).  Rows without a page are skipped and flagged (DS_DEV_BAD_INDEX); a query that sees no row
+ * gives o = 0, and so does one at a negative position, which is flagged.
+ * Scores, softmax and accumulation are f32; a probability enters the value product rounded to bf16, as in
+ * ds_sparse_attn.  The rows that queries of a sequence see must be finite in bf16 (their largest code times
+ * 2^k below 2^128), and scale * q, the scores and the products that are added up finite in f32.  Rows
+ * that no query of the sequence sees do not matter, nor does what unused pages hold.
+ *
+ * q          device bf16 [b][m][h][512]
+ * sink       device f32 [h]
+ * o          device bf16 [b][m][h][512], written (tokens at or behind lens[bi] are left as they were)
+ * first      device int32 [b];  lens: device int32 [b], or NULL for m
+ * window     >= 0;  ring 0, or at least window (window > 0) and at most max_pages * page, and without lens at
+ *            least window + m - 1, so that the chunk's rows replaced none that its queries see; with lens
+ *            the same must hold for the largest of them
+ * base       >= 0, and >= ring when there are both a ring and compressed rows
+ * workspace  at least ds_chunk_attn_fp8_paged_workspace_bytes bytes for the same arguments, 256-byte aligned (may
+ *            be NULL when that size is 0); its contents need no initialisation and mean nothing afterwards.
+ *            Calls that may run at the same time need one each.
+ * Supported: d = 512, 1 <= h <= 128, b * m * h < 2^31, pages * page < 2^31; q, o, codes and exps 16-byte aligned.
+ * Errors: DS_EINVAL, DS_EUNSUPPORTED, DS_EWORKSPACE, DS_ECUDA.
+ */
+size_t ds_chunk_attn_fp8_paged_workspace_bytes(int b, int m, int h, int d, int window, int ratio, int page,
+                                               int max_pages);
+int ds_chunk_attn_fp8_paged(const uint16_t *q, const uint8_t *codes, const int8_t *exps, int64_t pages, int page,
+                            const int32_t *block_table, int max_pages, const float *sink, float scale, uint16_t *o,
+                            int b, int m, int h, int d, const int32_t *first, const int32_t *lens, int window, int ring,
+                            int ratio, int base, void *workspace, size_t workspace_bytes, int rd, const float *table,
+                            int64_t table_rows, ds_stream_t stream);
 
 /*
  * ds_device_status -- synchronise `stream`, then read and clear the current device's status word

@@ -4,6 +4,7 @@
 
 #include <mutex>
 
+#include "chunk_attn_fp8.cuh"
 #include "common.cuh"
 #include "paged_rows.cuh"
 #include "sparse_attn_fp4.cuh"
@@ -307,7 +308,7 @@ int ds_indexer_topk(const uint16_t *q, const uint16_t *k, const float *w, int b,
     return launch_indexer_select(scores, ld, a, idx, strm);
 }
 
-// ---- the paged 4-bit row store -------------------------------------------------------------------
+// ---- the paged row stores --------------------------------------------------------------------------
 
 namespace {
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -353,6 +354,35 @@ int sparse_attn_fp4(const uint16_t *q, const uint8_t *codes, const int8_t *exps,
     if (!a.status) return DS_ECUDA;
     return topk == 0 ? launch_sparse_attn_fp4_none(a, st) : launch_sparse_attn_fp4(a, st);
 }
+// ds_kv_append_fp4_paged and ds_kv_append_fp8_paged (a.status is set here)
+int kv_append(AppendCall a, int (*launch)(const AppendCall &, cudaStream_t), ds_stream_t stream) {
+    if (a.b < 0 || a.s < 0 || a.d < 32 || a.d % 32 != 0 || a.pos_step < 1 || a.base < 0 || a.window < 0) return DS_EINVAL;
+    if (a.eps != 0.0f && !(a.eps >= 0x1p-100f)) return DS_EINVAL;
+    if (!rotation_ok(a.rd, a.d, a.table, a.table_rows) || !pool_ok(a.pages, a.page, a.max_pages)) return DS_EINVAL;
+    if (a.d > 1024 || !pool_fits(a.pages, a.page) || (int64_t)a.b * a.s > INT32_MAX) return DS_EUNSUPPORTED;
+    if ((int64_t)a.b * a.s == 0) return DS_OK;
+    if (!a.x || !a.first || !aligned16(a.x) || !aligned16(a.y) || !aligned16(a.weight) || !aligned4(a.first) || !aligned4(a.lens))
+        return DS_EINVAL;
+    if (!store_there(a.codes, a.exps, a.pages, a.block_table, a.max_pages) || !aligned16(a.codes) || !aligned4(a.block_table))
+        return DS_EINVAL;
+    if (!strides_ok(a.x_bstride, a.x_tstride, a.b, a.s, a.d)) return DS_EINVAL;
+    a.status = status_word();
+    if (!a.status) return DS_ECUDA;
+    return launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ds_kv_read_fp4_paged and ds_kv_read_fp8_paged
+int kv_read(ReadCall a, int (*launch)(const ReadCall &, cudaStream_t), ds_stream_t stream) {
+    if (a.b < 0 || a.n < 0 || a.d < 32 || a.d % 32 != 0 || !pool_ok(a.pages, a.page, a.max_pages)) return DS_EINVAL;
+    if (a.d > 1024 || !pool_fits(a.pages, a.page) || (int64_t)a.b * a.n > INT32_MAX) return DS_EUNSUPPORTED;
+    if ((int64_t)a.b * a.n == 0) return DS_OK;
+    if (!a.y || !aligned16(a.y) || !aligned4(a.idx) || !aligned4(a.first) || !aligned4(a.lens)) return DS_EINVAL;
+    if (!store_there(a.codes, a.exps, a.pages, a.block_table, a.max_pages) || !aligned16(a.codes) || !aligned4(a.block_table))
+        return DS_EINVAL;
+    a.status = status_word();
+    if (!a.status) return DS_ECUDA;
+    return launch(a, reinterpret_cast<cudaStream_t>(stream));
+}
 }  // namespace
 
 int ds_norm_rotary(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint16_t *y, int b, int s, int h, int d,
@@ -379,21 +409,67 @@ int ds_kv_append_fp4_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstri
                            uint8_t *codes, int8_t *exps, int64_t pages, int page, const int32_t *block_table,
                            int max_pages, ds_stream_t stream) {
     const Range range("ds_kv_append_fp4_paged");
-    if (b < 0 || s < 0 || d < 32 || d % 32 != 0 || pos_step < 1 || base < 0 || window < 0) return DS_EINVAL;
-    if (eps != 0.0f && !(eps >= 0x1p-100f)) return DS_EINVAL;
-    if (!rotation_ok(rd, d, table, table_rows) || !pool_ok(pages, page, max_pages)) return DS_EINVAL;
-    if (d > 1024 || !pool_fits(pages, page) || (int64_t)b * s > INT32_MAX) return DS_EUNSUPPORTED;
-    if ((int64_t)b * s == 0) return DS_OK;
-    if (!x || !first || !aligned16(x) || !aligned16(y) || !aligned16(weight) || !aligned4(first) || !aligned4(lens))
+    return kv_append({x, x_bstride, x_tstride, y, b, s, d, weight, eps, rd, table, table_rows, first, lens, pos_step, base,
+                      window, codes, exps, pages, page, block_table, max_pages, nullptr},
+                     launch_kv_append_fp4, stream);
+}
+
+int ds_kv_append_fp8_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, uint16_t *y, int b, int s, int d,
+                           const float *weight, float eps, int rd, const float *table, int64_t table_rows,
+                           const int32_t *first, const int32_t *lens, int pos_step, int base, int window,
+                           uint8_t *codes, int8_t *exps, int64_t pages, int page, const int32_t *block_table,
+                           int max_pages, ds_stream_t stream) {
+    const Range range("ds_kv_append_fp8_paged");
+    return kv_append({x, x_bstride, x_tstride, y, b, s, d, weight, eps, rd, table, table_rows, first, lens, pos_step, base,
+                      window, codes, exps, pages, page, block_table, max_pages, nullptr},
+                     launch_kv_append_fp8, stream);
+}
+
+int ds_kv_read_fp8_paged(const uint8_t *codes, const int8_t *exps, int64_t pages, int page, const int32_t *block_table,
+                         int max_pages, const int32_t *idx, const int32_t *first, const int32_t *lens, uint16_t *y,
+                         int b, int n, int d, ds_stream_t stream) {
+    const Range range("ds_kv_read_fp8_paged");
+    return kv_read({codes, exps, pages, page, block_table, max_pages, idx, first, lens, y, b, n, d, nullptr}, launch_kv_read_fp8,
+                   stream);
+}
+
+int ds_kv_read_fp4_paged(const uint8_t *codes, const int8_t *exps, int64_t pages, int page, const int32_t *block_table,
+                         int max_pages, const int32_t *idx, const int32_t *first, const int32_t *lens, uint16_t *y,
+                         int b, int n, int d, ds_stream_t stream) {
+    const Range range("ds_kv_read_fp4_paged");
+    return kv_read({codes, exps, pages, page, block_table, max_pages, idx, first, lens, y, b, n, d, nullptr}, launch_kv_read_fp4,
+                   stream);
+}
+
+size_t ds_chunk_attn_fp8_paged_workspace_bytes(int b, int m, int h, int d, int window, int ratio, int page, int max_pages) {
+    if (b < 0 || m < 0 || h < 1 || h > 128 || d != 512 || window < 0 || ratio < 0 || page < 1 || max_pages < 0) return 0;
+    if ((int64_t)b * m > INT32_MAX / h) return 0;
+    return chunk_attn_fp8_workspace_bytes(b, m, h, window, ratio, page, max_pages);
+}
+
+int ds_chunk_attn_fp8_paged(const uint16_t *q, const uint8_t *codes, const int8_t *exps, int64_t pages, int page,
+                            const int32_t *block_table, int max_pages, const float *sink, float scale, uint16_t *o,
+                            int b, int m, int h, int d, const int32_t *first, const int32_t *lens, int window, int ring,
+                            int ratio, int base, void *workspace, size_t workspace_bytes, int rd, const float *table,
+                            int64_t table_rows, ds_stream_t stream) {
+    const Range range("ds_chunk_attn_fp8_paged");
+    if (b < 0 || m < 0 || h < 1 || !pool_ok(pages, page, max_pages) || window < 0 || ring < 0 || ratio < 0 || base < 0)
         return DS_EINVAL;
-    if (!store_there(codes, exps, pages, block_table, max_pages) || !aligned16(codes) || !aligned4(block_table))
-        return DS_EINVAL;
-    if (!strides_ok(x_bstride, x_tstride, b, s, d)) return DS_EINVAL;
-    unsigned int *status = status_word();
-    if (!status) return DS_ECUDA;
-    return launch_kv_append_fp4(x, x_bstride, x_tstride, y, b, s, d, weight, eps, rd, table, table_rows, first, lens,
-                                pos_step, base, window, codes, exps, pages, page, block_table, max_pages, status,
-                                reinterpret_cast<cudaStream_t>(stream));
+    if (!rotation_ok(rd, d, table, table_rows)) return DS_EINVAL;
+    if (ring > 0 && (window == 0 || ring < window || ring > (int64_t)max_pages * page)) return DS_EINVAL;
+    if (ring > 0 && !lens && ring < (int64_t)window + m - 1) return DS_EINVAL;
+    if (ring > 0 && ratio > 0 && base < ring) return DS_EINVAL;
+    if (d != 512 || h > 128 || !pool_fits(pages, page) || (int64_t)b * m > INT32_MAX / h) return DS_EUNSUPPORTED;
+    if ((int64_t)b * m == 0) return DS_OK;
+    if (!q || !o || !sink || !first || !store_there(codes, exps, pages, block_table, max_pages)) return DS_EINVAL;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(codes) || !aligned16(exps)) return DS_EINVAL;
+    if (!aligned4(sink) || !aligned4(block_table) || !aligned4(first) || !aligned4(lens)) return DS_EINVAL;
+    if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return DS_EWORKSPACE;
+    const chunk::Args a{q, codes, exps, pages, page, block_table, max_pages, sink, scale, o, b, m, h, first, lens, window,
+                        ring, ratio, base, workspace, workspace_bytes, rd, reinterpret_cast<const float2 *>(table),
+                        table_rows, status_word()};
+    if (!a.status) return DS_ECUDA;
+    return launch_chunk_attn_fp8(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t ds_sparse_attn_fp4_paged_workspace_bytes(int b, int m, int h, int d, int topk) {

@@ -81,6 +81,17 @@ _lib.ds_norm_rotary.restype = _i32
 _lib.ds_kv_append_fp4_paged.argtypes = [_P, _i64, _i64, _P, _i32, _i32, _i32, _P, _f32, _i32, _P, _i64, _P, _P, _i32,
                                         _i32, _i32, _P, _P, _i64, _i32, _P, _i32, _P]
 _lib.ds_kv_append_fp4_paged.restype = _i32
+_lib.ds_kv_append_fp8_paged.argtypes = _lib.ds_kv_append_fp4_paged.argtypes
+_lib.ds_kv_append_fp8_paged.restype = _i32
+_lib.ds_kv_read_fp8_paged.argtypes = [_P, _P, _i64, _i32, _P, _i32, _P, _P, _P, _P, _i32, _i32, _i32, _P]
+_lib.ds_kv_read_fp8_paged.restype = _i32
+_lib.ds_kv_read_fp4_paged.argtypes = _lib.ds_kv_read_fp8_paged.argtypes
+_lib.ds_kv_read_fp4_paged.restype = _i32
+_lib.ds_chunk_attn_fp8_paged_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32]
+_lib.ds_chunk_attn_fp8_paged_workspace_bytes.restype = _sz
+_lib.ds_chunk_attn_fp8_paged.argtypes = [_P, _P, _P, _i64, _i32, _P, _i32, _P, _f32, _P, _i32, _i32, _i32, _i32, _P, _P,
+                                         _i32, _i32, _i32, _i32, _P, _sz, _i32, _P, _i64, _P]
+_lib.ds_chunk_attn_fp8_paged.restype = _i32
 _lib.ds_sparse_attn_fp4_paged_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32]
 _lib.ds_sparse_attn_fp4_paged_workspace_bytes.restype = _sz
 _lib.ds_sparse_attn_fp4_paged.argtypes = [_P, _P, _P, _i64, _i32, _P, _i32, _P, _P, _i32, _f32, _P, _i32, _i32, _i32,
@@ -393,7 +404,7 @@ def sparse_attn_fp8kv(q: torch.Tensor, kv_codes: torch.Tensor, kv_exps: torch.Te
     return o
 
 
-# ---- the paged 4-bit row store: calls of a few microseconds, so their checks are single comparisons on the
+# ---- the paged row stores: calls of a few microseconds, so their checks are single comparisons on the
 # ---- way in, and only a refused call goes back over them to say what is wrong
 
 _BF16, _F32, _I32, _U8, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.int8
@@ -483,40 +494,170 @@ def kv_append_fp4_paged(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor
     row store ``codes [pages][page][d/2]``, ``exps [pages][page][d/32]``: row ``i = first[b] + t`` goes to
     logical row ``base + i % window`` (``window`` > 0, the last ``window`` tokens) or ``base + i``, rotated
     to position ``i * pos_step``.  ``y``: bf16 [b][s][d] contiguous, receives the stored values."""
+    _kv_append("ds_kv_append_fp4_paged", _lib.ds_kv_append_fp4_paged, 4, x, codes, exps, block_table, first, rd, table, eps,
+               weight, lens, pos_step, base, window, y, stream)
+
+
+def kv_append_fp8_paged(x: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor, block_table: torch.Tensor,
+                        first: torch.Tensor, rd: int = 0, table: torch.Tensor | None = None, eps: float = 0.0,
+                        weight: torch.Tensor | None = None, lens: torch.Tensor | None = None, pos_step: int = 1,
+                        base: int = 0, window: int = 0, y: torch.Tensor | None = None, stream=None) -> None:
+    """``kv_append_fp4_paged`` into the paged 8-bit row store: ``codes [pages][page][d]`` of e4m3 codes."""
+    _kv_append("ds_kv_append_fp8_paged", _lib.ds_kv_append_fp8_paged, 8, x, codes, exps, block_table, first, rd, table, eps,
+               weight, lens, pos_step, base, window, y, stream)
+
+
+_ROW = {4: "d/2", 8: "d"}     # bytes of a row's codes
+
+
+def _kv_append(name, call, bits, x, codes, exps, block_table, first, rd, table, eps, weight, lens, pos_step, base, window, y,
+               stream):
     if x.dim() != 3 or codes.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("x must be [b][s][d], codes [pages][page][d/2] and block_table [b][max_pages]")
+        raise ValueError(f"x must be [b][s][d], codes [pages][page][{_ROW[bits]}] and block_table [b][max_pages]")
     b, s, d = x.shape
     xb, xt, xd = x.stride()
-    pages, page, half = codes.shape
+    pages, page, row = codes.shape
     tables, max_pages = block_table.shape
     dev = x.get_device()
     tab = _table_shape(rd, table) if rd else None
     if not (x.dtype is _BF16 and dev >= 0 and dev == _device()
-            and codes.dtype is _U8 and half == d // 2 and codes.is_contiguous() and codes.get_device() == dev
+            and codes.dtype is _U8 and row == d * bits // 8 and codes.is_contiguous() and codes.get_device() == dev
             and _fits(exps, _I8, (pages, page, d // 32), dev) and block_table.dtype is _I32 and tables == b
             and block_table.is_contiguous() and block_table.get_device() == dev and _row_fits(first, _I32, b, dev)
             and (lens is None or _row_fits(lens, _I32, b, dev)) and (weight is None or _row_fits(weight, _F32, d, dev))
             and (rd == 0 or (table is not None and _fits(table, _F32, tab, dev)))
             and (y is None or _fits(y, _BF16, (b, s, d), dev))):
         given = {"lens": (lens, _I32, (b,)), "weight": (weight, _F32, (d,)), "y": (y, _BF16, x.shape)}
-        _refuse(x=(x, _BF16, None), codes=(codes, _U8, (pages, page, d // 2)), exps=(exps, _I8, (pages, page, d // 32)),
+        _refuse(x=(x, _BF16, None), codes=(codes, _U8, (pages, page, d * bits // 8)), exps=(exps, _I8, (pages, page, d // 32)),
                 block_table=(block_table, _I32, (b, max_pages)), first=(first, _I32, (b,)),
                 **{k: v for k, v in given.items() if v[0] is not None}, **({"table": (table, _F32, tab)} if rd else {}))
     if x.numel() and xd != 1:
         raise ValueError("the values of a row must be contiguous")
     if (b * s | page | max_pages | pos_step | base | window | rd) >> 31:
-        _refuse_wide("ds_kv_append_fp4_paged", b * s, page, max_pages, pos_step, base, window, rd)
+        _refuse_wide(name, b * s, page, max_pages, pos_step, base, window, rd)
     if 0.0 < eps < 2.0 ** -100:            # as a float it could be 0, which is no norm
-        raise DsError("ds_kv_append_fp4_paged", DS_EINVAL)
-    st = _lib.ds_kv_append_fp4_paged(x.data_ptr(), xb if b > 1 else 0, xt if s > 1 else 0,
-                                     None if y is None else y.data_ptr(), b, s, d,
-                                     None if weight is None else weight.data_ptr(), eps, rd,
-                                     table.data_ptr() if rd else None, tab[0] if rd else 0, first.data_ptr(),
-                                     None if lens is None else lens.data_ptr(), pos_step, base, window,
-                                     codes.data_ptr(), exps.data_ptr(), pages, page, block_table.data_ptr(), max_pages,
-                                     _raw_stream(dev) if stream is None else stream.cuda_stream)
+        raise DsError(name, DS_EINVAL)
+    st = call(x.data_ptr(), xb if b > 1 else 0, xt if s > 1 else 0, None if y is None else y.data_ptr(), b, s, d,
+              None if weight is None else weight.data_ptr(), eps, rd, table.data_ptr() if rd else None, tab[0] if rd else 0,
+              first.data_ptr(), None if lens is None else lens.data_ptr(), pos_step, base, window, codes.data_ptr(),
+              exps.data_ptr(), pages, page, block_table.data_ptr(), max_pages,
+              _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
-        _check("ds_kv_append_fp4_paged", st)
+        _check(name, st)
+
+
+def kv_read_fp8_paged(codes: torch.Tensor, exps: torch.Tensor, block_table: torch.Tensor, n: int,
+                      first: torch.Tensor | None = None, idx: torch.Tensor | None = None,
+                      lens: torch.Tensor | None = None, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``n`` rows of every sequence of the paged 8-bit row store as bf16 ``y [b][n][d]``: logical rows
+    ``idx [b][n]`` (entries < 0: zeros), or rows ``first[b] + i`` (``first`` missing: from row 0).  Rows at or behind
+    ``lens[b]`` leave ``y`` as it was (zeros in a new one)."""
+    return _kv_read("ds_kv_read_fp8_paged", _lib.ds_kv_read_fp8_paged, 8, codes, exps, block_table, n, first, idx, lens, y,
+                    stream)
+
+
+def kv_read_fp4_paged(codes: torch.Tensor, exps: torch.Tensor, block_table: torch.Tensor, n: int,
+                      first: torch.Tensor | None = None, idx: torch.Tensor | None = None,
+                      lens: torch.Tensor | None = None, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``kv_read_fp8_paged`` of the paged 4-bit row store (``codes [pages][page][d/2]``)."""
+    return _kv_read("ds_kv_read_fp4_paged", _lib.ds_kv_read_fp4_paged, 4, codes, exps, block_table, n, first, idx, lens, y,
+                    stream)
+
+
+def _kv_read(name, call, bits, codes, exps, block_table, n, first, idx, lens, y, stream):
+    if codes.dim() != 3 or block_table.dim() != 2:
+        raise ValueError(f"codes must be [pages][page][{_ROW[bits]}] and block_table [b][max_pages]")
+    pages, page, row = codes.shape
+    d = row * 8 // bits
+    b, max_pages = block_table.shape
+    dev = codes.get_device()
+    if not (codes.dtype is _U8 and codes.is_contiguous() and dev >= 0 and dev == _device()
+            and _fits(exps, _I8, (pages, page, d // 32), dev) and _fits(block_table, _I32, (b, max_pages), dev)
+            and (first is None or _row_fits(first, _I32, b, dev)) and (idx is None or _fits(idx, _I32, (b, n), dev))
+            and (lens is None or _row_fits(lens, _I32, b, dev)) and (y is None or _fits(y, _BF16, (b, n, d), dev))):
+        given = {"first": (first, _I32, (b,)), "idx": (idx, _I32, (b, n)), "lens": (lens, _I32, (b,)), "y": (y, _BF16, (b, n, d))}
+        _refuse(codes=(codes, _U8, codes.shape), exps=(exps, _I8, (pages, page, d // 32)),
+                block_table=(block_table, _I32, (b, max_pages)), **{k: v for k, v in given.items() if v[0] is not None})
+    if idx is not None and first is not None:
+        raise ValueError("rows are listed by idx or follow first, not both")
+    if n < 0 or (b * n | page | max_pages) >> 31:
+        _refuse_wide(name, b * n, page, max_pages)
+        raise DsError(name, DS_EINVAL)
+    if y is None:
+        with _on(stream):
+            y = (torch.empty if lens is None else torch.zeros)((b, n, d), dtype=_BF16, device=codes.device)
+    st = call(codes.data_ptr(), exps.data_ptr(), pages, page, block_table.data_ptr(), max_pages,
+              None if idx is None else idx.data_ptr(), None if first is None else first.data_ptr(),
+              None if lens is None else lens.data_ptr(), y.data_ptr(), b, n, d,
+              _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check(name, st)
+    return y
+
+
+def chunk_attn_fp8_paged_workspace_bytes(b: int, m: int, h: int, d: int, window: int, ratio: int, page: int,
+                                         max_pages: int) -> int:
+    return int(_lib.ds_chunk_attn_fp8_paged_workspace_bytes(b, m, h, d, window, ratio, page, max_pages))
+
+
+@functools.lru_cache(maxsize=64)
+def _chunk_workspace_bytes(dev: int, *args: int) -> int:
+    return chunk_attn_fp8_paged_workspace_bytes(*args)
+
+
+def chunk_attn_fp8_paged(q: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor, block_table: torch.Tensor,
+                         first: torch.Tensor, sink: torch.Tensor, scale: float, window: int, ring: int = 0, ratio: int = 0,
+                         base: int = 0, lens: torch.Tensor | None = None, rd: int = 0, table: torch.Tensor | None = None,
+                         o: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of a chunk of new tokens ``q [b][m][h][512]`` over the paged 8-bit row store.  Token t of a sequence is at
+    position ``p = first[b] + t`` and sees the rows of its last ``window`` positions (0: all; position i is logical row
+    ``i % ring``, or i without a ring) and compressed rows 0 .. (p + 1) // ratio - 1 (``ratio`` 0: none), logical
+    rows ``base + j``; with ``rd`` > 0 the last ``rd`` values of its output are rotated back.  Tokens at or behind
+    ``lens[b]`` leave ``o`` as it was (zeros in a new one)."""
+    if q.dim() != 4 or codes.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [b][m][h][d], codes [pages][page][d] and block_table [b][max_pages]")
+    b, m, h, d = q.shape
+    pages, page, row = codes.shape
+    tables, max_pages = block_table.shape
+    dev = q.get_device()
+    tab = _table_shape(rd, table) if rd else None
+    if not (q.dtype is _BF16 and q.is_contiguous() and dev >= 0 and dev == _device()
+            and codes.dtype is _U8 and row == d and codes.is_contiguous() and codes.get_device() == dev
+            and _fits(exps, _I8, (pages, page, d // 32), dev) and block_table.dtype is _I32 and tables == b
+            and block_table.is_contiguous() and block_table.get_device() == dev and _row_fits(sink, _F32, h, dev)
+            and _row_fits(first, _I32, b, dev) and (lens is None or _row_fits(lens, _I32, b, dev))
+            and (o is None or _fits(o, _BF16, (b, m, h, d), dev))
+            and (rd == 0 or (table is not None and _fits(table, _F32, tab, dev)))
+            and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))):
+        given = {"lens": (lens, _I32, (b,)), "o": (o, _BF16, q.shape),
+                 "workspace": (workspace, None if workspace is None else workspace.dtype, None if workspace is None else workspace.shape)}
+        _refuse(q=(q, _BF16, q.shape), codes=(codes, _U8, (pages, page, d)), exps=(exps, _I8, (pages, page, d // 32)),
+                block_table=(block_table, _I32, (b, max_pages)), first=(first, _I32, (b,)), sink=(sink, _F32, (h,)),
+                **{k: v for k, v in given.items() if v[0] is not None}, **({"table": (table, _F32, tab)} if rd else {}))
+    if (b * m * h | page | max_pages | window | ring | ratio | base | rd) >> 31:
+        _refuse_wide("ds_chunk_attn_fp8_paged", b * m * h, page, max_pages, window, ring, ratio, base, rd)
+    if o is None:
+        with _on(stream):
+            o = torch.empty_like(q) if lens is None else torch.zeros_like(q)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        need = _chunk_workspace_bytes(dev, b, m, h, d, window, ratio, page, max_pages)
+        if need:
+            with _on(stream):
+                workspace = torch.empty(need, dtype=_U8, device=q.device)
+            ws, ws_bytes = workspace.data_ptr(), need
+    st = _lib.ds_chunk_attn_fp8_paged(q.data_ptr(), codes.data_ptr(), exps.data_ptr(), pages, page, block_table.data_ptr(),
+                                      max_pages, sink.data_ptr(), scale, o.data_ptr(), b, m, h, d, first.data_ptr(),
+                                      None if lens is None else lens.data_ptr(), window, ring, ratio, base, ws, ws_bytes,
+                                      rd, table.data_ptr() if rd else None, tab[0] if rd else 0,
+                                      _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        # the size kept for this shape may be the 0 of a query that failed: the next call asks anew
+        _chunk_workspace_bytes.cache_clear()
+        _check("ds_chunk_attn_fp8_paged", st)
+    return o
 
 
 def sparse_attn_fp4_paged_workspace_bytes(b: int, m: int, h: int, d: int, topk: int) -> int:

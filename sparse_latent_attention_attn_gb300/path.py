@@ -15,6 +15,10 @@ A decode step over the paged 4-bit row store has every sequence at a position of
 row is normalised, rotated and stored as codes in its ring slot, the queries are normalised and rotated,
 and sparse_attn runs over the listed rows of the store with its output rotated back.
 
+A step over the paged 8-bit row store takes a chunk of one or many new tokens of every sequence, a prompt's next piece as
+well as a decode step, in a layer where a query sees its window and every complete compressed row (while there are
+no more of those than the Indexer would keep, or in a layer without them): no index rows are made.
+
 The caller lays kv out as [window rows | compressed rows] per sequence and idx as
 [window cols | compressed cols], so no concatenation copy is made.
 """
@@ -75,3 +79,29 @@ def decode_step_fp4_paged(q: torch.Tensor, new_kv: torch.Tensor, codes: torch.Te
     qn = dsattn.norm_rotary(q, eps, rd, table, first, lens=lens, y=qn, stream=stream)
     return dsattn.sparse_attn_fp4_paged(qn, codes, exps, block_table, sink, idx, scale, rd=rd, table=table,
                                         first=first, o=o, workspace=workspace, stream=stream, lens=lens)
+
+
+def chunk_step_fp8_paged(q: torch.Tensor, new_kv: torch.Tensor, codes: torch.Tensor, exps: torch.Tensor,
+                         block_table: torch.Tensor, first: torch.Tensor, sink: torch.Tensor, window: int, ring: int,
+                         scale: float, rd: int, table: torch.Tensor, eps: float, kv_weight: torch.Tensor | None = None,
+                         lens: torch.Tensor | None = None, ratio: int = 0, base: int = 0,
+                         o: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q [b][s][h][d] and new_kv [b][s][d] as their projections leave them (neither is modified); the token (bi, t) is at
+    position first[bi] + t.  Its row is normalised, rotated and stored as e4m3 codes (in slot position % ring of the
+    ring, or at its position for ring = 0), and its queries see the last `window` positions (0: all) and, with
+    ratio > 0, the compressed rows of every complete group of `ratio` positions, which are in the store from logical row
+    `base` on (kv_append_fp8_paged with pos_step = ratio and that base).  Tokens at or behind lens[bi] are
+    padding: nothing of theirs is stored, and o is left as it was (zeros in a new one).  The ring must hold
+    window + s - 1 rows (with lens: window + the largest of them - 1)."""
+    s = q.shape[1]
+    if lens is None and 0 < ring < window + s - 1:
+        raise ValueError(f"a ring of {ring} slots does not hold a window of {window} and the step's {s} tokens")
+    dsattn.kv_append_fp8_paged(new_kv, codes, exps, block_table, first, rd=rd, table=table, eps=eps, weight=kv_weight,
+                               lens=lens, window=ring, stream=stream)
+    qn = None
+    if lens is not None:                   # the padding of q is not read: no zeros for it
+        with dsattn._on(stream):
+            qn = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    qn = dsattn.norm_rotary(q, eps, rd, table, first, lens=lens, y=qn, stream=stream)
+    return dsattn.chunk_attn_fp8_paged(qn, codes, exps, block_table, first, sink, scale, window, ring=ring, ratio=ratio,
+                                       base=base, lens=lens, rd=rd, table=table, o=o, workspace=workspace, stream=stream)
