@@ -500,6 +500,7 @@ int ds_sparse_attn_fp4_paged_ragged(const uint16_t *q, const uint8_t *codes, con
 void ds_test_set_stall(int on) {
     set_test_stall(on != 0);
     set_test_stall_fp4(on != 0);
+    set_test_stall_chunk(on != 0);
 }
 
 int ds_sparse_attn_launches(int b, int m, int h, int d, int topk, int *kernel, size_t *workspace_bytes) {

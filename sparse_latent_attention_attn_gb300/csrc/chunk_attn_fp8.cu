@@ -3,111 +3,1193 @@
 // For the query (token t of sequence bi, head hh) at position p = first[bi] + t, over the rows that it sees (positions
 // max(0, p - window + 1) .. p, and compressed rows 0 .. (p + 1) / ratio - 1):
 //     s_j = scale q . k_j,  o = sum_j exp(s_j) k_j / (sum_j exp(s_j) + exp(sink[hh])),
-// then the inverse rotation of the last rd values.  One warp a query, its 512 values of q and o in registers, the softmax's
-// running maximum and sum; f32 throughout.
+// then the inverse rotation of the last rd values ("DeepSeek V4.1", attention/attend and attention/query-latent).
+//
+// Queries of neighbouring tokens see nearly the same rows, so a unit of work is up to 128 query rows (a sequence's
+// tokens and heads in one line: any number of heads fills it) against the union of the rows that they see, window rows
+// first and compressed rows behind them, in tiles of 128; each query's own range is a mask.  With rows of 512 values an
+// accumulator of 128 queries in f32 fills the tensor memory of an SM, which leaves no room for scores.  So two SMs share
+// a unit (a cluster of two CTAs, cta_group::2), each with 64 of its queries and with one half of d:
+//   * S = Q K^T: M = 128 queries (64 a CTA), N = 128 rows (each CTA widens 64 of them), K = 512.  A CTA's scores lie on
+//     all 128 lanes: query r on lane r with rows 0-63 of the tile, and on lane r + 64 with rows 64-127.
+//   * O^T += V^T P^T: M = 256 values of d (128 a CTA, twice), N = 128 queries (each CTA's P), K = 128 rows.  Each CTA widens
+//     all 128 rows for its own half of d; O^T takes 256 columns of tensor memory, and two tiles of scores 128.
+// No scores and no probabilities cross between the CTAs: the tensor cores read both CTAs' operands.  The MMAs of a tile take
+// 0.75 + 0.53 us (23.3 ns for each of 32, 32.9 ns for each of 16, measured), 0.85 of the tensor cores' rate.
+//
+// The codes are widened to bf16 in registers (exact: at most four significant bits; a code's bits moved to a bf16's,
+// times 2^(120 + k)) on their way into the operands, once for S and once for P V, which spares a copy in HBM: 33/32 byte a
+// value is all that is read.  An operand half is handed back as soon as its MMAs are done, while the next tile's codes
+// wait in registers.
+//
+// The softmax works on a reference per query: the first tile's maximum, moved (by whole octaves, so that O^T and the sum are
+// scaled exactly) only when a later one exceeds it by more than kSlack octaves.  It is never more than 64 octaves below the
+// sink, so that 1 / (sum + sink) is a normal number wherever an output is.  P is rounded to bf16 for the product, as in
+// ds_sparse_attn; the sum takes it unrounded.
+//
+// Warps: 0-3 softmax, 4-7 output (and O^T's rescaling, on request), 8-11 widen K, 12-15 widen V, 16 issues the MMAs (in the
+// cluster's first CTA, for both), 17 fetches q by TMA.  Every wait gives up after 2 s (DS_DEV_TIMEOUT).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
 #include "chunk_attn_fp8.cuh"
+#include "f32x2.cuh"
+#include "ptx.cuh"
 #include "row_norm.cuh"
 
 namespace dsattn {
 namespace chunk {
 
+using namespace ptx;
 using rows::Divisor;
 
 constexpr int D = 512;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int BN = 128;                     // rows of a tile
+constexpr int HR = 64;                      // of them widened for S by each CTA; also query rows of a CTA, at most
+constexpr int NTHREADS = 576;               // 18 warps
+constexpr int W_OUT = 4, W_K = 8, W_V = 12, W_MMA = 16, W_Q = 17;
 
-__global__ void __launch_bounds__(256) chunk_attn_plain_kernel(const Args a, const Divisor page, int64_t nrows) {
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= nrows) return;
-    const int hh = (int)(row % a.h);
-    const int t = (int)(row / a.h % a.m), bi = (int)(row / a.h / a.m);
-    if (a.lens && t >= a.lens[bi]) return;
-    const int64_t p = (int64_t)a.first[bi] + t;
-    float q[16], o[16];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t w = reinterpret_cast<const uint32_t *>(a.q + row * D)[lane * 8 + j];
-        q[2 * j] = bf16_lo(w);
-        q[2 * j + 1] = bf16_hi(w);
+constexpr int K_CHUNK = HR * 128;           // 64 rows of 64 values
+constexpr int V_CHUNK = BN * 128;           // 128 rows of 64 values
+constexpr int SM_Q = 0;                     // 8 chunks of 64 query rows
+constexpr int SM_K = SM_Q + 8 * K_CHUNK;    // 8 chunks
+constexpr int SM_V = SM_K + 8 * K_CHUNK;    // 4 chunks (this CTA's half of d)
+constexpr int P_BYTES = 2 * K_CHUNK;        // 64 query rows of 128 probabilities
+constexpr int SM_P = SM_V + 4 * V_CHUNK;    // two buffers
+constexpr int SM_CTL = SM_P + 2 * P_BYTES;
+constexpr int SMEM_BYTES = SM_CTL + 3072;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+
+constexpr int TM_O = 0, TM_S = 256, TM_COLS = 512;
+
+// barriers (8 bytes each); "first": used in the cluster's first CTA only
+enum : int {
+    B_KFULL = 0,              // [2] half of K's chunks widened in both CTAs (first)
+    B_KFREE = B_KFULL + 2,    // [2] its MMAs are done
+    B_VFULL = B_KFREE + 2,    // [2] half of V's chunks widened in both CTAs (first)
+    B_VFREE = B_VFULL + 2,    // [2]
+    B_S = B_VFREE + 2,        // [2] scores of tile J there (J & 1)
+    B_P = B_S + 2,            // [2] P of tile J written in both CTAs (first)
+    B_QLOC = B_P + 2,         // q of a unit landed in this CTA
+    B_Q = B_QLOC + 1,         // ... in both (first)
+    B_QFREE = B_Q + 1,        // the unit's last S is done
+    B_O = B_QFREE + 1,        // the unit's last P V is done
+    B_OFREE = B_O + 1,        // O^T read in both CTAs (first)
+    B_INV = B_OFREE + 1,      // [2] the unit's factors (unit & 1) are there
+    B_RESC = B_INV + 2,       // O^T is to be rescaled
+    B_RESCD = B_RESC + 1,     // ... and is, in both CTAs (first)
+    B_SYNC = B_RESCD + 1,     // P V so far is done (first)
+    B_DRAIN = B_SYNC + 1,
+    B_COUNT = B_DRAIN + 1
+};
+constexpr int C_TMEM = 8 * B_COUNT, C_ABORT = C_TMEM + 4, C_RESC = C_ABORT + 4;   // [2] int: tile + 1 that needs a rescale
+constexpr int C_CNT = C_RESC + 8;                                                 // [4] int: tiles of the units under way
+constexpr int C_PAR = C_CNT + 16;                                                 // int: J & 1 of the rescale under way
+static_assert(C_PAR + 4 <= 256, "control block");
+constexpr int C_ALPHA = 256;                // [2][128] int16: octaves by which a query's column of O^T is to be lowered
+constexpr int C_INV = C_ALPHA + 512;        // [2][128] f32: 1 / denominator
+constexpr int C_XCH = C_INV + 1024;         // [2][2][64] f32: maxima and sums, between the two threads of a query
+static_assert(SM_CTL + C_XCH + 1024 <= SMEM_BYTES, "control block");
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kUnitLimitNs = 30 * kWaitLimitNs;   // of waits that last as long as a unit
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 20.0f;             // octaves above the reference up to which P may go
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct Params {
+    Args a;
+    Divisor h, page, ring, b, parts;
+    int R;               // query rows of a CTA: 64, 32 or 16
+    int nqt;             // query tiles of a sequence
+    uint32_t units;
+    int64_t cap;         // logical rows that the block table can hold, at most 2^31
+    float scale_log2;
+    float *ws;
+    int stall;
+};
+
+// A unit's rows: tile t holds rows [128 t, 128 t + 128) of the list of nw window rows (positions wlo ..) and nc compressed
+// rows; this unit takes tiles [t0, t1).
+struct Unit {
+    int bi, part;
+    int r0, rows;        // query rows [r0, min(r0 + 2 R, rows)) of the sequence
+    int64_t first;
+    int64_t wlo;
+    uint32_t nw, nc;
+    int t0, t1;
+    bool clipped;        // rows beyond the block table
+};
+
+__device__ __forceinline__ int2 fetch_unit(const Params &p, uint32_t u) {
+    if (u >= p.units) return make_int2(0, 0);
+    uint32_t part, bi;
+    p.b.div(p.parts.div(u, part), bi);
+    return make_int2(__ldg(p.a.first + bi), p.a.lens ? __ldg(p.a.lens + bi) : p.a.m);
+}
+
+// raw: fetch_unit(u).  Later tokens see more, so a sequence's last query tiles come first.
+__device__ __forceinline__ void make_unit(const Params &p, uint32_t u, int2 raw, Unit &x) {
+    uint32_t part, bi;
+    const int qt = p.nqt - 1 - (int)p.b.div(p.parts.div(u, part), bi);
+    x.bi = (int)bi;
+    x.part = (int)part;
+    x.first = raw.x;
+    x.rows = max(0, min(raw.y, p.a.m)) * p.a.h;
+    x.r0 = qt * 2 * p.R;
+    x.nw = x.nc = 0;
+    x.wlo = 0;
+    x.t0 = x.t1 = 0;
+    x.clipped = false;
+    if (x.r0 >= x.rows) return;
+    uint32_t rest;
+    const int64_t lo = x.first + p.h.div((uint32_t)x.r0, rest);
+    const int64_t hi = x.first + p.h.div((uint32_t)min(x.r0 + 2 * p.R, x.rows) - 1, rest);
+    if (hi < 0) return;
+    if (p.a.window) x.wlo = max((int64_t)0, lo - p.a.window + 1);
+    int64_t end = hi + 1;
+    if (!p.a.ring && end > p.cap) {
+        end = p.cap;
+        x.clipped = true;
     }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) o[j] = 0.0f;
-    bool bad = p < 0;
-    const int64_t wlo = a.window ? max((int64_t)0, p - a.window + 1) : 0, nw = max((int64_t)0, p + 1 - wlo);
-    const int64_t nc = a.ratio && p >= 0 ? (p + 1) / a.ratio : 0;
-    const int64_t cap = (int64_t)a.max_pages * a.page;
-    // the reference of the exponentials is never more than 64 octaves below the sink: 1 / l stays a normal number, and what
-    // it multiplies is lost only where the output itself is below f32's range
-    const float sink2 = fminf(a.sink[hh] * kLog2e, 1e37f);
-    float top = sink2 - 64.0f, l = 0.0f;
-    for (int64_t v = 0; v < nw + nc; ++v) {
-        const int64_t r = v < nw ? (a.ring ? (wlo + v) % a.ring : wlo + v) : a.base + (v - nw);
-        if (r >= cap) {
-            bad = true;
-            if (v < nw && a.ring) continue;
-            if (v >= nw) break;
-            v = nw - 1;
-            continue;
+    x.nw = (uint32_t)max((int64_t)0, end - x.wlo);
+    if (p.a.ratio) {
+        int64_t nc = (hi + 1) / p.a.ratio;
+        if (nc > p.cap - p.a.base) {
+            nc = max((int64_t)0, p.cap - p.a.base);
+            x.clipped = true;
         }
-        const int id = a.block_table[(int64_t)bi * a.max_pages + r / a.page];
-        if (id < 0 || id >= a.pages) {
-            bad = true;
-            continue;
-        }
-        const int64_t slot = (int64_t)id * a.page + r % a.page;
-        const uint4 c = reinterpret_cast<const uint4 *>(a.codes + slot * D)[lane];
-        const float sc = exp2f((float)a.exps[slot * (D / 32) + lane / 2]);
-        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-        float k[16], s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint32_t f;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"((uint16_t)(cw[j / 2] >> (16 * (j % 2)))));
-            k[2 * j] = __half2float(__ushort_as_half((unsigned short)(f & 0xffffu))) * sc;
-            k[2 * j + 1] = __half2float(__ushort_as_half((unsigned short)(f >> 16))) * sc;
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) s = fmaf(q[j], k[j], s);
-        s = rows::row_sum<32>(s) * a.scale * kLog2e;
-        const float next = fmaxf(top, s), f = exp2f(top - next), e = exp2f(s - next);
-        top = next;
-        l = l * f + e;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[j] = fmaf(e, k[j], o[j] * f);
+        x.nc = (uint32_t)nc;
     }
-    const float inv = l > 0.0f ? 1.0f / (l + exp2f(sink2 - top)) : 0.0f;
+    const int64_t nt = ((int64_t)x.nw + x.nc + BN - 1) / BN;
+    x.t0 = (int)(nt * x.part / (int)p.parts.d);
+    x.t1 = (int)(nt * (x.part + 1) / (int)p.parts.d);
+}
+
+// Block table entry of the list's row v, and the row's place in its page (kNoRow behind the list's end).
+constexpr uint32_t kNoRow = UINT32_MAX;
+__device__ __forceinline__ int page_of(const Params &p, const Unit &x, int64_t v, uint32_t &off) {
+    off = kNoRow;
+    if (v >= (int64_t)x.nw + x.nc) return -1;
+    uint32_t r;
+    if (v < x.nw) {
+        r = (uint32_t)(x.wlo + v);
+        if (p.a.ring) p.ring.div((uint32_t)(x.wlo + v), r);
+    } else {
+        r = (uint32_t)(p.a.base + (v - x.nw));
+    }
+    const uint32_t pg = p.page.div(r, off);
+    return pg < (uint32_t)p.a.max_pages ? __ldg(p.a.block_table + (int64_t)x.bi * p.a.max_pages + pg) : -1;
+}
+__device__ __forceinline__ bool is_page(const Params &p, int id) { return id >= 0 && id < p.a.pages; }
+
+// Walks the tiles of this cluster's units.
+struct TileIter {
+    uint32_t u, step;
+    Unit x;
+    int t;
+    bool valid;
+    __device__ __forceinline__ void seek(const Params &p) {      // the first unit from u on with tiles
+        for (; u < p.units; u += step) {
+            make_unit(p, u, fetch_unit(p, u), x);
+            if (x.t1 > x.t0) {
+                t = x.t0;
+                valid = true;
+                return;
+            }
+        }
+        valid = false;
+    }
+    __device__ __forceinline__ void start(const Params &p, uint32_t first, uint32_t stride) {
+        u = first;
+        step = stride;
+        seek(p);
+    }
+    __device__ __forceinline__ void next(const Params &p) {
+        if (++t < x.t1) return;
+        u += step;
+        seek(p);
+    }
+};
+
+// ---- single instructions ------------------------------------------------------------------------------------
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on this barrier in both CTAs once the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+// bf16 A and B, f32 accumulator; A K-major or MN-major, B K-major
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// Arrive on a barrier of any CTA of the cluster (an address from mapa); what this thread wrote or saw is visible to who waits.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool test_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u16(uint32_t addr, uint16_t v) {
+    asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ uint4 ld_codes(const uint8_t *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Sixteen codes times 2^k as bf16 pairs.  A code's exponent and mantissa bits, moved to a bf16's, are its value times 2^-120
+// (subnormals too), so one product with 2^(120 + k) makes it; above k = 7 that power is beyond bf16 and is applied in two.
+__device__ __forceinline__ void widen16(const uint4 c, int k, uint32_t (&w)[8]) {
+    const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+    const uint32_t s = (uint32_t)(247 + min(k, 7)) << 7, scale = s | (s << 16);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) o[j] *= inv;
-    if (a.rd && p >= a.table_rows) bad = true;
-    else if (a.rd && p >= 0) {
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int pr = lane * 8 + j - (D - a.rd) / 2;
-            if (pr < 0) continue;
-            const float2 cs = a.table[p * (a.rd / 2) + pr];
-            const float re = o[2 * j] * cs.x + o[2 * j + 1] * cs.y, im = o[2 * j + 1] * cs.x - o[2 * j] * cs.y;
-            o[2 * j] = re;
-            o[2 * j + 1] = im;
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t x = __byte_perm(cw[i], 0, j ? 0x3424 : 0x1404);
+            w[2 * i + j] = mul_bf16x2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), scale);
+        }
+    if (k > 7) {
+        const uint32_t s2 = (uint32_t)(120 + k) << 7, more = s2 | (s2 << 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = mul_bf16x2(w[i], more);
+    }
+}
+
+// 2^k of an unsigned 64-bit mask's bits [lo, hi), both clamped to [0, 64].
+__device__ __forceinline__ uint64_t bits(int64_t lo, int64_t hi) {
+    const int a = (int)max((int64_t)0, min((int64_t)64, lo)), z = (int)max((int64_t)0, min((int64_t)64, hi));
+    if (z <= a) return 0;
+    return (z - a == 64 ? ~0ull : ((1ull << (z - a)) - 1)) << a;
+}
+
+// What a role needs to wait, and to tell both CTAs to give up.
+struct Ctl {
+    uint32_t bars;
+    volatile int *abort;
+    uint32_t abort_own, abort_peer;
+    __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * (uint32_t)i; }
+    __device__ __forceinline__ void give_up() const {
+        st_cluster_u32(abort_own, 1);
+        st_cluster_u32(abort_peer, 1);
+    }
+    // Every lane waits; false once a CTA of the cluster has given up.
+    template <bool kCluster>
+    __device__ __forceinline__ bool wait(int i, uint32_t phase) const {
+        const uint32_t b = bar(i);
+        bool ok = kCluster ? mbar_try_wait_cluster(b, phase & 1u) : mbar_try_wait(b, phase & 1u);
+        if (!ok) {
+            const uint64_t t0 = globaltimer_ns();
+            for (uint32_t n = 1;; ++n) {
+                ok = kCluster ? mbar_try_wait_cluster(b, phase & 1u) : mbar_try_wait(b, phase & 1u);
+                if (ok) break;
+                if ((n & 15u) == 0u) {
+                    if (*abort) break;
+                    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                        give_up();
+                        break;
+                    }
+                }
+            }
+        }
+        return __all_sync(kAll, ok);
+    }
+};
+
+// ---- the kernel ---------------------------------------------------------------------------------------------
+
+template <bool SPLIT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    uint8_t *ctl_mem = smem + SM_CTL;
+    const uint32_t rank = cluster_ctarank();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+    Ctl c;
+    c.bars = base + SM_CTL;
+    c.abort = reinterpret_cast<volatile int *>(ctl_mem + C_ABORT);
+    c.abort_own = mapa(c.bars + C_ABORT, rank);
+    c.abort_peer = mapa(c.bars + C_ABORT, rank ^ 1u);
+    auto first_bar = [&](int i) -> uint32_t { return mapa(c.bar(i), 0); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(c.bar(B_KFULL + i), 8);
+            mbar_init(c.bar(B_KFREE + i), 1);
+            mbar_init(c.bar(B_VFULL + i), 8);
+            mbar_init(c.bar(B_VFREE + i), 1);
+            mbar_init(c.bar(B_S + i), 1);
+            mbar_init(c.bar(B_P + i), 8);
+            mbar_init(c.bar(B_INV + i), 4);
+        }
+        mbar_init(c.bar(B_QLOC), 1);
+        mbar_init(c.bar(B_Q), 2);
+        mbar_init(c.bar(B_QFREE), 1);
+        mbar_init(c.bar(B_O), 1);
+        mbar_init(c.bar(B_OFREE), 8);
+        mbar_init(c.bar(B_RESC), 1);
+        mbar_init(c.bar(B_RESCD), 8);
+        mbar_init(c.bar(B_SYNC), 1);
+        mbar_init(c.bar(B_DRAIN), 1);
+        *c.abort = (base & 1023u) != 0u;    // the operands' layout needs it aligned
+        reinterpret_cast<int *>(ctl_mem + C_RESC)[0] = 0;
+        reinterpret_cast<int *>(ctl_mem + C_RESC)[1] = 0;
+        fence_mbar_init();
+        grid_launch_dependents();
+    }
+    if (threadIdx.x < 256) reinterpret_cast<int16_t *>(ctl_mem + C_ALPHA)[threadIdx.x] = 0;
+    if (warp == W_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(c.bars + C_TMEM), "n"(TM_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl_mem + C_TMEM);
+    // up to here this overlaps the kernel before it on the stream
+    grid_dependency_wait();
+
+    if (warp >= W_K && warp < W_V) {
+        // ================================ K: 64 rows of the tile, all of d ================================
+        // Warp w takes rows 16 w .. 16 w + 15 of this CTA's 64: step i rows 2 i and 2 i + 1, 16 lanes of 16 codes each (half of
+        // d).  The codes of the next half are fetched while the ones in registers are widened.
+        const int w = warp - W_K, l16 = lane & 15;
+        const uint32_t full0 = first_bar(B_KFULL), full1 = first_bar(B_KFULL + 1);
+        // lane's 16 values are 16-byte units 2 (l16 % 4) and the next one of chunk l16 / 4; odd chunks' lanes store the second
+        // one first, so that eight lanes meet every bank once
+        const uint32_t odd = (l16 >> 2) & 1u;
+        TileIter it;
+        it.start(p, cid, ncl);
+        uint4 code[8];
+        int kx[8];
+        bool bad = false;
+        auto row_of = [&](const TileIter &i) -> int64_t { return (int64_t)i.t * BN + HR * (int)rank + 16 * w + l16; };
+        auto fetch = [&](int i, int slot, int hk) {
+            const int s = __shfl_sync(kAll, slot, 2 * i + (lane >> 4));
+            code[i] = make_uint4(0, 0, 0, 0);
+            kx[i] = 0;
+            if (s >= 0) {
+                code[i] = ld_codes(p.a.codes + (int64_t)s * D + hk * 256 + l16 * 16);
+                kx[i] = __ldg(p.a.exps + (int64_t)s * (D / 32) + hk * 8 + (l16 >> 1));
+            }
+        };
+        auto put = [&](int i, int hk) {
+            uint32_t v[8];
+            widen16(code[i], kx[i], v);
+            const int r = 16 * w + 2 * i + (lane >> 4);
+            const uint32_t at = base + SM_K + (hk * 4 + (l16 >> 2)) * K_CHUNK + r * 128;
+            const uint32_t u0 = 2 * (l16 & 3) + odd, u1 = u0 ^ 1u;
+            st_shared_v4(at + ((u0 ^ (r & 7)) << 4), odd ? v[4] : v[0], odd ? v[5] : v[1], odd ? v[6] : v[2], odd ? v[7] : v[3]);
+            st_shared_v4(at + ((u1 ^ (r & 7)) << 4), odd ? v[0] : v[4], odd ? v[1] : v[5], odd ? v[2] : v[6], odd ? v[3] : v[7]);
+        };
+        auto slot_of = [&](int id, uint32_t off) -> int {
+            bad |= off != kNoRow && !is_page(p, id);
+            return is_page(p, id) ? (int)((uint32_t)id * p.page.d + off) : -1;
+        };
+        uint32_t off = 0;
+        int slot = -1;
+        if (it.valid) {
+            const int id = page_of(p, it.x, row_of(it), off);
+            slot = slot_of(id, off);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) fetch(i, slot, 0);
+        }
+        for (uint32_t J = 0; it.valid; ++J) {
+            it.next(p);
+            const int id = it.valid ? page_of(p, it.x, row_of(it), off) : -1;
+            if (!it.valid) off = kNoRow;
+            if (!c.wait<false>(B_KFREE, J + 1)) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                put(i, 0);
+                fetch(i, slot, 1);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && !(p.stall && J == 0)) arrive_cluster(full0);
+            slot = slot_of(id, off);
+            if (!c.wait<false>(B_KFREE + 1, J + 1)) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                put(i, 1);
+                fetch(i, slot, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(full1);
+        }
+        if (__any_sync(kAll, bad) && lane == 0) flag_status(p.a.status, DS_DEV_BAD_INDEX);
+    } else if (warp >= W_V && warp < W_MMA) {
+        // ============================ V: 128 rows of the tile, this CTA's half of d ============================
+        // Warp w takes rows 32 w .. 32 w + 31: step i rows 4 i .. 4 i + 3, 8 lanes of 16 codes each (a quarter of d).
+        const int w = warp - W_V, l8 = lane & 7;
+        const uint32_t full0 = first_bar(B_VFULL), full1 = first_bar(B_VFULL + 1);
+        const uint32_t odd = (l8 >> 2) & 1u;
+        TileIter it;
+        it.start(p, cid, ncl);
+        uint4 code[8];
+        int kx[8];
+        auto row_of = [&](const TileIter &i) -> int64_t { return (int64_t)i.t * BN + 32 * w + lane; };
+        auto fetch = [&](int i, int slot, int hv) {
+            const int s = __shfl_sync(kAll, slot, 4 * i + (lane >> 3));
+            code[i] = make_uint4(0, 0, 0, 0);
+            kx[i] = 0;
+            if (s >= 0) {
+                code[i] = ld_codes(p.a.codes + (int64_t)s * D + (int)rank * 256 + hv * 128 + l8 * 16);
+                kx[i] = __ldg(p.a.exps + (int64_t)s * (D / 32) + (int)rank * 8 + hv * 4 + (l8 >> 1));
+            }
+        };
+        auto put = [&](int i, int hv) {
+            uint32_t v[8];
+            widen16(code[i], kx[i], v);
+            const int r = 32 * w + 4 * i + (lane >> 3);
+            const uint32_t at = base + SM_V + (hv * 2 + (l8 >> 2)) * V_CHUNK + r * 128;
+            const uint32_t u0 = 2 * (l8 & 3) + odd, u1 = u0 ^ 1u;
+            st_shared_v4(at + ((u0 ^ (r & 7)) << 4), odd ? v[4] : v[0], odd ? v[5] : v[1], odd ? v[6] : v[2], odd ? v[7] : v[3]);
+            st_shared_v4(at + ((u1 ^ (r & 7)) << 4), odd ? v[0] : v[4], odd ? v[1] : v[5], odd ? v[2] : v[6], odd ? v[3] : v[7]);
+        };
+        auto slot_of = [&](int id, uint32_t off) -> int { return is_page(p, id) ? (int)((uint32_t)id * p.page.d + off) : -1; };
+        uint32_t off = 0;
+        int slot = -1;
+        if (it.valid) {
+            const int id = page_of(p, it.x, row_of(it), off);
+            slot = slot_of(id, off);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) fetch(i, slot, 0);
+        }
+        for (uint32_t J = 0; it.valid; ++J) {
+            it.next(p);
+            const int id = it.valid ? page_of(p, it.x, row_of(it), off) : -1;
+            if (!c.wait<false>(B_VFREE, J + 1)) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                put(i, 0);
+                fetch(i, slot, 1);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(full0);
+            slot = slot_of(id, off);
+            if (!c.wait<false>(B_VFREE + 1, J + 1)) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                put(i, 1);
+                fetch(i, slot, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(full1);
+        }
+    } else if (warp == W_MMA) {
+        // ======================================== MMA issue ========================================
+        // The first CTA's warp walks the loop (its conditions are votes), an elected lane issues for both.  S of the next tile
+        // goes before P V of this one when both can.
+        if (rank == 0) {
+            const uint32_t i_s = idesc(128, BN, false), i_pv = idesc(256, 2 * p.R, true);
+            const uint64_t qd = smem_desc_sw128(base + SM_Q, 16, 1024), kd = smem_desc_sw128(base + SM_K, 16, 1024);
+            const uint64_t vd = smem_desc_sw128(base + SM_V, V_CHUNK, 1024), pd = smem_desc_sw128(base + SM_P, 16, 1024);
+            volatile int *cnt = reinterpret_cast<volatile int *>(ctl_mem + C_CNT);
+            volatile int *resc = reinterpret_cast<volatile int *>(ctl_mem + C_RESC);
+            auto done = [&](int b, uint32_t phase) -> bool { return __all_sync(kAll, test_wait_cluster(c.bar(b), phase & 1u)); };
+            uint32_t u = cid;                      // S: its unit, that unit's tiles left, units begun
+            int s_left = 0;
+            uint32_t s_unit = 0, v_unit = 0;
+            int v_left = 0;
+            int2 raw = fetch_unit(p, u);
+            auto begin = [&]() {                   // the next unit with tiles
+                while (u < p.units) {
+                    Unit x;
+                    make_unit(p, u, raw, x);
+                    u += ncl;
+                    raw = fetch_unit(p, u);
+                    if (x.t1 > x.t0) {
+                        s_left = x.t1 - x.t0;
+                        __syncwarp();
+                        cnt[s_unit & 3u] = s_left;
+                        ++s_unit;
+                        return;
+                    }
+                }
+                s_left = 0;
+            };
+            uint32_t sJ = 0, vJ = 0, s_half = 0, v_half = 0, resc_n = 0, idle = 0;
+            bool s_first = true, v_first = true;
+            uint64_t since = 0;
+            begin();
+            while (s_left > 0 || vJ < sJ) {
+                if (s_left > 0 && sJ - vJ < 2 && s_half == 0 && done(B_KFULL, sJ) && (!s_first || done(B_Q, s_unit - 1))) {
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const uint64_t at = (uint64_t)(((k >> 2) * K_CHUNK + (k & 3) * 32) >> 4);
+                            mma_pair(tmem + TM_S + (sJ & 1u) * 64, qd + at, kd + at, i_s, k > 0);
+                        }
+                        commit_pair(c.bar(B_KFREE));
+                    }
+                    __syncwarp();
+                    s_half = 1;
+                    idle = 0;
+                } else if (s_half == 1 && done(B_KFULL + 1, sJ)) {
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 16; k < 32; ++k) {
+                            const uint64_t at = (uint64_t)(((k >> 2) * K_CHUNK + (k & 3) * 32) >> 4);
+                            mma_pair(tmem + TM_S + (sJ & 1u) * 64, qd + at, kd + at, i_s, 1);
+                        }
+                        commit_pair(c.bar(B_S + (int)(sJ & 1u)));
+                        commit_pair(c.bar(B_KFREE + 1));
+                        if (s_left == 1) commit_pair(c.bar(B_QFREE));
+                    }
+                    __syncwarp();
+                    s_half = 0;
+                    s_first = false;
+                    ++sJ;
+                    if (--s_left == 0) {
+                        begin();
+                        s_first = true;
+                    }
+                    idle = 0;
+                } else if (vJ < sJ && v_half == 0 && done(B_P + (int)(vJ & 1u), vJ >> 1) && done(B_VFULL, vJ) &&
+                           (!v_first || v_unit == 0 || done(B_OFREE, v_unit - 1))) {
+                    if (v_first) v_left = cnt[v_unit & 3u];
+                    tc_fence_after();
+                    if (__any_sync(kAll, resc[vJ & 1u] == (int)(vJ + 1))) {
+                        // a reference has moved: O^T of the tiles before this one is scaled first
+                        if (elect_one()) asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(c.bar(B_SYNC)) : "memory");
+                        __syncwarp();
+                        if (!c.wait<true>(B_SYNC, resc_n)) break;
+                        if (lane < 2) {
+                            st_cluster_u32(mapa(c.bars + C_PAR, (uint32_t)lane), vJ & 1u);
+                            arrive_cluster(mapa(c.bar(B_RESC), (uint32_t)lane));
+                        }
+                        if (!c.wait<true>(B_RESCD, resc_n)) break;
+                        ++resc_n;
+                        tc_fence_after();
+                    }
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_pair(tmem + TM_O, vd + (uint64_t)((k * 2048) >> 4),
+                                     pd + (uint64_t)(((vJ & 1u) * P_BYTES + (k >> 2) * K_CHUNK + (k & 3) * 32) >> 4), i_pv,
+                                     k > 0 || !v_first);
+                        commit_pair(c.bar(B_VFREE));
+                    }
+                    __syncwarp();
+                    v_half = 1;
+                    idle = 0;
+                } else if (v_half == 1 && done(B_VFULL + 1, vJ)) {
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_pair(tmem + TM_O + 128, vd + (uint64_t)((2 * V_CHUNK + k * 2048) >> 4),
+                                     pd + (uint64_t)(((vJ & 1u) * P_BYTES + (k >> 2) * K_CHUNK + (k & 3) * 32) >> 4), i_pv,
+                                     k > 0 || !v_first);
+                        commit_pair(c.bar(B_VFREE + 1));
+                        if (v_left == 1) commit_pair(c.bar(B_O));
+                    }
+                    __syncwarp();
+                    v_half = 0;
+                    v_first = false;
+                    ++vJ;
+                    if (--v_left == 0) {
+                        ++v_unit;
+                        v_first = true;
+                    }
+                    idle = 0;
+                } else {
+                    __nanosleep(20);
+                    if ((++idle & 63u) == 0u) {
+                        const uint64_t now = globaltimer_ns();
+                        if (idle == 64u) since = now;
+                        else if (now - since > kWaitLimitNs) c.give_up();
+                        if (__any_sync(kAll, *c.abort != 0)) break;
+                    }
+                }
+            }
+            if (elect_one()) commit_pair(c.bar(B_DRAIN));
+            __syncwarp();
+        }
+    } else if (warp == W_Q) {
+        // ======================================== q by TMA ========================================
+        if (lane == 0) {
+            const uint32_t full = first_bar(B_Q);
+            TileIter it;
+            it.start(p, cid, ncl);
+            for (uint32_t n = 0; it.valid; ++n) {
+                const bool ok = mbar_wait(c.bar(B_QFREE), (n & 1u) ^ 1u, c.abort, kUnitLimitNs);
+                if (!ok) {
+                    c.give_up();
+                    break;
+                }
+                mbar_arrive_expect_tx(c.bar(B_QLOC), (uint32_t)(p.R * D * 2));
+                const int32_t y = (int32_t)((int64_t)it.x.bi * p.a.m * p.a.h + it.x.r0 + (int)rank * p.R);
+                for (int ch = 0; ch < 8; ++ch) tma_load_2d(base + SM_Q + ch * K_CHUNK, &qmap, ch * 64, y, c.bar(B_QLOC));
+                if (!mbar_wait(c.bar(B_QLOC), n & 1u, c.abort, kWaitLimitNs)) {
+                    c.give_up();
+                    mbar_wait_drain(c.bar(B_QLOC), n & 1u, kWaitLimitNs);   // nothing may land after the CTA is gone
+                    break;
+                }
+                arrive_cluster(full);
+                it.t = it.x.t1 - 1;
+                it.next(p);
+            }
+        }
+        __syncwarp();
+    } else if (warp < W_OUT) {
+        // ======================================== softmax ========================================
+        // Lane r of the scores (warps 0 and 1: r < 64) has query r and the tile's rows 0-63, lane r + 64 the same query and rows
+        // 64-127; the two threads share the reference through shared memory and a barrier of their two warps.
+        const int half = warp >> 1, row = (warp & 1) * 32 + lane;
+        const uint32_t tm = tmem + ((uint32_t)(warp * 32) << 16) + TM_S;
+        const uint32_t pfull[2] = {first_bar(B_P), first_bar(B_P + 1)};
+        const uint32_t resc = mapa(c.bars + C_RESC, 0);
+        float *xch = reinterpret_cast<float *>(ctl_mem + C_XCH);
+        const bool idle_warp = (warp & 1) * 32 >= p.R;          // no query of these 32
+        bool dead = false, bad = false;
+        uint32_t J = 0, unit = 0, ex = 0;                       // tiles, units with tiles, exchanges
+        uint32_t lowered = 0;                                   // bit J & 1: this thread's entry of alpha is not 0
+        auto exchange = [&](float v) -> float {                 // the other thread's value
+            float *x = xch + (ex & 1u) * 128;
+            ++ex;
+            x[half * 64 + row] = v;
+            named_bar_sync(1 + (warp & 1), 64);
+            return x[(half ^ 1) * 64 + row];
+        };
+        for (uint32_t u = cid; u < p.units; u += ncl) {
+            Unit x;
+            make_unit(p, u, fetch_unit(p, u), x);
+            const int rq = (int)rank * p.R + row;               // query row of the unit
+            const bool live = row < p.R && x.r0 + rq < x.rows;
+            uint32_t hh = 0;
+            const int64_t pos = x.first + (live ? p.h.div((uint32_t)(x.r0 + rq), hh) : 0);
+            bad |= (live && pos < 0) || x.clipped;
+            const float sink2 = live ? fminf(__ldg(p.a.sink + hh) * kLog2e, 1e37f) : 0.0f;
+            // rows [a0, a1) and [nw, c1) of the list
+            int64_t a0 = 0, a1 = 0, c1 = 0;
+            if (live && pos >= 0) {
+                a0 = p.a.window ? max((int64_t)0, pos - p.a.window + 1 - x.wlo) : 0;
+                a1 = min(pos + 1 - x.wlo, (int64_t)x.nw);
+                c1 = (int64_t)x.nw + (p.a.ratio ? min((pos + 1) / p.a.ratio, (int64_t)x.nc) : 0);
+            }
+            float ref = sink2 - 64.0f, l = 0.0f;
+            bool set = false;
+            for (int t = x.t0; t < x.t1; ++t, ++J) {
+                const int64_t v0 = (int64_t)t * BN + half * 64;
+                uint64_t mask = 0;
+                if (!idle_warp) {
+                    uint32_t off;
+                    const bool there0 = is_page(p, page_of(p, x, v0 + lane, off)), there1 = is_page(p, page_of(p, x, v0 + 32 + lane, off));
+                    const uint64_t there = (uint64_t)__ballot_sync(kAll, there0) | ((uint64_t)__ballot_sync(kAll, there1) << 32);
+                    mask = there & (bits(a0 - v0, a1 - v0) | bits((int64_t)x.nw - v0, c1 - v0));
+                }
+                if (!dead) dead = !c.wait<false>(B_S + (int)(J & 1u), J >> 1);
+                if (!idle_warp) {
+                    tc_fence_after();
+                    uint32_t s[2][32];
+                    tmem_ld32(tm + (J & 1u) * 64, s[0]);
+                    tmem_ld32(tm + (J & 1u) * 64 + 32, s[1]);
+                    tmem_ld_wait(s);
+                    tc_fence_before();
+                    float m = -INFINITY;
+                    if (__all_sync(kAll, mask == ~0ull)) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g)
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                const float v = __uint_as_float(s[g][i]) * p.scale_log2, z = __uint_as_float(s[g][i + 1]) * p.scale_log2;
+                                s[g][i] = __float_as_uint(v);
+                                s[g][i + 1] = __float_as_uint(z);
+                                m = max3(m, v, z);
+                            }
+                    } else {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            const uint32_t mk = (uint32_t)(mask >> (32 * g));
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                const float v = (mk >> i) & 1u ? __uint_as_float(s[g][i]) * p.scale_log2 : -INFINITY;
+                                const float z = (mk >> (i + 1)) & 1u ? __uint_as_float(s[g][i + 1]) * p.scale_log2 : -INFINITY;
+                                s[g][i] = __float_as_uint(v);
+                                s[g][i + 1] = __float_as_uint(z);
+                                m = max3(m, v, z);
+                            }
+                        }
+                    }
+                    m = fmaxf(m, exchange(m));
+                    const int q = (int)rank * p.R + row;
+                    const uint32_t alpha = c.bars + C_ALPHA + ((J & 1u) * 128 + q) * 2;
+                    float up = 0.0f;
+                    if (!set) {
+                        if (m > -INFINITY) {
+                            ref = fmaxf(ref, m);
+                            set = true;
+                        }
+                    } else if (m > ref + kSlack) {
+                        up = fminf(ceilf(m - ref), 16384.0f);
+                        ref = up < 16384.0f ? ref + up : m;
+                        l *= ex2(-up);
+                    }
+                    // alpha's entries of this tile were last used two tiles ago
+                    if (half == 0 && row < p.R && (up > 0.0f || ((lowered >> (J & 1u)) & 1u))) {
+                        st_cluster_u16(mapa(alpha, 0), (uint16_t)up);
+                        st_cluster_u16(mapa(alpha, 1), (uint16_t)up);
+                        lowered = (lowered & ~(1u << (J & 1u))) | ((up > 0.0f ? 1u : 0u) << (J & 1u));
+                        if (up > 0.0f) st_cluster_u32(resc + (J & 1u) * 4, J + 1);
+                    }
+                    const float r = set ? ref : 0.0f;
+                    float sum[2] = {0.0f, 0.0f};
+                    const uint32_t at = base + SM_P + (J & 1u) * P_BYTES + half * K_CHUNK + row * 128;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float e0 = ex2(__uint_as_float(s[g][i + 2 * j]) - r), e1 = ex2(__uint_as_float(s[g][i + 2 * j + 1]) - r);
+                                sum[0] += e0;
+                                sum[1] += e1;
+                                w[j] = pack_bf16x2(e0, e1);
+                            }
+                            st_shared_v4(at + (((uint32_t)(g * 4 + i / 8) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+                        }
+                    l += sum[0] + sum[1];
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) arrive_cluster(pfull[J & 1u]);
+            }
+            if (x.t1 == x.t0) {
+                if (SPLIT && live && half == 0) {
+                    float *st = p.ws + ((size_t)u * (D + 2) + D) * (2 * p.R) + 2 * rq;
+                    st[0] = -INFINITY;
+                    st[1] = 0.0f;
+                }
+                continue;
+            }
+            if (!idle_warp) l += exchange(l);
+            if (half == 0) {
+                if (SPLIT) {
+                    if (live) {
+                        float *st = p.ws + ((size_t)u * (D + 2) + D) * (2 * p.R) + 2 * rq;
+                        st[0] = ref;
+                        st[1] = l;
+                    }
+                } else {
+                    if (row < p.R) {
+                        const float inv = l > 0.0f ? 1.0f / (l + ex2(sink2 - ref)) : (l == 0.0f ? 0.0f : l);
+                        const uint32_t at = c.bars + C_INV + ((unit & 1u) * 128 + rq) * 4;
+                        st_cluster_u32(mapa(at, 0), __float_as_uint(inv));
+                        st_cluster_u32(mapa(at, 1), __float_as_uint(inv));
+                    }
+                    __syncwarp();
+                    if (lane < 2) arrive_cluster(mapa(c.bar(B_INV + (int)(unit & 1u)), (uint32_t)lane));
+                }
+            }
+            ++unit;
+        }
+        if (__any_sync(kAll, bad) && lane == 0) flag_status(p.a.status, DS_DEV_BAD_INDEX);
+    } else {
+        // ================================== output, and O^T's rescaling ==================================
+        // Thread (warp w, lane) has d = 256 rank + 128 v + 32 w + lane of every query: column q of O^T's block v.
+        const int w = warp - W_OUT;
+        const uint32_t tm = tmem + ((uint32_t)(w * 32) << 16) + TM_O;
+        const uint32_t free_bar = first_bar(B_OFREE), resc_bar = first_bar(B_RESCD);
+        const int16_t *alpha = reinterpret_cast<const int16_t *>(ctl_mem + C_ALPHA);
+        const int nq = 2 * p.R;
+        const int d0 = 256 * (int)rank + 32 * w + lane;
+        uint32_t unit = 0, resc_n = 0;
+        bool bad = false, ok = true;
+        for (uint32_t u = cid; u < p.units && ok; u += ncl) {
+            Unit x;
+            make_unit(p, u, fetch_unit(p, u), x);
+            const bool some = x.t1 > x.t0;
+            if (SPLIT && !some) continue;
+            if (some) {
+                uint32_t idle = 0;
+                uint64_t since = 0;
+                for (;;) {
+                    if (__all_sync(kAll, mbar_test_wait(c.bar(B_O), unit & 1u))) break;
+                    if (__all_sync(kAll, test_wait_cluster(c.bar(B_RESC), resc_n & 1u))) {
+                        tc_fence_after();
+                        const int16_t *al = alpha + *reinterpret_cast<volatile int *>(ctl_mem + C_PAR) * 128;
+                        for (int g = 0; g < nq; g += 32) {
+                            const int up = *reinterpret_cast<const volatile int16_t *>(al + g + lane);
+                            if (!__any_sync(kAll, up != 0)) continue;
+                            const float f = ex2(-(float)up);
+                            for (int v = 0; v < 2; ++v) {
+                                uint32_t r[32];
+                                tmem_ld32(tm + v * 128 + g, r);
+                                tmem_ld_wait(r);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * __shfl_sync(kAll, f, j));
+                                tmem_st32(tm + v * 128 + g, r);
+                            }
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_cluster(resc_bar);
+                        ++resc_n;
+                        continue;
+                    }
+                    __nanosleep(40);
+                    if ((++idle & 63u) == 0u) {
+                        const uint64_t now = globaltimer_ns();
+                        if (since == 0) since = now;
+                        else if (now - since > kUnitLimitNs) c.give_up();
+                        if (__any_sync(kAll, *c.abort != 0)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                }
+                if (ok && !SPLIT) ok = c.wait<true>(B_INV + (int)(unit & 1u), unit >> 1);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            const int there = x.rows - x.r0;                 // queries of this unit
+            const float *inv = reinterpret_cast<const float *>(ctl_mem + C_INV) + (unit & 1u) * 128;
+            const bool rot = p.a.rd > 0 && 256 * (int)rank + 128 + 32 * w + 31 >= D - p.a.rd;
+            uint16_t *o = p.a.o + ((int64_t)x.bi * p.a.m * p.a.h + x.r0) * D;
+            float *part = SPLIT ? p.ws + (size_t)u * (D + 2) * nq : nullptr;
+            for (int g = 0; g < nq && g < there; g += 32) {
+                uint32_t hh;
+                const int64_t pos0 = x.first + p.h.div((uint32_t)(x.r0 + g), hh);
+                for (int v = 0; v < 2; ++v) {
+                    const int d = d0 + 128 * v;
+                    uint32_t r[32];
+                    if (some) {
+                        tmem_ld32(tm + v * 128 + g, r);
+                        tmem_ld_wait(r);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = 0;
+                    }
+                    if (some && v == 1 && (g + 32 >= nq || g + 32 >= there)) {      // the last read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_cluster(free_bar);
+                    }
+                    if (SPLIT) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (g + j < there) part[(size_t)(g + j) * D + d] = __uint_as_float(r[j]);
+                        continue;
+                    }
+                    if (some) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(inv + g + j);
+                            r[j] = __float_as_uint(__uint_as_float(r[j]) * f.x);
+                            r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) * f.y);
+                            r[j + 2] = __float_as_uint(__uint_as_float(r[j + 2]) * f.z);
+                            r[j + 3] = __float_as_uint(__uint_as_float(r[j + 3]) * f.w);
+                        }
+                    }
+                    if (rot) {
+                        const bool turned = d >= D - p.a.rd;
+                        int64_t pos = pos0;
+                        uint32_t at = hh;
+                        float2 cs = make_float2(1.0f, 0.0f);
+                        bool fresh = true;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            if (fresh) {
+                                const bool in = pos >= 0 && pos < p.a.table_rows;
+                                cs = make_float2(1.0f, 0.0f);
+                                if (in && turned) cs = __ldg(p.a.table + pos * (p.a.rd / 2) + ((d - (D - p.a.rd)) >> 1));
+                                bad |= !in && g + j < there;
+                            }
+                            const float y = __shfl_xor_sync(kAll, __uint_as_float(r[j]), 1), z = __uint_as_float(r[j]);
+                            r[j] = __float_as_uint(z * cs.x + y * ((d & 1) ? -cs.y : cs.y));
+                            fresh = ++at == p.h.d;
+                            if (fresh) {
+                                at = 0;
+                                ++pos;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (g + j < there) o[(int64_t)(g + j) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[j])));
+                }
+            }
+            if (some) ++unit;
+        }
+        if (__any_sync(kAll, bad) && lane == 0) flag_status(p.a.status, DS_DEV_BAD_INDEX);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *c.abort) flag_status(p.a.status, DS_DEV_TIMEOUT);
+    // no MMA and no commit is under way in either CTA once this has passed
+    if (warp == W_MMA) {
+        mbar_wait_drain(c.bar(B_DRAIN), 0, 2 * kWaitLimitNs);
+        __syncwarp();
+    }
+    __syncthreads();
+    cluster_sync();
+    if (warp == W_MMA)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(TM_COLS) : "memory");
+}
+
+// ---- parts of a unit joined ------------------------------------------------------------------------------------
+
+constexpr int kMaxParts = 64;
+
+// One query row a block; thread i has values 4 i .. 4 i + 3.  Each part has its reference, its sum and its O^T.
+__global__ void __launch_bounds__(128) chunk_merge_kernel(const __grid_constant__ Params p) {
+    grid_dependency_wait();
+    const uint32_t tile = blockIdx.x;               // unit / parts
+    const int q = blockIdx.y, lane = threadIdx.x & 31;
+    uint32_t bi, hh;
+    const int qt = p.nqt - 1 - (int)p.b.div(tile, bi);
+    const int n = p.a.lens ? max(0, min(__ldg(p.a.lens + bi), p.a.m)) : p.a.m, r = qt * 2 * p.R + q;
+    if (r >= n * p.a.h) return;
+    const int64_t pos = (int64_t)__ldg(p.a.first + bi) + p.h.div((uint32_t)r, hh);
+    const int np = (int)p.parts.d;
+    const size_t slot = (size_t)(D + 2) * (2 * p.R);
+    const float *ws = p.ws + (size_t)tile * np * slot;
+    float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int k = lane + 32 * i;
+        if (k < np) {
+            const float2 st = *reinterpret_cast<const float2 *>(ws + k * slot + (size_t)D * (2 * p.R) + 2 * q);
+            l[i] = st.y;
+            ref[i] = st.y == 0.0f ? -INFINITY : st.x;
         }
     }
+    float top = fmaxf(ref[0], ref[1]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        uint32_t w;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(o[2 * j + 1]), "f"(o[2 * j]));
-        reinterpret_cast<uint32_t *>(a.o + row * D)[lane * 8 + j] = w;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    float wgt[2], den = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        wgt[i] = l[i] == 0.0f ? 0.0f : ex2(ref[i] - top);
+        den += wgt[i] * l[i];
     }
-    if (bad && lane == 0) flag_status(a.status, DS_DEV_BAD_INDEX);
+    den = rows::row_sum<32>(den);
+    const float sink2 = fminf(__ldg(p.a.sink + hh) * kLog2e, 1e37f);
+    const float inv = den == 0.0f ? 0.0f : 1.0f / (den + ex2(sink2 - top));
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float *src = ws + (size_t)q * D + 4 * threadIdx.x;
+#pragma unroll 4
+    for (int k = 0; k < np; ++k) {
+        const float f = __shfl_sync(kAll, k < 32 ? wgt[0] : wgt[1], k & 31);
+        if (f == 0.0f) continue;                    // a part without rows wrote none
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + k * slot));
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+    }
+    acc.x *= inv;
+    acc.y *= inv;
+    acc.z *= inv;
+    acc.w *= inv;
+    const int j = 4 * (int)threadIdx.x - (D - p.a.rd);
+    if (p.a.rd) {
+        if (pos >= 0 && pos < p.a.table_rows) {
+            if (j >= 0) {
+                const float2 *cs = p.a.table + pos * (p.a.rd / 2) + j / 2;
+                const float2 c0 = __ldg(cs), c1 = __ldg(cs + 1);
+                acc = make_float4(acc.x * c0.x + acc.y * c0.y, acc.y * c0.x - acc.x * c0.y, acc.z * c1.x + acc.w * c1.y,
+                                  acc.w * c1.x - acc.z * c1.y);
+            }
+        } else if (threadIdx.x == 0) {
+            flag_status(p.a.status, DS_DEV_BAD_INDEX);
+        }
+    }
+    reinterpret_cast<uint2 *>(p.a.o + (((int64_t)bi * p.a.m * p.a.h + r) * D))[threadIdx.x] =
+        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+}
+
+// ---- host side --------------------------------------------------------------------------------------------------
+
+constexpr int kMaxDev = 64;
+int g_clusters[kMaxDev];
+std::mutex g_mutex;
+std::atomic<int> g_test_stall{0};
+
+// Clusters that run at once on the current device, 0 when the kernel cannot be configured.
+int max_clusters(int dev) {
+    if (dev < 0 || dev >= kMaxDev) return 0;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (g_clusters[dev]) return g_clusters[dev];
+    int n = 0, sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    for (const void *k : {(const void *)chunk_attn_kernel<false>, (const void *)chunk_attn_kernel<true>})
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms / 2 * 2), 1, 1);
+    cfg.blockDim = dim3(NTHREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    if (cudaOccupancyMaxActiveClusters(&n, (const void *)chunk_attn_kernel<false>, &cfg) != cudaSuccess || n < 1) return 0;
+    return g_clusters[dev] = n;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 f = known.load(std::memory_order_relaxed);
+    if (!f) {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess || !fn)
+            return nullptr;
+        f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+        known.store(f, std::memory_order_relaxed);
+    }
+    return f;
+}
+
+// q as rows of 512 values, boxes of 64 columns by R rows in the MMA's 128-byte swizzle.
+bool make_q_map(CUtensorMap *map, const void *q, int64_t nrows, int R) {
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)nrows};
+    cuuint64_t strides[1] = {(cuuint64_t)D * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)R};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(q), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Plan {
+    int R, nqt, parts, clusters;
+    int64_t units;
+};
+
+// Query rows a CTA: the fewest that hold a sequence's queries in one unit.  Parts of a unit: with fewer units than clusters
+// (or little more), the number of least estimated time, in tiles: rounds of units, each its tiles and two for its ends, and
+// from two parts on the merge.
+bool plan(int b, int m, int h, int window, int ratio, int page, int max_pages, Plan &pl) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const int g = max_clusters(dev);
+    if (g <= 0) return false;
+    const int64_t nr = (int64_t)m * h;
+    pl.R = nr <= 32 ? 16 : nr <= 64 ? 32 : 64;
+    pl.nqt = (int)((nr + 2 * pl.R - 1) / (2 * pl.R));
+    const int64_t units = (int64_t)b * pl.nqt, cap = (int64_t)max_pages * page;
+    // rows that a unit can have at most, for all that the host knows
+    const int64_t span = (2 * pl.R + h - 2) / h;
+    int64_t most = window ? std::min<int64_t>(cap, (int64_t)window + span) : cap;
+    if (ratio) most = std::min(cap, most + cap / 1);
+    const int64_t tiles = std::max<int64_t>(1, (most + BN - 1) / BN);
+    pl.parts = 1;
+    if (units < 4 * (int64_t)g) {
+        double least = 1e30;
+        for (int k = 1; k <= kMaxParts && k <= tiles; ++k) {
+            const double rounds = (double)((units * k + g - 1) / g);
+            const double cost = rounds * ((double)((tiles + k - 1) / k) + 2.0) + (k > 1 ? 3.0 + 0.05 * k : 0.0);
+            if (cost < least) {
+                least = cost;
+                pl.parts = k;
+            }
+        }
+    }
+    pl.units = units * pl.parts;
+    pl.clusters = (int)std::min<int64_t>(pl.units, g);
+    return pl.units < UINT32_MAX / 2;
+}
+
+size_t workspace_bytes(const Plan &pl) {
+    return pl.parts > 1 ? (size_t)pl.units * (D + 2) * (2 * pl.R) * sizeof(float) : 0;
 }
 
 }  // namespace chunk
 
-size_t chunk_attn_fp8_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
+void set_test_stall_chunk(bool on) { chunk::g_test_stall.store(on ? 1 : 0, std::memory_order_relaxed); }
+
+size_t chunk_attn_fp8_workspace_bytes(int b, int m, int h, int window, int ratio, int page, int max_pages) {
+    chunk::Plan pl;
+    if ((int64_t)b * m == 0 || !chunk::plan(b, m, h, window, ratio, page, max_pages, pl)) return 0;
+    return chunk::workspace_bytes(pl);
+}
 
 int launch_chunk_attn_fp8(const chunk::Args &a, cudaStream_t stream) {
-    const int64_t nrows = (int64_t)a.b * a.m * a.h;
-    chunk::chunk_attn_plain_kernel<<<(unsigned)((nrows + 7) / 8), 256, 0, stream>>>(a, rows::Divisor((uint32_t)a.page), nrows);
-    return launch_status();
+    using namespace chunk;
+    Plan pl;
+    if (!plan(a.b, a.m, a.h, a.window, a.ratio, a.page, a.max_pages, pl)) return launch_failed();
+    const size_t need = workspace_bytes(pl);
+    if (a.workspace_bytes < need || (need && !a.workspace)) return DS_EWORKSPACE;
+    Params p{a, Divisor((uint32_t)a.h), Divisor((uint32_t)a.page), Divisor((uint32_t)std::max(a.ring, 1)), Divisor((uint32_t)a.b),
+             Divisor((uint32_t)pl.parts), pl.R, pl.nqt, (uint32_t)pl.units,
+             std::min<int64_t>((int64_t)a.max_pages * a.page, (int64_t)1 << 31), a.scale * kLog2e, static_cast<float *>(a.workspace),
+             g_test_stall.load(std::memory_order_relaxed)};
+    CUtensorMap qmap;
+    if (!make_q_map(&qmap, a.q, (int64_t)a.b * a.m * a.h, pl.R)) return DS_ECUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pl.clusters), 1, 1);
+    cfg.blockDim = dim3(NTHREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = stream;
+    // programmatic dependent launch: the set-up overlaps the previous kernel on the stream
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const bool split = pl.parts > 1;
+    if (cudaLaunchKernelEx(&cfg, split ? chunk_attn_kernel<true> : chunk_attn_kernel<false>, qmap, p) != cudaSuccess) return launch_failed();
+    if (split) {
+        cfg.gridDim = dim3((unsigned)(pl.units / pl.parts), (unsigned)(2 * pl.R), 1);
+        cfg.blockDim = dim3(128, 1, 1);
+        cfg.dynamicSmemBytes = 0;
+        if (cudaLaunchKernelEx(&cfg, chunk_merge_kernel, p) != cudaSuccess) return launch_failed();
+    }
+    return DS_OK;
 }
 
 }  // namespace dsattn

@@ -33,6 +33,7 @@ struct Args {
 }  // namespace chunk
 
 size_t chunk_attn_fp8_workspace_bytes(int b, int m, int h, int window, int ratio, int page, int max_pages);
+void set_test_stall_chunk(bool on);
 int launch_chunk_attn_fp8(const chunk::Args &a, cudaStream_t stream);
 
 }  // namespace dsattn
