@@ -459,7 +459,8 @@ int ds_chunk_attn_fp8_paged(const uint16_t *q, const uint8_t *codes, const int8_
     if (ring > 0 && (window == 0 || ring < window || ring > (int64_t)max_pages * page)) return DS_EINVAL;
     if (ring > 0 && !lens && ring < (int64_t)window + m - 1) return DS_EINVAL;
     if (ring > 0 && ratio > 0 && base < ring) return DS_EINVAL;
-    if (d != 512 || h > 128 || !pool_fits(pages, page) || (int64_t)b * m > INT32_MAX / h) return DS_EUNSUPPORTED;
+    if (d != 512 || h > 128 || !pool_fits(pages, page) || (int64_t)b * m > INT32_MAX / h || ring > 1 << 29)
+        return DS_EUNSUPPORTED;
     if ((int64_t)b * m == 0) return DS_OK;
     if (!q || !o || !sink || !first || !store_there(codes, exps, pages, block_table, max_pages)) return DS_EINVAL;
     if (!aligned16(q) || !aligned16(o) || !aligned16(codes) || !aligned16(exps)) return DS_EINVAL;

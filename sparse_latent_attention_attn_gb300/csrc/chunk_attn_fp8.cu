@@ -10,25 +10,27 @@
 // first and compressed rows behind them, in tiles of 128; each query's own range is a mask.  With rows of 512 values an
 // accumulator of 128 queries in f32 fills the tensor memory of an SM, which leaves no room for scores.  So two SMs share
 // a unit (a cluster of two CTAs, cta_group::2), each with 64 of its queries and with one half of d:
-//   * S = Q K^T: M = 128 queries (64 a CTA), N = 128 rows (each CTA widens 64 of them), K = 512.  A CTA's scores lie on
-//     all 128 lanes: query r on lane r with rows 0-63 of the tile, and on lane r + 64 with rows 64-127.
-//   * O^T += V^T P^T: M = 256 values of d (128 a CTA, twice), N = 128 queries (each CTA's P), K = 128 rows.  Each CTA widens
-//     all 128 rows for its own half of d; O^T takes 256 columns of tensor memory, and two tiles of scores 128.
-// No scores and no probabilities cross between the CTAs: the tensor cores read both CTAs' operands.  The MMAs of a tile take
-// 0.75 + 0.53 us (23.3 ns for each of 32, 32.9 ns for each of 16, measured), 0.85 of the tensor cores' rate.
+//   * S = Q K^T: M = 128 queries (64 a CTA), N = 128 rows (64 a CTA), K = 512.  A CTA's scores lie on all 128 lanes: query r
+//     on lane r with rows 0-63 of the tile, and on lane r + 64 with rows 64-127.
+//   * O^T += V^T P^T: M = 256 values of d (128 a CTA, twice), N = 128 queries (each CTA's P), K = 128 rows.  O^T takes 256
+//     columns of tensor memory, and two tiles of scores 128.
+// The tensor cores read both CTAs' operands, so no scores and no probabilities cross between the CTAs.  The MMAs of a tile
+// take 0.75 + 0.53 us (23.3 ns for each of 32, 32.9 ns for each of 16, measured), 0.85 of the tensor cores' rate.
 //
-// The codes are widened to bf16 in registers (exact: at most four significant bits; a code's bits moved to a bf16's,
-// times 2^(120 + k)) on their way into the operands, once for S and once for P V, which spares a copy in HBM: 33/32 byte a
-// value is all that is read.  An operand half is handed back as soon as its MMAs are done, while the next tile's codes
-// wait in registers.
+// The codes are widened to bf16 in registers (exact: at most four significant bits; a code's bits moved to a bf16's, times
+// 2^(120 + k)) on their way into shared memory, which spares a copy in HBM: 33/32 byte a value is all that is read.
+// Each CTA widens its 64 rows once, as K; for P V it needs its half of d of all 128, and the copy engine brings them: half of
+// K's chunks go to the CTA's own V, half to the other's, 8 KB each, in the layout that they have (a widening of each row in
+// both CTAs took the integer pipe 2100 cycles a tile, of 2500 that the MMAs take).  An operand half is handed back as
+// soon as its readers are done, while the next tile's codes wait in registers.
 //
 // The softmax works on a reference per query: the first tile's maximum, moved (by whole octaves, so that O^T and the sum are
 // scaled exactly) only when a later one exceeds it by more than kSlack octaves.  It is never more than 64 octaves below the
 // sink, so that 1 / (sum + sink) is a normal number wherever an output is.  P is rounded to bf16 for the product, as in
 // ds_sparse_attn; the sum takes it unrounded.
 //
-// Warps: 0-3 softmax, 4-7 output (and O^T's rescaling, on request), 8-11 widen K, 12-15 widen V, 16 issues the MMAs (in the
-// cluster's first CTA, for both), 17 fetches q by TMA.  Every wait gives up after 2 s (DS_DEV_TIMEOUT).
+// Warps: 0-3 softmax, 4-7 output (and O^T's rescaling, on request), 8-15 widen, 16 issues the MMAs (in the cluster's first
+// CTA, for both), 17 fetches q by TMA, 18 and 19 have the halves of K copied to V.  Every wait gives up after 2 s (DS_DEV_TIMEOUT).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -50,8 +52,10 @@ using rows::Divisor;
 constexpr int D = 512;
 constexpr int BN = 128;                     // rows of a tile
 constexpr int HR = 64;                      // of them widened for S by each CTA; also query rows of a CTA, at most
-constexpr int NTHREADS = 576;               // 18 warps
-constexpr int W_OUT = 4, W_K = 8, W_V = 12, W_MMA = 16, W_Q = 17;
+constexpr int NTHREADS = 640;               // 20 warps, five warpgroups
+// registers: 128 * (136 + 72 + 112 + 112 + 48) is what 640 threads have with 96 each
+constexpr uint32_t REG_SOFTMAX = 136, REG_OUT = 72, REG_WIDEN = 112, REG_MMA = 48;
+constexpr int W_OUT = 4, W_WIDEN = 8, W_MMA = 16, W_Q = 17, W_COPY = 18;
 
 constexpr int K_CHUNK = HR * 128;           // 64 rows of 64 values
 constexpr int V_CHUNK = BN * 128;           // 128 rows of 64 values
@@ -69,27 +73,28 @@ constexpr int TM_O = 0, TM_S = 256, TM_COLS = 512;
 // barriers (8 bytes each); "first": used in the cluster's first CTA only
 enum : int {
     B_KFULL = 0,              // [2] half of K's chunks widened in both CTAs (first)
-    B_KFREE = B_KFULL + 2,    // [2] its MMAs are done
-    B_VFULL = B_KFREE + 2,    // [2] half of V's chunks widened in both CTAs (first)
-    B_VFREE = B_VFULL + 2,    // [2]
+    B_KLOC = B_KFULL + 2,     // [2] ... in this CTA
+    B_KFREE = B_KLOC + 2,     // [2] its MMAs are done, and its copies have been read
+    B_VLOC = B_KFREE + 2,     // [2] half of V's chunks landed in this CTA
+    B_VFULL = B_VLOC + 2,     // [2] ... in both (first)
+    B_VFREE = B_VFULL + 2,    // [2] its MMAs are done
     B_S = B_VFREE + 2,        // [2] scores of tile J there (J & 1)
     B_P = B_S + 2,            // [2] P of tile J written in both CTAs (first)
     B_QLOC = B_P + 2,         // q of a unit landed in this CTA
     B_Q = B_QLOC + 1,         // ... in both (first)
     B_QFREE = B_Q + 1,        // the unit's last S is done
-    B_O = B_QFREE + 1,        // the unit's last P V is done
+    B_O = B_QFREE + 1,        // for the output warps: the unit's last P V is done, or O^T is to be rescaled (C_EVENT)
     B_OFREE = B_O + 1,        // O^T read in both CTAs (first)
     B_INV = B_OFREE + 1,      // [2] the unit's factors (unit & 1) are there
-    B_RESC = B_INV + 2,       // O^T is to be rescaled
-    B_RESCD = B_RESC + 1,     // ... and is, in both CTAs (first)
+    B_RESCD = B_INV + 2,      // O^T rescaled in both CTAs (first)
     B_SYNC = B_RESCD + 1,     // P V so far is done (first)
     B_DRAIN = B_SYNC + 1,
     B_COUNT = B_DRAIN + 1
 };
 constexpr int C_TMEM = 8 * B_COUNT, C_ABORT = C_TMEM + 4, C_RESC = C_ABORT + 4;   // [2] int: tile + 1 that needs a rescale
 constexpr int C_CNT = C_RESC + 8;                                                 // [4] int: tiles of the units under way
-constexpr int C_PAR = C_CNT + 16;                                                 // int: J & 1 of the rescale under way
-static_assert(C_PAR + 4 <= 256, "control block");
+constexpr int C_EVENT = C_CNT + 16;         // [2] int: 2 (n + 1) + (J & 1) where phase n of B_O asks for a rescale at tile J
+static_assert(C_EVENT + 8 <= 256, "control block");
 constexpr int C_ALPHA = 256;                // [2][128] int16: octaves by which a query's column of O^T is to be lowered
 constexpr int C_INV = C_ALPHA + 512;        // [2][128] f32: 1 / denominator
 constexpr int C_XCH = C_INV + 1024;         // [2][2][64] f32: maxima and sums, between the two threads of a query
@@ -107,20 +112,21 @@ struct Params {
     int R;               // query rows of a CTA: 64, 32 or 16
     int nqt;             // query tiles of a sequence
     uint32_t units;
-    int64_t cap;         // logical rows that the block table can hold, at most 2^31
+    int64_t cap;         // logical rows that the block table can hold, at most kMaxRows
     float scale_log2;
     float *ws;
     int stall;
 };
 
 // A unit's rows: tile t holds rows [128 t, 128 t + 128) of the list of nw window rows (positions wlo ..) and nc compressed
-// rows; this unit takes tiles [t0, t1).
+// rows; this unit takes tiles [t0, t1).  Logical rows are below kMaxRows, so what counts them fits an int.
+constexpr int64_t kMaxRows = 1 << 29;
 struct Unit {
     int bi, part;
     int r0, rows;        // query rows [r0, min(r0 + 2 R, rows)) of the sequence
-    int64_t first;
-    int64_t wlo;
-    uint32_t nw, nc;
+    int first;
+    uint32_t wlo;
+    int nw, nc;
     int t0, t1;
     bool clipped;        // rows beyond the block table
 };
@@ -147,72 +153,78 @@ __device__ __forceinline__ void make_unit(const Params &p, uint32_t u, int2 raw,
     x.clipped = false;
     if (x.r0 >= x.rows) return;
     uint32_t rest;
-    const int64_t lo = x.first + p.h.div((uint32_t)x.r0, rest);
-    const int64_t hi = x.first + p.h.div((uint32_t)min(x.r0 + 2 * p.R, x.rows) - 1, rest);
+    const int64_t lo = (int64_t)x.first + p.h.div((uint32_t)x.r0, rest);
+    const int64_t hi = (int64_t)x.first + p.h.div((uint32_t)min(x.r0 + 2 * p.R, x.rows) - 1, rest);
     if (hi < 0) return;
-    if (p.a.window) x.wlo = max((int64_t)0, lo - p.a.window + 1);
+    if (p.a.window) x.wlo = (uint32_t)max((int64_t)0, lo - p.a.window + 1);
     int64_t end = hi + 1;
     if (!p.a.ring && end > p.cap) {
         end = p.cap;
         x.clipped = true;
     }
-    x.nw = (uint32_t)max((int64_t)0, end - x.wlo);
+    x.nw = (int)max((int64_t)0, end - x.wlo);
     if (p.a.ratio) {
         int64_t nc = (hi + 1) / p.a.ratio;
         if (nc > p.cap - p.a.base) {
             nc = max((int64_t)0, p.cap - p.a.base);
             x.clipped = true;
         }
-        x.nc = (uint32_t)nc;
+        x.nc = (int)nc;
     }
-    const int64_t nt = ((int64_t)x.nw + x.nc + BN - 1) / BN;
+    const int64_t nt = (x.nw + x.nc + BN - 1) / BN;
     x.t0 = (int)(nt * x.part / (int)p.parts.d);
     x.t1 = (int)(nt * (x.part + 1) / (int)p.parts.d);
 }
 
+// What is left of a unit for whoever fetches its rows.
+struct List {
+    const int32_t *table;    // the sequence's pages
+    uint32_t wlo;
+    int nw, nv;              // window rows, all rows
+};
+__device__ __forceinline__ List list_of(const Params &p, const Unit &x) {
+    return {p.a.block_table + (int64_t)x.bi * p.a.max_pages, x.wlo, x.nw, x.nw + x.nc};
+}
+
 // Block table entry of the list's row v, and the row's place in its page (kNoRow behind the list's end).
 constexpr uint32_t kNoRow = UINT32_MAX;
-__device__ __forceinline__ int page_of(const Params &p, const Unit &x, int64_t v, uint32_t &off) {
+__device__ __forceinline__ int page_of(const Params &p, const List &x, int v, uint32_t &off) {
     off = kNoRow;
-    if (v >= (int64_t)x.nw + x.nc) return -1;
-    uint32_t r;
-    if (v < x.nw) {
-        r = (uint32_t)(x.wlo + v);
-        if (p.a.ring) p.ring.div((uint32_t)(x.wlo + v), r);
-    } else {
-        r = (uint32_t)(p.a.base + (v - x.nw));
-    }
+    if (v >= x.nv) return -1;
+    uint32_t r = v < x.nw ? x.wlo + (uint32_t)v : (uint32_t)(p.a.base + (v - x.nw));
+    if (v < x.nw && p.a.ring) p.ring.div(x.wlo + (uint32_t)v, r);
     const uint32_t pg = p.page.div(r, off);
-    return pg < (uint32_t)p.a.max_pages ? __ldg(p.a.block_table + (int64_t)x.bi * p.a.max_pages + pg) : -1;
+    return pg < (uint32_t)p.a.max_pages ? __ldg(x.table + pg) : -1;
 }
 __device__ __forceinline__ bool is_page(const Params &p, int id) { return id >= 0 && id < p.a.pages; }
 
 // Walks the tiles of this cluster's units.
 struct TileIter {
-    uint32_t u, step;
-    Unit x;
-    int t;
-    bool valid;
-    __device__ __forceinline__ void seek(const Params &p) {      // the first unit from u on with tiles
+    uint32_t u;
+    int t, t1;
+    List x;
+    __device__ __forceinline__ bool valid() const { return t < t1; }
+    __device__ __forceinline__ void seek(const Params &p, uint32_t step) {      // the first unit from u on with tiles
         for (; u < p.units; u += step) {
-            make_unit(p, u, fetch_unit(p, u), x);
-            if (x.t1 > x.t0) {
-                t = x.t0;
-                valid = true;
+            Unit unit;
+            make_unit(p, u, fetch_unit(p, u), unit);
+            if (unit.t1 > unit.t0) {
+                t = unit.t0;
+                t1 = unit.t1;
+                x = list_of(p, unit);
                 return;
             }
         }
-        valid = false;
+        t = t1 = 0;
     }
-    __device__ __forceinline__ void start(const Params &p, uint32_t first, uint32_t stride) {
+    __device__ __forceinline__ void start(const Params &p, uint32_t first, uint32_t step) {
         u = first;
-        step = stride;
-        seek(p);
+        seek(p, step);
     }
-    __device__ __forceinline__ void next(const Params &p) {
-        if (++t < x.t1) return;
+    __device__ __forceinline__ void next(const Params &p, uint32_t step) {
+        if (++t < t1) return;
         u += step;
-        seek(p);
+        seek(p, step);
     }
 };
 
@@ -241,7 +253,13 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
     return r != 0;
 }
-// Arrive on a barrier of any CTA of the cluster (an address from mapa); what this thread wrote or saw is visible to who waits.
+// Arrive on a barrier of any CTA of the cluster (an address from mapa).  For operands: they were written to this CTA's shared
+// memory and fenced for the async proxy, and it is this SM's tensor core that reads them.  (At cluster scope a
+// release waits for the codes under way too: 12000 cycles a tile instead of 3000.)
+__device__ __forceinline__ void arrive_operand(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same for what threads of the other CTA read: what this thread wrote or saw is visible to who waits at cluster scope.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -268,6 +286,20 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
+// 16 columns of this thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&f)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ uint4 ld_codes(const uint8_t *p) {
     uint4 v;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
@@ -279,28 +311,35 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Sixteen codes times 2^k as bf16 pairs.  A code's exponent and mantissa bits, moved to a bf16's, are its value times 2^-120
-// (subnormals too), so one product with 2^(120 + k) makes it; above k = 7 that power is beyond bf16 and is applied in two.
-__device__ __forceinline__ void widen16(const uint4 c, int k, uint32_t (&w)[8]) {
+// Sixteen codes times a power of two as bf16 pairs.  A code's exponent and mantissa bits, moved to a bf16's, are its value
+// times 2^-120 (subnormals too), so one product with 2^(120 + k) makes it: b is that power's exponent field, 247 + k, or 0
+// for zeros.
+__device__ __forceinline__ void widen16(const uint4 c, uint32_t b, uint32_t (&w)[8]) {
     const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-    const uint32_t s = (uint32_t)(247 + min(k, 7)) << 7, scale = s | (s << 16);
+    const uint32_t scale = b * 0x00800080u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t x = __byte_perm(cw[i], 0, j ? 0x3424 : 0x1404);
-            w[2 * i + j] = mul_bf16x2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), scale);
-        }
-    if (k > 7) {
-        const uint32_t s2 = (uint32_t)(120 + k) << 7, more = s2 | (s2 << 16);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = mul_bf16x2(w[i], more);
+    for (int i = 0; i < 4; ++i) {
+        // a bf16's low bytes, and its high bytes with the sign
+        const uint32_t lo = (cw[i] << 4) & 0xf0f0f0f0u, hi = ((cw[i] >> 4) & 0x07070707u) | (cw[i] & 0x80808080u);
+        w[2 * i] = mul_bf16x2(__byte_perm(lo, hi, 0x5140), scale);
+        w[2 * i + 1] = mul_bf16x2(__byte_perm(lo, hi, 0x7362), scale);
     }
 }
 
-// 2^k of an unsigned 64-bit mask's bits [lo, hi), both clamped to [0, 64].
-__device__ __forceinline__ uint64_t bits(int64_t lo, int64_t hi) {
-    const int a = (int)max((int64_t)0, min((int64_t)64, lo)), z = (int)max((int64_t)0, min((int64_t)64, hi));
+// The exponents k of four blocks as widen16 takes them, 247 + min(k, 7); -128 stands for zeros.
+constexpr uint32_t kZeros = 0x80808080u;
+// A byte's top bit where k > 7.
+__device__ __forceinline__ uint32_t above7(uint32_t four) { return ((four & 0x7f7f7f7fu) + 0x78787878u) & ~four & 0x80808080u; }
+__device__ __forceinline__ uint32_t fields(uint32_t four, bool some_above7) {
+    const uint32_t f = __vadd4(some_above7 ? __vmins4(four, 0x07070707u) : four, 0xf7f7f7f7u);
+    // -128: the top bit and no other
+    const uint32_t zero = four & ~((four & 0x7f7f7f7fu) + 0x7f7f7f7fu) & 0x80808080u;
+    return zero ? f & ~((zero >> 7) * 255u) : f;
+}
+
+// Bits [lo, hi) of 64, both ends clamped to [0, 64].
+__device__ __forceinline__ uint64_t bits(int lo, int hi) {
+    const int a = max(0, min(64, lo)), z = max(0, min(64, hi));
     if (z <= a) return 0;
     return (z - a == 64 ? ~0ull : ((1ull << (z - a)) - 1)) << a;
 }
@@ -316,7 +355,7 @@ struct Ctl {
         st_cluster_u32(abort_peer, 1);
     }
     // Every lane waits; false once a CTA of the cluster has given up.
-    template <bool kCluster>
+    template <bool kCluster, uint64_t kLimit = kWaitLimitNs>
     __device__ __forceinline__ bool wait(int i, uint32_t phase) const {
         const uint32_t b = bar(i);
         bool ok = kCluster ? mbar_try_wait_cluster(b, phase & 1u) : mbar_try_wait(b, phase & 1u);
@@ -327,7 +366,7 @@ struct Ctl {
                 if (ok) break;
                 if ((n & 15u) == 0u) {
                     if (*abort) break;
-                    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                    if (globaltimer_ns() - t0 > kLimit) {
                         give_up();
                         break;
                     }
@@ -358,9 +397,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(c.bar(B_KFULL + i), 8);
-            mbar_init(c.bar(B_KFREE + i), 1);
-            mbar_init(c.bar(B_VFULL + i), 8);
+            mbar_init(c.bar(B_KFULL + i), 16);
+            mbar_init(c.bar(B_KLOC + i), 8);
+            mbar_init(c.bar(B_KFREE + i), 2);
+            mbar_init(c.bar(B_VLOC + i), 1);
+            mbar_init(c.bar(B_VFULL + i), 2);
             mbar_init(c.bar(B_VFREE + i), 1);
             mbar_init(c.bar(B_S + i), 1);
             mbar_init(c.bar(B_P + i), 8);
@@ -371,11 +412,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         mbar_init(c.bar(B_QFREE), 1);
         mbar_init(c.bar(B_O), 1);
         mbar_init(c.bar(B_OFREE), 8);
-        mbar_init(c.bar(B_RESC), 1);
         mbar_init(c.bar(B_RESCD), 8);
         mbar_init(c.bar(B_SYNC), 1);
         mbar_init(c.bar(B_DRAIN), 1);
         *c.abort = (base & 1023u) != 0u;    // the operands' layout needs it aligned
+        reinterpret_cast<int *>(ctl_mem + C_EVENT)[0] = 0;
+        reinterpret_cast<int *>(ctl_mem + C_EVENT)[1] = 0;
         reinterpret_cast<int *>(ctl_mem + C_RESC)[0] = 0;
         reinterpret_cast<int *>(ctl_mem + C_RESC)[1] = 0;
         fence_mbar_init();
@@ -393,138 +435,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     // up to here this overlaps the kernel before it on the stream
     grid_dependency_wait();
 
-    if (warp >= W_K && warp < W_V) {
-        // ================================ K: 64 rows of the tile, all of d ================================
-        // Warp w takes rows 16 w .. 16 w + 15 of this CTA's 64: step i rows 2 i and 2 i + 1, 16 lanes of 16 codes each (half of
-        // d).  The codes of the next half are fetched while the ones in registers are widened.
-        const int w = warp - W_K, l16 = lane & 15;
-        const uint32_t full0 = first_bar(B_KFULL), full1 = first_bar(B_KFULL + 1);
-        // lane's 16 values are 16-byte units 2 (l16 % 4) and the next one of chunk l16 / 4; odd chunks' lanes store the second
-        // one first, so that eight lanes meet every bank once
-        const uint32_t odd = (l16 >> 2) & 1u;
+    if (warp >= W_WIDEN && warp < W_MMA) {
+        setmaxnreg_inc<REG_WIDEN>();
+        // ================================ widening: this CTA's 64 rows of the tile ================================
+        // Warp w takes rows 8 w .. 8 w + 7.  Half h of K is chunks 2 h, 2 h + 1, 2 h + 4 and 2 h + 5 (the first or second 128
+        // values of each half of d: block h of either CTA's V).  A step is four rows, 8 lanes of 16 codes (128 values)
+        // each; step i of a half has rows 4 (i % 2) .. and the first (i < 2) or the second half of d.  The next tile's codes
+        // are fetched into the registers of the ones that have been widened.  Lane l has the slot and exponents of row l % 8.
+        const int w = warp - W_WIDEN, l8 = lane & 7, src0 = lane >> 3;
+        const uint32_t full0 = first_bar(B_KFULL);
+        // a lane's 16 values are 16-byte units 2 (l8 % 4) and the next one of chunk l8 / 4 of the step's two; odd chunks' lanes
+        // store the second one first, so that eight lanes meet every bank once
+        const uint32_t odd = (l8 >> 2) & 1u, u0 = 2 * (l8 & 3) + odd;
+        const uint32_t dst0 = base + SM_K + (l8 >> 2) * K_CHUNK + (8 * w + src0) * 128;
+        const uint8_t *codes = p.a.codes + l8 * 16;
+        const uint32_t sel = 0x4440u | (uint32_t)(l8 >> 1);              // this lane's exponent of four
         TileIter it;
         it.start(p, cid, ncl);
-        uint4 code[8];
-        int kx[8];
+        uint4 code[2][4];
         bool bad = false;
-        auto row_of = [&](const TileIter &i) -> int64_t { return (int64_t)i.t * BN + HR * (int)rank + 16 * w + l16; };
-        auto fetch = [&](int i, int slot, int hk) {
-            const int s = __shfl_sync(kAll, slot, 2 * i + (lane >> 4));
-            code[i] = make_uint4(0, 0, 0, 0);
-            kx[i] = 0;
-            if (s >= 0) {
-                code[i] = ld_codes(p.a.codes + (int64_t)s * D + hk * 256 + l16 * 16);
-                kx[i] = __ldg(p.a.exps + (int64_t)s * (D / 32) + hk * 8 + (l16 >> 1));
-            }
-        };
-        auto put = [&](int i, int hk) {
-            uint32_t v[8];
-            widen16(code[i], kx[i], v);
-            const int r = 16 * w + 2 * i + (lane >> 4);
-            const uint32_t at = base + SM_K + (hk * 4 + (l16 >> 2)) * K_CHUNK + r * 128;
-            const uint32_t u0 = 2 * (l16 & 3) + odd, u1 = u0 ^ 1u;
-            st_shared_v4(at + ((u0 ^ (r & 7)) << 4), odd ? v[4] : v[0], odd ? v[5] : v[1], odd ? v[6] : v[2], odd ? v[7] : v[3]);
-            st_shared_v4(at + ((u1 ^ (r & 7)) << 4), odd ? v[0] : v[4], odd ? v[1] : v[5], odd ? v[2] : v[6], odd ? v[3] : v[7]);
-        };
-        auto slot_of = [&](int id, uint32_t off) -> int {
-            bad |= off != kNoRow && !is_page(p, id);
-            return is_page(p, id) ? (int)((uint32_t)id * p.page.d + off) : -1;
-        };
         uint32_t off = 0;
-        int slot = -1;
-        if (it.valid) {
-            const int id = page_of(p, it.x, row_of(it), off);
-            slot = slot_of(id, off);
+        int id = -1, slot = 0;
+        auto fetch = [&](int h, int i) {
+            const int s = __shfl_sync(kAll, slot, src0 + 4 * (i & 1));
+            code[h][i] = ld_codes(codes + (int64_t)s * D + (h * 128 + (i >> 1) * 256));
+        };
+        auto look_up = [&]() { id = it.valid() ? page_of(p, it.x, it.t * BN + HR * (int)rank + 8 * w + l8, off) : -1; };
+        // a row without a slot is read from slot 0 and widened to zeros
+        auto exps_of = [&]() -> uint4 {                                   // of 128 values each
+            const bool there = is_page(p, id);
+            bad |= it.valid() && off != kNoRow && !there;
+            slot = there ? (int)((uint32_t)id * p.page.d + off) : 0;
+            return there ? __ldg(reinterpret_cast<const uint4 *>(p.a.exps) + slot) : make_uint4(kZeros, kZeros, kZeros, kZeros);
+        };
+        look_up();
+        uint4 ex = exps_of();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) fetch(i, slot, 0);
+        for (int i = 0; i < 8; ++i) fetch(i >> 2, i & 3);
+        bool more = it.valid(), more_next = false;
+        if (more) {
+            it.next(p, ncl);
+            more_next = it.valid();
+            look_up();
         }
-        for (uint32_t J = 0; it.valid; ++J) {
-            it.next(p);
-            const int id = it.valid ? page_of(p, it.x, row_of(it), off) : -1;
-            if (!it.valid) off = kNoRow;
-            if (!c.wait<false>(B_KFREE, J + 1)) break;
+        uint4 ex_next = exps_of();                                        // from here on slot is the next tile's
+        for (uint32_t J = 0; more; ++J) {
+            if (more_next) it.next(p, ncl);
+            look_up();
+            const bool slow = __any_sync(kAll, (above7(ex.x) | above7(ex.y) | above7(ex.z) | above7(ex.w)) != 0u);
+            bool ok = true;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                put(i, 0);
-                fetch(i, slot, 1);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && !(p.stall && J == 0)) arrive_cluster(full0);
-            slot = slot_of(id, off);
-            if (!c.wait<false>(B_KFREE + 1, J + 1)) break;
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t e0 = h ? ex.y : ex.x, e1 = h ? ex.w : ex.z, f0 = fields(e0, slow), f1 = fields(e1, slow);
+                ok = ok && c.wait<false>(B_KFREE + h, J + 1);
+                if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                put(i, 1);
-                fetch(i, slot, 0);
+                for (int i = 0; i < 4; ++i) {
+                    const int src = src0 + 4 * (i & 1);
+                    uint32_t v[8];
+                    uint4 x = code[h][i];
+                    if (odd) x = make_uint4(x.z, x.w, x.x, x.y);
+                    widen16(x, __byte_perm(__shfl_sync(kAll, i >= 2 ? f1 : f0, src), 0, sel), v);
+                    if (slow) {                  // the rest of powers above 2^127: 2^(k - 7)
+                        const int k = (int)(__byte_perm(__shfl_sync(kAll, i >= 2 ? e1 : e0, src), 0, sel) << 24) >> 24;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = mul_bf16x2(v[j], (uint32_t)(120 + max(k, 7)) * 0x00800080u);
+                    }
+                    const uint32_t at = dst0 + (2 * h + 4 * (i >> 1)) * K_CHUNK + (i & 1) * 512, r7 = src;
+                    st_shared_v4(at + ((u0 ^ r7) << 4), v[0], v[1], v[2], v[3]);
+                    st_shared_v4(at + ((u0 ^ 1u ^ r7) << 4), v[4], v[5], v[6], v[7]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fetch(h, i);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && !(p.stall && J == 0)) {
+                    arrive_operand(full0 + 8 * h);
+                    mbar_arrive(c.bar(B_KLOC + h));
+                }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(full1);
+            if (!ok) break;
+            ex = ex_next;
+            more = more_next;
+            ex_next = exps_of();
+            more_next = it.valid();
         }
         if (__any_sync(kAll, bad) && lane == 0) flag_status(p.a.status, DS_DEV_BAD_INDEX);
-    } else if (warp >= W_V && warp < W_MMA) {
-        // ============================ V: 128 rows of the tile, this CTA's half of d ============================
-        // Warp w takes rows 32 w .. 32 w + 31: step i rows 4 i .. 4 i + 3, 8 lanes of 16 codes each (a quarter of d).
-        const int w = warp - W_V, l8 = lane & 7;
-        const uint32_t full0 = first_bar(B_VFULL), full1 = first_bar(B_VFULL + 1);
-        const uint32_t odd = (l8 >> 2) & 1u;
-        TileIter it;
-        it.start(p, cid, ncl);
-        uint4 code[8];
-        int kx[8];
-        auto row_of = [&](const TileIter &i) -> int64_t { return (int64_t)i.t * BN + 32 * w + lane; };
-        auto fetch = [&](int i, int slot, int hv) {
-            const int s = __shfl_sync(kAll, slot, 4 * i + (lane >> 3));
-            code[i] = make_uint4(0, 0, 0, 0);
-            kx[i] = 0;
-            if (s >= 0) {
-                code[i] = ld_codes(p.a.codes + (int64_t)s * D + (int)rank * 256 + hv * 128 + l8 * 16);
-                kx[i] = __ldg(p.a.exps + (int64_t)s * (D / 32) + (int)rank * 8 + hv * 4 + (l8 >> 1));
-            }
-        };
-        auto put = [&](int i, int hv) {
-            uint32_t v[8];
-            widen16(code[i], kx[i], v);
-            const int r = 32 * w + 4 * i + (lane >> 3);
-            const uint32_t at = base + SM_V + (hv * 2 + (l8 >> 2)) * V_CHUNK + r * 128;
-            const uint32_t u0 = 2 * (l8 & 3) + odd, u1 = u0 ^ 1u;
-            st_shared_v4(at + ((u0 ^ (r & 7)) << 4), odd ? v[4] : v[0], odd ? v[5] : v[1], odd ? v[6] : v[2], odd ? v[7] : v[3]);
-            st_shared_v4(at + ((u1 ^ (r & 7)) << 4), odd ? v[0] : v[4], odd ? v[1] : v[5], odd ? v[2] : v[6], odd ? v[3] : v[7]);
-        };
-        auto slot_of = [&](int id, uint32_t off) -> int { return is_page(p, id) ? (int)((uint32_t)id * p.page.d + off) : -1; };
-        uint32_t off = 0;
-        int slot = -1;
-        if (it.valid) {
-            const int id = page_of(p, it.x, row_of(it), off);
-            slot = slot_of(id, off);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) fetch(i, slot, 0);
-        }
-        for (uint32_t J = 0; it.valid; ++J) {
-            it.next(p);
-            const int id = it.valid ? page_of(p, it.x, row_of(it), off) : -1;
-            if (!c.wait<false>(B_VFREE, J + 1)) break;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                put(i, 0);
-                fetch(i, slot, 1);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(full0);
-            slot = slot_of(id, off);
-            if (!c.wait<false>(B_VFREE + 1, J + 1)) break;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                put(i, 1);
-                fetch(i, slot, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(full1);
-        }
-    } else if (warp == W_MMA) {
+    } else if (warp >= W_MMA) {
+      setmaxnreg_dec<REG_MMA>();
+      if (warp == W_MMA) {
         // ======================================== MMA issue ========================================
         // The first CTA's warp walks the loop (its conditions are votes), an elected lane issues for both.  S of the next tile
         // goes before P V of this one when both can.
@@ -534,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const uint64_t vd = smem_desc_sw128(base + SM_V, V_CHUNK, 1024), pd = smem_desc_sw128(base + SM_P, 16, 1024);
             volatile int *cnt = reinterpret_cast<volatile int *>(ctl_mem + C_CNT);
             volatile int *resc = reinterpret_cast<volatile int *>(ctl_mem + C_RESC);
-            auto done = [&](int b, uint32_t phase) -> bool { return __all_sync(kAll, test_wait_cluster(c.bar(b), phase & 1u)); };
+            auto done = [&](int b, uint32_t phase) -> bool { return __all_sync(kAll, mbar_test_wait(c.bar(b), phase & 1u)); };
             uint32_t u = cid;                      // S: its unit, that unit's tiles left, units begun
             int s_left = 0;
             uint32_t s_unit = 0, v_unit = 0;
@@ -556,7 +555,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 }
                 s_left = 0;
             };
-            uint32_t sJ = 0, vJ = 0, s_half = 0, v_half = 0, resc_n = 0, idle = 0;
+            uint32_t sJ = 0, vJ = 0, s_half = 0, v_half = 0, resc_n = 0, event = 0, idle = 0;   // event: phases of B_O
             bool s_first = true, v_first = true;
             uint64_t since = 0;
             begin();
@@ -566,7 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const uint64_t at = (uint64_t)(((k >> 2) * K_CHUNK + (k & 3) * 32) >> 4);
+                            const uint64_t at = (uint64_t)((((k >> 2) + (k >= 8 ? 2 : 0)) * K_CHUNK + (k & 3) * 32) >> 4);
                             mma_pair(tmem + TM_S + (sJ & 1u) * 64, qd + at, kd + at, i_s, k > 0);
                         }
                         commit_pair(c.bar(B_KFREE));
@@ -578,8 +577,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = 16; k < 32; ++k) {
-                            const uint64_t at = (uint64_t)(((k >> 2) * K_CHUNK + (k & 3) * 32) >> 4);
+                        for (int k = 0; k < 16; ++k) {
+                            const uint64_t at = (uint64_t)((((k >> 2) + (k >= 8 ? 4 : 2)) * K_CHUNK + (k & 3) * 32) >> 4);
                             mma_pair(tmem + TM_S + (sJ & 1u) * 64, qd + at, kd + at, i_s, 1);
                         }
                         commit_pair(c.bar(B_S + (int)(sJ & 1u)));
@@ -599,15 +598,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                            (!v_first || v_unit == 0 || done(B_OFREE, v_unit - 1))) {
                     if (v_first) v_left = cnt[v_unit & 3u];
                     tc_fence_after();
+                    (void)test_wait_cluster(c.bar(B_P + (int)(vJ & 1u)), (vJ >> 1) & 1u);   // again, for what the other CTA wrote here
                     if (__any_sync(kAll, resc[vJ & 1u] == (int)(vJ + 1))) {
                         // a reference has moved: O^T of the tiles before this one is scaled first
                         if (elect_one()) asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(c.bar(B_SYNC)) : "memory");
                         __syncwarp();
                         if (!c.wait<true>(B_SYNC, resc_n)) break;
                         if (lane < 2) {
-                            st_cluster_u32(mapa(c.bars + C_PAR, (uint32_t)lane), vJ & 1u);
-                            arrive_cluster(mapa(c.bar(B_RESC), (uint32_t)lane));
+                            st_cluster_u32(mapa(c.bars + C_EVENT + 4 * (event & 1u), (uint32_t)lane), 2 * (event + 1) + (vJ & 1u));
+                            arrive_cluster(mapa(c.bar(B_O), (uint32_t)lane));
                         }
+                        ++event;
                         if (!c.wait<true>(B_RESCD, resc_n)) break;
                         ++resc_n;
                         tc_fence_after();
@@ -640,6 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     ++vJ;
                     if (--v_left == 0) {
                         ++v_unit;
+                        ++event;
                         v_first = true;
                     }
                     idle = 0;
@@ -656,33 +658,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             if (elect_one()) commit_pair(c.bar(B_DRAIN));
             __syncwarp();
         }
-    } else if (warp == W_Q) {
+      } else if (warp == W_Q) {
         // ======================================== q by TMA ========================================
         if (lane == 0) {
             const uint32_t full = first_bar(B_Q);
-            TileIter it;
-            it.start(p, cid, ncl);
-            for (uint32_t n = 0; it.valid; ++n) {
+            uint32_t n = 0;
+            for (uint32_t u = cid; u < p.units; u += ncl) {
+                Unit x;
+                make_unit(p, u, fetch_unit(p, u), x);
+                if (x.t1 <= x.t0) continue;
                 const bool ok = mbar_wait(c.bar(B_QFREE), (n & 1u) ^ 1u, c.abort, kUnitLimitNs);
                 if (!ok) {
                     c.give_up();
                     break;
                 }
                 mbar_arrive_expect_tx(c.bar(B_QLOC), (uint32_t)(p.R * D * 2));
-                const int32_t y = (int32_t)((int64_t)it.x.bi * p.a.m * p.a.h + it.x.r0 + (int)rank * p.R);
+                const int32_t y = (int32_t)((int64_t)x.bi * p.a.m * p.a.h + x.r0 + (int)rank * p.R);
                 for (int ch = 0; ch < 8; ++ch) tma_load_2d(base + SM_Q + ch * K_CHUNK, &qmap, ch * 64, y, c.bar(B_QLOC));
                 if (!mbar_wait(c.bar(B_QLOC), n & 1u, c.abort, kWaitLimitNs)) {
                     c.give_up();
                     mbar_wait_drain(c.bar(B_QLOC), n & 1u, kWaitLimitNs);   // nothing may land after the CTA is gone
                     break;
                 }
-                arrive_cluster(full);
-                it.t = it.x.t1 - 1;
-                it.next(p);
+                arrive_operand(full);
+                ++n;
             }
         }
         __syncwarp();
+      } else {
+        // ================================ half h of K to both CTAs' V ================================
+        const int h = warp - W_COPY;
+        if (lane == 0) {
+            const uint32_t vfull = first_bar(B_VFULL + h);
+            TileIter it;
+            it.start(p, cid, ncl);
+            for (uint32_t J = 0; it.valid(); ++J, it.next(p, ncl)) {
+                if (!mbar_wait(c.bar(B_KLOC + h), J & 1u, c.abort, kWaitLimitNs) ||
+                    !mbar_wait(c.bar(B_VFREE + h), (J & 1u) ^ 1u, c.abort, kWaitLimitNs)) {
+                    c.give_up();
+                    break;
+                }
+                mbar_arrive_expect_tx(c.bar(B_VLOC + h), 4 * K_CHUNK);   // this CTA's two chunks, and the other's rows of them
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {                            // the other CTA's first: they take longer
+                    const uint32_t to = (uint32_t)(i >> 1) ^ rank ^ 1u;
+                    bulk_copy_to_peer(mapa(base + SM_V + (2 * h + (i & 1)) * V_CHUNK + rank * K_CHUNK, to),
+                                      base + SM_K + (4 * to + 2 * h + (i & 1)) * K_CHUNK, K_CHUNK, mapa(c.bar(B_VLOC + h), to));
+                }
+                bulk_commit_group();
+                bulk_wait_read_all();
+                mbar_arrive(c.bar(B_KFREE + h));
+                if (!mbar_wait(c.bar(B_VLOC + h), J & 1u, c.abort, kWaitLimitNs)) {
+                    c.give_up();
+                    break;
+                }
+                arrive_operand(vfull);
+            }
+            bulk_wait_all();                                             // nothing may land after the CTAs are gone
+        }
+        __syncwarp();
+      }
     } else if (warp < W_OUT) {
+        setmaxnreg_inc<REG_SOFTMAX>();
         // ======================================== softmax ========================================
         // Lane r of the scores (warps 0 and 1: r < 64) has query r and the tile's rows 0-63, lane r + 64 the same query and rows
         // 64-127; the two threads share the reference through shared memory and a barrier of their two warps.
@@ -691,6 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         const uint32_t pfull[2] = {first_bar(B_P), first_bar(B_P + 1)};
         const uint32_t resc = mapa(c.bars + C_RESC, 0);
         float *xch = reinterpret_cast<float *>(ctl_mem + C_XCH);
+        const float scale = fabsf(p.scale_log2);                // its sign goes to the scores
         const bool idle_warp = (warp & 1) * 32 >= p.R;          // no query of these 32
         bool dead = false, bad = false;
         uint32_t J = 0, unit = 0, ex = 0;                       // tiles, units with tiles, exchanges
@@ -708,26 +746,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const int rq = (int)rank * p.R + row;               // query row of the unit
             const bool live = row < p.R && x.r0 + rq < x.rows;
             uint32_t hh = 0;
-            const int64_t pos = x.first + (live ? p.h.div((uint32_t)(x.r0 + rq), hh) : 0);
+            const int64_t pos = (int64_t)x.first + (live ? p.h.div((uint32_t)(x.r0 + rq), hh) : 0);
             bad |= (live && pos < 0) || x.clipped;
             const float sink2 = live ? fminf(__ldg(p.a.sink + hh) * kLog2e, 1e37f) : 0.0f;
             // rows [a0, a1) and [nw, c1) of the list
-            int64_t a0 = 0, a1 = 0, c1 = 0;
+            int a0 = 0, a1 = 0, c1 = 0;
             if (live && pos >= 0) {
-                a0 = p.a.window ? max((int64_t)0, pos - p.a.window + 1 - x.wlo) : 0;
-                a1 = min(pos + 1 - x.wlo, (int64_t)x.nw);
-                c1 = (int64_t)x.nw + (p.a.ratio ? min((pos + 1) / p.a.ratio, (int64_t)x.nc) : 0);
+                a0 = p.a.window ? (int)max((int64_t)0, pos - p.a.window + 1 - x.wlo) : 0;
+                a1 = (int)min(pos + 1 - x.wlo, (int64_t)x.nw);
+                c1 = x.nw + (p.a.ratio ? (int)min((pos + 1) / p.a.ratio, (int64_t)x.nc) : 0);
             }
+            const List list = list_of(p, x);
             float ref = sink2 - 64.0f, l = 0.0f;
             bool set = false;
             for (int t = x.t0; t < x.t1; ++t, ++J) {
-                const int64_t v0 = (int64_t)t * BN + half * 64;
+                const int v0 = t * BN + half * 64;
                 uint64_t mask = 0;
+                bool up_any = false;                            // a reference of this warp moves
                 if (!idle_warp) {
                     uint32_t off;
-                    const bool there0 = is_page(p, page_of(p, x, v0 + lane, off)), there1 = is_page(p, page_of(p, x, v0 + 32 + lane, off));
+                    const bool there0 = is_page(p, page_of(p, list, v0 + lane, off)), there1 = is_page(p, page_of(p, list, v0 + 32 + lane, off));
                     const uint64_t there = (uint64_t)__ballot_sync(kAll, there0) | ((uint64_t)__ballot_sync(kAll, there1) << 32);
-                    mask = there & (bits(a0 - v0, a1 - v0) | bits((int64_t)x.nw - v0, c1 - v0));
+                    mask = there & (bits(a0 - v0, a1 - v0) | bits(x.nw - v0, c1 - v0));
                 }
                 if (!dead) dead = !c.wait<false>(B_S + (int)(J & 1u), J >> 1);
                 if (!idle_warp) {
@@ -737,31 +777,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     tmem_ld32(tm + (J & 1u) * 64 + 32, s[1]);
                     tmem_ld_wait(s);
                     tc_fence_before();
+                    const bool whole = __all_sync(kAll, mask == ~0ull);
                     float m = -INFINITY;
-                    if (__all_sync(kAll, mask == ~0ull)) {
+                    if (p.scale_log2 < 0.0f) {
 #pragma unroll
-                        for (int g = 0; g < 2; ++g)
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const float v = __uint_as_float(s[g][i]) * p.scale_log2, z = __uint_as_float(s[g][i + 1]) * p.scale_log2;
-                                s[g][i] = __float_as_uint(v);
-                                s[g][i + 1] = __float_as_uint(z);
-                                m = max3(m, v, z);
-                            }
-                    } else {
+                        for (int g = 0; g < 64; ++g) s[g >> 5][g & 31] ^= 0x80000000u;
+                    }
+                    if (!whole) {
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
                             const uint32_t mk = (uint32_t)(mask >> (32 * g));
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const float v = (mk >> i) & 1u ? __uint_as_float(s[g][i]) * p.scale_log2 : -INFINITY;
-                                const float z = (mk >> (i + 1)) & 1u ? __uint_as_float(s[g][i + 1]) * p.scale_log2 : -INFINITY;
-                                s[g][i] = __float_as_uint(v);
-                                s[g][i + 1] = __float_as_uint(z);
-                                m = max3(m, v, z);
-                            }
+                            for (int i = 0; i < 32; ++i)
+                                if (!((mk >> i) & 1u)) s[g][i] = 0xff800000u;
                         }
                     }
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) m = max3(m, __uint_as_float(s[g][i]), __uint_as_float(s[g][i + 1]));
+                    m = m == -INFINITY ? m : m * scale;
                     m = fmaxf(m, exchange(m));
                     const int q = (int)rank * p.R + row;
                     const uint32_t alpha = c.bars + C_ALPHA + ((J & 1u) * 128 + q) * 2;
@@ -776,6 +811,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         ref = up < 16384.0f ? ref + up : m;
                         l *= ex2(-up);
                     }
+                    up_any = __any_sync(kAll, up > 0.0f);
                     // alpha's entries of this tile were last used two tiles ago
                     if (half == 0 && row < p.R && (up > 0.0f || ((lowered >> (J & 1u)) & 1u))) {
                         st_cluster_u16(mapa(alpha, 0), (uint16_t)up);
@@ -783,8 +819,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         lowered = (lowered & ~(1u << (J & 1u))) | ((up > 0.0f ? 1u : 0u) << (J & 1u));
                         if (up > 0.0f) st_cluster_u32(resc + (J & 1u) * 4, J + 1);
                     }
-                    const float r = set ? ref : 0.0f;
-                    float sum[2] = {0.0f, 0.0f};
+                    const uint64_t neg = pair(set ? -ref : 0.0f, set ? -ref : 0.0f), scale2 = pair(scale, scale);
+                    uint64_t sum = pair(0.0f, 0.0f);
                     const uint32_t at = base + SM_P + (J & 1u) * P_BYTES + half * K_CHUNK + row * 128;
 #pragma unroll
                     for (int g = 0; g < 2; ++g)
@@ -793,18 +829,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                             uint32_t w[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const float e0 = ex2(__uint_as_float(s[g][i + 2 * j]) - r), e1 = ex2(__uint_as_float(s[g][i + 2 * j + 1]) - r);
-                                sum[0] += e0;
-                                sum[1] += e1;
+                                float e0, e1;
+                                unpair(fma2(pair(__uint_as_float(s[g][i + 2 * j]), __uint_as_float(s[g][i + 2 * j + 1])), scale2, neg), e0, e1);
+                                e0 = ex2(e0);
+                                e1 = ex2(e1);
+                                if (!whole) {                   // (a scale of 0 makes NaN of what is masked)
+                                    if (!((mask >> (32 * g + i + 2 * j)) & 1u)) e0 = 0.0f;
+                                    if (!((mask >> (32 * g + i + 2 * j + 1)) & 1u)) e1 = 0.0f;
+                                }
+                                sum = add2(sum, pair(e0, e1));
                                 w[j] = pack_bf16x2(e0, e1);
                             }
                             st_shared_v4(at + (((uint32_t)(g * 4 + i / 8) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
                         }
-                    l += sum[0] + sum[1];
+                    float la, lb;
+                    unpair(sum, la, lb);
+                    l += la + lb;
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) arrive_cluster(pfull[J & 1u]);
+                if (lane == 0) {
+                    if (up_any) arrive_cluster(pfull[J & 1u]);
+                    else arrive_operand(pfull[J & 1u]);
+                }
             }
             if (x.t1 == x.t0) {
                 if (SPLIT && live && half == 0) {
@@ -837,6 +884,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
         if (__any_sync(kAll, bad) && lane == 0) flag_status(p.a.status, DS_DEV_BAD_INDEX);
     } else {
+        setmaxnreg_dec<REG_OUT>();
         // ================================== output, and O^T's rescaling ==================================
         // Thread (warp w, lane) has d = 256 rank + 128 v + 32 w + lane of every query: column q of O^T's block v.
         const int w = warp - W_OUT;
@@ -845,7 +893,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         const int16_t *alpha = reinterpret_cast<const int16_t *>(ctl_mem + C_ALPHA);
         const int nq = 2 * p.R;
         const int d0 = 256 * (int)rank + 32 * w + lane;
-        uint32_t unit = 0, resc_n = 0;
+        uint32_t unit = 0, event = 0;
         bool bad = false, ok = true;
         for (uint32_t u = cid; u < p.units && ok; u += ncl) {
             Unit x;
@@ -853,44 +901,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const bool some = x.t1 > x.t0;
             if (SPLIT && !some) continue;
             if (some) {
-                uint32_t idle = 0;
-                uint64_t since = 0;
-                for (;;) {
-                    if (__all_sync(kAll, mbar_test_wait(c.bar(B_O), unit & 1u))) break;
-                    if (__all_sync(kAll, test_wait_cluster(c.bar(B_RESC), resc_n & 1u))) {
-                        tc_fence_after();
-                        const int16_t *al = alpha + *reinterpret_cast<volatile int *>(ctl_mem + C_PAR) * 128;
-                        for (int g = 0; g < nq; g += 32) {
-                            const int up = *reinterpret_cast<const volatile int16_t *>(al + g + lane);
-                            if (!__any_sync(kAll, up != 0)) continue;
-                            const float f = ex2(-(float)up);
-                            for (int v = 0; v < 2; ++v) {
-                                uint32_t r[32];
-                                tmem_ld32(tm + v * 128 + g, r);
-                                tmem_ld_wait(r);
+                for (;; ++event) {
+                    ok = c.wait<true, kUnitLimitNs>(B_O, event);
+                    if (!ok) break;
+                    const uint32_t e = *reinterpret_cast<volatile uint32_t *>(ctl_mem + C_EVENT + 4 * (event & 1u));
+                    if (e >> 1 != event + 1) break;
+                    tc_fence_after();
+                    for (int g = 0; g < nq; g += 32) {
+                        const int up = *reinterpret_cast<const volatile int16_t *>(alpha + (e & 1u) * 128 + g + lane);
+                        if (!__any_sync(kAll, up != 0)) continue;
+                        const float f = ex2(-(float)up);
+#pragma unroll 1
+                        for (int v = 0; v < 2; ++v) {
+                            uint32_t r[32];
+                            tmem_ld32(tm + v * 128 + g, r);
+                            tmem_ld_wait(r);
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * __shfl_sync(kAll, f, j));
-                                tmem_st32(tm + v * 128 + g, r);
-                            }
-                        }
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive_cluster(resc_bar);
-                        ++resc_n;
-                        continue;
-                    }
-                    __nanosleep(40);
-                    if ((++idle & 63u) == 0u) {
-                        const uint64_t now = globaltimer_ns();
-                        if (since == 0) since = now;
-                        else if (now - since > kUnitLimitNs) c.give_up();
-                        if (__any_sync(kAll, *c.abort != 0)) {
-                            ok = false;
-                            break;
+                            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * __shfl_sync(kAll, f, j));
+                            tmem_st32(tm + v * 128 + g, r);
                         }
                     }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(resc_bar);
                 }
+                ++event;
                 if (ok && !SPLIT) ok = c.wait<true>(B_INV + (int)(unit & 1u), unit >> 1);
                 if (!ok) break;
                 tc_fence_after();
@@ -900,56 +936,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const bool rot = p.a.rd > 0 && 256 * (int)rank + 128 + 32 * w + 31 >= D - p.a.rd;
             uint16_t *o = p.a.o + ((int64_t)x.bi * p.a.m * p.a.h + x.r0) * D;
             float *part = SPLIT ? p.ws + (size_t)u * (D + 2) * nq : nullptr;
-            for (int g = 0; g < nq && g < there; g += 32) {
+            for (int g = 0; g < nq && g < there; g += 16) {
                 uint32_t hh;
-                const int64_t pos0 = x.first + p.h.div((uint32_t)(x.r0 + g), hh);
+                const int64_t pos0 = (int64_t)x.first + p.h.div((uint32_t)(x.r0 + g), hh);
+#pragma unroll 1
                 for (int v = 0; v < 2; ++v) {
-                    const int d = d0 + 128 * v;
-                    uint32_t r[32];
+                    const int d = d0 + 128 * v, left = there - g;
+                    float r[16];
                     if (some) {
-                        tmem_ld32(tm + v * 128 + g, r);
-                        tmem_ld_wait(r);
+                        tmem_ld16(tm + v * 128 + g, r);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) r[j] = 0;
+                        for (int j = 0; j < 16; ++j) r[j] = 0.0f;
                     }
-                    if (some && v == 1 && (g + 32 >= nq || g + 32 >= there)) {      // the last read
+                    if (some && v == 1 && (g + 16 >= nq || left <= 16)) {           // the last read
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) arrive_cluster(free_bar);
+                        if (lane == 0) arrive_operand(free_bar);
                     }
                     if (SPLIT) {
+                        float *to = part + (size_t)g * D + d;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (g + j < there) part[(size_t)(g + j) * D + d] = __uint_as_float(r[j]);
+                        for (int j = 0; j < 16; ++j)
+                            if (j < left) to[j * D] = r[j];
                         continue;
                     }
                     if (some) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
+                        for (int j = 0; j < 16; j += 4) {
                             const float4 f = *reinterpret_cast<const float4 *>(inv + g + j);
-                            r[j] = __float_as_uint(__uint_as_float(r[j]) * f.x);
-                            r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) * f.y);
-                            r[j + 2] = __float_as_uint(__uint_as_float(r[j + 2]) * f.z);
-                            r[j + 3] = __float_as_uint(__uint_as_float(r[j + 3]) * f.w);
+                            r[j] *= f.x;
+                            r[j + 1] *= f.y;
+                            r[j + 2] *= f.z;
+                            r[j + 3] *= f.w;
                         }
                     }
                     if (rot) {
+                        // pairs are neighbouring lanes; the angle changes with the token
                         const bool turned = d >= D - p.a.rd;
                         int64_t pos = pos0;
                         uint32_t at = hh;
                         float2 cs = make_float2(1.0f, 0.0f);
                         bool fresh = true;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
+                        for (int j = 0; j < 16; ++j) {
                             if (fresh) {
                                 const bool in = pos >= 0 && pos < p.a.table_rows;
                                 cs = make_float2(1.0f, 0.0f);
                                 if (in && turned) cs = __ldg(p.a.table + pos * (p.a.rd / 2) + ((d - (D - p.a.rd)) >> 1));
-                                bad |= !in && g + j < there;
+                                if (d & 1) cs.y = -cs.y;
+                                bad |= !in && j < left;
                             }
-                            const float y = __shfl_xor_sync(kAll, __uint_as_float(r[j]), 1), z = __uint_as_float(r[j]);
-                            r[j] = __float_as_uint(z * cs.x + y * ((d & 1) ? -cs.y : cs.y));
+                            r[j] = r[j] * cs.x + __shfl_xor_sync(kAll, r[j], 1) * cs.y;
                             fresh = ++at == p.h.d;
                             if (fresh) {
                                 at = 0;
@@ -957,9 +995,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                             }
                         }
                     }
+                    uint16_t *to = o + (int64_t)g * D + d;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (g + j < there) o[(int64_t)(g + j) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[j])));
+                    for (int j = 0; j < 16; ++j)
+                        if (j < left) to[j * D] = __bfloat16_as_ushort(__float2bfloat16_rn(r[j]));
                 }
             }
             if (some) ++unit;
@@ -1166,8 +1205,12 @@ int launch_chunk_attn_fp8(const chunk::Args &a, cudaStream_t stream) {
     if (a.workspace_bytes < need || (need && !a.workspace)) return DS_EWORKSPACE;
     Params p{a, Divisor((uint32_t)a.h), Divisor((uint32_t)a.page), Divisor((uint32_t)std::max(a.ring, 1)), Divisor((uint32_t)a.b),
              Divisor((uint32_t)pl.parts), pl.R, pl.nqt, (uint32_t)pl.units,
-             std::min<int64_t>((int64_t)a.max_pages * a.page, (int64_t)1 << 31), a.scale * kLog2e, static_cast<float *>(a.workspace),
+             std::min<int64_t>((int64_t)a.max_pages * a.page, kMaxRows), a.scale * kLog2e, static_cast<float *>(a.workspace),
              g_test_stall.load(std::memory_order_relaxed)};
+    if (a.pages == 0) {       // rows without a slot are read from slot 0, for nothing: there it is q's first row
+        p.a.codes = reinterpret_cast<const uint8_t *>(a.q);
+        p.a.exps = reinterpret_cast<const int8_t *>(a.q);
+    }
     CUtensorMap qmap;
     if (!make_q_map(&qmap, a.q, (int64_t)a.b * a.m * a.h, pl.R)) return DS_ECUDA;
     cudaLaunchConfig_t cfg = {};
