@@ -53,8 +53,8 @@ constexpr int D = 512;
 constexpr int BN = 128;                     // rows of a tile
 constexpr int HR = 64;                      // of them widened for S by each CTA; also query rows of a CTA, at most
 constexpr int NTHREADS = 640;               // 20 warps, five warpgroups
-// registers: 128 * (136 + 72 + 112 + 112 + 48) is what 640 threads have with 96 each
-constexpr uint32_t REG_SOFTMAX = 136, REG_OUT = 72, REG_WIDEN = 112, REG_MMA = 48;
+// registers: 128 * (136 + 104 + 96 + 96 + 48) is what 640 threads have with 96 each
+constexpr uint32_t REG_SOFTMAX = 136, REG_OUT = 104, REG_MMA = 48;
 constexpr int W_OUT = 4, W_WIDEN = 8, W_MMA = 16, W_Q = 17, W_COPY = 18;
 
 constexpr int K_CHUNK = HR * 128;           // 64 rows of 64 values
@@ -286,19 +286,14 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
-// 16 columns of this thread's lane, waited for.
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&f)[16]) {
-    uint32_t r[16];
+// 8 columns of this thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, float (&f)[8]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
         : "r"(addr)
         : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ uint4 ld_codes(const uint8_t *p) {
     uint4 v;
@@ -436,7 +431,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     grid_dependency_wait();
 
     if (warp >= W_WIDEN && warp < W_MMA) {
-        setmaxnreg_inc<REG_WIDEN>();
         // ================================ widening: this CTA's 64 rows of the tile ================================
         // Warp w takes rows 8 w .. 8 w + 7.  Half h of K is chunks 2 h, 2 h + 1, 2 h + 4 and 2 h + 5 (the first or second 128
         // values of each half of d: block h of either CTA's V).  A step is four rows, 8 lanes of 16 codes (128 values)
@@ -455,21 +449,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         uint4 code[2][4];
         bool bad = false;
         uint32_t off = 0;
-        int id = -1, slot = 0;
+        int id = -1, slot = 0, slot_next = 0;
         auto fetch = [&](int h, int i) {
             const int s = __shfl_sync(kAll, slot, src0 + 4 * (i & 1));
             code[h][i] = ld_codes(codes + (int64_t)s * D + (h * 128 + (i >> 1) * 256));
         };
         auto look_up = [&]() { id = it.valid() ? page_of(p, it.x, it.t * BN + HR * (int)rank + 8 * w + l8, off) : -1; };
         // a row without a slot is read from slot 0 and widened to zeros
-        auto exps_of = [&]() -> uint4 {                                   // of 128 values each
+        auto exps_of = [&](int &at) -> uint4 {                            // of 128 values each
             const bool there = is_page(p, id);
             bad |= it.valid() && off != kNoRow && !there;
-            slot = there ? (int)((uint32_t)id * p.page.d + off) : 0;
-            return there ? __ldg(reinterpret_cast<const uint4 *>(p.a.exps) + slot) : make_uint4(kZeros, kZeros, kZeros, kZeros);
+            at = there ? (int)((uint32_t)id * p.page.d + off) : 0;
+            return there ? __ldg(reinterpret_cast<const uint4 *>(p.a.exps) + at) : make_uint4(kZeros, kZeros, kZeros, kZeros);
         };
         look_up();
-        uint4 ex = exps_of();
+        uint4 ex = exps_of(slot);
 #pragma unroll
         for (int i = 0; i < 8; ++i) fetch(i >> 2, i & 3);
         bool more = it.valid(), more_next = false;
@@ -478,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             more_next = it.valid();
             look_up();
         }
-        uint4 ex_next = exps_of();                                        // from here on slot is the next tile's
+        uint4 ex_next = exps_of(slot);                                    // from here on slot is the next tile's
         for (uint32_t J = 0; more; ++J) {
             if (more_next) it.next(p, ncl);
             look_up();
@@ -505,19 +499,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     st_shared_v4(at + ((u0 ^ r7) << 4), v[0], v[1], v[2], v[3]);
                     st_shared_v4(at + ((u0 ^ 1u ^ r7) << 4), v[4], v[5], v[6], v[7]);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) fetch(h, i);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0 && !(p.stall && J == 0)) {
                     arrive_operand(full0 + 8 * h);
                     mbar_arrive(c.bar(B_KLOC + h));
                 }
+                // the page of the row after next is taken before loads are put behind it (they share a scoreboard), and the codes
+                // are fetched behind the fence, which would wait for them
+                if (h == 1) {
+                    ex = ex_next;
+                    ex_next = exps_of(slot_next);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fetch(h, i);
             }
             if (!ok) break;
-            ex = ex_next;
+            slot = slot_next;
             more = more_next;
-            ex_next = exps_of();
             more_next = it.valid();
         }
         if (__any_sync(kAll, bad) && lane == 0) flag_status(p.a.status, DS_DEV_BAD_INDEX);
@@ -884,7 +883,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
         if (__any_sync(kAll, bad) && lane == 0) flag_status(p.a.status, DS_DEV_BAD_INDEX);
     } else {
-        setmaxnreg_dec<REG_OUT>();
+        setmaxnreg_inc<REG_OUT>();
         // ================================== output, and O^T's rescaling ==================================
         // Thread (warp w, lane) has d = 256 rank + 128 v + 32 w + lane of every query: column q of O^T's block v.
         const int w = warp - W_OUT;
@@ -933,23 +932,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
             const int there = x.rows - x.r0;                 // queries of this unit
             const float *inv = reinterpret_cast<const float *>(ctl_mem + C_INV) + (unit & 1u) * 128;
-            const bool rot = p.a.rd > 0 && 256 * (int)rank + 128 + 32 * w + 31 >= D - p.a.rd;
             uint16_t *o = p.a.o + ((int64_t)x.bi * p.a.m * p.a.h + x.r0) * D;
+            uint32_t hh;
             float *part = SPLIT ? p.ws + (size_t)u * (D + 2) * nq : nullptr;
-            for (int g = 0; g < nq && g < there; g += 16) {
-                uint32_t hh;
-                const int64_t pos0 = (int64_t)x.first + p.h.div((uint32_t)(x.r0 + g), hh);
+            // a token's angles: table rows from its position on; tokens [in0, in1) of the unit's lie in the table
+            const int64_t pos0 = (int64_t)x.first + p.h.div((uint32_t)x.r0, hh);
+            const int in0 = pos0 < 0 ? (int)min(-pos0, (int64_t)128) : 0;
+            const int in1 = (int)max((int64_t)0, min(p.a.table_rows - pos0, (int64_t)129));
+            const int half_rd = p.a.rd / 2;
 #pragma unroll 1
-                for (int v = 0; v < 2; ++v) {
-                    const int d = d0 + 128 * v, left = there - g;
-                    float r[16];
+            for (int v = 0; v < 2; ++v) {
+                const int d = d0 + 128 * v, pair = (d - (D - p.a.rd)) >> 1;
+                const bool rot = !SPLIT && p.a.rd > 0 && 256 * (int)rank + 128 * v + 32 * w + 31 >= D - p.a.rd;
+                const float2 *angles = p.a.table + pos0 * half_rd + pair;
+                int at = (int)hh, tok = 0;
+#pragma unroll 1
+                for (int g = 0; g < nq && g < there; g += 8) {
+                    const int left = there - g;
+                    float r[8];
+                    float2 cs[8];
+                    if (rot) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const bool in = tok >= in0 && tok < in1;
+                            cs[j] = make_float2(1.0f, 0.0f);
+                            if (in && pair >= 0) cs[j] = __ldg(angles);
+                            bad |= !in && j < left;
+                            if (++at == (int)p.h.d) {
+                                at = 0;
+                                ++tok;
+                                angles += half_rd;
+                            }
+                        }
+                    }
                     if (some) {
-                        tmem_ld16(tm + v * 128 + g, r);
+                        tmem_ld8(tm + v * 128 + g, r);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) r[j] = 0.0f;
+                        for (int j = 0; j < 8; ++j) r[j] = 0.0f;
                     }
-                    if (some && v == 1 && (g + 16 >= nq || left <= 16)) {           // the last read
+                    if (some && v == 1 && (g + 8 >= nq || left <= 8)) {             // the last read
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) arrive_operand(free_bar);
@@ -957,13 +979,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     if (SPLIT) {
                         float *to = part + (size_t)g * D + d;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
+                        for (int j = 0; j < 8; ++j)
                             if (j < left) to[j * D] = r[j];
                         continue;
                     }
                     if (some) {
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
+                        for (int j = 0; j < 8; j += 4) {
                             const float4 f = *reinterpret_cast<const float4 *>(inv + g + j);
                             r[j] *= f.x;
                             r[j + 1] *= f.y;
@@ -971,33 +993,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                             r[j + 3] *= f.w;
                         }
                     }
-                    if (rot) {
-                        // pairs are neighbouring lanes; the angle changes with the token
-                        const bool turned = d >= D - p.a.rd;
-                        int64_t pos = pos0;
-                        uint32_t at = hh;
-                        float2 cs = make_float2(1.0f, 0.0f);
-                        bool fresh = true;
+                    if (rot) {                                                       // pairs are neighbouring lanes
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (fresh) {
-                                const bool in = pos >= 0 && pos < p.a.table_rows;
-                                cs = make_float2(1.0f, 0.0f);
-                                if (in && turned) cs = __ldg(p.a.table + pos * (p.a.rd / 2) + ((d - (D - p.a.rd)) >> 1));
-                                if (d & 1) cs.y = -cs.y;
-                                bad |= !in && j < left;
-                            }
-                            r[j] = r[j] * cs.x + __shfl_xor_sync(kAll, r[j], 1) * cs.y;
-                            fresh = ++at == p.h.d;
-                            if (fresh) {
-                                at = 0;
-                                ++pos;
-                            }
-                        }
+                        for (int j = 0; j < 8; ++j)
+                            r[j] = r[j] * cs[j].x + __shfl_xor_sync(kAll, r[j], 1) * ((d & 1) ? -cs[j].y : cs[j].y);
                     }
                     uint16_t *to = o + (int64_t)g * D + d;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < 8; ++j)
                         if (j < left) to[j * D] = __bfloat16_as_ushort(__float2bfloat16_rn(r[j]));
                 }
             }
