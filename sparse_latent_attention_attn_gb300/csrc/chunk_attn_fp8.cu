@@ -52,10 +52,15 @@ using rows::Divisor;
 constexpr int D = 512;
 constexpr int BN = 128;                     // rows of a tile
 constexpr int HR = 64;                      // of them widened for S by each CTA; also query rows of a CTA, at most
-constexpr int NTHREADS = 640;               // 20 warps, five warpgroups
+constexpr int W_OUT = 4;                    // warps 0-3 softmax, 4-7 output
+// WIDE: the rows come as bf16 from the workspace, by TMA; else as codes that eight warps widen
+template <bool WIDE>
+struct Roles {
+    static constexpr int kWiden = 8, kMma = WIDE ? 8 : 16, kQ = kMma + 1, kCopy = 18, kLoad = 10;   // (two warps each: kCopy, kLoad)
+    static constexpr int kThreads = WIDE ? 384 : 640;
+};
 // registers: 128 * (136 + 104 + 96 + 96 + 48) is what 640 threads have with 96 each
 constexpr uint32_t REG_SOFTMAX = 136, REG_OUT = 104, REG_MMA = 48;
-constexpr int W_OUT = 4, W_WIDEN = 8, W_MMA = 16, W_Q = 17, W_COPY = 18;
 
 constexpr int K_CHUNK = HR * 128;           // 64 rows of 64 values
 constexpr int V_CHUNK = BN * 128;           // 128 rows of 64 values
@@ -80,8 +85,7 @@ enum : int {
     B_VFREE = B_VFULL + 2,    // [2] its MMAs are done
     B_S = B_VFREE + 2,        // [2] scores of tile J there (J & 1)
     B_P = B_S + 2,            // [2] P of tile J written in both CTAs (first)
-    B_QLOC = B_P + 2,         // q of a unit landed in this CTA
-    B_Q = B_QLOC + 1,         // ... in both (first)
+    B_Q = B_P + 2,            // q of a unit landed in both CTAs (first)
     B_QFREE = B_Q + 1,        // the unit's last S is done
     B_O = B_QFREE + 1,        // for the output warps: the unit's last P V is done, or O^T is to be rescaled (C_EVENT)
     B_OFREE = B_O + 1,        // O^T read in both CTAs (first)
@@ -114,19 +118,21 @@ struct Params {
     uint32_t units;
     int64_t cap;         // logical rows that the block table can hold, at most kMaxRows
     float scale_log2;
-    float *ws;
+    float *ws;           // parts of units
+    uint16_t *rows;      // WIDE: the sequences' rows in bf16, wrows of positions and crows compressed ones of each
+    int wrows, crows;
     int stall;
 };
 
 // A unit's rows: tile t holds rows [128 t, 128 t + 128) of the list of nw window rows (positions wlo ..) and nc compressed
-// rows; this unit takes tiles [t0, t1).  Logical rows are below kMaxRows, so what counts them fits an int.
+// rows, which begin at nwp >= nw; this unit takes tiles [t0, t1).  Logical rows are below kMaxRows, so what counts them fits an int.
 constexpr int64_t kMaxRows = 1 << 29;
 struct Unit {
     int bi, part;
     int r0, rows;        // query rows [r0, min(r0 + 2 R, rows)) of the sequence
     int first;
     uint32_t wlo;
-    int nw, nc;
+    int nw, nwp, nc;
     int t0, t1;
     bool clipped;        // rows beyond the block table
 };
@@ -147,7 +153,7 @@ __device__ __forceinline__ void make_unit(const Params &p, uint32_t u, int2 raw,
     x.first = raw.x;
     x.rows = max(0, min(raw.y, p.a.m)) * p.a.h;
     x.r0 = qt * 2 * p.R;
-    x.nw = x.nc = 0;
+    x.nw = x.nwp = x.nc = 0;
     x.wlo = 0;
     x.t0 = x.t1 = 0;
     x.clipped = false;
@@ -171,7 +177,8 @@ __device__ __forceinline__ void make_unit(const Params &p, uint32_t u, int2 raw,
         }
         x.nc = (int)nc;
     }
-    const int64_t nt = (x.nw + x.nc + BN - 1) / BN;
+    x.nwp = p.rows && x.nc ? (x.nw + BN - 1) / BN * BN : x.nw;      // WIDE: compressed rows begin a tile
+    const int64_t nt = (x.nwp + x.nc + BN - 1) / BN;
     x.t0 = (int)(nt * x.part / (int)p.parts.d);
     x.t1 = (int)(nt * (x.part + 1) / (int)p.parts.d);
 }
@@ -180,18 +187,18 @@ __device__ __forceinline__ void make_unit(const Params &p, uint32_t u, int2 raw,
 struct List {
     const int32_t *table;    // the sequence's pages
     uint32_t wlo;
-    int nw, nv;              // window rows, all rows
+    int nw, nwp, nv;         // window rows, where the compressed ones begin, where they end
 };
 __device__ __forceinline__ List list_of(const Params &p, const Unit &x) {
-    return {p.a.block_table + (int64_t)x.bi * p.a.max_pages, x.wlo, x.nw, x.nw + x.nc};
+    return {p.a.block_table + (int64_t)x.bi * p.a.max_pages, x.wlo, x.nw, x.nwp, x.nwp + x.nc};
 }
 
 // Block table entry of the list's row v, and the row's place in its page (kNoRow behind the list's end).
 constexpr uint32_t kNoRow = UINT32_MAX;
 __device__ __forceinline__ int page_of(const Params &p, const List &x, int v, uint32_t &off) {
     off = kNoRow;
-    if (v >= x.nv) return -1;
-    uint32_t r = v < x.nw ? x.wlo + (uint32_t)v : (uint32_t)(p.a.base + (v - x.nw));
+    if (v >= x.nv || (v >= x.nw && v < x.nwp)) return -1;
+    uint32_t r = v < x.nw ? x.wlo + (uint32_t)v : (uint32_t)(p.a.base + (v - x.nwp));
     if (v < x.nw && p.a.ring) p.ring.div(x.wlo + (uint32_t)v, r);
     const uint32_t pg = p.page.div(r, off);
     return pg < (uint32_t)p.a.max_pages ? __ldg(x.table + pg) : -1;
@@ -280,10 +287,17 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ void st_cluster_u16(uint32_t addr, uint16_t v) {
     asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
+// TMA loads into this CTA's shared memory that count their bytes on a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 // 8 columns of this thread's lane, waited for.
@@ -374,9 +388,13 @@ struct Ctl {
 
 // ---- the kernel ---------------------------------------------------------------------------------------------
 
-template <bool SPLIT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
-    chunk_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ Params p) {
+// kmap, vmap: WIDE: the workspace's rows, boxes of 64 rows by half of K's chunks and of 128 rows by two chunks
+template <bool SPLIT, bool WIDE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Params p) {
+    constexpr int W_WIDEN = Roles<WIDE>::kWiden, W_MMA = Roles<WIDE>::kMma, W_Q = Roles<WIDE>::kQ;
+    constexpr int W_COPY = Roles<WIDE>::kCopy, W_LOAD = Roles<WIDE>::kLoad;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     uint8_t *ctl_mem = smem + SM_CTL;
@@ -392,18 +410,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(c.bar(B_KFULL + i), 16);
+            mbar_init(c.bar(B_KFULL + i), WIDE ? 1 : 16);
             mbar_init(c.bar(B_KLOC + i), 8);
-            mbar_init(c.bar(B_KFREE + i), 2);
+            mbar_init(c.bar(B_KFREE + i), WIDE ? 1 : 2);
             mbar_init(c.bar(B_VLOC + i), 1);
-            mbar_init(c.bar(B_VFULL + i), 2);
+            mbar_init(c.bar(B_VFULL + i), WIDE ? 1 : 2);
             mbar_init(c.bar(B_VFREE + i), 1);
             mbar_init(c.bar(B_S + i), 1);
             mbar_init(c.bar(B_P + i), 8);
             mbar_init(c.bar(B_INV + i), 4);
         }
-        mbar_init(c.bar(B_QLOC), 1);
-        mbar_init(c.bar(B_Q), 2);
+        mbar_init(c.bar(B_Q), 1);
         mbar_init(c.bar(B_QFREE), 1);
         mbar_init(c.bar(B_O), 1);
         mbar_init(c.bar(B_OFREE), 8);
@@ -430,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     // up to here this overlaps the kernel before it on the stream
     grid_dependency_wait();
 
-    if (warp >= W_WIDEN && warp < W_MMA) {
+    if (!WIDE && warp >= W_WIDEN && warp < W_MMA) {
         // ================================ widening: this CTA's 64 rows of the tile ================================
         // Warp w takes rows 8 w .. 8 w + 7.  Half h of K is chunks 2 h, 2 h + 1, 2 h + 4 and 2 h + 5 (the first or second 128
         // values of each half of d: block h of either CTA's V).  A step is four rows, 8 lanes of 16 codes (128 values)
@@ -521,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
         if (__any_sync(kAll, bad) && lane == 0) flag_status(p.a.status, DS_DEV_BAD_INDEX);
     } else if (warp >= W_MMA) {
-      setmaxnreg_dec<REG_MMA>();
+      if constexpr (!WIDE) setmaxnreg_dec<REG_MMA>();
       if (warp == W_MMA) {
         // ======================================== MMA issue ========================================
         // The first CTA's warp walks the loop (its conditions are votes), an elected lane issues for both.  S of the next tile
@@ -564,7 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const uint64_t at = (uint64_t)((((k >> 2) + (k >= 8 ? 2 : 0)) * K_CHUNK + (k & 3) * 32) >> 4);
+                            const uint64_t at = (uint64_t)((((k >> 2) + (!WIDE && k >= 8 ? 2 : 0)) * K_CHUNK + (k & 3) * 32) >> 4);
                             mma_pair(tmem + TM_S + (sJ & 1u) * 64, qd + at, kd + at, i_s, k > 0);
                         }
                         commit_pair(c.bar(B_KFREE));
@@ -577,7 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const uint64_t at = (uint64_t)((((k >> 2) + (k >= 8 ? 4 : 2)) * K_CHUNK + (k & 3) * 32) >> 4);
+                            const uint64_t at = (uint64_t)((((k >> 2) + (WIDE || k >= 8 ? 4 : 2)) * K_CHUNK + (k & 3) * 32) >> 4);
                             mma_pair(tmem + TM_S + (sJ & 1u) * 64, qd + at, kd + at, i_s, 1);
                         }
                         commit_pair(c.bar(B_S + (int)(sJ & 1u)));
@@ -666,21 +683,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 Unit x;
                 make_unit(p, u, fetch_unit(p, u), x);
                 if (x.t1 <= x.t0) continue;
-                const bool ok = mbar_wait(c.bar(B_QFREE), (n & 1u) ^ 1u, c.abort, kUnitLimitNs);
+                if (!mbar_wait(c.bar(B_QFREE), (n & 1u) ^ 1u, c.abort, kUnitLimitNs)) {
+                    c.give_up();
+                    break;
+                }
+                if (rank == 0) mbar_arrive_expect_tx(c.bar(B_Q), (uint32_t)(2 * p.R * D * 2));    // both CTAs'
+                const int32_t y = (int32_t)((int64_t)x.bi * p.a.m * p.a.h + x.r0 + (int)rank * p.R);
+                for (int ch = 0; ch < 8; ++ch) tma_load_2d(base + SM_Q + ch * K_CHUNK, &qmap, ch * 64, y, full);
+                ++n;
+            }
+        }
+        __syncwarp();
+      } else if (WIDE) {
+        // ======================= K (warp W_LOAD) and V (the next one) by TMA, in halves =======================
+        const bool isv = warp != W_LOAD;
+        if (lane == 0) {
+            const CUtensorMap *map = isv ? &vmap : &kmap;
+            const uint32_t full = first_bar(isv ? B_VFULL : B_KFULL);
+            const int free0 = isv ? B_VFREE : B_KFREE;
+            const uint32_t dst = base + (isv ? SM_V : SM_K);
+            uint32_t J = 0;
+            for (uint32_t u = cid; u < p.units; u += ncl) {
+                Unit x;
+                make_unit(p, u, fetch_unit(p, u), x);
+                const int64_t wbase = p.a.window ? max((int64_t)0, (int64_t)x.first - p.a.window + 1) : 0;
+                bool ok = true;
+                for (int t = x.t0; t < x.t1; ++t, ++J) {
+                    const int v0 = t * BN, w0 = (int)(x.wlo - wbase) + v0;
+                    const int y = x.bi * (p.wrows + p.crows) + (v0 < x.nwp ? w0 : p.wrows + v0 - x.nwp) + (isv ? 0 : HR * (int)rank);
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && mbar_wait(c.bar(free0 + h), (J & 1u) ^ 1u, c.abort, kWaitLimitNs);
+                        if (!ok) break;
+                        if (rank == 0 && !(p.stall && J == 0)) mbar_arrive_expect_tx(c.bar((isv ? B_VFULL : B_KFULL) + h), 8 * K_CHUNK);
+                        tma_load_3d(dst + h * 4 * K_CHUNK, map, 0, y, isv ? 4 * (int)rank + 2 * h : 4 * h, full + 8 * h);
+                    }
+                    if (!ok) break;
+                }
                 if (!ok) {
                     c.give_up();
                     break;
                 }
-                mbar_arrive_expect_tx(c.bar(B_QLOC), (uint32_t)(p.R * D * 2));
-                const int32_t y = (int32_t)((int64_t)x.bi * p.a.m * p.a.h + x.r0 + (int)rank * p.R);
-                for (int ch = 0; ch < 8; ++ch) tma_load_2d(base + SM_Q + ch * K_CHUNK, &qmap, ch * 64, y, c.bar(B_QLOC));
-                if (!mbar_wait(c.bar(B_QLOC), n & 1u, c.abort, kWaitLimitNs)) {
-                    c.give_up();
-                    mbar_wait_drain(c.bar(B_QLOC), n & 1u, kWaitLimitNs);   // nothing may land after the CTA is gone
-                    break;
-                }
-                arrive_operand(full);
-                ++n;
             }
         }
         __syncwarp();
@@ -718,7 +760,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         __syncwarp();
       }
     } else if (warp < W_OUT) {
-        setmaxnreg_inc<REG_SOFTMAX>();
+        if constexpr (!WIDE) setmaxnreg_inc<REG_SOFTMAX>();
         // ======================================== softmax ========================================
         // Lane r of the scores (warps 0 and 1: r < 64) has query r and the tile's rows 0-63, lane r + 64 the same query and rows
         // 64-127; the two threads share the reference through shared memory and a barrier of their two warps.
@@ -748,12 +790,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const int64_t pos = (int64_t)x.first + (live ? p.h.div((uint32_t)(x.r0 + rq), hh) : 0);
             bad |= (live && pos < 0) || x.clipped;
             const float sink2 = live ? fminf(__ldg(p.a.sink + hh) * kLog2e, 1e37f) : 0.0f;
-            // rows [a0, a1) and [nw, c1) of the list
+            // rows [a0, a1) and [nwp, c1) of the list
             int a0 = 0, a1 = 0, c1 = 0;
             if (live && pos >= 0) {
                 a0 = p.a.window ? (int)max((int64_t)0, pos - p.a.window + 1 - x.wlo) : 0;
                 a1 = (int)min(pos + 1 - x.wlo, (int64_t)x.nw);
-                c1 = x.nw + (p.a.ratio ? (int)min((pos + 1) / p.a.ratio, (int64_t)x.nc) : 0);
+                c1 = x.nwp + (p.a.ratio ? (int)min((pos + 1) / p.a.ratio, (int64_t)x.nc) : 0);
             }
             const List list = list_of(p, x);
             float ref = sink2 - 64.0f, l = 0.0f;
@@ -766,7 +808,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     uint32_t off;
                     const bool there0 = is_page(p, page_of(p, list, v0 + lane, off)), there1 = is_page(p, page_of(p, list, v0 + 32 + lane, off));
                     const uint64_t there = (uint64_t)__ballot_sync(kAll, there0) | ((uint64_t)__ballot_sync(kAll, there1) << 32);
-                    mask = there & (bits(a0 - v0, a1 - v0) | bits(x.nw - v0, c1 - v0));
+                    mask = there & (bits(a0 - v0, a1 - v0) | bits(x.nwp - v0, c1 - v0));
                 }
                 if (!dead) dead = !c.wait<false>(B_S + (int)(J & 1u), J >> 1);
                 if (!idle_warp) {
@@ -883,7 +925,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
         if (__any_sync(kAll, bad) && lane == 0) flag_status(p.a.status, DS_DEV_BAD_INDEX);
     } else {
-        setmaxnreg_inc<REG_OUT>();
+        if constexpr (!WIDE) setmaxnreg_inc<REG_OUT>();
         // ================================== output, and O^T's rescaling ==================================
         // Thread (warp w, lane) has d = 256 rank + 128 v + 32 w + lane of every query: column q of O^T's block v.
         const int w = warp - W_OUT;
@@ -1011,7 +1053,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && *c.abort) flag_status(p.a.status, DS_DEV_TIMEOUT);
+    if (*c.abort) {
+        if (threadIdx.x == 0) flag_status(p.a.status, DS_DEV_TIMEOUT);
+        // loads that were issued before somebody gave up land within microseconds
+        for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 2000000ull;) {
+        }
+    }
     // no MMA and no commit is under way in either CTA once this has passed
     if (warp == W_MMA) {
         mbar_wait_drain(c.bar(B_DRAIN), 0, 2 * kWaitLimitNs);
@@ -1023,9 +1070,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(TM_COLS) : "memory");
 }
 
+// ---- WIDE: the rows that the queries see, in bf16 ----------------------------------------------------------------
+
+constexpr int kRowsBlock = 64;
+
+// Block (x, bi): 64 rows of sequence bi, of positions from the first that a query sees on, then compressed ones.  Behind each
+// kind's last row come 128 of zeros: a tile's end is read, and P V adds 0 times what it holds.
+__global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__ Params p) {
+    if (threadIdx.x == 0) grid_launch_dependents();
+    grid_dependency_wait();
+    __shared__ int slot[kRowsBlock];         // -1: zeros, -2: nothing
+    const int bi = blockIdx.y, wblocks = (p.wrows + kRowsBlock - 1) / kRowsBlock;
+    const bool comp = (int)blockIdx.x >= wblocks;
+    const int i0 = ((int)blockIdx.x - (comp ? wblocks : 0)) * kRowsBlock;
+    if ((int)threadIdx.x < kRowsBlock) {
+        const int n = p.a.lens ? max(0, min(__ldg(p.a.lens + bi), p.a.m)) : p.a.m, i = i0 + threadIdx.x;
+        const int64_t first = __ldg(p.a.first + bi), end = first + n;          // positions below end are seen
+        const int64_t wbase = p.a.window ? max((int64_t)0, first - p.a.window + 1) : 0;
+        int64_t count = comp ? (end > 0 ? end / p.a.ratio : 0) : max((int64_t)0, end - wbase);
+        if (comp) count = min(count, max((int64_t)0, p.cap - p.a.base));
+        else if (!p.a.ring) count = min(count, max((int64_t)0, p.cap - wbase));
+        int at = -2;
+        if (n > 0 && i < (comp ? p.crows : p.wrows) && i < count + BN) {
+            at = -1;
+            if (i < count) {
+                uint32_t r = comp ? (uint32_t)(p.a.base + i) : (uint32_t)(wbase + i), off;
+                if (!comp && p.a.ring) p.ring.div((uint32_t)(wbase + i), r);
+                const uint32_t pg = p.page.div(r, off);
+                const int id = pg < (uint32_t)p.a.max_pages ? __ldg(p.a.block_table + (int64_t)bi * p.a.max_pages + pg) : -1;
+                if (is_page(p, id)) at = (int)((uint32_t)id * p.page.d + off);
+                else flag_status(p.a.status, DS_DEV_BAD_INDEX);
+            }
+        }
+        slot[threadIdx.x] = at;
+    }
+    __syncthreads();
+    uint4 *out = reinterpret_cast<uint4 *>(p.rows) + ((int64_t)bi * (p.wrows + p.crows) + (comp ? p.wrows : 0) + i0) * (D / 8);
+    constexpr int kSteps = 4;
+#pragma unroll 1
+    for (int u0 = threadIdx.x; u0 < kRowsBlock * (D / 8); u0 += 256 * kSteps) {
+        uint2 code[kSteps];
+        int k[kSteps], at[kSteps];
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            const int u = u0 + 256 * j, ch = u % (D / 8);
+            at[j] = slot[u / (D / 8)];
+            code[j] = make_uint2(0, 0);
+            k[j] = -128;
+            if (at[j] >= 0) {
+                code[j] = __ldg(reinterpret_cast<const uint2 *>(p.a.codes) + (int64_t)at[j] * (D / 8) + ch);
+                k[j] = __ldg(p.a.exps + (int64_t)at[j] * (D / 32) + (ch >> 2));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            if (at[j] == -2) continue;
+            uint32_t w[8];
+            widen16(make_uint4(code[j].x, code[j].y, 0, 0), k[j] == -128 ? 0u : (uint32_t)(247 + min(k[j], 7)), w);
+            if (k[j] > 7) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = mul_bf16x2(w[i], (uint32_t)(120 + k[j]) * 0x00800080u);
+            }
+            out[u0 + 256 * j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
 // ---- parts of a unit joined ------------------------------------------------------------------------------------
 
 constexpr int kMaxParts = 64;
+constexpr int kWideTiles = 4;
 
 // One query row a block; thread i has values 4 i .. 4 i + 3.  Each part has its reference, its sum and its O^T.
 __global__ void __launch_bounds__(128) chunk_merge_kernel(const __grid_constant__ Params p) {
@@ -1107,16 +1221,25 @@ int max_clusters(int dev) {
     if (dev < 0 || dev >= kMaxDev) return 0;
     std::lock_guard<std::mutex> lock(g_mutex);
     if (g_clusters[dev]) return g_clusters[dev];
-    int n = 0, sms = 0;
+    int least = INT32_MAX, sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    for (const void *k : {(const void *)chunk_attn_kernel<false>, (const void *)chunk_attn_kernel<true>})
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess) return 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(sms / 2 * 2), 1, 1);
-    cfg.blockDim = dim3(NTHREADS, 1, 1);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
-    if (cudaOccupancyMaxActiveClusters(&n, (const void *)chunk_attn_kernel<false>, &cfg) != cudaSuccess || n < 1) return 0;
-    return g_clusters[dev] = n;
+    auto add = [&](const void *k, int threads) {
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess) return false;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(sms / 2 * 2), 1, 1);
+        cfg.blockDim = dim3((unsigned)threads, 1, 1);
+        cfg.dynamicSmemBytes = SMEM_BYTES;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n < 1) return false;
+        least = std::min(least, n);
+        return true;
+    };
+    if (!add((const void *)chunk_attn_kernel<false, false>, Roles<false>::kThreads) ||
+        !add((const void *)chunk_attn_kernel<true, false>, Roles<false>::kThreads) ||
+        !add((const void *)chunk_attn_kernel<false, true>, Roles<true>::kThreads) ||
+        !add((const void *)chunk_attn_kernel<true, true>, Roles<true>::kThreads))
+        return 0;
+    return g_clusters[dev] = least;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -1147,14 +1270,32 @@ bool make_q_map(CUtensorMap *map, const void *q, int64_t nrows, int R) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The workspace's rows [b * (wrows + crows)][512] as chunks of 64 columns: boxes of `rows` rows of `chunks` chunks, each
+// chunk's rows together, in the MMA's 128-byte swizzle.
+bool make_rows_map(CUtensorMap *map, const void *rows, int64_t n, int box_rows, int box_chunks) {
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {64, (cuuint64_t)n, 8};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_chunks};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(rows), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Plan {
     int R, nqt, parts, clusters;
     int64_t units;
+    bool wide;
+    int wrows, crows;          // wide: rows of a sequence in the workspace
 };
 
-// Query rows a CTA: the fewest that hold a sequence's queries in one unit.  Parts of a unit: with fewer units than clusters
-// (or little more), the number of least estimated time, in tiles: rounds of units, each its tiles and two for its ends, and
-// from two parts on the merge.
+// Query rows a CTA: the fewest that hold a sequence's queries in one unit.
+// Rows widened once in a pass of their own (wide) when several units of a sequence read them, and they take no more than
+// 2 GB.
+// Parts of a unit: with fewer units than clusters (or little more), the number of least estimated time, in tiles: rounds of
+// units, each its tiles and two for its ends, and from two parts on the merge.
 bool plan(int b, int m, int h, int window, int ratio, int page, int max_pages, Plan &pl) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
@@ -1163,11 +1304,15 @@ bool plan(int b, int m, int h, int window, int ratio, int page, int max_pages, P
     const int64_t nr = (int64_t)m * h;
     pl.R = nr <= 32 ? 16 : nr <= 64 ? 32 : 64;
     pl.nqt = (int)((nr + 2 * pl.R - 1) / (2 * pl.R));
-    const int64_t units = (int64_t)b * pl.nqt, cap = (int64_t)max_pages * page;
+    const int64_t units = (int64_t)b * pl.nqt, cap = std::min<int64_t>((int64_t)max_pages * page, kMaxRows);
+    const int64_t wr = window ? std::min<int64_t>((int64_t)window + m - 1, (int64_t)1 << 30) + BN : cap + BN, cr = ratio ? cap + BN : 0;
+    pl.wide = pl.nqt >= kWideTiles && (wr + cr) * b * (D * 2) <= (int64_t)2 << 30;
+    pl.wrows = pl.wide ? (int)wr : 0;
+    pl.crows = pl.wide ? (int)cr : 0;
     // rows that a unit can have at most, for all that the host knows
     const int64_t span = (2 * pl.R + h - 2) / h;
     int64_t most = window ? std::min<int64_t>(cap, (int64_t)window + span) : cap;
-    if (ratio) most = std::min(cap, most + cap / 1);
+    if (ratio) most = std::min(cap, most + cap);
     const int64_t tiles = std::max<int64_t>(1, (most + BN - 1) / BN);
     pl.parts = 1;
     if (units < 4 * (int64_t)g) {
@@ -1186,8 +1331,9 @@ bool plan(int b, int m, int h, int window, int ratio, int page, int max_pages, P
     return pl.units < UINT32_MAX / 2;
 }
 
-size_t workspace_bytes(const Plan &pl) {
-    return pl.parts > 1 ? (size_t)pl.units * (D + 2) * (2 * pl.R) * sizeof(float) : 0;
+size_t rows_bytes(const Plan &pl, int b) { return (size_t)b * (size_t)(pl.wrows + pl.crows) * (D * 2); }
+size_t workspace_bytes(const Plan &pl, int b) {
+    return rows_bytes(pl, b) + (pl.parts > 1 ? (size_t)pl.units * (D + 2) * (2 * pl.R) * sizeof(float) : 0);
 }
 
 }  // namespace chunk
@@ -1197,38 +1343,51 @@ void set_test_stall_chunk(bool on) { chunk::g_test_stall.store(on ? 1 : 0, std::
 size_t chunk_attn_fp8_workspace_bytes(int b, int m, int h, int window, int ratio, int page, int max_pages) {
     chunk::Plan pl;
     if ((int64_t)b * m == 0 || !chunk::plan(b, m, h, window, ratio, page, max_pages, pl)) return 0;
-    return chunk::workspace_bytes(pl);
+    return chunk::workspace_bytes(pl, b);
 }
 
 int launch_chunk_attn_fp8(const chunk::Args &a, cudaStream_t stream) {
     using namespace chunk;
     Plan pl;
     if (!plan(a.b, a.m, a.h, a.window, a.ratio, a.page, a.max_pages, pl)) return launch_failed();
-    const size_t need = workspace_bytes(pl);
+    const size_t need = workspace_bytes(pl, a.b);
     if (a.workspace_bytes < need || (need && !a.workspace)) return DS_EWORKSPACE;
+    char *ws = static_cast<char *>(a.workspace);
     Params p{a, Divisor((uint32_t)a.h), Divisor((uint32_t)a.page), Divisor((uint32_t)std::max(a.ring, 1)), Divisor((uint32_t)a.b),
              Divisor((uint32_t)pl.parts), pl.R, pl.nqt, (uint32_t)pl.units,
-             std::min<int64_t>((int64_t)a.max_pages * a.page, kMaxRows), a.scale * kLog2e, static_cast<float *>(a.workspace),
+             std::min<int64_t>((int64_t)a.max_pages * a.page, kMaxRows), a.scale * kLog2e,
+             reinterpret_cast<float *>(ws + (pl.wide ? rows_bytes(pl, a.b) : 0)), pl.wide ? reinterpret_cast<uint16_t *>(ws) : nullptr, pl.wrows, pl.crows,
              g_test_stall.load(std::memory_order_relaxed)};
     if (a.pages == 0) {       // rows without a slot are read from slot 0, for nothing: there it is q's first row
         p.a.codes = reinterpret_cast<const uint8_t *>(a.q);
         p.a.exps = reinterpret_cast<const int8_t *>(a.q);
     }
-    CUtensorMap qmap;
+    CUtensorMap qmap, kmap, vmap;
     if (!make_q_map(&qmap, a.q, (int64_t)a.b * a.m * a.h, pl.R)) return DS_ECUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * pl.clusters), 1, 1);
-    cfg.blockDim = dim3(NTHREADS, 1, 1);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = stream;
-    // programmatic dependent launch: the set-up overlaps the previous kernel on the stream
+    // programmatic dependent launches: the set-up overlaps the previous kernel on the stream
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (pl.wide) {
+        const int64_t n = (int64_t)a.b * (pl.wrows + pl.crows);
+        if (!make_rows_map(&kmap, ws, n, HR, 4) || !make_rows_map(&vmap, ws, n, BN, 2)) return DS_ECUDA;
+        cfg.gridDim = dim3((unsigned)((pl.wrows + kRowsBlock - 1) / kRowsBlock + (pl.crows + kRowsBlock - 1) / kRowsBlock), (unsigned)a.b, 1);
+        cfg.blockDim = dim3(256, 1, 1);
+        if (cudaLaunchKernelEx(&cfg, chunk_rows_kernel, p) != cudaSuccess) return launch_failed();
+    } else {
+        kmap = vmap = qmap;
+    }
     const bool split = pl.parts > 1;
-    if (cudaLaunchKernelEx(&cfg, split ? chunk_attn_kernel<true> : chunk_attn_kernel<false>, qmap, p) != cudaSuccess) return launch_failed();
+    auto kernel = split ? (pl.wide ? chunk_attn_kernel<true, true> : chunk_attn_kernel<true, false>)
+                        : (pl.wide ? chunk_attn_kernel<false, true> : chunk_attn_kernel<false, false>);
+    cfg.gridDim = dim3((unsigned)(2 * pl.clusters), 1, 1);
+    cfg.blockDim = dim3((unsigned)(pl.wide ? Roles<true>::kThreads : Roles<false>::kThreads), 1, 1);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    if (cudaLaunchKernelEx(&cfg, kernel, qmap, kmap, vmap, p) != cudaSuccess) return launch_failed();
     if (split) {
         cfg.gridDim = dim3((unsigned)(pl.units / pl.parts), (unsigned)(2 * pl.R), 1);
         cfg.blockDim = dim3(128, 1, 1);
