@@ -52,12 +52,13 @@ using rows::Divisor;
 constexpr int D = 512;
 constexpr int BN = 128;                     // rows of a tile
 constexpr int HR = 64;                      // of them widened for S by each CTA; also query rows of a CTA, at most
-constexpr int W_OUT = 4;                    // warps 0-3 softmax, 4-7 output
+constexpr int W_OUT = 4;                    // warps 0-3 softmax, from 4 on output
 // WIDE: the rows come as bf16 from the workspace, by TMA; else as codes that eight warps widen
 template <bool WIDE>
 struct Roles {
-    static constexpr int kWiden = 8, kMma = WIDE ? 8 : 16, kQ = kMma + 1, kCopy = 18, kLoad = 10;   // (two warps each: kCopy, kLoad)
-    static constexpr int kThreads = WIDE ? 384 : 640;
+    static constexpr int kOut = WIDE ? 8 : 4;                            // output warps: one a lane quarter and block, or both blocks
+    static constexpr int kWiden = 8, kMma = WIDE ? 12 : 16, kQ = kMma + 1, kCopy = 18, kLoad = 14;   // (two warps each: kCopy, kLoad)
+    static constexpr int kThreads = WIDE ? 512 : 640;
 };
 // registers: 128 * (136 + 104 + 96 + 96 + 48) is what 640 threads have with 96 each
 constexpr uint32_t REG_SOFTMAX = 136, REG_OUT = 104, REG_MMA = 48;
@@ -300,14 +301,28 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// 8 columns of this thread's lane, waited for.
-__device__ __forceinline__ void tmem_ld8(uint32_t addr, float (&f)[8]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
-        : "r"(addr)
-        : "memory");
+// N columns of this thread's lane; they are there after tmem_ld_done.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&f)[N]) {
+    static_assert(N == 8 || N == 16, "8 or 16 columns");
+    if constexpr (N == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                     : "r"(addr)
+                     : "memory");
+    else
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]), "=f"(f[8]), "=f"(f[9]),
+              "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]), "=f"(f[14]), "=f"(f[15])
+            : "r"(addr)
+            : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_done(float (&f)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(f[i]));
 }
 __device__ __forceinline__ uint4 ld_codes(const uint8_t *p) {
     uint4 v;
@@ -423,8 +438,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
         mbar_init(c.bar(B_Q), 1);
         mbar_init(c.bar(B_QFREE), 1);
         mbar_init(c.bar(B_O), 1);
-        mbar_init(c.bar(B_OFREE), 8);
-        mbar_init(c.bar(B_RESCD), 8);
+        mbar_init(c.bar(B_OFREE), 2 * Roles<WIDE>::kOut);
+        mbar_init(c.bar(B_RESCD), 2 * Roles<WIDE>::kOut);
         mbar_init(c.bar(B_SYNC), 1);
         mbar_init(c.bar(B_DRAIN), 1);
         *c.abort = (base & 1023u) != 0u;    // the operands' layout needs it aligned
@@ -928,7 +943,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
         if constexpr (!WIDE) setmaxnreg_inc<REG_OUT>();
         // ================================== output, and O^T's rescaling ==================================
         // Thread (warp w, lane) has d = 256 rank + 128 v + 32 w + lane of every query: column q of O^T's block v.
-        const int w = warp - W_OUT;
+        const int w = warp & 3, vlo = WIDE ? (warp - W_OUT) >> 2 : 0, vhi = WIDE ? vlo + 1 : 2;   // its blocks
         const uint32_t tm = tmem + ((uint32_t)(w * 32) << 16) + TM_O;
         const uint32_t free_bar = first_bar(B_OFREE), resc_bar = first_bar(B_RESCD);
         const int16_t *alpha = reinterpret_cast<const int16_t *>(ctl_mem + C_ALPHA);
@@ -953,7 +968,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                         if (!__any_sync(kAll, up != 0)) continue;
                         const float f = ex2(-(float)up);
 #pragma unroll 1
-                        for (int v = 0; v < 2; ++v) {
+                        for (int v = vlo; v < vhi; ++v) {
                             uint32_t r[32];
                             tmem_ld32(tm + v * 128 + g, r);
                             tmem_ld_wait(r);
@@ -977,74 +992,119 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             uint16_t *o = p.a.o + ((int64_t)x.bi * p.a.m * p.a.h + x.r0) * D;
             uint32_t hh;
             float *part = SPLIT ? p.ws + (size_t)u * (D + 2) * nq : nullptr;
+            if (!some) {                                     // nothing seen: zeros, which no rotation changes
+                if (there <= 0) continue;
+                for (int q = 0; q < nq && q < there; ++q)
+                    for (int v = vlo; v < vhi; ++v) o[(int64_t)q * D + d0 + 128 * v] = 0;
+                const int64_t pos0 = (int64_t)x.first + p.h.div((uint32_t)x.r0, hh);
+                const int64_t pos1 = (int64_t)x.first + p.h.div((uint32_t)(x.r0 + min(nq, there) - 1), hh);
+                bad |= p.a.rd > 0 && (pos0 < 0 || pos1 >= p.a.table_rows);
+                continue;
+            }
             // a token's angles: table rows from its position on; tokens [in0, in1) of the unit's lie in the table
             const int64_t pos0 = (int64_t)x.first + p.h.div((uint32_t)x.r0, hh);
             const int in0 = pos0 < 0 ? (int)min(-pos0, (int64_t)128) : 0;
             const int in1 = (int)max((int64_t)0, min(p.a.table_rows - pos0, (int64_t)129));
             const int half_rd = p.a.rd / 2;
-#pragma unroll 1
-            for (int v = 0; v < 2; ++v) {
-                const int d = d0 + 128 * v, pair = (d - (D - p.a.rd)) >> 1;
-                const bool rot = !SPLIT && p.a.rd > 0 && 256 * (int)rank + 128 * v + 32 * w + 31 >= D - p.a.rd;
-                const float2 *angles = p.a.table + pos0 * half_rd + pair;
-                int at = (int)hh, tok = 0;
-#pragma unroll 1
-                for (int g = 0; g < nq && g < there; g += 8) {
-                    const int left = there - g;
-                    float r[8];
-                    float2 cs[8];
-                    if (rot) {
+            // steps of G queries of one block: a step's loads are under way while the one before it is worked on
+            constexpr int G = 8;
+            const int per = (min(nq, there) + G - 1) / G, steps = (vhi - vlo) * per;
+            int v = vlo, g = 0, at = (int)hh, tok = 0;       // of the step to be loaded
+            const float2 *angles = nullptr;
+            int rot = 0;                                     // 0: none, 1: one token's angles for the step, 2: each query's
+            auto block = [&]() {                             // block v begins
+                const int pair = (d0 + 128 * v - (D - p.a.rd)) >> 1;
+                rot = !SPLIT && p.a.rd > 0 && 256 * (int)rank + 128 * v + 32 * w + 31 >= D - p.a.rd;
+                angles = pair >= 0 ? p.a.table + pos0 * half_rd + pair : nullptr;
+                at = (int)hh;
+                tok = 0;
+                g = 0;
+            };
+            auto load = [&](float (&r)[G], float2 (&cs)[G]) -> int {
+                const int kind = rot == 0 ? 0 : at + G <= (int)p.h.d ? 1 : 2;
+                tmem_ld<G>(tm + v * 128 + g, r);
+                if (kind == 1) {
+                    const bool in = tok >= in0 && tok < in1;
+                    cs[0] = make_float2(1.0f, 0.0f);
+                    if (in && angles) cs[0] = __ldg(angles);
+                    bad |= !in;
+                    at += G;
+                    if (at == (int)p.h.d) {
+                        at = 0;
+                        ++tok;
+                        if (angles) angles += half_rd;
+                    }
+                } else if (kind == 2) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const bool in = tok >= in0 && tok < in1;
-                            cs[j] = make_float2(1.0f, 0.0f);
-                            if (in && pair >= 0) cs[j] = __ldg(angles);
-                            bad |= !in && j < left;
-                            if (++at == (int)p.h.d) {
-                                at = 0;
-                                ++tok;
-                                angles += half_rd;
-                            }
+                    for (int j = 0; j < G; ++j) {
+                        const bool in = tok >= in0 && tok < in1;
+                        cs[j] = make_float2(1.0f, 0.0f);
+                        if (in && angles) cs[j] = __ldg(angles);
+                        bad |= !in && g + j < there;
+                        if (++at == (int)p.h.d) {
+                            at = 0;
+                            ++tok;
+                            if (angles) angles += half_rd;
                         }
                     }
-                    if (some) {
-                        tmem_ld8(tm + v * 128 + g, r);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) r[j] = 0.0f;
-                    }
-                    if (some && v == 1 && (g + 8 >= nq || left <= 8)) {             // the last read
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive_operand(free_bar);
-                    }
-                    if (SPLIT) {
-                        float *to = part + (size_t)g * D + d;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (j < left) to[j * D] = r[j];
-                        continue;
-                    }
-                    if (some) {
-#pragma unroll
-                        for (int j = 0; j < 8; j += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(inv + g + j);
-                            r[j] *= f.x;
-                            r[j + 1] *= f.y;
-                            r[j + 2] *= f.z;
-                            r[j + 3] *= f.w;
-                        }
-                    }
-                    if (rot) {                                                       // pairs are neighbouring lanes
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            r[j] = r[j] * cs[j].x + __shfl_xor_sync(kAll, r[j], 1) * ((d & 1) ? -cs[j].y : cs[j].y);
-                    }
-                    uint16_t *to = o + (int64_t)g * D + d;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < left) to[j * D] = __bfloat16_as_ushort(__float2bfloat16_rn(r[j]));
                 }
+                g += G;
+                if (g >= per * G) {
+                    ++v;
+                    block();
+                }
+                return kind;
+            };
+            auto store = [&](int step, float (&r)[G], float2 (&cs)[G], int turned) {
+                const int second = step >= per ? 1 : 0, sv = vlo + second, sg = (step - second * per) * G, d = d0 + 128 * sv, left = there - sg;
+                if (SPLIT) {
+                    float *to = part + (size_t)sg * D + d;
+#pragma unroll
+                    for (int j = 0; j < G; ++j)
+                        if (j < left) to[j * D] = r[j];
+                    return;
+                }
+#pragma unroll
+                for (int j = 0; j < G; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(inv + sg + j);
+                    r[j] *= f.x;
+                    r[j + 1] *= f.y;
+                    r[j + 2] *= f.z;
+                    r[j + 3] *= f.w;
+                }
+                if (turned) {                                // pairs are neighbouring lanes
+#pragma unroll
+                    for (int j = 0; j < G; ++j) {
+                        const float2 a = turned == 1 ? cs[0] : cs[j];
+                        r[j] = r[j] * a.x + __shfl_xor_sync(kAll, r[j], 1) * ((d & 1) ? -a.y : a.y);
+                    }
+                }
+                uint16_t *to = o + (int64_t)sg * D + d;
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+                    if (j < left) to[j * D] = __bfloat16_as_ushort(__float2bfloat16_rn(r[j]));
+            };
+            float ra[G], rb[G];
+            float2 ca[G], cb[G];
+            block();
+            int turn = load(ra, ca), next = 0;
+#pragma unroll 1
+            for (int step = 0; step < steps; step += 2) {
+                tmem_ld_done(ra);
+                const bool last = step + 1 >= steps;
+                if (!last) next = load(rb, cb);
+                if (last || step + 2 >= steps) {
+                    // (with a step to come its columns are waited for first)
+                    if (!last) tmem_ld_done(rb);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_operand(free_bar);
+                }
+                store(step, ra, ca, turn);
+                if (last) break;
+                tmem_ld_done(rb);
+                if (step + 2 < steps) turn = load(ra, ca);
+                store(step + 1, rb, cb, next);
             }
             if (some) ++unit;
         }
