@@ -301,29 +301,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// N columns of this thread's lane; they are there after tmem_ld_done.
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&f)[N]) {
-    static_assert(N == 8 || N == 16, "8 or 16 columns");
-    if constexpr (N == 8)
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
-                     : "r"(addr)
-                     : "memory");
-    else
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-            : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]), "=f"(f[8]), "=f"(f[9]),
-              "=f"(f[10]), "=f"(f[11]), "=f"(f[12]), "=f"(f[13]), "=f"(f[14]), "=f"(f[15])
-            : "r"(addr)
-            : "memory");
-}
-template <int N>
-__device__ __forceinline__ void tmem_ld_done(float (&f)[N]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(f[i]));
-}
 __device__ __forceinline__ uint4 ld_codes(const uint8_t *p) {
     uint4 v;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
@@ -1006,60 +983,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             const int in0 = pos0 < 0 ? (int)min(-pos0, (int64_t)128) : 0;
             const int in1 = (int)max((int64_t)0, min(p.a.table_rows - pos0, (int64_t)129));
             const int half_rd = p.a.rd / 2;
-            // Steps of eight queries of a block, the next step's columns under way; one body, short enough to stay in the
-            // instruction cache (unrolled by two it took 5.5 us a unit).
-            constexpr int G = 8;
-            const int per = (min(nq, there) + G - 1) / G;
+            // 32 queries of a block at a time: issuing a load of tensor memory takes a warp some 150 cycles whatever its size
+            // (steps of eight queries took 540 cycles each, a unit 4.4 us).
+            constexpr int G = 32;
+            const int last = ((min(nq, there) + G - 1) / G - 1) * G;
 #pragma unroll 1
             for (int v = vlo; v < vhi; ++v) {
                 const int d = d0 + 128 * v, pair = (d - (D - p.a.rd)) >> 1;
                 const bool rot = !SPLIT && p.a.rd > 0 && 256 * (int)rank + 128 * v + 32 * w + 31 >= D - p.a.rd;
                 const bool odd = d & 1;
                 const float2 *angles = rot && pair >= 0 ? p.a.table + pos0 * half_rd + pair : nullptr;
-                int at = (int)hh, tok = 0;                   // of the step to come: its first query's head and token
-                float r[G];
-                float2 cn = make_float2(1.0f, 0.0f);         // its angles, where one token has all of it
+                int at = (int)hh, tok = 0;                   // the next query's head and token
                 auto angle = [&]() -> float2 {
                     const bool in = tok >= in0 && tok < in1;
                     bad |= !in;
-                    return in && angles ? __ldg(angles) : make_float2(1.0f, 0.0f);
+                    float2 cs = in && angles ? __ldg(angles) : make_float2(1.0f, 0.0f);
+                    if (odd) cs.y = -cs.y;
+                    return cs;
                 };
-                tmem_ld<G>(tm + v * 128, r);
-                if (rot && at + G <= (int)p.h.d) cn = angle();
+                auto advance = [&](int n) {
+                    if ((at += n) == (int)p.h.d) {
+                        at = 0;
+                        ++tok;
+                        if (angles) angles += half_rd;
+                    }
+                };
                 uint16_t *to = o + d;
                 float *top = SPLIT ? part + d : nullptr;
 #pragma unroll 1
-                for (int g = 0; g < per * G; g += G) {
-                    const int left = there - g;
-                    float x[G];
-                    tmem_ld_done(r);
-#pragma unroll
-                    for (int j = 0; j < G; ++j) x[j] = r[j];
-                    const float2 c0 = cn;
-                    const bool one = at + G <= (int)p.h.d;
-                    float2 cs[G];
-                    if (rot && !one) {                       // several tokens in a step
-#pragma unroll
-                        for (int j = 0; j < G; ++j) {
-                            cs[j] = j < left ? angle() : make_float2(1.0f, 0.0f);
-                            if (++at == (int)p.h.d) {
-                                at = 0;
-                                ++tok;
-                                if (angles) angles += half_rd;
-                            }
-                        }
-                    } else if (rot) {
-                        at += G;
-                        if (at == (int)p.h.d) {
-                            at = 0;
-                            ++tok;
-                            if (angles) angles += half_rd;
-                        }
+                for (int g = 0; g <= last; g += G) {
+                    uint32_t r[G];
+                    tmem_ld32(tm + v * 128 + g, r);
+                    float2 c8[4];                            // angles of eight queries that one token has
+                    uint32_t ones = 0;
+                    if (rot && at + G <= (int)p.h.d) {
+                        c8[0] = c8[1] = c8[2] = c8[3] = angle();
+                        advance(G);
+                        ones = 15;
                     }
-                    if (g + G < per * G) {
-                        tmem_ld<G>(tm + v * 128 + g + G, r);
-                        if (rot && at + G <= (int)p.h.d) cn = angle();
-                    } else if (v == vhi - 1) {
+                    tmem_ld_wait(r);
+                    if (g == last && v == vhi - 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) arrive_operand(free_bar);
@@ -1067,27 +1030,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                     if (SPLIT) {
 #pragma unroll
                         for (int j = 0; j < G; ++j)
-                            if (j < left) top[j * D] = x[j];
+                            if (g + j < there) top[j * D] = __uint_as_float(r[j]);
                         top += G * D;
                         continue;
                     }
-                    const float4 fa = *reinterpret_cast<const float4 *>(inv + g), fb = *reinterpret_cast<const float4 *>(inv + g + 4);
-                    const float f[G] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
 #pragma unroll
-                    for (int j = 0; j < G; ++j) x[j] *= f[j];
-                    if (rot) {                               // pairs are neighbouring lanes
-                        if (one) {
-                            const float sn = odd ? -c0.y : c0.y;
+                    for (int e = 0; e < 4; ++e) {
+                        const int left = there - g - 8 * e;
+                        const float4 fa = *reinterpret_cast<const float4 *>(inv + g + 8 * e);
+                        const float4 fb = *reinterpret_cast<const float4 *>(inv + g + 8 * e + 4);
+                        const float f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
+                        float x[8];
 #pragma unroll
-                            for (int j = 0; j < G; ++j) x[j] = x[j] * c0.x + __shfl_xor_sync(kAll, x[j], 1) * sn;
-                        } else {
+                        for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(r[8 * e + j]) * f[j];
+                        if (rot && left > 0) {               // pairs are neighbouring lanes
+                            if (!((ones >> e) & 1u) && at + 8 <= (int)p.h.d) {
+                                c8[e] = angle();
+                                advance(8);
+                                ones |= 1u << e;
+                            }
+                            if ((ones >> e) & 1u) {
 #pragma unroll
-                            for (int j = 0; j < G; ++j) x[j] = x[j] * cs[j].x + __shfl_xor_sync(kAll, x[j], 1) * (odd ? -cs[j].y : cs[j].y);
+                                for (int j = 0; j < 8; ++j) x[j] = x[j] * c8[e].x + __shfl_xor_sync(kAll, x[j], 1) * c8[e].y;
+                            } else {                         // several tokens in eight queries
+                                float2 cs[8];
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    cs[j] = j < left ? angle() : make_float2(1.0f, 0.0f);
+                                    advance(1);
+                                }
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) x[j] = x[j] * cs[j].x + __shfl_xor_sync(kAll, x[j], 1) * cs[j].y;
+                            }
                         }
-                    }
 #pragma unroll
-                    for (int j = 0; j < G; ++j)
-                        if (j < left) to[j * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[j]));
+                        for (int j = 0; j < 8; ++j)
+                            if (j < left) to[(8 * e + j) * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[j]));
+                    }
                     to += G * D;
                 }
             }
