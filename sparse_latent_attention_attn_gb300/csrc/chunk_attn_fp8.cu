@@ -116,7 +116,9 @@ struct Params {
     Divisor h, page, ring, b, parts;
     int R;               // query rows of a CTA: 64, 32 or 16
     int nqt;             // query tiles of a sequence
-    uint32_t units;
+    uint32_t units;      // whole ones, then parts of the others
+    uint32_t whole;
+    Divisor clusters;
     int64_t cap;         // logical rows that the block table can hold, at most kMaxRows
     float scale_log2;
     float *ws;           // parts of units
@@ -138,22 +140,52 @@ struct Unit {
     bool clipped;        // rows beyond the block table
 };
 
-__device__ __forceinline__ int2 fetch_unit(const Params &p, uint32_t u) {
-    if (u >= p.units) return make_int2(0, 0);
-    uint32_t part, bi;
-    p.b.div(p.parts.div(u, part), bi);
-    return make_int2(__ldg(p.a.first + bi), p.a.lens ? __ldg(p.a.lens + bi) : p.a.m);
+// Which of a sequence's query tiles unit u is (of), of which sequence, and which part of it.  Later tokens see more, so
+// the sequences' last tiles come first.  A cluster takes every `clusters`-th unit: the sequences change places
+// from round to round (by a hash of the round), so that it does not get one sequence's units only.
+struct Place {
+    uint32_t of, bi, part;
+    int qt;
+};
+__device__ __forceinline__ Place place_of(const Params &p, uint32_t of, uint32_t part) {
+    Place x;
+    x.of = of;
+    x.part = part;
+    uint32_t i, rest;
+    const uint32_t group = p.b.div(of, i);
+    x.qt = p.nqt - 1 - (int)group;
+    (void)p.b.div(i + ((p.clusters.div(group * p.b.d, rest) * 0x9E3779B1u) >> 16), x.bi);
+    return x;
+}
+__device__ __forceinline__ Place place(const Params &p, uint32_t u) {
+    uint32_t part = 0;
+    return place_of(p, u < p.whole ? u : p.whole + p.parts.div(u - p.whole, part), part);
 }
 
-// raw: fetch_unit(u).  Later tokens see more, so a sequence's last query tiles come first.
-__device__ __forceinline__ void make_unit(const Params &p, uint32_t u, int2 raw, Unit &x) {
-    uint32_t part, bi;
-    const int qt = p.nqt - 1 - (int)p.b.div(p.parts.div(u, part), bi);
-    x.bi = (int)bi;
-    x.part = (int)part;
-    x.first = raw.x;
-    x.rows = max(0, min(raw.y, p.a.m)) * p.a.h;
-    x.r0 = qt * 2 * p.R;
+// What unit u needs from memory, for make_unit: asked for one unit ahead.
+struct Ahead {
+    Place at;
+    int first, len;
+};
+__device__ __forceinline__ Ahead look(const Params &p, uint32_t u) {
+    Ahead x;
+    x.first = x.len = 0;
+    if (u < p.units) {
+        x.at = place(p, u);
+        x.first = __ldg(p.a.first + x.at.bi);
+        x.len = p.a.lens ? __ldg(p.a.lens + x.at.bi) : p.a.m;
+    }
+    return x;
+}
+
+// a: look(p, u)
+__device__ __forceinline__ void make_unit(const Params &p, uint32_t u, const Ahead &a, Unit &x) {
+    const int parts = u < p.whole ? 1 : (int)p.parts.d;
+    x.bi = (int)a.at.bi;
+    x.part = (int)a.at.part;
+    x.first = a.first;
+    x.rows = max(0, min(a.len, p.a.m)) * p.a.h;
+    x.r0 = a.at.qt * 2 * p.R;
     x.nw = x.nwp = x.nc = 0;
     x.wlo = 0;
     x.t0 = x.t1 = 0;
@@ -180,8 +212,8 @@ __device__ __forceinline__ void make_unit(const Params &p, uint32_t u, int2 raw,
     }
     x.nwp = p.rows && x.nc ? (x.nw + BN - 1) / BN * BN : x.nw;      // WIDE: compressed rows begin a tile
     const int64_t nt = (x.nwp + x.nc + BN - 1) / BN;
-    x.t0 = (int)(nt * x.part / (int)p.parts.d);
-    x.t1 = (int)(nt * (x.part + 1) / (int)p.parts.d);
+    x.t0 = (int)(nt * x.part / parts);
+    x.t1 = (int)(nt * (x.part + 1) / parts);
 }
 
 // What is left of a unit for whoever fetches its rows.
@@ -211,11 +243,14 @@ struct TileIter {
     uint32_t u;
     int t, t1;
     List x;
+    Ahead ahead;             // of unit u
     __device__ __forceinline__ bool valid() const { return t < t1; }
     __device__ __forceinline__ void seek(const Params &p, uint32_t step) {      // the first unit from u on with tiles
-        for (; u < p.units; u += step) {
+        while (u < p.units) {
             Unit unit;
-            make_unit(p, u, fetch_unit(p, u), unit);
+            make_unit(p, u, ahead, unit);
+            u += step;
+            ahead = look(p, u);
             if (unit.t1 > unit.t0) {
                 t = unit.t0;
                 t1 = unit.t1;
@@ -227,11 +262,11 @@ struct TileIter {
     }
     __device__ __forceinline__ void start(const Params &p, uint32_t first, uint32_t step) {
         u = first;
+        ahead = look(p, u);
         seek(p, step);
     }
     __device__ __forceinline__ void next(const Params &p, uint32_t step) {
         if (++t < t1) return;
-        u += step;
         seek(p, step);
     }
 };
@@ -546,13 +581,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             int s_left = 0;
             uint32_t s_unit = 0, v_unit = 0;
             int v_left = 0;
-            int2 raw = fetch_unit(p, u);
+            Ahead ahead = look(p, u);
             auto begin = [&]() {                   // the next unit with tiles
                 while (u < p.units) {
                     Unit x;
-                    make_unit(p, u, raw, x);
+                    make_unit(p, u, ahead, x);
                     u += ncl;
-                    raw = fetch_unit(p, u);
+                    ahead = look(p, u);
                     if (x.t1 > x.t0) {
                         s_left = x.t1 - x.t0;
                         __syncwarp();
@@ -671,9 +706,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
         if (lane == 0) {
             const uint32_t full = first_bar(B_Q);
             uint32_t n = 0;
+            Ahead ahead = look(p, cid);
             for (uint32_t u = cid; u < p.units; u += ncl) {
                 Unit x;
-                make_unit(p, u, fetch_unit(p, u), x);
+                make_unit(p, u, ahead, x);
+                ahead = look(p, u + ncl);
                 if (x.t1 <= x.t0) continue;
                 if (!mbar_wait(c.bar(B_QFREE), (n & 1u) ^ 1u, c.abort, kUnitLimitNs)) {
                     c.give_up();
@@ -695,9 +732,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             const int free0 = isv ? B_VFREE : B_KFREE;
             const uint32_t dst = base + (isv ? SM_V : SM_K);
             uint32_t J = 0;
+            Ahead ahead = look(p, cid);
             for (uint32_t u = cid; u < p.units; u += ncl) {
                 Unit x;
-                make_unit(p, u, fetch_unit(p, u), x);
+                make_unit(p, u, ahead, x);
+                ahead = look(p, u + ncl);
                 const int64_t wbase = p.a.window ? max((int64_t)0, (int64_t)x.first - p.a.window + 1) : 0;
                 bool ok = true;
                 for (int t = x.t0; t < x.t1; ++t, ++J) {
@@ -764,7 +803,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
         const float scale = fabsf(p.scale_log2);                // its sign goes to the scores
         const bool idle_warp = (warp & 1) * 32 >= p.R;          // no query of these 32
         bool dead = false, bad = false;
-        uint32_t J = 0, unit = 0, ex = 0;                       // tiles, units with tiles, exchanges
+        uint32_t J = 0, unit = 0, ex = 0;                       // tiles, whole units with tiles, exchanges
         uint32_t lowered = 0;                                   // bit J & 1: this thread's entry of alpha is not 0
         auto exchange = [&](float v) -> float {                 // the other thread's value
             float *x = xch + (ex & 1u) * 128;
@@ -773,9 +812,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             named_bar_sync(1 + (warp & 1), 64);
             return x[(half ^ 1) * 64 + row];
         };
+        Ahead ahead = look(p, cid);
         for (uint32_t u = cid; u < p.units; u += ncl) {
             Unit x;
-            make_unit(p, u, fetch_unit(p, u), x);
+            make_unit(p, u, ahead, x);
+            ahead = look(p, u + ncl);
             const int rq = (int)rank * p.R + row;               // query row of the unit
             const bool live = row < p.R && x.r0 + rq < x.rows;
             uint32_t hh = 0;
@@ -886,32 +927,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                     else arrive_operand(pfull[J & 1u]);
                 }
             }
+            const bool split = SPLIT && u >= p.whole;           // a part: its reference and sum go to the workspace
+            float *st = split ? p.ws + ((size_t)(u - p.whole) * (D + 2) + D) * (2 * p.R) + 2 * rq : nullptr;
             if (x.t1 == x.t0) {
-                if (SPLIT && live && half == 0) {
-                    float *st = p.ws + ((size_t)u * (D + 2) + D) * (2 * p.R) + 2 * rq;
+                if (split && live && half == 0) {
                     st[0] = -INFINITY;
                     st[1] = 0.0f;
                 }
                 continue;
             }
             if (!idle_warp) l += exchange(l);
-            if (half == 0) {
-                if (SPLIT) {
-                    if (live) {
-                        float *st = p.ws + ((size_t)u * (D + 2) + D) * (2 * p.R) + 2 * rq;
-                        st[0] = ref;
-                        st[1] = l;
-                    }
-                } else {
-                    if (row < p.R) {
-                        const float inv = l > 0.0f ? 1.0f / (l + ex2(sink2 - ref)) : (l == 0.0f ? 0.0f : l);
-                        const uint32_t at = c.bars + C_INV + ((unit & 1u) * 128 + rq) * 4;
-                        st_cluster_u32(mapa(at, 0), __float_as_uint(inv));
-                        st_cluster_u32(mapa(at, 1), __float_as_uint(inv));
-                    }
-                    __syncwarp();
-                    if (lane < 2) arrive_cluster(mapa(c.bar(B_INV + (int)(unit & 1u)), (uint32_t)lane));
+            if (split) {
+                if (live && half == 0) {
+                    st[0] = ref;
+                    st[1] = l;
                 }
+                continue;
+            }
+            if (half == 0) {
+                if (row < p.R) {
+                    const float inv = l > 0.0f ? 1.0f / (l + ex2(sink2 - ref)) : (l == 0.0f ? 0.0f : l);
+                    const uint32_t at = c.bars + C_INV + ((unit & 1u) * 128 + rq) * 4;
+                    st_cluster_u32(mapa(at, 0), __float_as_uint(inv));
+                    st_cluster_u32(mapa(at, 1), __float_as_uint(inv));
+                }
+                __syncwarp();
+                if (lane < 2) arrive_cluster(mapa(c.bar(B_INV + (int)(unit & 1u)), (uint32_t)lane));
             }
             ++unit;
         }
@@ -928,11 +969,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
         const int d0 = 256 * (int)rank + 32 * w + lane;
         uint32_t unit = 0, event = 0;
         bool bad = false, ok = true;
+        Ahead ahead = look(p, cid);
         for (uint32_t u = cid; u < p.units && ok; u += ncl) {
             Unit x;
-            make_unit(p, u, fetch_unit(p, u), x);
-            const bool some = x.t1 > x.t0;
-            if (SPLIT && !some) continue;
+            make_unit(p, u, ahead, x);
+            ahead = look(p, u + ncl);
+            const bool some = x.t1 > x.t0, split = SPLIT && u >= p.whole;
+            if (split && !some) continue;
+            uint32_t hh;
+            const int64_t pos0 = (int64_t)x.first + (x.r0 < x.rows ? p.h.div((uint32_t)x.r0, hh) : 0);
+            // a token's angles: table rows from its position on; tokens [in0, in1) of the unit's lie in the table
+            const int in0 = pos0 < 0 ? (int)min(-pos0, (int64_t)128) : 0;
+            const int in1 = (int)max((int64_t)0, min(p.a.table_rows - pos0, (int64_t)129));
+            const int half_rd = p.a.rd / 2;
+            bool rot = false, odd = d0 & 1;
+            const float2 *angles = nullptr;
+            int at = 0, tok = 0;                             // the next query's head and token
+            auto angle = [&]() -> float2 {
+                const bool in = tok >= in0 && tok < in1;
+                bad |= !in;
+                float2 cs = in && angles ? __ldg(angles) : make_float2(1.0f, 0.0f);
+                if (odd) cs.y = -cs.y;
+                return cs;
+            };
+            auto advance = [&](int n) {
+                if ((at += n) == (int)p.h.d) {
+                    at = 0;
+                    ++tok;
+                    if (angles) angles += half_rd;
+                }
+            };
+            constexpr int G = 32;                            // queries at a time
+            float2 cn = make_float2(1.0f, 0.0f);             // the angles of the next G queries, where one token has them all
+            auto look_ahead = [&]() {
+                if (rot && at + G <= (int)p.h.d) cn = angle();
+            };
+            auto block = [&](int v) {                        // block v begins
+                const int pair = (d0 + 128 * v - (D - p.a.rd)) >> 1;
+                rot = !split && some && p.a.rd > 0 && 256 * (int)rank + 128 * v + 32 * w + 31 >= D - p.a.rd;
+                angles = rot && pair >= 0 ? p.a.table + pos0 * half_rd + pair : nullptr;
+                at = (int)hh;
+                tok = 0;
+                look_ahead();
+            };
+            block(vlo);
             if (some) {
                 for (;; ++event) {
                     ok = c.wait<true, kUnitLimitNs>(B_O, event);
@@ -960,66 +1040,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                     if (lane == 0) arrive_cluster(resc_bar);
                 }
                 ++event;
-                if (ok && !SPLIT) ok = c.wait<true>(B_INV + (int)(unit & 1u), unit >> 1);
+                if (ok && !split) ok = c.wait<true>(B_INV + (int)(unit & 1u), unit >> 1);
                 if (!ok) break;
                 tc_fence_after();
             }
             const int there = x.rows - x.r0;                 // queries of this unit
             const float *inv = reinterpret_cast<const float *>(ctl_mem + C_INV) + (unit & 1u) * 128;
             uint16_t *o = p.a.o + ((int64_t)x.bi * p.a.m * p.a.h + x.r0) * D;
-            uint32_t hh;
-            float *part = SPLIT ? p.ws + (size_t)u * (D + 2) * nq : nullptr;
+            float *part = split ? p.ws + (size_t)(u - p.whole) * (D + 2) * nq : nullptr;
             if (!some) {                                     // nothing seen: zeros, which no rotation changes
                 if (there <= 0) continue;
                 for (int q = 0; q < nq && q < there; ++q)
                     for (int v = vlo; v < vhi; ++v) o[(int64_t)q * D + d0 + 128 * v] = 0;
-                const int64_t pos0 = (int64_t)x.first + p.h.div((uint32_t)x.r0, hh);
                 const int64_t pos1 = (int64_t)x.first + p.h.div((uint32_t)(x.r0 + min(nq, there) - 1), hh);
                 bad |= p.a.rd > 0 && (pos0 < 0 || pos1 >= p.a.table_rows);
                 continue;
             }
-            // a token's angles: table rows from its position on; tokens [in0, in1) of the unit's lie in the table
-            const int64_t pos0 = (int64_t)x.first + p.h.div((uint32_t)x.r0, hh);
-            const int in0 = pos0 < 0 ? (int)min(-pos0, (int64_t)128) : 0;
-            const int in1 = (int)max((int64_t)0, min(p.a.table_rows - pos0, (int64_t)129));
-            const int half_rd = p.a.rd / 2;
             // 32 queries of a block at a time: issuing a load of tensor memory takes a warp some 150 cycles whatever its size
             // (steps of eight queries took 540 cycles each, a unit 4.4 us).
-            constexpr int G = 32;
             const int last = ((min(nq, there) + G - 1) / G - 1) * G;
 #pragma unroll 1
             for (int v = vlo; v < vhi; ++v) {
-                const int d = d0 + 128 * v, pair = (d - (D - p.a.rd)) >> 1;
-                const bool rot = !SPLIT && p.a.rd > 0 && 256 * (int)rank + 128 * v + 32 * w + 31 >= D - p.a.rd;
-                const bool odd = d & 1;
-                const float2 *angles = rot && pair >= 0 ? p.a.table + pos0 * half_rd + pair : nullptr;
-                int at = (int)hh, tok = 0;                   // the next query's head and token
-                auto angle = [&]() -> float2 {
-                    const bool in = tok >= in0 && tok < in1;
-                    bad |= !in;
-                    float2 cs = in && angles ? __ldg(angles) : make_float2(1.0f, 0.0f);
-                    if (odd) cs.y = -cs.y;
-                    return cs;
-                };
-                auto advance = [&](int n) {
-                    if ((at += n) == (int)p.h.d) {
-                        at = 0;
-                        ++tok;
-                        if (angles) angles += half_rd;
-                    }
-                };
-                uint16_t *to = o + d;
-                float *top = SPLIT ? part + d : nullptr;
+                if (v > vlo) block(v);
+                uint16_t *to = o + d0 + 128 * v;
+                float *top = split ? part + d0 + 128 * v : nullptr;
 #pragma unroll 1
                 for (int g = 0; g <= last; g += G) {
                     uint32_t r[G];
                     tmem_ld32(tm + v * 128 + g, r);
-                    float2 c8[4];                            // angles of eight queries that one token has
-                    uint32_t ones = 0;
-                    if (rot && at + G <= (int)p.h.d) {
-                        c8[0] = c8[1] = c8[2] = c8[3] = angle();
+                    const bool one = at + G <= (int)p.h.d;
+                    const float2 c32 = cn;
+                    if (rot && one) {
                         advance(G);
-                        ones = 15;
+                        if (g < last) look_ahead();
                     }
                     tmem_ld_wait(r);
                     if (g == last && v == vhi - 1) {
@@ -1027,7 +1080,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                         __syncwarp();
                         if (lane == 0) arrive_operand(free_bar);
                     }
-                    if (SPLIT) {
+                    if (split) {
 #pragma unroll
                         for (int j = 0; j < G; ++j)
                             if (g + j < there) top[j * D] = __uint_as_float(r[j]);
@@ -1044,14 +1097,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
 #pragma unroll
                         for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(r[8 * e + j]) * f[j];
                         if (rot && left > 0) {               // pairs are neighbouring lanes
-                            if (!((ones >> e) & 1u) && at + 8 <= (int)p.h.d) {
-                                c8[e] = angle();
-                                advance(8);
-                                ones |= 1u << e;
-                            }
-                            if ((ones >> e) & 1u) {
+                            if (one || at + 8 <= (int)p.h.d) {
+                                float2 c8 = c32;
+                                if (!one) {
+                                    c8 = angle();
+                                    advance(8);
+                                }
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) x[j] = x[j] * c8[e].x + __shfl_xor_sync(kAll, x[j], 1) * c8[e].y;
+                                for (int j = 0; j < 8; ++j) x[j] = x[j] * c8.x + __shfl_xor_sync(kAll, x[j], 1) * c8.y;
                             } else {                         // several tokens in eight queries
                                 float2 cs[8];
 #pragma unroll
@@ -1067,10 +1120,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                         for (int j = 0; j < 8; ++j)
                             if (j < left) to[(8 * e + j) * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[j]));
                     }
+                    if (rot && !one && g < last) look_ahead();
                     to += G * D;
                 }
             }
-            if (some) ++unit;
+            if (some && !split) ++unit;
         }
         if (__any_sync(kAll, bad) && lane == 0) flag_status(p.a.status, DS_DEV_BAD_INDEX);
     }
@@ -1168,10 +1222,12 @@ constexpr int kWideTiles = 4;
 // One query row a block; thread i has values 4 i .. 4 i + 3.  Each part has its reference, its sum and its O^T.
 __global__ void __launch_bounds__(128) chunk_merge_kernel(const __grid_constant__ Params p) {
     grid_dependency_wait();
-    const uint32_t tile = blockIdx.x;               // unit / parts
+    const uint32_t tile = blockIdx.x;               // of those that are in parts
     const int q = blockIdx.y, lane = threadIdx.x & 31;
-    uint32_t bi, hh;
-    const int qt = p.nqt - 1 - (int)p.b.div(tile, bi);
+    const Place pl = place_of(p, p.whole + tile, 0);
+    const uint32_t bi = pl.bi;
+    const int qt = pl.qt;
+    uint32_t hh;
     const int n = p.a.lens ? max(0, min(__ldg(p.a.lens + bi), p.a.m)) : p.a.m, r = qt * 2 * p.R + q;
     if (r >= n * p.a.h) return;
     const int64_t pos = (int64_t)__ldg(p.a.first + bi) + p.h.div((uint32_t)r, hh);
@@ -1310,7 +1366,7 @@ bool make_rows_map(CUtensorMap *map, const void *rows, int64_t n, int box_rows, 
 
 struct Plan {
     int R, nqt, parts, clusters;
-    int64_t units;
+    int64_t whole, units;      // units that are not in parts, and with the parts of the others
     bool wide;
     int wrows, crows;          // wide: rows of a sequence in the workspace
 };
@@ -1318,8 +1374,10 @@ struct Plan {
 // Query rows a CTA: the fewest that hold a sequence's queries in one unit.
 // Rows widened once in a pass of their own (wide) when several units of a sequence read them, and they take no more than
 // 2 GB.
-// Parts of a unit: with fewer units than clusters (or little more), the number of least estimated time, in tiles: rounds of
-// units, each its tiles and two for its ends, and from two parts on the merge.
+// Parts of a unit: with fewer units than clusters, the number of least estimated time, in tiles: rounds of units, each its
+// tiles and two for its ends, and from two parts on the merge.  With more, those of a last round that would leave
+// half of the clusters or more without work are cut into as many parts as there are clusters for, where that saves
+// more than the merge takes (8 tiles' time).
 bool plan(int b, int m, int h, int window, int ratio, int page, int max_pages, Plan &pl) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
@@ -1339,7 +1397,8 @@ bool plan(int b, int m, int h, int window, int ratio, int page, int max_pages, P
     if (ratio) most = std::min(cap, most + cap);
     const int64_t tiles = std::max<int64_t>(1, (most + BN - 1) / BN);
     pl.parts = 1;
-    if (units < 4 * (int64_t)g) {
+    pl.whole = units;
+    if (units <= g) {
         double least = 1e30;
         for (int k = 1; k <= kMaxParts && k <= tiles; ++k) {
             const double rounds = (double)((units * k + g - 1) / g);
@@ -1349,15 +1408,22 @@ bool plan(int b, int m, int h, int window, int ratio, int page, int max_pages, P
                 pl.parts = k;
             }
         }
+        if (pl.parts > 1) pl.whole = 0;
+    } else if (units < 8 * (int64_t)g && units % g != 0) {
+        const int64_t rest = units % g, k = std::min<int64_t>({g / rest, tiles, kMaxParts});
+        if (k >= 2 && tiles - (tiles + k - 1) / k >= 8) {
+            pl.parts = (int)k;
+            pl.whole = units - rest;
+        }
     }
-    pl.units = units * pl.parts;
+    pl.units = pl.whole + (units - pl.whole) * pl.parts;
     pl.clusters = (int)std::min<int64_t>(pl.units, g);
     return pl.units < UINT32_MAX / 2;
 }
 
 size_t rows_bytes(const Plan &pl, int b) { return (size_t)b * (size_t)(pl.wrows + pl.crows) * (D * 2); }
 size_t workspace_bytes(const Plan &pl, int b) {
-    return rows_bytes(pl, b) + (pl.parts > 1 ? (size_t)pl.units * (D + 2) * (2 * pl.R) * sizeof(float) : 0);
+    return rows_bytes(pl, b) + (size_t)(pl.units - pl.whole) * (pl.parts > 1 ? 1 : 0) * (D + 2) * (2 * pl.R) * sizeof(float);
 }
 
 }  // namespace chunk
@@ -1378,7 +1444,7 @@ int launch_chunk_attn_fp8(const chunk::Args &a, cudaStream_t stream) {
     if (a.workspace_bytes < need || (need && !a.workspace)) return DS_EWORKSPACE;
     char *ws = static_cast<char *>(a.workspace);
     Params p{a, Divisor((uint32_t)a.h), Divisor((uint32_t)a.page), Divisor((uint32_t)std::max(a.ring, 1)), Divisor((uint32_t)a.b),
-             Divisor((uint32_t)pl.parts), pl.R, pl.nqt, (uint32_t)pl.units,
+             Divisor((uint32_t)pl.parts), pl.R, pl.nqt, (uint32_t)pl.units, (uint32_t)pl.whole, Divisor((uint32_t)pl.clusters),
              std::min<int64_t>((int64_t)a.max_pages * a.page, kMaxRows), a.scale * kLog2e,
              reinterpret_cast<float *>(ws + (pl.wide ? rows_bytes(pl, a.b) : 0)), pl.wide ? reinterpret_cast<uint16_t *>(ws) : nullptr, pl.wrows, pl.crows,
              g_test_stall.load(std::memory_order_relaxed)};
@@ -1413,7 +1479,7 @@ int launch_chunk_attn_fp8(const chunk::Args &a, cudaStream_t stream) {
     cfg.dynamicSmemBytes = SMEM_BYTES;
     if (cudaLaunchKernelEx(&cfg, kernel, qmap, kmap, vmap, p) != cudaSuccess) return launch_failed();
     if (split) {
-        cfg.gridDim = dim3((unsigned)(pl.units / pl.parts), (unsigned)(2 * pl.R), 1);
+        cfg.gridDim = dim3((unsigned)((pl.units - pl.whole) / pl.parts), (unsigned)(2 * pl.R), 1);
         cfg.blockDim = dim3(128, 1, 1);
         cfg.dynamicSmemBytes = 0;
         if (cudaLaunchKernelEx(&cfg, chunk_merge_kernel, p) != cudaSuccess) return launch_failed();
