@@ -154,7 +154,8 @@ __device__ __forceinline__ Place place_of(const Params &p, uint32_t of, uint32_t
     uint32_t i, rest;
     const uint32_t group = p.b.div(of, i);
     x.qt = p.nqt - 1 - (int)group;
-    (void)p.b.div(i + ((p.clusters.div(group * p.b.d, rest) * 0x9E3779B1u) >> 16), x.bi);
+    x.bi = 0;
+    if (p.b.d > 1) (void)p.b.div(i + ((p.clusters.div(group * p.b.d, rest) * 0x9E3779B1u) >> 16), x.bi);
     return x;
 }
 __device__ __forceinline__ Place place(const Params &p, uint32_t u) {
@@ -226,15 +227,28 @@ __device__ __forceinline__ List list_of(const Params &p, const Unit &x) {
     return {p.a.block_table + (int64_t)x.bi * p.a.max_pages, x.wlo, x.nw, x.nwp, x.nwp + x.nc};
 }
 
-// Block table entry of the list's row v, and the row's place in its page (kNoRow behind the list's end).
+// Loads that leave v as it is unless `there`.  (As a select behind a load, which waits for it where it stands, they took the
+// widening warps 0.7 us a tile each.)
+__device__ __forceinline__ void ld_if(bool there, const int32_t *at, int &v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}" : "+r"(v) : "l"(at), "r"((int)there));
+}
+__device__ __forceinline__ void ld_if(bool there, const void *at, uint4 &v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+                 : "l"(at), "r"((int)there));
+}
+
+// Block table entry of the list's row v (-1 without one), and the row's place in its page (kNoRow behind the list's end).
 constexpr uint32_t kNoRow = UINT32_MAX;
-__device__ __forceinline__ int page_of(const Params &p, const List &x, int v, uint32_t &off) {
-    off = kNoRow;
-    if (v >= x.nv || (v >= x.nw && v < x.nwp)) return -1;
+__device__ __forceinline__ int page_of(const Params &p, const List &x, int v, bool valid, uint32_t &off) {
+    const bool row = valid && v < x.nv && (v < x.nw || v >= x.nwp);
     uint32_t r = v < x.nw ? x.wlo + (uint32_t)v : (uint32_t)(p.a.base + (v - x.nwp));
     if (v < x.nw && p.a.ring) p.ring.div(x.wlo + (uint32_t)v, r);
     const uint32_t pg = p.page.div(r, off);
-    return pg < (uint32_t)p.a.max_pages ? __ldg(x.table + pg) : -1;
+    if (!row) off = kNoRow;
+    int id = -1;
+    ld_if(row && pg < (uint32_t)p.a.max_pages, x.table + pg, id);
+    return id;
 }
 __device__ __forceinline__ bool is_page(const Params &p, int id) { return id >= 0 && id < p.a.pages; }
 
@@ -498,13 +512,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             const int s = __shfl_sync(kAll, slot, src0 + 4 * (i & 1));
             code[h][i] = ld_codes(codes + (int64_t)s * D + (h * 128 + (i >> 1) * 256));
         };
-        auto look_up = [&]() { id = it.valid() ? page_of(p, it.x, it.t * BN + HR * (int)rank + 8 * w + l8, off) : -1; };
+        auto look_up = [&]() { id = page_of(p, it.x, it.t * BN + HR * (int)rank + 8 * w + l8, it.valid(), off); };
         // a row without a slot is read from slot 0 and widened to zeros
         auto exps_of = [&](int &at) -> uint4 {                            // of 128 values each
             const bool there = is_page(p, id);
             bad |= it.valid() && off != kNoRow && !there;
             at = there ? (int)((uint32_t)id * p.page.d + off) : 0;
-            return there ? __ldg(reinterpret_cast<const uint4 *>(p.a.exps) + at) : make_uint4(kZeros, kZeros, kZeros, kZeros);
+            uint4 e = make_uint4(kZeros, kZeros, kZeros, kZeros);
+            ld_if(there, reinterpret_cast<const uint4 *>(p.a.exps) + at, e);
+            return e;
         };
         look_up();
         uint4 ex = exps_of(slot);
@@ -759,35 +775,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
         __syncwarp();
       } else {
         // ================================ half h of K to both CTAs' V ================================
+        // The copy engine takes the other CTA's chunks, this warp its own (the engine with both: 2 us a tile, 1 us each 32 KB).
         const int h = warp - W_COPY;
-        if (lane == 0) {
-            const uint32_t vfull = first_bar(B_VFULL + h);
-            TileIter it;
-            it.start(p, cid, ncl);
-            for (uint32_t J = 0; it.valid(); ++J, it.next(p, ncl)) {
-                if (!mbar_wait(c.bar(B_KLOC + h), J & 1u, c.abort, kWaitLimitNs) ||
-                    !mbar_wait(c.bar(B_VFREE + h), (J & 1u) ^ 1u, c.abort, kWaitLimitNs)) {
-                    c.give_up();
-                    break;
-                }
-                mbar_arrive_expect_tx(c.bar(B_VLOC + h), 4 * K_CHUNK);   // this CTA's two chunks, and the other's rows of them
+        const uint32_t vfull = first_bar(B_VFULL + h), to = rank ^ 1u;
+        const uint32_t from = base + SM_K + (4 * rank + 2 * h) * K_CHUNK + lane * 16, own = base + SM_V + 2 * h * V_CHUNK + rank * K_CHUNK + lane * 16;
+        TileIter it;
+        it.start(p, cid, ncl);
+        for (uint32_t J = 0; it.valid(); ++J, it.next(p, ncl)) {
+            if (!c.wait<false>(B_KLOC + h, J) || !c.wait<false>(B_VFREE + h, J + 1)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(c.bar(B_VLOC + h), 2 * K_CHUNK);   // the other CTA's rows
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {                            // the other CTA's first: they take longer
-                    const uint32_t to = (uint32_t)(i >> 1) ^ rank ^ 1u;
-                    bulk_copy_to_peer(mapa(base + SM_V + (2 * h + (i & 1)) * V_CHUNK + rank * K_CHUNK, to),
-                                      base + SM_K + (4 * to + 2 * h + (i & 1)) * K_CHUNK, K_CHUNK, mapa(c.bar(B_VLOC + h), to));
-                }
+                for (int i = 0; i < 2; ++i)
+                    bulk_copy_to_peer(mapa(base + SM_V + (2 * h + i) * V_CHUNK + rank * K_CHUNK, to),
+                                      base + SM_K + (4 * to + 2 * h + i) * K_CHUNK, K_CHUNK, mapa(c.bar(B_VLOC + h), to));
                 bulk_commit_group();
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll 1
+                for (int k = 0; k < K_CHUNK; k += 2048) {
+                    float4 x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = ld_shared_v4(from + i * K_CHUNK + k + j * 512);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        st_shared_v4(own + i * V_CHUNK + k + j * 512, __float_as_uint(x[j].x), __float_as_uint(x[j].y), __float_as_uint(x[j].z),
+                                     __float_as_uint(x[j].w));
+                }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
                 bulk_wait_read_all();
                 mbar_arrive(c.bar(B_KFREE + h));
-                if (!mbar_wait(c.bar(B_VLOC + h), J & 1u, c.abort, kWaitLimitNs)) {
-                    c.give_up();
-                    break;
-                }
-                arrive_operand(vfull);
             }
-            bulk_wait_all();                                             // nothing may land after the CTAs are gone
+            if (!c.wait<false>(B_VLOC + h, J)) break;
+            if (lane == 0) arrive_operand(vfull);
         }
+        if (lane == 0) bulk_wait_all();                                  // nothing may land after the CTAs are gone
         __syncwarp();
       }
     } else if (warp < W_OUT) {
@@ -800,7 +825,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
         const uint32_t pfull[2] = {first_bar(B_P), first_bar(B_P + 1)};
         const uint32_t resc = mapa(c.bars + C_RESC, 0);
         float *xch = reinterpret_cast<float *>(ctl_mem + C_XCH);
-        const float scale = fabsf(p.scale_log2);                // its sign goes to the scores
+        const float scale = p.scale_log2 == 0.0f ? 1.0f : fabsf(p.scale_log2);   // its sign, or a 0, goes to the scores
         const bool idle_warp = (warp & 1) * 32 >= p.R;          // no query of these 32
         bool dead = false, bad = false;
         uint32_t J = 0, unit = 0, ex = 0;                       // tiles, whole units with tiles, exchanges
@@ -839,7 +864,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                 bool up_any = false;                            // a reference of this warp moves
                 if (!idle_warp) {
                     uint32_t off;
-                    const bool there0 = is_page(p, page_of(p, list, v0 + lane, off)), there1 = is_page(p, page_of(p, list, v0 + 32 + lane, off));
+                    const bool there0 = is_page(p, page_of(p, list, v0 + lane, true, off)), there1 = is_page(p, page_of(p, list, v0 + 32 + lane, true, off));
                     const uint64_t there = (uint64_t)__ballot_sync(kAll, there0) | ((uint64_t)__ballot_sync(kAll, there1) << 32);
                     mask = there & (bits(a0 - v0, a1 - v0) | bits(x.nwp - v0, c1 - v0));
                 }
@@ -853,9 +878,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                     tc_fence_before();
                     const bool whole = __all_sync(kAll, mask == ~0ull);
                     float m = -INFINITY;
-                    if (p.scale_log2 < 0.0f) {
+                    if (p.scale_log2 <= 0.0f) {
+                        const float f = p.scale_log2 < 0.0f ? -1.0f : 0.0f;
 #pragma unroll
-                        for (int g = 0; g < 64; ++g) s[g >> 5][g & 31] ^= 0x80000000u;
+                        for (int g = 0; g < 64; ++g) s[g >> 5][g & 31] = __float_as_uint(__uint_as_float(s[g >> 5][g & 31]) * f);
                     }
                     if (!whole) {
 #pragma unroll
@@ -907,10 +933,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                                 unpair(fma2(pair(__uint_as_float(s[g][i + 2 * j]), __uint_as_float(s[g][i + 2 * j + 1])), scale2, neg), e0, e1);
                                 e0 = ex2(e0);
                                 e1 = ex2(e1);
-                                if (!whole) {                   // (a scale of 0 makes NaN of what is masked)
-                                    if (!((mask >> (32 * g + i + 2 * j)) & 1u)) e0 = 0.0f;
-                                    if (!((mask >> (32 * g + i + 2 * j + 1)) & 1u)) e1 = 0.0f;
-                                }
                                 sum = add2(sum, pair(e0, e1));
                                 w[j] = pack_bf16x2(e0, e1);
                             }
@@ -976,43 +998,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             ahead = look(p, u + ncl);
             const bool some = x.t1 > x.t0, split = SPLIT && u >= p.whole;
             if (split && !some) continue;
-            uint32_t hh;
-            const int64_t pos0 = (int64_t)x.first + (x.r0 < x.rows ? p.h.div((uint32_t)x.r0, hh) : 0);
-            // a token's angles: table rows from its position on; tokens [in0, in1) of the unit's lie in the table
-            const int in0 = pos0 < 0 ? (int)min(-pos0, (int64_t)128) : 0;
-            const int in1 = (int)max((int64_t)0, min(p.a.table_rows - pos0, (int64_t)129));
-            const int half_rd = p.a.rd / 2;
-            bool rot = false, odd = d0 & 1;
-            const float2 *angles = nullptr;
-            int at = 0, tok = 0;                             // the next query's head and token
-            auto angle = [&]() -> float2 {
-                const bool in = tok >= in0 && tok < in1;
-                bad |= !in;
-                float2 cs = in && angles ? __ldg(angles) : make_float2(1.0f, 0.0f);
-                if (odd) cs.y = -cs.y;
-                return cs;
-            };
-            auto advance = [&](int n) {
-                if ((at += n) == (int)p.h.d) {
-                    at = 0;
-                    ++tok;
-                    if (angles) angles += half_rd;
-                }
-            };
-            constexpr int G = 32;                            // queries at a time
-            float2 cn = make_float2(1.0f, 0.0f);             // the angles of the next G queries, where one token has them all
-            auto look_ahead = [&]() {
-                if (rot && at + G <= (int)p.h.d) cn = angle();
-            };
-            auto block = [&](int v) {                        // block v begins
-                const int pair = (d0 + 128 * v - (D - p.a.rd)) >> 1;
-                rot = !split && some && p.a.rd > 0 && 256 * (int)rank + 128 * v + 32 * w + 31 >= D - p.a.rd;
-                angles = rot && pair >= 0 ? p.a.table + pos0 * half_rd + pair : nullptr;
-                at = (int)hh;
-                tok = 0;
-                look_ahead();
-            };
-            block(vlo);
             if (some) {
                 for (;; ++event) {
                     ok = c.wait<true, kUnitLimitNs>(B_O, event);
@@ -1047,32 +1032,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             const int there = x.rows - x.r0;                 // queries of this unit
             const float *inv = reinterpret_cast<const float *>(ctl_mem + C_INV) + (unit & 1u) * 128;
             uint16_t *o = p.a.o + ((int64_t)x.bi * p.a.m * p.a.h + x.r0) * D;
+            uint32_t hh;
             float *part = split ? p.ws + (size_t)(u - p.whole) * (D + 2) * nq : nullptr;
             if (!some) {                                     // nothing seen: zeros, which no rotation changes
                 if (there <= 0) continue;
                 for (int q = 0; q < nq && q < there; ++q)
                     for (int v = vlo; v < vhi; ++v) o[(int64_t)q * D + d0 + 128 * v] = 0;
+                const int64_t pos0 = (int64_t)x.first + p.h.div((uint32_t)x.r0, hh);
                 const int64_t pos1 = (int64_t)x.first + p.h.div((uint32_t)(x.r0 + min(nq, there) - 1), hh);
                 bad |= p.a.rd > 0 && (pos0 < 0 || pos1 >= p.a.table_rows);
                 continue;
             }
+            // a token's angles: table rows from its position on; tokens [in0, in1) of the unit's lie in the table
+            const int64_t pos0 = (int64_t)x.first + p.h.div((uint32_t)x.r0, hh);
+            const int in0 = pos0 < 0 ? (int)min(-pos0, (int64_t)128) : 0;
+            const int in1 = (int)max((int64_t)0, min(p.a.table_rows - pos0, (int64_t)129));
+            const int half_rd = p.a.rd / 2;
             // 32 queries of a block at a time: issuing a load of tensor memory takes a warp some 150 cycles whatever its size
             // (steps of eight queries took 540 cycles each, a unit 4.4 us).
+            constexpr int G = 32;
             const int last = ((min(nq, there) + G - 1) / G - 1) * G;
 #pragma unroll 1
             for (int v = vlo; v < vhi; ++v) {
-                if (v > vlo) block(v);
-                uint16_t *to = o + d0 + 128 * v;
-                float *top = split ? part + d0 + 128 * v : nullptr;
+                const int d = d0 + 128 * v, pair = (d - (D - p.a.rd)) >> 1;
+                const bool rot = !split && p.a.rd > 0 && 256 * (int)rank + 128 * v + 32 * w + 31 >= D - p.a.rd;
+                const bool odd = d & 1;
+                const float2 *angles = rot && pair >= 0 ? p.a.table + pos0 * half_rd + pair : nullptr;
+                int at = (int)hh, tok = 0;                   // the next query's head and token
+                auto angle = [&]() -> float2 {
+                    const bool in = tok >= in0 && tok < in1;
+                    bad |= !in;
+                    float2 cs = in && angles ? __ldg(angles) : make_float2(1.0f, 0.0f);
+                    if (odd) cs.y = -cs.y;
+                    return cs;
+                };
+                auto advance = [&](int n) {
+                    if ((at += n) == (int)p.h.d) {
+                        at = 0;
+                        ++tok;
+                        if (angles) angles += half_rd;
+                    }
+                };
+                uint16_t *to = o + d;
+                float *top = split ? part + d : nullptr;
 #pragma unroll 1
                 for (int g = 0; g <= last; g += G) {
                     uint32_t r[G];
                     tmem_ld32(tm + v * 128 + g, r);
-                    const bool one = at + G <= (int)p.h.d;
-                    const float2 c32 = cn;
-                    if (rot && one) {
+                    float2 c8[4];                            // angles of eight queries that one token has
+                    uint32_t ones = 0;
+                    if (rot && at + G <= (int)p.h.d) {
+                        c8[0] = c8[1] = c8[2] = c8[3] = angle();
                         advance(G);
-                        if (g < last) look_ahead();
+                        ones = 15;
                     }
                     tmem_ld_wait(r);
                     if (g == last && v == vhi - 1) {
@@ -1097,14 +1109,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
 #pragma unroll
                         for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(r[8 * e + j]) * f[j];
                         if (rot && left > 0) {               // pairs are neighbouring lanes
-                            if (one || at + 8 <= (int)p.h.d) {
-                                float2 c8 = c32;
-                                if (!one) {
-                                    c8 = angle();
-                                    advance(8);
-                                }
+                            if (!((ones >> e) & 1u) && at + 8 <= (int)p.h.d) {
+                                c8[e] = angle();
+                                advance(8);
+                                ones |= 1u << e;
+                            }
+                            if ((ones >> e) & 1u) {
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) x[j] = x[j] * c8.x + __shfl_xor_sync(kAll, x[j], 1) * c8.y;
+                                for (int j = 0; j < 8; ++j) x[j] = x[j] * c8[e].x + __shfl_xor_sync(kAll, x[j], 1) * c8[e].y;
                             } else {                         // several tokens in eight queries
                                 float2 cs[8];
 #pragma unroll
@@ -1120,7 +1132,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                         for (int j = 0; j < 8; ++j)
                             if (j < left) to[(8 * e + j) * D] = __bfloat16_as_ushort(__float2bfloat16_rn(x[j]));
                     }
-                    if (rot && !one && g < last) look_ahead();
                     to += G * D;
                 }
             }
@@ -1217,7 +1228,11 @@ __global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__
 // ---- parts of a unit joined ------------------------------------------------------------------------------------
 
 constexpr int kMaxParts = 64;
-constexpr int kWideTiles = 4;
+// Query tiles of a sequence from which its rows are widened once, in a pass of their own.  With two tiles that takes 0.83 of the
+// time (64 sequences, 2 tokens of 128 heads, 2176 rows: 119 us instead of 142; with three tiles, 32 sequences: 77 instead of
+// 104); with one tile 1.06 of it (32 sequences of 4224 rows: 79 instead of 74 us; 128 rows: 19.9 instead of 15), but for
+// single sequences (0.9).
+constexpr int kWideTiles = 2;
 
 // One query row a block; thread i has values 4 i .. 4 i + 3.  Each part has its reference, its sum and its O^T.
 __global__ void __launch_bounds__(128) chunk_merge_kernel(const __grid_constant__ Params p) {
