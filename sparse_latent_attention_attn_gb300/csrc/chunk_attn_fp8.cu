@@ -490,40 +490,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
 
     if (!WIDE && warp >= W_WIDEN && warp < W_MMA) {
         // ================================ widening: this CTA's 64 rows of the tile ================================
-        // Warp w takes rows 8 w .. 8 w + 7.  Half h of K is chunks 2 h, 2 h + 1, 2 h + 4 and 2 h + 5 (the first or second 128
-        // values of each half of d: block h of either CTA's V).  A step is four rows, 8 lanes of 16 codes (128 values)
-        // each; step i of a half has rows 4 (i % 2) .. and the first (i < 2) or the second half of d.  The next tile's codes
-        // are fetched into the registers of the ones that have been widened.  Lane l has the slot and exponents of row l % 8.
-        const int w = warp - W_WIDEN, l8 = lane & 7, src0 = lane >> 3;
+        // Warp w takes rows 8 w .. 8 w + 7, four lanes each.  Half h of K is chunks 2 h, 2 h + 1, 2 h + 4 and 2 h + 5 (half h of
+        // V in either CTA); a step is one chunk, 16 codes a lane.  The next tile's codes are fetched into the registers of the
+        // ones that have been widened.
+        const int w = warp - W_WIDEN, q = lane & 3, r = 8 * w + (lane >> 2);
         const uint32_t full0 = first_bar(B_KFULL);
-        // a lane's 16 values are 16-byte units 2 (l8 % 4) and the next one of chunk l8 / 4 of the step's two; odd chunks' lanes
-        // store the second one first, so that eight lanes meet every bank once
-        const uint32_t odd = (l8 >> 2) & 1u, u0 = 2 * (l8 & 3) + odd;
-        const uint32_t dst0 = base + SM_K + (l8 >> 2) * K_CHUNK + (8 * w + src0) * 128;
-        const uint8_t *codes = p.a.codes + l8 * 16;
-        const uint32_t sel = 0x4440u | (uint32_t)(l8 >> 1);              // this lane's exponent of four
+        // a lane's 16 values are 16-byte units 2 q and 2 q + 1 of the chunk: of two rows' lanes the swizzle makes one of each unit
+        const uint32_t dst0 = base + SM_K + r * 128 + (((2 * q) ^ (r & 7)) << 4), flip = dst0 ^ 16u;
+        const uint32_t sel = 0x4440u | (uint32_t)(q >> 1);               // this lane's exponent: of an even chunk; + 2: odd
         TileIter it;
         it.start(p, cid, ncl);
         uint4 code[2][4];
         bool bad = false;
         uint32_t off = 0;
-        int id = -1, slot = 0, slot_next = 0;
-        auto fetch = [&](int h, int i) {
-            const int s = __shfl_sync(kAll, slot, src0 + 4 * (i & 1));
-            code[h][i] = ld_codes(codes + (int64_t)s * D + (h * 128 + (i >> 1) * 256));
-        };
-        auto look_up = [&]() { id = page_of(p, it.x, it.t * BN + HR * (int)rank + 8 * w + l8, it.valid(), off); };
+        int id = -1;
+        const uint8_t *row = p.a.codes + q * 16, *row_next = row;
+        auto chunk_of = [](int h, int i) { return 2 * h + (i & 1) + 4 * (i >> 1); };
+        auto fetch = [&](int h, int i) { code[h][i] = ld_codes(row + chunk_of(h, i) * 64); };
+        auto look_up = [&]() { id = page_of(p, it.x, it.t * BN + HR * (int)rank + r, it.valid(), off); };
         // a row without a slot is read from slot 0 and widened to zeros
-        auto exps_of = [&](int &at) -> uint4 {                            // of 128 values each
+        auto exps_of = [&](const uint8_t *&at) -> uint4 {                 // of 128 values each
             const bool there = is_page(p, id);
             bad |= it.valid() && off != kNoRow && !there;
-            at = there ? (int)((uint32_t)id * p.page.d + off) : 0;
+            const int64_t slot = there ? (int64_t)((uint32_t)id * p.page.d + off) : 0;
+            at = p.a.codes + q * 16 + slot * D;
             uint4 e = make_uint4(kZeros, kZeros, kZeros, kZeros);
-            ld_if(there, reinterpret_cast<const uint4 *>(p.a.exps) + at, e);
+            ld_if(there, reinterpret_cast<const uint4 *>(p.a.exps) + slot, e);
             return e;
         };
         look_up();
-        uint4 ex = exps_of(slot);
+        uint4 ex = exps_of(row);
 #pragma unroll
         for (int i = 0; i < 8; ++i) fetch(i >> 2, i & 3);
         bool more = it.valid(), more_next = false;
@@ -532,7 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             more_next = it.valid();
             look_up();
         }
-        uint4 ex_next = exps_of(slot);                                    // from here on slot is the next tile's
+        uint4 ex_next = exps_of(row);                                     // from here on row is the next tile's
         for (uint32_t J = 0; more; ++J) {
             if (more_next) it.next(p, ncl);
             look_up();
@@ -540,24 +536,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             bool ok = true;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t e0 = h ? ex.y : ex.x, e1 = h ? ex.w : ex.z, f0 = fields(e0, slow), f1 = fields(e1, slow);
+                const uint32_t e[2] = {h ? ex.y : ex.x, h ? ex.w : ex.z}, f[2] = {fields(e[0], slow), fields(e[1], slow)};
                 ok = ok && c.wait<false>(B_KFREE + h, J + 1);
                 if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int src = src0 + 4 * (i & 1);
                     uint32_t v[8];
-                    uint4 x = code[h][i];
-                    if (odd) x = make_uint4(x.z, x.w, x.x, x.y);
-                    widen16(x, __byte_perm(__shfl_sync(kAll, i >= 2 ? f1 : f0, src), 0, sel), v);
+                    widen16(code[h][i], __byte_perm(f[i >> 1], 0, sel + 2 * (i & 1)), v);
                     if (slow) {                  // the rest of powers above 2^127: 2^(k - 7)
-                        const int k = (int)(__byte_perm(__shfl_sync(kAll, i >= 2 ? e1 : e0, src), 0, sel) << 24) >> 24;
+                        const int k = (int)(__byte_perm(e[i >> 1], 0, sel + 2 * (i & 1)) << 24) >> 24;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v[j] = mul_bf16x2(v[j], (uint32_t)(120 + max(k, 7)) * 0x00800080u);
                     }
-                    const uint32_t at = dst0 + (2 * h + 4 * (i >> 1)) * K_CHUNK + (i & 1) * 512, r7 = src;
-                    st_shared_v4(at + ((u0 ^ r7) << 4), v[0], v[1], v[2], v[3]);
-                    st_shared_v4(at + ((u0 ^ 1u ^ r7) << 4), v[4], v[5], v[6], v[7]);
+                    st_shared_v4(dst0 + chunk_of(h, i) * K_CHUNK, v[0], v[1], v[2], v[3]);
+                    st_shared_v4(flip + chunk_of(h, i) * K_CHUNK, v[4], v[5], v[6], v[7]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -569,13 +561,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                 // are fetched behind the fence, which would wait for them
                 if (h == 1) {
                     ex = ex_next;
-                    ex_next = exps_of(slot_next);
+                    ex_next = exps_of(row_next);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) fetch(h, i);
             }
             if (!ok) break;
-            slot = slot_next;
+            row = row_next;
             more = more_next;
             more_next = it.valid();
         }
