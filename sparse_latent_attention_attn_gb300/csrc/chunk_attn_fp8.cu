@@ -361,18 +361,26 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// Bytes of v with their signs above them: 16-bit integers.
+template <uint32_t kSel>
+__device__ __forceinline__ uint32_t sign_extended(uint32_t v) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(v), "n"(kSel));
+    return r;
+}
+
 // Sixteen codes times a power of two as bf16 pairs.  A code's exponent and mantissa bits, moved to a bf16's, are its value
 // times 2^-120 (subnormals too), so one product with 2^(120 + k) makes it: b is that power's exponent field, 247 + k, or 0
-// for zeros.
+// for zeros.  Two codes take a permutation and a mask in the integer pipe, and a shift and the product in the other (the bits put
+// together from a word's nibbles took seven operations of the integer pipe for four codes).
 __device__ __forceinline__ void widen16(const uint4 c, uint32_t b, uint32_t (&w)[8]) {
     const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
     const uint32_t scale = b * 0x00800080u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        // a bf16's low bytes, and its high bytes with the sign
-        const uint32_t lo = (cw[i] << 4) & 0xf0f0f0f0u, hi = ((cw[i] >> 4) & 0x07070707u) | (cw[i] & 0x80808080u);
-        w[2 * i] = mul_bf16x2(__byte_perm(lo, hi, 0x5140), scale);
-        w[2 * i + 1] = mul_bf16x2(__byte_perm(lo, hi, 0x7362), scale);
+        // what the shift takes from the lower into the upper code is masked
+        w[2 * i] = mul_bf16x2((sign_extended<0x9180>(cw[i]) * 16u) & 0x87f087f0u, scale);
+        w[2 * i + 1] = mul_bf16x2((sign_extended<0xb3a2>(cw[i]) * 16u) & 0x87f087f0u, scale);
     }
 }
 
