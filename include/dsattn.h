@@ -50,7 +50,7 @@ typedef struct CUstream_st *ds_stream_t;
 #define DS_DEV_TIMEOUT 1u     /* a bounded wait inside a kernel gave up; that launch's output is invalid */
 /* Every wait inside the attention kernels gives up after 2 s, sets DS_DEV_TIMEOUT, drains the
  * launch's own copies and MMAs and returns, so the context stays usable (ds_test_set_stall
- * exercises that path). */
+ * exercises that path).  In ds_chunk_attn_fp8_paged the waits that last as long as a sequence may take 60 s. */
 #define DS_DEV_BAD_INDEX 2u   /* an index >= n was seen; the entry was skipped                       */
 #define DS_DEV_BAD_VALUE 4u   /* a stored exponent above its range was seen; it was read as the range's largest */
 
@@ -540,7 +540,8 @@ int ds_kv_read_fp4_paged(const uint8_t *codes, const int8_t *exps, int64_t pages
  * Scores, softmax and accumulation are f32; a probability enters the value product rounded to bf16, as in
  * ds_sparse_attn.  The rows that queries of a sequence see must be finite in bf16 (their largest code times
  * 2^k below 2^128), and scale * q, the scores and the products that are added up finite in f32.  Rows
- * that no query of the sequence sees do not matter, nor does what unused pages hold.
+ * that no query of the sequence sees do not matter, nor does what unused pages hold.  A block whose exponent is -128
+ * counts as zeros (ds_kv_append_fp8_paged stores none below -22).
  *
  * q          device bf16 [b][m][h][512]
  * sink       device f32 [h]
@@ -548,12 +549,14 @@ int ds_kv_read_fp4_paged(const uint8_t *codes, const int8_t *exps, int64_t pages
  * first      device int32 [b];  lens: device int32 [b], or NULL for m
  * window     >= 0;  ring 0, or at least window (window > 0) and at most max_pages * page, and without lens at
  *            least window + m - 1, so that the chunk's rows replaced none that its queries see; with lens
- *            the same must hold for the largest of them
+ *            the same must hold for the largest of them.  Logical rows from 2^29 on count as rows without a page
  * base       >= 0, and >= ring when there are both a ring and compressed rows
  * workspace  at least ds_chunk_attn_fp8_paged_workspace_bytes bytes for the same arguments, 256-byte aligned (may
  *            be NULL when that size is 0); its contents need no initialisation and mean nothing afterwards.
- *            Calls that may run at the same time need one each.
- * Supported: d = 512, 1 <= h <= 128, b * m * h < 2^31, pages * page < 2^31; q, o, codes and exps 16-byte aligned.
+ *            Calls that may run at the same time need one each.  It holds partial results of long sequences, and, where
+ *            a sequence has more than 128 query rows (m * h), the block table's rows in bf16, up to 2 GB of them
+ * Supported: d = 512, 1 <= h <= 128, b * m * h < 2^31, pages * page < 2^31, ring <= 2^29; q, o, codes and exps 16-byte
+ * aligned.
  * Errors: DS_EINVAL, DS_EUNSUPPORTED, DS_EWORKSPACE, DS_ECUDA.
  */
 size_t ds_chunk_attn_fp8_paged_workspace_bytes(int b, int m, int h, int d, int window, int ratio, int page,
@@ -575,7 +578,7 @@ int ds_device_status(ds_stream_t stream, unsigned int *bits_out);
 /*
  * ds_test_set_stall -- test hook for the bounded waits (no counterpart on the pages).  While `on`
  * is nonzero (process-wide, every device), each ds_sparse_attn / ds_sparse_attn_fp8kv /
- * ds_sparse_attn_fp4_paged launch has its gather warps withhold the first tile's arrivals: the
+ * ds_sparse_attn_fp4_paged / ds_chunk_attn_fp8_paged launch has the warps that bring rows withhold the first tile's arrivals: the
  * launch's waits run out after about 2 s, it drains its own copies and MMAs, raises DS_DEV_TIMEOUT
  * and returns with its output invalid; no GPU fault is involved.  Default off; nothing in the library turns it on.
  */

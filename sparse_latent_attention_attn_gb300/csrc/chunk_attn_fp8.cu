@@ -17,20 +17,32 @@
 // The tensor cores read both CTAs' operands, so no scores and no probabilities cross between the CTAs.  The MMAs of a tile
 // take 0.75 + 0.53 us (23.3 ns for each of 32, 32.9 ns for each of 16, measured), 0.85 of the tensor cores' rate.
 //
-// The codes are widened to bf16 in registers (exact: at most four significant bits; a code's bits moved to a bf16's, times
-// 2^(120 + k)) on their way into shared memory, which spares a copy in HBM: 33/32 byte a value is all that is read.
-// Each CTA widens its 64 rows once, as K; for P V it needs its half of d of all 128, and the copy engine brings them: half of
-// K's chunks go to the CTA's own V, half to the other's, 8 KB each, in the layout that they have (a widening of each row in
-// both CTAs took the integer pipe 2100 cycles a tile, of 2500 that the MMAs take).  An operand half is handed back as
-// soon as its readers are done, while the next tile's codes wait in registers.
+// A code widens to bf16 exactly (at most four significant bits; its bits moved to a bf16's, times 2^(120 + k)).  Two forms:
+//   * Sequences with one tile of queries (decoding): each row is read once, as codes, and widened in registers on its way into
+//     shared memory, which spares a copy in HBM: 33/32 byte a value is all that is read.  Each CTA widens its 64 rows once,
+//     as K; for P V it needs its half of d of all 128, copied from K in the layout that it has: its own rows by a warp, the
+//     other CTA's by the copy engine, 8 KB each (the engine with both takes 2 us a tile).  K is held until its copies have been
+//     read, and V is filled when the last tile's P V is done, so the copies stand between two tiles: 3.3 us a tile where the
+//     MMAs take 1.28.  (The rows passed through a ring in the workspace instead, V by TMA: 204 -> 241 us for 256 sequences of
+//     2176 rows; V widened a second time by eight more warps: 252 -> 370.)
+//   * Sequences with several (WIDE; prompts): several units read the same rows, so a kernel before widens them once, into the
+//     workspace, and K and V come by TMA: 1.5 us a tile, and some 4 us between units, in which q is loaded and O^T read.
+// An operand half is handed back as soon as its readers are done.
 //
-// The softmax works on a reference per query: the first tile's maximum, moved (by whole octaves, so that O^T and the sum are
-// scaled exactly) only when a later one exceeds it by more than kSlack octaves.  It is never more than 64 octaves below the
-// sink, so that 1 / (sum + sink) is a normal number wherever an output is.  P is rounded to bf16 for the product, as in
-// ds_sparse_attn; the sum takes it unrounded.
+// The softmax works on a reference per query: kSlack octaves above the first tile's maximum, moved (by whole octaves, so that
+// O^T and the sum are scaled exactly) only when a later maximum exceeds it.  So P is at most 1, as large as it may be beside
+// rows near the end of bf16's range, and a number's distance from the maximum costs it nothing down to 2^-106 of that.  The
+// reference is never more than 64 octaves below the sink, so that 1 / (sum + sink) is a normal number wherever an output is.
+// P is rounded to bf16 for the product, as in ds_sparse_attn; the sum takes it unrounded.
 //
-// Warps: 0-3 softmax, 4-7 output (and O^T's rescaling, on request), 8-15 widen, 16 issues the MMAs (in the cluster's first
-// CTA, for both), 17 fetches q by TMA, 18 and 19 have the halves of K copied to V.  Every wait gives up after 2 s (DS_DEV_TIMEOUT).
+// Few units are cut into parts of their rows, and so are those of a last round that would leave clusters without work; a
+// kernel behind joins a unit's parts by their references and sums.
+//
+// Warps: 0-3 softmax; from 4 on output (and O^T's rescaling, on request): four, or eight with WIDE; 8-15 widen; one issues the
+// MMAs (in the cluster's first CTA, for both); one fetches q by TMA; two have the halves of K copied to V, or bring K and V.
+// What bounds the small calls is instructions: roles share their SM's issue slots and instruction caches, so a body that
+// is twice as long costs other roles time too.  Every wait gives up after 2 s, or 60 s
+// where it lasts as long as a unit (DS_DEV_TIMEOUT).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -53,7 +65,7 @@ constexpr int D = 512;
 constexpr int BN = 128;                     // rows of a tile
 constexpr int HR = 64;                      // of them widened for S by each CTA; also query rows of a CTA, at most
 constexpr int W_OUT = 4;                    // warps 0-3 softmax, from 4 on output
-// WIDE: the rows come as bf16 from the workspace, by TMA; else as codes that eight warps widen
+// First warps of the roles.  WIDE: the rows come as bf16 from the workspace, by TMA; else as codes that eight warps widen.
 template <bool WIDE>
 struct Roles {
     static constexpr int kOut = WIDE ? 8 : 4;                            // output warps: one a lane quarter and block, or both blocks
@@ -108,7 +120,7 @@ static_assert(SM_CTL + C_XCH + 1024 <= SMEM_BYTES, "control block");
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kUnitLimitNs = 30 * kWaitLimitNs;   // of waits that last as long as a unit
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 20.0f;             // octaves above the reference up to which P may go
+constexpr float kSlack = 20.0f;             // octaves that a reference is put above the maximum
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct Params {
@@ -227,8 +239,7 @@ __device__ __forceinline__ List list_of(const Params &p, const Unit &x) {
     return {p.a.block_table + (int64_t)x.bi * p.a.max_pages, x.wlo, x.nw, x.nwp, x.nwp + x.nc};
 }
 
-// Loads that leave v as it is unless `there`.  (As a select behind a load, which waits for it where it stands, they took the
-// widening warps 0.7 us a tile each.)
+// Loads that leave v as it is unless `there`: nothing behind them selects, and so waits, before the value is needed.
 __device__ __forceinline__ void ld_if(bool there, const int32_t *at, int &v) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}" : "+r"(v) : "l"(at), "r"((int)there));
 }
@@ -903,12 +914,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                     float up = 0.0f;
                     if (!set) {
                         if (m > -INFINITY) {
-                            ref = fmaxf(ref, m);
+                            ref = fmaxf(ref, m + kSlack);
                             set = true;
                         }
-                    } else if (m > ref + kSlack) {
-                        up = fminf(ceilf(m - ref), 16384.0f);
-                        ref = up < 16384.0f ? ref + up : m;
+                    } else if (m > ref) {
+                        up = fminf(ceilf(m - ref) + kSlack, 16384.0f);
+                        ref = up < 16384.0f ? ref + up : m + kSlack;
                         l *= ex2(-up);
                     }
                     up_any = __any_sync(kAll, up > 0.0f);

@@ -796,6 +796,140 @@ def test_attention_is_the_same_every_time(ds):
         assert torch.equal(ds.chunk_attn_fp8_paged(*args, ring=150, ratio=4, base=150), ref)
 
 
+# One tile of queries a sequence (its rows are widened in the kernel), several (widened once, before), and either in parts of a
+# long axis: b, m, h, window, ring, ratio, base, context.
+FORMS = {"one tile": (3, 1, 64, 128, 128, 4, 128, 700), "parts": (1, 1, 16, 128, 128, 4, 128, 9001),
+         "several tiles": (2, 40, 64, 64, 110, 2, 120, 500), "several tiles in parts": (1, 3, 128, 0, 0, 0, 0, 3000)}
+
+
+def of_form(name, seed=1, **more):
+    b, m, h, window, ring, ratio, base, ctx = FORMS[name]
+    first = ints(*[ctx - 97 * i for i in range(b)])
+    return (*filled(seed, b, m, h, window, ring, ratio, base, 16, first, **more), first, (window, ring, ratio, base))
+
+
+def some_tokens(q, n=7):
+    b, m = q.shape[:2]
+    every = [(i, t) for i in range(b) for t in range(m)]
+    return every[::-(-len(every) // n)]
+
+
+@gpu
+@pytest.mark.parametrize("form", FORMS)
+def test_attention_wait_that_runs_out(ds, form):
+    """With the hook on, the first tile's rows are withheld: the call ends, says so, and the next is clean."""
+    st, q, sink, first, how = of_form(form)
+    args = (dev(q), *st.on_gpu(), dev(first), dev(sink), 512 ** -0.5, how[0])
+    assert ds.device_status() == 0
+    ds.test_set_stall(True)
+    try:
+        ds.chunk_attn_fp8_paged(*args, ring=how[1], ratio=how[2], base=how[3])
+        bits = ds.device_status()
+    finally:
+        ds.test_set_stall(False)
+    assert bits == ds.DS_DEV_TIMEOUT
+    check(ds, st, q, first, sink, *how, tokens=some_tokens(q))
+
+
+@gpu
+@pytest.mark.parametrize("form", FORMS)
+def test_attention_workspace_ends(ds, form):
+    """Whatever the workspace holds, and nothing beyond it."""
+    st, q, sink, first, how = of_form(form, seed=3)
+    need = ds.chunk_attn_fp8_paged_workspace_bytes(*q.shape, how[0], how[2], 16, st.bt.shape[1])
+    ws = torch.full((need + 512,), 255, dtype=torch.uint8, device="cuda")
+    check(ds, st, q, first, sink, *how, tokens=some_tokens(q), workspace=ws[:need])
+    assert (ws[need:] == 255).all()
+
+
+@gpu
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("scale", [0.0, -0.05, 0.3])
+def test_attention_forms_at_scales(ds, form, scale):
+    st, q, sink, first, how = of_form(form, seed=5)
+    check(ds, st, q, first, sink, *how, scale=scale, tokens=some_tokens(q))
+
+
+@gpu
+@pytest.mark.parametrize("form", FORMS)
+def test_attention_forms_are_the_same_every_time(ds, form):
+    st, q, sink, first, how = of_form(form, seed=6)
+    args = (dev(q), *st.on_gpu(), dev(first), dev(sink), 512 ** -0.5, how[0])
+    ref = ds.chunk_attn_fp8_paged(*args, ring=how[1], ratio=how[2], base=how[3])
+    for _ in range(30):
+        assert torch.equal(ds.chunk_attn_fp8_paged(*args, ring=how[1], ratio=how[2], base=how[3]), ref)
+
+
+@gpu
+@pytest.mark.parametrize("m,h", [(2, 60), (1, 20), (30, 24)])
+def test_attention_forms_without_pages(ds, m, h):
+    """As in the test of rows without pages, with a tile of queries or several of them."""
+    first = ints(200, 90, 40)
+    st, q, sink = filled(6, 3, m, h, 64, 100, 4, 100, 16, first)
+    st.bt[0, 1], st.bt[0, 8], st.bt[1, :] = -1, st.pages, -7
+    bad = {0: {1, 8}, 1: set(range(st.bt.shape[1])), 2: set()}
+    check(ds, st, q, first, sink, 64, 100, 4, 100, status=ds.DS_DEV_BAD_INDEX, tokens=[(i, t) for i in range(3) for t in {0, m // 2, m - 1}],
+          rows_of=lambda i, rows: [r for r in rows if r // 16 not in bad[i]])
+
+
+@gpu
+@pytest.mark.parametrize("m,h", [(1, 20), (1, 128), (12, 20), (4, 100)])
+@pytest.mark.parametrize("k", [110, 8, -40])
+def test_attention_forms_at_exponents(ds, m, h, k):
+    """Rows of large and of tiny values beside each other (q is scaled the other way), and a block of zeros by its exponent."""
+    first = ints(300)
+    st, q, sink = filled(4, 1, m, h, 0, 0, 0, 0, 16, first)
+    at = torch.from_numpy(slots(st.bt, 0, range(300 + m), 16))
+    e = st.exps.view(-1, 16)
+    e[at] = (e[at].int() + k - torch.randint(0, 9, (300 + m, 16), generator=st.g)).to(torch.int8)
+    e[at[::5], 3] = -128                                 # counts as zeros: 448 * 2^-128 is nothing beside the others
+    check(ds, st, (q.float() * 2.0 ** -k).to(torch.bfloat16), first, sink, 0, 0, 0, 0, tokens=some_tokens(q, 4))
+
+
+@gpu
+@pytest.mark.parametrize("m,h", [(1, 16), (1, 128), (3, 128)])
+def test_attention_maximum_that_moves_in_parts(ds, m, h):
+    """A long axis of climbing, falling and flat scores: parts of a unit with references of their own."""
+    n = 4000
+    u = np.zeros(512)
+    u[::2] = 1.0
+    q = torch.from_numpy(np.broadcast_to(u * 4, (1, m, h, 512)).copy()).to(torch.bfloat16)
+    sink = torch.linspace(-3, 3, h)
+    for level in (np.linspace(-4, 4, n + m), np.linspace(4, -4, n + m), np.where(np.arange(n + m) == n // 3, 4.0, -4.0)):
+        st = Store(5, 1, n + m, 64)
+        st.put(0, range(n + m), level[:, None] * u + torch.randn((n + m, 512), generator=st.g).numpy() * 0.05)
+        check(ds, st, q, ints(n), sink, 0, 0, 0, 0)
+
+
+@gpu
+@pytest.mark.parametrize("b,m,h,ctx,ragged", [(80, 1, 128, 1300, False), (90, 1, 70, 1300, True), (7, 12, 128, 1400, False),
+                                              (5, 40, 60, 1500, True)])
+def test_attention_of_many_sequences(ds, b, m, h, ctx, ragged):
+    """A little more work than the GPU does at once: whole units, and the last ones in parts."""
+    g = torch.Generator().manual_seed(b)
+    first = torch.randint(ctx - 200, ctx + 1, (b,), generator=g, dtype=torch.int32)
+    lens = torch.randint(0, m + 1, (b,), generator=g, dtype=torch.int32) if ragged else None
+    page, top = 64, ctx + m
+    st = Store(b, b, top, page, garbage=False)
+    v = torch.randn((top, 512), generator=g).numpy()
+    for i in range(b):
+        st.put(i, range(int(first[i]) + m), np.roll(v, 31 * i, 0)[:int(first[i]) + m])
+    q = torch.randn((b, m, h, 512), generator=g).to(torch.bfloat16)
+    tokens = [(i, t) for i in range(0, b, max(1, b // 12)) for t in sorted({0, m // 2, m - 1})]
+    check(ds, st, q, first, torch.zeros(h), 0, 0, 0, 0, lens, 64, table_of(top, 64), tokens=tokens)
+
+
+@gpu
+@pytest.mark.parametrize("how", [dict(window=64, ring=70, ratio=4, base=70), dict(window=0, ring=0, ratio=0, base=0)])
+def test_attention_padding_and_empty_sequences(ds, how):
+    """lens of 0, of more than m and below 0; tokens behind a sequence's last are left as they were."""
+    for m, h in ((3, 40), (7, 40)):
+        first = ints(300, 5, 0, 90)
+        st, q, sink = filled(7, 4, m, h, page=16, first=first, **how)
+        for lens in (ints(0, 0, 0, 0), ints(-3, 1, m + 5, 0), ints(2, m, 1, m - 1)):
+            check(ds, st, q, first, sink, how["window"], how["ring"], how["ratio"], how["base"], lens)
+
+
 # ---- a run of them together -------------------------------------------------------------------------------------
 
 @gpu
@@ -925,7 +1059,8 @@ def test_attention_refusals(lib):
                 dict(window=0), dict(ring=127), dict(ring=129), dict(m=4), dict(ring=129, m=3), dict(mp=8), dict(base=129),
                 dict(ring=127, lens=FAKE)):
         assert call(f, base, **bad) == -1, bad
-    for bad in (dict(d=256), dict(h=129), dict(pages=1 << 27), dict(b=1 << 15, m=1 << 15, window=0, ring=0)):
+    for bad in (dict(d=256), dict(h=129), dict(pages=1 << 27), dict(b=1 << 15, m=1 << 15, window=0, ring=0),
+                dict(ring=(1 << 29) + 1, base=1 << 30, mp=1 << 26)):
         assert call(f, base, **bad) == -2, bad
     assert call(f, base, ws=FAKE + 16, wsb=1 << 30) == -3
     assert call(f, base, b=0, q=None, o=None, sink=None, first=None) == 0
