@@ -103,7 +103,8 @@ enum : int {
     B_O = B_QFREE + 1,        // for the output warps: the unit's last P V is done, or O^T is to be rescaled (C_EVENT)
     B_OFREE = B_O + 1,        // O^T read in both CTAs (first)
     B_INV = B_OFREE + 1,      // [2] the unit's factors (unit & 1) are there
-    B_RESCD = B_INV + 2,      // O^T rescaled in both CTAs (first)
+    B_INVFREE = B_INV + 2,    // [2] both CTAs' output warps are done with them
+    B_RESCD = B_INVFREE + 2,  // O^T rescaled in both CTAs (first)
     B_SYNC = B_RESCD + 1,     // P V so far is done (first)
     B_DRAIN = B_SYNC + 1,
     B_COUNT = B_DRAIN + 1
@@ -479,6 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             mbar_init(c.bar(B_S + i), 1);
             mbar_init(c.bar(B_P + i), 8);
             mbar_init(c.bar(B_INV + i), 4);
+            mbar_init(c.bar(B_INVFREE + i), 2 * Roles<WIDE>::kOut);
         }
         mbar_init(c.bar(B_Q), 1);
         mbar_init(c.bar(B_QFREE), 1);
@@ -978,6 +980,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                 continue;
             }
             if (half == 0) {
+                // the factors of two units ago have been read: units of one tile end faster than outputs are written
+                if (!dead) dead = !c.wait<true>(B_INVFREE + (int)(unit & 1u), (unit >> 1) + 1);
                 if (row < p.R) {
                     const float inv = l > 0.0f ? 1.0f / (l + ex2(sink2 - ref)) : (l == 0.0f ? 0.0f : l);
                     const uint32_t at = c.bars + C_INV + ((unit & 1u) * 128 + rq) * 4;
@@ -1146,7 +1150,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                     to += G * D;
                 }
             }
-            if (some && !split) ++unit;
+            if (!split) {                                    // (units without rows have gone on above)
+                __syncwarp();
+                if (lane < 2) arrive_operand(mapa(c.bar(B_INVFREE + (int)(unit & 1u)), (uint32_t)lane));
+                ++unit;
+            }
         }
         if (__any_sync(kAll, bad) && lane == 0) flag_status(p.a.status, DS_DEV_BAD_INDEX);
     }

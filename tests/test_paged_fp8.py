@@ -920,6 +920,18 @@ def test_attention_of_many_sequences(ds, b, m, h, ctx, ragged):
 
 
 @gpu
+@pytest.mark.parametrize("b,m,h", [(126, 93, 2), (2, 700, 100), (400, 1, 2), (300, 1, 128), (90, 5, 23)])
+def test_attention_of_one_row_a_query(ds, b, m, h):
+    """Units of a single tile, one behind the other: their factors must not meet."""
+    first = torch.arange(b, dtype=torch.int32) % 11
+    st, q, sink = filled(2, b, m, h, 1, m, 0, 0, 64, first)
+    args = (dev(q), *st.on_gpu(), dev(first), dev(sink), 512 ** -0.5, 1)
+    o = check(ds, st, q, first, sink, 1, m, 0, 0)
+    for _ in range(20):
+        assert torch.equal(ds.chunk_attn_fp8_paged(*args, ring=m), o)
+
+
+@gpu
 @pytest.mark.parametrize("how", [dict(window=64, ring=70, ratio=4, base=70), dict(window=0, ring=0, ratio=0, base=0)])
 def test_attention_padding_and_empty_sequences(ds, how):
     """lens of 0, of more than m and below 0; tokens behind a sequence's last are left as they were."""
