@@ -126,7 +126,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 
 struct Params {
     Args a;
-    Divisor h, page, ring, b, parts;
+    Divisor h, page, ring, b, parts, ratio;   // (a 64-bit division takes a warp half a microsecond, and every role makes its units)
     int R;               // query rows of a CTA: 64, 32 or 16
     int nqt;             // query tiles of a sequence
     uint32_t units;      // whole ones, then parts of the others
@@ -194,7 +194,6 @@ __device__ __forceinline__ Ahead look(const Params &p, uint32_t u) {
 
 // a: look(p, u)
 __device__ __forceinline__ void make_unit(const Params &p, uint32_t u, const Ahead &a, Unit &x) {
-    const int parts = u < p.whole ? 1 : (int)p.parts.d;
     x.bi = (int)a.at.bi;
     x.part = (int)a.at.part;
     x.first = a.first;
@@ -217,7 +216,7 @@ __device__ __forceinline__ void make_unit(const Params &p, uint32_t u, const Ahe
     }
     x.nw = (int)max((int64_t)0, end - x.wlo);
     if (p.a.ratio) {
-        int64_t nc = (hi + 1) / p.a.ratio;
+        int64_t nc = p.ratio.div((uint32_t)(hi + 1), rest);
         if (nc > p.cap - p.a.base) {
             nc = max((int64_t)0, p.cap - p.a.base);
             x.clipped = true;
@@ -225,9 +224,11 @@ __device__ __forceinline__ void make_unit(const Params &p, uint32_t u, const Ahe
         x.nc = (int)nc;
     }
     x.nwp = p.rows && x.nc ? (x.nw + BN - 1) / BN * BN : x.nw;      // WIDE: compressed rows begin a tile
-    const int64_t nt = (x.nwp + x.nc + BN - 1) / BN;
-    x.t0 = (int)(nt * x.part / parts);
-    x.t1 = (int)(nt * (x.part + 1) / parts);
+    x.t1 = (int)((uint32_t)(x.nwp + x.nc + BN - 1) / BN);
+    if (u >= p.whole) {                      // (at most 2^23 tiles, of at most 64 parts)
+        x.t0 = (int)p.parts.div((uint32_t)(x.t1 * x.part), rest);
+        x.t1 = (int)p.parts.div((uint32_t)(x.t1 * (x.part + 1)), rest);
+    }
 }
 
 // What is left of a unit for whoever fetches its rows.
@@ -866,7 +867,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             if (live && pos >= 0) {
                 a0 = p.a.window ? (int)max((int64_t)0, pos - p.a.window + 1 - x.wlo) : 0;
                 a1 = (int)min(pos + 1 - x.wlo, (int64_t)x.nw);
-                c1 = x.nwp + (p.a.ratio ? (int)min((pos + 1) / p.a.ratio, (int64_t)x.nc) : 0);
+                uint32_t rest;
+                c1 = x.nwp + (p.a.ratio ? min((int)p.ratio.div((uint32_t)(pos + 1), rest), x.nc) : 0);
             }
             const List list = list_of(p, x);
             float ref = sink2 - 64.0f, l = 0.0f;
@@ -890,7 +892,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                     tmem_ld_wait(s);
                     tc_fence_before();
                     const bool whole = __all_sync(kAll, mask == ~0ull);
-                    float m = -INFINITY;
                     if (p.scale_log2 <= 0.0f) {
                         const float f = p.scale_log2 < 0.0f ? -1.0f : 0.0f;
 #pragma unroll
@@ -905,10 +906,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                                 if (!((mk >> i) & 1u)) s[g][i] = 0xff800000u;
                         }
                     }
+                    float mm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};     // four chains: a chain of 32 is 0.1 us
 #pragma unroll
-                    for (int g = 0; g < 2; ++g)
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) m = max3(m, __uint_as_float(s[g][i]), __uint_as_float(s[g][i + 1]));
+                    for (int i = 0; i < 64; i += 2)
+                        mm[(i >> 1) & 3] = max3(mm[(i >> 1) & 3], __uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
+                    float m = fmaxf(max3(mm[0], mm[1], mm[2]), mm[3]);
                     m = m == -INFINITY ? m : m * scale;
                     m = fmaxf(m, exchange(m));
                     const int q = (int)rank * p.R + row;
@@ -1195,7 +1197,8 @@ __global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__
         const int n = p.a.lens ? max(0, min(__ldg(p.a.lens + bi), p.a.m)) : p.a.m, i = i0 + threadIdx.x;
         const int64_t first = __ldg(p.a.first + bi), end = first + n;          // positions below end are seen
         const int64_t wbase = p.a.window ? max((int64_t)0, first - p.a.window + 1) : 0;
-        int64_t count = comp ? (end > 0 ? end / p.a.ratio : 0) : max((int64_t)0, end - wbase);
+        uint32_t rest;
+        int64_t count = comp ? (end > 0 ? (int64_t)p.ratio.div((uint32_t)end, rest) : 0) : max((int64_t)0, end - wbase);
         if (comp) count = min(count, max((int64_t)0, p.cap - p.a.base));
         else if (!p.a.ring) count = min(count, max((int64_t)0, p.cap - wbase));
         int at = -2;
@@ -1478,7 +1481,7 @@ int launch_chunk_attn_fp8(const chunk::Args &a, cudaStream_t stream) {
     if (a.workspace_bytes < need || (need && !a.workspace)) return DS_EWORKSPACE;
     char *ws = static_cast<char *>(a.workspace);
     Params p{a, Divisor((uint32_t)a.h), Divisor((uint32_t)a.page), Divisor((uint32_t)std::max(a.ring, 1)), Divisor((uint32_t)a.b),
-             Divisor((uint32_t)pl.parts), pl.R, pl.nqt, (uint32_t)pl.units, (uint32_t)pl.whole, Divisor((uint32_t)pl.clusters),
+             Divisor((uint32_t)pl.parts), Divisor((uint32_t)std::max(a.ratio, 1)), pl.R, pl.nqt, (uint32_t)pl.units, (uint32_t)pl.whole, Divisor((uint32_t)pl.clusters),
              std::min<int64_t>((int64_t)a.max_pages * a.page, kMaxRows), a.scale * kLog2e,
              reinterpret_cast<float *>(ws + (pl.wide ? rows_bytes(pl, a.b) : 0)), pl.wide ? reinterpret_cast<uint16_t *>(ws) : nullptr, pl.wrows, pl.crows,
              g_test_stall.load(std::memory_order_relaxed)};
