@@ -541,7 +541,7 @@ int ds_kv_read_fp4_paged(const uint8_t *codes, const int8_t *exps, int64_t pages
  * ds_sparse_attn.  The rows that queries of a sequence see must be finite in bf16 (their largest code times
  * 2^k below 2^128), and scale * q, the scores and the products that are added up finite in f32.  Rows
  * that no query of the sequence sees do not matter, nor does what unused pages hold.  A block whose exponent is -128
- * counts as zeros (ds_kv_append_fp8_paged stores none below -22).
+ * counts as zeros (ds_kv_append_fp8_paged stores none below -22), and a NaN code, which no finite row has, as +-480.
  *
  * q          device bf16 [b][m][h][512]
  * sink       device f32 [h]
@@ -554,7 +554,7 @@ int ds_kv_read_fp4_paged(const uint8_t *codes, const int8_t *exps, int64_t pages
  * workspace  at least ds_chunk_attn_fp8_paged_workspace_bytes bytes for the same arguments, 256-byte aligned (may
  *            be NULL when that size is 0); its contents need no initialisation and mean nothing afterwards.
  *            Calls that may run at the same time need one each.  It holds partial results of long sequences, and, where
- *            a sequence has more than 128 query rows (m * h), the block table's rows in bf16, up to 2 GB of them
+ *            a sequence has more than 256 query rows (m * h), the block table's rows in bf16, up to 2 GB of them
  * Supported: d = 512, 1 <= h <= 128, b * m * h < 2^31, pages * page < 2^31, ring <= 2^29; q, o, codes and exps 16-byte
  * aligned.
  * Errors: DS_EINVAL, DS_EUNSUPPORTED, DS_EWORKSPACE, DS_ECUDA.

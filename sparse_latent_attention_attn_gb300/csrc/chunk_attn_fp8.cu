@@ -18,14 +18,14 @@
 // take 0.75 + 0.53 us (23.3 ns for each of 32, 32.9 ns for each of 16, measured), 0.85 of the tensor cores' rate.
 //
 // A code widens to bf16 exactly (at most four significant bits; its bits moved to a bf16's, times 2^(120 + k)).  Two forms:
-//   * Sequences with one tile of queries (decoding): each row is read once, as codes, and widened in registers on its way into
+//   * Sequences with one or two tiles of queries (decoding): each row is read once a tile, as codes, and widened in registers on its way into
 //     shared memory, which spares a copy in HBM: 33/32 byte a value is all that is read.  Each CTA widens its 64 rows once,
 //     as K; for P V it needs its half of d of all 128, copied from K in the layout that it has: its own rows by a warp, the
 //     other CTA's by the copy engine, 8 KB each (the engine with both takes 2 us a tile).  K is held until its copies have been
 //     read, and V is filled when the last tile's P V is done, so the copies stand between two tiles: 3.3 us a tile where the
 //     MMAs take 1.28.  (The rows passed through a ring in the workspace instead, V by TMA: 204 -> 241 us for 256 sequences of
 //     2176 rows; V widened a second time by eight more warps: 252 -> 370.)
-//   * Sequences with several (WIDE; prompts): several units read the same rows, so a kernel before widens them once, into the
+//   * Sequences with more (WIDE; prompts): several units read the same rows, so a kernel before widens them once, into the
 //     workspace, and K and V come by TMA: 1.5 us a tile, and some 4 us between units, in which q is loaded and O^T read.
 // An operand half is handed back as soon as its readers are done.
 //
@@ -1250,11 +1250,10 @@ __global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__
 // ---- parts of a unit joined ------------------------------------------------------------------------------------
 
 constexpr int kMaxParts = 64;
-// Query tiles of a sequence from which its rows are widened once, in a pass of their own.  With two tiles that takes 0.83 of the
-// time (64 sequences, 2 tokens of 128 heads, 2176 rows: 119 us instead of 142; with three tiles, 32 sequences: 77 instead of
-// 104); with one tile 1.06 of it (32 sequences of 4224 rows: 79 instead of 74 us; 128 rows: 19.9 instead of 15), but for
-// single sequences (0.9).
-constexpr int kWideTiles = 2;
+// Query tiles of a sequence from which its rows are widened once, in a pass of their own: with three tiles that takes 0.87 of
+// the time (32 sequences, 3 tokens of 128 heads, 2176 rows: 74 us instead of 85), with two 1.02 (64 sequences, 2 tokens: 117
+// instead of 114), with one 1.3 (32 sequences of 4224 rows: 78 instead of 59 us; 128 rows: 19.0 instead of 13.6).
+constexpr int kWideTiles = 3;
 
 // One query row a block; thread i has values 4 i .. 4 i + 3.  Each part has its reference, its sum and its O^T.
 __global__ void __launch_bounds__(128) chunk_merge_kernel(const __grid_constant__ Params p) {
