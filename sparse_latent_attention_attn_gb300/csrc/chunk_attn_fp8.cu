@@ -1000,7 +1000,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
         if constexpr (!WIDE) setmaxnreg_inc<REG_OUT>();
         // ================================== output, and O^T's rescaling ==================================
         // Thread (warp w, lane) has d = 256 rank + 128 v + 32 w + lane of every query: column q of O^T's block v.
-        const int w = warp & 3, vlo = WIDE ? (warp - W_OUT) >> 2 : 0, vhi = WIDE ? vlo + 1 : 2;   // its blocks
+        // Of eight warps, those of one lane quarter share it by queries, 64 each: the rotation falls on two quarters of the second
+        // block, and a warp that had all of that kept O^T 1.7 us longer (prompt of 4096 tokens: 384 us, 339 without a rotation).
+        const int w = warp & 3, q0 = WIDE ? ((warp - W_OUT) >> 2) * 64 : 0, q1 = WIDE ? q0 + 64 : 128;   // its queries
         const uint32_t tm = tmem + ((uint32_t)(w * 32) << 16) + TM_O;
         const uint32_t free_bar = first_bar(B_OFREE), resc_bar = first_bar(B_RESCD);
         const int16_t *alpha = reinterpret_cast<const int16_t *>(ctl_mem + C_ALPHA);
@@ -1022,12 +1024,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                     const uint32_t e = *reinterpret_cast<volatile uint32_t *>(ctl_mem + C_EVENT + 4 * (event & 1u));
                     if (e >> 1 != event + 1) break;
                     tc_fence_after();
-                    for (int g = 0; g < nq; g += 32) {
+                    for (int g = q0; g < min(nq, q1); g += 32) {
                         const int up = *reinterpret_cast<const volatile int16_t *>(alpha + (e & 1u) * 128 + g + lane);
                         if (!__any_sync(kAll, up != 0)) continue;
                         const float f = ex2(-(float)up);
 #pragma unroll 1
-                        for (int v = vlo; v < vhi; ++v) {
+                        for (int v = 0; v < 2; ++v) {
                             uint32_t r[32];
                             tmem_ld32(tm + v * 128 + g, r);
                             tmem_ld_wait(r);
@@ -1053,8 +1055,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             float *part = split ? p.ws + (size_t)(u - p.whole) * (D + 2) * nq : nullptr;
             if (!some) {                                     // nothing seen: zeros, which no rotation changes
                 if (there <= 0) continue;
-                for (int q = 0; q < nq && q < there; ++q)
-                    for (int v = vlo; v < vhi; ++v) o[(int64_t)q * D + d0 + 128 * v] = 0;
+                for (int q = q0; q < min(min(nq, q1), there); ++q)
+                    for (int v = 0; v < 2; ++v) o[(int64_t)q * D + d0 + 128 * v] = 0;
                 const int64_t pos0 = (int64_t)x.first + p.h.div((uint32_t)x.r0, hh);
                 const int64_t pos1 = (int64_t)x.first + p.h.div((uint32_t)(x.r0 + min(nq, there) - 1), hh);
                 bad |= p.a.rd > 0 && (pos0 < 0 || pos1 >= p.a.table_rows);
@@ -1068,14 +1070,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             // 32 queries of a block at a time: issuing a load of tensor memory takes a warp some 150 cycles whatever its size
             // (steps of eight queries took 540 cycles each, a unit 4.4 us).
             constexpr int G = 32;
-            const int last = ((min(nq, there) + G - 1) / G - 1) * G;
+            const int last = ((min(min(nq, q1), there) + G - 1) / G - 1) * G;
+            if (last < q0) {                                 // none of its queries is there
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_operand(free_bar);
+            }
 #pragma unroll 1
-            for (int v = vlo; v < vhi; ++v) {
+            for (int v = 0; v < 2; ++v) {
                 const int d = d0 + 128 * v, pair = (d - (D - p.a.rd)) >> 1;
                 const bool rot = !split && p.a.rd > 0 && 256 * (int)rank + 128 * v + 32 * w + 31 >= D - p.a.rd;
                 const bool odd = d & 1;
                 const float2 *angles = rot && pair >= 0 ? p.a.table + pos0 * half_rd + pair : nullptr;
-                int at = (int)hh, tok = 0;                   // the next query's head and token
+                uint32_t head;                               // the next query's head and token
+                int tok = (int)p.h.div(hh + (uint32_t)q0, head), at = (int)head;
                 auto angle = [&]() -> float2 {
                     const bool in = tok >= in0 && tok < in1;
                     bad |= !in;
@@ -1090,10 +1098,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                         if (angles) angles += half_rd;
                     }
                 };
-                uint16_t *to = o + d;
-                float *top = split ? part + d : nullptr;
+                if (angles) angles += tok * half_rd;
+                uint16_t *to = o + d + q0 * D;
+                float *top = split ? part + d + q0 * D : nullptr;
 #pragma unroll 1
-                for (int g = 0; g <= last; g += G) {
+                for (int g = q0; g <= last; g += G) {
                     uint32_t r[G];
                     tmem_ld32(tm + v * 128 + g, r);
                     float2 c8[4];                            // angles of eight queries that one token has
@@ -1104,7 +1113,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                         ones = 15;
                     }
                     tmem_ld_wait(r);
-                    if (g == last && v == vhi - 1) {
+                    if (g == last && v == 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) arrive_operand(free_bar);
