@@ -1264,7 +1264,11 @@ constexpr int kMaxParts = 64;
 // instead of 114), with one 1.3 (32 sequences of 4224 rows: 78 instead of 59 us; 128 rows: 19.0 instead of 13.6).
 constexpr int kWideTiles = 3;
 
-// One query row a block; thread i has values 4 i .. 4 i + 3.  Each part has its reference, its sum and its O^T.
+// One query row a block; thread i has values 4 i .. 4 i + 3.  Each part has its reference, its sum and its O^T, and kFlight parts
+// are read at once.  With few parts 16 in flight cost occupancy (two parts of 32 sequences: 62 us a call instead of 58, nine of 16
+// sequences 105 instead of 103), with many they save latency (44 parts: 21 instead of 25, 18 of four sequences 18 instead of 22).
+constexpr int kManyParts = 12;
+template <int kFlight>
 __global__ void __launch_bounds__(128) chunk_merge_kernel(const __grid_constant__ Params p) {
     grid_dependency_wait();
     const uint32_t tile = blockIdx.x;               // of those that are in parts
@@ -1303,15 +1307,24 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const __grid_constant_
     const float inv = den == 0.0f ? 0.0f : 1.0f / (den + ex2(sink2 - top));
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float *src = ws + (size_t)q * D + 4 * threadIdx.x;
-#pragma unroll 4
-    for (int k = 0; k < np; ++k) {
-        const float f = __shfl_sync(kAll, k < 32 ? wgt[0] : wgt[1], k & 31);
-        if (f == 0.0f) continue;                    // a part without rows wrote none
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + k * slot));
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
+    for (int k0 = 0; k0 < np; k0 += kFlight) {
+        float f[kFlight];
+        float4 v[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const int k = k0 + i;
+            f[i] = __shfl_sync(kAll, k < 32 ? wgt[0] : wgt[1], k & 31);
+            v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (k < np && f[i] != 0.0f) v[i] = __ldcg(reinterpret_cast<const float4 *>(src + k * slot));   // a part without rows wrote none
+            else f[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            acc.x = fmaf(f[i], v[i].x, acc.x);
+            acc.y = fmaf(f[i], v[i].y, acc.y);
+            acc.z = fmaf(f[i], v[i].z, acc.z);
+            acc.w = fmaf(f[i], v[i].w, acc.w);
+        }
     }
     acc.x *= inv;
     acc.y *= inv;
@@ -1420,9 +1433,10 @@ struct Plan {
 // Rows widened once in a pass of their own (wide) when several units of a sequence read them, and they take no more than
 // 2 GB.
 // Parts of a unit: with fewer units than clusters, the number of least estimated time, in tiles: rounds of units, each its
-// tiles and two for its ends, and from two parts on the merge.  With more, those of a last round that would leave
-// half of the clusters or more without work are cut into as many parts as there are clusters for, where that saves
-// more than the merge takes (8 tiles' time).
+// tiles and two for its ends, and from two parts on 1 + 0.02 k for the merge (at 3 + 0.05 k units of four tiles stayed whole: one
+// sequence of 448 rows and 128 heads 18.1 us instead of 15.1; all else was the same).  With more, those of a last round
+// that would leave half of the clusters or more without work are cut into as many parts as there are clusters for, where
+// that saves more than the merge takes (8 tiles' time).
 bool plan(int b, int m, int h, int window, int ratio, int page, int max_pages, Plan &pl) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
@@ -1447,7 +1461,7 @@ bool plan(int b, int m, int h, int window, int ratio, int page, int max_pages, P
         double least = 1e30;
         for (int k = 1; k <= kMaxParts && k <= tiles; ++k) {
             const double rounds = (double)((units * k + g - 1) / g);
-            const double cost = rounds * ((double)((tiles + k - 1) / k) + 2.0) + (k > 1 ? 3.0 + 0.05 * k : 0.0);
+            const double cost = rounds * ((double)((tiles + k - 1) / k) + 2.0) + (k > 1 ? 1.0 + 0.02 * k : 0.0);
             if (cost < least) {
                 least = cost;
                 pl.parts = k;
@@ -1527,7 +1541,7 @@ int launch_chunk_attn_fp8(const chunk::Args &a, cudaStream_t stream) {
         cfg.gridDim = dim3((unsigned)((pl.units - pl.whole) / pl.parts), (unsigned)(2 * pl.R), 1);
         cfg.blockDim = dim3(128, 1, 1);
         cfg.dynamicSmemBytes = 0;
-        if (cudaLaunchKernelEx(&cfg, chunk_merge_kernel, p) != cudaSuccess) return launch_failed();
+        if (cudaLaunchKernelEx(&cfg, pl.parts > kManyParts ? chunk_merge_kernel<16> : chunk_merge_kernel<4>, p) != cudaSuccess) return launch_failed();
     }
     return DS_OK;
 }
