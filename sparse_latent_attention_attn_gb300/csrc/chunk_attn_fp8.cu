@@ -18,13 +18,13 @@
 // take 0.75 + 0.53 us (23.3 ns for each of 32, 32.9 ns for each of 16, measured), 0.85 of the tensor cores' rate.
 //
 // A code widens to bf16 exactly (at most four significant bits; its bits moved to a bf16's, times 2^(120 + k)).  Two forms:
-//   * Sequences with one or two tiles of queries (decoding): each row is read once a tile, as codes, and widened in registers on its way into
-//     shared memory, which spares a copy in HBM: 33/32 byte a value is all that is read.  Each CTA widens its 64 rows once,
-//     as K; for P V it needs its half of d of all 128, copied from K in the layout that it has: its own rows by a warp, the
-//     other CTA's by the copy engine, 8 KB each (the engine with both takes 2 us a tile).  K is held until its copies have been
-//     read, and V is filled when the last tile's P V is done, so the copies stand between two tiles: 3.3 us a tile where the
-//     MMAs take 1.28.  (The rows passed through a ring in the workspace instead, V by TMA: 204 -> 241 us for 256 sequences of
-//     2176 rows; V widened a second time by eight more warps: 252 -> 370.)
+//   * Sequences with one or two tiles of queries (decoding): each row is read once a tile, as codes, and widened in registers
+//     on its way into shared memory, which spares a copy in HBM: 33/32 byte a value is all that is read.  Each CTA widens its
+//     64 rows once, as K; for P V it needs its half of d of all 128, copied from K in the layout that it has: its own rows by
+//     a warp, the other CTA's by the copy engine, 8 KB each (the engine with both takes 2 us a tile).  K is held until its
+//     copies have been read, and V is filled when the last tile's P V is done, so the copies stand between two tiles: 3.3 us
+//     a tile where the MMAs take 1.28.  (The rows passed through a ring in the workspace instead, V by TMA: 204 -> 241 us for
+//     256 sequences of 2176 rows; V widened a second time by eight more warps: 252 -> 370.)
 //   * Sequences with more (WIDE; prompts): several units read the same rows, so a kernel before widens them once, into the
 //     workspace, and K and V come by TMA: 1.5 us a tile, and some 4 us between units, in which q is loaded and O^T read.
 // An operand half is handed back as soon as its readers are done.
@@ -41,8 +41,8 @@
 // Warps: 0-3 softmax; from 4 on output (and O^T's rescaling, on request): four, or eight with WIDE; 8-15 widen; one issues the
 // MMAs (in the cluster's first CTA, for both); one fetches q by TMA; two have the halves of K copied to V, or bring K and V.
 // What bounds the small calls is instructions: roles share their SM's issue slots and instruction caches, so a body that
-// is twice as long costs other roles time too.  Every wait gives up after 2 s, or 60 s
-// where it lasts as long as a unit (DS_DEV_TIMEOUT).
+// is twice as long costs other roles time too.  Every wait gives up after 2 s, or 60 s where it lasts as long as a unit
+// (DS_DEV_TIMEOUT).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -313,6 +313,10 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
                  "h"((uint16_t)3)
                  : "memory");
+}
+// The same in the issuing CTA only.
+__device__ __forceinline__ void commit_first(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 // bf16 A and B, f32 accumulator; A K-major or MN-major, B K-major
 __host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn) {
@@ -595,240 +599,241 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
         }
         if (__any_sync(kAll, bad) && lane == 0) flag_status(p.a.status, DS_DEV_BAD_INDEX);
     } else if (warp >= W_MMA) {
-      if constexpr (!WIDE) setmaxnreg_dec<REG_MMA>();
-      if (warp == W_MMA) {
-        // ======================================== MMA issue ========================================
-        // The first CTA's warp walks the loop (its conditions are votes), an elected lane issues for both.  S of the next tile
-        // goes before P V of this one when both can.
-        if (rank == 0) {
-            const uint32_t i_s = idesc(128, BN, false), i_pv = idesc(256, 2 * p.R, true);
-            const uint64_t qd = smem_desc_sw128(base + SM_Q, 16, 1024), kd = smem_desc_sw128(base + SM_K, 16, 1024);
-            const uint64_t vd = smem_desc_sw128(base + SM_V, V_CHUNK, 1024), pd = smem_desc_sw128(base + SM_P, 16, 1024);
-            volatile int *cnt = reinterpret_cast<volatile int *>(ctl_mem + C_CNT);
-            volatile int *resc = reinterpret_cast<volatile int *>(ctl_mem + C_RESC);
-            auto done = [&](int b, uint32_t phase) -> bool { return __all_sync(kAll, mbar_test_wait(c.bar(b), phase & 1u)); };
-            uint32_t u = cid;                      // S: its unit, that unit's tiles left, units begun
-            int s_left = 0;
-            uint32_t s_unit = 0, v_unit = 0;
-            int v_left = 0;
-            Ahead ahead = look(p, u);
-            auto begin = [&]() {                   // the next unit with tiles
-                while (u < p.units) {
+        if constexpr (!WIDE) setmaxnreg_dec<REG_MMA>();
+        if (warp == W_MMA) {
+            // ======================================== MMA issue ========================================
+            // The first CTA's warp walks the loop (its conditions are votes), an elected lane issues for both.  S of the next tile
+            // goes before P V of this one when both can.
+            if (rank == 0) {
+                const uint32_t i_s = idesc(128, BN, false), i_pv = idesc(256, 2 * p.R, true);
+                const uint64_t qd = smem_desc_sw128(base + SM_Q, 16, 1024), kd = smem_desc_sw128(base + SM_K, 16, 1024);
+                const uint64_t vd = smem_desc_sw128(base + SM_V, V_CHUNK, 1024), pd = smem_desc_sw128(base + SM_P, 16, 1024);
+                volatile int *cnt = reinterpret_cast<volatile int *>(ctl_mem + C_CNT);
+                volatile int *resc = reinterpret_cast<volatile int *>(ctl_mem + C_RESC);
+                auto done = [&](int b, uint32_t phase) -> bool { return __all_sync(kAll, mbar_test_wait(c.bar(b), phase & 1u)); };
+                uint32_t u = cid;                      // S: its unit, that unit's tiles left, units begun
+                int s_left = 0;
+                uint32_t s_unit = 0, v_unit = 0;
+                int v_left = 0;
+                Ahead ahead = look(p, u);
+                auto begin = [&]() {                   // the next unit with tiles
+                    while (u < p.units) {
+                        Unit x;
+                        make_unit(p, u, ahead, x);
+                        u += ncl;
+                        ahead = look(p, u);
+                        if (x.t1 > x.t0) {
+                            s_left = x.t1 - x.t0;
+                            __syncwarp();
+                            cnt[s_unit & 3u] = s_left;
+                            ++s_unit;
+                            return;
+                        }
+                    }
+                    s_left = 0;
+                };
+                uint32_t sJ = 0, vJ = 0, s_half = 0, v_half = 0, resc_n = 0, event = 0, idle = 0;   // event: phases of B_O
+                bool s_first = true, v_first = true;
+                uint64_t since = 0;
+                begin();
+                while (s_left > 0 || vJ < sJ) {
+                    if (s_left > 0 && sJ - vJ < 2 && s_half == 0 && done(B_KFULL, sJ) && (!s_first || done(B_Q, s_unit - 1))) {
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const uint64_t at = (uint64_t)((((k >> 2) + (!WIDE && k >= 8 ? 2 : 0)) * K_CHUNK + (k & 3) * 32) >> 4);
+                                mma_pair(tmem + TM_S + (sJ & 1u) * 64, qd + at, kd + at, i_s, k > 0);
+                            }
+                            commit_pair(c.bar(B_KFREE));
+                        }
+                        __syncwarp();
+                        s_half = 1;
+                        idle = 0;
+                    } else if (s_half == 1 && done(B_KFULL + 1, sJ)) {
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const uint64_t at = (uint64_t)((((k >> 2) + (WIDE || k >= 8 ? 4 : 2)) * K_CHUNK + (k & 3) * 32) >> 4);
+                                mma_pair(tmem + TM_S + (sJ & 1u) * 64, qd + at, kd + at, i_s, 1);
+                            }
+                            commit_pair(c.bar(B_S + (int)(sJ & 1u)));
+                            commit_pair(c.bar(B_KFREE + 1));
+                            if (s_left == 1) commit_pair(c.bar(B_QFREE));
+                        }
+                        __syncwarp();
+                        s_half = 0;
+                        s_first = false;
+                        ++sJ;
+                        if (--s_left == 0) {
+                            begin();
+                            s_first = true;
+                        }
+                        idle = 0;
+                    } else if (vJ < sJ && v_half == 0 && done(B_P + (int)(vJ & 1u), vJ >> 1) && done(B_VFULL, vJ) &&
+                               (!v_first || v_unit == 0 || done(B_OFREE, v_unit - 1))) {
+                        if (v_first) v_left = cnt[v_unit & 3u];
+                        tc_fence_after();
+                        (void)test_wait_cluster(c.bar(B_P + (int)(vJ & 1u)), (vJ >> 1) & 1u);   // again, for what the other CTA wrote here
+                        if (__any_sync(kAll, resc[vJ & 1u] == (int)(vJ + 1))) {
+                            // a reference has moved: O^T of the tiles before this one is scaled first
+                            if (elect_one()) commit_first(c.bar(B_SYNC));
+                            __syncwarp();
+                            if (!c.wait<true>(B_SYNC, resc_n)) break;
+                            if (lane < 2) {
+                                st_cluster_u32(mapa(c.bars + C_EVENT + 4 * (event & 1u), (uint32_t)lane), 2 * (event + 1) + (vJ & 1u));
+                                arrive_cluster(mapa(c.bar(B_O), (uint32_t)lane));
+                            }
+                            ++event;
+                            if (!c.wait<true>(B_RESCD, resc_n)) break;
+                            ++resc_n;
+                            tc_fence_after();
+                        }
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                mma_pair(tmem + TM_O, vd + (uint64_t)((k * 2048) >> 4),
+                                         pd + (uint64_t)(((vJ & 1u) * P_BYTES + (k >> 2) * K_CHUNK + (k & 3) * 32) >> 4), i_pv,
+                                         k > 0 || !v_first);
+                            commit_pair(c.bar(B_VFREE));
+                        }
+                        __syncwarp();
+                        v_half = 1;
+                        idle = 0;
+                    } else if (v_half == 1 && done(B_VFULL + 1, vJ)) {
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                mma_pair(tmem + TM_O + 128, vd + (uint64_t)((2 * V_CHUNK + k * 2048) >> 4),
+                                         pd + (uint64_t)(((vJ & 1u) * P_BYTES + (k >> 2) * K_CHUNK + (k & 3) * 32) >> 4), i_pv,
+                                         k > 0 || !v_first);
+                            commit_pair(c.bar(B_VFREE + 1));
+                            if (v_left == 1) commit_pair(c.bar(B_O));
+                        }
+                        __syncwarp();
+                        v_half = 0;
+                        v_first = false;
+                        ++vJ;
+                        if (--v_left == 0) {
+                            ++v_unit;
+                            ++event;
+                            v_first = true;
+                        }
+                        idle = 0;
+                    } else {
+                        __nanosleep(20);
+                        if ((++idle & 63u) == 0u) {
+                            const uint64_t now = globaltimer_ns();
+                            if (idle == 64u) since = now;
+                            else if (now - since > kWaitLimitNs) c.give_up();
+                            if (__any_sync(kAll, *c.abort != 0)) break;
+                        }
+                    }
+                }
+                if (elect_one()) commit_pair(c.bar(B_DRAIN));
+                __syncwarp();
+            }
+        } else if (warp == W_Q) {
+            // ======================================== q by TMA ========================================
+            if (lane == 0) {
+                const uint32_t full = first_bar(B_Q);
+                uint32_t n = 0;
+                Ahead ahead = look(p, cid);
+                for (uint32_t u = cid; u < p.units; u += ncl) {
                     Unit x;
                     make_unit(p, u, ahead, x);
-                    u += ncl;
-                    ahead = look(p, u);
-                    if (x.t1 > x.t0) {
-                        s_left = x.t1 - x.t0;
-                        __syncwarp();
-                        cnt[s_unit & 3u] = s_left;
-                        ++s_unit;
-                        return;
+                    ahead = look(p, u + ncl);
+                    if (x.t1 <= x.t0) continue;
+                    if (!mbar_wait(c.bar(B_QFREE), (n & 1u) ^ 1u, c.abort, kUnitLimitNs)) {
+                        c.give_up();
+                        break;
                     }
-                }
-                s_left = 0;
-            };
-            uint32_t sJ = 0, vJ = 0, s_half = 0, v_half = 0, resc_n = 0, event = 0, idle = 0;   // event: phases of B_O
-            bool s_first = true, v_first = true;
-            uint64_t since = 0;
-            begin();
-            while (s_left > 0 || vJ < sJ) {
-                if (s_left > 0 && sJ - vJ < 2 && s_half == 0 && done(B_KFULL, sJ) && (!s_first || done(B_Q, s_unit - 1))) {
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const uint64_t at = (uint64_t)((((k >> 2) + (!WIDE && k >= 8 ? 2 : 0)) * K_CHUNK + (k & 3) * 32) >> 4);
-                            mma_pair(tmem + TM_S + (sJ & 1u) * 64, qd + at, kd + at, i_s, k > 0);
-                        }
-                        commit_pair(c.bar(B_KFREE));
-                    }
-                    __syncwarp();
-                    s_half = 1;
-                    idle = 0;
-                } else if (s_half == 1 && done(B_KFULL + 1, sJ)) {
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const uint64_t at = (uint64_t)((((k >> 2) + (WIDE || k >= 8 ? 4 : 2)) * K_CHUNK + (k & 3) * 32) >> 4);
-                            mma_pair(tmem + TM_S + (sJ & 1u) * 64, qd + at, kd + at, i_s, 1);
-                        }
-                        commit_pair(c.bar(B_S + (int)(sJ & 1u)));
-                        commit_pair(c.bar(B_KFREE + 1));
-                        if (s_left == 1) commit_pair(c.bar(B_QFREE));
-                    }
-                    __syncwarp();
-                    s_half = 0;
-                    s_first = false;
-                    ++sJ;
-                    if (--s_left == 0) {
-                        begin();
-                        s_first = true;
-                    }
-                    idle = 0;
-                } else if (vJ < sJ && v_half == 0 && done(B_P + (int)(vJ & 1u), vJ >> 1) && done(B_VFULL, vJ) &&
-                           (!v_first || v_unit == 0 || done(B_OFREE, v_unit - 1))) {
-                    if (v_first) v_left = cnt[v_unit & 3u];
-                    tc_fence_after();
-                    (void)test_wait_cluster(c.bar(B_P + (int)(vJ & 1u)), (vJ >> 1) & 1u);   // again, for what the other CTA wrote here
-                    if (__any_sync(kAll, resc[vJ & 1u] == (int)(vJ + 1))) {
-                        // a reference has moved: O^T of the tiles before this one is scaled first
-                        if (elect_one()) asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(c.bar(B_SYNC)) : "memory");
-                        __syncwarp();
-                        if (!c.wait<true>(B_SYNC, resc_n)) break;
-                        if (lane < 2) {
-                            st_cluster_u32(mapa(c.bars + C_EVENT + 4 * (event & 1u), (uint32_t)lane), 2 * (event + 1) + (vJ & 1u));
-                            arrive_cluster(mapa(c.bar(B_O), (uint32_t)lane));
-                        }
-                        ++event;
-                        if (!c.wait<true>(B_RESCD, resc_n)) break;
-                        ++resc_n;
-                        tc_fence_after();
-                    }
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_pair(tmem + TM_O, vd + (uint64_t)((k * 2048) >> 4),
-                                     pd + (uint64_t)(((vJ & 1u) * P_BYTES + (k >> 2) * K_CHUNK + (k & 3) * 32) >> 4), i_pv,
-                                     k > 0 || !v_first);
-                        commit_pair(c.bar(B_VFREE));
-                    }
-                    __syncwarp();
-                    v_half = 1;
-                    idle = 0;
-                } else if (v_half == 1 && done(B_VFULL + 1, vJ)) {
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_pair(tmem + TM_O + 128, vd + (uint64_t)((2 * V_CHUNK + k * 2048) >> 4),
-                                     pd + (uint64_t)(((vJ & 1u) * P_BYTES + (k >> 2) * K_CHUNK + (k & 3) * 32) >> 4), i_pv,
-                                     k > 0 || !v_first);
-                        commit_pair(c.bar(B_VFREE + 1));
-                        if (v_left == 1) commit_pair(c.bar(B_O));
-                    }
-                    __syncwarp();
-                    v_half = 0;
-                    v_first = false;
-                    ++vJ;
-                    if (--v_left == 0) {
-                        ++v_unit;
-                        ++event;
-                        v_first = true;
-                    }
-                    idle = 0;
-                } else {
-                    __nanosleep(20);
-                    if ((++idle & 63u) == 0u) {
-                        const uint64_t now = globaltimer_ns();
-                        if (idle == 64u) since = now;
-                        else if (now - since > kWaitLimitNs) c.give_up();
-                        if (__any_sync(kAll, *c.abort != 0)) break;
-                    }
+                    if (rank == 0) mbar_arrive_expect_tx(c.bar(B_Q), (uint32_t)(2 * p.R * D * 2));    // both CTAs'
+                    const int32_t y = (int32_t)((int64_t)x.bi * p.a.m * p.a.h + x.r0 + (int)rank * p.R);
+                    for (int ch = 0; ch < 8; ++ch) tma_load_2d(base + SM_Q + ch * K_CHUNK, &qmap, ch * 64, y, full);
+                    ++n;
                 }
             }
-            if (elect_one()) commit_pair(c.bar(B_DRAIN));
             __syncwarp();
-        }
-      } else if (warp == W_Q) {
-        // ======================================== q by TMA ========================================
-        if (lane == 0) {
-            const uint32_t full = first_bar(B_Q);
-            uint32_t n = 0;
-            Ahead ahead = look(p, cid);
-            for (uint32_t u = cid; u < p.units; u += ncl) {
-                Unit x;
-                make_unit(p, u, ahead, x);
-                ahead = look(p, u + ncl);
-                if (x.t1 <= x.t0) continue;
-                if (!mbar_wait(c.bar(B_QFREE), (n & 1u) ^ 1u, c.abort, kUnitLimitNs)) {
-                    c.give_up();
-                    break;
-                }
-                if (rank == 0) mbar_arrive_expect_tx(c.bar(B_Q), (uint32_t)(2 * p.R * D * 2));    // both CTAs'
-                const int32_t y = (int32_t)((int64_t)x.bi * p.a.m * p.a.h + x.r0 + (int)rank * p.R);
-                for (int ch = 0; ch < 8; ++ch) tma_load_2d(base + SM_Q + ch * K_CHUNK, &qmap, ch * 64, y, full);
-                ++n;
-            }
-        }
-        __syncwarp();
-      } else if (WIDE) {
-        // ======================= K (warp W_LOAD) and V (the next one) by TMA, in halves =======================
-        const bool isv = warp != W_LOAD;
-        if (lane == 0) {
-            const CUtensorMap *map = isv ? &vmap : &kmap;
-            const uint32_t full = first_bar(isv ? B_VFULL : B_KFULL);
-            const int free0 = isv ? B_VFREE : B_KFREE;
-            const uint32_t dst = base + (isv ? SM_V : SM_K);
-            uint32_t J = 0;
-            Ahead ahead = look(p, cid);
-            for (uint32_t u = cid; u < p.units; u += ncl) {
-                Unit x;
-                make_unit(p, u, ahead, x);
-                ahead = look(p, u + ncl);
-                const int64_t wbase = p.a.window ? max((int64_t)0, (int64_t)x.first - p.a.window + 1) : 0;
-                bool ok = true;
-                for (int t = x.t0; t < x.t1; ++t, ++J) {
-                    const int v0 = t * BN, w0 = (int)(x.wlo - wbase) + v0;
-                    const int y = x.bi * (p.wrows + p.crows) + (v0 < x.nwp ? w0 : p.wrows + v0 - x.nwp) + (isv ? 0 : HR * (int)rank);
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && mbar_wait(c.bar(free0 + h), (J & 1u) ^ 1u, c.abort, kWaitLimitNs);
-                        if (!ok) break;
-                        if (rank == 0 && !(p.stall && J == 0)) mbar_arrive_expect_tx(c.bar((isv ? B_VFULL : B_KFULL) + h), 8 * K_CHUNK);
-                        tma_load_3d(dst + h * 4 * K_CHUNK, map, 0, y, isv ? 4 * (int)rank + 2 * h : 4 * h, full + 8 * h);
-                    }
-                    if (!ok) break;
-                }
-                if (!ok) {
-                    c.give_up();
-                    break;
-                }
-            }
-        }
-        __syncwarp();
-      } else {
-        // ================================ half h of K to both CTAs' V ================================
-        // The copy engine takes the other CTA's chunks, this warp its own (the engine with both: 2 us a tile, 1 us each 32 KB).
-        const int h = warp - W_COPY;
-        const uint32_t vfull = first_bar(B_VFULL + h), to = rank ^ 1u;
-        const uint32_t from = base + SM_K + (4 * rank + 2 * h) * K_CHUNK + lane * 16, own = base + SM_V + 2 * h * V_CHUNK + rank * K_CHUNK + lane * 16;
-        TileIter it;
-        it.start(p, cid, ncl);
-        for (uint32_t J = 0; it.valid(); ++J, it.next(p, ncl)) {
-            if (!c.wait<false>(B_KLOC + h, J) || !c.wait<false>(B_VFREE + h, J + 1)) break;
+        } else if (WIDE) {
+            // ======================= K (warp W_LOAD) and V (the next one) by TMA, in halves =======================
+            const bool isv = warp != W_LOAD;
             if (lane == 0) {
-                mbar_arrive_expect_tx(c.bar(B_VLOC + h), 2 * K_CHUNK);   // the other CTA's rows
+                const CUtensorMap *map = isv ? &vmap : &kmap;
+                const uint32_t full = first_bar(isv ? B_VFULL : B_KFULL);
+                const int free0 = isv ? B_VFREE : B_KFREE;
+                const uint32_t dst = base + (isv ? SM_V : SM_K);
+                uint32_t J = 0;
+                Ahead ahead = look(p, cid);
+                for (uint32_t u = cid; u < p.units; u += ncl) {
+                    Unit x;
+                    make_unit(p, u, ahead, x);
+                    ahead = look(p, u + ncl);
+                    const int64_t wbase = p.a.window ? max((int64_t)0, (int64_t)x.first - p.a.window + 1) : 0;
+                    bool ok = true;
+                    for (int t = x.t0; t < x.t1; ++t, ++J) {
+                        const int v0 = t * BN, w0 = (int)(x.wlo - wbase) + v0;
+                        const int y = x.bi * (p.wrows + p.crows) + (v0 < x.nwp ? w0 : p.wrows + v0 - x.nwp) + (isv ? 0 : HR * (int)rank);
+                        for (int h = 0; h < 2; ++h) {
+                            ok = ok && mbar_wait(c.bar(free0 + h), (J & 1u) ^ 1u, c.abort, kWaitLimitNs);
+                            if (!ok) break;
+                            if (rank == 0 && !(p.stall && J == 0)) mbar_arrive_expect_tx(c.bar((isv ? B_VFULL : B_KFULL) + h), 8 * K_CHUNK);
+                            tma_load_3d(dst + h * 4 * K_CHUNK, map, 0, y, isv ? 4 * (int)rank + 2 * h : 4 * h, full + 8 * h);
+                        }
+                        if (!ok) break;
+                    }
+                    if (!ok) {
+                        c.give_up();
+                        break;
+                    }
+                }
+            }
+            __syncwarp();
+        } else {
+            // ================================ half h of K to both CTAs' V ================================
+            // The copy engine takes the other CTA's chunks, this warp its own (the engine with both: 2 us a tile, 1 us each 32 KB).
+            const int h = warp - W_COPY;
+            const uint32_t vfull = first_bar(B_VFULL + h), to = rank ^ 1u;
+            const uint32_t from = base + SM_K + (4 * rank + 2 * h) * K_CHUNK + lane * 16;
+            const uint32_t own = base + SM_V + 2 * h * V_CHUNK + rank * K_CHUNK + lane * 16;
+            TileIter it;
+            it.start(p, cid, ncl);
+            for (uint32_t J = 0; it.valid(); ++J, it.next(p, ncl)) {
+                if (!c.wait<false>(B_KLOC + h, J) || !c.wait<false>(B_VFREE + h, J + 1)) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(c.bar(B_VLOC + h), 2 * K_CHUNK);   // the other CTA's rows
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        bulk_copy_to_peer(mapa(base + SM_V + (2 * h + i) * V_CHUNK + rank * K_CHUNK, to),
+                                          base + SM_K + (4 * to + 2 * h + i) * K_CHUNK, K_CHUNK, mapa(c.bar(B_VLOC + h), to));
+                    bulk_commit_group();
+                }
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    bulk_copy_to_peer(mapa(base + SM_V + (2 * h + i) * V_CHUNK + rank * K_CHUNK, to),
-                                      base + SM_K + (4 * to + 2 * h + i) * K_CHUNK, K_CHUNK, mapa(c.bar(B_VLOC + h), to));
-                bulk_commit_group();
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
 #pragma unroll 1
-                for (int k = 0; k < K_CHUNK; k += 2048) {
-                    float4 x[4];
+                    for (int k = 0; k < K_CHUNK; k += 2048) {
+                        float4 x[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = ld_shared_v4(from + i * K_CHUNK + k + j * 512);
+                        for (int j = 0; j < 4; ++j) x[j] = ld_shared_v4(from + i * K_CHUNK + k + j * 512);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        st_shared_v4(own + i * V_CHUNK + k + j * 512, __float_as_uint(x[j].x), __float_as_uint(x[j].y), __float_as_uint(x[j].z),
-                                     __float_as_uint(x[j].w));
+                        for (int j = 0; j < 4; ++j)
+                            st_shared_v4(own + i * V_CHUNK + k + j * 512, __float_as_uint(x[j].x), __float_as_uint(x[j].y), __float_as_uint(x[j].z),
+                                         __float_as_uint(x[j].w));
+                    }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    bulk_wait_read_all();
+                    mbar_arrive(c.bar(B_KFREE + h));
                 }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                bulk_wait_read_all();
-                mbar_arrive(c.bar(B_KFREE + h));
+                if (!c.wait<false>(B_VLOC + h, J)) break;
+                if (lane == 0) arrive_operand(vfull);
             }
-            if (!c.wait<false>(B_VLOC + h, J)) break;
-            if (lane == 0) arrive_operand(vfull);
+            if (lane == 0) bulk_wait_all();                                  // nothing may land after the CTAs are gone
+            __syncwarp();
         }
-        if (lane == 0) bulk_wait_all();                                  // nothing may land after the CTAs are gone
-        __syncwarp();
-      }
     } else if (warp < W_OUT) {
         if constexpr (!WIDE) setmaxnreg_inc<REG_SOFTMAX>();
         // ======================================== softmax ========================================
@@ -879,7 +884,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                 bool up_any = false;                            // a reference of this warp moves
                 if (!idle_warp) {
                     uint32_t off;
-                    const bool there0 = is_page(p, page_of(p, list, v0 + lane, true, off)), there1 = is_page(p, page_of(p, list, v0 + 32 + lane, true, off));
+                    const bool there0 = is_page(p, page_of(p, list, v0 + lane, true, off));
+                    const bool there1 = is_page(p, page_of(p, list, v0 + 32 + lane, true, off));
                     const uint64_t there = (uint64_t)__ballot_sync(kAll, there0) | ((uint64_t)__ballot_sync(kAll, there1) << 32);
                     mask = there & (bits(a0 - v0, a1 - v0) | bits(x.nwp - v0, c1 - v0));
                 }
@@ -1315,8 +1321,8 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const __grid_constant_
             const int k = k0 + i;
             f[i] = __shfl_sync(kAll, k < 32 ? wgt[0] : wgt[1], k & 31);
             v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (k < np && f[i] != 0.0f) v[i] = __ldcg(reinterpret_cast<const float4 *>(src + k * slot));   // a part without rows wrote none
-            else f[i] = 0.0f;
+            if (k < np && f[i] != 0.0f) v[i] = __ldcg(reinterpret_cast<const float4 *>(src + k * slot));
+            else f[i] = 0.0f;                       // (a part without rows wrote none)
         }
 #pragma unroll
         for (int i = 0; i < kFlight; ++i) {
@@ -1502,11 +1508,11 @@ int launch_chunk_attn_fp8(const chunk::Args &a, cudaStream_t stream) {
     const size_t need = workspace_bytes(pl, a.b);
     if (a.workspace_bytes < need || (need && !a.workspace)) return DS_EWORKSPACE;
     char *ws = static_cast<char *>(a.workspace);
-    Params p{a, Divisor((uint32_t)a.h), Divisor((uint32_t)a.page), Divisor((uint32_t)std::max(a.ring, 1)), Divisor((uint32_t)a.b),
-             Divisor((uint32_t)pl.parts), Divisor((uint32_t)std::max(a.ratio, 1)), pl.R, pl.nqt, (uint32_t)pl.units, (uint32_t)pl.whole, Divisor((uint32_t)pl.clusters),
-             std::min<int64_t>((int64_t)a.max_pages * a.page, kMaxRows), a.scale * kLog2e,
-             reinterpret_cast<float *>(ws + (pl.wide ? rows_bytes(pl, a.b) : 0)), pl.wide ? reinterpret_cast<uint16_t *>(ws) : nullptr, pl.wrows, pl.crows,
-             g_test_stall.load(std::memory_order_relaxed)};
+    auto over = [](int64_t v) { return Divisor((uint32_t)std::max<int64_t>(v, 1)); };
+    Params p{a, over(a.h), over(a.page), over(a.ring), over(a.b), over(pl.parts), over(a.ratio), pl.R, pl.nqt, (uint32_t)pl.units,
+             (uint32_t)pl.whole, over(pl.clusters), std::min<int64_t>((int64_t)a.max_pages * a.page, kMaxRows), a.scale * kLog2e,
+             reinterpret_cast<float *>(ws + (pl.wide ? rows_bytes(pl, a.b) : 0)),
+             pl.wide ? reinterpret_cast<uint16_t *>(ws) : nullptr, pl.wrows, pl.crows, g_test_stall.load(std::memory_order_relaxed)};
     if (a.pages == 0) {       // rows without a slot are read from slot 0, for nothing: there it is q's first row
         p.a.codes = reinterpret_cast<const uint8_t *>(a.q);
         p.a.exps = reinterpret_cast<const int8_t *>(a.q);
@@ -1538,10 +1544,11 @@ int launch_chunk_attn_fp8(const chunk::Args &a, cudaStream_t stream) {
     cfg.dynamicSmemBytes = SMEM_BYTES;
     if (cudaLaunchKernelEx(&cfg, kernel, qmap, kmap, vmap, p) != cudaSuccess) return launch_failed();
     if (split) {
+        auto merge = pl.parts > kManyParts ? chunk_merge_kernel<16> : chunk_merge_kernel<4>;
         cfg.gridDim = dim3((unsigned)((pl.units - pl.whole) / pl.parts), (unsigned)(2 * pl.R), 1);
         cfg.blockDim = dim3(128, 1, 1);
         cfg.dynamicSmemBytes = 0;
-        if (cudaLaunchKernelEx(&cfg, pl.parts > kManyParts ? chunk_merge_kernel<16> : chunk_merge_kernel<4>, p) != cudaSuccess) return launch_failed();
+        if (cudaLaunchKernelEx(&cfg, merge, p) != cudaSuccess) return launch_failed();
     }
     return DS_OK;
 }
