@@ -83,7 +83,7 @@ constexpr int SM_V = SM_K + 8 * K_CHUNK;    // 4 chunks (this CTA's half of d)
 constexpr int P_BYTES = 2 * K_CHUNK;        // 64 query rows of 128 probabilities
 constexpr int SM_P = SM_V + 4 * V_CHUNK;    // two buffers
 constexpr int SM_CTL = SM_P + 2 * P_BYTES;
-constexpr int SMEM_BYTES = SM_CTL + 3072;
+constexpr int SMEM_BYTES = SM_CTL + 3 * 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
 constexpr int TM_O = 0, TM_S = 256, TM_COLS = 512;
