@@ -881,7 +881,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             for (int t = x.t0; t < x.t1; ++t, ++J) {
                 const int v0 = t * BN + half * 64;
                 uint64_t mask = 0;
-                bool up_any = false;                            // a reference of this warp moves
+                bool told = false;                              // this warp has stored what threads of the other CTA read
                 if (!idle_warp) {
                     uint32_t off;
                     const bool there0 = is_page(p, page_of(p, list, v0 + lane, true, off));
@@ -932,9 +932,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                         ref = up < 16384.0f ? ref + up : m + kSlack;
                         l *= ex2(-up);
                     }
-                    up_any = __any_sync(kAll, up > 0.0f);
-                    // alpha's entries of this tile were last used two tiles ago
-                    if (half == 0 && row < p.R && (up > 0.0f || ((lowered >> (J & 1u)) & 1u))) {
+                    // alpha's entries of this tile were last used two tiles ago: one that was not 0 then is set back
+                    const bool tell = half == 0 && row < p.R && (up > 0.0f || ((lowered >> (J & 1u)) & 1u));
+                    told = __any_sync(kAll, tell);
+                    if (tell) {
                         st_cluster_u16(mapa(alpha, 0), (uint16_t)up);
                         st_cluster_u16(mapa(alpha, 1), (uint16_t)up);
                         lowered = (lowered & ~(1u << (J & 1u))) | ((up > 0.0f ? 1u : 0u) << (J & 1u));
@@ -966,7 +967,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    if (up_any) arrive_cluster(pfull[J & 1u]);
+                    if (told) arrive_cluster(pfull[J & 1u]);
                     else arrive_operand(pfull[J & 1u]);
                 }
             }

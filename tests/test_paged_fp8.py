@@ -902,6 +902,30 @@ def test_attention_maximum_that_moves_in_parts(ds, m, h):
 
 
 @gpu
+@pytest.mark.parametrize("b,m", [(40, 1), (20, 1), (13, 3), (7, 3)])
+@pytest.mark.parametrize("order", [(0, 2, 1, 3), (2, 0, 3, 1), (0, 1, 2, 3), (3, 1, 0, 2)])
+def test_attention_maxima_that_move_in_turn(ds, b, m, order):
+    """Heads in four blocks of 32 (two blocks a CTA, a warp's queries each), and every second tile one block's maximum jumps: a
+    block's O^T is lowered at one tile, another block's at the tile where the first one's factors are set back.  Rows read by one tile
+    of queries and by several, units whole and in parts."""
+    n, h, page = 30 * 128, 128, 64
+    block = torch.arange(h) // 32                        # block i: values i, i + 4, ... of a row
+    st = Store(8, 1, n + m, page)
+    v = torch.randn((n + m, 512), generator=st.g).numpy() * 0.05
+    v -= 4
+    for j, t in enumerate(range(1, 30, 2)):              # a step of 1 moves a score by 128 * 4 / 512^0.5 = 22.6, 32 octaves
+        v[128 * t + 9 * j, order[j % 4]::4] += 1 + j // 4
+    st.put(0, range(n + m), v)
+    st.bt = st.bt.expand(b, -1).contiguous()             # every sequence has the same rows
+    on = (torch.arange(512) % 4 == block[:, None]).float() * 4
+    q = (on + 0.01 * torch.randn((b, m, h, 512), generator=st.g)).to(torch.bfloat16)
+    first = torch.full((b,), n, dtype=torch.int32)
+    o = check(ds, st, q, first, torch.linspace(-3, 3, h), 0, 0, 0, 0, tokens=some_tokens(q, 5))
+    for _ in range(20):
+        assert torch.equal(o, ds.chunk_attn_fp8_paged(dev(q), *st.on_gpu(), dev(first), dev(torch.linspace(-3, 3, h)), 512 ** -0.5, 0))
+
+
+@gpu
 @pytest.mark.parametrize("b,m,h,ctx,ragged", [(80, 1, 128, 1300, False), (90, 1, 70, 1300, True), (7, 12, 128, 1400, False),
                                               (5, 40, 60, 1500, True)])
 def test_attention_of_many_sequences(ds, b, m, h, ctx, ragged):
