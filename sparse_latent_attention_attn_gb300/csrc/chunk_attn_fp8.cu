@@ -873,7 +873,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
                 a0 = p.a.window ? (int)max((int64_t)0, pos - p.a.window + 1 - x.wlo) : 0;
                 a1 = (int)min(pos + 1 - x.wlo, (int64_t)x.nw);
                 uint32_t rest;
-                c1 = x.nwp + (p.a.ratio ? min((int)p.ratio.div((uint32_t)(pos + 1), rest), x.nc) : 0);
+                c1 = x.nwp + (p.a.ratio ? (int)min(p.ratio.div((uint32_t)(pos + 1), rest), (uint32_t)x.nc) : 0);
             }
             const List list = list_of(p, x);
             float ref = sink2 - 64.0f, l = 0.0f;

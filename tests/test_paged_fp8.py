@@ -618,6 +618,25 @@ def test_attention_positions_at_the_ends(ds):
 
 
 @gpu
+@pytest.mark.parametrize("m,h", [(1, 20), (2, 128), (3, 128), (30, 24)])
+def test_attention_last_positions_with_a_row_each(ds, m, h):
+    """Positions around 2^31 with one compressed row a position, of which the table holds some: the quotient passes an int."""
+    first, ring, base = ints((1 << 31) - 1), 40, 40
+    st = Store(3, 1, 120, 16)
+    cap = 16 * st.bt.shape[1]
+    st.put(0, range(cap), torch.randn((cap, 512), generator=st.g).numpy())
+    q, sink = torch.randn((1, m, h, 512), generator=st.g).to(torch.bfloat16), torch.randn((h,), generator=st.g)
+    o = torch.empty((1, m, h, 512), dtype=torch.bfloat16, device="cuda")
+    ds.chunk_attn_fp8_paged(dev(q), *st.on_gpu(), dev(first), dev(sink), 512 ** -0.5, 8, ring=ring, ratio=1, base=base, o=o)
+    assert ds.device_status() == ds.DS_DEV_BAD_INDEX                 # rows beyond the table
+    for t in sorted({0, 1, m // 2, m - 1} & set(range(m))):
+        p = int(first[0]) + t
+        rows = [i % ring for i in range(p - 7, p + 1)] + list(range(base, cap))
+        want, tol = attention(f64(q)[0, t], st.get(0, rows), f64(sink), 512 ** -0.5)
+        assert (np.abs(f64(o)[0, t] - want) <= tol).all(), t
+
+
+@gpu
 @pytest.mark.parametrize("what", [math.inf, -math.inf, math.nan])
 def test_attention_of_queries_that_are_not_finite(ds, what):
     """A head of q with an infinity or a NaN touches no other head, and no other token."""
