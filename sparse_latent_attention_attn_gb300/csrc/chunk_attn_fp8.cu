@@ -216,12 +216,9 @@ __device__ __forceinline__ void make_unit(const Params &p, uint32_t u, const Ahe
     }
     x.nw = (int)max((int64_t)0, end - x.wlo);
     if (p.a.ratio) {
-        int64_t nc = p.ratio.div((uint32_t)(hi + 1), rest);
-        if (nc > p.cap - p.a.base) {
-            nc = max((int64_t)0, p.cap - p.a.base);
-            x.clipped = true;
-        }
-        x.nc = (int)nc;
+        const int64_t nc = p.ratio.div((uint32_t)(hi + 1), rest), most = max((int64_t)0, p.cap - p.a.base);
+        x.clipped |= nc > most;
+        x.nc = (int)min(nc, most);
     }
     x.nwp = p.rows && x.nc ? (x.nw + BN - 1) / BN * BN : x.nw;      // WIDE: compressed rows begin a tile
     x.t1 = (int)((uint32_t)(x.nwp + x.nc + BN - 1) / BN);

@@ -637,6 +637,17 @@ def test_attention_last_positions_with_a_row_each(ds, m, h):
 
 
 @gpu
+@pytest.mark.parametrize("m,h", [(1, 20), (1, 128), (3, 128)])
+def test_attention_compressed_rows_begin_beyond_the_table(ds, m, h):
+    """A table that ends before the first compressed row's place: right as long as there is none, flagged from the first on."""
+    st, q, sink = filled(6, 1, m, h, 20, 32, 0, 0, 16, ints(20))
+    st.put(0, range(32), torch.randn((32, 512), generator=st.g).numpy())
+    assert st.bt.shape[1] * 16 < 80
+    check(ds, st, q, ints(20), sink, 20, 32, 64, 80)
+    check(ds, st, q, ints(64), sink, 20, 32, 64, 80, status=ds.DS_DEV_BAD_INDEX, rows_of=lambda i, rows: [r for r in rows if r < 80])
+
+
+@gpu
 @pytest.mark.parametrize("what", [math.inf, -math.inf, math.nan])
 def test_attention_of_queries_that_are_not_finite(ds, what):
     """A head of q with an infinity or a NaN touches no other head, and no other token."""
