@@ -536,7 +536,7 @@ int ds_kv_read_fp4_paged(const uint8_t *codes, const int8_t *exps, int64_t pages
  * compressed rows with pos_step = ratio and this base).  Over the rows that it sees the operation is ds_sparse_attn's,
  * with the inverse RoPE of position p before o's one rounding when rd > 0 (a position outside the table leaves
  * that token's o unrotated).  Rows without a page are skipped and flagged (DS_DEV_BAD_INDEX); a query that sees no row
- * gives o = 0, and so does one at a negative position, which is flagged.
+ * gives o = 0, and so does one at a negative position, which is flagged.  A NaN in sink gives NaN for its head's other queries.
  * Scores, softmax and accumulation are f32; a probability enters the value product rounded to bf16, as in
  * ds_sparse_attn.  The rows that queries of a sequence see must be finite in bf16 (their largest code times
  * 2^k below 2^128), and scale * q, the scores and the products that are added up finite in f32.  Rows

@@ -416,6 +416,12 @@ __device__ __forceinline__ uint64_t bits(int lo, int hi) {
     return (z - a == 64 ? ~0ull : ((1ull << (z - a)) - 1)) << a;
 }
 
+// A head's sink in octaves, finite from above; a NaN stays one (in no reference, as fmaxf leaves it out, but in the denominator).
+__device__ __forceinline__ float sink_log2(const Params &p, uint32_t hh) {
+    const float v = __ldg(p.a.sink + hh) * kLog2e;
+    return v > 1e37f ? 1e37f : v;
+}
+
 // What a role needs to wait, and to tell both CTAs to give up.
 struct Ctl {
     uint32_t bars;
@@ -863,7 +869,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             uint32_t hh = 0;
             const int64_t pos = (int64_t)x.first + (live ? p.h.div((uint32_t)(x.r0 + rq), hh) : 0);
             bad |= (live && pos < 0) || x.clipped;
-            const float sink2 = live ? fminf(__ldg(p.a.sink + hh) * kLog2e, 1e37f) : 0.0f;
+            const float sink2 = live ? sink_log2(p, hh) : 0.0f;
             // rows [a0, a1) and [nwp, c1) of the list
             int a0 = 0, a1 = 0, c1 = 0;
             if (live && pos >= 0) {
@@ -1307,7 +1313,7 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const __grid_constant_
         den += wgt[i] * l[i];
     }
     den = rows::row_sum<32>(den);
-    const float sink2 = fminf(__ldg(p.a.sink + hh) * kLog2e, 1e37f);
+    const float sink2 = sink_log2(p, hh);
     const float inv = den == 0.0f ? 0.0f : 1.0f / (den + ex2(sink2 - top));
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float *src = ws + (size_t)q * D + 4 * threadIdx.x;

@@ -863,6 +863,22 @@ def test_attention_wait_that_runs_out(ds, form):
 
 @gpu
 @pytest.mark.parametrize("form", FORMS)
+def test_attention_sink_that_is_nan(ds, form):
+    """As in ds_sparse_attn: NaN for its head, nothing for the others; a query that sees no row gives zeros all the same."""
+    st, q, sink, first, how = of_form(form, seed=4)
+    clean = check(ds, st, q, first, sink, *how, tokens=some_tokens(q, 3))
+    sink[5] = math.nan
+    args = (dev(q), *st.on_gpu(), dev(first), dev(sink), 512 ** -0.5, how[0])
+    got = ds.chunk_attn_fp8_paged(*args, ring=how[1], ratio=how[2], base=how[3])
+    assert got[:, :, 5].isnan().all() and ds.device_status() == 0
+    got[:, :, 5] = clean[:, :, 5]
+    assert torch.equal(got, clean)
+    got = ds.chunk_attn_fp8_paged(*args[:3], torch.full_like(args[3], -1), *args[4:], ring=how[1], ratio=how[2], base=how[3])
+    assert not got.any() and ds.device_status() == ds.DS_DEV_BAD_INDEX
+
+
+@gpu
+@pytest.mark.parametrize("form", FORMS)
 def test_attention_workspace_ends(ds, form):
     """Whatever the workspace holds, and nothing beyond it."""
     st, q, sink, first, how = of_form(form, seed=3)
