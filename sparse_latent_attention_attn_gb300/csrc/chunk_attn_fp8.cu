@@ -209,9 +209,11 @@ __device__ __forceinline__ void make_unit(const Params &p, uint32_t u, const Ahe
     const int64_t hi = (int64_t)x.first + p.h.div((uint32_t)min(x.r0 + 2 * p.R, x.rows) - 1, rest);
     if (hi < 0) return;
     if (p.a.window) x.wlo = (uint32_t)max((int64_t)0, lo - p.a.window + 1);
-    int64_t end = hi + 1;
-    if (!p.a.ring && end > p.cap) {
-        end = p.cap;
+    // positions that have a place; a ring has one for each, but the workspace only for those of a chunk that the ring holds
+    int64_t end = hi + 1, held = p.a.ring ? end : p.cap;
+    if (p.a.ring && p.rows) held = max((int64_t)0, (int64_t)x.first - p.a.window + 1) + (p.wrows - BN);
+    if (end > held) {
+        end = held;
         x.clipped = true;
     }
     x.nw = (int)max((int64_t)0, end - x.wlo);
@@ -1219,7 +1221,7 @@ __global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__
         uint32_t rest;
         int64_t count = comp ? (end > 0 ? (int64_t)p.ratio.div((uint32_t)end, rest) : 0) : max((int64_t)0, end - wbase);
         if (comp) count = min(count, max((int64_t)0, p.cap - p.a.base));
-        else if (!p.a.ring) count = min(count, max((int64_t)0, p.cap - wbase));
+        else count = min(count, p.a.ring ? (int64_t)(p.wrows - BN) : max((int64_t)0, p.cap - wbase));
         int at = -2;
         if (n > 0 && i < (comp ? p.crows : p.wrows) && i < count + BN) {
             at = -1;
@@ -1456,7 +1458,8 @@ bool plan(int b, int m, int h, int window, int ratio, int page, int max_pages, P
     pl.R = nr <= 32 ? 16 : nr <= 64 ? 32 : 64;
     pl.nqt = (int)((nr + 2 * pl.R - 1) / (2 * pl.R));
     const int64_t units = (int64_t)b * pl.nqt, cap = std::min<int64_t>((int64_t)max_pages * page, kMaxRows);
-    const int64_t wr = window ? std::min<int64_t>((int64_t)window + m - 1, (int64_t)1 << 30) + BN : cap + BN, cr = ratio ? cap + BN : 0;
+    // (a ring, too, holds all that a chunk sees of positions, and the block table holds the ring)
+    const int64_t wr = (window ? std::min<int64_t>((int64_t)window + m - 1, cap) : cap) + BN, cr = ratio ? cap + BN : 0;
     pl.wide = pl.nqt >= kWideTiles && (wr + cr) * b * (D * 2) <= (int64_t)2 << 30;
     pl.wrows = pl.wide ? (int)wr : 0;
     pl.crows = pl.wide ? (int)cr : 0;

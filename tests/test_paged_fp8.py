@@ -972,6 +972,41 @@ def test_attention_maxima_that_move_in_turn(ds, b, m, order):
 
 
 @gpu
+@pytest.mark.parametrize("m,h", [(1, 20), (5, 128), (40, 24)])
+def test_attention_window_beyond_the_table(ds, m, h):
+    """A window wider than the table has rows is one over all positions, in the workspace too."""
+    first = ints(300, 77)
+    st, q, sink = filled(12, 2, m, h, 0, 0, 0, 0, 16, first)
+    o = check(ds, st, q, first, sink, 0, 0, 0, 0, tokens=some_tokens(q, 6))
+    for window in (16 * st.bt.shape[1], 1 << 20, (1 << 31) - 1):
+        assert (ds.chunk_attn_fp8_paged_workspace_bytes(2, m, h, 512, window, 0, 16, st.bt.shape[1])
+                == ds.chunk_attn_fp8_paged_workspace_bytes(2, m, h, 512, 0, 0, 16, st.bt.shape[1]))
+        assert torch.equal(o, ds.chunk_attn_fp8_paged(dev(q), *st.on_gpu(), dev(first), dev(sink), 512 ** -0.5, window))
+    assert ds.device_status() == 0
+
+
+@gpu
+def test_attention_chunk_that_its_ring_does_not_hold(ds):
+    """With lens, a chunk longer than its ring holds cannot be told on the host: what the workspace has no room for is skipped and
+    flagged, and the tokens before it are what they are in a chunk that fits."""
+    b, m, h, window, ring = 2, 200, 4, 30, 64
+    st = Store(2, b, ring, 16)
+    for i in range(b):
+        st.put(i, range(ring), torch.randn((ring, 512), generator=st.g).numpy())
+    q, sink, first = torch.randn((b, m, h, 512), generator=st.g).to(torch.bfloat16), torch.randn((h,), generator=st.g), ints(100, 90)
+    fits = ring - window + 1
+    args = (dev(q), *st.on_gpu(), dev(first), dev(sink), 512 ** -0.5, window)
+    want = ds.chunk_attn_fp8_paged(*args, ring=ring, lens=dev(ints(fits, fits)))
+    assert ds.device_status() == 0
+    got = ds.chunk_attn_fp8_paged(*args, ring=ring, lens=dev(ints(m, fits)))
+    assert ds.device_status() == ds.DS_DEV_BAD_INDEX
+    # the first sequence's tiles of queries have other unions of rows, the second's the same
+    assert torch.equal(got[1], want[1]) and got.isfinite().all()
+    check(ds, st, q, first, sink, window, ring, 0, 0, lens=ints(m, fits), tokens=[(0, t) for t in range(0, fits, 4)],
+          status=ds.DS_DEV_BAD_INDEX)
+
+
+@gpu
 @pytest.mark.parametrize("b,m,h,ctx,ragged", [(80, 1, 128, 1300, False), (90, 1, 70, 1300, True), (7, 12, 128, 1400, False),
                                               (5, 40, 60, 1500, True)])
 def test_attention_of_many_sequences(ds, b, m, h, ctx, ragged):
