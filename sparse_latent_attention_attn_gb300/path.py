@@ -92,10 +92,14 @@ def chunk_step_fp8_paged(q: torch.Tensor, new_kv: torch.Tensor, codes: torch.Ten
     ratio > 0, the compressed rows of every complete group of `ratio` positions, which are in the store from logical row
     `base` on (kv_append_fp8_paged with pos_step = ratio and that base).  Tokens at or behind lens[bi] are
     padding: nothing of theirs is stored, and o is left as it was (zeros in a new one).  The ring must hold
-    window + s - 1 rows (with lens: window + the largest of them - 1)."""
+    window + s - 1 rows (with lens: window + the largest of them - 1) and lie in the block table, before the compressed rows;
+    one that does not is refused before anything is stored in it."""
     s = q.shape[1]
-    if lens is None and 0 < ring < window + s - 1:
+    if ring > 0 and (window <= 0 or ring < window + (max(s, 1) - 1 if lens is None else 0)):
         raise ValueError(f"a ring of {ring} slots does not hold a window of {window} and the step's {s} tokens")
+    if ring > 0 and codes.dim() == 3 and (ring > codes.shape[1] * block_table.shape[-1] or (ratio > 0 and base < ring)):
+        raise ValueError(f"a ring of {ring} slots does not fit into {block_table.shape[-1]} pages of {codes.shape[1]} rows, "
+                         f"before the compressed rows from {base} on")
     dsattn.kv_append_fp8_paged(new_kv, codes, exps, block_table, first, rd=rd, table=table, eps=eps, weight=kv_weight,
                                lens=lens, window=ring, stream=stream)
     qn = None

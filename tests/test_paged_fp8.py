@@ -1208,6 +1208,37 @@ def test_bindings_refuse_cpu_tensors_and_shapes(lib):
                                   9, 0.1, 0, None, 1e-6)
 
 
+LAYOUTS = [dict(window=0, ring=8), dict(window=9, ring=8, lens=True), dict(window=8, ring=9), dict(window=30, ring=50),
+           dict(window=8, ring=16, ratio=4, base=15)]
+
+
+def layout_step(path, how, on):
+    """A step whose ring and rows do not fit together; the store must be as it was."""
+    q, x = torch.ones((1, 3, 2, 512), dtype=torch.bfloat16), torch.ones((1, 3, 512), dtype=torch.bfloat16)
+    st = Store(1, 1, 48, 16, garbage=False)
+    how = dict(how)
+    lens = on(ints(1)) if how.pop("lens", False) else None
+    codes, exps, bt = (on(t) for t in (st.codes, st.exps, st.bt))
+    with pytest.raises(ValueError, match="ring"):
+        path.chunk_step_fp8_paged(on(q), on(x), codes, exps, bt, on(ints(5)), on(torch.zeros(2)), scale=0.1, rd=0, table=None,
+                                  eps=1e-6, lens=lens, **how)
+    assert not codes.any() and not exps.any()
+
+
+@pytest.mark.parametrize("how", LAYOUTS)
+def test_step_refuses_a_ring_before_it_stores(lib, how):
+    from sparse_latent_attention_attn_gb300 import path
+    layout_step(path, how, lambda t: t)
+
+
+@gpu
+@pytest.mark.parametrize("how", LAYOUTS)
+def test_step_refuses_a_ring_before_it_stores_on_the_gpu(ds, how):
+    from sparse_latent_attention_attn_gb300 import path
+    layout_step(path, how, dev)
+    assert ds.device_status() == 0
+
+
 @gpu
 def test_bindings_refuse_what_does_not_fit(ds):
     st = Store(1, 2, 40, 16, garbage=False)
