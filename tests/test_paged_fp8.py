@@ -1007,6 +1007,22 @@ def test_attention_chunk_that_its_ring_does_not_hold(ds):
 
 
 @gpu
+@pytest.mark.parametrize("b,m,h,window,ratio", [(1, 12, 60, 0, 0), (2, 304, 128, 40, 4), (1, 700, 3, 0, 0), (3, 9, 128, 64, 2),
+                                                (2, 40, 128, 0, 0)])
+def test_attention_of_a_table_too_wide_to_widen(ds, b, m, h, window, ratio):
+    """Tables of 2^21 rows, next to all of them without a page: several tiles of queries a sequence, whose rows, had they to be
+    widened for the whole table, would pass the workspace's 2 GB, and are widened by each unit; in parts and whole."""
+    page, first = 256, ints(*[430 - 60 * i for i in range(b)])
+    base = (500 + m) // page * page + page if ratio else 0
+    st, q, sink = filled(14, b, m, h, window, 0, ratio, base, page, first)
+    st.bt = torch.cat((st.bt, torch.full((b, 8192 - st.bt.shape[1]), -1, dtype=torch.int32)), dim=1)
+    assert ds.chunk_attn_fp8_paged_workspace_bytes(b, m, h, 512, window, ratio, page, 8192) < 1 << 31
+    check(ds, st, q, first, sink, window, 0, ratio, base, rd=64, tab=table_of(440 + m, 64), tokens=some_tokens(q, 9))
+    lens = ints(*[max(1, m - 3 * i) for i in range(b)])
+    check(ds, st, q, first, sink, window, 0, ratio, base, lens=lens, tokens=some_tokens(q, 5))
+
+
+@gpu
 @pytest.mark.parametrize("b,m,h,ctx,ragged", [(80, 1, 128, 1300, False), (90, 1, 70, 1300, True), (7, 12, 128, 1400, False),
                                               (5, 40, 60, 1500, True)])
 def test_attention_of_many_sequences(ds, b, m, h, ctx, ragged):
