@@ -549,8 +549,8 @@ int ds_kv_read_fp4_paged(const uint8_t *codes, const int8_t *exps, int64_t pages
  * first      device int32 [b];  lens: device int32 [b], or NULL for m
  * window     >= 0;  ring 0, or at least window (window > 0) and at most max_pages * page, and without lens at
  *            least window + m - 1, so that the chunk's rows replaced none that its queries see; with lens
- *            the same must hold for the largest of them (a longer one's queries see rows of other positions, or
- *            rows are skipped and flagged).  Logical rows from 2^29 on count as rows without a page
+ *            the same must hold for the largest of them (a longer one's queries see rows of other positions).
+ *            Logical rows from 2^29 on count as rows without a page
  * base       >= 0, and >= ring when there are both a ring and compressed rows
  * workspace  at least ds_chunk_attn_fp8_paged_workspace_bytes bytes for the same arguments, 256-byte aligned (may
  *            be NULL when that size is 0); its contents need no initialisation and mean nothing afterwards.

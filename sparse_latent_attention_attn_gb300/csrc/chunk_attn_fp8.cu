@@ -209,18 +209,19 @@ __device__ __forceinline__ void make_unit(const Params &p, uint32_t u, const Ahe
     const int64_t hi = (int64_t)x.first + p.h.div((uint32_t)min(x.r0 + 2 * p.R, x.rows) - 1, rest);
     if (hi < 0) return;
     if (p.a.window) x.wlo = (uint32_t)max((int64_t)0, lo - p.a.window + 1);
-    // positions that have a place; a ring has one for each, but the workspace only for those of a chunk that the ring holds
-    int64_t end = hi + 1, held = p.a.ring ? end : p.cap;
-    if (p.a.ring && p.rows) held = max((int64_t)0, (int64_t)x.first - p.a.window + 1) + (p.wrows - BN);
-    if (end > held) {
-        end = held;
+    int64_t end = hi + 1;
+    if (!p.a.ring && end > p.cap) {
+        end = p.cap;
         x.clipped = true;
     }
     x.nw = (int)max((int64_t)0, end - x.wlo);
     if (p.a.ratio) {
-        const int64_t nc = p.ratio.div((uint32_t)(hi + 1), rest), most = max((int64_t)0, p.cap - p.a.base);
-        x.clipped |= nc > most;
-        x.nc = (int)min(nc, most);
+        int64_t nc = p.ratio.div((uint32_t)(hi + 1), rest);
+        if (nc > p.cap - p.a.base) {
+            x.clipped |= nc > 0;
+            nc = max((int64_t)0, p.cap - p.a.base);
+        }
+        x.nc = (int)nc;
     }
     x.nwp = p.rows && x.nc ? (x.nw + BN - 1) / BN * BN : x.nw;      // WIDE: compressed rows begin a tile
     x.t1 = (int)((uint32_t)(x.nwp + x.nc + BN - 1) / BN);
@@ -1221,7 +1222,7 @@ __global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__
         uint32_t rest;
         int64_t count = comp ? (end > 0 ? (int64_t)p.ratio.div((uint32_t)end, rest) : 0) : max((int64_t)0, end - wbase);
         if (comp) count = min(count, max((int64_t)0, p.cap - p.a.base));
-        else count = min(count, p.a.ring ? (int64_t)(p.wrows - BN) : max((int64_t)0, p.cap - wbase));
+        else if (!p.a.ring) count = min(count, max((int64_t)0, p.cap - wbase));
         int at = -2;
         if (n > 0 && i < (comp ? p.crows : p.wrows) && i < count + BN) {
             at = -1;
@@ -1439,6 +1440,10 @@ struct Plan {
     int64_t whole, units;      // units that are not in parts, and with the parts of the others
     bool wide;
     int wrows, crows;          // wide: rows of a sequence in the workspace
+    void no_rows() {
+        wide = false;
+        wrows = crows = 0;
+    }
 };
 
 // Query rows a CTA: the fewest that hold a sequence's queries in one unit.
@@ -1458,7 +1463,7 @@ bool plan(int b, int m, int h, int window, int ratio, int page, int max_pages, P
     pl.R = nr <= 32 ? 16 : nr <= 64 ? 32 : 64;
     pl.nqt = (int)((nr + 2 * pl.R - 1) / (2 * pl.R));
     const int64_t units = (int64_t)b * pl.nqt, cap = std::min<int64_t>((int64_t)max_pages * page, kMaxRows);
-    // (a ring, too, holds all that a chunk sees of positions, and the block table holds the ring)
+    // (a ring holds every position that the chunk sees, and the block table holds the ring)
     const int64_t wr = (window ? std::min<int64_t>((int64_t)window + m - 1, cap) : cap) + BN, cr = ratio ? cap + BN : 0;
     pl.wide = pl.nqt >= kWideTiles && (wr + cr) * b * (D * 2) <= (int64_t)2 << 30;
     pl.wrows = pl.wide ? (int)wr : 0;
@@ -1512,6 +1517,8 @@ int launch_chunk_attn_fp8(const chunk::Args &a, cudaStream_t stream) {
     using namespace chunk;
     Plan pl;
     if (!plan(a.b, a.m, a.h, a.window, a.ratio, a.page, a.max_pages, pl)) return launch_failed();
+    // with lens, a chunk as long as m may see more positions than the table has rows: the workspace would not hold them
+    if (a.ring && (int64_t)a.window + a.m - 1 > (int64_t)a.max_pages * a.page) pl.no_rows();
     const size_t need = workspace_bytes(pl, a.b);
     if (a.workspace_bytes < need || (need && !a.workspace)) return DS_EWORKSPACE;
     char *ws = static_cast<char *>(a.workspace);

@@ -986,24 +986,18 @@ def test_attention_window_beyond_the_table(ds, m, h):
 
 
 @gpu
-def test_attention_chunk_that_its_ring_does_not_hold(ds):
-    """With lens, a chunk longer than its ring holds cannot be told on the host: what the workspace has no room for is skipped and
-    flagged, and the tokens before it are what they are in a chunk that fits."""
-    b, m, h, window, ring = 2, 200, 4, 30, 64
+@pytest.mark.parametrize("window,ring,m", [(30, 64, 200), (30, 64, 40), (1, 16, 300)])
+def test_attention_padded_longer_than_the_table(ds, window, ring, m):
+    """Padded chunks with more tokens than the ring, or the table, has rows: what lens says is there is right.  A sequence that its
+    ring does not hold, which lens tells on the device only, sees what lies in the slots of its positions."""
+    b, h = 2, 9
     st = Store(2, b, ring, 16)
     for i in range(b):
         st.put(i, range(ring), torch.randn((ring, 512), generator=st.g).numpy())
-    q, sink, first = torch.randn((b, m, h, 512), generator=st.g).to(torch.bfloat16), torch.randn((h,), generator=st.g), ints(100, 90)
+    q, sink, first = torch.randn((b, m, h, 512), generator=st.g).to(torch.bfloat16), torch.randn((h,), generator=st.g), ints(100, 3)
     fits = ring - window + 1
-    args = (dev(q), *st.on_gpu(), dev(first), dev(sink), 512 ** -0.5, window)
-    want = ds.chunk_attn_fp8_paged(*args, ring=ring, lens=dev(ints(fits, fits)))
-    assert ds.device_status() == 0
-    got = ds.chunk_attn_fp8_paged(*args, ring=ring, lens=dev(ints(m, fits)))
-    assert ds.device_status() == ds.DS_DEV_BAD_INDEX
-    # the first sequence's tiles of queries have other unions of rows, the second's the same
-    assert torch.equal(got[1], want[1]) and got.isfinite().all()
-    check(ds, st, q, first, sink, window, ring, 0, 0, lens=ints(m, fits), tokens=[(0, t) for t in range(0, fits, 4)],
-          status=ds.DS_DEV_BAD_INDEX)
+    for lens in (ints(fits, 2), ints(m, fits)):
+        check(ds, st, q, first, sink, window, ring, 0, 0, lens=lens, tokens=some_tokens(q, 30))
 
 
 @gpu
