@@ -555,7 +555,11 @@ int ds_kv_read_fp4_paged(const uint8_t *codes, const int8_t *exps, int64_t pages
  * workspace  at least ds_chunk_attn_fp8_paged_workspace_bytes bytes for the same arguments, 256-byte aligned (may
  *            be NULL when that size is 0); its contents need no initialisation and mean nothing afterwards.
  *            Calls that may run at the same time need one each.  It holds partial results of long sequences, and, where
- *            a sequence has more than 256 query rows (m * h), the block table's rows in bf16, up to 2 GB of them
+ *            a sequence has more than 256 query rows (m * h), rows in bf16: of every sequence the positions that its
+ *            queries can see (window + m - 1, at most the block table's rows) and, with ratio > 0, all of the table's rows;
+ *            none where that would be more than 2 GB, which takes up to twice as long.  The size goes by max_pages, whatever
+ *            the table holds: a table much wider than the sequences are long costs workspace and time, and a narrow
+ *            copy of its first columns does not
  * Supported: d = 512, 1 <= h <= 128, b * m * h < 2^31, pages * page < 2^31, ring <= 2^29; q, o, codes and exps 16-byte
  * aligned.
  * Errors: DS_EINVAL, DS_EUNSUPPORTED, DS_EWORKSPACE, DS_ECUDA.

@@ -15,10 +15,11 @@
 //   * O^T += V^T P^T: M = 256 values of d (128 a CTA, twice), N = 128 queries (each CTA's P), K = 128 rows.  O^T takes 256
 //     columns of tensor memory, and two tiles of scores 128.
 // The tensor cores read both CTAs' operands, so no scores and no probabilities cross between the CTAs.  The MMAs of a tile
-// take 0.75 + 0.53 us (23.3 ns for each of 32, 32.9 ns for each of 16, measured), 0.85 of the tensor cores' rate.
+// take 0.75 + 0.53 us (23.3 ns for each of 32, 32.9 ns for each of 16, measured at 2070 MHz: 48 and 68 cycles, where 8192
+// operations a cycle and SM would be 32 and 64, so 0.66 of that rate for S, 0.94 for P V, 0.78 for both).
 //
 // A code widens to bf16 exactly (at most four significant bits; its bits moved to a bf16's, times 2^(120 + k)).  Two forms:
-//   * Sequences with one or two tiles of queries (decoding): each row is read once a tile, as codes, and widened in registers
+//   * Sequences with one or two tiles of queries (decoding), or where the form below does not fit: each row is read once a tile, as codes, and widened in registers
 //     on its way into shared memory, which spares a copy in HBM: 33/32 byte a value is all that is read.  Each CTA widens its
 //     64 rows once, as K; for P V it needs its half of d of all 128, copied from K in the layout that it has: its own rows by
 //     a warp, the other CTA's by the copy engine, 8 KB each (the engine with both takes 2 us a tile).  K is held until its
@@ -27,7 +28,12 @@
 //     256 sequences of 2176 rows; V widened a second time by eight more warps: 252 -> 370.)
 //   * Sequences with more (WIDE; prompts): several units read the same rows, so a kernel before widens them once, into the
 //     workspace, and K and V come by TMA: 1.5 us a tile, and some 4 us between units, in which q is loaded and O^T read.
+//     The host knows the block table's width, not how much of it is used: tables of more rows than the workspace may take
+//     (plan()) are read in the other form (16 prompts' chunks of 512 tokens and 128 heads over 2176 rows: 3.1 ms with a table
+//     of 2688 rows, 5.5 with one of 262272).
 // An operand half is handed back as soon as its readers are done.
+//
+// (Times: calls captured in a graph, one behind the other, unless another kind is named.)
 //
 // The softmax works on a reference per query: kSlack octaves above the first tile's maximum, moved (by whole octaves, so that
 // O^T and the sum are scaled exactly) only when a later maximum exceeds it.  So P is at most 1, as large as it may be beside

@@ -2,7 +2,7 @@
 // k = ceil(log2(max(amax, 1e-4) / 448)): "Module attn", act_quant_inplace and pow2_ceil.
 //
 // Bound by instructions, as in 4 bits (two thirds of the issue slots, no pipe full): 32 us for 8 x 4096 rows of 512, whose
-// bytes alone would take 13.7; 256 rows 14.9 us a call.
+// bytes alone would take 13.7; 256 rows 14.5 us a call through the binding among others, bound by the host.
 #include "kv_append.cuh"
 
 namespace dsattn {

@@ -7,7 +7,8 @@
 // Bound by HBM: 33/32 (17/32 in 4 bits) byte read and 2 written a value.  A block takes up to 64 rows: the
 // first threads look up their slots, one dependent chain (list, page) for all of them, then every thread moves eight
 // values a step, so that a warp stores 512 contiguous bytes, kSteps steps in flight.  Few rows are spread over more blocks.
-// 16 x 4224 rows of 512 in 8 bits: 18.1 us, where their bytes alone take 15.4; 64 x 640 listed rows in 4 bits: 10.3 us a call.
+// 16 x 4224 rows of 512 in 8 bits, whose bytes alone take 15.4 us: 18.1 us on the device (profiler, cold caches), 22.7 a call
+// through the binding among others; 64 x 640 listed rows in 4 bits: 10.3 us such a call.
 #include "paged_rows.cuh"
 #include "row_norm.cuh"
 

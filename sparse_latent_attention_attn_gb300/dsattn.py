@@ -613,7 +613,8 @@ def chunk_attn_fp8_paged(q: torch.Tensor, codes: torch.Tensor, exps: torch.Tenso
     position ``p = first[b] + t`` and sees the rows of its last ``window`` positions (0: all; position i is logical row
     ``i % ring``, or i without a ring) and compressed rows 0 .. (p + 1) // ratio - 1 (``ratio`` 0: none), logical
     rows ``base + j``; with ``rd`` > 0 the last ``rd`` values of its output are rotated back.  Tokens at or behind
-    ``lens[b]`` leave ``o`` as it was (zeros in a new one)."""
+    ``lens[b]`` leave ``o`` as it was (zeros in a new one).  Workspace and form go by ``block_table``'s columns: one much
+    wider than the sequences are long is better given as a copy of its first columns."""
     if q.dim() != 4 or codes.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be [b][m][h][d], codes [pages][page][d] and block_table [b][max_pages]")
     b, m, h, d = q.shape
