@@ -339,7 +339,8 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void arrive_operand(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same for what threads of the other CTA read: what this thread wrote or saw is visible to who waits at cluster scope.
+// The same for what threads of the other CTA read, or write once it has been read: what this thread wrote or saw comes before what
+// follows for who waits at cluster scope.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -1182,7 +1183,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<WIDE>::kThread
             }
             if (!split) {                                    // (units without rows have gone on above)
                 __syncwarp();
-                if (lane < 2) arrive_operand(mapa(c.bar(B_INVFREE + (int)(unit & 1u)), (uint32_t)lane));
+                // both CTAs' softmax threads write the next ones.  (At cluster scope this waits for the output's stores, 0.3 us where nothing
+                // is left to do: not behind the last unit, for which nobody waits.)
+                if (lane < 2 && u + ncl < p.units) arrive_cluster(mapa(c.bar(B_INVFREE + (int)(unit & 1u)), (uint32_t)lane));
                 ++unit;
             }
         }

@@ -1047,6 +1047,20 @@ def test_attention_of_one_row_a_query(ds, b, m, h):
 
 
 @gpu
+@pytest.mark.parametrize("b,m,h", [(126, 93, 2), (2, 700, 100), (300, 1, 128), (90, 5, 23)])
+def test_attention_of_one_row_a_query_under_sinks(ds, b, m, h):
+    """Units of a single tile whose factors lie decades apart, from head to head and from unit to unit: one unit's factors are
+    written only when both CTAs have read those of two units ago."""
+    first = torch.arange(b, dtype=torch.int32) % 11
+    st, q, _ = filled(5, b, m, h, 1, m, 0, 0, 64, first)
+    sink = 12.0 * torch.randn((h,), generator=st.g)
+    q = (q.float() * torch.linspace(0.1, 2.0, b * m).view(b, m, 1, 1)).to(torch.bfloat16)
+    o = check(ds, st, q, first, sink, 1, m, 0, 0, tokens=some_tokens(q, 60))
+    for _ in range(20):
+        assert torch.equal(ds.chunk_attn_fp8_paged(dev(q), *st.on_gpu(), dev(first), dev(sink), 512 ** -0.5, 1, ring=m), o)
+
+
+@gpu
 @pytest.mark.parametrize("how", [dict(window=64, ring=70, ratio=4, base=70), dict(window=0, ring=0, ratio=0, base=0)])
 def test_attention_padding_and_empty_sequences(ds, how):
     """lens of 0, of more than m and below 0; tokens behind a sequence's last are left as they were."""
